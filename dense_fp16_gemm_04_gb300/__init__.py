@@ -27,6 +27,9 @@ __all__ = [
     "build", "load", "Plan", "GemmError", "gemm", "gemm_host", "default_plan",
     "ACC_F32", "ACC_F16", "K_CONTIGUOUS", "MN_CONTIGUOUS", "status_string", "variant_names", "variant_info",
     "LIB_PATH",
+    # Operators beside the GEMM (ops.py; loaded with torch on first use).
+    "Ops", "default_ops", "gated_ffn", "gated_ffn_backward", "w4_linear", "w4_gated", "w4_quantize",
+    "orthogonalize", "NEWTON_SCHULZ",
 ]
 
 LIB_PATH = _build.LIB_PATH
@@ -383,3 +386,18 @@ def gemm_host(a, b, acc="f32", out=None, stream=None, plan: Plan | None = None):
                           pin_memory=bool(getattr(a, "is_pinned", lambda: False)()))
     (plan or default_plan()).run_host(a, b, out, acc=acc, stream=stream)
     return out
+
+
+_OPS = ("Ops", "default_ops", "gated_ffn", "gated_ffn_backward", "w4_linear", "w4_gated",
+        "w4_quantize", "orthogonalize", "NEWTON_SCHULZ")
+
+
+def __getattr__(name):
+    """The operators' names: ops.py imports torch, which the GEMM's C-pointer
+    interface does without, so it is loaded when one of them is first used."""
+    if name in _OPS:
+        from . import ops
+        for n in _OPS:
+            globals()[n] = getattr(ops, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,7 +1,7 @@
 """Build the sm_103a CUDA library in-tree with nvcc (no torch, no cmake).
 
-Produces ``libgb300gemm.so`` next to this file from ``csrc/*.cu``; the
-compiled code targets exactly sm_103a (GB300).
+Produces ``libgb300gemm.so`` next to this file from ``csrc/*.cu`` (the GEMM)
+and ``csrc/ops/*.cu`` (the operators beside it); the compiled code targets exactly sm_103a (GB300).
 """
 from __future__ import annotations
 
@@ -27,12 +27,12 @@ def _nvcc() -> str:
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "ops", "*.cu")))
 
 
 def _inputs():
-    return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
-        os.path.join(INCLUDE, "gemm.h"), os.path.abspath(__file__)]
+    return (sources() + sorted(glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True)) +
+            sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
@@ -47,7 +47,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB_PATH
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17",
+    cmd = [_nvcc(), *ARCH_FLAGS, "-t", "0", "-O3", "-lineinfo", "-std=c++17",
            "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared",
            "-I", INCLUDE, "-I", CSRC, *sources(), "-o", tmp]
     if verbose:

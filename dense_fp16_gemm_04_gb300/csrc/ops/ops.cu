@@ -1,0 +1,750 @@
+// ops.cu -- host side of the C ABI declared in include/gemm_ops.h: argument
+// checks, tensor maps, the choice of kernel and the launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+
+#include "fused_kernel.cuh"
+#include "gemm_ops.h"
+#include "ortho_kernels.cuh"
+#include "reduce_kernels.cuh"
+#include "stream_kernel.cuh"
+
+struct gemm_ops_s {
+  int device = 0;
+  int num_sms = 0;
+  int max_pairs = 0;  // CTA pairs of the pair kernels that fit on the device at once
+  void* encode = nullptr;
+  uint32_t* d_err = nullptr;  // 4-word watchdog record
+  uint32_t last_err[4] = {0, 0, 0, 0};
+  uint64_t timeout_ns = 2000000000ull;
+  int32_t skip_kb = -1;
+  uint64_t launches = 0;
+};
+
+namespace {
+
+using namespace gb300::ops;
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+constexpr int64_t kMaxStreamTokens = 16;  // tokens of the streaming products of 16-bit weights
+constexpr int kGroupM = 8;
+
+// Tile configurations: a pair of CTAs on 256 x 256 sums, or one CTA on
+// 128 x 128 for problems of few tiles.
+template <int kEpi>
+using Pair = FusedCfg<2, 256, kEpi == kEpiStore ? 6 : 5, kEpi, kEpi == kEpiStore ? 2 : 4>;
+template <int kEpi>
+using Lone = FusedCfg<1, 128, 5, kEpi, 4>;
+
+struct DeviceGuard {
+  int prev = -1;
+  bool ok = false;
+  explicit DeviceGuard(int dev) {
+    if (cudaGetDevice(&prev) != cudaSuccess) return;
+    ok = (prev == dev) || (cudaSetDevice(dev) == cudaSuccess);
+  }
+  ~DeviceGuard() {
+    int cur = -1;
+    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+  }
+};
+
+bool on_device(const void* ptr, int dev) {
+  cudaPointerAttributes at;
+  if (cudaPointerGetAttributes(&at, ptr) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return at.type == cudaMemoryTypeDevice && at.device == dev;
+}
+
+// A buffer of a call: [rows] rows of `row` bytes, `pitch` bytes apart.
+struct Buf {
+  const void* p;
+  int64_t rows, row, pitch;
+  bool out;
+  size_t bytes() const { return rows > 0 && row > 0 ? static_cast<size_t>((rows - 1) * pitch + row) : 0; }
+};
+
+// Device memory throughout, and no output overlapping another buffer.
+template <int kN>
+gemm_status_t check_bufs(const gemm_ops_s* h, const Buf (&b)[kN]) {
+  for (int i = 0; i < kN; ++i) {
+    if (b[i].bytes() == 0) continue;
+    if (!b[i].p || !on_device(b[i].p, h->device)) return GEMM_ERR_INVALID_ARG;
+    if (!b[i].out) continue;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(b[i].p);
+    for (int j = 0; j < kN; ++j) {
+      if (j == i || b[j].bytes() == 0 || (b[j].out && j < i)) continue;
+      const uintptr_t y = reinterpret_cast<uintptr_t>(b[j].p);
+      if (x < y + b[j].bytes() && y < x + b[i].bytes()) return GEMM_ERR_INVALID_ARG;
+    }
+  }
+  return GEMM_OK;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool dim_ok(int64_t v) { return v >= 0 && v <= INT32_MAX; }
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int64_t cdiv(int64_t v, int64_t m) { return (v + m - 1) / m; }
+
+// ------------------------------------------------------------ tensor maps --
+// A stack of `z` row-major 16-bit matrices of rows x cols, rows `pitch` and
+// matrices `zstride` elements apart.
+struct Stack {
+  const void* p;
+  int64_t rows, cols, pitch, z, zstride;
+};
+
+bool make_map(const gemm_ops_s* h, CUtensorMap* m, const Stack& s, bool bf16, uint32_t box_cols,
+              uint32_t box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(s.cols), static_cast<cuuint64_t>(s.rows),
+                              static_cast<cuuint64_t>(s.z)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.pitch) * 2,
+                                 static_cast<cuuint64_t>(s.zstride) * 2};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  // Rows whose pitch is not a multiple of 128 bytes straddle L2 lines:
+  // promoting their requests to 256 bytes costs more than it saves.
+  const CUtensorMapL2promotion l2 = s.pitch % 64 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                                      : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+  return reinterpret_cast<EncodeTiledFn>(h->encode)(
+             m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(s.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ---------------------------------------------------------------- launches --
+template <class... Params, class... Args>
+gemm_status_t launch(gemm_ops_s* h, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                     int cluster, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  // Set-up may overlap the end of the previous kernel of the stream; every
+  // kernel waits for it before touching global memory.
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  ++h->launches;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return GEMM_OK;
+  cudaGetLastError();
+  return GEMM_ERR_CUDA;
+}
+
+// One product: acc[M, N] over segs x K, A and B stacks, their layouts.
+struct Product {
+  int64_t M, N, K;
+  Stack a, b;
+  bool a_mn, b_mn;  // stored [K, M] / [K, N]
+  bool bf16;
+  int64_t batch, segs, z_mul;
+};
+
+FusedArgs base_args(const gemm_ops_s* h, const Product& p) {
+  FusedArgs a = {};
+  a.M = static_cast<int32_t>(p.M);
+  a.N = static_cast<int32_t>(p.N);
+  a.num_kb = static_cast<int32_t>(cdiv(p.K, 64));
+  a.segs = static_cast<int32_t>(p.segs);
+  a.z_mul = static_cast<int32_t>(p.z_mul);
+  a.splits = 1;
+  a.group_m = kGroupM;
+  a.a_mn = p.a_mn;
+  a.b_mn = p.b_mn;
+  a.bf16 = p.bf16;
+  a.alpha = 1.0f;
+  a.err = h->d_err;
+  a.timeout_ns = h->timeout_ns;
+  a.skip_kb = h->skip_kb;
+  return a;
+}
+
+template <class Cfg>
+gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const Stack& c,
+                           const Stack& d, cudaStream_t stream) {
+  CUtensorMap ma, mb, mc, md;
+  const uint32_t b_rows = Cfg::kGlu && Cfg::kCtas == 1 ? Cfg::kBN / 2 : Cfg::kBRows;
+  bool ok = make_map(h, &ma, p.a, p.bf16, 64, p.a_mn ? 64 : Cfg::kBM) &&
+            make_map(h, &mb, p.b, p.bf16, 64, p.b_mn ? 64 : b_rows);
+  if (ok && c.p) ok = make_map(h, &mc, c, p.bf16, 64, 32);
+  if (ok && d.p)
+    ok = Cfg::kSym ? make_map(h, &md, d, p.bf16, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE)
+                   : make_map(h, &md, d, p.bf16, 64, 32);
+  if (!ok) return GEMM_ERR_CUDA;
+  if (!c.p) mc = ma;  // not used by this epilogue
+  if (!d.p) md = ma;
+  const int64_t tm = cdiv(p.M, Cfg::kTileM), tn = cdiv(p.N, Cfg::kOutN);
+  const int64_t per = Cfg::kSym ? tn * (tn + 1) / 2 : tm * tn;
+  const int64_t items = per * p.batch * a.splits;
+  if (items > INT32_MAX / 2) return GEMM_ERR_INVALID_ARG;
+  a.tiles_m = static_cast<int32_t>(tm);
+  a.tiles_n = static_cast<int32_t>(tn);
+  a.per_batch = static_cast<int32_t>(per);
+  a.items = static_cast<int32_t>(items);
+  const int64_t fit = Cfg::kCtas == 2 ? h->max_pairs : h->num_sms;
+  const int units = static_cast<int>(std::min<int64_t>(items, fit));
+  return launch(h, fused_kernel<Cfg>, dim3(units * Cfg::kCtas), dim3(Cfg::kThreads), Cfg::kSmemBytes,
+                Cfg::kCtas, stream, ma, mb, mc, md, a);
+}
+
+// Pairs when their 256-row tiles fill at least half of the device.
+bool use_pair(const gemm_ops_s* h, int64_t tiles) { return h->max_pairs > 0 && 2 * tiles >= h->max_pairs; }
+
+template <int kEpi>
+gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const Stack& c,
+                    const Stack& d, cudaStream_t stream) {
+  const int64_t tm = cdiv(p.M, 256), tn = cdiv(p.N, Pair<kEpi>::kOutN);
+  const int64_t tiles = (Pair<kEpi>::kSym ? tn * (tn + 1) / 2 : tm * tn) * p.batch;
+  return use_pair(h, tiles) ? launch_fused<Pair<kEpi>>(h, p, a, c, d, stream)
+                            : launch_fused<Lone<kEpi>>(h, p, a, c, d, stream);
+}
+
+// k-ranges per tile for a product of few 128 x 128 tiles: enough to give
+// every SM one, of at least four k-blocks each.
+int64_t splits_for(const gemm_ops_s* h, int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = cdiv(M, 128) * cdiv(N, 128);
+  if (2 * tiles > h->num_sms) return 1;
+  return std::max<int64_t>(1, std::min<int64_t>(h->num_sms / tiles, cdiv(K, 64) / 4));
+}
+
+size_t partial_bytes(const gemm_ops_s* h, int64_t M, int64_t N, int64_t K) {
+  const int64_t s = splits_for(h, M, N, K);
+  return s > 1 ? static_cast<size_t>(s) * M * N * 4 : 0;
+}
+
+// out = A B^T, rounded to 16 bits.
+gemm_status_t product(gemm_ops_s* h, const Product& p, void* out, int64_t ldo, void* partial,
+                      cudaStream_t stream) {
+  FusedArgs a = base_args(h, p);
+  const int64_t s = splits_for(h, p.M, p.N, p.K);
+  if (s == 1) return fused<kEpiStore>(h, p, a, {out, p.M, p.N, ldo, 1, p.M * ldo}, {}, stream);
+  a.splits = static_cast<int32_t>(s);
+  a.partial = static_cast<float*>(partial);
+  a.part_ld = p.N;
+  a.part_stride = p.M * p.N;
+  gemm_status_t st = launch_fused<Lone<kEpiPartial>>(h, p, a, {}, {}, stream);
+  if (st != GEMM_OK) return st;
+  ReduceArgs r = {a.partial, a.part_ld, a.part_stride, a.splits, a.M, a.N, a.bf16, 0,
+                  static_cast<uint16_t*>(out), ldo, nullptr, nullptr};
+  const int64_t blocks = std::min<int64_t>(cdiv(p.M * p.N / 4, 256), 8 * h->num_sms);
+  return launch(h, reduce_kernel<kReduceStore>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, stream, r);
+}
+
+// Few tokens through weights read once: warps share K so that the device has
+// about sixteen warps on every SM, each with at least 128 k.
+template <bool kW4, bool kGlu>
+gemm_status_t stream_product(gemm_ops_s* h, const StreamArgs& a, bool bf16, cudaStream_t stream) {
+  const int64_t tiles = cdiv(a.N, 16);
+  const int64_t tok = a.T > 8 ? 16 : 8;
+  int64_t warps = cdiv(16 * h->num_sms, tiles);
+  warps = std::min<int64_t>(warps <= 4 ? 4 : warps <= 8 ? 8 : 16, std::max<int64_t>(1, cdiv(a.K, 128)));
+  const size_t smem = static_cast<size_t>(warps) * (kGlu ? 2 : 1) * (tok / 8) * 128 * sizeof(float);
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(cdiv(a.T, tok)));
+  const dim3 block(static_cast<unsigned>(32 * warps));
+  if (bf16)
+    return tok == 8 ? launch(h, stream_kernel<true, kW4, kGlu, 1>, grid, block, smem, 1, stream, a)
+                    : launch(h, stream_kernel<true, kW4, kGlu, 2>, grid, block, smem, 1, stream, a);
+  return tok == 8 ? launch(h, stream_kernel<false, kW4, kGlu, 1>, grid, block, smem, 1, stream, a)
+                  : launch(h, stream_kernel<false, kW4, kGlu, 2>, grid, block, smem, 1, stream, a);
+}
+
+template <class Cfg>
+bool set_attr() {
+  return cudaFuncSetAttribute(fused_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Cfg::kSmemBytes) == cudaSuccess;
+}
+
+template <class Cfg>
+int max_clusters() {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(Cfg::kCtas, 1, 1);
+  cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = Cfg::kCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fused_kernel<Cfg>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+// Checks shared by the block's two passes.
+gemm_status_t check_ffn(const gemm_ops_s* h, int64_t T, int64_t D, int64_t F, gemm_act_t act,
+                        gemm_dtype_t dtype) {
+  if (!h || !dim_ok(T) || !dim_ok(D) || !dim_ok(F) || F > INT32_MAX / 2) return GEMM_ERR_INVALID_ARG;
+  if (act < GEMM_ACT_SILU || act > GEMM_ACT_RELU) return GEMM_ERR_INVALID_ARG;
+  if (dtype != GEMM_F16 && dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;
+  if (D % 8 != 0 || F % 8 != 0) return GEMM_ERR_ALIGNMENT;
+  return GEMM_OK;
+}
+
+gemm_status_t check_ld(int64_t ld, int64_t cols) {
+  if (ld < cols || ld > (1ll << 38)) return GEMM_ERR_INVALID_ARG;
+  return ld % 8 != 0 ? GEMM_ERR_ALIGNMENT : GEMM_OK;
+}
+
+// Offsets into the backward pass's workspace.
+struct BwdSpace {
+  size_t dgu, h, partial, total;
+};
+BwdSpace bwd_space(const gemm_ops_s* h, int64_t T, int64_t D, int64_t F) {
+  BwdSpace s;
+  s.dgu = 0;
+  s.h = up(T * 2 * F * 2, 256);
+  s.partial = s.h + up(T * F * 2, 256);
+  // dh, dx, dw_down and dw_in are summed one after the other.
+  size_t part = std::max(partial_bytes(h, T, F, D), partial_bytes(h, T, D, 2 * F));
+  part = std::max(part, std::max(partial_bytes(h, D, F, T), partial_bytes(h, 2 * F, D, T)));
+  s.total = s.partial + part;
+  return s;
+}
+
+struct OrthoSpace {
+  int64_t r, pitch, pitch_r;  // r: order of the Gram matrix
+  size_t x0, x1, p, q, partial, total;
+};
+OrthoSpace ortho_space(int64_t batch, int64_t M, int64_t N) {
+  OrthoSpace s;
+  s.r = std::min(M, N);
+  s.pitch = up(N, 8);
+  s.pitch_r = up(s.r, 8);
+  const size_t xb = up(batch * 2 * M * s.pitch * 2, 256), pb = up(batch * 2 * s.r * s.pitch_r * 2, 256);
+  s.x0 = 0;
+  s.x1 = xb;
+  s.p = 2 * xb;
+  s.q = s.p + pb;
+  s.partial = s.q + pb;
+  s.total = s.partial + up(batch * kNormBlocks * 4, 256);
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_ops_create(gemm_ops_t* out, int device) {
+  if (!out) return GEMM_ERR_INVALID_ARG;
+  *out = nullptr;
+  int ndev = 0;
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (device < 0 || device >= ndev) return GEMM_ERR_INVALID_ARG;
+  DeviceGuard g(device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  int major = 0, minor = 0, sms = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+    return GEMM_ERR_CUDA;
+  if (major != 10 || minor != 3) return GEMM_ERR_UNSUPPORTED_DEVICE;
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
+          cudaSuccess ||
+      q != cudaDriverEntryPointSuccess || !fn)
+    return GEMM_ERR_CUDA;
+  if (!set_attr<Pair<kEpiStore>>() || !set_attr<Pair<kEpiGlu>>() || !set_attr<Pair<kEpiGluBwd>>() ||
+      !set_attr<Pair<kEpiSplit>>() || !set_attr<Pair<kEpiSplitSym>>() || !set_attr<Lone<kEpiStore>>() ||
+      !set_attr<Lone<kEpiGlu>>() || !set_attr<Lone<kEpiGluBwd>>() || !set_attr<Lone<kEpiSplit>>() ||
+      !set_attr<Lone<kEpiSplitSym>>() || !set_attr<Lone<kEpiPartial>>())
+    return GEMM_ERR_CUDA;
+  gemm_ops_s* h = new (std::nothrow) gemm_ops_s();
+  if (!h) return GEMM_ERR_OOM;
+  h->device = device;
+  h->num_sms = sms;
+  h->encode = fn;
+  h->max_pairs = std::min({max_clusters<Pair<kEpiStore>>(), max_clusters<Pair<kEpiGlu>>(),
+                           max_clusters<Pair<kEpiGluBwd>>(), max_clusters<Pair<kEpiSplit>>(),
+                           max_clusters<Pair<kEpiSplitSym>>()});
+  if (cudaMalloc(&h->d_err, sizeof(h->last_err)) != cudaSuccess) {
+    delete h;
+    return GEMM_ERR_OOM;
+  }
+  if (cudaMemset(h->d_err, 0, sizeof(h->last_err)) != cudaSuccess) {
+    cudaFree(h->d_err);
+    delete h;
+    return GEMM_ERR_CUDA;
+  }
+  *out = h;
+  return GEMM_OK;
+}
+
+gemm_status_t gemm_ops_destroy(gemm_ops_t h) {
+  if (!h) return GEMM_OK;
+  DeviceGuard g(h->device);
+  if (h->d_err) cudaFree(h->d_err);
+  delete h;
+  return GEMM_OK;
+}
+
+gemm_status_t gemm_ops_check_error(gemm_ops_t h) {
+  if (!h) return GEMM_ERR_INVALID_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  uint32_t rec[4] = {0, 0, 0, 0};
+  if (cudaDeviceSynchronize() != cudaSuccess) return GEMM_ERR_CUDA;
+  if (cudaMemcpy(rec, h->d_err, sizeof(rec), cudaMemcpyDeviceToHost) != cudaSuccess)
+    return GEMM_ERR_CUDA;
+  if (rec[0] == 0) return GEMM_OK;
+  std::memcpy(h->last_err, rec, sizeof(rec));
+  if (cudaMemset(h->d_err, 0, sizeof(rec)) != cudaSuccess) return GEMM_ERR_CUDA;
+  return static_cast<gemm_status_t>(rec[0]);
+}
+
+gemm_status_t gemm_ops_last_error_detail(gemm_ops_t h, uint32_t detail[4]) {
+  if (!h || !detail) return GEMM_ERR_INVALID_ARG;
+  std::memcpy(detail, h->last_err, sizeof(h->last_err));
+  return GEMM_OK;
+}
+
+gemm_status_t gemm_ops_set_watchdog(gemm_ops_t h, uint64_t timeout_ns, int32_t skip_k_block) {
+  if (!h || skip_k_block < -1) return GEMM_ERR_INVALID_ARG;
+  h->timeout_ns = timeout_ns ? timeout_ns : kDefaultTimeoutNs;
+  h->skip_kb = skip_k_block;
+  return GEMM_OK;
+}
+
+uint64_t gemm_ops_launch_count(gemm_ops_t h) { return h ? h->launches : 0; }
+
+size_t gemm_gated_ffn_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t F) {
+  if (!h || T <= 0 || D <= 0 || F <= 0) return 0;
+  size_t s = up(T * F * 2, 256);
+  if (T > kMaxStreamTokens)
+    s += std::max(partial_bytes(h, T, 2 * F, D), partial_bytes(h, T, D, F));
+  return s;
+}
+
+gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const void* w_in,
+                             int64_t ldw_in, const void* w_down, int64_t ldw_down, void* y,
+                             int64_t ldy, void* gu, void* workspace, size_t workspace_bytes, int64_t T,
+                             int64_t D, int64_t F, gemm_act_t act, gemm_dtype_t dtype, void* stream) {
+  gemm_status_t st = check_ffn(h, T, D, F, act, dtype);
+  if (st != GEMM_OK) return st;
+  if (T == 0 || D == 0) return GEMM_OK;
+  for (auto [ld, cols] : {std::pair<int64_t, int64_t>(ldx, D), {ldw_in, D}, {ldw_down, F}, {ldy, D}})
+    if ((st = check_ld(ld, cols)) != GEMM_OK) return st;
+  if (!aligned16(x) || !aligned16(w_in) || !aligned16(w_down) || !aligned16(y) || !aligned16(gu) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return GEMM_ERR_ALIGNMENT;
+  const size_t need = gemm_gated_ffn_workspace(h, T, D, F);
+  if (workspace_bytes < need) return GEMM_ERR_INVALID_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  const Buf bufs[] = {{x, T, D * 2, ldx * 2, false},
+                      {w_in, 2 * F, D * 2, ldw_in * 2, false},
+                      {w_down, F > 0 ? D : 0, F * 2, ldw_down * 2, false},
+                      {y, T, D * 2, ldy * 2, true},
+                      {gu, gu ? T : 0, 4 * F, 4 * F, true},
+                      {workspace, 1, static_cast<int64_t>(need), static_cast<int64_t>(need), true}};
+  if ((st = check_bufs(h, bufs)) != GEMM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (F == 0)
+    return cudaMemset2DAsync(y, ldy * 2, 0, D * 2, T, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  const bool bf16 = dtype == GEMM_BF16;
+  void* hid = workspace;
+  if (T <= kMaxStreamTokens) {
+    StreamArgs a = {static_cast<const uint16_t*>(x), ldx, w_in, ldw_in, nullptr, nullptr,
+                    static_cast<uint16_t*>(hid), F, static_cast<uint16_t*>(gu), static_cast<int32_t>(T),
+                    static_cast<int32_t>(F), static_cast<int32_t>(D), 0, act};
+    if ((st = stream_product<false, true>(h, a, bf16, s)) != GEMM_OK) return st;
+    StreamArgs b = {static_cast<const uint16_t*>(hid), F, w_down, ldw_down, nullptr, nullptr,
+                    static_cast<uint16_t*>(y), ldy, nullptr, static_cast<int32_t>(T),
+                    static_cast<int32_t>(D), static_cast<int32_t>(F), 0, act};
+    return stream_product<false, false>(h, b, bf16, s);
+  }
+  void* partial = static_cast<char*>(workspace) + up(T * F * 2, 256);
+  const Stack xs = {x, T, D, ldx, 1, T * ldx};
+  const int64_t split = splits_for(h, T, 2 * F, D);
+  if (split == 1) {
+    const Product p = {T, F, D, xs, {w_in, F, D, ldw_in, 2, F * ldw_in}, false, false, bf16, 1, 1, 0};
+    FusedArgs a = base_args(h, p);
+    a.act = act;
+    a.save = gu != nullptr;
+    const Stack keep = {gu, T, F, 2 * F, 2, F};
+    st = fused<kEpiGlu>(h, p, a, {hid, T, F, F, 1, T * F}, gu ? keep : Stack{}, s);
+  } else {
+    const Product p = {T, 2 * F, D, xs, {w_in, 2 * F, D, ldw_in, 1, 2 * F * ldw_in}, false, false, bf16, 1, 1, 0};
+    FusedArgs a = base_args(h, p);
+    a.splits = static_cast<int32_t>(split);
+    a.partial = static_cast<float*>(partial);
+    a.part_ld = 2 * F;
+    a.part_stride = T * 2 * F;
+    st = launch_fused<Lone<kEpiPartial>>(h, p, a, {}, {}, s);
+    if (st != GEMM_OK) return st;
+    ReduceArgs r = {a.partial, a.part_ld, a.part_stride, a.splits, a.M, static_cast<int32_t>(F), a.bf16, act,
+                    static_cast<uint16_t*>(hid), F, static_cast<uint16_t*>(gu), nullptr};
+    const int64_t blocks = std::min<int64_t>(cdiv(T * F / 4, 256), 8 * h->num_sms);
+    st = launch(h, reduce_kernel<kReduceGlu>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, s, r);
+  }
+  if (st != GEMM_OK) return st;
+  const Product p = {T, D, F, {hid, T, F, F, 1, T * F}, {w_down, D, F, ldw_down, 1, D * ldw_down},
+                     false, false, bf16, 1, 1, 0};
+  return product(h, p, y, ldy, partial, s);
+}
+
+size_t gemm_gated_ffn_backward_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t F) {
+  if (!h || T <= 0 || D <= 0 || F <= 0) return 0;
+  return bwd_space(h, T, D, F).total;
+}
+
+gemm_status_t gemm_gated_ffn_backward(gemm_ops_t h, const void* dy, int64_t lddy, const void* x,
+                                      int64_t ldx, const void* w_in, int64_t ldw_in,
+                                      const void* w_down, int64_t ldw_down, const void* gu, void* dx,
+                                      int64_t lddx, void* dw_in, void* dw_down, void* workspace,
+                                      size_t workspace_bytes, int64_t T, int64_t D, int64_t F,
+                                      gemm_act_t act, gemm_dtype_t dtype, void* stream) {
+  gemm_status_t st = check_ffn(h, T, D, F, act, dtype);
+  if (st != GEMM_OK) return st;
+  if (D == 0) return GEMM_OK;
+  for (auto [ld, cols] :
+       {std::pair<int64_t, int64_t>(lddy, D), {ldx, D}, {ldw_in, D}, {ldw_down, F}, {lddx, D}})
+    if ((st = check_ld(ld, cols)) != GEMM_OK) return st;
+  for (const void* p : {dy, x, w_in, w_down, gu, static_cast<const void*>(dx), static_cast<const void*>(dw_in),
+                        static_cast<const void*>(dw_down)})
+    if (!aligned16(p)) return GEMM_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255) return GEMM_ERR_ALIGNMENT;
+  const size_t need = gemm_gated_ffn_backward_workspace(h, T, D, F);
+  if (workspace_bytes < need) return GEMM_ERR_INVALID_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  const int64_t wrows = F > 0 ? D : 0;
+  const Buf bufs[] = {{dy, T, D * 2, lddy * 2, false},
+                      {x, T, D * 2, ldx * 2, false},
+                      {w_in, 2 * F, D * 2, ldw_in * 2, false},
+                      {w_down, wrows, F * 2, ldw_down * 2, false},
+                      {gu, F > 0 ? T : 0, 4 * F, 4 * F, false},
+                      {dx, T, D * 2, lddx * 2, true},
+                      {dw_in, 2 * F, D * 2, D * 2, true},
+                      {dw_down, wrows, F * 2, F * 2, true},
+                      {workspace, need ? 1 : 0, static_cast<int64_t>(need), static_cast<int64_t>(need), true}};
+  if ((st = check_bufs(h, bufs)) != GEMM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (F == 0)
+    return T == 0 || cudaMemset2DAsync(dx, lddx * 2, 0, D * 2, T, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  if (T == 0)  // no token, no gradient
+    return cudaMemsetAsync(dw_in, 0, 4 * F * D, s) == cudaSuccess &&
+                   cudaMemsetAsync(dw_down, 0, 2 * F * D, s) == cudaSuccess
+               ? GEMM_OK
+               : GEMM_ERR_CUDA;
+  const bool bf16 = dtype == GEMM_BF16;
+  const BwdSpace sp = bwd_space(h, T, D, F);
+  char* ws = static_cast<char*>(workspace);
+  uint16_t* dgu = reinterpret_cast<uint16_t*>(ws + sp.dgu);
+  uint16_t* hid = reinterpret_cast<uint16_t*>(ws + sp.h);
+  void* partial = ws + sp.partial;
+  const Stack dys = {dy, T, D, lddy, 1, T * lddy};
+  {
+    // dh = dy Wd (Wd is stored [K, N] here), then dg, du and h.
+    const Product p = {T, F, D, dys, {w_down, D, F, ldw_down, 1, D * ldw_down}, false, true, bf16, 1, 1, 0};
+    FusedArgs a = base_args(h, p);
+    a.act = act;
+    const int64_t split = splits_for(h, T, F, D);
+    if (split == 1) {
+      a.src = static_cast<const uint16_t*>(gu);
+      a.src_ld = 2 * F;
+      st = fused<kEpiGluBwd>(h, p, a, {hid, T, F, F, 1, T * F}, {dgu, T, F, 2 * F, 2, F}, s);
+    } else {
+      a.splits = static_cast<int32_t>(split);
+      a.partial = static_cast<float*>(partial);
+      a.part_ld = F;
+      a.part_stride = T * F;
+      st = launch_fused<Lone<kEpiPartial>>(h, p, a, {}, {}, s);
+      if (st != GEMM_OK) return st;
+      ReduceArgs r = {a.partial, a.part_ld, a.part_stride, a.splits, a.M, a.N, a.bf16, act,
+                      hid, F, const_cast<uint16_t*>(static_cast<const uint16_t*>(gu)), dgu};
+      const int64_t blocks = std::min<int64_t>(cdiv(T * F / 4, 256), 8 * h->num_sms);
+      st = launch(h, reduce_kernel<kReduceGluBwd>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, s, r);
+    }
+    if (st != GEMM_OK) return st;
+  }
+  // dw_down [D, F] = dy^T h; dx = [dg du] w_in; dw_in [2F, D] = [dg du]^T x.
+  const Stack hs = {hid, T, F, F, 1, T * F}, dgus = {dgu, T, 2 * F, 2 * F, 1, T * 2 * F};
+  const Product pd = {D, F, T, dys, hs, true, true, bf16, 1, 1, 0};
+  if ((st = product(h, pd, dw_down, F, partial, s)) != GEMM_OK) return st;
+  const Product px = {T, D, 2 * F, dgus, {w_in, 2 * F, D, ldw_in, 1, 2 * F * ldw_in}, false, true, bf16, 1, 1, 0};
+  if ((st = product(h, px, dx, lddx, partial, s)) != GEMM_OK) return st;
+  const Product pi = {2 * F, D, T, dgus, {x, T, D, ldx, 1, T * ldx}, true, true, bf16, 1, 1, 0};
+  return product(h, pi, dw_in, D, partial, s);
+}
+
+static gemm_status_t w4_run(gemm_ops_t h, const void* x, int64_t ldx, const void* codes,
+                            const void* scales, const void* zeros, void* y, int64_t ldy, int64_t T,
+                            int64_t N, int64_t K, int64_t group, gemm_act_t act, gemm_dtype_t dtype,
+                            bool gated, void* stream) {
+  if (!h || !dim_ok(T) || !dim_ok(N) || !dim_ok(K) || N > INT32_MAX / 2 || T > 16 * 65535)
+    return GEMM_ERR_INVALID_ARG;
+  if (act < GEMM_ACT_SILU || act > GEMM_ACT_RELU) return GEMM_ERR_INVALID_ARG;
+  if (dtype != GEMM_F16 && dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;
+  if (group < 32 || group > (1 << 30) || (group & (group - 1)) != 0 || K % group != 0)
+    return GEMM_ERR_INVALID_ARG;
+  if (T == 0 || N == 0) return GEMM_OK;
+  if (ldy < N) return GEMM_ERR_INVALID_ARG;
+  gemm_status_t st = check_ld(ldx, K);
+  if (st != GEMM_OK) return st;
+  if (!aligned16(x) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 1) ||
+      (reinterpret_cast<uintptr_t>(y) & 1))
+    return GEMM_ERR_ALIGNMENT;
+  DeviceGuard g(h->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  const int64_t rows = gated ? 2 * N : N, groups = K / group;
+  const Buf bufs[] = {{x, T, K * 2, ldx * 2, false},
+                      {codes, rows, K / 2, K / 2, false},
+                      {scales, rows, groups * 2, groups * 2, false},
+                      {zeros, zeros ? rows : 0, groups, groups, false},
+                      {y, T, N * 2, ldy * 2, true}};
+  if ((st = check_bufs(h, bufs)) != GEMM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (K == 0)
+    return cudaMemset2DAsync(y, ldy * 2, 0, N * 2, T, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  int shift = 0;
+  while ((1ll << shift) < group) ++shift;
+  const StreamArgs a = {static_cast<const uint16_t*>(x), ldx, codes, K / 2,
+                        static_cast<const uint16_t*>(scales), static_cast<const uint8_t*>(zeros),
+                        static_cast<uint16_t*>(y), ldy, nullptr, static_cast<int32_t>(T),
+                        static_cast<int32_t>(N), static_cast<int32_t>(K), shift, act};
+  const bool bf16 = dtype == GEMM_BF16;
+  return gated ? stream_product<true, true>(h, a, bf16, s) : stream_product<true, false>(h, a, bf16, s);
+}
+
+gemm_status_t gemm_w4_linear(gemm_ops_t h, const void* x, int64_t ldx, const void* codes,
+                             const void* scales, const void* zeros, void* y, int64_t ldy, int64_t T,
+                             int64_t N, int64_t K, int64_t group, gemm_dtype_t dtype, void* stream) {
+  return w4_run(h, x, ldx, codes, scales, zeros, y, ldy, T, N, K, group, GEMM_ACT_SILU, dtype, false, stream);
+}
+
+gemm_status_t gemm_w4_gated(gemm_ops_t h, const void* x, int64_t ldx, const void* codes,
+                            const void* scales, const void* zeros, void* y, int64_t ldy, int64_t T,
+                            int64_t N, int64_t K, int64_t group, gemm_act_t act, gemm_dtype_t dtype,
+                            void* stream) {
+  return w4_run(h, x, ldx, codes, scales, zeros, y, ldy, T, N, K, group, act, dtype, true, stream);
+}
+
+size_t gemm_orthogonalize_workspace(gemm_ops_t h, int64_t batch, int64_t M, int64_t N) {
+  if (!h || batch <= 0 || M <= 0 || N <= 0) return 0;
+  return ortho_space(batch, M, N).total;
+}
+
+gemm_status_t gemm_orthogonalize(gemm_ops_t h, const void* m, int64_t ldm, int64_t stride_m, void* out,
+                                 int64_t ldo, int64_t stride_o, void* workspace, size_t workspace_bytes,
+                                 int64_t batch, int64_t M, int64_t N, int32_t steps,
+                                 const float coeffs[3], float eps, gemm_dtype_t in_dtype,
+                                 gemm_dtype_t out_dtype, void* stream) {
+  if (!h || !coeffs || !dim_ok(batch) || !dim_ok(M) || !dim_ok(N) || batch > 65535 || steps < 0)
+    return GEMM_ERR_INVALID_ARG;
+  for (gemm_dtype_t d : {in_dtype, out_dtype})
+    if (d != GEMM_F16 && d != GEMM_BF16 && d != GEMM_F32) return GEMM_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f)) return GEMM_ERR_INVALID_ARG;
+  if (batch == 0 || M == 0 || N == 0) return GEMM_OK;
+  if (ldm < N || ldo < N || (batch > 1 && (stride_m < 0 || stride_o < (M - 1) * ldo + N)))
+    return GEMM_ERR_INVALID_ARG;
+  const int64_t ei = in_dtype == GEMM_F32 ? 4 : 2, eo = out_dtype == GEMM_F32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(m) % ei) || (reinterpret_cast<uintptr_t>(out) % eo) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return GEMM_ERR_ALIGNMENT;
+  const OrthoSpace sp = ortho_space(batch, M, N);
+  if (workspace_bytes < sp.total) return GEMM_ERR_INVALID_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  const int64_t one_m = ((M - 1) * ldm + N) * ei, one_o = ((M - 1) * ldo + N) * eo;
+  const Buf bufs[] = {{m, batch, one_m, batch > 1 ? stride_m * ei : 0, false},
+                      {out, batch, one_o, batch > 1 ? stride_o * eo : 0, true},
+                      {workspace, 1, static_cast<int64_t>(sp.total), 0, true}};
+  gemm_status_t st = check_bufs(h, bufs);
+  if (st != GEMM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // X, P and Q = b P + c P^2 are held scaled by these powers of two.
+  constexpr float kSx = 8192.0f, kSp = 2048.0f, kSq = 1024.0f;
+  char* ws = static_cast<char*>(workspace);
+  uint16_t* x[2] = {reinterpret_cast<uint16_t*>(ws + sp.x0), reinterpret_cast<uint16_t*>(ws + sp.x1)};
+  uint16_t* P = reinterpret_cast<uint16_t*>(ws + sp.p);
+  uint16_t* Q = reinterpret_cast<uint16_t*>(ws + sp.q);
+  OrthoArgs oa = {};
+  oa.in = m;
+  oa.ld = ldm;
+  oa.bs = batch > 1 ? stride_m : 0;
+  oa.dtype = in_dtype;
+  oa.rows = static_cast<int32_t>(M);
+  oa.cols = static_cast<int32_t>(N);
+  oa.x = x[0];
+  oa.pitch = sp.pitch;
+  oa.partial = reinterpret_cast<float*>(ws + sp.partial);
+  oa.eps = eps;
+  oa.scale = kSx;
+  const unsigned by = static_cast<unsigned>(batch);
+  if ((st = launch(h, ortho_norm, dim3(kNormBlocks, by), dim3(256), 0, 1, s, oa)) != GEMM_OK) return st;
+  const unsigned bx = static_cast<unsigned>(std::min<int64_t>(M, cdiv(8 * h->num_sms, batch)));
+  if ((st = launch(h, ortho_split, dim3(bx, by), dim3(256), 0, 1, s, oa)) != GEMM_OK) return st;
+  const bool wide = M <= N;
+  const int64_t r = sp.r, xpart = M * sp.pitch, ppart = r * sp.pitch_r;
+  const float ca = coeffs[0], cb = coeffs[1], cc = coeffs[2];
+  const Stack ps = {P, r, r, sp.pitch_r, 2 * batch, ppart}, qs = {Q, r, r, sp.pitch_r, 2 * batch, ppart};
+  int cur = 0;
+  for (int i = 0; i < steps; ++i, cur ^= 1) {
+    const Stack xs = {x[cur], M, N, sp.pitch, 2 * batch, xpart};
+    const Stack xn = {x[cur ^ 1], M, N, sp.pitch, 2 * batch, xpart};
+    {  // P = X X^T (X^T X)
+      const Product p = {r, r, wide ? N : M, xs, xs, !wide, !wide, false, batch, 3, 2};
+      FusedArgs a = base_args(h, p);
+      a.alpha = kSp / (kSx * kSx);
+      if ((st = fused<kEpiSplitSym>(h, p, a, ps, ps, s)) != GEMM_OK) return st;
+    }
+    {  // Q = c P P + b P
+      const Product p = {r, r, r, ps, ps, false, false, false, batch, 3, 2};
+      FusedArgs a = base_args(h, p);
+      a.alpha = cc * (kSq / (kSp * kSp));
+      a.beta = cb * (kSq / kSp);
+      a.src = P;
+      a.src_ld = sp.pitch_r;
+      a.src_part = ppart;
+      if ((st = fused<kEpiSplitSym>(h, p, a, qs, qs, s)) != GEMM_OK) return st;
+    }
+    {  // X <- Q X + a X (X Q + a X); Q is symmetric
+      const Product p = wide ? Product{M, N, r, qs, xs, false, true, false, batch, 3, 2}
+                             : Product{M, N, r, xs, qs, false, false, false, batch, 3, 2};
+      FusedArgs a = base_args(h, p);
+      a.alpha = 1.0f / kSq;
+      a.beta = ca;
+      a.src = x[cur];
+      a.src_ld = sp.pitch;
+      a.src_part = xpart;
+      if ((st = fused<kEpiSplit>(h, p, a, xn, {}, s)) != GEMM_OK) return st;
+    }
+  }
+  oa.x = x[cur];
+  oa.dtype = out_dtype;
+  oa.out = out;
+  oa.ld_out = ldo;
+  oa.bs_out = batch > 1 ? stride_o : 0;
+  return launch(h, ortho_join, dim3(bx, by), dim3(256), 0, 1, s, oa);
+}
+
+}  // extern "C"
