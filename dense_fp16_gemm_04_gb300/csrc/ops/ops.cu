@@ -253,22 +253,117 @@ gemm_status_t product(gemm_ops_s* h, const Product& p, void* out, int64_t ldo, v
   return launch(h, reduce_kernel<kReduceStore>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, stream, r);
 }
 
-// Few tokens through weights read once: warps share K so that the device has
-// about sixteen warps on every SM, each with at least 128 k.
-template <bool kW4, bool kGlu>
-gemm_status_t stream_product(gemm_ops_s* h, const StreamArgs& a, bool bf16, cudaStream_t stream) {
-  const int64_t tiles = cdiv(a.N, 16);
-  const int64_t tok = a.T > 8 ? 16 : 8;
-  int64_t warps = cdiv(16 * h->num_sms, tiles);
-  warps = std::min<int64_t>(warps <= 4 ? 4 : warps <= 8 ? 8 : 16, std::max<int64_t>(1, cdiv(a.K, 128)));
-  const size_t smem = static_cast<size_t>(warps) * (kGlu ? 2 : 1) * (tok / 8) * 128 * sizeof(float);
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(cdiv(a.T, tok)));
-  const dim3 block(static_cast<unsigned>(32 * warps));
-  if (bf16)
-    return tok == 8 ? launch(h, stream_kernel<true, kW4, kGlu, 1>, grid, block, smem, 1, stream, a)
-                    : launch(h, stream_kernel<true, kW4, kGlu, 2>, grid, block, smem, 1, stream, a);
-  return tok == 8 ? launch(h, stream_kernel<false, kW4, kGlu, 1>, grid, block, smem, 1, stream, a)
-                  : launch(h, stream_kernel<false, kW4, kGlu, 2>, grid, block, smem, 1, stream, a);
+// How a product of few tokens is laid out: warps per CTA, CTAs per k-slice,
+// k-slices, and the CTA's shared memory.
+struct StreamPlan {
+  int64_t warps, ctas, slices, ring;
+  size_t smem;
+};
+
+constexpr size_t kStreamSmem = 226 * 1024;
+
+// 8-column tiles per CTA: 1, 2 or 4 (16-bit weights and whole groups: 8 tokens
+// each, so two make the most a call is expected to have).
+template <int kW>
+int stream_tiles(int64_t T) {
+  const int64_t n = cdiv(T, stream_tokens(kW));
+  return n <= 1 ? 1 : n <= 2 || stream_groups(kW) == 1 ? 2 : 4;
+}
+
+template <int kW, bool kGlu>
+StreamPlan stream_plan(const gemm_ops_s* h, int64_t T, int64_t N, int64_t K) {
+  StreamPlan p;
+  const int64_t bk = stream_block_k(kW), blocks = cdiv(K, bk), tiles = cdiv(N, stream_tile(kGlu));
+  const int64_t nt = stream_tiles<kW>(T), held = std::min(T, nt * stream_tokens(kW));
+  // Enough warps that each keeps a block or two of a tile; the rest of the
+  // parallelism comes from tiles, or from cutting K where they are few.
+  p.warps = blocks >= 16 ? 16 : blocks >= 8 ? 8 : 4;
+  p.ring = kStreamMaxRing;
+  p.slices = std::max<int64_t>(1, std::min(h->num_sms / tiles, blocks / (2 * p.warps)));
+  auto smem = [&] {  // the warps' sums, their blocks in flight, x and its sums
+    return static_cast<size_t>(p.warps) * (2 * nt * 128 * sizeof(float) + p.ring * stream_slot_bytes(kW)) +
+           static_cast<size_t>(cdiv(blocks, p.slices)) * (bk * held * 2 + (kW != kW16 ? 8 * nt * sizeof(float) : 0));
+  };
+  while (p.ring > 2 && smem() > kStreamSmem) --p.ring;
+  while (p.slices < blocks && smem() > kStreamSmem) ++p.slices;
+  while (p.ring < kStreamMaxRing) {  // what the slices freed
+    ++p.ring;
+    if (smem() > kStreamSmem) {
+      --p.ring;
+      break;
+    }
+  }
+  p.smem = smem();
+  const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(16 / p.warps, kStreamSmem / p.smem));
+  p.ctas = std::min(tiles, std::max<int64_t>(1, per_sm * h->num_sms / p.slices));
+  return p;
+}
+
+// The kernel's offsets into W are 32 bits: rows of one launch, 4 GB at most and
+// a whole number of tiles (a row has at most kMaxStreamRow bytes).
+constexpr int64_t kMaxStreamRow = 1 << 27;
+int64_t stream_rows(int64_t row_bytes) { return (1ll << 32) / row_bytes / 32 * 32; }
+
+template <int kW, bool kGlu>
+size_t stream_partial_bytes(const gemm_ops_s* h, int64_t T, int64_t N, int64_t K) {
+  if (kW != kW16) N = std::min(N, stream_rows(K / 2));
+  const StreamPlan p = stream_plan<kW, kGlu>(h, T, N, K);
+  return p.slices > 1 ? static_cast<size_t>(p.slices) * T * N * (kGlu ? 2 : 1) * 4 : 0;
+}
+
+// Whether a block's weights (rows ld 16-bit elements apart) suit one launch.
+bool stream_fits(int64_t rows, int64_t ld) { return 2 * ld <= kMaxStreamRow && rows <= stream_rows(2 * ld); }
+
+typedef void (*StreamKernel)(const StreamArgs);
+
+template <int kW, bool kGlu>
+StreamKernel stream_variant(bool bf16, int nt) {
+  if (nt == 1) return bf16 ? stream_kernel<true, kW, kGlu, 1> : stream_kernel<false, kW, kGlu, 1>;
+  if constexpr (stream_groups(kW) > 1)
+    if (nt == 4) return bf16 ? stream_kernel<true, kW, kGlu, 4> : stream_kernel<false, kW, kGlu, 4>;
+  return bf16 ? stream_kernel<true, kW, kGlu, 2> : stream_kernel<false, kW, kGlu, 2>;
+}
+
+// The products of a.cols columns; `a` is complete but for N and the up rows.
+template <int kW, bool kGlu>
+gemm_status_t stream_product(gemm_ops_s* h, StreamArgs a, bool bf16, cudaStream_t stream) {
+  const int64_t row_bytes = a.ldw * (kW == kW16 ? 2 : 1), groups = kW == kW16 ? 0 : a.K >> a.group_shift;
+  a.up_w = a.cols * row_bytes;
+  a.up_s = a.cols * groups;
+  const int64_t most = stream_rows(row_bytes), cols = a.cols;
+  const int nt = stream_tiles<kW>(a.T);
+  const StreamPlan p = stream_plan<kW, kGlu>(h, a.T, std::min(cols, most), a.K);
+  a.ring = static_cast<int32_t>(p.ring);
+  for (int64_t n0 = 0; n0 < cols; n0 += most) {
+    a.N = static_cast<int32_t>(std::min(most, cols - n0));
+    const int64_t ctas = std::min<int64_t>(p.ctas, cdiv(a.N, stream_tile(kGlu)));
+    const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(p.slices),
+                    static_cast<unsigned>(cdiv(a.T, nt * stream_tokens(kW))));
+    const dim3 block(static_cast<unsigned>(32 * p.warps));
+    gemm_status_t st = launch(h, stream_variant<kW, kGlu>(bf16, nt), grid, block, p.smem, 1, stream, a);
+    if (st == GEMM_OK && p.slices > 1) {
+      const int64_t n = std::min<int64_t>(cdiv(static_cast<int64_t>(a.T) * a.N, 256), 8 * h->num_sms);
+      st = launch(h, stream_reduce<kGlu>, dim3(static_cast<unsigned>(n)), dim3(256), 0, 1, stream, a,
+                  static_cast<int32_t>(p.slices), static_cast<int32_t>(bf16));
+    }
+    if (st != GEMM_OK) return st;
+    a.w = static_cast<const char*>(a.w) + most * row_bytes;
+    a.y += most;
+    if (a.gu) a.gu += most;
+    if (a.scales) a.scales += most * groups;
+    if (a.zeros) a.zeros += most * groups;
+  }
+  return GEMM_OK;
+}
+
+template <int kW, bool kGlu>
+bool set_stream_attr() {
+  for (bool bf16 : {false, true})
+    for (int nt : {1, 2, 4})
+      if (cudaFuncSetAttribute(stream_variant<kW, kGlu>(bf16, nt), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kStreamSmem) != cudaSuccess)
+        return false;
+  return true;
 }
 
 template <class Cfg>
@@ -309,7 +404,7 @@ gemm_status_t check_ffn(const gemm_ops_s* h, int64_t T, int64_t D, int64_t F, ge
 }
 
 gemm_status_t check_ld(int64_t ld, int64_t cols) {
-  if (ld < cols || ld > (1ll << 38)) return GEMM_ERR_INVALID_ARG;
+  if (ld < cols || ld >= (1ll << 30)) return GEMM_ERR_INVALID_ARG;
   return ld % 8 != 0 ? GEMM_ERR_ALIGNMENT : GEMM_OK;
 }
 
@@ -375,7 +470,11 @@ gemm_status_t gemm_ops_create(gemm_ops_t* out, int device) {
   if (!set_attr<Pair<kEpiStore>>() || !set_attr<Pair<kEpiGlu>>() || !set_attr<Pair<kEpiGluBwd>>() ||
       !set_attr<Pair<kEpiSplit>>() || !set_attr<Pair<kEpiSplitSym>>() || !set_attr<Lone<kEpiStore>>() ||
       !set_attr<Lone<kEpiGlu>>() || !set_attr<Lone<kEpiGluBwd>>() || !set_attr<Lone<kEpiSplit>>() ||
-      !set_attr<Lone<kEpiSplitSym>>() || !set_attr<Lone<kEpiPartial>>())
+      !set_attr<Lone<kEpiSplitSym>>() || !set_attr<Lone<kEpiPartial>>() ||
+      !set_stream_attr<kW16, false>() || !set_stream_attr<kW16, true>() ||
+      !set_stream_attr<kW4G32, false>() || !set_stream_attr<kW4G32, true>() ||
+      !set_stream_attr<kW4G64, false>() || !set_stream_attr<kW4G64, true>() ||
+      !set_stream_attr<kW4G128, false>() || !set_stream_attr<kW4G128, true>())
     return GEMM_ERR_CUDA;
   gemm_ops_s* h = new (std::nothrow) gemm_ops_s();
   if (!h) return GEMM_ERR_OOM;
@@ -438,9 +537,10 @@ uint64_t gemm_ops_launch_count(gemm_ops_t h) { return h ? h->launches : 0; }
 size_t gemm_gated_ffn_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t F) {
   if (!h || T <= 0 || D <= 0 || F <= 0) return 0;
   size_t s = up(T * F * 2, 256);
-  if (T > kMaxStreamTokens)
-    s += std::max(partial_bytes(h, T, 2 * F, D), partial_bytes(h, T, D, F));
-  return s;
+  // Few tokens whose weights do not suit the streaming kernel take the other way.
+  if (T <= kMaxStreamTokens)
+    s += std::max(stream_partial_bytes<kW16, true>(h, T, F, D), stream_partial_bytes<kW16, false>(h, T, D, F));
+  return s + std::max(partial_bytes(h, T, 2 * F, D), partial_bytes(h, T, D, F));
 }
 
 gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const void* w_in,
@@ -471,17 +571,33 @@ gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const voi
     return cudaMemset2DAsync(y, ldy * 2, 0, D * 2, T, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
   const bool bf16 = dtype == GEMM_BF16;
   void* hid = workspace;
-  if (T <= kMaxStreamTokens) {
-    StreamArgs a = {static_cast<const uint16_t*>(x), ldx, w_in, ldw_in, nullptr, nullptr,
-                    static_cast<uint16_t*>(hid), F, static_cast<uint16_t*>(gu), static_cast<int32_t>(T),
-                    static_cast<int32_t>(F), static_cast<int32_t>(D), 0, act};
-    if ((st = stream_product<false, true>(h, a, bf16, s)) != GEMM_OK) return st;
-    StreamArgs b = {static_cast<const uint16_t*>(hid), F, w_down, ldw_down, nullptr, nullptr,
-                    static_cast<uint16_t*>(y), ldy, nullptr, static_cast<int32_t>(T),
-                    static_cast<int32_t>(D), static_cast<int32_t>(F), 0, act};
-    return stream_product<false, false>(h, b, bf16, s);
-  }
   void* partial = static_cast<char*>(workspace) + up(T * F * 2, 256);
+  if (T <= kMaxStreamTokens && stream_fits(F, ldw_in) && stream_fits(D, ldw_down)) {
+    StreamArgs a = {};
+    a.x = static_cast<const uint16_t*>(x);
+    a.ldx = ldx;
+    a.w = w_in;
+    a.ldw = ldw_in;
+    a.y = static_cast<uint16_t*>(hid);
+    a.ldy = F;
+    a.gu = static_cast<uint16_t*>(gu);
+    a.partial = static_cast<float*>(partial);
+    a.T = static_cast<int32_t>(T);
+    a.K = static_cast<int32_t>(D);
+    a.cols = static_cast<int32_t>(F);
+    a.act = act;
+    if ((st = stream_product<kW16, true>(h, a, bf16, s)) != GEMM_OK) return st;
+    a.x = static_cast<const uint16_t*>(hid);
+    a.ldx = F;
+    a.w = w_down;
+    a.ldw = ldw_down;
+    a.y = static_cast<uint16_t*>(y);
+    a.ldy = ldy;
+    a.gu = nullptr;
+    a.K = static_cast<int32_t>(F);
+    a.cols = static_cast<int32_t>(D);
+    return stream_product<kW16, false>(h, a, bf16, s);
+  }
   const Stack xs = {x, T, D, ldx, 1, T * ldx};
   const int64_t split = splits_for(h, T, 2 * F, D);
   if (split == 1) {
@@ -596,23 +712,39 @@ gemm_status_t gemm_gated_ffn_backward(gemm_ops_t h, const void* dy, int64_t lddy
   return product(h, pi, dw_in, D, partial, s);
 }
 
+static size_t w4_workspace(gemm_ops_t h, int64_t T, int64_t N, int64_t K, bool gated) {
+  if (!h || T <= 0 || N <= 0 || K <= 0 || K / 2 > kMaxStreamRow) return 0;
+  // Whatever the groups.
+  return gated ? std::max({stream_partial_bytes<kW4G32, true>(h, T, N, K), stream_partial_bytes<kW4G64, true>(h, T, N, K),
+                           stream_partial_bytes<kW4G128, true>(h, T, N, K)})
+               : std::max({stream_partial_bytes<kW4G32, false>(h, T, N, K), stream_partial_bytes<kW4G64, false>(h, T, N, K),
+                           stream_partial_bytes<kW4G128, false>(h, T, N, K)});
+}
+
+size_t gemm_w4_workspace(gemm_ops_t h, int64_t T, int64_t N, int64_t K, int32_t gated) {
+  return w4_workspace(h, T, N, K, gated != 0);
+}
+
 static gemm_status_t w4_run(gemm_ops_t h, const void* x, int64_t ldx, const void* codes,
-                            const void* scales, const void* zeros, void* y, int64_t ldy, int64_t T,
-                            int64_t N, int64_t K, int64_t group, gemm_act_t act, gemm_dtype_t dtype,
-                            bool gated, void* stream) {
-  if (!h || !dim_ok(T) || !dim_ok(N) || !dim_ok(K) || N > INT32_MAX / 2 || T > 16 * 65535)
+                            const void* scales, const void* zeros, void* y, int64_t ldy, void* workspace,
+                            size_t workspace_bytes, int64_t T, int64_t N, int64_t K, int64_t group,
+                            gemm_act_t act, gemm_dtype_t dtype, bool gated, void* stream) {
+  if (!h || !dim_ok(T) || !dim_ok(N) || !dim_ok(K) || N > INT32_MAX / 2 || T > 8 * 65535)
     return GEMM_ERR_INVALID_ARG;
   if (act < GEMM_ACT_SILU || act > GEMM_ACT_RELU) return GEMM_ERR_INVALID_ARG;
   if (dtype != GEMM_F16 && dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;
   if (group < 32 || group > (1 << 30) || (group & (group - 1)) != 0 || K % group != 0)
     return GEMM_ERR_INVALID_ARG;
   if (T == 0 || N == 0) return GEMM_OK;
-  if (ldy < N) return GEMM_ERR_INVALID_ARG;
+  if (ldy < N || K / 2 > kMaxStreamRow) return GEMM_ERR_INVALID_ARG;
   gemm_status_t st = check_ld(ldx, K);
   if (st != GEMM_OK) return st;
   if (!aligned16(x) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 1) ||
       (reinterpret_cast<uintptr_t>(y) & 1))
     return GEMM_ERR_ALIGNMENT;
+  const size_t need = w4_workspace(h, T, N, K, gated);
+  if (workspace_bytes < need) return GEMM_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255) return GEMM_ERR_ALIGNMENT;
   DeviceGuard g(h->device);
   if (!g.ok) return GEMM_ERR_CUDA;
   const int64_t rows = gated ? 2 * N : N, groups = K / group;
@@ -620,32 +752,51 @@ static gemm_status_t w4_run(gemm_ops_t h, const void* x, int64_t ldx, const void
                       {codes, rows, K / 2, K / 2, false},
                       {scales, rows, groups * 2, groups * 2, false},
                       {zeros, zeros ? rows : 0, groups, groups, false},
-                      {y, T, N * 2, ldy * 2, true}};
+                      {y, T, N * 2, ldy * 2, true},
+                      {workspace, need ? 1 : 0, static_cast<int64_t>(need), 0, true}};
   if ((st = check_bufs(h, bufs)) != GEMM_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (K == 0)
     return cudaMemset2DAsync(y, ldy * 2, 0, N * 2, T, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
   int shift = 0;
   while ((1ll << shift) < group) ++shift;
-  const StreamArgs a = {static_cast<const uint16_t*>(x), ldx, codes, K / 2,
-                        static_cast<const uint16_t*>(scales), static_cast<const uint8_t*>(zeros),
-                        static_cast<uint16_t*>(y), ldy, nullptr, static_cast<int32_t>(T),
-                        static_cast<int32_t>(N), static_cast<int32_t>(K), shift, act};
+  StreamArgs a = {};
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = ldx;
+  a.w = codes;
+  a.ldw = K / 2;
+  a.scales = static_cast<const uint16_t*>(scales);
+  a.zeros = static_cast<const uint8_t*>(zeros);
+  a.y = static_cast<uint16_t*>(y);
+  a.ldy = ldy;
+  a.partial = static_cast<float*>(workspace);
+  a.T = static_cast<int32_t>(T);
+  a.K = static_cast<int32_t>(K);
+  a.cols = static_cast<int32_t>(N);
+  a.group_shift = shift;
+  a.act = act;
   const bool bf16 = dtype == GEMM_BF16;
-  return gated ? stream_product<true, true>(h, a, bf16, s) : stream_product<true, false>(h, a, bf16, s);
+  if (gated)
+    return group == 32   ? stream_product<kW4G32, true>(h, a, bf16, s)
+           : group == 64 ? stream_product<kW4G64, true>(h, a, bf16, s)
+                         : stream_product<kW4G128, true>(h, a, bf16, s);
+  return group == 32   ? stream_product<kW4G32, false>(h, a, bf16, s)
+         : group == 64 ? stream_product<kW4G64, false>(h, a, bf16, s)
+                       : stream_product<kW4G128, false>(h, a, bf16, s);
 }
 
 gemm_status_t gemm_w4_linear(gemm_ops_t h, const void* x, int64_t ldx, const void* codes,
-                             const void* scales, const void* zeros, void* y, int64_t ldy, int64_t T,
-                             int64_t N, int64_t K, int64_t group, gemm_dtype_t dtype, void* stream) {
-  return w4_run(h, x, ldx, codes, scales, zeros, y, ldy, T, N, K, group, GEMM_ACT_SILU, dtype, false, stream);
+                             const void* scales, const void* zeros, void* y, int64_t ldy, void* workspace,
+                             size_t workspace_bytes, int64_t T, int64_t N, int64_t K, int64_t group,
+                             gemm_dtype_t dtype, void* stream) {
+  return w4_run(h, x, ldx, codes, scales, zeros, y, ldy, workspace, workspace_bytes, T, N, K, group, GEMM_ACT_SILU, dtype, false, stream);
 }
 
 gemm_status_t gemm_w4_gated(gemm_ops_t h, const void* x, int64_t ldx, const void* codes,
-                            const void* scales, const void* zeros, void* y, int64_t ldy, int64_t T,
-                            int64_t N, int64_t K, int64_t group, gemm_act_t act, gemm_dtype_t dtype,
-                            void* stream) {
-  return w4_run(h, x, ldx, codes, scales, zeros, y, ldy, T, N, K, group, act, dtype, true, stream);
+                            const void* scales, const void* zeros, void* y, int64_t ldy, void* workspace,
+                            size_t workspace_bytes, int64_t T, int64_t N, int64_t K, int64_t group,
+                            gemm_act_t act, gemm_dtype_t dtype, void* stream) {
+  return w4_run(h, x, ldx, codes, scales, zeros, y, ldy, workspace, workspace_bytes, T, N, K, group, act, dtype, true, stream);
 }
 
 size_t gemm_orthogonalize_workspace(gemm_ops_t h, int64_t batch, int64_t M, int64_t N) {

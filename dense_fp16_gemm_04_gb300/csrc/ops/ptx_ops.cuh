@@ -67,13 +67,44 @@ __device__ __forceinline__ uint4 ld_global_v4_u32(const void* p) {
   return v;
 }
 
-// 16 bytes of read-once data: past L1, evicted first from it.
-__device__ __forceinline__ uint4 ld_global_stream_v4(const void* p) {
+// 16-byte asynchronous copy global -> shared past L1; a thread's copies are
+// counted in groups, and its own wait makes its own copies readable.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4_u32(uint32_t addr) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "r"(addr)
+               : "memory");
   return v;
+}
+
+// The same where `on`; else v keeps its value.
+__device__ __forceinline__ void ld_shared_v4_if(uint32_t on, uint32_t addr, uint4& v) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "@p ld.shared.v4.u32 {%0, %1, %2, %3}, [%5];\n\t}"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "r"(on), "r"(addr)
+      : "memory");
+}
+
+// (w & mask) | bits.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+  return r;
 }
 
 // tcgen05.mma kind::f16 with bf16 A and B (both operands' format fields).

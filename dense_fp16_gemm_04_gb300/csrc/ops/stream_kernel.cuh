@@ -7,19 +7,39 @@
 // Bound by the weights' bytes.  The sums run on warp-level matrix products
 // (16 rows of W x 16 k x 8 tokens): tcgen05 would have to stage every weight
 // through shared memory for a tile of 64 rows or more, while here a warp's
-// weights go from memory to registers and stop there, 16 bytes a lane, in the
-// order a row stores them.  That order is free because a sum over k may be
+// weights are read by the lane that fetched them, 16 bytes a lane, in the order
+// a row stores them.  That order is free because a sum over k may be
 // taken in any order, the same for W and x: lane t of a row's four lanes takes
 // eight consecutive k of every 32 as its k-slots of two products.
 //
-// 4-bit codes become 16-bit floats without a conversion: a code's bits below
-// the exponent of 1024 (fp16) or 128 (bf16) read 1024 + q or 128 + q, and
-// subtracting 1024 + z or 128 + z is exact.  Products of 16-bit x and these
-// integers are exact in fp32; the scale multiplies the fp32 sum of its group.
+// 4-bit codes become 16-bit floats without a conversion: four bits set in the
+// mantissa of 64 (fp16) or 128 (bf16) read O + q with O that number.  With
 //
-// A CTA takes 16 rows of the output (gated: the 16 gate rows and 16 up rows
-// of the same columns), its warps split K, and their sums meet in shared
-// memory in warp order (the result does not depend on timing).
+//   sum over a group of (q - z) x = sum (O + q) x - (O + z) sum x,
+//
+// a group's sum starts at -(O + z) sum x (fp32, from the staged x) instead of
+// 0 and nothing is subtracted from the codes.  Products of 16-bit x and O + q
+// are exact; the offset makes the fp32 sum's roundings at most 16 to 30 times
+// those of q x alone, 2^-20 of the group's size, far below the 16-bit result's
+// own rounding.  The scale multiplies the finished fp32 sum.
+//
+// A lane's 16 bytes are 32 codes of one row, so the four lanes of a row hold
+// 128 k: one group, two, or four.  Smaller groups are kept apart by columns:
+// a product's eight columns are 8, 4 or 2 tokens x 1, 2 or 4 groups, and a
+// column's x is zero in the lanes whose k lie in another group.  A column then
+// sums one group alone, without moving any code between lanes.
+//
+// CTAs are persistent: x (this CTA's k-slice of it) is staged in shared memory
+// once, and tiles of 32 rows of W follow one another (gated: 16 gate rows and
+// the 16 up rows of the same columns), two products for every read of x: with
+// 16 rows the reads of x alone filled shared memory's bandwidth (5 tokens,
+// 8192 x 8192 codes: 34 us at 81% of it).  A tile's k-blocks are dealt
+// to the warps in turn, so that the CTA reads contiguous pieces of each row;
+// every lane keeps its pieces of the next kRing blocks in flight (asynchronous
+// copies to a place of its own in shared memory: no barrier, no registers),
+// across tile ends.  The warps' sums meet in shared memory in warp order, so the result
+// does not depend on timing.  Where there are few tiles, or x does not fit,
+// K is also cut over CTAs and a second kernel adds the slices.
 #pragma once
 #include "act.cuh"
 #include "ptx_ops.cuh"
@@ -37,75 +57,241 @@ struct StreamArgs {
   uint16_t* y;           // [T, N], rows ldy apart
   int64_t ldy;
   uint16_t* gu;          // gated: g and u, [T, 2N], or null
-  int32_t T, N, K;       // N: rows of the output per matrix (gated: W has 2N rows)
+  float* partial;        // several k-slices: [slice][T][N or 2N]
+  int32_t T, N, K;       // N: columns of the output this launch makes, of `cols` in all
+  int32_t cols;
+  int64_t up_w, up_s;    // gated: from gate to up rows, in bytes of W and in scales
   int32_t group_shift;   // log2 G
   int32_t act;
+  int32_t ring;          // blocks a warp keeps in flight, 2 .. 4
 };
 
 constexpr int kStreamMaxWarps = 16;
 
-// The quad's 4 x 4 transpose: lane t holds word j of row j' = t; afterwards
-// it holds word t of every lane's: v[j] = lane j's word t.
-__device__ __forceinline__ void quad_transpose(uint32_t (&v)[4], int t) {
-  const bool hi = (t & 2) != 0, odd = (t & 1) != 0;
-  {
-    const uint32_t s0 = hi ? v[0] : v[2], s1 = hi ? v[1] : v[3];
-    const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 2), r1 = __shfl_xor_sync(0xffffffffu, s1, 2);
-    if (hi)
-      v[0] = r0, v[1] = r1;
-    else
-      v[2] = r0, v[3] = r1;
-  }
-  {
-    const uint32_t s0 = odd ? v[0] : v[1], s1 = odd ? v[2] : v[3];
-    const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 1), r1 = __shfl_xor_sync(0xffffffffu, s1, 1);
-    if (odd)
-      v[0] = r0, v[2] = r1;
-    else
-      v[1] = r0, v[3] = r1;
-  }
-}
+// How W is stored: 16-bit values, or codes whose groups are 32, 64, or 128 k
+// and more.
+enum StreamW : int { kW16 = 0, kW4G32 = 1, kW4G64 = 2, kW4G128 = 3 };
 
-// Eight codes to four pairs (code j, code j + 4), less the zero point.
+// k of a block; groups of a block (1 for 16 bits); tokens of an 8-column tile.
+__host__ __device__ constexpr int stream_block_k(int w) { return w == kW16 ? 32 : 128; }
+__host__ __device__ constexpr int stream_groups(int w) { return w == kW4G32 ? 4 : w == kW4G64 ? 2 : 1; }
+__host__ __device__ constexpr int stream_tokens(int w) { return 8 / stream_groups(w); }
+// Rows of W a lane reads per tile (g, g + 8 of two 16-row halves); what a warp
+// keeps for a block in flight: 16 bytes of W a row and lane and, with codes,
+// 8 bytes a row for its scales and 8 for its zero points.
+constexpr int kStreamRows = 4;
+__host__ __device__ constexpr int stream_slot_bytes(int w) {
+  return kStreamRows * (32 * 16 + (w == kW16 ? 0 : 8 * 16));
+}
+constexpr int kStreamMaxRing = 4;
+__host__ __device__ constexpr int stream_tile(bool glu) { return glu ? 16 : 32; }  // columns of y
+
+// Eight codes to four pairs (code j, code j + 4) of O + q: a shift and one
+// and-or each.
 template <bool kBf16>
-__device__ __forceinline__ void dequant8(uint32_t w, uint32_t zsub, uint32_t (&p)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t v = ((w >> (4 * j)) & 0x000f000fu) | (kBf16 ? 0x43004300u : 0x64006400u);
-    if constexpr (kBf16) {
-      const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                       *reinterpret_cast<const __nv_bfloat162*>(&zsub));
-      p[j] = *reinterpret_cast<const uint32_t*>(&r);
-    } else {
-      const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v),
-                                *reinterpret_cast<const __half2*>(&zsub));
-      p[j] = *reinterpret_cast<const uint32_t*>(&r);
-    }
+__device__ __forceinline__ void offset_codes(uint32_t w, uint32_t (&p)[4]) {
+  if constexpr (kBf16) {
+    p[0] = ptx::and_or(w, 0x000f000fu, 0x43004300u);
+    p[1] = ptx::and_or(w >> 4, 0x000f000fu, 0x43004300u);
+    p[2] = ptx::and_or(w >> 8, 0x000f000fu, 0x43004300u);
+    p[3] = ptx::and_or(w >> 12, 0x000f000fu, 0x43004300u);
+  } else {
+    // In place: bits 4-7 of 64 (0x5400), or bits 0-3 of 1024 (0x6400) and
+    // 960 less, an exact difference on another pipe than the bit operations.
+    const uint32_t w8 = w >> 8;
+    const __half2 d = __half2half2(__ushort_as_half(0xe380));  // -960
+    uint32_t e0 = ptx::and_or(w, 0x000f000fu, 0x64006400u), e2 = ptx::and_or(w8, 0x000f000fu, 0x64006400u);
+    const __half2 h0 = __hadd2(*reinterpret_cast<__half2*>(&e0), d);
+    const __half2 h2 = __hadd2(*reinterpret_cast<__half2*>(&e2), d);
+    p[0] = *reinterpret_cast<const uint32_t*>(&h0);
+    p[1] = ptx::and_or(w, 0x00f000f0u, 0x54005400u);
+    p[2] = *reinterpret_cast<const uint32_t*>(&h2);
+    p[3] = ptx::and_or(w8, 0x00f000f0u, 0x54005400u);
   }
 }
 
-// (1024 + z, 1024 + z) or (128 + z, 128 + z).
-template <bool kBf16>
-__device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
-  const uint32_t v = (kBf16 ? 0x4300u : 0x6400u) | z;
-  return v | (v << 16);
+// The aligned 4-byte word that holds *p.
+__device__ __forceinline__ const void* word_of(const void* p) {
+  return reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(3));
 }
 
-// kMT: 16-row tiles per warp (2 when gated: gate rows, up rows); kNT: tiles of
-// 8 tokens.
-template <bool kBf16, bool kW4, bool kGlu, int kNT>
-__global__ void __launch_bounds__(32 * kStreamMaxWarps) stream_kernel(const StreamArgs a) {
-  constexpr int kMT = kGlu ? 2 : 1;
-  extern __shared__ float red[];  // [warp][kMT][kNT][4][32]
+template <bool kBf16, int kW, bool kGlu, int kNT>
+__global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const StreamArgs a) {
+  constexpr bool kW4 = kW != kW16;
+  constexpr int kMT = 2;  // 16-row halves of a tile
+  constexpr int kBK = stream_block_k(kW);
+  constexpr int kSlot = stream_slot_bytes(kW);
+  constexpr int kRows = kStreamRows;
+  constexpr int kTileN = stream_tile(kGlu);
+  constexpr int kGroups = stream_groups(kW);
+  constexpr int kTok = stream_tokens(kW);  // tokens per 8-column tile
+  constexpr int kRed = kMT * kNT * 128;    // floats one warp leaves per tile
+  constexpr float kOffset = kBf16 ? 128.0f : 64.0f;
+  extern __shared__ __align__(16) uint8_t stream_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int32_t n0 = blockIdx.x * 16;
-  const int32_t t0 = blockIdx.y * (8 * kNT);
-  // This warp's k-range, in units of 128 k.
-  const int32_t units = (a.K + 127) / 128;
-  const int32_t u0 = static_cast<int32_t>(static_cast<int64_t>(warp) * units / warps);
-  const int32_t u1 = static_cast<int32_t>(static_cast<int64_t>(warp + 1) * units / warps);
+  const int32_t t0 = blockIdx.z * (kTok * kNT);
+  const int32_t tokens = min(a.T - t0, kTok * kNT);
+  // This CTA's k-slice (whole blocks; slices partition them).
+  const int32_t blocks = (a.K + kBK - 1) / kBK;
+  const int32_t b0 = static_cast<int32_t>(static_cast<int64_t>(blockIdx.y) * blocks / gridDim.y);
+  const int32_t b1 = static_cast<int32_t>(static_cast<int64_t>(blockIdx.y + 1) * blocks / gridDim.y);
+  const int32_t k_begin = b0 * kBK;
+  float* red = reinterpret_cast<float*>(stream_smem);  // [warp][kMT][kNT][row][column]
+  float* sums = red + warps * kRed;                    // 4 bits: [block][8 kNT columns]
+  // [warp][slot]: [row of the lane][lane][16 B], then the scales and the zero
+  // points [row][g][two words].
+  uint8_t* wr = reinterpret_cast<uint8_t*>(sums + (kW4 ? (b1 - b0) * 8 * kNT : 0));
+  uint8_t* xs = wr + warps * a.ring * kSlot;  // [block][i][token][t][16 B]
+  const int32_t per_tile = (b1 - b0 + warps - 1) / warps;  // blocks of a tile per warp
+  const int32_t tiles = (a.N + kTileN - 1) / kTileN;
+  const int32_t my_tiles = (tiles - static_cast<int32_t>(blockIdx.x) + static_cast<int32_t>(gridDim.x) - 1) /
+                           static_cast<int32_t>(gridDim.x);
+  const int32_t items = my_tiles * per_tile;
+
+  // The warp's blocks in order: block load_blk of tile load_tile.  A lane reads
+  // rows i = 0 .. 3: g and g + 8 of the tile's first half, then of its second.
+  // row_of(tile, i): the row of W, from the base of its half (32-bit byte
+  // offsets: the host cuts larger matrices).  Rows past N read the last row,
+  // and k past K the last codes: the sums of the former are not stored, x is 0
+  // in the latter.
+  int32_t load_tile = blockIdx.x, load_blk = 0;
+  const uint32_t slot0 = ptx::smem_addr(wr) + warp * (a.ring * kSlot);
+  const uint32_t groups = kW4 ? a.K >> a.group_shift : 0;
+  const uint32_t row_bytes = static_cast<uint32_t>(a.ldw) * (kW4 ? 1 : 2);
+  constexpr int kOwn = kGlu ? 2 : 4;  // different rows (gated: the up rows repeat the gate's)
+  auto row_of = [&](int32_t tile, int i) {
+    return static_cast<uint32_t>(min(tile * kTileN + g + 8 * i, a.N - 1));
+  };
+  uint32_t w_off[kOwn], s_off[kOwn];
+  auto rows_of_tile = [&]() {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const uint32_t n = row_of(load_tile, i);
+      w_off[i] = n * row_bytes;
+      s_off[i] = n * groups;
+    }
+  };
+  rows_of_tile();
+  const uint8_t* w_base[2] = {static_cast<const uint8_t*>(a.w), static_cast<const uint8_t*>(a.w) + a.up_w};
+  const uint16_t* s_base[2] = {a.scales, a.scales + a.up_s};
+  const uint8_t* z_base[2] = {a.zeros, a.zeros + a.up_s};
+  constexpr int kHalf = kGlu ? 1 : 0;  // whether rows 2, 3 have the other base
+  // This lane's two columns belong to groups j, j + 1 of a row (or to one
+  // group).  Their scales share an aligned word, and so do their zero points,
+  // unless rows hold an odd number of small groups or start off such a word:
+  // then they are read when they are needed.  A row's words are fetched by one
+  // lane each: two for four groups, else one.
+  const bool words = kGroups == 1 || (((groups | static_cast<uint32_t>(a.up_s)) & 1) == 0 &&
+                                      (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0 &&
+                                      (reinterpret_cast<uintptr_t>(a.zeros) & 1) == 0);
+  const bool fetches = kGroups == 4 ? t < 2 : t == 0;
+  const uint32_t s_lane = kRows * 512 + g * 8 + (kGroups == 4 ? (t & 1) * 4 : 0);
+  auto group_of = [&](int32_t b) {
+    return min((b * kBK >> a.group_shift) + (2 * t & (kGroups - 1)), static_cast<int32_t>(groups) - (kGroups > 1 ? 2 : 1));
+  };
+  auto issue = [&](uint32_t slot) {
+    const int32_t b = b0 + load_blk * warps + warp;
+    if (b < b1) {
+      const int32_t k0 = b * kBK;
+      const uint32_t at = kW4 ? min(k0 + 32 * t, a.K - 32) >> 1 : 2 * min(k0 + 8 * t, a.K - 8);
+      const uint32_t dst = slot + lane * 16;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        ptx::cp_async_16(dst + i * 512, w_base[kHalf * (i >> 1)] + (w_off[i & (kOwn - 1)] + at));
+      if constexpr (kW4) {
+        if (words && fetches) {
+          const uint32_t j = group_of(b);
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)  // the aligned word lies in the same allocation
+            ptx::cp_async_4(slot + s_lane + i * 64, word_of(s_base[kHalf * (i >> 1)] + (s_off[i & (kOwn - 1)] + j)));
+          if (a.zeros) {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+              ptx::cp_async_4(slot + s_lane + (kRows + i) * 64,
+                              word_of(z_base[kHalf * (i >> 1)] + (s_off[i & (kOwn - 1)] + j)));
+          }
+        }
+      }
+    }
+    if (++load_blk == per_tile) {
+      load_blk = 0;
+      load_tile += gridDim.x;
+      rows_of_tile();
+    }
+  };
+
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  for (int i = 0; i < a.ring; ++i) {
+    if (i < items) issue(slot0 + i * kSlot);
+    ptx::cp_async_commit();
+  }
+  // Stage x: 16-byte chunks of eight k, in the order the products read them
+  // (4 bits: chunk 4 t + i of a block is word i of lane t), four loads in
+  // flight a thread; zeros past K.
+  {
+    constexpr int kPer = kBK / 8;              // chunks per block
+    constexpr int kLanes = kPer / kGroups;     // neighbouring chunks of one group
+    const int32_t chunks = (b1 - b0) * kPer, total = chunks * tokens;
+    if constexpr (kW4)  // columns of tokens past T
+      for (int32_t i = threadIdx.x; i < (b1 - b0) * 8 * kNT; i += blockDim.x)
+        if ((i & (8 * kNT - 1)) >= tokens * kGroups) sums[i] = 0.0f;
+    for (int32_t i0 = threadIdx.x; i0 - lane < total; i0 += 4 * blockDim.x) {
+      uint4 v[4];
+      int32_t tok[4], c[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int32_t i = i0 + u * blockDim.x;
+        tok[u] = i / chunks;
+        c[u] = i - tok[u] * chunks;
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (i < total && k_begin + 8 * c[u] < a.K)
+          v[u] = ptx::ld_global_v4_u32(a.x + (t0 + tok[u]) * a.ldx + k_begin + 8 * c[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool in = i0 + u * static_cast<int32_t>(blockDim.x) < total;
+        const int32_t blk = c[u] / kPer, ch = c[u] & (kPer - 1);
+        uint4 o = v[u];
+        int i = ch >> 2, l = ch & 3;
+        if constexpr (kW4) {
+          // Pairs (x j, x j + 4), as the codes unpack.
+          o = make_uint4(__byte_perm(v[u].x, v[u].z, 0x5410), __byte_perm(v[u].x, v[u].z, 0x7632),
+                         __byte_perm(v[u].y, v[u].w, 0x5410), __byte_perm(v[u].y, v[u].w, 0x7632));
+          const float2 f0 = unpack16(kBf16, v[u].x), f1 = unpack16(kBf16, v[u].y);
+          const float2 f2 = unpack16(kBf16, v[u].z), f3 = unpack16(kBf16, v[u].w);
+          float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+#pragma unroll
+          for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          if (in && (ch & (kLanes - 1)) == 0) sums[blk * (8 * kNT) + tok[u] * kGroups + ch / kLanes] = sum;
+          i = ch & 3, l = ch >> 2;
+        }
+        if (in)
+          *reinterpret_cast<uint4*>(xs + (((blk * (kPer / 4) + i) * tokens + tok[u]) * 4 + l) * 16) = o;
+      }
+    }
+  }
+  __syncthreads();
+  // Column g of tile n is token n kTok + g / kGroups, group g % kGroups; lane
+  // t's k lie in group t kGroups / 4 of the block.
+  uint32_t xl[kNT];
+  uint32_t mine[kNT];
+#pragma unroll
+  for (int n = 0; n < kNT; ++n) {
+    const int32_t tok = n * kTok + g / kGroups;
+    mine[n] = tok < tokens && t * kGroups / 4 == g % kGroups;
+    xl[n] = ptx::smem_addr(xs) + tok * 64 + t * 16;
+  }
+  const uint32_t x_step = tokens * 64;  // bytes from i to i + 1
+  // Zero for good in the lanes whose column lacks their k: they never load.
+  uint4 xb[2][kNT];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) xb[j][n] = make_uint4(0, 0, 0, 0);
+
   float acc[kMT][kNT][4];
 #pragma unroll
   for (int m = 0; m < kMT; ++m)
@@ -113,157 +299,211 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps) stream_kernel(const Stre
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-  // Rows of W this lane reads: g and g + 8 of each tile; rows past N read the
-  // last row (their sums are not stored).
-  int64_t row[kMT][2];
+  int32_t tile = blockIdx.x, blk = 0;
+  auto consume = [&](uint32_t slot, int32_t rel) {  // block b0 + rel
+    if (rel >= b1 - b0) return;
+    constexpr int kWords = kBK / 32;
+    const uint32_t x_at = rel * kWords * x_step;
+    uint4 wv[kRows];
 #pragma unroll
-  for (int m = 0; m < kMT; ++m)
+    for (int i = 0; i < kRows; ++i) wv[i] = ptx::ld_shared_v4_u32(slot + i * 512 + lane * 16);
+    if constexpr (kW4) {
+      // Scales (two to a word) and zero points (two bytes) of this lane's
+      // columns in its rows.
+      uint32_t sv[kRows], zv[kRows];
+      const uint32_t j = group_of(b0 + rel);
+      if (words) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int32_t n = n0 + g + 8 * r;
-      row[m][r] = static_cast<int64_t>(n < a.N ? n : a.N - 1) + static_cast<int64_t>(m) * a.N;
-    }
-  // Tokens this lane supplies: t0 + g of each tile.
-  const uint16_t* xp[kNT];
-#pragma unroll
-  for (int n = 0; n < kNT; ++n) {
-    const int32_t tok = t0 + 8 * n + g;
-    xp[n] = tok < a.T ? a.x + static_cast<int64_t>(tok) * a.ldx : nullptr;
-  }
-  auto load_x = [&](int n, int32_t k) {
-    return xp[n] != nullptr && k < a.K ? ptx::ld_global_v4_u32(xp[n] + k) : make_uint4(0, 0, 0, 0);
-  };
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
-  if constexpr (kW4) {
-    const uint8_t* w = static_cast<const uint8_t*>(a.w);
-    const int64_t groups = a.K >> a.group_shift;
-    for (int32_t u = u0; u < u1; ++u) {
-      const int32_t k0 = u * 128;
-      uint32_t c[kMT][2][4];
-#pragma unroll
-      for (int m = 0; m < kMT; ++m)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint4 v = k0 + 32 * t < a.K
-                              ? ptx::ld_global_stream_v4(w + row[m][r] * a.ldw + k0 / 2 + 16 * t)
-                              : make_uint4(0, 0, 0, 0);
-          c[m][r][0] = v.x, c[m][r][1] = v.y, c[m][r][2] = v.z, c[m][r][3] = v.w;
+        for (int i = 0; i < kRows; ++i) {
+          sv[i] = ptx::ld_shared_u32(slot + s_lane + i * 64);
+          if (kGroups == 1)
+            sv[i] >>= 8 * (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+                               s_base[kHalf * (i >> 1)] + (row_of(tile, i & (kOwn - 1)) * groups + j))) & 2);
         }
+        if (a.zeros) {
 #pragma unroll
-      for (int m = 0; m < kMT; ++m)
+          for (int i = 0; i < kRows; ++i)
+            zv[i] = ptx::ld_shared_u32(slot + s_lane + (kRows + i) * 64) >>
+                    (8 * (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+                              z_base[kHalf * (i >> 1)] + (row_of(tile, i & (kOwn - 1)) * groups + j))) & 3));
+        }
+      } else {
+        const uint32_t j0 = min(((b0 + rel) * kBK >> a.group_shift) + (2u * t & (kGroups - 1)), groups - 1);
+        const uint32_t j1 = min(j0 + 1, groups - 1);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) quad_transpose(c[m][r], t);
+        for (int i = 0; i < kRows; ++i) {
+          const uint32_t o = row_of(tile, i & (kOwn - 1)) * groups;
+          const uint16_t* sp = s_base[kHalf * (i >> 1)] + o;
+          const uint8_t* zp = z_base[kHalf * (i >> 1)] + o;
+          sv[i] = sp[j0] | static_cast<uint32_t>(sp[j1]) << 16;
+          if (a.zeros) zv[i] = zp[j0] | static_cast<uint32_t>(zp[j1]) << 8;
+        }
+      }
+      float z0[kRows], z1[kRows];
+      if (a.zeros) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          z0[i] = -kOffset - static_cast<float>(zv[i] & 15u);
+          z1[i] = kGroups > 1 ? -kOffset - static_cast<float>((zv[i] >> 8) & 15u) : z0[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) z0[i] = z1[i] = -kOffset - 8.0f;
+      }
       float part[kMT][kNT][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int32_t k = k0 + 32 * j;
-        if (k >= a.K) break;
-        const int32_t grp = k >> a.group_shift;
-        const bool first = ((k >> 5) & ((1 << (a.group_shift - 5)) - 1)) == 0 || j == 0;
-        const bool last = (((k + 32) >> 5) & ((1 << (a.group_shift - 5)) - 1)) == 0 || j == 3 || k + 32 >= a.K;
-        uint32_t xb[kNT][4];
+      for (int n = 0; n < kNT; ++n) {
+        const float2 s = *reinterpret_cast<const float2*>(sums + (rel * kNT + n) * 8 + 2 * t);
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-          const uint4 v = load_x(n, k + 8 * t);
-          xb[n][0] = __byte_perm(v.x, v.z, 0x5410);
-          xb[n][1] = __byte_perm(v.x, v.z, 0x7632);
-          xb[n][2] = __byte_perm(v.y, v.w, 0x5410);
-          xb[n][3] = __byte_perm(v.y, v.w, 0x7632);
+        for (int i = 0; i < kRows; ++i) {
+          part[i >> 1][n][2 * (i & 1)] = z0[i] * s.x;
+          part[i >> 1][n][2 * (i & 1) + 1] = z1[i] * s.y;
         }
+      }
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) ptx::ld_shared_v4_if(mine[n], xl[n] + x_at + i * x_step, xb[i & 1][n]);
 #pragma unroll
         for (int m = 0; m < kMT; ++m) {
-          uint32_t p[2][4];
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t z = a.zeros ? a.zeros[row[m][r] * groups + grp] & 15u : 8u;
-            dequant8<kBf16>(c[m][r][j], zero_pair<kBf16>(z), p[r]);
-          }
+          uint32_t p0[4], p1[4];
+          const uint4 w0 = wv[2 * m], w1 = wv[2 * m + 1];
+          offset_codes<kBf16>(i == 0 ? w0.x : i == 1 ? w0.y : i == 2 ? w0.z : w0.w, p0);
+          offset_codes<kBf16>(i == 0 ? w1.x : i == 1 ? w1.y : i == 2 ? w1.z : w1.w, p1);
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
-            if (first)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) part[m][n][i] = 0.0f;
-            ptx::mma_16816<kBf16>(part[m][n], p[0][0], p[1][0], p[0][1], p[1][1], xb[n][0], xb[n][1]);
-            ptx::mma_16816<kBf16>(part[m][n], p[0][2], p[1][2], p[0][3], p[1][3], xb[n][2], xb[n][3]);
-          }
-          if (last) {
-            const float s0 = widen16(kBf16, a.scales[row[m][0] * groups + grp]);
-            const float s1 = widen16(kBf16, a.scales[row[m][1] * groups + grp]);
-#pragma unroll
-            for (int n = 0; n < kNT; ++n) {
-              acc[m][n][0] = fmaf(s0, part[m][n][0], acc[m][n][0]);
-              acc[m][n][1] = fmaf(s0, part[m][n][1], acc[m][n][1]);
-              acc[m][n][2] = fmaf(s1, part[m][n][2], acc[m][n][2]);
-              acc[m][n][3] = fmaf(s1, part[m][n][3], acc[m][n][3]);
-            }
+            ptx::mma_16816<kBf16>(part[m][n], p0[0], p1[0], p0[1], p1[1], xb[i & 1][n].x, xb[i & 1][n].y);
+            ptx::mma_16816<kBf16>(part[m][n], p0[2], p1[2], p0[3], p1[3], xb[i & 1][n].z, xb[i & 1][n].w);
           }
         }
       }
-    }
-  } else {
-    const uint16_t* w = static_cast<const uint16_t*>(a.w);
-    for (int32_t u = u0; u < u1; ++u) {
-      uint4 wv[4][kMT][2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int32_t k = u * 128 + 32 * j + 8 * t;
-#pragma unroll
-        for (int m = 0; m < kMT; ++m)
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            wv[j][m][r] = k < a.K ? ptx::ld_global_stream_v4(w + row[m][r] * a.ldw + k)
-                                  : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int i = 0; i < kRows; ++i) {
+        const float2 f = unpack16(kBf16, sv[i]);
+        const float f1 = kGroups == 1 ? f.x : f.y;
 #pragma unroll
         for (int n = 0; n < kNT; ++n) {
-          const uint4 x = load_x(n, u * 128 + 32 * j + 8 * t);
+          float* c = acc[i >> 1][n] + 2 * (i & 1);
+          const float* p = part[i >> 1][n] + 2 * (i & 1);
+          c[0] = fmaf(f.x, p[0], c[0]);
+          c[1] = fmaf(f1, p[1], c[1]);
+        }
+      }
+    } else {
 #pragma unroll
-          for (int m = 0; m < kMT; ++m) {
-            const uint4 p = wv[j][m][0], q = wv[j][m][1];
-            ptx::mma_16816<kBf16>(acc[m][n], p.x, q.x, p.y, q.y, x.x, x.y);
-            ptx::mma_16816<kBf16>(acc[m][n], p.z, q.z, p.w, q.w, x.z, x.w);
-          }
+      for (int n = 0; n < kNT; ++n) {
+        ptx::ld_shared_v4_if(mine[n], xl[n] + x_at, xb[0][n]);
+        const uint4 x = xb[0][n];
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+          const uint4 p = wv[2 * m], q = wv[2 * m + 1];
+          ptx::mma_16816<kBf16>(acc[m][n], p.x, q.x, p.y, q.y, x.x, x.y);
+          ptx::mma_16816<kBf16>(acc[m][n], p.z, q.z, p.w, q.w, x.z, x.w);
         }
       }
     }
+  };
+
+  auto finish_tile = [&]() {
+    // The warps' sums, in warp order.
+    __syncthreads();  // the last tile's have been read
+#pragma unroll
+    for (int m = 0; m < kMT; ++m)
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        float* p = red + warp * kRed + (m * kNT + n) * 128 + g * 8 + 2 * t;
+        *reinterpret_cast<float2*>(p) = make_float2(acc[m][n][0], acc[m][n][1]);
+        *reinterpret_cast<float2*>(p + 64) = make_float2(acc[m][n][2], acc[m][n][3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+      }
+    __syncthreads();
+    // A thread per element (gated: of both halves); then the columns of one
+    // token.
+    constexpr int kEach = kGlu ? 2 : 1;
+    for (int e = threadIdx.x; e < 2 / kEach * 128 * kNT; e += blockDim.x) {
+      float v[kEach];
+#pragma unroll
+      for (int m = 0; m < kEach; ++m) {
+        float s = 0.0f;
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) s += red[w * kRed + m * kNT * 128 + e];
+#pragma unroll
+        for (int d = 1; d < kGroups; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        v[m] = s;
+      }
+      const int col = e & 7, q = e >> 7;  // q: 16-row half (plain) and column tile
+      const int tok = q % kNT * kTok + col / kGroups;
+      const int32_t n = tile * kTileN + q / kNT * 16 + ((e >> 3) & 15), tk = t0 + tok;
+      if (n >= a.N || tok >= tokens || col % kGroups != 0) continue;
+      if (gridDim.y > 1) {
+#pragma unroll
+        for (int m = 0; m < kEach; ++m)
+          a.partial[((static_cast<int64_t>(blockIdx.y) * a.T + tk) * kEach + m) * a.N + n] = v[m];
+        continue;
+      }
+      float out = v[0];
+      if constexpr (kGlu) {
+        out = act_value(a.act, v[0]) * v[1];
+        if (a.gu) {
+          a.gu[static_cast<int64_t>(tk) * 2 * a.cols + n] = round16(kBf16, v[0]);
+          a.gu[static_cast<int64_t>(tk) * 2 * a.cols + a.cols + n] = round16(kBf16, v[1]);
+        }
+      }
+      a.y[static_cast<int64_t>(tk) * a.ldy + n] = round16(kBf16, out);
+    }
+    tile += gridDim.x;
+  };
+  uint32_t slot = slot0;
+#pragma unroll 1
+  for (int32_t i = 0; i < items; ++i) {
+    // This lane's oldest block has landed; then the warp's, whose lanes share
+    // the scales.
+    if (a.ring == 4)
+      ptx::cp_async_wait<3>();
+    else if (a.ring == 3)
+      ptx::cp_async_wait<2>();
+    else
+      ptx::cp_async_wait<1>();
+    __syncwarp();
+    consume(slot, blk * warps + warp);
+    __syncwarp();
+    if (i + a.ring < items) issue(slot);
+    ptx::cp_async_commit();  // one group per block, empty at the end
+    slot += kSlot;
+    if (slot == slot0 + a.ring * kSlot) slot = slot0;
+    if (++blk == per_tile) {
+      blk = 0;
+      finish_tile();
+    }
   }
-  // Sum the warps' k-ranges, in order.
-#pragma unroll
-  for (int m = 0; m < kMT; ++m)
-#pragma unroll
-    for (int n = 0; n < kNT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        red[((warp * kMT + m) * kNT + n) * 128 + i * 32 + lane] = acc[m][n][i];
-  __syncthreads();
-  // Thread j finishes element (row, token) of the CTA's 16 x 8 kNT tile.
-  for (int e = threadIdx.x; e < 16 * 8 * kNT; e += blockDim.x) {
-    const int r = e & 15, tok = e >> 4;
-    const int32_t n = n0 + r, tk = t0 + tok;
-    if (n >= a.N || tk >= a.T) continue;
-    // Fragment element of (row r, token tok & 7): lane 4 (r & 7) + (tok & 7) / 2,
-    // value (tok & 1) + 2 (r >= 8).
-    const int nt = tok >> 3, c = tok & 7;
-    const int at = ((c & 1) + 2 * (r >> 3)) * 32 + 4 * (r & 7) + (c >> 1);
+}
+
+// Adds the k-slices of stream_kernel, in order, and finishes the output.
+template <bool kGlu>
+__global__ void __launch_bounds__(256) stream_reduce(const StreamArgs a, int32_t slices, int32_t bf16) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  constexpr int kMT = kGlu ? 2 : 1;
+  const int64_t total = static_cast<int64_t>(a.T) * a.N, stride = total * kMT;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int64_t tk = i / a.N, n = i - tk * a.N;
+    const float* p = a.partial + tk * kMT * a.N + n;
     float v[kMT];
 #pragma unroll
-    for (int m = 0; m < kMT; ++m) {
-      float s = 0.0f;
-      for (int wp = 0; wp < warps; ++wp) s += red[((wp * kMT + m) * kNT + nt) * 128 + at];
-      v[m] = s;
-    }
+    for (int m = 0; m < kMT; ++m) v[m] = 0.0f;
+    for (int32_t s = 0; s < slices; ++s)
+#pragma unroll
+      for (int m = 0; m < kMT; ++m) v[m] += __ldcg(p + s * stride + m * a.N);
     float out = v[0];
     if constexpr (kGlu) {
       out = act_value(a.act, v[0]) * v[1];
       if (a.gu) {
-        a.gu[static_cast<int64_t>(tk) * 2 * a.N + n] = round16(kBf16, v[0]);
-        a.gu[static_cast<int64_t>(tk) * 2 * a.N + a.N + n] = round16(kBf16, v[1]);
+        a.gu[tk * 2 * a.cols + n] = round16(bf16, v[0]);
+        a.gu[tk * 2 * a.cols + a.cols + n] = round16(bf16, v[1]);
       }
     }
-    a.y[static_cast<int64_t>(tk) * a.ldy + n] = round16(kBf16, out);
+    a.y[tk * a.ldy + n] = round16(bf16, out);
   }
 }
 

@@ -58,8 +58,11 @@ def _lib():
                 "gemm_gated_ffn_backward_workspace": (sz, [vp, i64, i64, i64]),
                 "gemm_gated_ffn_backward": (st, [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64,
                                                  vp, vp, vp, sz, i64, i64, i64, st, st, vp]),
-                "gemm_w4_linear": (st, [vp, vp, i64, vp, vp, vp, vp, i64, i64, i64, i64, i64, st, vp]),
-                "gemm_w4_gated": (st, [vp, vp, i64, vp, vp, vp, vp, i64, i64, i64, i64, i64, st, st, vp]),
+                "gemm_w4_workspace": (sz, [vp, i64, i64, i64, i32]),
+                "gemm_w4_linear": (st, [vp, vp, i64, vp, vp, vp, vp, i64, vp, sz, i64, i64, i64, i64, st,
+                                        vp]),
+                "gemm_w4_gated": (st, [vp, vp, i64, vp, vp, vp, vp, i64, vp, sz, i64, i64, i64, i64, st,
+                                       st, vp]),
                 "gemm_orthogonalize_workspace": (sz, [vp, i64, i64, i64]),
                 "gemm_orthogonalize": (st, [vp, vp, i64, i64, vp, i64, i64, vp, sz, i64, i64, i64, i32,
                                             ctypes.POINTER(f32), f32, st, st, vp]),
@@ -215,9 +218,11 @@ class Ops:
         if out is None:
             out = torch.empty((T, N), dtype=dt, device=dev)
         ldy = _matrix(out, "out", dt, dev, (T, N))
+        need = self._lib.gemm_w4_workspace(self._h, T, N, K, gated)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         args = (self._h, x.data_ptr(), ldx, codes.data_ptr(), scales.data_ptr(),
-                zeros.data_ptr() if zeros is not None else None, out.data_ptr(), ldy, T, N, K,
-                K // groups if groups else 32)
+                zeros.data_ptr() if zeros is not None else None, out.data_ptr(), ldy,
+                ws.data_ptr() if need else None, need, T, N, K, K // groups if groups else 32)
         if gated:
             _check(self._lib.gemm_w4_gated(*args, a, _DTYPE[dt], _stream(stream, dev)), "gemm_w4_gated")
         else:

@@ -113,15 +113,18 @@ GEMM_API gemm_status_t gemm_gated_ffn_backward(
  * Made for few tokens: the weights are read once for every 16 tokens.  x
  * and codes 16-byte aligned, ldx a multiple of 8 (GEMM_ERR_ALIGNMENT);
  * N, T and ldy are free.  The integers q - zero and their products with x are
- * exact; a group's sum is fp32 and so is its product with the scale. */
+ * exact; a group's sum is fp32 and so is its product with the scale.
+ * workspace: gemm_w4_workspace(ops, T, N, K, gated) bytes (none for most
+ * shapes), 256-byte aligned. */
+GEMM_API size_t gemm_w4_workspace(gemm_ops_t ops, int64_t T, int64_t N, int64_t K, int32_t gated);
 GEMM_API gemm_status_t gemm_w4_linear(gemm_ops_t ops, const void* x, int64_t ldx, const void* codes,
                                       const void* scales, const void* zeros, void* y, int64_t ldy,
-                                      int64_t T, int64_t N, int64_t K, int64_t group,
+                                      void* workspace, size_t workspace_bytes, int64_t T, int64_t N, int64_t K, int64_t group,
                                       gemm_dtype_t dtype, void* stream);
 /* y = act(x Wg^T) * (x Wu^T), W of 2 N rows (gate rows, then up rows). */
 GEMM_API gemm_status_t gemm_w4_gated(gemm_ops_t ops, const void* x, int64_t ldx, const void* codes,
                                      const void* scales, const void* zeros, void* y, int64_t ldy,
-                                     int64_t T, int64_t N, int64_t K, int64_t group, gemm_act_t act,
+                                     void* workspace, size_t workspace_bytes, int64_t T, int64_t N, int64_t K, int64_t group, gemm_act_t act,
                                      gemm_dtype_t dtype, void* stream);
 
 /* The orthogonalised update: `steps` steps of an odd polynomial that drives
