@@ -22,9 +22,14 @@
 //                the source S.
 //   kEpiSplitSym the same for a symmetric C: only tiles on and above the
 //                diagonal are computed, and each is also stored transposed.
-//   kEpiPartial  fp32 partial sums of one of several k-ranges of a tile, to be
-//                added by a second kernel (fused_reduce.cuh): for few tiles
-//                with long K.
+// Few tiles with long K (kSplit = 2, 4 or 8): a cluster of kSplit CTAs takes one
+// 128 x 128 tile, each CTA a k-range of it, so that more SMs load operands (one
+// SM's loads, 32 KB a k-block against 128 clocks of MMAs, bound a lone CTA).
+// Each CTA then finishes 128 / kSplit of the tile's columns: every CTA sends
+// the others their columns of its partial sums through distributed shared
+// memory, and after one cluster barrier adds the kSplit partials of its own in
+// rank order (the result does not depend on timing) and runs the epilogue on
+// them.
 //
 // Units (a CTA with a 128-row tile, or a pair of CTAs with a 256-row one) are
 // persistent and take tiles round robin.  Inside a CTA: warp 0 loads A and
@@ -48,15 +53,13 @@ enum FusedEpi : int {
   kEpiGluBwd = 2,
   kEpiSplit = 3,
   kEpiSplitSym = 4,
-  kEpiPartial = 5,
 };
 
 struct FusedArgs {
   int32_t M, N;               // rows and columns of the output (of h for the gated forward)
   int32_t tiles_m, tiles_n;   // tiles of one matrix of the batch
   int32_t per_batch;          // tiles computed per matrix (tiles_m tiles_n, or the triangle)
-  int32_t items;              // work items: per_batch x batch x splits
-  int32_t splits;             // k-ranges per tile (kEpiPartial), else 1
+  int32_t items;              // tiles of the whole batch
   int32_t num_kb;             // 64-deep k-blocks of one segment
   int32_t segs;               // segments (1, or 3: high high + high low + low high)
   int32_t z_mul;              // third coordinate of matrix b of the batch: b z_mul + part
@@ -68,15 +71,19 @@ struct FusedArgs {
   const uint16_t* src;        // kEpiSplit*: S (rows src_ld apart), its low part src_part further,
   int64_t src_ld, src_part;   //   the next matrix of the batch 2 src_part further;
                               // kEpiGluBwd: g and u, [M, 2N]
-  float* partial;             // kEpiPartial: [split][M][part_ld]
-  int64_t part_ld, part_stride;
+  // Split clusters store their columns themselves: c the output, or h; d g and
+  // u, or dg and du, [M, 2N]; c_part from C's high to its low part.
+  uint16_t *c, *d;
+  int64_t ldc, c_part;
   uint32_t* err;
   uint64_t timeout_ns;
   int32_t skip_kb;            // fault injection, -1 = off
 };
 
-template <int kCtas_, int kBN_, int kStages_, int kEpi_, int kEpiBufs_>
+template <int kCtas_, int kBN_, int kStages_, int kEpi_, int kEpiBufs_, int kSplit_ = 1>
 struct FusedCfg {
+  static constexpr int kSplit = kSplit_;  // CTAs sharing a tile, each a k-range
+  static constexpr int kCluster = kCtas_ * kSplit_;
   static constexpr int kCtas = kCtas_;
   static constexpr int kBN = kBN_;  // columns of the accumulator
   static constexpr int kStages = kStages_;
@@ -107,26 +114,23 @@ struct FusedCfg {
   static_assert(kOutN % 64 == 0, "the epilogue works on 64-column chunks");
   static_assert(!kSym || kTileM == kBN, "symmetric tiles are square");
   static_assert(kTmemCols <= 512, "TMEM columns");
+  // The partials a split CTA receives, its own among them: 128 rows x 128
+  // columns in all, in the staging buffers' place.
+  static_assert(kSplit == 1 || (kCtas == 1 && kBN == 128 && kEpiWarps * kEpiBufs * kBufBytes >= kBM * kBN * 4),
+                "split clusters: single CTAs, 128 x 128 tiles");
 };
 
-// One tile's k-range.
+// One tile, and a CTA's k-range of it.
 struct FusedItem {
-  int32_t mb, nb, batch, split, kb0, kb1;
+  int32_t mb, nb, batch, kb0, kb1;
 };
 
 template <class Cfg>
-__device__ __forceinline__ FusedItem fused_item(const FusedArgs& a, int32_t it) {
+__device__ __forceinline__ FusedItem fused_item(const FusedArgs& a, int32_t t, int32_t rank) {
   FusedItem w;
   const int32_t total = a.num_kb * a.segs;
-  int32_t t = it;
-  w.split = 0;
-  if constexpr (Cfg::kEpi == kEpiPartial) {
-    // Neighbouring units take the k-ranges of one tile.
-    t = it / a.splits;
-    w.split = it - t * a.splits;
-  }
-  w.kb0 = static_cast<int32_t>(static_cast<int64_t>(w.split) * total / a.splits);
-  w.kb1 = static_cast<int32_t>(static_cast<int64_t>(w.split + 1) * total / a.splits);
+  w.kb0 = Cfg::kSplit > 1 ? rank * total / Cfg::kSplit : 0;
+  w.kb1 = Cfg::kSplit > 1 ? (rank + 1) * total / Cfg::kSplit : total;
   w.batch = t / a.per_batch;
   const int32_t r = t - w.batch * a.per_batch;
   if constexpr (Cfg::kSym) {
@@ -142,6 +146,190 @@ __device__ __forceinline__ FusedItem fused_item(const FusedArgs& a, int32_t it) 
   return w;
 }
 
+// 2 kN bytes of kN 16-bit values at p (aligned to them).
+template <int kN>
+__device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&v)[kN / 2]) {
+  if constexpr (kN == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(v[0], v[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN / 8; ++i)
+      ptx::st_global_v4(p + 8 * i, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
+}
+
+// The end of a split cluster's tile, run by all 256 threads of each CTA.
+template <class Cfg>
+__device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t unit, int32_t rank,
+                                               uint32_t tmem_base, uint32_t recv, uint32_t tfull,
+                                               const Watch& w) {
+  constexpr int kS = Cfg::kSplit;
+  constexpr int kCols = Cfg::kBN / kS;  // accumulator columns this CTA finishes
+  constexpr int kHalfCols = kCols / 2;  // gated: gate columns, then as many up columns
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ptx::griddep_wait();  // reads S, g and u; writes the outputs
+  bool ok = wait_bar_warp<false>(tfull, 0u, w, kSiteTmemFull, unit);
+  if (ok) {
+    // Send: warp quarter q owns 32 rows, warps 0-3 columns 0-63, warps 4-7 the
+    // rest (gated: gate, up).  Receiver's slot: [source][4 columns][row][16 B],
+    // so a warp writes 512 contiguous bytes at a time.
+    ptx::tc_fence_after();
+    const int q = warp & 3, side = warp >> 2;
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + side * 64;
+    const uint32_t mine = recv + static_cast<uint32_t>(rank * (kCols / 4) * 128 + q * 32 + lane) * 16u;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint32_t v[16];
+      ptx::tmem_ld_32x32b_x16(t_row + g * 16, v);
+      ptx::tmem_wait_ld(v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = g * 16 + j * 4;  // of this side's 64
+        int to, at;                    // receiving CTA, its 4-column group
+        if (Cfg::kGlu) {
+          to = c / kHalfCols;
+          at = (c % kHalfCols) / 4 + side * (kHalfCols / 4);
+        } else {
+          to = (side * 64 + c) / kCols;
+          at = (side * 64 + c) % kCols / 4;
+        }
+        ptx::st_shared_cluster_v4(ptx::mapa(mine + static_cast<uint32_t>(at * 128) * 16u, static_cast<uint32_t>(to)),
+                                  v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      }
+    }
+  }
+  ptx::cluster_sync();
+  if (!ok) return;
+  // Add and finish: thread (row, half) takes half of the CTA's columns.
+  constexpr int kN = Cfg::kGlu ? kHalfCols / 2 : kCols / 2;
+  const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
+  const FusedItem wi = fused_item<Cfg>(args, unit, rank);
+  const int32_t row = wi.mb * Cfg::kBM + r;
+  const int32_t col0 = wi.nb * Cfg::kOutN + rank * (Cfg::kOutN / kS) + half * kN;
+  if (row >= args.M || col0 >= args.N) return;
+  auto sum = [&](int first4, float (&v)[kN]) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kS; ++s)
+#pragma unroll
+      for (int i = 0; i < kN / 4; ++i) {
+        const float4 p = ptx::ld_shared_v4_f32(
+            recv + static_cast<uint32_t>((s * (kCols / 4) + first4 + i) * 128 + r) * 16u);
+        v[4 * i] += p.x, v[4 * i + 1] += p.y, v[4 * i + 2] += p.z, v[4 * i + 3] += p.w;
+      }
+  };
+  const bool bf16 = args.bf16 != 0;
+  // Columns come in groups of eight that are in or out together (four, gated
+  // over eight CTAs): N is a multiple of 8, or the rows are padded to one.
+  constexpr int kG = kN < 8 ? kN : 8;
+  float v[kN];
+  sum(half * (kN / 4), v);
+  if constexpr (Cfg::kEpi == kEpiStore) {
+    uint16_t* c = args.c + static_cast<int64_t>(row) * args.ldc + col0;
+#pragma unroll
+    for (int i = 0; i < kN; i += kG) {
+      uint32_t p[kG / 2];
+#pragma unroll
+      for (int j = 0; j < kG / 2; ++j)
+        p[j] = pack16(bf16, args.alpha * v[i + 2 * j], args.alpha * v[i + 2 * j + 1]);
+      if (col0 + i < args.N) store16<kG>(c + i, p);
+    }
+  } else if constexpr (Cfg::kEpi == kEpiGlu) {
+    float u[kN];
+    sum(kHalfCols / 4 + half * (kN / 4), u);
+    uint16_t* c = args.c + static_cast<int64_t>(row) * args.ldc + col0;
+    uint16_t* d = args.d + static_cast<int64_t>(row) * 2 * args.N + col0;
+#pragma unroll
+    for (int i = 0; i < kN; i += kG) {
+      uint32_t h[kG / 2], gp[kG / 2], up[kG / 2];
+#pragma unroll
+      for (int j = 0; j < kG / 2; ++j) {
+        const int k = i + 2 * j;
+        h[j] = pack16(bf16, act_value(args.act, v[k]) * u[k], act_value(args.act, v[k + 1]) * u[k + 1]);
+        gp[j] = pack16(bf16, v[k], v[k + 1]);
+        up[j] = pack16(bf16, u[k], u[k + 1]);
+      }
+      if (col0 + i < args.N) {
+        store16<kG>(c + i, h);
+        if (args.save) {
+          store16<kG>(d + i, gp);
+          store16<kG>(d + args.N + i, up);
+        }
+      }
+    }
+  } else if constexpr (Cfg::kEpi == kEpiGluBwd) {
+    const uint16_t* gu = args.src + static_cast<int64_t>(row) * args.src_ld + col0;
+    uint16_t* c = args.c + static_cast<int64_t>(row) * args.ldc + col0;
+    uint16_t* d = args.d + static_cast<int64_t>(row) * 2 * args.N + col0;
+#pragma unroll
+    for (int i = 0; i < kN; i += kG) {
+      if (col0 + i >= args.N) break;
+      const uint4 gv = ptx::ld_global_v4_u32(gu + i), uv = ptx::ld_global_v4_u32(gu + args.N + i);
+      const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w}, uw[4] = {uv.x, uv.y, uv.z, uv.w};
+      uint32_t h[kG / 2], dg[kG / 2], du[kG / 2];
+#pragma unroll
+      for (int j = 0; j < kG / 2; ++j) {
+        const float2 gf = unpack16(bf16, gw[j]), uf = unpack16(bf16, uw[j]);
+        float a0, a1, s0, s1;
+        act_both(args.act, gf.x, a0, s0);
+        act_both(args.act, gf.y, a1, s1);
+        const float d0 = v[i + 2 * j], d1 = v[i + 2 * j + 1];
+        dg[j] = pack16(bf16, d0 * uf.x * s0, d1 * uf.y * s1);
+        du[j] = pack16(bf16, d0 * a0, d1 * a1);
+        h[j] = pack16(bf16, a0 * uf.x, a1 * uf.y);
+      }
+      store16<kG>(c + i, h);
+      store16<kG>(d + i, dg);
+      store16<kG>(d + args.N + i, du);
+    }
+  } else {
+    const int64_t batch = static_cast<int64_t>(wi.batch) * 2;
+    const uint16_t* sh = args.src + batch * args.src_part + static_cast<int64_t>(row) * args.src_ld + col0;
+    uint16_t* base = args.c + batch * args.c_part;
+    uint16_t* c = base + static_cast<int64_t>(row) * args.ldc + col0;
+#pragma unroll
+    for (int i = 0; i < kN; i += kG) {
+      if (col0 + i >= args.N) break;
+      float x[kG];
+#pragma unroll
+      for (int j = 0; j < kG; ++j) x[j] = args.alpha * v[i + j];
+      if (args.beta != 0.0f) {
+        const uint4 a = ptx::ld_global_v4_u32(sh + i), b = ptx::ld_global_v4_u32(sh + args.src_part + i);
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < kG / 2; ++j) {
+          const float2 hf = unpack16(false, aw[j]), lf = unpack16(false, bw[j]);
+          x[2 * j] = fmaf(args.beta, hf.x + lf.x, x[2 * j]);
+          x[2 * j + 1] = fmaf(args.beta, hf.y + lf.y, x[2 * j + 1]);
+        }
+      }
+      uint32_t hi[kG / 2], lo[kG / 2];
+#pragma unroll
+      for (int j = 0; j < kG / 2; ++j) {
+        hi[j] = pack16(false, x[2 * j], x[2 * j + 1]);
+        const float2 back = unpack16(false, hi[j]);
+        lo[j] = pack16(false, x[2 * j] - back.x, x[2 * j + 1] - back.y);
+      }
+      store16<kG>(c + i, hi);
+      store16<kG>(c + args.c_part + i, lo);
+      if constexpr (Cfg::kSym) {
+        // Transposed: a warp's 32 rows are 64 contiguous bytes of each column.
+        if (wi.mb != wi.nb) {
+#pragma unroll
+          for (int j = 0; j < kG; ++j) {
+            uint16_t* t = base + static_cast<int64_t>(col0 + i + j) * args.ldc + row;
+            if (col0 + i + j < args.N) {
+              ptx::st_global_b16(t, static_cast<uint16_t>(hi[j / 2] >> (16 * (j & 1))));
+              ptx::st_global_b16(t + args.c_part, static_cast<uint16_t>(lo[j / 2] >> (16 * (j & 1))));
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     fused_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -155,9 +343,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   const uint32_t sb = ptx::smem_addr(smem);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  constexpr bool kCluster = Cfg::kCluster > 1;
   const uint32_t cta = kPair ? ptx::cluster_ctarank() : 0u;  // 0: issues the MMAs
-  const int32_t unit = kPair ? static_cast<int32_t>(ptx::cluster_id_x()) : static_cast<int32_t>(blockIdx.x);
-  const int32_t units = kPair ? static_cast<int32_t>(ptx::num_clusters_x()) : static_cast<int32_t>(gridDim.x);
+  const int32_t rank = Cfg::kSplit > 1 ? static_cast<int32_t>(ptx::cluster_ctarank()) : 0;  // k-range
+  const int32_t unit = kCluster ? static_cast<int32_t>(ptx::cluster_id_x()) : static_cast<int32_t>(blockIdx.x);
+  const int32_t units = kCluster ? static_cast<int32_t>(ptx::num_clusters_x()) : static_cast<int32_t>(gridDim.x);
 
   const uint32_t bar0 = sb + Cfg::kOffBar;
   auto bar_full = [&](int s) { return bar0 + 8u * s; };
@@ -190,8 +380,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     ptx::tmem_relinquish<Cfg::kCtas>();
   }
   ptx::tc_fence_before();
-  if constexpr (kPair)
-    ptx::cluster_sync();  // both CTAs' barriers exist before either uses the other's
+  if constexpr (kCluster)
+    ptx::cluster_sync();  // every CTA runs, its barriers set up, before another uses its memory
   else
     __syncthreads();
   ptx::tc_fence_after();
@@ -216,7 +406,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     int64_t fills = 0;
     bool ok = true, first_item = true;
     for (int32_t it = unit; ok && it < args.items; it += units) {
-      const FusedItem wi = fused_item<Cfg>(args, it);
+      const FusedItem wi = fused_item<Cfg>(args, it, rank);
       int32_t row, z0 = wi.batch * args.z_mul;
       if (is_a)
         row = wi.mb * Cfg::kTileM + static_cast<int32_t>(cta) * Cfg::kBM;
@@ -303,7 +493,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       int32_t acc_iter = 0;
       bool ok = true;
       for (int32_t it = unit; ok && it < args.items; it += units) {
-        const FusedItem wi = fused_item<Cfg>(args, it);
+        const FusedItem wi = fused_item<Cfg>(args, it, rank);
         const int buf = acc_iter & 1;
         const uint32_t use_par = static_cast<uint32_t>((acc_iter >> 1) & 1);
         if (!wait_bar_warp<kPair>(bar_tempty(buf), use_par ^ 1u, w, kSiteTmemEmpty, it)) {
@@ -357,7 +547,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       __syncwarp();
       wait_bar_warp<kPair>(bar_mma_done, 0u, w, kSiteMmaDone, -1, /*honor_abort=*/false);
     }
-  } else if (warp >= 2 && warp < 2 + Cfg::kEpiWarps) {
+  } else if (Cfg::kSplit == 1 && warp >= 2 && warp < 2 + Cfg::kEpiWarps) {
     // ------------------------------------------------------------ epilogue --
     ptx::griddep_wait();  // reads S, g and u; writes the outputs
     const int q = warp & 3;  // this warp may touch TMEM lanes 32q .. 32q+31 only
@@ -416,7 +606,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     for (int32_t it = unit;; it += units) {
       // Every warp takes the same decision, so none is left at a barrier.
       if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, it < args.items)) break;
-      const FusedItem wi = fused_item<Cfg>(args, it);
+      const FusedItem wi = fused_item<Cfg>(args, it, rank);
       const int buf = acc_iter & 1;
       const uint32_t use_par = static_cast<uint32_t>((acc_iter >> 1) & 1);
       ++acc_iter;
@@ -562,26 +752,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
               store_chunk_t(lo, col0, row0, z + 1, in);
             }
           }
-        } else {  // kEpiPartial
-          float* out = args.partial + static_cast<int64_t>(wi.split) * args.part_stride +
-                       static_cast<int64_t>(row) * args.part_ld + col0;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t v[32];
-            ptx::tmem_ld_32x32b_x32(t_row + c * 64 + half * 32, v);
-            ptx::tmem_wait_ld(v);
-            if (last && half == 1) release_tmem();
-#pragma unroll
-            for (int j = 0; j < 8; ++j)  // part_ld is a multiple of 4 and covers N
-              if (row_in && col0 + half * 32 + j * 4 < args.N)
-                ptx::st_global_v4(out + half * 32 + j * 4, v[4 * j], v[4 * j + 1], v[4 * j + 2],
-                                  v[4 * j + 3]);
-          }
         }
       }
     }
     if (lane == 0) ptx::bulk_wait_group<0>();
     __syncwarp();
+  }
+
+  if constexpr (Cfg::kSplit > 1) {
+    __syncwarp();
+    split_epilogue<Cfg>(args, unit, rank, tmem_base, sb + Cfg::kOffEpi, bar_tfull(0), w);
   }
 
   ptx::tc_fence_before();

@@ -12,13 +12,13 @@
 #include "fused_kernel.cuh"
 #include "gemm_ops.h"
 #include "ortho_kernels.cuh"
-#include "reduce_kernels.cuh"
 #include "stream_kernel.cuh"
 
 struct gemm_ops_s {
   int device = 0;
   int num_sms = 0;
   int max_pairs = 0;  // CTA pairs of the pair kernels that fit on the device at once
+  int max_split[4] = {};  // clusters of 1, 2, 4, 8 CTAs sharing a tile
   void* encode = nullptr;
   uint32_t* d_err = nullptr;  // 4-word watchdog record
   uint32_t last_err[4] = {0, 0, 0, 0};
@@ -44,8 +44,8 @@ constexpr int kGroupM = 8;
 // 128 x 128 for problems of few tiles.
 template <int kEpi>
 using Pair = FusedCfg<2, 256, kEpi == kEpiStore ? 6 : 5, kEpi, kEpi == kEpiStore ? 2 : 4>;
-template <int kEpi>
-using Lone = FusedCfg<1, 128, 5, kEpi, 4>;
+template <int kEpi, int kSplit = 1>
+using Lone = FusedCfg<1, 128, 5, kEpi, 4, kSplit>;
 
 struct DeviceGuard {
   int prev = -1;
@@ -170,7 +170,6 @@ FusedArgs base_args(const gemm_ops_s* h, const Product& p) {
   a.num_kb = static_cast<int32_t>(cdiv(p.K, 64));
   a.segs = static_cast<int32_t>(p.segs);
   a.z_mul = static_cast<int32_t>(p.z_mul);
-  a.splits = 1;
   a.group_m = kGroupM;
   a.a_mn = p.a_mn;
   a.b_mn = p.b_mn;
@@ -198,59 +197,52 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
   if (!d.p) md = ma;
   const int64_t tm = cdiv(p.M, Cfg::kTileM), tn = cdiv(p.N, Cfg::kOutN);
   const int64_t per = Cfg::kSym ? tn * (tn + 1) / 2 : tm * tn;
-  const int64_t items = per * p.batch * a.splits;
+  const int64_t items = per * p.batch;
   if (items > INT32_MAX / 2) return GEMM_ERR_INVALID_ARG;
   a.tiles_m = static_cast<int32_t>(tm);
   a.tiles_n = static_cast<int32_t>(tn);
   a.per_batch = static_cast<int32_t>(per);
   a.items = static_cast<int32_t>(items);
+  a.c = static_cast<uint16_t*>(const_cast<void*>(c.p));
+  a.ldc = c.pitch;
+  a.c_part = c.zstride;
+  a.d = static_cast<uint16_t*>(const_cast<void*>(d.p));
   const int64_t fit = Cfg::kCtas == 2 ? h->max_pairs : h->num_sms;
-  const int units = static_cast<int>(std::min<int64_t>(items, fit));
-  return launch(h, fused_kernel<Cfg>, dim3(units * Cfg::kCtas), dim3(Cfg::kThreads), Cfg::kSmemBytes,
-                Cfg::kCtas, stream, ma, mb, mc, md, a);
+  const int64_t units = Cfg::kSplit > 1 ? items : std::min<int64_t>(items, fit);
+  return launch(h, fused_kernel<Cfg>, dim3(static_cast<unsigned>(units * Cfg::kCluster)), dim3(Cfg::kThreads),
+                Cfg::kSmemBytes, Cfg::kCluster, stream, ma, mb, mc, md, a);
 }
 
-// Pairs when their 256-row tiles fill at least half of the device.
-bool use_pair(const gemm_ops_s* h, int64_t tiles) { return h->max_pairs > 0 && 2 * tiles >= h->max_pairs; }
-
+// Which form: split clusters where the 128 x 128 tiles are few (each CTA with
+// two k-blocks at least); pairs when the 256-row tiles fill at least half of
+// the device; else lone CTAs.  Of clusters of eight CTAs 15 fit at once, of
+// four 36, of two 76.  The batched products (high and low parts) go by one
+// matrix's tiles alone, so that a matrix of a batch gets the same sums as by
+// itself, and split less, since the others of the batch fill the device too
+// (6 x 1000 x 344: 395 us for the update with the limits of single products).
 template <int kEpi>
 gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const Stack& c,
                     const Stack& d, cudaStream_t stream) {
-  const int64_t tm = cdiv(p.M, 256), tn = cdiv(p.N, Pair<kEpi>::kOutN);
-  const int64_t tiles = (Pair<kEpi>::kSym ? tn * (tn + 1) / 2 : tm * tn) * p.batch;
-  return use_pair(h, tiles) ? launch_fused<Pair<kEpi>>(h, p, a, c, d, stream)
-                            : launch_fused<Lone<kEpi>>(h, p, a, c, d, stream);
-}
-
-// k-ranges per tile for a product of few 128 x 128 tiles: enough to give
-// every SM one, of at least four k-blocks each.
-int64_t splits_for(const gemm_ops_s* h, int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = cdiv(M, 128) * cdiv(N, 128);
-  if (2 * tiles > h->num_sms) return 1;
-  return std::max<int64_t>(1, std::min<int64_t>(h->num_sms / tiles, cdiv(K, 64) / 4));
-}
-
-size_t partial_bytes(const gemm_ops_s* h, int64_t M, int64_t N, int64_t K) {
-  const int64_t s = splits_for(h, M, N, K);
-  return s > 1 ? static_cast<size_t>(s) * M * N * 4 : 0;
+  auto tiles = [&](int64_t tm, int64_t tn) { return Pair<kEpi>::kSym ? tn * (tn + 1) / 2 : tm * tn; };
+  const int64_t small = tiles(cdiv(p.M, 128), cdiv(p.N, Lone<kEpi>::kOutN));
+  const int64_t kb = cdiv(p.K, 64) * p.segs;
+  constexpr bool kBatched = kEpi == kEpiSplit || kEpi == kEpiSplitSym;
+  const int64_t most[3] = {kBatched ? 36 : h->max_split[1], kBatched ? 16 : h->max_split[2],
+                           kBatched ? 2 : h->max_split[3]};
+  if (small <= std::min<int64_t>(most[2], h->max_split[3]) && kb >= 16)
+    return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream);
+  if (small <= std::min<int64_t>(most[1], h->max_split[2]) && kb >= 8)
+    return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream);
+  if (small <= std::min<int64_t>(most[0], h->max_split[1]) && kb >= 4)
+    return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream);
+  const int64_t big = tiles(cdiv(p.M, 256), cdiv(p.N, Pair<kEpi>::kOutN));
+  return h->max_pairs > 0 && 2 * big >= h->max_pairs ? launch_fused<Pair<kEpi>>(h, p, a, c, d, stream)
+                                                     : launch_fused<Lone<kEpi>>(h, p, a, c, d, stream);
 }
 
 // out = A B^T, rounded to 16 bits.
-gemm_status_t product(gemm_ops_s* h, const Product& p, void* out, int64_t ldo, void* partial,
-                      cudaStream_t stream) {
-  FusedArgs a = base_args(h, p);
-  const int64_t s = splits_for(h, p.M, p.N, p.K);
-  if (s == 1) return fused<kEpiStore>(h, p, a, {out, p.M, p.N, ldo, 1, p.M * ldo}, {}, stream);
-  a.splits = static_cast<int32_t>(s);
-  a.partial = static_cast<float*>(partial);
-  a.part_ld = p.N;
-  a.part_stride = p.M * p.N;
-  gemm_status_t st = launch_fused<Lone<kEpiPartial>>(h, p, a, {}, {}, stream);
-  if (st != GEMM_OK) return st;
-  ReduceArgs r = {a.partial, a.part_ld, a.part_stride, a.splits, a.M, a.N, a.bf16, 0,
-                  static_cast<uint16_t*>(out), ldo, nullptr, nullptr};
-  const int64_t blocks = std::min<int64_t>(cdiv(p.M * p.N / 4, 256), 8 * h->num_sms);
-  return launch(h, reduce_kernel<kReduceStore>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, stream, r);
+gemm_status_t product(gemm_ops_s* h, const Product& p, void* out, int64_t ldo, cudaStream_t stream) {
+  return fused<kEpiStore>(h, p, base_args(h, p), {out, p.M, p.N, ldo, 1, p.M * ldo}, {}, stream);
 }
 
 // How a product of few tokens is laid out: warps per CTA, CTAs per k-slice,
@@ -372,15 +364,22 @@ bool set_attr() {
                               Cfg::kSmemBytes) == cudaSuccess;
 }
 
+template <int kSplit>
+bool set_split_attr() {
+  return set_attr<Lone<kEpiStore, kSplit>>() && set_attr<Lone<kEpiGlu, kSplit>>() &&
+         set_attr<Lone<kEpiGluBwd, kSplit>>() && set_attr<Lone<kEpiSplit, kSplit>>() &&
+         set_attr<Lone<kEpiSplitSym, kSplit>>();
+}
+
 template <class Cfg>
 int max_clusters() {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(Cfg::kCtas, 1, 1);
+  cfg.gridDim = dim3(Cfg::kCluster, 1, 1);
   cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Cfg::kSmemBytes;
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = Cfg::kCtas;
+  attr[0].val.clusterDim.x = Cfg::kCluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -408,21 +407,8 @@ gemm_status_t check_ld(int64_t ld, int64_t cols) {
   return ld % 8 != 0 ? GEMM_ERR_ALIGNMENT : GEMM_OK;
 }
 
-// Offsets into the backward pass's workspace.
-struct BwdSpace {
-  size_t dgu, h, partial, total;
-};
-BwdSpace bwd_space(const gemm_ops_s* h, int64_t T, int64_t D, int64_t F) {
-  BwdSpace s;
-  s.dgu = 0;
-  s.h = up(T * 2 * F * 2, 256);
-  s.partial = s.h + up(T * F * 2, 256);
-  // dh, dx, dw_down and dw_in are summed one after the other.
-  size_t part = std::max(partial_bytes(h, T, F, D), partial_bytes(h, T, D, 2 * F));
-  part = std::max(part, std::max(partial_bytes(h, D, F, T), partial_bytes(h, 2 * F, D, T)));
-  s.total = s.partial + part;
-  return s;
-}
+// The backward pass's workspace: dg and du, then h.
+size_t bwd_h_offset(int64_t T, int64_t F) { return up(T * 2 * F * 2, 256); }
 
 struct OrthoSpace {
   int64_t r, pitch, pitch_r;  // r: order of the Gram matrix
@@ -470,7 +456,8 @@ gemm_status_t gemm_ops_create(gemm_ops_t* out, int device) {
   if (!set_attr<Pair<kEpiStore>>() || !set_attr<Pair<kEpiGlu>>() || !set_attr<Pair<kEpiGluBwd>>() ||
       !set_attr<Pair<kEpiSplit>>() || !set_attr<Pair<kEpiSplitSym>>() || !set_attr<Lone<kEpiStore>>() ||
       !set_attr<Lone<kEpiGlu>>() || !set_attr<Lone<kEpiGluBwd>>() || !set_attr<Lone<kEpiSplit>>() ||
-      !set_attr<Lone<kEpiSplitSym>>() || !set_attr<Lone<kEpiPartial>>() ||
+      !set_attr<Lone<kEpiSplitSym>>() ||
+      !set_split_attr<2>() || !set_split_attr<4>() || !set_split_attr<8>() ||
       !set_stream_attr<kW16, false>() || !set_stream_attr<kW16, true>() ||
       !set_stream_attr<kW4G32, false>() || !set_stream_attr<kW4G32, true>() ||
       !set_stream_attr<kW4G64, false>() || !set_stream_attr<kW4G64, true>() ||
@@ -484,6 +471,9 @@ gemm_status_t gemm_ops_create(gemm_ops_t* out, int device) {
   h->max_pairs = std::min({max_clusters<Pair<kEpiStore>>(), max_clusters<Pair<kEpiGlu>>(),
                            max_clusters<Pair<kEpiGluBwd>>(), max_clusters<Pair<kEpiSplit>>(),
                            max_clusters<Pair<kEpiSplitSym>>()});
+  h->max_split[1] = max_clusters<Lone<kEpiStore, 2>>();
+  h->max_split[2] = max_clusters<Lone<kEpiStore, 4>>();
+  h->max_split[3] = max_clusters<Lone<kEpiStore, 8>>();
   if (cudaMalloc(&h->d_err, sizeof(h->last_err)) != cudaSuccess) {
     delete h;
     return GEMM_ERR_OOM;
@@ -537,10 +527,9 @@ uint64_t gemm_ops_launch_count(gemm_ops_t h) { return h ? h->launches : 0; }
 size_t gemm_gated_ffn_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t F) {
   if (!h || T <= 0 || D <= 0 || F <= 0) return 0;
   size_t s = up(T * F * 2, 256);
-  // Few tokens whose weights do not suit the streaming kernel take the other way.
   if (T <= kMaxStreamTokens)
     s += std::max(stream_partial_bytes<kW16, true>(h, T, F, D), stream_partial_bytes<kW16, false>(h, T, D, F));
-  return s + std::max(partial_bytes(h, T, 2 * F, D), partial_bytes(h, T, D, F));
+  return s;
 }
 
 gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const void* w_in,
@@ -598,38 +587,22 @@ gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const voi
     a.cols = static_cast<int32_t>(D);
     return stream_product<kW16, false>(h, a, bf16, s);
   }
-  const Stack xs = {x, T, D, ldx, 1, T * ldx};
-  const int64_t split = splits_for(h, T, 2 * F, D);
-  if (split == 1) {
-    const Product p = {T, F, D, xs, {w_in, F, D, ldw_in, 2, F * ldw_in}, false, false, bf16, 1, 1, 0};
-    FusedArgs a = base_args(h, p);
-    a.act = act;
-    a.save = gu != nullptr;
-    const Stack keep = {gu, T, F, 2 * F, 2, F};
-    st = fused<kEpiGlu>(h, p, a, {hid, T, F, F, 1, T * F}, gu ? keep : Stack{}, s);
-  } else {
-    const Product p = {T, 2 * F, D, xs, {w_in, 2 * F, D, ldw_in, 1, 2 * F * ldw_in}, false, false, bf16, 1, 1, 0};
-    FusedArgs a = base_args(h, p);
-    a.splits = static_cast<int32_t>(split);
-    a.partial = static_cast<float*>(partial);
-    a.part_ld = 2 * F;
-    a.part_stride = T * 2 * F;
-    st = launch_fused<Lone<kEpiPartial>>(h, p, a, {}, {}, s);
-    if (st != GEMM_OK) return st;
-    ReduceArgs r = {a.partial, a.part_ld, a.part_stride, a.splits, a.M, static_cast<int32_t>(F), a.bf16, act,
-                    static_cast<uint16_t*>(hid), F, static_cast<uint16_t*>(gu), nullptr};
-    const int64_t blocks = std::min<int64_t>(cdiv(T * F / 4, 256), 8 * h->num_sms);
-    st = launch(h, reduce_kernel<kReduceGlu>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, s, r);
-  }
-  if (st != GEMM_OK) return st;
-  const Product p = {T, D, F, {hid, T, F, F, 1, T * F}, {w_down, D, F, ldw_down, 1, D * ldw_down},
+  const Product p = {T, F, D, {x, T, D, ldx, 1, T * ldx}, {w_in, F, D, ldw_in, 2, F * ldw_in},
                      false, false, bf16, 1, 1, 0};
-  return product(h, p, y, ldy, partial, s);
+  FusedArgs a = base_args(h, p);
+  a.act = act;
+  a.save = gu != nullptr;
+  const Stack keep = {gu, T, F, 2 * F, 2, F};
+  st = fused<kEpiGlu>(h, p, a, {hid, T, F, F, 1, T * F}, gu ? keep : Stack{}, s);
+  if (st != GEMM_OK) return st;
+  const Product down = {T, D, F, {hid, T, F, F, 1, T * F}, {w_down, D, F, ldw_down, 1, D * ldw_down},
+                        false, false, bf16, 1, 1, 0};
+  return product(h, down, y, ldy, s);
 }
 
 size_t gemm_gated_ffn_backward_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t F) {
   if (!h || T <= 0 || D <= 0 || F <= 0) return 0;
-  return bwd_space(h, T, D, F).total;
+  return bwd_h_offset(T, F) + up(T * F * 2, 256);
 }
 
 gemm_status_t gemm_gated_ffn_backward(gemm_ops_t h, const void* dy, int64_t lddy, const void* x,
@@ -672,44 +645,24 @@ gemm_status_t gemm_gated_ffn_backward(gemm_ops_t h, const void* dy, int64_t lddy
                ? GEMM_OK
                : GEMM_ERR_CUDA;
   const bool bf16 = dtype == GEMM_BF16;
-  const BwdSpace sp = bwd_space(h, T, D, F);
-  char* ws = static_cast<char*>(workspace);
-  uint16_t* dgu = reinterpret_cast<uint16_t*>(ws + sp.dgu);
-  uint16_t* hid = reinterpret_cast<uint16_t*>(ws + sp.h);
-  void* partial = ws + sp.partial;
+  uint16_t* dgu = static_cast<uint16_t*>(workspace);
+  uint16_t* hid = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + bwd_h_offset(T, F));
   const Stack dys = {dy, T, D, lddy, 1, T * lddy};
-  {
-    // dh = dy Wd (Wd is stored [K, N] here), then dg, du and h.
-    const Product p = {T, F, D, dys, {w_down, D, F, ldw_down, 1, D * ldw_down}, false, true, bf16, 1, 1, 0};
-    FusedArgs a = base_args(h, p);
-    a.act = act;
-    const int64_t split = splits_for(h, T, F, D);
-    if (split == 1) {
-      a.src = static_cast<const uint16_t*>(gu);
-      a.src_ld = 2 * F;
-      st = fused<kEpiGluBwd>(h, p, a, {hid, T, F, F, 1, T * F}, {dgu, T, F, 2 * F, 2, F}, s);
-    } else {
-      a.splits = static_cast<int32_t>(split);
-      a.partial = static_cast<float*>(partial);
-      a.part_ld = F;
-      a.part_stride = T * F;
-      st = launch_fused<Lone<kEpiPartial>>(h, p, a, {}, {}, s);
-      if (st != GEMM_OK) return st;
-      ReduceArgs r = {a.partial, a.part_ld, a.part_stride, a.splits, a.M, a.N, a.bf16, act,
-                      hid, F, const_cast<uint16_t*>(static_cast<const uint16_t*>(gu)), dgu};
-      const int64_t blocks = std::min<int64_t>(cdiv(T * F / 4, 256), 8 * h->num_sms);
-      st = launch(h, reduce_kernel<kReduceGluBwd>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, s, r);
-    }
-    if (st != GEMM_OK) return st;
-  }
-  // dw_down [D, F] = dy^T h; dx = [dg du] w_in; dw_in [2F, D] = [dg du]^T x.
   const Stack hs = {hid, T, F, F, 1, T * F}, dgus = {dgu, T, 2 * F, 2 * F, 1, T * 2 * F};
+  // dh = dy Wd (Wd is stored [K, N] here), then dg, du and h.
+  const Product ph = {T, F, D, dys, {w_down, D, F, ldw_down, 1, D * ldw_down}, false, true, bf16, 1, 1, 0};
+  FusedArgs a = base_args(h, ph);
+  a.act = act;
+  a.src = static_cast<const uint16_t*>(gu);
+  a.src_ld = 2 * F;
+  if ((st = fused<kEpiGluBwd>(h, ph, a, hs, {dgu, T, F, 2 * F, 2, F}, s)) != GEMM_OK) return st;
+  // dw_down [D, F] = dy^T h; dx = [dg du] w_in; dw_in [2F, D] = [dg du]^T x.
   const Product pd = {D, F, T, dys, hs, true, true, bf16, 1, 1, 0};
-  if ((st = product(h, pd, dw_down, F, partial, s)) != GEMM_OK) return st;
+  if ((st = product(h, pd, dw_down, F, s)) != GEMM_OK) return st;
   const Product px = {T, D, 2 * F, dgus, {w_in, 2 * F, D, ldw_in, 1, 2 * F * ldw_in}, false, true, bf16, 1, 1, 0};
-  if ((st = product(h, px, dx, lddx, partial, s)) != GEMM_OK) return st;
+  if ((st = product(h, px, dx, lddx, s)) != GEMM_OK) return st;
   const Product pi = {2 * F, D, T, dgus, {x, T, D, ldx, 1, T * ldx}, true, true, bf16, 1, 1, 0};
-  return product(h, pi, dw_in, D, partial, s);
+  return product(h, pi, dw_in, D, s);
 }
 
 static size_t w4_workspace(gemm_ops_t h, int64_t T, int64_t N, int64_t K, bool gated) {

@@ -26,6 +26,7 @@ from . import GemmError, _check, load as _load
 __all__ = ["Ops", "default_ops", "gated_ffn", "gated_ffn_backward", "w4_linear", "w4_gated",
            "w4_quantize", "orthogonalize", "NEWTON_SCHULZ"]
 
+_F16, _BF16 = torch.float16, torch.bfloat16
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _ACT = {"silu": 0, "gelu_tanh": 1, "relu": 2}
 
@@ -81,32 +82,57 @@ def _act(act) -> int:
         raise ValueError(f"act must be one of {sorted(_ACT)}, got {act!r}") from None
 
 
-def _matrix(t, name, dtype, device, shape=None, contiguous=False):
+def _matrix(t, name, dtype, index, shape, contiguous=False):
     """Checks one 2-D operand; returns its row distance in elements."""
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+        return shape[1]  # the common case, in few calls: small products are bound by the host
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be {list(shape) if shape is not None else '2-D'}, got {list(t.shape)}")
-    rows, cols = t.shape
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    rows, cols = shape
     ld, inner = t.stride()
-    if (cols > 1 and inner != 1) or (rows > 1 and ld < cols) or (contiguous and not t.is_contiguous()):
-        raise ValueError(f"{name}'s rows must be contiguous" if not contiguous else f"{name} must be contiguous")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if (cols > 1 and inner != 1) or (rows > 1 and ld < cols):
+        raise ValueError(f"{name}'s rows must be contiguous")
     # One row or none, or nothing in a row: the distance to the next is free.
-    return ld if rows > 1 and cols else (cols + 7) // 8 * 8
+    return ld if rows > 1 and cols else cols
 
 
-def _floating(t, name):
-    if t.dtype != torch.float16 and t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
-    if not t.is_cuda:
+def _operand(t, name):
+    """Type, device index and shape of a call's first operand."""
+    dt, index, shape = t.dtype, t.get_device(), t.shape
+    if dt is not _F16 and dt is not _BF16:
+        raise TypeError(f"{name} must be float16 or bfloat16, got {dt}")
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {list(shape)}")
+    return dt, index, shape
 
 
-def _stream(stream, device):
+def _columns(t, name, rows):
+    """Columns of a matrix that has to have `rows` rows."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows:
+        raise ValueError(f"{name} must be a matrix of {rows} rows, got {list(shape)}")
+    return shape[1]
+
+
+def _current_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The handle alone, without building a stream object (where torch has it).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
+def _stream(stream, index):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current_stream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -117,7 +143,9 @@ class Ops:
         self._lib = _lib()
         self._h = ctypes.c_void_p()
         _check(self._lib.gemm_ops_create(ctypes.byref(self._h), int(device)), "gemm_ops_create")
-        self.device = torch.device("cuda", int(device))
+        self.index = int(device)
+        self.device = torch.device("cuda", self.index)
+        self._needs = {}  # workspace bytes by operator and sizes
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
@@ -147,86 +175,106 @@ class Ops:
     def launch_count(self) -> int:
         return int(self._lib.gemm_ops_launch_count(self._h))
 
+    def _workspace(self, query, *sizes):
+        """A workspace of torch's allocator: (tensor, address, bytes)."""
+        key = (query, sizes)
+        need = self._needs.get(key)
+        if need is None:
+            if len(self._needs) >= 4096:
+                self._needs.clear()
+            need = self._needs[key] = getattr(self._lib, query)(self._h, *sizes)
+        if not need:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return ws, ws.data_ptr(), need
+
+    def _same_device(self, index, name):
+        if index != self.index:
+            raise ValueError(f"{name} is on cuda:{index}, the handle on cuda:{self.index}")
+
     # -- the gated block ----------------------------------------------------
     def gated_ffn(self, x, w_in, w_down, act="silu", save=False, out=None, stream=None):
-        _floating(x, "x")
-        dt, dev = x.dtype, self.device
+        dt, dev, (T, D) = _operand(x, "x")
+        self._same_device(dev, "x")
         a = _act(act)
-        ldx = _matrix(x, "x", dt, dev)
-        T, D = x.shape
-        ldd = _matrix(w_down, "w_down", dt, dev)
-        F = w_down.shape[1]
-        if w_down.shape[0] != D:
-            raise ValueError(f"w_down must be [{D}, F], got {list(w_down.shape)}")
+        ldx = _matrix(x, "x", dt, dev, (T, D))
+        F = _columns(w_down, "w_down", D)
+        ldd = _matrix(w_down, "w_down", dt, dev, (D, F))
         ldi = _matrix(w_in, "w_in", dt, dev, (2 * F, D))
         if out is None:
-            out = torch.empty((T, D), dtype=dt, device=dev)
-        ldy = _matrix(out, "out", dt, dev, (T, D))
-        gu = torch.empty((T, 2 * F), dtype=dt, device=dev) if save else None
-        need = self._lib.gemm_gated_ffn_workspace(self._h, T, D, F)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        _check(self._lib.gemm_gated_ffn(
+            out = torch.empty((T, D), dtype=dt, device=self.device)
+            ldy = D
+        else:
+            ldy = _matrix(out, "out", dt, dev, (T, D))
+        gu = torch.empty((T, 2 * F), dtype=dt, device=self.device) if save else None
+        ws, wp, need = self._workspace("gemm_gated_ffn_workspace", T, D, F)
+        st = self._lib.gemm_gated_ffn(
             self._h, x.data_ptr(), ldx, w_in.data_ptr(), ldi, w_down.data_ptr(), ldd, out.data_ptr(), ldy,
-            gu.data_ptr() if save else None, ws.data_ptr(), need, T, D, F, a, _DTYPE[dt],
-            _stream(stream, dev)), "gemm_gated_ffn")
+            gu.data_ptr() if save else None, wp, need, T, D, F, a, _DTYPE[dt], _stream(stream, dev))
+        if st:
+            _check(st, "gemm_gated_ffn")
         return (out, gu) if save else out
 
     def gated_ffn_backward(self, dy, x, w_in, w_down, gu, act="silu", stream=None):
-        _floating(x, "x")
-        dt, dev = x.dtype, self.device
+        dt, dev, (T, D) = _operand(x, "x")
+        self._same_device(dev, "x")
         a = _act(act)
-        ldx = _matrix(x, "x", dt, dev)
-        T, D = x.shape
-        ldd = _matrix(w_down, "w_down", dt, dev)
-        F = w_down.shape[1]
-        if w_down.shape[0] != D:
-            raise ValueError(f"w_down must be [{D}, F], got {list(w_down.shape)}")
+        ldx = _matrix(x, "x", dt, dev, (T, D))
+        F = _columns(w_down, "w_down", D)
+        ldd = _matrix(w_down, "w_down", dt, dev, (D, F))
         ldi = _matrix(w_in, "w_in", dt, dev, (2 * F, D))
         ldy = _matrix(dy, "dy", dt, dev, (T, D))
         _matrix(gu, "gu", dt, dev, (T, 2 * F), contiguous=True)
-        dx = torch.empty((T, D), dtype=dt, device=dev)
-        dw_in = torch.empty((2 * F, D), dtype=dt, device=dev)
-        dw_down = torch.empty((D, F), dtype=dt, device=dev)
-        need = self._lib.gemm_gated_ffn_backward_workspace(self._h, T, D, F)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        _check(self._lib.gemm_gated_ffn_backward(
+        dx = torch.empty((T, D), dtype=dt, device=self.device)
+        dw_in = torch.empty((2 * F, D), dtype=dt, device=self.device)
+        dw_down = torch.empty((D, F), dtype=dt, device=self.device)
+        ws, wp, need = self._workspace("gemm_gated_ffn_backward_workspace", T, D, F)
+        st = self._lib.gemm_gated_ffn_backward(
             self._h, dy.data_ptr(), ldy, x.data_ptr(), ldx, w_in.data_ptr(), ldi, w_down.data_ptr(), ldd,
-            gu.data_ptr(), dx.data_ptr(), D, dw_in.data_ptr(), dw_down.data_ptr(), ws.data_ptr(), need,
-            T, D, F, a, _DTYPE[dt], _stream(stream, dev)), "gemm_gated_ffn_backward")
+            gu.data_ptr(), dx.data_ptr(), D, dw_in.data_ptr(), dw_down.data_ptr(), wp, need,
+            T, D, F, a, _DTYPE[dt], _stream(stream, dev))
+        if st:
+            _check(st, "gemm_gated_ffn_backward")
         return dx, dw_in, dw_down
 
     # -- 4-bit weights ------------------------------------------------------
     def _w4(self, x, codes, scales, zeros, gated, act, out, stream):
-        _floating(x, "x")
-        dt, dev = x.dtype, self.device
+        dt, dev, (T, K) = _operand(x, "x")
+        self._same_device(dev, "x")
         a = _act(act)
-        ldx = _matrix(x, "x", dt, dev)
-        T, K = x.shape
-        _matrix(codes, "codes", torch.uint8, dev, contiguous=True)
-        rows = codes.shape[0]
-        if codes.shape[1] * 2 != K:
-            raise ValueError(f"codes must be [N, {K // 2}] for x of {K} columns, got {list(codes.shape)}")
-        _matrix(scales, "scales", dt, dev, contiguous=True)
-        groups = scales.shape[1]
-        if scales.shape[0] != rows or (groups == 0) != (K == 0) or (K and K % groups):
+        ldx = _matrix(x, "x", dt, dev, (T, K))
+        shape = codes.shape
+        if len(shape) != 2 or shape[1] * 2 != K:
+            raise ValueError(f"codes must be [N, {K // 2}] for x of {K} columns, got {list(shape)}")
+        rows = shape[0]
+        _matrix(codes, "codes", torch.uint8, dev, shape, contiguous=True)
+        groups = _columns(scales, "scales", rows)
+        if (groups == 0) != (K == 0) or (K and K % groups):
             raise ValueError(f"scales must be [{rows}, K / group], got {list(scales.shape)}")
+        _matrix(scales, "scales", dt, dev, (rows, groups), contiguous=True)
         if zeros is not None:
             _matrix(zeros, "zeros", torch.uint8, dev, (rows, groups), contiguous=True)
         if gated and rows % 2:
             raise ValueError("gated weights have an even number of rows: gate rows, then up rows")
         N = rows // 2 if gated else rows
         if out is None:
-            out = torch.empty((T, N), dtype=dt, device=dev)
-        ldy = _matrix(out, "out", dt, dev, (T, N))
-        need = self._lib.gemm_w4_workspace(self._h, T, N, K, gated)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        args = (self._h, x.data_ptr(), ldx, codes.data_ptr(), scales.data_ptr(),
-                zeros.data_ptr() if zeros is not None else None, out.data_ptr(), ldy,
-                ws.data_ptr() if need else None, need, T, N, K, K // groups if groups else 32)
-        if gated:
-            _check(self._lib.gemm_w4_gated(*args, a, _DTYPE[dt], _stream(stream, dev)), "gemm_w4_gated")
+            out = torch.empty((T, N), dtype=dt, device=self.device)
+            ldy = N
         else:
-            _check(self._lib.gemm_w4_linear(*args, _DTYPE[dt], _stream(stream, dev)), "gemm_w4_linear")
+            ldy = _matrix(out, "out", dt, dev, (T, N))
+        ws, wp, need = self._workspace("gemm_w4_workspace", T, N, K, gated)
+        zp = zeros.data_ptr() if zeros is not None else None
+        group = K // groups if groups else 32
+        if gated:
+            st = self._lib.gemm_w4_gated(
+                self._h, x.data_ptr(), ldx, codes.data_ptr(), scales.data_ptr(), zp, out.data_ptr(), ldy, wp,
+                need, T, N, K, group, a, _DTYPE[dt], _stream(stream, dev))
+        else:
+            st = self._lib.gemm_w4_linear(
+                self._h, x.data_ptr(), ldx, codes.data_ptr(), scales.data_ptr(), zp, out.data_ptr(), ldy, wp,
+                need, T, N, K, group, _DTYPE[dt], _stream(stream, dev))
+        if st:
+            _check(st, "gemm_w4_gated" if gated else "gemm_w4_linear")
         return out
 
     def w4_linear(self, x, codes, scales, zeros=None, out=None, stream=None):
@@ -262,12 +310,11 @@ class Ops:
             if N > 1 and inner != 1 or M > 1 and ld < N:
                 raise ValueError(f"{name}'s rows must be contiguous")
             lds += [ld if M > 1 else N, bs if B > 1 else 0]
-        need = self._lib.gemm_orthogonalize_workspace(self._h, B, M, N)
-        ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        ws, wp, need = self._workspace("gemm_orthogonalize_workspace", B, M, N)
         _check(self._lib.gemm_orthogonalize(
-            self._h, m.data_ptr(), lds[0], lds[1], out.data_ptr(), lds[2], lds[3], ws.data_ptr(), need, B,
-            M, N, int(steps), (ctypes.c_float * 3)(*coeffs), float(eps), _DTYPE[m.dtype], _DTYPE[dtype],
-            _stream(stream, self.device)), "gemm_orthogonalize")
+            self._h, m.data_ptr(), lds[0], lds[1], out.data_ptr(), lds[2], lds[3], wp, need, B, M, N,
+            int(steps), (ctypes.c_float * 3)(*coeffs), float(eps), _DTYPE[m.dtype], _DTYPE[dtype],
+            _stream(stream, self.index)), "gemm_orthogonalize")
         return out
 
 
@@ -292,9 +339,10 @@ def default_ops(device=None) -> Ops:
 def _of(t, ops) -> Ops:
     if ops is not None:
         return ops
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    return default_ops(t.device.index)
+    return _ops.get(index) or default_ops(index)
 
 
 def gated_ffn(x, w_in, w_down, act="silu", save=False, out=None, stream=None, ops: Ops | None = None):
