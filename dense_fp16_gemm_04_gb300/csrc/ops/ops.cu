@@ -227,7 +227,7 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
   const int64_t small = tiles(cdiv(p.M, 128), cdiv(p.N, Lone<kEpi>::kOutN));
   const int64_t kb = cdiv(p.K, 64) * p.segs;
   constexpr bool kBatched = kEpi == kEpiSplit || kEpi == kEpiSplitSym;
-  const int64_t most[3] = {kBatched ? 36 : h->max_split[1], kBatched ? 16 : h->max_split[2],
+  const int64_t most[3] = {kBatched ? 0 : h->max_split[1], kBatched ? 16 : h->max_split[2],
                            kBatched ? 2 : h->max_split[3]};
   if (small <= std::min<int64_t>(most[2], h->max_split[3]) && kb >= 16)
     return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream);
@@ -272,9 +272,9 @@ StreamPlan stream_plan(const gemm_ops_s* h, int64_t T, int64_t N, int64_t K) {
   p.warps = blocks >= 16 ? 16 : blocks >= 8 ? 8 : 4;
   p.ring = kStreamMaxRing;
   p.slices = std::max<int64_t>(1, std::min(h->num_sms / tiles, blocks / (2 * p.warps)));
-  auto smem = [&] {  // the warps' sums, their blocks in flight, x and its sums
+  auto smem = [&] {  // the warps' sums, their blocks in flight, and x
     return static_cast<size_t>(p.warps) * (2 * nt * 128 * sizeof(float) + p.ring * stream_slot_bytes(kW)) +
-           static_cast<size_t>(cdiv(blocks, p.slices)) * (bk * held * 2 + (kW != kW16 ? 8 * nt * sizeof(float) : 0));
+           static_cast<size_t>(cdiv(blocks, p.slices)) * bk * held * 2 + 128;
   };
   while (p.ring > 2 && smem() > kStreamSmem) --p.ring;
   while (p.slices < blocks && smem() > kStreamSmem) ++p.slices;

@@ -57,6 +57,22 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B, from zero.
+template <bool kBf16>
+__device__ __forceinline__ void mma_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (kBf16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // 16 bytes another kernel of the stream wrote, read after griddepcontrol.wait.
 __device__ __forceinline__ uint4 ld_global_v4_u32(const void* p) {
   uint4 v;
@@ -88,16 +104,6 @@ __device__ __forceinline__ uint4 ld_shared_v4_u32(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
-}
-
-// The same where `on`; else v keeps its value.
-__device__ __forceinline__ void ld_shared_v4_if(uint32_t on, uint32_t addr, uint4& v) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "@p ld.shared.v4.u32 {%0, %1, %2, %3}, [%5];\n\t}"
-      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-      : "r"(on), "r"(addr)
-      : "memory");
 }
 
 // (w & mask) | bits.

@@ -17,11 +17,11 @@
 //
 //   sum over a group of (q - z) x = sum (O + q) x - (O + z) sum x,
 //
-// a group's sum starts at -(O + z) sum x (fp32, from the staged x) instead of
-// 0 and nothing is subtracted from the codes.  Products of 16-bit x and O + q
-// are exact; the offset makes the fp32 sum's roundings at most 16 to 30 times
-// those of q x alone, 2^-20 of the group's size, far below the 16-bit result's
-// own rounding.  The scale multiplies the finished fp32 sum.
+// nothing is subtracted from the codes; the group's sum of x comes from one
+// product more, of a matrix of ones with the same x.  Products of 16-bit x and
+// O + q are exact; the offset makes the fp32 sum's roundings at most 16 to 30
+// times those of q x alone, 2^-20 of the group's size, far below the 16-bit
+// result's own rounding.  The scale multiplies the finished fp32 sum.
 //
 // A lane's 16 bytes are 32 codes of one row, so the four lanes of a row hold
 // 128 k: one group, two, or four.  Smaller groups are kept apart by columns:
@@ -126,7 +126,6 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   constexpr int kGroups = stream_groups(kW);
   constexpr int kTok = stream_tokens(kW);  // tokens per 8-column tile
   constexpr int kRed = kMT * kNT * 128;    // floats one warp leaves per tile
-  constexpr float kOffset = kBf16 ? 128.0f : 64.0f;
   extern __shared__ __align__(16) uint8_t stream_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5;
@@ -139,11 +138,10 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   const int32_t b1 = static_cast<int32_t>(static_cast<int64_t>(blockIdx.y + 1) * blocks / gridDim.y);
   const int32_t k_begin = b0 * kBK;
   float* red = reinterpret_cast<float*>(stream_smem);  // [warp][kMT][kNT][row][column]
-  float* sums = red + warps * kRed;                    // 4 bits: [block][8 kNT columns]
   // [warp][slot]: [row of the lane][lane][16 B], then the scales and the zero
   // points [row][g][two words].
-  uint8_t* wr = reinterpret_cast<uint8_t*>(sums + (kW4 ? (b1 - b0) * 8 * kNT : 0));
-  uint8_t* xs = wr + warps * a.ring * kSlot;  // [block][i][token][t][16 B]
+  uint8_t* wr = reinterpret_cast<uint8_t*>(red + warps * kRed);
+  uint8_t* xs = wr + warps * a.ring * kSlot;  // 128 bytes of zeros, then [block][i][token][t][16 B]
   const int32_t per_tile = (b1 - b0 + warps - 1) / warps;  // blocks of a tile per warp
   const int32_t tiles = (a.N + kTileN - 1) / kTileN;
   const int32_t my_tiles = (tiles - static_cast<int32_t>(blockIdx.x) + static_cast<int32_t>(gridDim.x) - 1) /
@@ -178,6 +176,14 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   const uint16_t* s_base[2] = {a.scales, a.scales + a.up_s};
   const uint8_t* z_base[2] = {a.zeros, a.zeros + a.up_s};
   constexpr int kHalf = kGlu ? 1 : 0;  // whether rows 2, 3 have the other base
+  // The low bits of those addresses: where in its word a scale or zero lies.
+  const uint32_t s_low[2] = {static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s_base[0])),
+                             static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s_base[1]))};
+  const uint32_t z_low[2] = {static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z_base[0])),
+                             static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z_base[1]))};
+  uint32_t sum_off[kOwn];  // s_off of the tile being summed
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) sum_off[i] = s_off[i];
   // This lane's two columns belong to groups j, j + 1 of a row (or to one
   // group).  Their scales share an aligned word, and so do their zero points,
   // unless rows hold an odd number of small groups or start off such a word:
@@ -232,65 +238,50 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   // (4 bits: chunk 4 t + i of a block is word i of lane t), four loads in
   // flight a thread; zeros past K.
   {
-    constexpr int kPer = kBK / 8;              // chunks per block
-    constexpr int kLanes = kPer / kGroups;     // neighbouring chunks of one group
-    const int32_t chunks = (b1 - b0) * kPer, total = chunks * tokens;
-    if constexpr (kW4)  // columns of tokens past T
-      for (int32_t i = threadIdx.x; i < (b1 - b0) * 8 * kNT; i += blockDim.x)
-        if ((i & (8 * kNT - 1)) >= tokens * kGroups) sums[i] = 0.0f;
-    for (int32_t i0 = threadIdx.x; i0 - lane < total; i0 += 4 * blockDim.x) {
+    constexpr int kPer = kBK / 8;  // chunks per block
+    const int32_t chunks = (b1 - b0) * kPer;
+    if (threadIdx.x < 8) *reinterpret_cast<uint4*>(xs + 16 * threadIdx.x) = make_uint4(0, 0, 0, 0);
+    int32_t next_tok = 0, next_c = threadIdx.x;  // chunk next_c of token next_tok
+    while (next_tok < tokens) {
       uint4 v[4];
       int32_t tok[4], c[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int32_t i = i0 + u * blockDim.x;
-        tok[u] = i / chunks;
-        c[u] = i - tok[u] * chunks;
+        while (next_c >= chunks) {
+          next_c -= chunks;
+          ++next_tok;
+        }
+        tok[u] = next_tok;
+        c[u] = next_c;
+        next_c += blockDim.x;
         v[u] = make_uint4(0, 0, 0, 0);
-        if (i < total && k_begin + 8 * c[u] < a.K)
+        if (tok[u] < tokens && k_begin + 8 * c[u] < a.K)
           v[u] = ptx::ld_global_v4_u32(a.x + (t0 + tok[u]) * a.ldx + k_begin + 8 * c[u]);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const bool in = i0 + u * static_cast<int32_t>(blockDim.x) < total;
+        if (tok[u] >= tokens) break;
         const int32_t blk = c[u] / kPer, ch = c[u] & (kPer - 1);
         uint4 o = v[u];
-        int i = ch >> 2, l = ch & 3;
-        if constexpr (kW4) {
-          // Pairs (x j, x j + 4), as the codes unpack.
+        if constexpr (kW4)  // pairs (x j, x j + 4), as the codes unpack
           o = make_uint4(__byte_perm(v[u].x, v[u].z, 0x5410), __byte_perm(v[u].x, v[u].z, 0x7632),
                          __byte_perm(v[u].y, v[u].w, 0x5410), __byte_perm(v[u].y, v[u].w, 0x7632));
-          const float2 f0 = unpack16(kBf16, v[u].x), f1 = unpack16(kBf16, v[u].y);
-          const float2 f2 = unpack16(kBf16, v[u].z), f3 = unpack16(kBf16, v[u].w);
-          float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
-#pragma unroll
-          for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-          if (in && (ch & (kLanes - 1)) == 0) sums[blk * (8 * kNT) + tok[u] * kGroups + ch / kLanes] = sum;
-          i = ch & 3, l = ch >> 2;
-        }
-        if (in)
-          *reinterpret_cast<uint4*>(xs + (((blk * (kPer / 4) + i) * tokens + tok[u]) * 4 + l) * 16) = o;
+        const int i = kW4 ? ch & 3 : 0, l = kW4 ? ch >> 2 : ch;
+        *reinterpret_cast<uint4*>(xs + 128 + (((blk * (kPer / 4) + i) * tokens + tok[u]) * 4 + l) * 16) = o;
       }
     }
   }
   __syncthreads();
   // Column g of tile n is token n kTok + g / kGroups, group g % kGroups; lane
   // t's k lie in group t kGroups / 4 of the block.
-  uint32_t xl[kNT];
-  uint32_t mine[kNT];
+  uint32_t xl[kNT], x_step[kNT];  // bytes from i to i + 1; the other lanes stay at the zeros
 #pragma unroll
   for (int n = 0; n < kNT; ++n) {
     const int32_t tok = n * kTok + g / kGroups;
-    mine[n] = tok < tokens && t * kGroups / 4 == g % kGroups;
-    xl[n] = ptx::smem_addr(xs) + tok * 64 + t * 16;
+    const bool mine = tok < tokens && t * kGroups / 4 == g % kGroups;
+    xl[n] = ptx::smem_addr(xs) + (mine ? 128 + tok * 64 + t * 16 : lane % 8 * 16);
+    x_step[n] = mine ? tokens * 64 : 0;
   }
-  const uint32_t x_step = tokens * 64;  // bytes from i to i + 1
-  // Zero for good in the lanes whose column lacks their k: they never load.
-  uint4 xb[2][kNT];
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int n = 0; n < kNT; ++n) xb[j][n] = make_uint4(0, 0, 0, 0);
 
   float acc[kMT][kNT][4];
 #pragma unroll
@@ -303,7 +294,9 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   auto consume = [&](uint32_t slot, int32_t rel) {  // block b0 + rel
     if (rel >= b1 - b0) return;
     constexpr int kWords = kBK / 32;
-    const uint32_t x_at = rel * kWords * x_step;
+    uint32_t xa[kNT];
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) xa[n] = xl[n] + rel * kWords * x_step[n];
     uint4 wv[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) wv[i] = ptx::ld_shared_v4_u32(slot + i * 512 + lane * 16);
@@ -316,54 +309,59 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
           sv[i] = ptx::ld_shared_u32(slot + s_lane + i * 64);
-          if (kGroups == 1)
-            sv[i] >>= 8 * (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
-                               s_base[kHalf * (i >> 1)] + (row_of(tile, i & (kOwn - 1)) * groups + j))) & 2);
+          // A lone scale is the word's low or high half.
+          if (kGroups == 1) sv[i] >>= ((s_low[kHalf * (i >> 1)] + 2 * (sum_off[i & (kOwn - 1)] + j)) & 2) * 8;
         }
         if (a.zeros) {
 #pragma unroll
           for (int i = 0; i < kRows; ++i)
             zv[i] = ptx::ld_shared_u32(slot + s_lane + (kRows + i) * 64) >>
-                    (8 * (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
-                              z_base[kHalf * (i >> 1)] + (row_of(tile, i & (kOwn - 1)) * groups + j))) & 3));
+                    ((z_low[kHalf * (i >> 1)] + sum_off[i & (kOwn - 1)] + j) & 3) * 8;
         }
       } else {
         const uint32_t j0 = min(((b0 + rel) * kBK >> a.group_shift) + (2u * t & (kGroups - 1)), groups - 1);
         const uint32_t j1 = min(j0 + 1, groups - 1);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-          const uint32_t o = row_of(tile, i & (kOwn - 1)) * groups;
+          const uint32_t o = sum_off[i & (kOwn - 1)];
           const uint16_t* sp = s_base[kHalf * (i >> 1)] + o;
           const uint8_t* zp = z_base[kHalf * (i >> 1)] + o;
           sv[i] = sp[j0] | static_cast<uint32_t>(sp[j1]) << 16;
           if (a.zeros) zv[i] = zp[j0] | static_cast<uint32_t>(zp[j1]) << 8;
         }
       }
+      // -(O + z) is z's bits in the mantissa of -O.
       float z0[kRows], z1[kRows];
+      constexpr uint32_t kMinusO = kBf16 ? 0xc3000000u : 0xc2800000u;
+      constexpr int kBit = kBf16 ? 16 : 17;
       if (a.zeros) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-          z0[i] = -kOffset - static_cast<float>(zv[i] & 15u);
-          z1[i] = kGroups > 1 ? -kOffset - static_cast<float>((zv[i] >> 8) & 15u) : z0[i];
+          z0[i] = __uint_as_float(ptx::and_or(zv[i] << kBit, 15u << kBit, kMinusO));
+          z1[i] = kGroups > 1 ? __uint_as_float(ptx::and_or(zv[i] << (kBit - 8), 15u << kBit, kMinusO)) : z0[i];
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) z0[i] = z1[i] = -kOffset - 8.0f;
+        for (int i = 0; i < kRows; ++i) z0[i] = z1[i] = __uint_as_float(kMinusO | 8u << kBit);
       }
-      float part[kMT][kNT][4];
-#pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        const float2 s = *reinterpret_cast<const float2*>(sums + (rel * kNT + n) * 8 + 2 * t);
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          part[i >> 1][n][2 * (i & 1)] = z0[i] * s.x;
-          part[i >> 1][n][2 * (i & 1) + 1] = z1[i] * s.y;
-        }
-      }
+      float part[kMT][kNT][4], sx[kNT][4];  // sums of (O + q) x, and of x (in every row)
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
+        uint4 xb[kNT];
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) ptx::ld_shared_v4_if(mine[n], xl[n] + x_at + i * x_step, xb[i & 1][n]);
+        for (int n = 0; n < kNT; ++n) {
+          xb[n] = ptx::ld_shared_v4_u32(xa[n]);
+          xa[n] += x_step[n];
+        }
+        constexpr uint32_t kOnes = kBf16 ? 0x3f803f80u : 0x3c003c00u;
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+          if (i == 0)
+            ptx::mma_16816_zero<kBf16>(sx[n], kOnes, kOnes, kOnes, kOnes, xb[n].x, xb[n].y);
+          else
+            ptx::mma_16816<kBf16>(sx[n], kOnes, kOnes, kOnes, kOnes, xb[n].x, xb[n].y);
+          ptx::mma_16816<kBf16>(sx[n], kOnes, kOnes, kOnes, kOnes, xb[n].z, xb[n].w);
+        }
 #pragma unroll
         for (int m = 0; m < kMT; ++m) {
           uint32_t p0[4], p1[4];
@@ -372,8 +370,11 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
           offset_codes<kBf16>(i == 0 ? w1.x : i == 1 ? w1.y : i == 2 ? w1.z : w1.w, p1);
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
-            ptx::mma_16816<kBf16>(part[m][n], p0[0], p1[0], p0[1], p1[1], xb[i & 1][n].x, xb[i & 1][n].y);
-            ptx::mma_16816<kBf16>(part[m][n], p0[2], p1[2], p0[3], p1[3], xb[i & 1][n].z, xb[i & 1][n].w);
+            if (i == 0)
+              ptx::mma_16816_zero<kBf16>(part[m][n], p0[0], p1[0], p0[1], p1[1], xb[n].x, xb[n].y);
+            else
+              ptx::mma_16816<kBf16>(part[m][n], p0[0], p1[0], p0[1], p1[1], xb[n].x, xb[n].y);
+            ptx::mma_16816<kBf16>(part[m][n], p0[2], p1[2], p0[3], p1[3], xb[n].z, xb[n].w);
           }
         }
       }
@@ -385,15 +386,14 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
         for (int n = 0; n < kNT; ++n) {
           float* c = acc[i >> 1][n] + 2 * (i & 1);
           const float* p = part[i >> 1][n] + 2 * (i & 1);
-          c[0] = fmaf(f.x, p[0], c[0]);
-          c[1] = fmaf(f1, p[1], c[1]);
+          c[0] = fmaf(f.x, fmaf(z0[i], sx[n][0], p[0]), c[0]);
+          c[1] = fmaf(f1, fmaf(z1[i], sx[n][1], p[1]), c[1]);
         }
       }
     } else {
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        ptx::ld_shared_v4_if(mine[n], xl[n] + x_at, xb[0][n]);
-        const uint4 x = xb[0][n];
+        const uint4 x = ptx::ld_shared_v4_u32(xa[n]);
 #pragma unroll
         for (int m = 0; m < kMT; ++m) {
           const uint4 p = wv[2 * m], q = wv[2 * m + 1];
@@ -453,6 +453,8 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
       a.y[static_cast<int64_t>(tk) * a.ldy + n] = round16(kBf16, out);
     }
     tile += gridDim.x;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) sum_off[i] = row_of(tile, i) * groups;
   };
   uint32_t slot = slot0;
 #pragma unroll 1
