@@ -29,7 +29,9 @@
 // the others their columns of its partial sums through distributed shared
 // memory, and after one cluster barrier adds the kSplit partials of its own in
 // rank order (the result does not depend on timing) and runs the epilogue on
-// them.
+// them.  In a batch whose tiles fill the device as they are, lone CTAs keep the
+// same k-ranges in kParts accumulators side by side and add them in the same
+// order: a matrix gets the same sums whatever the batch.
 //
 // Units (a CTA with a 128-row tile, or a pair of CTAs with a 256-row one) are
 // persistent and take tiles round robin.  Inside a CTA: warp 0 loads A and
@@ -80,8 +82,9 @@ struct FusedArgs {
   int32_t skip_kb;            // fault injection, -1 = off
 };
 
-template <int kCtas_, int kBN_, int kStages_, int kEpi_, int kEpiBufs_, int kSplit_ = 1>
+template <int kCtas_, int kBN_, int kStages_, int kEpi_, int kEpiBufs_, int kSplit_ = 1, int kParts_ = 1>
 struct FusedCfg {
+  static constexpr int kParts = kParts_;  // accumulators of a tile, one per k-range
   static constexpr int kSplit = kSplit_;  // CTAs sharing a tile, each a k-range
   static constexpr int kCluster = kCtas_ * kSplit_;
   static constexpr int kCtas = kCtas_;
@@ -107,13 +110,15 @@ struct FusedCfg {
   static constexpr int kOffSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffAbort = kOffSlot + 4;
   static constexpr int kSmemBytes = kOffAbort + 4 + 1024;  // + slack to align the base
-  static constexpr int kTmemCols = 2 * kBN;
+  static constexpr int kAccBufs = kParts > 1 ? 1 : 2;  // tiles in tensor memory
+  static constexpr int kTmemCols = kAccBufs * kParts * kBN;
   static constexpr int kThreads = 256;
   static constexpr uint32_t kIdesc = ptx::idesc_f16(kTileM, kBN, true);
   static_assert(kSmemBytes <= 232448, "exceeds 227 KB of shared memory per CTA");
   static_assert(kOutN % 64 == 0, "the epilogue works on 64-column chunks");
   static_assert(!kSym || kTileM == kBN, "symmetric tiles are square");
   static_assert(kTmemCols <= 512, "TMEM columns");
+  static_assert(kParts == 1 || (kSplit == 1 && (kEpi == kEpiSplit || kEpi == kEpiSplitSym)), "parts");
   // The partials a split CTA receives, its own among them: 128 rows x 128
   // columns in all, in the staging buffers' place.
   static_assert(kSplit == 1 || (kCtas == 1 && kBN == 128 && kEpiWarps * kEpiBufs * kBufBytes >= kBM * kBN * 4),
@@ -198,15 +203,32 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
       }
     }
   }
-  ptx::cluster_sync();
-  if (!ok) return;
-  // Add and finish: thread (row, half) takes half of the CTA's columns.
+  // Thread (row, half) finishes half of the CTA's columns.  What the epilogue
+  // reads comes in while the partials do.
   constexpr int kN = Cfg::kGlu ? kHalfCols / 2 : kCols / 2;
+  constexpr bool kReads = Cfg::kEpi == kEpiGluBwd || Cfg::kEpi == kEpiSplit || Cfg::kEpi == kEpiSplitSym;
   const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
   const FusedItem wi = fused_item<Cfg>(args, unit, rank);
   const int32_t row = wi.mb * Cfg::kBM + r;
   const int32_t col0 = wi.nb * Cfg::kOutN + rank * (Cfg::kOutN / kS) + half * kN;
-  if (row >= args.M || col0 >= args.N) return;
+  const bool in = row < args.M && col0 < args.N;
+  uint4 s0[kReads ? kN / 8 : 1], s1[kReads ? kN / 8 : 1];
+  if constexpr (kReads) {
+    const bool gated = Cfg::kEpi == kEpiGluBwd;
+    const int64_t second = gated ? args.N : args.src_part;
+    const uint16_t* src = args.src + (gated ? 0 : static_cast<int64_t>(wi.batch) * 2 * args.src_part) +
+                          static_cast<int64_t>(row) * args.src_ld + col0;
+    if (in && (gated || args.beta != 0.0f)) {
+#pragma unroll
+      for (int i = 0; i < kN / 8; ++i)
+        if (col0 + 8 * i < args.N) {
+          s0[i] = ptx::ld_global_v4_u32(src + 8 * i);
+          s1[i] = ptx::ld_global_v4_u32(src + second + 8 * i);
+        }
+    }
+  }
+  ptx::cluster_sync();
+  if (!ok || !in) return;
   auto sum = [&](int first4, float (&v)[kN]) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) v[i] = 0.0f;
@@ -259,13 +281,12 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
       }
     }
   } else if constexpr (Cfg::kEpi == kEpiGluBwd) {
-    const uint16_t* gu = args.src + static_cast<int64_t>(row) * args.src_ld + col0;
     uint16_t* c = args.c + static_cast<int64_t>(row) * args.ldc + col0;
     uint16_t* d = args.d + static_cast<int64_t>(row) * 2 * args.N + col0;
 #pragma unroll
     for (int i = 0; i < kN; i += kG) {
       if (col0 + i >= args.N) break;
-      const uint4 gv = ptx::ld_global_v4_u32(gu + i), uv = ptx::ld_global_v4_u32(gu + args.N + i);
+      const uint4 gv = s0[i / 8], uv = s1[i / 8];
       const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w}, uw[4] = {uv.x, uv.y, uv.z, uv.w};
       uint32_t h[kG / 2], dg[kG / 2], du[kG / 2];
 #pragma unroll
@@ -285,7 +306,6 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
     }
   } else {
     const int64_t batch = static_cast<int64_t>(wi.batch) * 2;
-    const uint16_t* sh = args.src + batch * args.src_part + static_cast<int64_t>(row) * args.src_ld + col0;
     uint16_t* base = args.c + batch * args.c_part;
     uint16_t* c = base + static_cast<int64_t>(row) * args.ldc + col0;
 #pragma unroll
@@ -295,7 +315,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
 #pragma unroll
       for (int j = 0; j < kG; ++j) x[j] = args.alpha * v[i + j];
       if (args.beta != 0.0f) {
-        const uint4 a = ptx::ld_global_v4_u32(sh + i), b = ptx::ld_global_v4_u32(sh + args.src_part + i);
+        const uint4 a = s0[i / 8], b = s1[i / 8];
         const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int j = 0; j < kG / 2; ++j) {
@@ -494,15 +514,21 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       bool ok = true;
       for (int32_t it = unit; ok && it < args.items; it += units) {
         const FusedItem wi = fused_item<Cfg>(args, it, rank);
-        const int buf = acc_iter & 1;
-        const uint32_t use_par = static_cast<uint32_t>((acc_iter >> 1) & 1);
+        const int buf = acc_iter % Cfg::kAccBufs;
+        const uint32_t use_par = static_cast<uint32_t>((acc_iter / Cfg::kAccBufs) & 1);
         if (!wait_bar_warp<kPair>(bar_tempty(buf), use_par ^ 1u, w, kSiteTmemEmpty, it)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * Cfg::kBN);
+        uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * Cfg::kBN);
+        int32_t first = wi.kb0, part = 0;  // first k-block of the current accumulator
         for (int32_t kb = wi.kb0; kb < wi.kb1; ++kb) {
+          if (Cfg::kParts > 1 && kb == (part + 1) * wi.kb1 / Cfg::kParts) {
+            ++part;
+            first = kb;
+            d_tmem += Cfg::kBN;
+          }
           if (!wait_bar_warp<kPair>(bar_full(stage), phase, w, kSiteFull, it)) {
             ok = false;
             break;
@@ -510,7 +536,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           ptx::tc_fence_after();
           const uint64_t a_desc = a_desc0 + kADescStage * static_cast<uint32_t>(stage);
           const uint64_t b_desc = b_desc0 + kBDescStage * static_cast<uint32_t>(stage);
-          const uint32_t acc_first = kb != wi.kb0 ? 1u : 0u;
+          const uint32_t acc_first = kb != first ? 1u : 0u;
           if (ptx::elect_one()) {
 #pragma unroll
             for (int k = 0; k < Cfg::kBK / 16; ++k)
@@ -607,8 +633,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       // Every warp takes the same decision, so none is left at a barrier.
       if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, it < args.items)) break;
       const FusedItem wi = fused_item<Cfg>(args, it, rank);
-      const int buf = acc_iter & 1;
-      const uint32_t use_par = static_cast<uint32_t>((acc_iter >> 1) & 1);
+      const int buf = acc_iter % Cfg::kAccBufs;
+      const uint32_t use_par = static_cast<uint32_t>((acc_iter / Cfg::kAccBufs) & 1);
       ++acc_iter;
       int ok = 1;
       if (lane == 0) ok = wait_bar<kPair>(bar_tfull(buf), use_par, w, kSiteTmemFull, it) ? 1 : 0;
@@ -719,6 +745,20 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           for (int half = 0; half < 2; ++half) {
             uint32_t v[32], a[16], b[16];
             ptx::tmem_ld_32x32b_x32(t_row + c * 64 + half * 32, v);
+            if constexpr (Cfg::kParts > 1) {  // from zero, in order, as a cluster adds
+              ptx::tmem_wait_ld(v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(0.0f + __uint_as_float(v[i]));
+#pragma unroll 1
+              for (int q = 1; q < Cfg::kParts; ++q) {
+                uint32_t u[32];
+                ptx::tmem_ld_32x32b_x32(t_row + q * Cfg::kBN + c * 64 + half * 32, u);
+                ptx::tmem_wait_ld(u);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(u[i]));
+              }
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               // Rows of S are padded to a multiple of 8 columns.

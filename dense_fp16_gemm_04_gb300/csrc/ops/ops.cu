@@ -44,8 +44,8 @@ constexpr int kGroupM = 8;
 // 128 x 128 for problems of few tiles.
 template <int kEpi>
 using Pair = FusedCfg<2, 256, kEpi == kEpiStore ? 6 : 5, kEpi, kEpi == kEpiStore ? 2 : 4>;
-template <int kEpi, int kSplit = 1>
-using Lone = FusedCfg<1, 128, 5, kEpi, 4, kSplit>;
+template <int kEpi, int kSplit = 1, int kParts = 1>
+using Lone = FusedCfg<1, 128, 5, kEpi, 4, kSplit, kParts>;
 
 struct DeviceGuard {
   int prev = -1;
@@ -216,25 +216,29 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
 // Which form: split clusters where the 128 x 128 tiles are few (each CTA with
 // two k-blocks at least); pairs when the 256-row tiles fill at least half of
 // the device; else lone CTAs.  Of clusters of eight CTAs 15 fit at once, of
-// four 36, of two 76.  The batched products (high and low parts) go by one
-// matrix's tiles alone, so that a matrix of a batch gets the same sums as by
-// itself, and split less, since the others of the batch fill the device too
-// (6 x 1000 x 344: 395 us for the update with the limits of single products).
+// four 36, of two 76.
 template <int kEpi>
 gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const Stack& c,
                     const Stack& d, cudaStream_t stream) {
+  constexpr bool kBatched = kEpi == kEpiSplit || kEpi == kEpiSplitSym;
   auto tiles = [&](int64_t tm, int64_t tn) { return Pair<kEpi>::kSym ? tn * (tn + 1) / 2 : tm * tn; };
   const int64_t small = tiles(cdiv(p.M, 128), cdiv(p.N, Lone<kEpi>::kOutN));
   const int64_t kb = cdiv(p.K, 64) * p.segs;
-  constexpr bool kBatched = kEpi == kEpiSplit || kEpi == kEpiSplitSym;
-  const int64_t most[3] = {kBatched ? 0 : h->max_split[1], kBatched ? 16 : h->max_split[2],
-                           kBatched ? 2 : h->max_split[3]};
-  if (small <= std::min<int64_t>(most[2], h->max_split[3]) && kb >= 16)
-    return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream);
-  if (small <= std::min<int64_t>(most[1], h->max_split[2]) && kb >= 8)
-    return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream);
-  if (small <= std::min<int64_t>(most[0], h->max_split[1]) && kb >= 4)
-    return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream);
+  const int* most = h->max_split;
+  if constexpr (kBatched) {
+    // The number of k-ranges goes by one matrix's tiles, so that a matrix of a
+    // batch gets the same sums as by itself; who sums them by the batch's.
+    if (small <= most[2] && kb >= 8)
+      return small * p.batch <= most[2] ? launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream)
+                                        : launch_fused<Lone<kEpi, 1, 4>>(h, p, a, c, d, stream);
+    if (small <= most[1] && kb >= 4)
+      return small * p.batch <= most[1] ? launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream)
+                                        : launch_fused<Lone<kEpi, 1, 2>>(h, p, a, c, d, stream);
+  } else {
+    if (small <= std::min(8, most[3]) && kb >= 16) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream);
+    if (small <= most[2] && kb >= 8) return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream);
+    if (small <= most[1] && kb >= 4) return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream);
+  }
   const int64_t big = tiles(cdiv(p.M, 256), cdiv(p.N, Pair<kEpi>::kOutN));
   return h->max_pairs > 0 && 2 * big >= h->max_pairs ? launch_fused<Pair<kEpi>>(h, p, a, c, d, stream)
                                                      : launch_fused<Lone<kEpi>>(h, p, a, c, d, stream);
@@ -366,9 +370,13 @@ bool set_attr() {
 
 template <int kSplit>
 bool set_split_attr() {
+  if constexpr (kSplit < 8) {
+    if (!set_attr<Lone<kEpiSplit, kSplit>>() || !set_attr<Lone<kEpiSplitSym, kSplit>>() ||
+        !set_attr<Lone<kEpiSplit, 1, kSplit>>() || !set_attr<Lone<kEpiSplitSym, 1, kSplit>>())
+      return false;
+  }
   return set_attr<Lone<kEpiStore, kSplit>>() && set_attr<Lone<kEpiGlu, kSplit>>() &&
-         set_attr<Lone<kEpiGluBwd, kSplit>>() && set_attr<Lone<kEpiSplit, kSplit>>() &&
-         set_attr<Lone<kEpiSplitSym, kSplit>>();
+         set_attr<Lone<kEpiGluBwd, kSplit>>();
 }
 
 template <class Cfg>
