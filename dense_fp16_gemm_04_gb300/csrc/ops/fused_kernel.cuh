@@ -64,7 +64,10 @@ struct FusedArgs {
   int32_t items;              // tiles of the whole batch
   int32_t num_kb;             // 64-deep k-blocks of one segment
   int32_t segs;               // segments (1, or 3: high high + high low + low high)
-  int32_t z_mul;              // third coordinate of matrix b of the batch: b z_mul + part
+  // Third coordinate of matrix b of the batch: b a_zb + a_seg[segment] of A's
+  // stack, b b_zb + b_seg[segment] of B's, b c_zb (+ 1: low part) of C's.
+  int32_t a_zb, b_zb, c_zb;
+  int32_t a_seg[3], b_seg[3];
   int32_t group_m;            // raster group height, in tiles
   int32_t a_mn, b_mn;         // operand layouts: 0 K-contiguous, 1 MN-contiguous
   int32_t bf16;               // operands and 16-bit outputs are bf16
@@ -74,9 +77,10 @@ struct FusedArgs {
   int64_t src_ld, src_part;   //   the next matrix of the batch 2 src_part further;
                               // kEpiGluBwd: g and u, [M, 2N]
   // Split clusters store their columns themselves: c the output, or h; d g and
-  // u, or dg and du, [M, 2N]; c_part from C's high to its low part.
+  // u, or dg and du: rows ldd apart, u (du) d_up columns further.
   uint16_t *c, *d;
-  int64_t ldc, c_part;
+  int64_t ldd, d_up;
+  int64_t ldc, c_z;           // c_z: from one matrix of C's stack to the next
   uint32_t* err;
   uint64_t timeout_ns;
   int32_t skip_kb;            // fault injection, -1 = off
@@ -248,7 +252,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
   float v[kN];
   sum(half * (kN / 4), v);
   if constexpr (Cfg::kEpi == kEpiStore) {
-    uint16_t* c = args.c + static_cast<int64_t>(row) * args.ldc + col0;
+    uint16_t* c = args.c + wi.batch * args.c_zb * args.c_z + static_cast<int64_t>(row) * args.ldc + col0;
 #pragma unroll
     for (int i = 0; i < kN; i += kG) {
       uint32_t p[kG / 2];
@@ -261,7 +265,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
     float u[kN];
     sum(kHalfCols / 4 + half * (kN / 4), u);
     uint16_t* c = args.c + static_cast<int64_t>(row) * args.ldc + col0;
-    uint16_t* d = args.d + static_cast<int64_t>(row) * 2 * args.N + col0;
+    uint16_t* d = args.d + static_cast<int64_t>(row) * args.ldd + col0;
 #pragma unroll
     for (int i = 0; i < kN; i += kG) {
       uint32_t h[kG / 2], gp[kG / 2], up[kG / 2];
@@ -276,13 +280,13 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
         store16<kG>(c + i, h);
         if (args.save) {
           store16<kG>(d + i, gp);
-          store16<kG>(d + args.N + i, up);
+          store16<kG>(d + args.d_up + i, up);
         }
       }
     }
   } else if constexpr (Cfg::kEpi == kEpiGluBwd) {
     uint16_t* c = args.c + static_cast<int64_t>(row) * args.ldc + col0;
-    uint16_t* d = args.d + static_cast<int64_t>(row) * 2 * args.N + col0;
+    uint16_t* d = args.d + static_cast<int64_t>(row) * args.ldd + col0;
 #pragma unroll
     for (int i = 0; i < kN; i += kG) {
       if (col0 + i >= args.N) break;
@@ -302,11 +306,10 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
       }
       store16<kG>(c + i, h);
       store16<kG>(d + i, dg);
-      store16<kG>(d + args.N + i, du);
+      store16<kG>(d + args.d_up + i, du);
     }
   } else {
-    const int64_t batch = static_cast<int64_t>(wi.batch) * 2;
-    uint16_t* base = args.c + batch * args.c_part;
+    uint16_t* base = args.c + wi.batch * args.c_zb * args.c_z;
     uint16_t* c = base + static_cast<int64_t>(row) * args.ldc + col0;
 #pragma unroll
     for (int i = 0; i < kN; i += kG) {
@@ -332,7 +335,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
         lo[j] = pack16(false, x[2 * j] - back.x, x[2 * j + 1] - back.y);
       }
       store16<kG>(c + i, hi);
-      store16<kG>(c + args.c_part + i, lo);
+      store16<kG>(c + args.c_z + i, lo);
       if constexpr (Cfg::kSym) {
         // Transposed: a warp's 32 rows are 64 contiguous bytes of each column.
         if (wi.mb != wi.nb) {
@@ -341,7 +344,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
             uint16_t* t = base + static_cast<int64_t>(col0 + i + j) * args.ldc + row;
             if (col0 + i + j < args.N) {
               ptx::st_global_b16(t, static_cast<uint16_t>(hi[j / 2] >> (16 * (j & 1))));
-              ptx::st_global_b16(t + args.c_part, static_cast<uint16_t>(lo[j / 2] >> (16 * (j & 1))));
+              ptx::st_global_b16(t + args.c_z, static_cast<uint16_t>(lo[j / 2] >> (16 * (j & 1))));
             }
           }
         }
@@ -427,7 +430,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     bool ok = true, first_item = true;
     for (int32_t it = unit; ok && it < args.items; it += units) {
       const FusedItem wi = fused_item<Cfg>(args, it, rank);
-      int32_t row, z0 = wi.batch * args.z_mul;
+      int32_t row;
+      const int32_t z0 = wi.batch * (is_a ? args.a_zb : args.b_zb);
       if (is_a)
         row = wi.mb * Cfg::kTileM + static_cast<int32_t>(cta) * Cfg::kBM;
       else if (Cfg::kGlu)
@@ -443,8 +447,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const bool skip = args.skip_kb == kb && first_item && unit == 0 && cta == 0;
         if (!skip && ptx::elect_one()) {
           const uint32_t dst = op_base + static_cast<uint32_t>(stage) * op_bytes;
-          // Segments: high high, high low, low high.
-          const int32_t z = z0 + (is_a ? (seg == 2 ? 1 : 0) : (seg == 1 ? 1 : 0));
+          const int32_t z = z0 + (is_a ? args.a_seg[seg] : args.b_seg[seg]);
           uint32_t full = bar_full(stage);
           if constexpr (kPair) {
             full = ptx::mapa(full, 0);
@@ -676,7 +679,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             packed[16 + i] = pack16(bf16, args.alpha * __uint_as_float(v1[2 * i]),
                                     args.alpha * __uint_as_float(v1[2 * i + 1]));
           }
-          store_chunk(&tmC, packed, col0, row0, wi.batch * args.z_mul, in);
+          store_chunk(&tmC, packed, col0, row0, wi.batch * args.c_zb, in);
         } else if constexpr (Cfg::kEpi == kEpiGlu) {
           uint32_t h[32], gp[32], up[32];
 #pragma unroll
@@ -783,7 +786,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             }
           }
           if (last) release_tmem();
-          const int32_t z = wi.batch * args.z_mul;
+          const int32_t z = wi.batch * args.c_zb;
           store_chunk(&tmC, hi, col0, row0, z, in);
           store_chunk(&tmC, lo, col0, row0, z + 1, in);
           if constexpr (Cfg::kSym) {

@@ -160,7 +160,9 @@ struct Product {
   Stack a, b;
   bool a_mn, b_mn;  // stored [K, M] / [K, N]
   bool bf16;
-  int64_t batch, segs, z_mul;
+  int64_t batch, segs;
+  int32_t a_zb, b_zb, c_zb;   // stack coordinates: FusedArgs
+  int32_t a_seg[3], b_seg[3];
 };
 
 FusedArgs base_args(const gemm_ops_s* h, const Product& p) {
@@ -169,7 +171,13 @@ FusedArgs base_args(const gemm_ops_s* h, const Product& p) {
   a.N = static_cast<int32_t>(p.N);
   a.num_kb = static_cast<int32_t>(cdiv(p.K, 64));
   a.segs = static_cast<int32_t>(p.segs);
-  a.z_mul = static_cast<int32_t>(p.z_mul);
+  a.a_zb = p.a_zb;
+  a.b_zb = p.b_zb;
+  a.c_zb = p.c_zb;
+  for (int i = 0; i < 3; ++i) {
+    a.a_seg[i] = p.a_seg[i];
+    a.b_seg[i] = p.b_seg[i];
+  }
   a.group_m = kGroupM;
   a.a_mn = p.a_mn;
   a.b_mn = p.b_mn;
@@ -205,7 +213,9 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
   a.items = static_cast<int32_t>(items);
   a.c = static_cast<uint16_t*>(const_cast<void*>(c.p));
   a.ldc = c.pitch;
-  a.c_part = c.zstride;
+  a.c_z = c.zstride;
+  a.ldd = d.pitch;
+  a.d_up = d.zstride;
   a.d = static_cast<uint16_t*>(const_cast<void*>(d.p));
   const int64_t fit = Cfg::kCtas == 2 ? h->max_pairs : h->num_sms;
   const int64_t units = Cfg::kSplit > 1 ? items : std::min<int64_t>(items, fit);
@@ -235,18 +245,19 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
       return small * p.batch <= most[1] ? launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream)
                                         : launch_fused<Lone<kEpi, 1, 2>>(h, p, a, c, d, stream);
   } else {
-    if (small <= std::min(8, most[3]) && kb >= 16) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream);
-    if (small <= most[2] && kb >= 8) return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream);
-    if (small <= most[1] && kb >= 4) return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream);
+    const int64_t all = small * p.batch;
+    if (all <= std::min(8, most[3]) && kb >= 16) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream);
+    if (all <= most[2] && kb >= 8) return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream);
+    if (all <= most[1] && kb >= 4) return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream);
   }
-  const int64_t big = tiles(cdiv(p.M, 256), cdiv(p.N, Pair<kEpi>::kOutN));
+  const int64_t big = tiles(cdiv(p.M, 256), cdiv(p.N, Pair<kEpi>::kOutN)) * (kBatched ? 1 : p.batch);
   return h->max_pairs > 0 && 2 * big >= h->max_pairs ? launch_fused<Pair<kEpi>>(h, p, a, c, d, stream)
                                                      : launch_fused<Lone<kEpi>>(h, p, a, c, d, stream);
 }
 
 // out = A B^T, rounded to 16 bits.
-gemm_status_t product(gemm_ops_s* h, const Product& p, void* out, int64_t ldo, cudaStream_t stream) {
-  return fused<kEpiStore>(h, p, base_args(h, p), {out, p.M, p.N, ldo, 1, p.M * ldo}, {}, stream);
+gemm_status_t product(gemm_ops_s* h, const Product& p, const Stack& out, cudaStream_t stream) {
+  return fused<kEpiStore>(h, p, base_args(h, p), out, {}, stream);
 }
 
 // How a product of few tokens is laid out: warps per CTA, CTAs per k-slice,
@@ -415,8 +426,12 @@ gemm_status_t check_ld(int64_t ld, int64_t cols) {
   return ld % 8 != 0 ? GEMM_ERR_ALIGNMENT : GEMM_OK;
 }
 
-// The backward pass's workspace: dg and du, then h.
-size_t bwd_h_offset(int64_t T, int64_t F) { return up(T * 2 * F * 2, 256); }
+// Rows of the hidden tensors in workspaces, elements apart: whole 128-byte
+// lines, so that no load of them straddles two.
+int64_t hidden_pitch(int64_t F) { return up(F, 64); }
+// Bytes of h; the backward pass's workspace is dg and du (rows of two pitches),
+// then h.
+size_t hidden_bytes(int64_t T, int64_t F) { return up(T * hidden_pitch(F) * 2, 256); }
 
 struct OrthoSpace {
   int64_t r, pitch, pitch_r;  // r: order of the Gram matrix
@@ -534,7 +549,7 @@ uint64_t gemm_ops_launch_count(gemm_ops_t h) { return h ? h->launches : 0; }
 
 size_t gemm_gated_ffn_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t F) {
   if (!h || T <= 0 || D <= 0 || F <= 0) return 0;
-  size_t s = up(T * F * 2, 256);
+  size_t s = hidden_bytes(T, F);
   if (T <= kMaxStreamTokens)
     s += std::max(stream_partial_bytes<kW16, true>(h, T, F, D), stream_partial_bytes<kW16, false>(h, T, D, F));
   return s;
@@ -568,7 +583,8 @@ gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const voi
     return cudaMemset2DAsync(y, ldy * 2, 0, D * 2, T, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
   const bool bf16 = dtype == GEMM_BF16;
   void* hid = workspace;
-  void* partial = static_cast<char*>(workspace) + up(T * F * 2, 256);
+  const int64_t pf = hidden_pitch(F);
+  void* partial = static_cast<char*>(workspace) + hidden_bytes(T, F);
   if (T <= kMaxStreamTokens && stream_fits(F, ldw_in) && stream_fits(D, ldw_down)) {
     StreamArgs a = {};
     a.x = static_cast<const uint16_t*>(x);
@@ -576,7 +592,7 @@ gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const voi
     a.w = w_in;
     a.ldw = ldw_in;
     a.y = static_cast<uint16_t*>(hid);
-    a.ldy = F;
+    a.ldy = pf;
     a.gu = static_cast<uint16_t*>(gu);
     a.partial = static_cast<float*>(partial);
     a.T = static_cast<int32_t>(T);
@@ -585,7 +601,7 @@ gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const voi
     a.act = act;
     if ((st = stream_product<kW16, true>(h, a, bf16, s)) != GEMM_OK) return st;
     a.x = static_cast<const uint16_t*>(hid);
-    a.ldx = F;
+    a.ldx = pf;
     a.w = w_down;
     a.ldw = ldw_down;
     a.y = static_cast<uint16_t*>(y);
@@ -596,21 +612,20 @@ gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const voi
     return stream_product<kW16, false>(h, a, bf16, s);
   }
   const Product p = {T, F, D, {x, T, D, ldx, 1, T * ldx}, {w_in, F, D, ldw_in, 2, F * ldw_in},
-                     false, false, bf16, 1, 1, 0};
+                     false, false, bf16, 1, 1};
   FusedArgs a = base_args(h, p);
   a.act = act;
   a.save = gu != nullptr;
-  const Stack keep = {gu, T, F, 2 * F, 2, F};
-  st = fused<kEpiGlu>(h, p, a, {hid, T, F, F, 1, T * F}, gu ? keep : Stack{}, s);
+  const Stack keep = {gu, T, F, 2 * F, 2, F}, hs = {hid, T, F, pf, 1, T * pf};
+  st = fused<kEpiGlu>(h, p, a, hs, gu ? keep : Stack{}, s);
   if (st != GEMM_OK) return st;
-  const Product down = {T, D, F, {hid, T, F, F, 1, T * F}, {w_down, D, F, ldw_down, 1, D * ldw_down},
-                        false, false, bf16, 1, 1, 0};
-  return product(h, down, y, ldy, s);
+  const Product down = {T, D, F, hs, {w_down, D, F, ldw_down, 1, D * ldw_down}, false, false, bf16, 1, 1};
+  return product(h, down, {y, T, D, ldy, 1, T * ldy}, s);
 }
 
 size_t gemm_gated_ffn_backward_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t F) {
   if (!h || T <= 0 || D <= 0 || F <= 0) return 0;
-  return bwd_h_offset(T, F) + up(T * F * 2, 256);
+  return 3 * hidden_bytes(T, F);
 }
 
 gemm_status_t gemm_gated_ffn_backward(gemm_ops_t h, const void* dy, int64_t lddy, const void* x,
@@ -653,24 +668,29 @@ gemm_status_t gemm_gated_ffn_backward(gemm_ops_t h, const void* dy, int64_t lddy
                ? GEMM_OK
                : GEMM_ERR_CUDA;
   const bool bf16 = dtype == GEMM_BF16;
+  const int64_t pf = hidden_pitch(F);
   uint16_t* dgu = static_cast<uint16_t*>(workspace);
-  uint16_t* hid = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + bwd_h_offset(T, F));
+  uint16_t* hid = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + 2 * hidden_bytes(T, F));
   const Stack dys = {dy, T, D, lddy, 1, T * lddy};
-  const Stack hs = {hid, T, F, F, 1, T * F}, dgus = {dgu, T, 2 * F, 2 * F, 1, T * 2 * F};
+  // dg and du are two matrices side by side, as are the halves of w_in one
+  // after the other.
+  const Stack hs = {hid, T, F, pf, 1, T * pf}, dgus = {dgu, T, F, 2 * pf, 2, pf};
+  const Stack w_ins = {w_in, F, D, ldw_in, 2, F * ldw_in};
   // dh = dy Wd (Wd is stored [K, N] here), then dg, du and h.
-  const Product ph = {T, F, D, dys, {w_down, D, F, ldw_down, 1, D * ldw_down}, false, true, bf16, 1, 1, 0};
+  const Product ph = {T, F, D, dys, {w_down, D, F, ldw_down, 1, D * ldw_down}, false, true, bf16, 1, 1};
   FusedArgs a = base_args(h, ph);
   a.act = act;
   a.src = static_cast<const uint16_t*>(gu);
   a.src_ld = 2 * F;
-  if ((st = fused<kEpiGluBwd>(h, ph, a, hs, {dgu, T, F, 2 * F, 2, F}, s)) != GEMM_OK) return st;
-  // dw_down [D, F] = dy^T h; dx = [dg du] w_in; dw_in [2F, D] = [dg du]^T x.
-  const Product pd = {D, F, T, dys, hs, true, true, bf16, 1, 1, 0};
-  if ((st = product(h, pd, dw_down, F, s)) != GEMM_OK) return st;
-  const Product px = {T, D, 2 * F, dgus, {w_in, 2 * F, D, ldw_in, 1, 2 * F * ldw_in}, false, true, bf16, 1, 1, 0};
-  if ((st = product(h, px, dx, lddx, s)) != GEMM_OK) return st;
-  const Product pi = {2 * F, D, T, dgus, {x, T, D, ldx, 1, T * ldx}, true, true, bf16, 1, 1, 0};
-  return product(h, pi, dw_in, D, s);
+  if ((st = fused<kEpiGluBwd>(h, ph, a, hs, dgus, s)) != GEMM_OK) return st;
+  // dw_down [D, F] = dy^T h; dx = dg Wg + du Wu (two segments); the halves of
+  // dw_in, dg^T x and du^T x (a batch of two).
+  const Product pd = {D, F, T, dys, hs, true, true, bf16, 1, 1};
+  if ((st = product(h, pd, {dw_down, D, F, F, 1, D * F}, s)) != GEMM_OK) return st;
+  const Product px = {T, D, F, dgus, w_ins, false, true, bf16, 1, 2, 0, 0, 0, {0, 1, 0}, {0, 1, 0}};
+  if ((st = product(h, px, {dx, T, D, lddx, 1, T * lddx}, s)) != GEMM_OK) return st;
+  const Product pi = {F, D, T, dgus, {x, T, D, ldx, 1, T * ldx}, true, true, bf16, 2, 1, 1, 0, 1};
+  return product(h, pi, {dw_in, F, D, D, 2, F * D}, s);
 }
 
 static size_t w4_workspace(gemm_ops_t h, int64_t T, int64_t N, int64_t K, bool gated) {
@@ -824,13 +844,13 @@ gemm_status_t gemm_orthogonalize(gemm_ops_t h, const void* m, int64_t ldm, int64
     const Stack xs = {x[cur], M, N, sp.pitch, 2 * batch, xpart};
     const Stack xn = {x[cur ^ 1], M, N, sp.pitch, 2 * batch, xpart};
     {  // P = X X^T (X^T X)
-      const Product p = {r, r, wide ? N : M, xs, xs, !wide, !wide, false, batch, 3, 2};
+      const Product p = {r, r, wide ? N : M, xs, xs, !wide, !wide, false, batch, 3, 2, 2, 2, {0, 0, 1}, {0, 1, 0}};
       FusedArgs a = base_args(h, p);
       a.alpha = kSp / (kSx * kSx);
       if ((st = fused<kEpiSplitSym>(h, p, a, ps, ps, s)) != GEMM_OK) return st;
     }
     {  // Q = c P P + b P
-      const Product p = {r, r, r, ps, ps, false, false, false, batch, 3, 2};
+      const Product p = {r, r, r, ps, ps, false, false, false, batch, 3, 2, 2, 2, {0, 0, 1}, {0, 1, 0}};
       FusedArgs a = base_args(h, p);
       a.alpha = cc * (kSq / (kSp * kSp));
       a.beta = cb * (kSq / kSp);
@@ -840,8 +860,8 @@ gemm_status_t gemm_orthogonalize(gemm_ops_t h, const void* m, int64_t ldm, int64
       if ((st = fused<kEpiSplitSym>(h, p, a, qs, qs, s)) != GEMM_OK) return st;
     }
     {  // X <- Q X + a X (X Q + a X); Q is symmetric
-      const Product p = wide ? Product{M, N, r, qs, xs, false, true, false, batch, 3, 2}
-                             : Product{M, N, r, xs, qs, false, false, false, batch, 3, 2};
+      const Product p = wide ? Product{M, N, r, qs, xs, false, true, false, batch, 3, 2, 2, 2, {0, 0, 1}, {0, 1, 0}}
+                             : Product{M, N, r, xs, qs, false, false, false, batch, 3, 2, 2, 2, {0, 0, 1}, {0, 1, 0}};
       FusedArgs a = base_args(h, p);
       a.alpha = 1.0f / kSq;
       a.beta = ca;
