@@ -1,7 +1,8 @@
 """Build the sm_103a CUDA library in-tree with nvcc (no torch, no cmake).
 
 Produces ``libgb300gemm.so`` next to this file from ``csrc/*.cu`` (the GEMM)
-and ``csrc/ops/*.cu`` (the operators beside it); the compiled code targets exactly sm_103a (GB300).
+and ``csrc/ops/*.cu`` (the operators beside it), and the operators' CPython
+binding ``_binding*.so`` from ``csrc/ops/binding.cpp``; the compiled code targets exactly sm_103a (GB300).
 """
 from __future__ import annotations
 
@@ -9,6 +10,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -16,6 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libgb300gemm.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+BINDING_SRC = os.path.join(CSRC, "ops", "binding.cpp")
+BINDING_PATH = os.path.join(HERE, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,17 +39,34 @@ def _inputs():
             sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [os.path.abspath(__file__)])
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+def _newer(target, inputs) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(p) <= t for p in inputs)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB_PATH, _inputs()) and _newer(BINDING_PATH, _binding_inputs())
+
+
+def _binding_inputs():
+    return [BINDING_SRC, *sorted(glob.glob(os.path.join(INCLUDE, "*.h"))), os.path.abspath(__file__)]
+
+
+def _build_binding():
+    """Start compiling the binding; returns (process, its output, command)."""
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, BINDING_SRC, "-o", tmp]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True), tmp, cmd
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the library if any source is newer than it; return its path."""
     if not force and up_to_date():
         return LIB_PATH
+    binding, binding_tmp, binding_cmd = _build_binding()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     nvcc = _nvcc()
     # The CUDA runtime is linked shared: with torch in the process both use one
@@ -58,6 +79,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     res = subprocess.run(cmd, capture_output=True, text=True)
+    said, _ = binding.communicate()
+    if binding.returncode != 0:
+        raise RuntimeError("the binding failed to build:\n" + " ".join(binding_cmd) + "\n" + said)
+    os.replace(binding_tmp, BINDING_PATH)
     if res.returncode != 0:
         raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
     if verbose:

@@ -1,8 +1,9 @@
 """Operators beside the GEMM: the gated feed-forward block, its backward pass,
 its products from 4-bit weights, and the orthogonalised update of its matrices.
 
-Thin ctypes bindings over the C ABI in ``include/gemm_ops.h``; every step runs
-in the sm_103a kernels of ``libgb300gemm.so``.  Tensors are CUDA tensors of one
+Thin bindings over the C ABI in ``include/gemm_ops.h`` (the calls of single
+products through the compiled ``_binding``, whose cost to the host is most of
+theirs); every step runs in the sm_103a kernels of ``libgb300gemm.so``.  Tensors are CUDA tensors of one
 device, float16 or bfloat16; workspaces come from torch's allocator on the
 current stream.  There is no fallback: wrong arguments and other devices raise.
 
@@ -17,18 +18,18 @@ current stream.  There is no fallback: wrong arguments and other devices raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 import threading
 
 import torch
 
-from . import GemmError, _check, load as _load
+from . import GemmError, _build, _check, load as _load
 
 __all__ = ["Ops", "default_ops", "gated_ffn", "gated_ffn_backward", "w4_linear", "w4_gated",
            "w4_quantize", "orthogonalize", "NEWTON_SCHULZ"]
 
-_F16, _BF16 = torch.float16, torch.bfloat16
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
-_ACT = {"silu": 0, "gelu_tanh": 1, "relu": 2}
 
 #: Coefficients a, b, c of X <- a X + (b P + c P^2) X, P = X X^T.
 NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
@@ -53,17 +54,6 @@ def _lib():
                 "gemm_ops_last_error_detail": (st, [vp, ctypes.POINTER(ctypes.c_uint32)]),
                 "gemm_ops_set_watchdog": (st, [vp, u64, i32]),
                 "gemm_ops_launch_count": (u64, [vp]),
-                "gemm_gated_ffn_workspace": (sz, [vp, i64, i64, i64]),
-                "gemm_gated_ffn": (st, [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, sz, i64, i64,
-                                        i64, st, st, vp]),
-                "gemm_gated_ffn_backward_workspace": (sz, [vp, i64, i64, i64]),
-                "gemm_gated_ffn_backward": (st, [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64,
-                                                 vp, vp, vp, sz, i64, i64, i64, st, st, vp]),
-                "gemm_w4_workspace": (sz, [vp, i64, i64, i64, i32]),
-                "gemm_w4_linear": (st, [vp, vp, i64, vp, vp, vp, vp, i64, vp, sz, i64, i64, i64, i64, st,
-                                        vp]),
-                "gemm_w4_gated": (st, [vp, vp, i64, vp, vp, vp, vp, i64, vp, sz, i64, i64, i64, i64, st,
-                                       st, vp]),
                 "gemm_orthogonalize_workspace": (sz, [vp, i64, i64, i64]),
                 "gemm_orthogonalize": (st, [vp, vp, i64, i64, vp, i64, i64, vp, sz, i64, i64, i64, i32,
                                             ctypes.POINTER(f32), f32, st, st, vp]),
@@ -73,53 +63,6 @@ def _lib():
                 fn.restype, fn.argtypes = res, args
             _SIG = sig
     return lib
-
-
-def _act(act) -> int:
-    try:
-        return _ACT[act]
-    except (KeyError, TypeError):
-        raise ValueError(f"act must be one of {sorted(_ACT)}, got {act!r}") from None
-
-
-def _matrix(t, name, dtype, index, shape, contiguous=False):
-    """Checks one 2-D operand; returns its row distance in elements."""
-    if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
-        return shape[1]  # the common case, in few calls: small products are bound by the host
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    rows, cols = shape
-    ld, inner = t.stride()
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if (cols > 1 and inner != 1) or (rows > 1 and ld < cols):
-        raise ValueError(f"{name}'s rows must be contiguous")
-    # One row or none, or nothing in a row: the distance to the next is free.
-    return ld if rows > 1 and cols else cols
-
-
-def _operand(t, name):
-    """Type, device index and shape of a call's first operand."""
-    dt, index, shape = t.dtype, t.get_device(), t.shape
-    if dt is not _F16 and dt is not _BF16:
-        raise TypeError(f"{name} must be float16 or bfloat16, got {dt}")
-    if index < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if len(shape) != 2:
-        raise ValueError(f"{name} must be 2-D, got {list(shape)}")
-    return dt, index, shape
-
-
-def _columns(t, name, rows):
-    """Columns of a matrix that has to have `rows` rows."""
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != rows:
-        raise ValueError(f"{name} must be a matrix of {rows} rows, got {list(shape)}")
-    return shape[1]
 
 
 def _current_stream(index):
@@ -136,6 +79,29 @@ def _stream(stream, index):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+_binding = None
+
+
+def _load_binding():
+    """The compiled binding, set up with torch's objects and the library's functions."""
+    global _binding
+    lib = _lib()
+    with _sig_lock:
+        if _binding is None:
+            if not os.path.exists(_build.BINDING_PATH):
+                raise ImportError(f"{_build.BINDING_PATH} is missing: build it with "
+                                  "dense_fp16_gemm_04_gb300.build()")
+            spec = importlib.util.spec_from_file_location("_binding", _build.BINDING_PATH)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            fns = ("gemm_gated_ffn_workspace", "gemm_gated_ffn", "gemm_gated_ffn_backward_workspace",
+                   "gemm_gated_ffn_backward", "gemm_w4_workspace", "gemm_w4_linear", "gemm_w4_gated")
+            mod.setup(torch.empty, torch.float16, torch.bfloat16, torch.float32, torch.uint8, _current_stream,
+                      GemmError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in fns))
+            _binding = mod
+    return _binding
+
+
 class Ops:
     """Owns a ``gemm_ops_t`` bound to one CUDA device."""
 
@@ -145,12 +111,14 @@ class Ops:
         _check(self._lib.gemm_ops_create(ctypes.byref(self._h), int(device)), "gemm_ops_create")
         self.index = int(device)
         self.device = torch.device("cuda", self.index)
-        self._needs = {}  # workspace bytes by operator and sizes
+        self._addr = self._h.value
+        self._b = _load_binding()
 
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
             self._lib.gemm_ops_destroy(self._h)
             self._h = ctypes.c_void_p()
+            self._addr = 0
 
     def __del__(self):
         try:
@@ -175,113 +143,22 @@ class Ops:
     def launch_count(self) -> int:
         return int(self._lib.gemm_ops_launch_count(self._h))
 
-    def _workspace(self, query, *sizes):
-        """A workspace of torch's allocator: (tensor, address, bytes)."""
-        key = (query, sizes)
-        need = self._needs.get(key)
-        if need is None:
-            if len(self._needs) >= 4096:
-                self._needs.clear()
-            need = self._needs[key] = getattr(self._lib, query)(self._h, *sizes)
-        if not need:
-            return None, None, 0
-        ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        return ws, ws.data_ptr(), need
-
-    def _same_device(self, index, name):
-        if index != self.index:
-            raise ValueError(f"{name} is on cuda:{index}, the handle on cuda:{self.index}")
-
     # -- the gated block ----------------------------------------------------
     def gated_ffn(self, x, w_in, w_down, act="silu", save=False, out=None, stream=None):
-        dt, dev, (T, D) = _operand(x, "x")
-        self._same_device(dev, "x")
-        a = _act(act)
-        ldx = _matrix(x, "x", dt, dev, (T, D))
-        F = _columns(w_down, "w_down", D)
-        ldd = _matrix(w_down, "w_down", dt, dev, (D, F))
-        ldi = _matrix(w_in, "w_in", dt, dev, (2 * F, D))
-        if out is None:
-            out = torch.empty((T, D), dtype=dt, device=self.device)
-            ldy = D
-        else:
-            ldy = _matrix(out, "out", dt, dev, (T, D))
-        gu = torch.empty((T, 2 * F), dtype=dt, device=self.device) if save else None
-        ws, wp, need = self._workspace("gemm_gated_ffn_workspace", T, D, F)
-        st = self._lib.gemm_gated_ffn(
-            self._h, x.data_ptr(), ldx, w_in.data_ptr(), ldi, w_down.data_ptr(), ldd, out.data_ptr(), ldy,
-            gu.data_ptr() if save else None, wp, need, T, D, F, a, _DTYPE[dt], _stream(stream, dev))
-        if st:
-            _check(st, "gemm_gated_ffn")
-        return (out, gu) if save else out
+        return self._b.gated_ffn(self._addr, self.index, self.device, x, w_in, w_down, act, save, out, stream)
 
     def gated_ffn_backward(self, dy, x, w_in, w_down, gu, act="silu", stream=None):
-        dt, dev, (T, D) = _operand(x, "x")
-        self._same_device(dev, "x")
-        a = _act(act)
-        ldx = _matrix(x, "x", dt, dev, (T, D))
-        F = _columns(w_down, "w_down", D)
-        ldd = _matrix(w_down, "w_down", dt, dev, (D, F))
-        ldi = _matrix(w_in, "w_in", dt, dev, (2 * F, D))
-        ldy = _matrix(dy, "dy", dt, dev, (T, D))
-        _matrix(gu, "gu", dt, dev, (T, 2 * F), contiguous=True)
-        dx = torch.empty((T, D), dtype=dt, device=self.device)
-        dw_in = torch.empty((2 * F, D), dtype=dt, device=self.device)
-        dw_down = torch.empty((D, F), dtype=dt, device=self.device)
-        ws, wp, need = self._workspace("gemm_gated_ffn_backward_workspace", T, D, F)
-        st = self._lib.gemm_gated_ffn_backward(
-            self._h, dy.data_ptr(), ldy, x.data_ptr(), ldx, w_in.data_ptr(), ldi, w_down.data_ptr(), ldd,
-            gu.data_ptr(), dx.data_ptr(), D, dw_in.data_ptr(), dw_down.data_ptr(), wp, need,
-            T, D, F, a, _DTYPE[dt], _stream(stream, dev))
-        if st:
-            _check(st, "gemm_gated_ffn_backward")
-        return dx, dw_in, dw_down
+        return self._b.gated_ffn_backward(self._addr, self.index, self.device, dy, x, w_in, w_down, gu, act,
+                                          stream)
 
     # -- 4-bit weights ------------------------------------------------------
-    def _w4(self, x, codes, scales, zeros, gated, act, out, stream):
-        dt, dev, (T, K) = _operand(x, "x")
-        self._same_device(dev, "x")
-        a = _act(act)
-        ldx = _matrix(x, "x", dt, dev, (T, K))
-        shape = codes.shape
-        if len(shape) != 2 or shape[1] * 2 != K:
-            raise ValueError(f"codes must be [N, {K // 2}] for x of {K} columns, got {list(shape)}")
-        rows = shape[0]
-        _matrix(codes, "codes", torch.uint8, dev, shape, contiguous=True)
-        groups = _columns(scales, "scales", rows)
-        if (groups == 0) != (K == 0) or (K and K % groups):
-            raise ValueError(f"scales must be [{rows}, K / group], got {list(scales.shape)}")
-        _matrix(scales, "scales", dt, dev, (rows, groups), contiguous=True)
-        if zeros is not None:
-            _matrix(zeros, "zeros", torch.uint8, dev, (rows, groups), contiguous=True)
-        if gated and rows % 2:
-            raise ValueError("gated weights have an even number of rows: gate rows, then up rows")
-        N = rows // 2 if gated else rows
-        if out is None:
-            out = torch.empty((T, N), dtype=dt, device=self.device)
-            ldy = N
-        else:
-            ldy = _matrix(out, "out", dt, dev, (T, N))
-        ws, wp, need = self._workspace("gemm_w4_workspace", T, N, K, gated)
-        zp = zeros.data_ptr() if zeros is not None else None
-        group = K // groups if groups else 32
-        if gated:
-            st = self._lib.gemm_w4_gated(
-                self._h, x.data_ptr(), ldx, codes.data_ptr(), scales.data_ptr(), zp, out.data_ptr(), ldy, wp,
-                need, T, N, K, group, a, _DTYPE[dt], _stream(stream, dev))
-        else:
-            st = self._lib.gemm_w4_linear(
-                self._h, x.data_ptr(), ldx, codes.data_ptr(), scales.data_ptr(), zp, out.data_ptr(), ldy, wp,
-                need, T, N, K, group, _DTYPE[dt], _stream(stream, dev))
-        if st:
-            _check(st, "gemm_w4_gated" if gated else "gemm_w4_linear")
-        return out
-
     def w4_linear(self, x, codes, scales, zeros=None, out=None, stream=None):
-        return self._w4(x, codes, scales, zeros, False, "silu", out, stream)
+        return self._b.w4(self._addr, self.index, self.device, x, codes, scales, zeros, None, out, stream)
 
     def w4_gated(self, x, codes, scales, zeros=None, act="silu", out=None, stream=None):
-        return self._w4(x, codes, scales, zeros, True, act, out, stream)
+        if act is None:
+            raise ValueError("act must be 'silu', 'gelu_tanh' or 'relu', got None")
+        return self._b.w4(self._addr, self.index, self.device, x, codes, scales, zeros, act, out, stream)
 
     # -- the orthogonalised update -------------------------------------------
     def orthogonalize(self, m, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, dtype=None, out=None, stream=None):
@@ -310,9 +187,10 @@ class Ops:
             if N > 1 and inner != 1 or M > 1 and ld < N:
                 raise ValueError(f"{name}'s rows must be contiguous")
             lds += [ld if M > 1 else N, bs if B > 1 else 0]
-        ws, wp, need = self._workspace("gemm_orthogonalize_workspace", B, M, N)
+        need = self._lib.gemm_orthogonalize_workspace(self._h, B, M, N)
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         _check(self._lib.gemm_orthogonalize(
-            self._h, m.data_ptr(), lds[0], lds[1], out.data_ptr(), lds[2], lds[3], wp, need, B, M, N,
+            self._h, m.data_ptr(), lds[0], lds[1], out.data_ptr(), lds[2], lds[3], ws.data_ptr(), need, B, M, N,
             int(steps), (ctypes.c_float * 3)(*coeffs), float(eps), _DTYPE[m.dtype], _DTYPE[dtype],
             _stream(stream, self.index)), "gemm_orthogonalize")
         return out
