@@ -224,7 +224,7 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
 }
 
 // Which form: split clusters where the 128 x 128 tiles are few (each CTA with
-// two k-blocks at least); pairs when the 256-row tiles fill at least half of
+// two k-blocks at least, one for the batched products); pairs when the 256-row tiles fill at least half of
 // the device; else lone CTAs.  Of clusters of eight CTAs 15 fit at once, of
 // four 36, of two 76.
 template <int kEpi>
@@ -238,7 +238,7 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
   if constexpr (kBatched) {
     // The number of k-ranges goes by one matrix's tiles, so that a matrix of a
     // batch gets the same sums as by itself; who sums them by the batch's.
-    if (small <= most[2] && kb >= 8)
+    if (small <= most[2] && kb >= 4)
       return small * p.batch <= most[2] ? launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream)
                                         : launch_fused<Lone<kEpi, 1, 4>>(h, p, a, c, d, stream);
     if (small <= most[1] && kb >= 4)
