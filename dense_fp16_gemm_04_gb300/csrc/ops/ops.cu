@@ -224,8 +224,8 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
 }
 
 // Which form: split clusters where the 128 x 128 tiles are few (each CTA with
-// two k-blocks at least, one for the batched products); pairs when the 256-row tiles fill at least half of
-// the device; else lone CTAs.  Of clusters of eight CTAs 15 fit at once, of
+// two k-blocks at least, one for the batched products); else pairs or lone
+// CTAs, by their rounds of tiles.  Of clusters of eight CTAs 15 fit at once, of
 // four 36, of two 76.
 template <int kEpi>
 gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const Stack& c,
@@ -250,9 +250,13 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
     if (all <= most[2] && kb >= 8) return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream);
     if (all <= most[1] && kb >= 4) return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream);
   }
-  const int64_t big = tiles(cdiv(p.M, 256), cdiv(p.N, Pair<kEpi>::kOutN)) * (kBatched ? 1 : p.batch);
-  return h->max_pairs > 0 && 2 * big >= h->max_pairs ? launch_fused<Pair<kEpi>>(h, p, a, c, d, stream)
-                                                     : launch_fused<Lone<kEpi>>(h, p, a, c, d, stream);
+  // Rounds of tiles times the time of one (units of 10 ns: a k-block of a pair's
+  // tile, of a lone CTA's, and what starts and ends a tile).
+  const int64_t n = kBatched ? 1 : p.batch;
+  const int64_t big = tiles(cdiv(p.M, 256), cdiv(p.N, Pair<kEpi>::kOutN)) * n;
+  const int64_t pairs = h->max_pairs > 0 ? cdiv(big, h->max_pairs) * (33 * kb + 500) : INT64_MAX;
+  return pairs <= cdiv(small * n, h->num_sms) * (27 * kb + 400) ? launch_fused<Pair<kEpi>>(h, p, a, c, d, stream)
+                                                                 : launch_fused<Lone<kEpi>>(h, p, a, c, d, stream);
 }
 
 // out = A B^T, rounded to 16 bits.

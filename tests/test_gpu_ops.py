@@ -478,3 +478,116 @@ def test_refusals(g):
         g.orthogonalize(torch.zeros(3, 3, device="cuda", dtype=torch.int32))
     with pytest.raises(ValueError):
         g.orthogonalize(torch.zeros(3, 4, device="cuda").t())
+
+
+# ---------------------------------------------- shared tiles, batches, long offsets --
+# 256 x 256 tiles just past a round of 76 pairs: their k-blocks are shared out.
+@pytest.mark.parametrize("shape", [(2817, 1096, 2104), (1300, 4104, 2056)])
+def test_ffn_shared_tiles(g, shape):
+    T, D, F = shape
+    dt = torch.float16
+    x, w_in, w_down, dy = make_ffn(T, D, F, dt, seed=7)
+    y, gu = run_ffn(g, x, w_in, w_down, "silu", dt)
+    for _ in range(2):
+        y2, gu2 = g.gated_ffn(x, w_in, w_down, save=True)
+        assert torch.equal(y, y2) and torch.equal(gu, gu2)
+    got = g.gated_ffn_backward(dy, x, w_in, w_down, gu)
+    g.default_ops().check_error()
+    for name, o, (ref, err) in zip(("dx", "dw_in", "dw_down"), got,
+                                   ffn_backward_ref(dy, x, w_in, w_down, gu, "silu", dt)):
+        check(o, ref, err, dt, name)
+    for a, b in zip(got, g.gated_ffn_backward(dy, x, w_in, w_down, gu)):
+        assert torch.equal(a, b)
+
+
+def test_orthogonalize_shared_tiles(g):
+    m = torch.randn(3000, 3010, device="cuda")
+    ref, err = ns_ref(m, 2, COEFFS, 1e-7)
+    o = g.orthogonalize(m, steps=2)
+    g.default_ops().check_error()
+    assert (o.to(F64) - ref).norm() <= err
+    both = g.orthogonalize(torch.stack((m, 2 * m)), steps=2)
+    assert torch.equal(both[0], o) and torch.equal(both[0], both[1])  # twice m is the same after scaling
+
+
+@pytest.mark.parametrize("shape", [(7, 130, 300), (20, 64, 64), (5, 900, 1000), (3, 1200, 500), (40, 128, 70)])
+def test_orthogonalize_larger_batches(g, shape):
+    m = torch.randn(*shape, device="cuda")
+    o = g.orthogonalize(m)
+    for b in (0, 1, shape[0] - 1):
+        assert torch.equal(o[b], g.orthogonalize(m[b]))
+        ref, err = ns_ref(m[b], 5, COEFFS, 1e-7)
+        assert (o[b].to(F64) - ref).norm() <= err
+
+
+def test_w4_scales_off_a_word(g):
+    """Scales and zero points that start on any element of their allocation."""
+    for group in (32, 64, 128):
+        x, codes, scales, z = make_w4(3, 50, 256, group, True, torch.float16)
+        want = g.w4_linear(x, codes, scales, z)
+        for shift in (1, 2, 3):
+            def moved(t):
+                b = torch.empty(t.numel() + shift, dtype=t.dtype, device="cuda")
+                b[shift:] = t.flatten()
+                return b[shift:].view(t.shape)
+            assert torch.equal(g.w4_linear(x, codes, moved(scales), moved(z)), want)
+            assert torch.equal(g.w4_linear(x, codes, moved(scales)), g.w4_linear(x, codes, scales))
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_w4_past_four_gigabytes(g, gated):
+    """Codes of 5.1 GB: rows past the 32-bit byte offsets of one launch."""
+    T, N, K, G = 2, 40000, 262144, 128
+    if gated:
+        N //= 2
+    rows = 2 * N if gated else N
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, K, generator=gen, device="cuda").to(torch.float16)
+    codes = torch.randint(0, 256, (rows, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    scales = (torch.rand(rows, K // G, generator=gen, device="cuda") * K ** -0.5).to(torch.float16)
+    got = g.w4_gated(x, codes, scales) if gated else g.w4_linear(x, codes, scales)
+    pick = torch.tensor([0, 1, N // 2, 32767 % N, 32768 % N, N - 2, N - 1], device="cuda")
+    if gated:
+        sel = torch.cat((pick, pick + N))
+        h, eh, _, _ = gated_ref(x, w4_ref(codes[sel], scales[sel], None), "silu", torch.float16)
+        check(got[:, pick], h, eh, torch.float16, "h")
+    else:
+        w = w4_ref(codes[pick], scales[pick], None)
+        check(got[:, pick], x.to(F64) @ w.t(), sum_eps(K) * (x.to(F64).abs() @ w.abs().t()), torch.float16, "y")
+
+
+def test_ffn_past_two_gigaelements(g):
+    """gu of 2.3e9 elements: token offsets past 32 bits."""
+    T, D, F = 70000, 64, 16640
+    x, w_in, w_down, dy = make_ffn(T, D, F, torch.float16)
+    y, gu = g.gated_ffn(x, w_in, w_down, save=True)
+    pick = torch.tensor([0, 1, 64528, 64529, T - 130, T - 1], device="cuda")
+    h, eh, p, ep = gated_ref(x[pick], w_in, "silu", torch.float16)
+    check(gu[pick], p, ep, torch.float16, "gu")
+    wd = w_down.to(F64)
+    eh = eh + U[torch.float16] * (h.abs() + eh) + TINY[torch.float16]
+    check(y[pick], h @ wd.t(), eh @ wd.abs().t() + sum_eps(F) * ((h.abs() + eh) @ wd.abs().t()), torch.float16, "y")
+    dx, _, _ = g.gated_ffn_backward(dy, x, w_in, w_down, gu)
+    ref, err = ffn_backward_ref(dy[pick], x[pick], w_in, w_down, gu[pick], "silu", torch.float16)[0]
+    check(dx[pick], ref, err, torch.float16, "dx")
+
+
+def test_dependent_calls_back_to_back(g):
+    """Each call reads what the one before wrote, with nothing waiting between."""
+    dt = torch.float16
+    x, w_in, w_down, _ = make_ffn(20, 256, 512, dt)
+    _, codes, scales, z = make_w4(1, 256, 256, 64, True, dt)
+    def chain(sync):
+        v = x
+        for i in range(20):
+            v = g.gated_ffn(v[:4] if i % 3 == 0 else v, w_in, w_down)
+            if sync:
+                torch.cuda.synchronize()
+            v = g.w4_linear(v, codes, scales, z)
+            if sync:
+                torch.cuda.synchronize()
+            v = (v / v.float().norm().to(dt)).repeat(5 if v.shape[0] == 4 else 1, 1)
+        return v
+    want = chain(True)
+    for _ in range(3):
+        assert torch.equal(chain(False), want)
