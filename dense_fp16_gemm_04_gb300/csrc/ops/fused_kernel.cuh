@@ -22,8 +22,8 @@
 //                the source S.
 //   kEpiSplitSym the same for a symmetric C: only tiles on and above the
 //                diagonal are computed, and each is also stored transposed.
-// Few tiles with long K (kSplit = 2, 4 or 8): a cluster of kSplit CTAs takes one
-// 128 x 128 tile, each CTA a k-range of it, so that more SMs load operands (one
+// Few tiles with long K (kSplit = 2, 4 or 8; two pairs: 2): a cluster of kSplit
+// CTAs takes one 128 x 128 tile (two pairs one of 256 x 256), each CTA a k-range of it, so that more SMs load operands (one
 // SM's loads, 32 KB a k-block against 128 clocks of MMAs, bound a lone CTA).
 // Each CTA then finishes 128 / kSplit of the tile's columns: every CTA sends
 // the others their columns of its partial sums through distributed shared
@@ -98,6 +98,7 @@ struct FusedCfg {
   static constexpr int kEpiBufs = kEpiBufs_;  // 32 x 64 staging buffers per epilogue warp
   static constexpr bool kGlu = kEpi == kEpiGlu;
   static constexpr bool kSym = kEpi == kEpiSplitSym;
+  static constexpr bool kReads = kEpi == kEpiGluBwd || kEpi == kEpiSplit || kSym;  // the epilogue reads too
   static constexpr int kOutN = kGlu ? kBN / 2 : kBN;  // output columns per tile
   static constexpr int kBM = 128, kBK = 64;
   static constexpr int kTileM = kBM * kCtas;
@@ -123,10 +124,11 @@ struct FusedCfg {
   static_assert(!kSym || kTileM == kBN, "symmetric tiles are square");
   static_assert(kTmemCols <= 512, "TMEM columns");
   static_assert(kParts == 1 || (kSplit == 1 && (kEpi == kEpiSplit || kEpi == kEpiSplitSym)), "parts");
-  // The partials a split CTA receives, its own among them: 128 rows x 128
-  // columns in all, in the staging buffers' place.
-  static_assert(kSplit == 1 || (kCtas == 1 && kBN == 128 && kEpiWarps * kEpiBufs * kBufBytes >= kBM * kBN * 4),
-                "split clusters: single CTAs, 128 x 128 tiles");
+  // The partials a split CTA receives (a lone one its own among them): 128 rows
+  // x 128 columns in all, in the staging buffers' place.
+  static_assert(kSplit == 1 || kEpiWarps * kEpiBufs * kBufBytes >= kBM * 128 * 4, "partials");
+  static_assert(kSplit == 1 || (kCtas == 1 && kBN == 128) || (kCtas == 2 && kBN == 256 && kSplit == 2),
+                "split clusters: lone CTAs on 128 x 128 tiles, two pairs on 256 x 256 ones");
 };
 
 // One tile, and a CTA's k-range of it.
@@ -167,90 +169,16 @@ __device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&v)[kN / 2]
   }
 }
 
-// The end of a split cluster's tile, run by all 256 threads of each CTA.
-template <class Cfg>
-__device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t unit, int32_t rank,
-                                               uint32_t tmem_base, uint32_t recv, uint32_t tfull,
-                                               const Watch& w) {
-  constexpr int kS = Cfg::kSplit;
-  constexpr int kCols = Cfg::kBN / kS;  // accumulator columns this CTA finishes
-  constexpr int kHalfCols = kCols / 2;  // gated: gate columns, then as many up columns
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  ptx::griddep_wait();  // reads S, g and u; writes the outputs
-  bool ok = wait_bar_warp<false>(tfull, 0u, w, kSiteTmemFull, unit);
-  if (ok) {
-    // Send: warp quarter q owns 32 rows, warps 0-3 columns 0-63, warps 4-7 the
-    // rest (gated: gate, up).  Receiver's slot: [source][4 columns][row][16 B],
-    // so a warp writes 512 contiguous bytes at a time.
-    ptx::tc_fence_after();
-    const int q = warp & 3, side = warp >> 2;
-    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + side * 64;
-    const uint32_t mine = recv + static_cast<uint32_t>(rank * (kCols / 4) * 128 + q * 32 + lane) * 16u;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      uint32_t v[16];
-      ptx::tmem_ld_32x32b_x16(t_row + g * 16, v);
-      ptx::tmem_wait_ld(v);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = g * 16 + j * 4;  // of this side's 64
-        int to, at;                    // receiving CTA, its 4-column group
-        if (Cfg::kGlu) {
-          to = c / kHalfCols;
-          at = (c % kHalfCols) / 4 + side * (kHalfCols / 4);
-        } else {
-          to = (side * 64 + c) / kCols;
-          at = (side * 64 + c) % kCols / 4;
-        }
-        ptx::st_shared_cluster_v4(ptx::mapa(mine + static_cast<uint32_t>(at * 128) * 16u, static_cast<uint32_t>(to)),
-                                  v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      }
-    }
-  }
-  // Thread (row, half) finishes half of the CTA's columns.  What the epilogue
-  // reads comes in while the partials do.
-  constexpr int kN = Cfg::kGlu ? kHalfCols / 2 : kCols / 2;
-  constexpr bool kReads = Cfg::kEpi == kEpiGluBwd || Cfg::kEpi == kEpiSplit || Cfg::kEpi == kEpiSplitSym;
-  const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
-  const FusedItem wi = fused_item<Cfg>(args, unit, rank);
-  const int32_t row = wi.mb * Cfg::kBM + r;
-  const int32_t col0 = wi.nb * Cfg::kOutN + rank * (Cfg::kOutN / kS) + half * kN;
-  const bool in = row < args.M && col0 < args.N;
-  uint4 s0[kReads ? kN / 8 : 1], s1[kReads ? kN / 8 : 1];
-  if constexpr (kReads) {
-    const bool gated = Cfg::kEpi == kEpiGluBwd;
-    const int64_t second = gated ? args.N : args.src_part;
-    const uint16_t* src = args.src + (gated ? 0 : static_cast<int64_t>(wi.batch) * 2 * args.src_part) +
-                          static_cast<int64_t>(row) * args.src_ld + col0;
-    if (in && (gated || args.beta != 0.0f)) {
-#pragma unroll
-      for (int i = 0; i < kN / 8; ++i)
-        if (col0 + 8 * i < args.N) {
-          s0[i] = ptx::ld_global_v4_u32(src + 8 * i);
-          s1[i] = ptx::ld_global_v4_u32(src + second + 8 * i);
-        }
-    }
-  }
-  ptx::cluster_sync();
-  if (!ok || !in) return;
-  auto sum = [&](int first4, float (&v)[kN]) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) v[i] = 0.0f;
-#pragma unroll
-    for (int s = 0; s < kS; ++s)
-#pragma unroll
-      for (int i = 0; i < kN / 4; ++i) {
-        const float4 p = ptx::ld_shared_v4_f32(
-            recv + static_cast<uint32_t>((s * (kCols / 4) + first4 + i) * 128 + r) * 16u);
-        v[4 * i] += p.x, v[4 * i + 1] += p.y, v[4 * i + 2] += p.z, v[4 * i + 3] += p.w;
-      }
-  };
+// The epilogue of kN columns of one row, from col0 on: v their sums (gated: of
+// the gate, u of the up projection), s0 and s1 what the epilogue reads there.
+template <class Cfg, int kN>
+__device__ __forceinline__ void finish_columns(const FusedArgs& args, const FusedItem& wi, int32_t row,
+                                               int32_t col0, const float (&v)[kN], const float* u,
+                                               const uint4* s0, const uint4* s1) {
   const bool bf16 = args.bf16 != 0;
   // Columns come in groups of eight that are in or out together (four, gated
   // over eight CTAs): N is a multiple of 8, or the rows are padded to one.
   constexpr int kG = kN < 8 ? kN : 8;
-  float v[kN];
-  sum(half * (kN / 4), v);
   if constexpr (Cfg::kEpi == kEpiStore) {
     uint16_t* c = args.c + wi.batch * args.c_zb * args.c_z + static_cast<int64_t>(row) * args.ldc + col0;
 #pragma unroll
@@ -262,8 +190,6 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
       if (col0 + i < args.N) store16<kG>(c + i, p);
     }
   } else if constexpr (Cfg::kEpi == kEpiGlu) {
-    float u[kN];
-    sum(kHalfCols / 4 + half * (kN / 4), u);
     uint16_t* c = args.c + static_cast<int64_t>(row) * args.ldc + col0;
     uint16_t* d = args.d + static_cast<int64_t>(row) * args.ldd + col0;
 #pragma unroll
@@ -353,6 +279,162 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
   }
 }
 
+// What the epilogue of kN columns reads: S and its low part, or g and u.
+template <class Cfg, int kN>
+__device__ __forceinline__ void read_columns(const FusedArgs& args, const FusedItem& wi, int32_t row,
+                                             int32_t col0, uint4* s0, uint4* s1) {
+  if constexpr (Cfg::kReads) {
+    const bool gated = Cfg::kEpi == kEpiGluBwd;
+    const int64_t second = gated ? args.N : args.src_part;
+    const uint16_t* src = args.src + (gated ? 0 : static_cast<int64_t>(wi.batch) * 2 * args.src_part) +
+                          static_cast<int64_t>(row) * args.src_ld + col0;
+    if (gated || args.beta != 0.0f) {
+#pragma unroll
+      for (int i = 0; i < kN / 8; ++i)
+        if (col0 + 8 * i < args.N) {
+          s0[i] = ptx::ld_global_v4_u32(src + 8 * i);
+          s1[i] = ptx::ld_global_v4_u32(src + second + 8 * i);
+        }
+    }
+  }
+}
+
+// The end of a split cluster's tile, run by all 256 threads of each CTA: lone
+// CTAs.
+template <class Cfg>
+__device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t unit, int32_t rank,
+                                               uint32_t tmem_base, uint32_t recv, uint32_t tfull,
+                                               const Watch& w) {
+  constexpr int kS = Cfg::kSplit;
+  constexpr int kCols = Cfg::kBN / kS;  // accumulator columns this CTA finishes
+  constexpr int kHalfCols = kCols / 2;  // gated: gate columns, then as many up columns
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ptx::griddep_wait();  // reads S, g and u; writes the outputs
+  bool ok = wait_bar_warp<false>(tfull, 0u, w, kSiteTmemFull, unit);
+  if (ok) {
+    // Send: warp quarter q owns 32 rows, warps 0-3 columns 0-63, warps 4-7 the
+    // rest (gated: gate, up).  Receiver's slot: [source][4 columns][row][16 B],
+    // so a warp writes 512 contiguous bytes at a time.
+    ptx::tc_fence_after();
+    const int q = warp & 3, side = warp >> 2;
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + side * 64;
+    const uint32_t mine = recv + static_cast<uint32_t>(rank * (kCols / 4) * 128 + q * 32 + lane) * 16u;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint32_t v[16];
+      ptx::tmem_ld_32x32b_x16(t_row + g * 16, v);
+      ptx::tmem_wait_ld(v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = g * 16 + j * 4;  // of this side's 64
+        int to, at;                    // receiving CTA, its 4-column group
+        if (Cfg::kGlu) {
+          to = c / kHalfCols;
+          at = (c % kHalfCols) / 4 + side * (kHalfCols / 4);
+        } else {
+          to = (side * 64 + c) / kCols;
+          at = (side * 64 + c) % kCols / 4;
+        }
+        ptx::st_shared_cluster_v4(ptx::mapa(mine + static_cast<uint32_t>(at * 128) * 16u, static_cast<uint32_t>(to)),
+                                  v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      }
+    }
+  }
+  // Thread (row, half) finishes half of the CTA's columns.  What the epilogue
+  // reads comes in while the partials do.
+  constexpr int kN = Cfg::kGlu ? kHalfCols / 2 : kCols / 2;
+  const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
+  const FusedItem wi = fused_item<Cfg>(args, unit, rank);
+  const int32_t row = wi.mb * Cfg::kBM + r;
+  const int32_t col0 = wi.nb * Cfg::kOutN + rank * (Cfg::kOutN / kS) + half * kN;
+  const bool in = row < args.M && col0 < args.N;
+  uint4 s0[Cfg::kReads ? kN / 8 : 1], s1[Cfg::kReads ? kN / 8 : 1];
+  if (in) read_columns<Cfg, kN>(args, wi, row, col0, s0, s1);
+  ptx::cluster_sync();
+  if (!ok || !in) return;
+  auto sum = [&](int first4, float (&v)[kN]) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kS; ++s)
+#pragma unroll
+      for (int i = 0; i < kN / 4; ++i) {
+        const float4 p = ptx::ld_shared_v4_f32(
+            recv + static_cast<uint32_t>((s * (kCols / 4) + first4 + i) * 128 + r) * 16u);
+        v[4 * i] += p.x, v[4 * i + 1] += p.y, v[4 * i + 2] += p.z, v[4 * i + 3] += p.w;
+      }
+  };
+  float v[kN], u[Cfg::kGlu ? kN : 1];
+  sum(half * (kN / 4), v);
+  if constexpr (Cfg::kGlu) sum(kHalfCols / 4 + half * (kN / 4), u);
+  finish_columns<Cfg, kN>(args, wi, row, col0, v, u, s0, s1);
+}
+
+// The same for two pairs of CTAs, each with half of the k-blocks of a 256 x 256
+// tile: pair k finishes half k of its columns (gated: of the gate's and of the
+// up projection's), and each CTA sends its 128 rows of the other half to the
+// CTA of the same rows in the other pair.  A sum of two: its order is free.
+template <class Cfg>
+__device__ __forceinline__ void pair_split_epilogue(const FusedArgs& args, int32_t unit, int32_t k, uint32_t cta,
+                                                    uint32_t tmem_base, uint32_t recv, uint32_t tfull,
+                                                    const Watch& w) {
+  constexpr int kOut = Cfg::kOutN / 2;           // output columns a pair finishes
+  constexpr int kN = kOut / 2;                   // and a thread
+  constexpr int kSide = Cfg::kGlu ? 128 : 64;    // accumulator columns between the two sides' first
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, side = warp >> 2;
+  const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+  ptx::griddep_wait();
+  const bool ok = wait_bar_warp<true>(tfull, 0u, w, kSiteTmemFull, unit);
+  const int r = q * 32 + lane;
+  if (ok) {
+    // Sides: 64 columns each (gated: gate and up).  Slot: [4 columns][row][16 B].
+    ptx::tc_fence_after();
+    const uint32_t to = ptx::mapa(recv, static_cast<uint32_t>((k ^ 1) * 2) + cta) +
+                        static_cast<uint32_t>(side * 16 * 128 + r) * 16u;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint32_t v[16];
+      ptx::tmem_ld_32x32b_x16(t_row + (k ^ 1) * kOut + side * kSide + g * 16, v);
+      ptx::tmem_wait_ld(v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        ptx::st_shared_cluster_v4(to + static_cast<uint32_t>((g * 4 + j) * 128) * 16u, v[4 * j], v[4 * j + 1],
+                                  v[4 * j + 2], v[4 * j + 3]);
+    }
+  }
+  const FusedItem wi = fused_item<Cfg>(args, unit, k);
+  const int32_t row = wi.mb * Cfg::kTileM + static_cast<int32_t>(cta) * Cfg::kBM + r;
+  const int32_t col0 = wi.nb * Cfg::kOutN + k * kOut + side * kN;
+  const bool in = row < args.M && col0 < args.N;
+  uint4 s0[Cfg::kReads ? kN / 8 : 1], s1[Cfg::kReads ? kN / 8 : 1];
+  if (in) read_columns<Cfg, kN>(args, wi, row, col0, s0, s1);
+  ptx::cluster_sync();
+  if (!ok) return;
+  auto sum = [&](int col, int group4, float (&v)[16]) {  // every lane: tensor memory
+    uint32_t t[16];
+    ptx::tmem_ld_32x32b_x16(t_row + col, t);
+    ptx::tmem_wait_ld(t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 p = ptx::ld_shared_v4_f32(recv + static_cast<uint32_t>((group4 + i) * 128 + r) * 16u);
+      v[4 * i] = __uint_as_float(t[4 * i]) + p.x;
+      v[4 * i + 1] = __uint_as_float(t[4 * i + 1]) + p.y;
+      v[4 * i + 2] = __uint_as_float(t[4 * i + 2]) + p.z;
+      v[4 * i + 3] = __uint_as_float(t[4 * i + 3]) + p.w;
+    }
+  };
+#pragma unroll
+  for (int c = 0; c < kN; c += 16) {
+    float v[16], u[16];
+    sum(k * kOut + side * kN + c, (side * kN + c) / 4, v);
+    if constexpr (Cfg::kGlu) sum(128 + k * kOut + side * kN + c, 16 + (side * kN + c) / 4, u);
+    if (in)
+      finish_columns<Cfg, 16>(args, wi, row, col0 + c, v, u, s0 + (Cfg::kReads ? c / 8 : 0),
+                              s1 + (Cfg::kReads ? c / 8 : 0));
+    __syncwarp();
+  }
+}
+
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     fused_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -367,8 +449,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   constexpr bool kCluster = Cfg::kCluster > 1;
-  const uint32_t cta = kPair ? ptx::cluster_ctarank() : 0u;  // 0: issues the MMAs
-  const int32_t rank = Cfg::kSplit > 1 ? static_cast<int32_t>(ptx::cluster_ctarank()) : 0;  // k-range
+  const uint32_t crank = kCluster ? ptx::cluster_ctarank() : 0u;
+  const uint32_t cta = kPair ? crank & 1u : 0u;  // 0: issues the MMAs
+  const uint32_t leader = kPair ? crank & ~1u : 0u;  // the pair's CTA that does
+  const uint16_t pair_mask = static_cast<uint16_t>(0x3u << leader);
+  const int32_t rank = Cfg::kSplit > 1 ? static_cast<int32_t>(crank) / Cfg::kCtas : 0;  // k-range
   const int32_t unit = kCluster ? static_cast<int32_t>(ptx::cluster_id_x()) : static_cast<int32_t>(blockIdx.x);
   const int32_t units = kCluster ? static_cast<int32_t>(ptx::num_clusters_x()) : static_cast<int32_t>(gridDim.x);
 
@@ -450,7 +535,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           const int32_t z = z0 + (is_a ? args.a_seg[seg] : args.b_seg[seg]);
           uint32_t full = bar_full(stage);
           if constexpr (kPair) {
-            full = ptx::mapa(full, 0);
+            full = ptx::mapa(full, leader);
             if (cta == 0) ptx::mbar_arrive_expect_tx(bar_full(stage), op_tx);
           } else {
             ptx::mbar_arrive_expect_tx(full, op_tx);
@@ -546,7 +631,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
               ptx::mma_f16<Cfg::kCtas>(d_tmem, a_desc + a_kstep * k, b_desc + b_kstep * k, idesc,
                                        k != 0 ? 1u : acc_first);
             if constexpr (kPair)
-              ptx::mma_commit_pair(bar_empty(stage), 0x3);
+              ptx::mma_commit_pair(bar_empty(stage), pair_mask);
             else
               ptx::mma_commit(bar_empty(stage));
           }
@@ -559,7 +644,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         if (!ok) break;
         if (ptx::elect_one()) {
           if constexpr (kPair)
-            ptx::mma_commit_pair(bar_tfull(buf), 0x3);
+            ptx::mma_commit_pair(bar_tfull(buf), pair_mask);
           else
             ptx::mma_commit(bar_tfull(buf));
         }
@@ -569,7 +654,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       // Every MMA has finished before tensor memory is freed.
       if (ptx::elect_one()) {
         if constexpr (kPair)
-          ptx::mma_commit_pair(bar_mma_done, 0x1);
+          ptx::mma_commit_pair(bar_mma_done, static_cast<uint16_t>(1u << leader));
         else
           ptx::mma_commit(bar_mma_done);
       }
@@ -582,7 +667,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const int q = warp & 3;  // this warp may touch TMEM lanes 32q .. 32q+31 only
     const uint32_t stage_base =
         sb + Cfg::kOffEpi + static_cast<uint32_t>(q * Cfg::kEpiBufs * Cfg::kBufBytes);
-    const uint32_t tempty_bar0 = kPair ? ptx::mapa(bar_tempty(0), 0) : bar_tempty(0);
+    const uint32_t tempty_bar0 = kPair ? ptx::mapa(bar_tempty(0), leader) : bar_tempty(0);
     const bool bf16 = args.bf16 != 0;
     uint32_t next_buf = 0, used = 0;
     int32_t acc_iter = 0;
@@ -804,7 +889,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
   if constexpr (Cfg::kSplit > 1) {
     __syncwarp();
-    split_epilogue<Cfg>(args, unit, rank, tmem_base, sb + Cfg::kOffEpi, bar_tfull(0), w);
+    if constexpr (kPair)
+      pair_split_epilogue<Cfg>(args, unit, rank, cta, tmem_base, sb + Cfg::kOffEpi, bar_tfull(0), w);
+    else
+      split_epilogue<Cfg>(args, unit, rank, tmem_base, sb + Cfg::kOffEpi, bar_tfull(0), w);
   }
 
   ptx::tc_fence_before();

@@ -18,6 +18,7 @@ struct gemm_ops_s {
   int device = 0;
   int num_sms = 0;
   int max_pairs = 0;  // CTA pairs of the pair kernels that fit on the device at once
+  int max_twos = 0;       // clusters of two pairs sharing a tile
   int max_split[4] = {};  // clusters of 1, 2, 4, 8 CTAs sharing a tile
   void* encode = nullptr;
   uint32_t* d_err = nullptr;  // 4-word watchdog record
@@ -44,6 +45,8 @@ constexpr int kGroupM = 8;
 // 128 x 128 for problems of few tiles.
 template <int kEpi>
 using Pair = FusedCfg<2, 256, kEpi == kEpiStore ? 6 : 5, kEpi, kEpi == kEpiStore ? 2 : 4>;
+template <int kEpi>
+using TwoPairs = FusedCfg<2, 256, 5, kEpi, 4, 2>;  // one tile, half of its k-blocks each
 template <int kEpi, int kSplit = 1, int kParts = 1>
 using Lone = FusedCfg<1, 128, 5, kEpi, 4, kSplit, kParts>;
 
@@ -223,40 +226,49 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
                 Cfg::kSmemBytes, Cfg::kCluster, stream, ma, mb, mc, md, a);
 }
 
-// Which form: split clusters where the 128 x 128 tiles are few (each CTA with
-// two k-blocks at least, one for the batched products); else pairs or lone
-// CTAs, by their rounds of tiles.  Of clusters of eight CTAs 15 fit at once, of
-// four 36, of two 76.
+// Which form: the one whose rounds of tiles take the least time by this model,
+// in units of 10 ns: a k-block takes a lone CTA 0.27 us (its 32 KB of operands
+// through the SM's L2 port), a pair 0.33 us (the tensor pipe), and a tile starts
+// and ends in 4 to 7 us.  Of clusters of two CTAs 76 fit at once, of four 36, of
+// eight 15.  Lone clusters split a tile only where all fit at once.
+//
+// The batched products (high and low parts) go by one matrix's tiles alone, so
+// that a matrix of a batch gets the same sums as by itself: the number of its
+// k-ranges is fixed, and the batch's tiles decide who sums them.
 template <int kEpi>
 gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const Stack& c,
                     const Stack& d, cudaStream_t stream) {
   constexpr bool kBatched = kEpi == kEpiSplit || kEpi == kEpiSplitSym;
   auto tiles = [&](int64_t tm, int64_t tn) { return Pair<kEpi>::kSym ? tn * (tn + 1) / 2 : tm * tn; };
-  const int64_t small = tiles(cdiv(p.M, 128), cdiv(p.N, Lone<kEpi>::kOutN));
-  const int64_t kb = cdiv(p.K, 64) * p.segs;
-  const int* most = h->max_split;
-  if constexpr (kBatched) {
-    // The number of k-ranges goes by one matrix's tiles, so that a matrix of a
-    // batch gets the same sums as by itself; who sums them by the batch's.
-    if (small <= most[2] && kb >= 4)
-      return small * p.batch <= most[2] ? launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream)
-                                        : launch_fused<Lone<kEpi, 1, 4>>(h, p, a, c, d, stream);
-    if (small <= most[1] && kb >= 4)
-      return small * p.batch <= most[1] ? launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream)
-                                        : launch_fused<Lone<kEpi, 1, 2>>(h, p, a, c, d, stream);
-  } else {
-    const int64_t all = small * p.batch;
-    if (all <= std::min(8, most[3]) && kb >= 16) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream);
-    if (all <= most[2] && kb >= 8) return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream);
-    if (all <= most[1] && kb >= 4) return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream);
-  }
-  // Rounds of tiles times the time of one (units of 10 ns: a k-block of a pair's
-  // tile, of a lone CTA's, and what starts and ends a tile).
-  const int64_t n = kBatched ? 1 : p.batch;
+  const int64_t n = kBatched ? 1 : p.batch, kb = cdiv(p.K, 64) * p.segs;
+  const int64_t small = tiles(cdiv(p.M, 128), cdiv(p.N, Lone<kEpi>::kOutN)) * n;
   const int64_t big = tiles(cdiv(p.M, 256), cdiv(p.N, Pair<kEpi>::kOutN)) * n;
-  const int64_t pairs = h->max_pairs > 0 ? cdiv(big, h->max_pairs) * (33 * kb + 500) : INT64_MAX;
-  return pairs <= cdiv(small * n, h->num_sms) * (27 * kb + 400) ? launch_fused<Pair<kEpi>>(h, p, a, c, d, stream)
-                                                                 : launch_fused<Lone<kEpi>>(h, p, a, c, d, stream);
+  const int* most = h->max_split;
+  enum { kPairs, kPairs2, kLone, kLone2, kLone4, kLone8, kForms };
+  constexpr int64_t kNever = INT64_MAX;
+  const int64_t cost[kForms] = {
+      h->max_pairs > 0 ? cdiv(big, h->max_pairs) * (33 * kb + 500) : kNever,
+      h->max_twos > 0 && kb >= 4 ? cdiv(big, h->max_twos) * (33 * cdiv(kb, 2) + 700) : kNever,
+      cdiv(small, h->num_sms) * (27 * kb + 400),
+      small <= most[1] && kb >= 4 ? 27 * cdiv(kb, 2) + 550 : kNever,
+      small <= most[2] && kb >= (kBatched ? 4 : 8) ? 27 * cdiv(kb, 4) + 550 : kNever,
+      !kBatched && small <= std::min(8, most[3]) && kb >= 16 ? 27 * cdiv(kb, 8) + 550 : kNever};
+  switch (static_cast<int>(std::min_element(cost, cost + kForms) - cost)) {
+    case kPairs: return launch_fused<Pair<kEpi>>(h, p, a, c, d, stream);
+    case kPairs2: return launch_fused<TwoPairs<kEpi>>(h, p, a, c, d, stream);
+    case kLone2:
+      if constexpr (kBatched)
+        if (small * p.batch > most[1]) return launch_fused<Lone<kEpi, 1, 2>>(h, p, a, c, d, stream);
+      return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream);
+    case kLone4:
+      if constexpr (kBatched)
+        if (small * p.batch > most[2]) return launch_fused<Lone<kEpi, 1, 4>>(h, p, a, c, d, stream);
+      return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream);
+    case kLone8:
+      if constexpr (!kBatched) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream);
+      [[fallthrough]];
+    default: return launch_fused<Lone<kEpi>>(h, p, a, c, d, stream);
+  }
 }
 
 // out = A B^T, rounded to 16 bits.
@@ -484,7 +496,8 @@ gemm_status_t gemm_ops_create(gemm_ops_t* out, int device) {
       !set_attr<Pair<kEpiSplit>>() || !set_attr<Pair<kEpiSplitSym>>() || !set_attr<Lone<kEpiStore>>() ||
       !set_attr<Lone<kEpiGlu>>() || !set_attr<Lone<kEpiGluBwd>>() || !set_attr<Lone<kEpiSplit>>() ||
       !set_attr<Lone<kEpiSplitSym>>() ||
-      !set_split_attr<2>() || !set_split_attr<4>() || !set_split_attr<8>() ||
+      !set_attr<TwoPairs<kEpiStore>>() || !set_attr<TwoPairs<kEpiGlu>>() || !set_attr<TwoPairs<kEpiGluBwd>>() ||
+      !set_attr<TwoPairs<kEpiSplit>>() || !set_attr<TwoPairs<kEpiSplitSym>>() || !set_split_attr<2>() || !set_split_attr<4>() || !set_split_attr<8>() ||
       !set_stream_attr<kW16, false>() || !set_stream_attr<kW16, true>() ||
       !set_stream_attr<kW4G32, false>() || !set_stream_attr<kW4G32, true>() ||
       !set_stream_attr<kW4G64, false>() || !set_stream_attr<kW4G64, true>() ||
@@ -498,6 +511,9 @@ gemm_status_t gemm_ops_create(gemm_ops_t* out, int device) {
   h->max_pairs = std::min({max_clusters<Pair<kEpiStore>>(), max_clusters<Pair<kEpiGlu>>(),
                            max_clusters<Pair<kEpiGluBwd>>(), max_clusters<Pair<kEpiSplit>>(),
                            max_clusters<Pair<kEpiSplitSym>>()});
+  h->max_twos = std::min({max_clusters<TwoPairs<kEpiStore>>(), max_clusters<TwoPairs<kEpiGlu>>(),
+                          max_clusters<TwoPairs<kEpiGluBwd>>(), max_clusters<TwoPairs<kEpiSplit>>(),
+                          max_clusters<TwoPairs<kEpiSplitSym>>()});
   h->max_split[1] = max_clusters<Lone<kEpiStore, 2>>();
   h->max_split[2] = max_clusters<Lone<kEpiStore, 4>>();
   h->max_split[3] = max_clusters<Lone<kEpiStore, 8>>();
