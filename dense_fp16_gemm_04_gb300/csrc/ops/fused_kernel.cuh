@@ -35,9 +35,10 @@
 //
 // Units (a CTA with a 128-row tile, or a pair of CTAs with a 256-row one) are
 // persistent and take tiles round robin.  Inside a CTA: warp 0 loads A and
-// warp 6 loads B (TMA, 128-byte swizzle, a ring of kStages k-blocks), warp 1
-// issues tcgen05.mma, warps 2-5 run the epilogue of the tile before (the
-// accumulator is double-buffered in TMEM).  Bounded waits as in
+// warp 2 or 6 loads B (TMA, 128-byte swizzle, a ring of kStages k-blocks), warp 1
+// issues tcgen05.mma, warps 4 and on run the epilogue of the tile before (the
+// accumulator is double-buffered in TMEM): one or two warps to each quarter of
+// its rows, taking its 64-column chunks in turn.  Bounded waits as in
 // ../gemm_kernel.cuh: a wait that outlives the timeout records its site and
 // every role leaves.
 #pragma once
@@ -105,7 +106,12 @@ struct FusedCfg {
   static constexpr int kBRows = kBN / kCtas;
   static constexpr int kABytes = kBM * kBK * 2;
   static constexpr int kBBytes = kBRows * kBK * 2;
-  static constexpr int kEpiWarps = 4;
+  // Eight epilogue warps where few k-blocks make the epilogue the bound (weight
+  // gradients of 1000 tokens: -5%); four where K is three times as long and the
+  // power cap sets the speed (update of 4096 x 8192: eight cost 2%).
+  static constexpr int kEpiWarps = kEpi == kEpiSplit || kEpi == kEpiSplitSym ? 4 : 8;
+  static constexpr int kGroups = kEpiWarps / 4;  // warps per quarter of the rows
+  static constexpr int kWarpB = kSplit > 1 ? 6 : 2;  // loads B
   static constexpr int kBufBytes = 32 * 128;
   static constexpr int kOffA = 0;
   static constexpr int kOffB = kStages * kABytes;
@@ -117,7 +123,8 @@ struct FusedCfg {
   static constexpr int kSmemBytes = kOffAbort + 4 + 1024;  // + slack to align the base
   static constexpr int kAccBufs = kParts > 1 ? 1 : 2;  // tiles in tensor memory
   static constexpr int kTmemCols = kAccBufs * kParts * kBN;
-  static constexpr int kThreads = 256;
+  // Split clusters end in an epilogue of all eight warps; else warps 4 and on.
+  static constexpr int kThreads = kSplit > 1 ? 256 : 128 + 32 * kEpiWarps;
   static constexpr uint32_t kIdesc = ptx::idesc_f16(kTileM, kBN, true);
   static_assert(kSmemBytes <= 232448, "exceeds 227 KB of shared memory per CTA");
   static_assert(kOutN % 64 == 0, "the epilogue works on 64-column chunks");
@@ -495,7 +502,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffSlot);
 
-  if (warp == 0 || warp == 6) {
+  if (warp == 0 || warp == Cfg::kWarpB) {
     // ------------------------------------------------------- TMA producers --
     const bool is_a = warp == 0;
     const CUtensorMap* tm = is_a ? &tmA : &tmB;
@@ -661,12 +668,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       __syncwarp();
       wait_bar_warp<kPair>(bar_mma_done, 0u, w, kSiteMmaDone, -1, /*honor_abort=*/false);
     }
-  } else if (Cfg::kSplit == 1 && warp >= 2 && warp < 2 + Cfg::kEpiWarps) {
+  } else if (Cfg::kSplit == 1 && warp >= 4) {
     // ------------------------------------------------------------ epilogue --
     ptx::griddep_wait();  // reads S, g and u; writes the outputs
     const int q = warp & 3;  // this warp may touch TMEM lanes 32q .. 32q+31 only
+    const int group = (warp - 4) >> 2;  // which of the two warps of quarter q
     const uint32_t stage_base =
-        sb + Cfg::kOffEpi + static_cast<uint32_t>(q * Cfg::kEpiBufs * Cfg::kBufBytes);
+        sb + Cfg::kOffEpi + static_cast<uint32_t>((warp - 4) * Cfg::kEpiBufs * Cfg::kBufBytes);
     const uint32_t tempty_bar0 = kPair ? ptx::mapa(bar_tempty(0), leader) : bar_tempty(0);
     const bool bf16 = args.bf16 != 0;
     uint32_t next_buf = 0, used = 0;
@@ -745,11 +753,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         }
       };
       constexpr int kChunks = Cfg::kOutN / 64;
+      if (group >= kChunks) release_tmem();
 #pragma unroll 1
-      for (int c = 0; c < kChunks; ++c) {
+      for (int c = group; c < kChunks; c += Cfg::kGroups) {
         const int32_t col0 = wi.nb * Cfg::kOutN + c * 64;
         const bool in = row0 < args.M && col0 < args.N;
-        const bool last = c == kChunks - 1;
+        const bool last = c + Cfg::kGroups >= kChunks;
         if constexpr (Cfg::kEpi == kEpiStore) {
           uint32_t v0[32], v1[32], packed[32];
           ptx::tmem_ld_32x32b_x32(t_row + c * 64, v0);

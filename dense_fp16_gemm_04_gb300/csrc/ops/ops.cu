@@ -41,14 +41,17 @@ constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
 constexpr int64_t kMaxStreamTokens = 16;  // tokens of the streaming products of 16-bit weights
 constexpr int kGroupM = 8;
 
+// Staging buffers of an epilogue warp: 64 KB in all beside five stages.
+constexpr int epi_bufs(int epi) { return epi == kEpiSplit || epi == kEpiSplitSym ? 4 : 2; }
+
 // Tile configurations: a pair of CTAs on 256 x 256 sums, or one CTA on
 // 128 x 128 for problems of few tiles.
 template <int kEpi>
-using Pair = FusedCfg<2, 256, kEpi == kEpiStore ? 6 : 5, kEpi, kEpi == kEpiStore ? 2 : 4>;
+using Pair = FusedCfg<2, 256, kEpi == kEpiStore ? 6 : 5, kEpi, kEpi == kEpiStore ? 1 : epi_bufs(kEpi)>;
 template <int kEpi>
-using TwoPairs = FusedCfg<2, 256, 5, kEpi, 4, 2>;  // one tile, half of its k-blocks each
+using TwoPairs = FusedCfg<2, 256, 5, kEpi, epi_bufs(kEpi), 2>;  // one tile, half of its k-blocks each
 template <int kEpi, int kSplit = 1, int kParts = 1>
-using Lone = FusedCfg<1, 128, 5, kEpi, 4, kSplit, kParts>;
+using Lone = FusedCfg<1, 128, 5, kEpi, epi_bufs(kEpi), kSplit, kParts>;
 
 struct DeviceGuard {
   int prev = -1;
