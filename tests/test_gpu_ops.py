@@ -591,3 +591,23 @@ def test_dependent_calls_back_to_back(g):
     want = chain(True)
     for _ in range(3):
         assert torch.equal(chain(False), want)
+
+
+def test_example_trains_and_serves(g):
+    """examples/gated_block.py: the loss falls, and the 4-bit block answers like
+    the 16-bit one but for the rounding of its weights."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "gated_block.py")
+    spec = importlib.util.spec_from_file_location("gated_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    losses, w_in, w_down = ex.train(steps=40, tokens=512, dim=128, hidden=256)
+    assert torch.isfinite(losses).all() and losses[-1] < 0.5 * losses[0]
+    x = torch.randn(3, 128, device="cuda").to(w_in.dtype)
+    served = ex.W4Block(w_in, w_down)
+    h, eh, _, _ = gated_ref(x, w4_ref(*served.w_in), "silu", torch.float16)
+    eh = eh + U[torch.float16] * (h.abs() + eh) + TINY[torch.float16]
+    wd = w4_ref(*served.w_down)
+    check(served(x), h @ wd.t(), eh @ wd.abs().t() + sum_eps(256) * ((h.abs() + eh) @ wd.abs().t()),
+          torch.float16, "served")

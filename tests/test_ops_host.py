@@ -1,0 +1,103 @@
+"""Host-side checks of the operators: the header compiles as C99 and every
+function it declares is exported, null handles and tensors off the GPU are
+refused, and quantised codes decode to the nearest levels.  No kernel is
+launched."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+import dense_fp16_gemm_04_gb300 as g
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "gemm_ops.h")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    g.build()
+    return g.load()
+
+
+def declared():
+    return re.findall(r"GEMM_API\s+[\w\s\*]+?\b(gemm_\w+)\s*\(", open(HEADER).read())
+
+
+def test_header_compiles_as_c99(tmp_path):
+    src = tmp_path / "h.c"
+    src.write_text('#include "gemm_ops.h"\nint main(void) { return (int)GEMM_ACT_SILU; }\n')
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", "-I",
+                    os.path.join(ROOT, "include"), "-c", str(src), "-o", str(tmp_path / "h.o")], check=True)
+
+
+def test_every_declared_function_is_exported(lib):
+    names = declared()
+    assert {"gemm_ops_create", "gemm_gated_ffn", "gemm_gated_ffn_backward", "gemm_w4_linear",
+            "gemm_w4_gated", "gemm_orthogonalize"} <= set(names)
+    raw = ctypes.CDLL(g.LIB_PATH)
+    assert [n for n in names if not hasattr(raw, n)] == []
+
+
+def test_null_handles_are_refused(lib):
+    vp = ctypes.c_void_p
+    assert lib.gemm_ops_create(None, 0) == 1
+    assert lib.gemm_ops_destroy(None) == 0
+    assert lib.gemm_ops_check_error(None) == 1
+    assert lib.gemm_ops_set_watchdog(None, 0, -1) == 1
+    assert lib.gemm_ops_launch_count(None) == 0
+    i64, z = ctypes.c_int64, ctypes.c_size_t
+    for name, n_sizes in (("gemm_gated_ffn_workspace", 3), ("gemm_gated_ffn_backward_workspace", 3),
+                          ("gemm_orthogonalize_workspace", 3)):
+        fn = getattr(lib, name)
+        fn.restype = z
+        assert fn(vp(), *[i64(8)] * n_sizes) == 0
+    p, l, s, i = vp(), i64(8), z(0), ctypes.c_int(0)
+    assert lib.gemm_gated_ffn(p, p, l, p, l, p, l, p, l, p, p, s, l, l, l, i, i, p) == 1
+    assert lib.gemm_gated_ffn_backward(p, p, l, p, l, p, l, p, l, p, p, l, p, p, p, s, l, l, l, i, i, p) == 1
+    assert lib.gemm_w4_linear(p, p, l, p, p, p, p, l, p, s, l, l, l, i64(32), i, p) == 1
+    assert lib.gemm_w4_gated(p, p, l, p, p, p, p, l, p, s, l, l, l, i64(32), i, i, p) == 1
+
+
+def test_cpu_tensors_are_refused(lib):
+    x = torch.zeros(4, 64, dtype=torch.float16)
+    w_in, w_down = torch.zeros(256, 64, dtype=torch.float16), torch.zeros(64, 128, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        g.gated_ffn(x, w_in, w_down)
+    with pytest.raises(ValueError):
+        g.gated_ffn_backward(x, x, w_in, w_down, torch.zeros(4, 256, dtype=torch.float16))
+    with pytest.raises(ValueError):
+        g.w4_linear(x, torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.float16))
+    with pytest.raises(ValueError):
+        g.orthogonalize(torch.zeros(4, 4))
+
+
+@pytest.mark.parametrize("zero_point", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 256])
+def test_quantised_codes_are_the_nearest_levels(group, zero_point):
+    """Every code is the best of the sixteen for its group's scale and zero point
+    (among equally near ones, any), and a group's ends are reached."""
+    gen = torch.Generator().manual_seed(group)
+    w = torch.randn(6, 512, generator=gen).to(torch.float16)
+    codes, scales, zeros = g.w4_quantize(w, group, zero_point)
+    assert codes.shape == (6, 256) and codes.dtype == torch.uint8
+    assert scales.shape == (6, 512 // group) and scales.dtype == w.dtype
+    assert (zeros is None) == (not zero_point)
+    q = torch.stack((codes & 15, codes >> 4), -1).flatten(1).double()
+    z = (zeros.double() if zero_point else torch.full_like(scales, 8).double()).repeat_interleave(group, 1)
+    s = scales.double().repeat_interleave(group, 1)
+    err = ((q - z) * s - w.double()).abs()
+    levels = ((torch.arange(16).double().view(16, 1, 1) - z) * s - w.double()).abs().amin(0)
+    # Dividing by the scale in fp32 may take either of two levels a rounding apart.
+    assert (err <= levels + 16 * s * 2.0 ** -23).all()
+
+
+def test_quantise_refusals():
+    w = torch.zeros(4, 96, dtype=torch.float16)
+    for group in (16, 48, 64):
+        with pytest.raises(ValueError):
+            g.w4_quantize(w, group)
+    codes, scales, _ = g.w4_quantize(w, 32)
+    assert (codes == 0x88).all() and (scales == 0).all()
