@@ -42,10 +42,12 @@ __device__ __forceinline__ void act_both(int32_t act, float g, float& a, float& 
   }
   const bool silu = act == kActSilu;
   const float p = silu ? g : g * fmaf(kGeluB * g, g, kGeluA);
-  const float dp = silu ? 1.0f : fmaf(3.0f * kGeluB * g, g, kGeluA);
   const float s = sigmoid(p);
   a = g * s;
-  da = fmaf(a * dp, 1.0f - s, s);
+  // From |g| = 64 on, GELU's s is 0 or 1: p' must not overflow there.
+  const float c = silu ? g : fminf(fmaxf(g, -64.0f), 64.0f);
+  const float dp = silu ? 1.0f : fmaf(3.0f * kGeluB * c, c, kGeluA);
+  da = fmaf(c * s * dp, 1.0f - s, s);
 }
 
 // Two fp32 values rounded to the nearest 16-bit ones, `lo` in the low half.

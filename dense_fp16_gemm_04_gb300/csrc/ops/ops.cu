@@ -288,12 +288,10 @@ struct StreamPlan {
 
 constexpr size_t kStreamSmem = 226 * 1024;
 
-// 8-column tiles per CTA: 1, 2 or 4 (16-bit weights and whole groups: 8 tokens
-// each, so two make the most a call is expected to have).
+// 8-column tiles per CTA.
 template <int kW>
 int stream_tiles(int64_t T) {
-  const int64_t n = cdiv(T, stream_tokens(kW));
-  return n <= 1 ? 1 : n <= 2 || stream_groups(kW) == 1 ? 2 : 4;
+  return T <= stream_tokens(kW) ? 1 : 2;
 }
 
 template <int kW, bool kGlu>
@@ -307,7 +305,7 @@ StreamPlan stream_plan(const gemm_ops_s* h, int64_t T, int64_t N, int64_t K) {
   p.ring = kStreamMaxRing;
   p.slices = std::max<int64_t>(1, std::min(h->num_sms / tiles, blocks / (2 * p.warps)));
   auto smem = [&] {  // the warps' sums, their blocks in flight, and x
-    return static_cast<size_t>(p.warps) * (2 * nt * 128 * sizeof(float) + p.ring * stream_slot_bytes(kW)) +
+    return static_cast<size_t>(p.warps) * (2 * 2 * nt * 128 * sizeof(float) + p.ring * stream_slot_bytes(kW)) +
            static_cast<size_t>(cdiv(blocks, p.slices)) * bk * held * 2 + 128;
   };
   while (p.ring > 2 && smem() > kStreamSmem) --p.ring;
@@ -344,10 +342,12 @@ typedef void (*StreamKernel)(const StreamArgs);
 
 template <int kW, bool kGlu>
 StreamKernel stream_variant(bool bf16, int nt) {
-  if (nt == 1) return bf16 ? stream_kernel<true, kW, kGlu, 1> : stream_kernel<false, kW, kGlu, 1>;
   if constexpr (stream_groups(kW) > 1)
-    if (nt == 4) return bf16 ? stream_kernel<true, kW, kGlu, 4> : stream_kernel<false, kW, kGlu, 4>;
-  return bf16 ? stream_kernel<true, kW, kGlu, 2> : stream_kernel<false, kW, kGlu, 2>;
+    return bf16 ? stream_kernel<true, kW, kGlu, 1> : stream_kernel<false, kW, kGlu, 1>;
+  else if (nt == 1)
+    return bf16 ? stream_kernel<true, kW, kGlu, 1> : stream_kernel<false, kW, kGlu, 1>;
+  else
+    return bf16 ? stream_kernel<true, kW, kGlu, 2> : stream_kernel<false, kW, kGlu, 2>;
 }
 
 // The products of a.cols columns; `a` is complete but for N and the up rows.
@@ -385,11 +385,34 @@ gemm_status_t stream_product(gemm_ops_s* h, StreamArgs a, bool bf16, cudaStream_
 template <int kW, bool kGlu>
 bool set_stream_attr() {
   for (bool bf16 : {false, true})
-    for (int nt : {1, 2, 4})
+    for (int nt : {1, 2})
       if (cudaFuncSetAttribute(stream_variant<kW, kGlu>(bf16, nt), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                kStreamSmem) != cudaSuccess)
         return false;
   return true;
+}
+
+// The forms of small groups for few tokens: see stream_kernel.cuh.
+constexpr int64_t kFewG32 = stream_tokens(kW4G32Few), kFewG64 = stream_tokens(kW4G64Few);
+
+template <bool kGlu>
+size_t w4_workspace(gemm_ops_s* h, int64_t T, int64_t N, int64_t K) {
+  if (!h || T <= 0 || N <= 0 || K <= 0 || K / 2 > kMaxStreamRow) return 0;
+  // Whatever the groups.
+  return std::max({T <= kFewG32 ? stream_partial_bytes<kW4G32Few, kGlu>(h, T, N, K)
+                                : stream_partial_bytes<kW4G32, kGlu>(h, T, N, K),
+                   T <= kFewG64 ? stream_partial_bytes<kW4G64Few, kGlu>(h, T, N, K)
+                                : stream_partial_bytes<kW4G64, kGlu>(h, T, N, K),
+                   stream_partial_bytes<kW4G128, kGlu>(h, T, N, K)});
+}
+
+template <bool kGlu>
+gemm_status_t w4_product(gemm_ops_s* h, const StreamArgs& a, int64_t group, bool bf16, cudaStream_t s) {
+  if (group == 32)
+    return a.T <= kFewG32 ? stream_product<kW4G32Few, kGlu>(h, a, bf16, s) : stream_product<kW4G32, kGlu>(h, a, bf16, s);
+  if (group == 64)
+    return a.T <= kFewG64 ? stream_product<kW4G64Few, kGlu>(h, a, bf16, s) : stream_product<kW4G64, kGlu>(h, a, bf16, s);
+  return stream_product<kW4G128, kGlu>(h, a, bf16, s);
 }
 
 template <class Cfg>
@@ -504,7 +527,9 @@ gemm_status_t gemm_ops_create(gemm_ops_t* out, int device) {
       !set_stream_attr<kW16, false>() || !set_stream_attr<kW16, true>() ||
       !set_stream_attr<kW4G32, false>() || !set_stream_attr<kW4G32, true>() ||
       !set_stream_attr<kW4G64, false>() || !set_stream_attr<kW4G64, true>() ||
-      !set_stream_attr<kW4G128, false>() || !set_stream_attr<kW4G128, true>())
+      !set_stream_attr<kW4G128, false>() || !set_stream_attr<kW4G128, true>() ||
+      !set_stream_attr<kW4G32Few, false>() || !set_stream_attr<kW4G32Few, true>() ||
+      !set_stream_attr<kW4G64Few, false>() || !set_stream_attr<kW4G64Few, true>())
     return GEMM_ERR_CUDA;
   gemm_ops_s* h = new (std::nothrow) gemm_ops_s();
   if (!h) return GEMM_ERR_OOM;
@@ -716,17 +741,8 @@ gemm_status_t gemm_gated_ffn_backward(gemm_ops_t h, const void* dy, int64_t lddy
   return product(h, pi, {dw_in, F, D, D, 2, F * D}, s);
 }
 
-static size_t w4_workspace(gemm_ops_t h, int64_t T, int64_t N, int64_t K, bool gated) {
-  if (!h || T <= 0 || N <= 0 || K <= 0 || K / 2 > kMaxStreamRow) return 0;
-  // Whatever the groups.
-  return gated ? std::max({stream_partial_bytes<kW4G32, true>(h, T, N, K), stream_partial_bytes<kW4G64, true>(h, T, N, K),
-                           stream_partial_bytes<kW4G128, true>(h, T, N, K)})
-               : std::max({stream_partial_bytes<kW4G32, false>(h, T, N, K), stream_partial_bytes<kW4G64, false>(h, T, N, K),
-                           stream_partial_bytes<kW4G128, false>(h, T, N, K)});
-}
-
 size_t gemm_w4_workspace(gemm_ops_t h, int64_t T, int64_t N, int64_t K, int32_t gated) {
-  return w4_workspace(h, T, N, K, gated != 0);
+  return gated ? w4_workspace<true>(h, T, N, K) : w4_workspace<false>(h, T, N, K);
 }
 
 static gemm_status_t w4_run(gemm_ops_t h, const void* x, int64_t ldx, const void* codes,
@@ -746,7 +762,7 @@ static gemm_status_t w4_run(gemm_ops_t h, const void* x, int64_t ldx, const void
   if (!aligned16(x) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 1) ||
       (reinterpret_cast<uintptr_t>(y) & 1))
     return GEMM_ERR_ALIGNMENT;
-  const size_t need = w4_workspace(h, T, N, K, gated);
+  const size_t need = gemm_w4_workspace(h, T, N, K, gated);
   if (workspace_bytes < need) return GEMM_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return GEMM_ERR_ALIGNMENT;
   DeviceGuard g(h->device);
@@ -780,13 +796,7 @@ static gemm_status_t w4_run(gemm_ops_t h, const void* x, int64_t ldx, const void
   a.group_shift = shift;
   a.act = act;
   const bool bf16 = dtype == GEMM_BF16;
-  if (gated)
-    return group == 32   ? stream_product<kW4G32, true>(h, a, bf16, s)
-           : group == 64 ? stream_product<kW4G64, true>(h, a, bf16, s)
-                         : stream_product<kW4G128, true>(h, a, bf16, s);
-  return group == 32   ? stream_product<kW4G32, false>(h, a, bf16, s)
-         : group == 64 ? stream_product<kW4G64, false>(h, a, bf16, s)
-                       : stream_product<kW4G128, false>(h, a, bf16, s);
+  return gated ? w4_product<true>(h, a, group, bf16, s) : w4_product<false>(h, a, group, bf16, s);
 }
 
 gemm_status_t gemm_w4_linear(gemm_ops_t h, const void* x, int64_t ldx, const void* codes,

@@ -69,12 +69,14 @@ struct StreamArgs {
 constexpr int kStreamMaxWarps = 16;
 
 // How W is stored: 16-bit values, or codes whose groups are 32, 64, or 128 k
-// and more.
-enum StreamW : int { kW16 = 0, kW4G32 = 1, kW4G64 = 2, kW4G128 = 3 };
+// and more; the small ones kept apart in turn or (Few) by columns.
+enum StreamW : int { kW16 = 0, kW4G32 = 1, kW4G64 = 2, kW4G128 = 3, kW4G32Few = 4, kW4G64Few = 5 };
 
-// k of a block; groups of a block (1 for 16 bits); tokens of an 8-column tile.
+// k of a block; its groups that share a product's columns, and that take turns;
+// tokens of an 8-column tile.
 __host__ __device__ constexpr int stream_block_k(int w) { return w == kW16 ? 32 : 128; }
-__host__ __device__ constexpr int stream_groups(int w) { return w == kW4G32 ? 4 : w == kW4G64 ? 2 : 1; }
+__host__ __device__ constexpr int stream_groups(int w) { return w == kW4G32Few ? 4 : w == kW4G64Few ? 2 : 1; }
+__host__ __device__ constexpr int stream_turns(int w) { return w == kW4G32 ? 4 : w == kW4G64 ? 2 : 1; }
 __host__ __device__ constexpr int stream_tokens(int w) { return 8 / stream_groups(w); }
 // Rows of W a lane reads per tile (g, g + 8 of two 16-row halves); what a warp
 // keeps for a block in flight: 16 bytes of W a row and lane and, with codes,
@@ -124,6 +126,8 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   constexpr int kRows = kStreamRows;
   constexpr int kTileN = stream_tile(kGlu);
   constexpr int kGroups = stream_groups(kW);
+  constexpr int kTurns = stream_turns(kW);
+  constexpr int kInBlock = kGroups * kTurns;  // groups of a block
   constexpr int kTok = stream_tokens(kW);  // tokens per 8-column tile
   constexpr int kRed = kMT * kNT * 128;    // floats one warp leaves per tile
   extern __shared__ __align__(16) uint8_t stream_smem[];
@@ -137,10 +141,11 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   const int32_t b0 = static_cast<int32_t>(static_cast<int64_t>(blockIdx.y) * blocks / gridDim.y);
   const int32_t b1 = static_cast<int32_t>(static_cast<int64_t>(blockIdx.y + 1) * blocks / gridDim.y);
   const int32_t k_begin = b0 * kBK;
-  float* red = reinterpret_cast<float*>(stream_smem);  // [warp][kMT][kNT][row][column]
+  float* const red0 = reinterpret_cast<float*>(stream_smem);  // [2][warp][kMT][kNT][row][column]
+  float* red = red0;
   // [warp][slot]: [row of the lane][lane][16 B], then the scales and the zero
   // points [row][g][two words].
-  uint8_t* wr = reinterpret_cast<uint8_t*>(red + warps * kRed);
+  uint8_t* wr = reinterpret_cast<uint8_t*>(red0 + 2 * warps * kRed);
   uint8_t* xs = wr + warps * a.ring * kSlot;  // 128 bytes of zeros, then [block][i][token][t][16 B]
   const int32_t per_tile = (b1 - b0 + warps - 1) / warps;  // blocks of a tile per warp
   const int32_t tiles = (a.N + kTileN - 1) / kTileN;
@@ -162,14 +167,11 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   auto row_of = [&](int32_t tile, int i) {
     return static_cast<uint32_t>(min(tile * kTileN + g + 8 * i, a.N - 1));
   };
-  uint32_t w_off[kOwn], s_off[kOwn];
+  uint32_t w_off[kOwn], s_off = 0;  // s_off: of row i = t, whose scales this lane fetches
   auto rows_of_tile = [&]() {
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      const uint32_t n = row_of(load_tile, i);
-      w_off[i] = n * row_bytes;
-      s_off[i] = n * groups;
-    }
+    for (int i = 0; i < kOwn; ++i) w_off[i] = row_of(load_tile, i) * row_bytes;
+    if constexpr (kW4) s_off = row_of(load_tile, t & (kOwn - 1)) * groups;
   };
   rows_of_tile();
   const uint8_t* w_base[2] = {static_cast<const uint8_t*>(a.w), static_cast<const uint8_t*>(a.w) + a.up_w};
@@ -181,43 +183,50 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
                              static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s_base[1]))};
   const uint32_t z_low[2] = {static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z_base[0])),
                              static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z_base[1]))};
-  uint32_t sum_off[kOwn];  // s_off of the tile being summed
+  uint32_t sum_off[kOwn];  // rows times groups, of the tile being summed
 #pragma unroll
-  for (int i = 0; i < kOwn; ++i) sum_off[i] = s_off[i];
-  // This lane's two columns belong to groups j, j + 1 of a row (or to one
-  // group).  Their scales share an aligned word, and so do their zero points,
-  // unless rows hold an odd number of small groups or start off such a word:
-  // then they are read when they are needed.  A row's words are fetched by one
-  // lane each: two for four groups, else one.
-  const bool words = kGroups == 1 || (((groups | static_cast<uint32_t>(a.up_s)) & 1) == 0 &&
-                                      (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0 &&
-                                      (reinterpret_cast<uintptr_t>(a.zeros) & 1) == 0);
-  const bool fetches = kGroups == 4 ? t < 2 : t == 0;
-  const uint32_t s_lane = kRows * 512 + g * 8 + (kGroups == 4 ? (t & 1) * 4 : 0);
-  auto group_of = [&](int32_t b) {
-    return min((b * kBK >> a.group_shift) + (2 * t & (kGroups - 1)), static_cast<int32_t>(groups) - (kGroups > 1 ? 2 : 1));
+  for (int i = 0; i < kOwn; ++i) sum_off[i] = row_of(load_tile, i) * groups;
+  // The scales of a row's groups in one block share an aligned word (of 8 bytes
+  // for four), and so do its zero points, unless rows do not hold whole blocks
+  // or start off such a word: then they are read when they are needed.  Lane t
+  // fetches row t's: 32 rows with one instruction.
+  const bool words = kInBlock == 1 || (((groups | static_cast<uint32_t>(a.up_s)) & (kInBlock - 1)) == 0 &&
+                                       (reinterpret_cast<uintptr_t>(a.scales) & (2 * kInBlock - 1)) == 0 &&
+                                       (reinterpret_cast<uintptr_t>(a.zeros) & (kInBlock - 1)) == 0);
+  const uint16_t* s_mine = kGlu && t > 1 ? s_base[1] : s_base[0];
+  const uint8_t* z_mine = kGlu && t > 1 ? z_base[1] : z_base[0];
+  // The first group of block b, or of pair `pair` of its groups.
+  auto group_of = [&](int32_t b, int pair) {
+    return static_cast<uint32_t>(b * kBK >> a.group_shift) + (2u * pair & (kInBlock - 1));
   };
+  // Where a lane's 16 bytes of a row go: with groups in turn, the other lanes of
+  // the row read parts of them, and chunks change places so that the eight rows
+  // of such a read fall on different banks.
+  const uint32_t swap = kTurns > 1 ? (g & 2) | (g >> 2) : 0;
+  const uint32_t put = (g * 4 + (t ^ swap)) * 16;
   auto issue = [&](uint32_t slot) {
     const int32_t b = b0 + load_blk * warps + warp;
     if (b < b1) {
       const int32_t k0 = b * kBK;
       const uint32_t at = kW4 ? min(k0 + 32 * t, a.K - 32) >> 1 : 2 * min(k0 + 8 * t, a.K - 8);
-      const uint32_t dst = slot + lane * 16;
+      const uint32_t bytes = k0 + 8 * t < a.K ? 16 : 0;  // zeros past K: infinity times x's 0 is NaN
+      const uint32_t dst = slot + put;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i)
-        ptx::cp_async_16(dst + i * 512, w_base[kHalf * (i >> 1)] + (w_off[i & (kOwn - 1)] + at));
+      for (int i = 0; i < kRows; ++i) {
+        const void* src = w_base[kHalf * (i >> 1)] + (w_off[i & (kOwn - 1)] + at);
+        if constexpr (kW4)
+          ptx::cp_async_16(dst + i * 512, src);
+        else
+          ptx::cp_async_16(dst + i * 512, src, bytes);
+      }
       if constexpr (kW4) {
-        if (words && fetches) {
-          const uint32_t j = group_of(b);
-#pragma unroll
-          for (int i = 0; i < kRows; ++i)  // the aligned word lies in the same allocation
-            ptx::cp_async_4(slot + s_lane + i * 64, word_of(s_base[kHalf * (i >> 1)] + (s_off[i & (kOwn - 1)] + j)));
-          if (a.zeros) {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i)
-              ptx::cp_async_4(slot + s_lane + (kRows + i) * 64,
-                              word_of(z_base[kHalf * (i >> 1)] + (s_off[i & (kOwn - 1)] + j)));
-          }
+        if (words) {  // the aligned word lies in the same allocation
+          const uint32_t at = s_off + group_of(b, 0), dst = slot + kRows * 512 + t * 64 + g * 8;
+          if constexpr (kInBlock == 4)
+            ptx::cp_async_8(dst, s_mine + at);
+          else
+            ptx::cp_async_4(dst, word_of(s_mine + at));
+          if (a.zeros) ptx::cp_async_4(dst + kRows * 64, word_of(z_mine + at));
         }
       }
     }
@@ -266,7 +275,9 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
         if constexpr (kW4)  // pairs (x j, x j + 4), as the codes unpack
           o = make_uint4(__byte_perm(v[u].x, v[u].z, 0x5410), __byte_perm(v[u].x, v[u].z, 0x7632),
                          __byte_perm(v[u].y, v[u].w, 0x5410), __byte_perm(v[u].y, v[u].w, 0x7632));
-        const int i = kW4 ? ch & 3 : 0, l = kW4 ? ch >> 2 : ch;
+        // The product i and lane l that take this chunk.
+        const int i = kTurns == 4 ? ch >> 2 : kTurns == 2 ? (ch >> 3) * 2 + (ch & 1) : kW4 ? ch & 3 : 0;
+        const int l = kTurns == 4 ? ch & 3 : kTurns == 2 ? ch >> 1 & 3 : kW4 ? ch >> 2 : ch;
         *reinterpret_cast<uint4*>(xs + 128 + (((blk * (kPer / 4) + i) * tokens + tok[u]) * 4 + l) * 16) = o;
       }
     }
@@ -297,56 +308,80 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
     uint32_t xa[kNT];
 #pragma unroll
     for (int n = 0; n < kNT; ++n) xa[n] = xl[n] + rel * kWords * x_step[n];
-    uint4 wv[kRows];
+    // Word i of a row holds the codes of product i.
+    uint32_t wv[kRows][4];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) wv[i] = ptx::ld_shared_v4_u32(slot + i * 512 + lane * 16);
-    if constexpr (kW4) {
-      // Scales (two to a word) and zero points (two bytes) of this lane's
-      // columns in its rows.
-      uint32_t sv[kRows], zv[kRows];
-      const uint32_t j = group_of(b0 + rel);
-      if (words) {
+    for (int i = 0; i < kRows; ++i) {
+      if constexpr (kTurns == 1) {
+        const uint4 v = ptx::ld_shared_v4_u32(slot + i * 512 + put);
+        wv[i][0] = v.x, wv[i][1] = v.y, wv[i][2] = v.z, wv[i][3] = v.w;
+      } else if constexpr (kTurns == 2) {
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          sv[i] = ptx::ld_shared_u32(slot + s_lane + i * 64);
-          // A lone scale is the word's low or high half.
-          if (kGroups == 1) sv[i] >>= ((s_low[kHalf * (i >> 1)] + 2 * (sum_off[i & (kOwn - 1)] + j)) & 2) * 8;
-        }
-        if (a.zeros) {
-#pragma unroll
-          for (int i = 0; i < kRows; ++i)
-            zv[i] = ptx::ld_shared_u32(slot + s_lane + (kRows + i) * 64) >>
-                    ((z_low[kHalf * (i >> 1)] + sum_off[i & (kOwn - 1)] + j) & 3) * 8;
+        for (int s = 0; s < 2; ++s) {
+          const uint2 v = ptx::ld_shared_v2_u32(slot + i * 512 + g * 64 + ((2 * s + (t >> 1)) ^ swap) * 16 + (t & 1) * 8);
+          wv[i][2 * s] = v.x, wv[i][2 * s + 1] = v.y;
         }
       } else {
-        const uint32_t j0 = min(((b0 + rel) * kBK >> a.group_shift) + (2u * t & (kGroups - 1)), groups - 1);
-        const uint32_t j1 = min(j0 + 1, groups - 1);
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const uint32_t o = sum_off[i & (kOwn - 1)];
-          const uint16_t* sp = s_base[kHalf * (i >> 1)] + o;
-          const uint8_t* zp = z_base[kHalf * (i >> 1)] + o;
-          sv[i] = sp[j0] | static_cast<uint32_t>(sp[j1]) << 16;
-          if (a.zeros) zv[i] = zp[j0] | static_cast<uint32_t>(zp[j1]) << 8;
+        for (int s = 0; s < 4; ++s) wv[i][s] = ptx::ld_shared_u32(slot + i * 512 + g * 64 + (s ^ swap) * 16 + t * 4);
+      }
+    }
+    if constexpr (kW4) {
+      // Scales (two to a word) and zero points (two bytes) of a pair of groups.
+      constexpr int kPairs = kTurns == 4 ? 2 : 1;
+      uint32_t sv[kPairs][kRows], zv[kPairs][kRows];
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        const int pair = kGroups > 1 ? t : p;
+        const uint32_t j = group_of(b0 + rel, pair), at = slot + kRows * 512 + g * 8;
+        if (words) {
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            sv[p][i] = ptx::ld_shared_u32(at + i * 64 + (kInBlock == 4 ? (pair & 1) * 4 : 0));
+            // A lone scale is the word's low or high half.
+            if (kInBlock == 1) sv[p][i] >>= ((s_low[kHalf * (i >> 1)] + 2 * (sum_off[i & (kOwn - 1)] + j)) & 2) * 8;
+          }
+          if (a.zeros) {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+              zv[p][i] = ptx::ld_shared_u32(at + (kRows + i) * 64) >>
+                         ((z_low[kHalf * (i >> 1)] + sum_off[i & (kOwn - 1)] + j) & 3) * 8;
+          }
+        } else {
+          const uint32_t j0 = min(j, groups - 1), j1 = min(j0 + 1, groups - 1);
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const uint32_t o = sum_off[i & (kOwn - 1)];
+            const uint16_t* sp = s_base[kHalf * (i >> 1)] + o;
+            const uint8_t* zp = z_base[kHalf * (i >> 1)] + o;
+            sv[p][i] = sp[j0] | static_cast<uint32_t>(sp[j1]) << 16;
+            if (a.zeros) zv[p][i] = zp[j0] | static_cast<uint32_t>(zp[j1]) << 8;
+          }
         }
       }
       // -(O + z) is z's bits in the mantissa of -O.
-      float z0[kRows], z1[kRows];
+      float z0[kPairs][kRows], z1[kPairs][kRows];
       constexpr uint32_t kMinusO = kBf16 ? 0xc3000000u : 0xc2800000u;
       constexpr int kBit = kBf16 ? 16 : 17;
       if (a.zeros) {
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          z0[i] = __uint_as_float(ptx::and_or(zv[i] << kBit, 15u << kBit, kMinusO));
-          z1[i] = kGroups > 1 ? __uint_as_float(ptx::and_or(zv[i] << (kBit - 8), 15u << kBit, kMinusO)) : z0[i];
-        }
+        for (int p = 0; p < kPairs; ++p)
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            z0[p][i] = __uint_as_float(ptx::and_or(zv[p][i] << kBit, 15u << kBit, kMinusO));
+            z1[p][i] = kInBlock > 1 ? __uint_as_float(ptx::and_or(zv[p][i] << (kBit - 8), 15u << kBit, kMinusO))
+                                    : z0[p][i];
+          }
       } else {
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) z0[i] = z1[i] = __uint_as_float(kMinusO | 8u << kBit);
+        for (int p = 0; p < kPairs; ++p)
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) z0[p][i] = z1[p][i] = __uint_as_float(kMinusO | 8u << kBit);
       }
       float part[kMT][kNT][4], sx[kNT][4];  // sums of (O + q) x, and of x (in every row)
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
+        const bool first = i % (kWords / kTurns) == 0;  // of a group's, or of the block's
         uint4 xb[kNT];
 #pragma unroll
         for (int n = 0; n < kNT; ++n) {
@@ -356,7 +391,7 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
         constexpr uint32_t kOnes = kBf16 ? 0x3f803f80u : 0x3c003c00u;
 #pragma unroll
         for (int n = 0; n < kNT; ++n) {
-          if (i == 0)
+          if (first)
             ptx::mma_16816_zero<kBf16>(sx[n], kOnes, kOnes, kOnes, kOnes, xb[n].x, xb[n].y);
           else
             ptx::mma_16816<kBf16>(sx[n], kOnes, kOnes, kOnes, kOnes, xb[n].x, xb[n].y);
@@ -365,29 +400,32 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
 #pragma unroll
         for (int m = 0; m < kMT; ++m) {
           uint32_t p0[4], p1[4];
-          const uint4 w0 = wv[2 * m], w1 = wv[2 * m + 1];
-          offset_codes<kBf16>(i == 0 ? w0.x : i == 1 ? w0.y : i == 2 ? w0.z : w0.w, p0);
-          offset_codes<kBf16>(i == 0 ? w1.x : i == 1 ? w1.y : i == 2 ? w1.z : w1.w, p1);
+          offset_codes<kBf16>(wv[2 * m][i], p0);
+          offset_codes<kBf16>(wv[2 * m + 1][i], p1);
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
-            if (i == 0)
+            if (first)
               ptx::mma_16816_zero<kBf16>(part[m][n], p0[0], p1[0], p0[1], p1[1], xb[n].x, xb[n].y);
             else
               ptx::mma_16816<kBf16>(part[m][n], p0[0], p1[0], p0[1], p1[1], xb[n].x, xb[n].y);
             ptx::mma_16816<kBf16>(part[m][n], p0[2], p1[2], p0[3], p1[3], xb[n].z, xb[n].w);
           }
         }
-      }
+        if ((i + 1) % (kWords / kTurns) != 0) continue;
+        // The end of a group (by columns: of the groups of this lane's two).
+        const int turn = i / (kWords / kTurns), pair = turn / 2;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const float2 f = unpack16(kBf16, sv[i]);
-        const float f1 = kGroups == 1 ? f.x : f.y;
+        for (int r = 0; r < kRows; ++r) {
+          const float2 f = unpack16(kBf16, sv[pair][r]);
+          const float f0 = turn & 1 ? f.y : f.x, f1 = kGroups > 1 ? f.y : f0;
+          const float m0 = turn & 1 ? z1[pair][r] : z0[pair][r], m1 = kGroups > 1 ? z1[pair][r] : m0;
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-          float* c = acc[i >> 1][n] + 2 * (i & 1);
-          const float* p = part[i >> 1][n] + 2 * (i & 1);
-          c[0] = fmaf(f.x, fmaf(z0[i], sx[n][0], p[0]), c[0]);
-          c[1] = fmaf(f1, fmaf(z1[i], sx[n][1], p[1]), c[1]);
+          for (int n = 0; n < kNT; ++n) {
+            float* c = acc[r >> 1][n] + 2 * (r & 1);
+            const float* p = part[r >> 1][n] + 2 * (r & 1);
+            c[0] = fmaf(f0, fmaf(m0, sx[n][0], p[0]), c[0]);
+            c[1] = fmaf(f1, fmaf(m1, sx[n][1], p[1]), c[1]);
+          }
         }
       }
     } else {
@@ -396,17 +434,18 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
         const uint4 x = ptx::ld_shared_v4_u32(xa[n]);
 #pragma unroll
         for (int m = 0; m < kMT; ++m) {
-          const uint4 p = wv[2 * m], q = wv[2 * m + 1];
-          ptx::mma_16816<kBf16>(acc[m][n], p.x, q.x, p.y, q.y, x.x, x.y);
-          ptx::mma_16816<kBf16>(acc[m][n], p.z, q.z, p.w, q.w, x.z, x.w);
+          const uint32_t *p = wv[2 * m], *q = wv[2 * m + 1];
+          ptx::mma_16816<kBf16>(acc[m][n], p[0], q[0], p[1], q[1], x.x, x.y);
+          ptx::mma_16816<kBf16>(acc[m][n], p[2], q[2], p[3], q[3], x.z, x.w);
         }
       }
     }
   };
 
   auto finish_tile = [&]() {
-    // The warps' sums, in warp order.
-    __syncthreads();  // the last tile's have been read
+    // The warps' sums, in warp order.  Two tiles' places take turns: a thread
+    // that passes a tile's barrier has read the sums of the one before.
+    red = red0 + (red == red0 ? warps * kRed : 0);
 #pragma unroll
     for (int m = 0; m < kMT; ++m)
 #pragma unroll

@@ -611,3 +611,61 @@ def test_example_trains_and_serves(g):
     wd = w4_ref(*served.w_down)
     check(served(x), h @ wd.t(), eh @ wd.abs().t() + sum_eps(256) * ((h.abs() + eh) @ wd.abs().t()),
           torch.float16, "served")
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9, 16, 20])
+def test_w4_small_groups_at_every_count(g, T, group, zeros):
+    """Small groups are kept apart in one way for a token or two, in another for
+    more; an odd number of groups, and even ones that end inside a block of 128
+    or with it."""
+    for K in (7 * group, 30 * group):
+        for dt in DTYPES:
+            x, codes, scales, z = make_w4(T, 70, K, group, zeros, dt, seed=T)
+            w = w4_ref(codes, scales, z)
+            check(g.w4_linear(x, codes, scales, z), x.to(F64) @ w.t(), sum_eps(K) * (x.to(F64).abs() @ w.abs().t()),
+                  dt, "y")
+            h, eh, _, _ = gated_ref(x, w, "silu", dt)
+            check(g.w4_gated(x, codes, scales, z), h, eh, dt, "h")
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T", [1, 4, 7, 16])
+def test_w4_single_weights_are_exact(g, T, group):
+    """One-hot x, T columns at a time: every code meets its own scale and zero point."""
+    K, N = 384, 40
+    _, codes, scales, z = make_w4(1, N, K, group, True, torch.bfloat16, seed=T)
+    want = w4_ref(codes, scales, z).t().to(torch.bfloat16)
+    for x, y in zip(torch.eye(K, device="cuda", dtype=torch.bfloat16).split(T), want.split(T)):
+        assert torch.equal(g.w4_linear(x, codes, scales, z), y)
+
+
+@pytest.mark.parametrize("T", [2, 20])
+def test_ffn_infinite_weights_at_the_end_of_rows(g, T):
+    """Rows that end inside a block of 32: an infinite weight there gives
+    infinity, and does not meet the zeros beyond."""
+    D = F = 40
+    x = torch.ones(T, D, device="cuda", dtype=torch.float16)
+    w_in = torch.full((2 * F, D), 0.01, device="cuda", dtype=torch.float16)
+    w_down = torch.full((D, F), 0.01, device="cuda", dtype=torch.float16)
+    w_down[5, F - 1] = float("inf")
+    y = g.gated_ffn(x, w_in, w_down)
+    assert torch.isposinf(y[:, 5]).all() and torch.isfinite(y[:, :5]).all() and torch.isfinite(y[:, 6:]).all()
+    w_in[F + 3, D - 1] = float("inf")
+    _, gu = g.gated_ffn(x, w_in, w_down, save=True)
+    assert torch.isposinf(gu[:, F + 3]).all() and torch.isfinite(gu[:, :F + 3]).all() and torch.isfinite(gu[:, F + 4:]).all()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_ffn_backward_of_large_gates(g, act):
+    """Gates as large as the type holds: slopes 0 and 1, not NaN."""
+    T, D, F = 3, 8, 8
+    one = torch.ones(T, D, device="cuda", dtype=torch.bfloat16)
+    gu = torch.ones(T, 2 * F, device="cuda", dtype=torch.bfloat16)
+    gu[0, :F], gu[1, :F], gu[2, :F] = 1e30, -1e30, -3e38
+    w_in = torch.zeros(2 * F, D, device="cuda", dtype=torch.bfloat16)
+    w_in[:F] = 1
+    w_down = torch.eye(D, F, device="cuda", dtype=torch.bfloat16)
+    dx, _, _ = g.gated_ffn_backward(one, one, w_in, w_down, gu, act=act)
+    assert torch.equal(dx.float(), torch.tensor([[8.0], [0.0], [0.0]], device="cuda").expand(T, D))
