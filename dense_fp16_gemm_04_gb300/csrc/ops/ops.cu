@@ -306,7 +306,7 @@ StreamPlan stream_plan(const gemm_ops_s* h, int64_t T, int64_t N, int64_t K) {
   p.slices = std::max<int64_t>(1, std::min(h->num_sms / tiles, blocks / (2 * p.warps)));
   auto smem = [&] {  // the warps' sums, their blocks in flight, and x
     return static_cast<size_t>(p.warps) * (2 * 2 * nt * 128 * sizeof(float) + p.ring * stream_slot_bytes(kW)) +
-           static_cast<size_t>(cdiv(blocks, p.slices)) * bk * held * 2 + 128;
+           static_cast<size_t>(cdiv(blocks, p.slices)) * bk * held * 2 + kStreamHead;
   };
   while (p.ring > 2 && smem() > kStreamSmem) --p.ring;
   while (p.slices < blocks && smem() > kStreamSmem) ++p.slices;

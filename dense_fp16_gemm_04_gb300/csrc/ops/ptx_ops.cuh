@@ -119,10 +119,11 @@ __device__ __forceinline__ uint2 ld_shared_v2_u32(uint32_t addr) {
   return v;
 }
 
-// (w & mask) | bits.
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+// (w & kMask) | bits.
+template <uint32_t kMask>
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t bits) {
   uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "n"(kMask), "r"(bits));
   return r;
 }
 

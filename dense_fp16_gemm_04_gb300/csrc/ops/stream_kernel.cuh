@@ -86,29 +86,25 @@ __host__ __device__ constexpr int stream_slot_bytes(int w) {
   return kStreamRows * (32 * 16 + (w == kW16 ? 0 : 8 * 16));
 }
 constexpr int kStreamMaxRing = 4;
+constexpr int kStreamHead = 128 + 16;  // of x in shared memory
 __host__ __device__ constexpr int stream_tile(bool glu) { return glu ? 16 : 32; }  // columns of y
 
 // Eight codes to four pairs (code j, code j + 4) of O + q: a shift and one
 // and-or each.
 template <bool kBf16>
 __device__ __forceinline__ void offset_codes(uint32_t w, uint32_t (&p)[4]) {
+  constexpr uint32_t bits = kBf16 ? 0x43004300u : 0x54005400u;
   if constexpr (kBf16) {
-    p[0] = ptx::and_or(w, 0x000f000fu, 0x43004300u);
-    p[1] = ptx::and_or(w >> 4, 0x000f000fu, 0x43004300u);
-    p[2] = ptx::and_or(w >> 8, 0x000f000fu, 0x43004300u);
-    p[3] = ptx::and_or(w >> 12, 0x000f000fu, 0x43004300u);
+    p[0] = ptx::and_or<0x000f000fu>(w, bits);
+    p[1] = ptx::and_or<0x000f000fu>(w >> 4, bits);
+    p[2] = ptx::and_or<0x000f000fu>(w >> 8, bits);
+    p[3] = ptx::and_or<0x000f000fu>(w >> 12, bits);
   } else {
-    // In place: bits 4-7 of 64 (0x5400), or bits 0-3 of 1024 (0x6400) and
-    // 960 less, an exact difference on another pipe than the bit operations.
-    const uint32_t w8 = w >> 8;
-    const __half2 d = __half2half2(__ushort_as_half(0xe380));  // -960
-    uint32_t e0 = ptx::and_or(w, 0x000f000fu, 0x64006400u), e2 = ptx::and_or(w8, 0x000f000fu, 0x64006400u);
-    const __half2 h0 = __hadd2(*reinterpret_cast<__half2*>(&e0), d);
-    const __half2 h2 = __hadd2(*reinterpret_cast<__half2*>(&e2), d);
-    p[0] = *reinterpret_cast<const uint32_t*>(&h0);
-    p[1] = ptx::and_or(w, 0x00f000f0u, 0x54005400u);
-    p[2] = *reinterpret_cast<const uint32_t*>(&h2);
-    p[3] = ptx::and_or(w8, 0x00f000f0u, 0x54005400u);
+    const uint32_t w8 = w >> 8;  // shifts left run on another pipe than the bit operations
+    p[0] = ptx::and_or<0x00f000f0u>(w << 4, bits);
+    p[1] = ptx::and_or<0x00f000f0u>(w, bits);
+    p[2] = ptx::and_or<0x00f000f0u>(w8 << 4, bits);
+    p[3] = ptx::and_or<0x00f000f0u>(w8, bits);
   }
 }
 
@@ -146,12 +142,11 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   // [warp][slot]: [row of the lane][lane][16 B], then the scales and the zero
   // points [row][g][two words].
   uint8_t* wr = reinterpret_cast<uint8_t*>(red0 + 2 * warps * kRed);
-  uint8_t* xs = wr + warps * a.ring * kSlot;  // 128 bytes of zeros, then [block][i][token][t][16 B]
-  const int32_t per_tile = (b1 - b0 + warps - 1) / warps;  // blocks of a tile per warp
+  uint8_t* xs = wr + warps * a.ring * kSlot;  // kStreamHead bytes (zeros, then ones), then [block][i][token][t][16 B]
+  const int32_t per_tile = (b1 - b0 - warp + warps - 1) / warps;  // this warp's blocks of a tile
   const int32_t tiles = (a.N + kTileN - 1) / kTileN;
   const int32_t my_tiles = (tiles - static_cast<int32_t>(blockIdx.x) + static_cast<int32_t>(gridDim.x) - 1) /
                            static_cast<int32_t>(gridDim.x);
-  const int32_t items = my_tiles * per_tile;
 
   // The warp's blocks in order: block load_blk of tile load_tile.  A lane reads
   // rows i = 0 .. 3: g and g + 8 of the tile's first half, then of its second.
@@ -159,7 +154,7 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   // offsets: the host cuts larger matrices).  Rows past N read the last row,
   // and k past K the last codes: the sums of the former are not stored, x is 0
   // in the latter.
-  int32_t load_tile = blockIdx.x, load_blk = 0;
+  int32_t load_tile = blockIdx.x, load_blk = 0, to_load = my_tiles * per_tile;
   const uint32_t slot0 = ptx::smem_addr(wr) + warp * (a.ring * kSlot);
   const uint32_t groups = kW4 ? a.K >> a.group_shift : 0;
   const uint32_t row_bytes = static_cast<uint32_t>(a.ldw) * (kW4 ? 1 : 2);
@@ -206,30 +201,29 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   const uint32_t put = (g * 4 + (t ^ swap)) * 16;
   auto issue = [&](uint32_t slot) {
     const int32_t b = b0 + load_blk * warps + warp;
-    if (b < b1) {
-      const int32_t k0 = b * kBK;
-      const uint32_t at = kW4 ? min(k0 + 32 * t, a.K - 32) >> 1 : 2 * min(k0 + 8 * t, a.K - 8);
-      const uint32_t bytes = k0 + 8 * t < a.K ? 16 : 0;  // zeros past K: infinity times x's 0 is NaN
-      const uint32_t dst = slot + put;
+    const int32_t k0 = b * kBK;
+    const uint32_t at = kW4 ? min(k0 + 32 * t, a.K - 32) >> 1 : 2 * min(k0 + 8 * t, a.K - 8);
+    const uint32_t bytes = k0 + 8 * t < a.K ? 16 : 0;  // zeros past K: infinity times x's 0 is NaN
+    const uint32_t dst = slot + put;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const void* src = w_base[kHalf * (i >> 1)] + (w_off[i & (kOwn - 1)] + at);
-        if constexpr (kW4)
-          ptx::cp_async_16(dst + i * 512, src);
+    for (int i = 0; i < kRows; ++i) {
+      const void* src = w_base[kHalf * (i >> 1)] + (w_off[i & (kOwn - 1)] + at);
+      if constexpr (kW4)
+        ptx::cp_async_16(dst + i * 512, src);
+      else
+        ptx::cp_async_16(dst + i * 512, src, bytes);
+    }
+    if constexpr (kW4) {
+      if (words) {  // the aligned word lies in the same allocation
+        const uint32_t at = s_off + group_of(b, 0), dst = slot + kRows * 512 + t * 64 + g * 8;
+        if constexpr (kInBlock == 4)
+          ptx::cp_async_8(dst, s_mine + at);
         else
-          ptx::cp_async_16(dst + i * 512, src, bytes);
-      }
-      if constexpr (kW4) {
-        if (words) {  // the aligned word lies in the same allocation
-          const uint32_t at = s_off + group_of(b, 0), dst = slot + kRows * 512 + t * 64 + g * 8;
-          if constexpr (kInBlock == 4)
-            ptx::cp_async_8(dst, s_mine + at);
-          else
-            ptx::cp_async_4(dst, word_of(s_mine + at));
-          if (a.zeros) ptx::cp_async_4(dst + kRows * 64, word_of(z_mine + at));
-        }
+          ptx::cp_async_4(dst, word_of(s_mine + at));
+        if (a.zeros) ptx::cp_async_4(dst + kRows * 64, word_of(z_mine + at));
       }
     }
+    --to_load;
     if (++load_blk == per_tile) {
       load_blk = 0;
       load_tile += gridDim.x;
@@ -240,7 +234,7 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   for (int i = 0; i < a.ring; ++i) {
-    if (i < items) issue(slot0 + i * kSlot);
+    if (to_load > 0) issue(slot0 + i * kSlot);
     ptx::cp_async_commit();
   }
   // Stage x: 16-byte chunks of eight k, in the order the products read them
@@ -249,7 +243,7 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   {
     constexpr int kPer = kBK / 8;  // chunks per block
     const int32_t chunks = (b1 - b0) * kPer;
-    if (threadIdx.x < 8) *reinterpret_cast<uint4*>(xs + 16 * threadIdx.x) = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x < 36) reinterpret_cast<uint32_t*>(xs)[threadIdx.x] = threadIdx.x < 32 ? 0u : kBf16 ? 0x3f803f80u : 0x3c003c00u;
     int32_t next_tok = 0, next_c = threadIdx.x;  // chunk next_c of token next_tok
     while (next_tok < tokens) {
       uint4 v[4];
@@ -278,7 +272,7 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
         // The product i and lane l that take this chunk.
         const int i = kTurns == 4 ? ch >> 2 : kTurns == 2 ? (ch >> 3) * 2 + (ch & 1) : kW4 ? ch & 3 : 0;
         const int l = kTurns == 4 ? ch & 3 : kTurns == 2 ? ch >> 1 & 3 : kW4 ? ch >> 2 : ch;
-        *reinterpret_cast<uint4*>(xs + 128 + (((blk * (kPer / 4) + i) * tokens + tok[u]) * 4 + l) * 16) = o;
+        *reinterpret_cast<uint4*>(xs + kStreamHead + (((blk * (kPer / 4) + i) * tokens + tok[u]) * 4 + l) * 16) = o;
       }
     }
   }
@@ -290,7 +284,7 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   for (int n = 0; n < kNT; ++n) {
     const int32_t tok = n * kTok + g / kGroups;
     const bool mine = tok < tokens && t * kGroups / 4 == g % kGroups;
-    xl[n] = ptx::smem_addr(xs) + (mine ? 128 + tok * 64 + t * 16 : lane % 8 * 16);
+    xl[n] = ptx::smem_addr(xs) + (mine ? kStreamHead + tok * 64 + t * 16 : lane % 8 * 16);
     x_step[n] = mine ? tokens * 64 : 0;
   }
 
@@ -301,9 +295,13 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-  int32_t tile = blockIdx.x, blk = 0;
+  int32_t tile = blockIdx.x;
+  // The matrix of ones, from shared memory: the compiler makes a constant anew
+  // for every product.  (Four groups and two tiles have no registers to hold it.)
+  constexpr uint32_t kOnes = kBf16 ? 0x3f803f80u : 0x3c003c00u;
+  uint4 ones = make_uint4(kOnes, kOnes, kOnes, kOnes);
+  if constexpr (kW4 && kTurns * kNT < 8) ones = ptx::ld_shared_v4_u32(ptx::smem_addr(xs) + 128);
   auto consume = [&](uint32_t slot, int32_t rel) {  // block b0 + rel
-    if (rel >= b1 - b0) return;
     constexpr int kWords = kBK / 32;
     uint32_t xa[kNT];
 #pragma unroll
@@ -368,8 +366,8 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
         for (int p = 0; p < kPairs; ++p)
 #pragma unroll
           for (int i = 0; i < kRows; ++i) {
-            z0[p][i] = __uint_as_float(ptx::and_or(zv[p][i] << kBit, 15u << kBit, kMinusO));
-            z1[p][i] = kInBlock > 1 ? __uint_as_float(ptx::and_or(zv[p][i] << (kBit - 8), 15u << kBit, kMinusO))
+            z0[p][i] = __uint_as_float(ptx::and_or<15u << kBit>(zv[p][i] << kBit, kMinusO));
+            z1[p][i] = kInBlock > 1 ? __uint_as_float(ptx::and_or<15u << kBit>(zv[p][i] << (kBit - 8), kMinusO))
                                     : z0[p][i];
           }
       } else {
@@ -388,14 +386,13 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
           xb[n] = ptx::ld_shared_v4_u32(xa[n]);
           xa[n] += x_step[n];
         }
-        constexpr uint32_t kOnes = kBf16 ? 0x3f803f80u : 0x3c003c00u;
 #pragma unroll
         for (int n = 0; n < kNT; ++n) {
           if (first)
-            ptx::mma_16816_zero<kBf16>(sx[n], kOnes, kOnes, kOnes, kOnes, xb[n].x, xb[n].y);
+            ptx::mma_16816_zero<kBf16>(sx[n], ones.x, ones.y, ones.z, ones.w, xb[n].x, xb[n].y);
           else
-            ptx::mma_16816<kBf16>(sx[n], kOnes, kOnes, kOnes, kOnes, xb[n].x, xb[n].y);
-          ptx::mma_16816<kBf16>(sx[n], kOnes, kOnes, kOnes, kOnes, xb[n].z, xb[n].w);
+            ptx::mma_16816<kBf16>(sx[n], ones.x, ones.y, ones.z, ones.w, xb[n].x, xb[n].y);
+          ptx::mma_16816<kBf16>(sx[n], ones.x, ones.y, ones.z, ones.w, xb[n].z, xb[n].w);
         }
 #pragma unroll
         for (int m = 0; m < kMT; ++m) {
@@ -497,26 +494,26 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
   };
   uint32_t slot = slot0;
 #pragma unroll 1
-  for (int32_t i = 0; i < items; ++i) {
-    // This lane's oldest block has landed; then the warp's, whose lanes share
-    // the scales.
-    if (a.ring == 4)
-      ptx::cp_async_wait<3>();
-    else if (a.ring == 3)
-      ptx::cp_async_wait<2>();
-    else
-      ptx::cp_async_wait<1>();
-    __syncwarp();
-    consume(slot, blk * warps + warp);
-    __syncwarp();
-    if (i + a.ring < items) issue(slot);
-    ptx::cp_async_commit();  // one group per block, empty at the end
-    slot += kSlot;
-    if (slot == slot0 + a.ring * kSlot) slot = slot0;
-    if (++blk == per_tile) {
-      blk = 0;
-      finish_tile();
+  for (int32_t i = 0; i < my_tiles; ++i) {
+#pragma unroll 1
+    for (int32_t rel = warp; rel < b1 - b0; rel += warps) {
+      // This lane's oldest block has landed; then the warp's, whose lanes share
+      // the scales.
+      if (a.ring == 4)
+        ptx::cp_async_wait<3>();
+      else if (a.ring == 3)
+        ptx::cp_async_wait<2>();
+      else
+        ptx::cp_async_wait<1>();
+      __syncwarp();
+      consume(slot, rel);
+      __syncwarp();
+      if (to_load > 0) issue(slot);
+      ptx::cp_async_commit();  // one group per block, empty at the end
+      slot += kSlot;
+      if (slot == slot0 + a.ring * kSlot) slot = slot0;
     }
+    finish_tile();
   }
 }
 
