@@ -71,6 +71,9 @@ struct FusedArgs {
   int32_t a_seg[3], b_seg[3];
   int32_t group_m;            // raster group height, in tiles
   int32_t a_mn, b_mn;         // operand layouts: 0 K-contiguous, 1 MN-contiguous
+  // Bit 0, 1: A, B were complete before the previous kernel of the stream let
+  // this one start, and may be loaded before it ends.
+  int32_t early;
   int32_t bf16;               // operands and 16-bit outputs are bf16
   int32_t act, save;          // gated epilogues: activation; keep g and u
   float alpha, beta;
@@ -317,6 +320,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
   constexpr int kHalfCols = kCols / 2;  // gated: gate columns, then as many up columns
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   ptx::griddep_wait();  // reads S, g and u; writes the outputs
+  ptx::griddep_launch_dependents();
   bool ok = wait_bar_warp<false>(tfull, 0u, w, kSiteTmemFull, unit);
   if (ok) {
     // Send: warp quarter q owns 32 rows, warps 0-3 columns 0-63, warps 4-7 the
@@ -391,6 +395,7 @@ __device__ __forceinline__ void pair_split_epilogue(const FusedArgs& args, int32
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, side = warp >> 2;
   const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   const bool ok = wait_bar_warp<true>(tfull, 0u, w, kSiteTmemFull, unit);
   const int r = q * 32 + lane;
   if (ok) {
@@ -514,8 +519,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     // the gate rows and up rows of the same columns of h (a pair's CTAs load
     // one half each, a lone CTA both); then the row and the matrix differ.
     constexpr int kGluBoxes = kPair ? 1 : 2;
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
+    if (!(args.early & (is_a ? 1 : 2))) {
+      ptx::griddep_wait();
+      ptx::griddep_launch_dependents();
+    }
     int stage = 0;
     uint32_t phase = 0;
     int64_t fills = 0;
@@ -671,6 +678,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   } else if (Cfg::kSplit == 1 && warp >= 4) {
     // ------------------------------------------------------------ epilogue --
     ptx::griddep_wait();  // reads S, g and u; writes the outputs
+    ptx::griddep_launch_dependents();
     const int q = warp & 3;  // this warp may touch TMEM lanes 32q .. 32q+31 only
     const int group = (warp - 4) >> 2;  // which of the two warps of quarter q
     const uint32_t stage_base =

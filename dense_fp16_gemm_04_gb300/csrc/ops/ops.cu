@@ -274,9 +274,15 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
   }
 }
 
-// out = A B^T, rounded to 16 bits.
-gemm_status_t product(gemm_ops_s* h, const Product& p, const Stack& out, cudaStream_t stream) {
-  return fused<kEpiStore>(h, p, base_args(h, p), out, {}, stream);
+// out = A B^T, rounded to 16 bits.  `early`: operands that may be loaded while
+// the previous kernel ends.  A kernel of this file lets the next one start only
+// after it has waited for the one before it, so what is complete by then are
+// the caller's tensors, and what the last kernel but one wrote.
+enum { kEarlyA = 1, kEarlyB = 2 };
+gemm_status_t product(gemm_ops_s* h, const Product& p, const Stack& out, int early, cudaStream_t stream) {
+  FusedArgs a = base_args(h, p);
+  a.early = early;
+  return fused<kEpiStore>(h, p, a, out, {}, stream);
 }
 
 // How a product of few tokens is laid out: warps per CTA, CTAs per k-slice,
@@ -655,6 +661,7 @@ gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const voi
     a.y = static_cast<uint16_t*>(y);
     a.ldy = ldy;
     a.gu = nullptr;
+    a.early = 1;  // the kernels above wrote neither W nor what they waited for
     a.K = static_cast<int32_t>(F);
     a.cols = static_cast<int32_t>(D);
     return stream_product<kW16, false>(h, a, bf16, s);
@@ -668,7 +675,7 @@ gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const voi
   st = fused<kEpiGlu>(h, p, a, hs, gu ? keep : Stack{}, s);
   if (st != GEMM_OK) return st;
   const Product down = {T, D, F, hs, {w_down, D, F, ldw_down, 1, D * ldw_down}, false, false, bf16, 1, 1};
-  return product(h, down, {y, T, D, ldy, 1, T * ldy}, s);
+  return product(h, down, {y, T, D, ldy, 1, T * ldy}, kEarlyB, s);
 }
 
 size_t gemm_gated_ffn_backward_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t F) {
@@ -734,11 +741,11 @@ gemm_status_t gemm_gated_ffn_backward(gemm_ops_t h, const void* dy, int64_t lddy
   // dw_down [D, F] = dy^T h; dx = dg Wg + du Wu (two segments); the halves of
   // dw_in, dg^T x and du^T x (a batch of two).
   const Product pd = {D, F, T, dys, hs, true, true, bf16, 1, 1};
-  if ((st = product(h, pd, {dw_down, D, F, F, 1, D * F}, s)) != GEMM_OK) return st;
+  if ((st = product(h, pd, {dw_down, D, F, F, 1, D * F}, kEarlyA, s)) != GEMM_OK) return st;
   const Product px = {T, D, F, dgus, w_ins, false, true, bf16, 1, 2, 0, 0, 0, {0, 1, 0}, {0, 1, 0}};
-  if ((st = product(h, px, {dx, T, D, lddx, 1, T * lddx}, s)) != GEMM_OK) return st;
+  if ((st = product(h, px, {dx, T, D, lddx, 1, T * lddx}, kEarlyA | kEarlyB, s)) != GEMM_OK) return st;
   const Product pi = {F, D, T, dgus, {x, T, D, ldx, 1, T * ldx}, true, true, bf16, 2, 1, 1, 0, 1};
-  return product(h, pi, {dw_in, F, D, D, 2, F * D}, s);
+  return product(h, pi, {dw_in, F, D, D, 2, F * D}, kEarlyA | kEarlyB, s);
 }
 
 size_t gemm_w4_workspace(gemm_ops_t h, int64_t T, int64_t N, int64_t K, int32_t gated) {

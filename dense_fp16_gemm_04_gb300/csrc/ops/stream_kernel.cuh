@@ -64,6 +64,7 @@ struct StreamArgs {
   int32_t group_shift;   // log2 G
   int32_t act;
   int32_t ring;          // blocks a warp keeps in flight, 2 .. 4
+  int32_t early;         // W may be read before the previous kernel has ended
 };
 
 constexpr int kStreamMaxWarps = 16;
@@ -231,12 +232,13 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
     }
   };
 
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
+  if (!a.early) ptx::griddep_wait();
   for (int i = 0; i < a.ring; ++i) {
     if (to_load > 0) issue(slot0 + i * kSlot);
     ptx::cp_async_commit();
   }
+  if (a.early) ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   // Stage x: 16-byte chunks of eight k, in the order the products read them
   // (4 bits: chunk 4 t + i of a block is word i of lane t), four loads in
   // flight a thread; zeros past K.
