@@ -70,6 +70,7 @@ struct FusedArgs {
   int32_t a_zb, b_zb, c_zb;
   int32_t a_seg[3], b_seg[3];
   int32_t group_m;            // raster group height, in tiles
+  uint32_t a_tx;              // bytes of A a CTA loads per k-block
   int32_t a_mn, b_mn;         // operand layouts: 0 K-contiguous, 1 MN-contiguous
   // Bit 0, 1: A, B were complete before the previous kernel of the stream let
   // this one start, and may be loaded before it ends.
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const bool mn = is_a ? args.a_mn != 0 : args.b_mn != 0;
     const uint32_t op_bytes = is_a ? Cfg::kABytes : Cfg::kBBytes;
     const uint32_t op_base = sb + (is_a ? Cfg::kOffA : Cfg::kOffB);
-    const uint32_t op_tx = op_bytes * Cfg::kCtas;
+    const uint32_t op_tx = (is_a ? args.a_tx : op_bytes) * Cfg::kCtas;
     // The operand's rows arrive as kBoxes boxes per stage.  Gated forward, B:
     // the gate rows and up rows of the same columns of h (a pair's CTAs load
     // one half each, a lone CTA both); then the row and the matrix differ.

@@ -200,7 +200,12 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
                            const Stack& d, cudaStream_t stream) {
   CUtensorMap ma, mb, mc, md;
   const uint32_t b_rows = Cfg::kGlu && Cfg::kCtas == 1 ? Cfg::kBN / 2 : Cfg::kBRows;
-  bool ok = make_map(h, &ma, p.a, p.bf16, 64, p.a_mn ? 64 : Cfg::kBM) &&
+  // Fewer rows than a tile: a box of those alone.  The tile's other rows keep
+  // what they held; they meet no stored row of the product.
+  const uint32_t a_rows =
+      Cfg::kCtas == 1 && !p.a_mn ? static_cast<uint32_t>(std::min<int64_t>(Cfg::kBM, up(p.M, 8))) : Cfg::kBM;
+  a.a_tx = a_rows * Cfg::kBK * 2;
+  bool ok = make_map(h, &ma, p.a, p.bf16, 64, p.a_mn ? 64 : a_rows) &&
             make_map(h, &mb, p.b, p.bf16, 64, p.b_mn ? 64 : b_rows);
   if (ok && c.p) ok = make_map(h, &mc, c, p.bf16, 64, 32);
   if (ok && d.p)
