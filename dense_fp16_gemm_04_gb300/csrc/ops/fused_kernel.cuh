@@ -71,6 +71,7 @@ struct FusedArgs {
   int32_t a_seg[3], b_seg[3];
   int32_t group_m;            // raster group height, in tiles
   uint32_t a_tx;              // bytes of A a CTA loads per k-block
+  int32_t stages;             // kFlex: k-blocks in flight, A's a_tx bytes apart
   int32_t a_mn, b_mn;         // operand layouts: 0 K-contiguous, 1 MN-contiguous
   // Bit 0, 1: A, B were complete before the previous kernel of the stream let
   // this one start, and may be loaded before it ends.
@@ -121,7 +122,10 @@ struct FusedCfg {
   static constexpr int kOffB = kStages * kABytes;
   static constexpr int kOffEpi = kOffB + kStages * kBBytes;
   static constexpr int kOffBar = kOffEpi + kEpiWarps * kEpiBufs * kBufBytes;
-  static constexpr int kNumBars = 2 * kStages + 5;
+  // Few rows leave room for more k-blocks: their number is the launch's.
+  static constexpr bool kFlex = kCtas == 1 && (kEpi == kEpiStore || kEpi == kEpiGlu);
+  static constexpr int kMaxStages = kFlex ? 8 : kStages;
+  static constexpr int kNumBars = 2 * kMaxStages + 5;
   static constexpr int kOffSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffAbort = kOffSlot + 4;
   static constexpr int kSmemBytes = kOffAbort + 4 + 1024;  // + slack to align the base
@@ -453,7 +457,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     fused_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmD,
                  const FusedArgs args) {
-  constexpr int S = Cfg::kStages;
+  const int S = Cfg::kFlex ? args.stages : Cfg::kStages;
+  const uint32_t a_stage = Cfg::kFlex ? args.a_tx : Cfg::kABytes;
+  const uint32_t off_b = Cfg::kFlex ? S * a_stage : Cfg::kOffB;
+  constexpr int kBars = Cfg::kMaxStages;
   constexpr bool kPair = Cfg::kCtas == 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -472,10 +479,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
   const uint32_t bar0 = sb + Cfg::kOffBar;
   auto bar_full = [&](int s) { return bar0 + 8u * s; };
-  auto bar_empty = [&](int s) { return bar0 + 8u * (S + s); };
-  auto bar_tfull = [&](int b) { return bar0 + 8u * (2 * S + b); };
-  auto bar_tempty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
-  const uint32_t bar_mma_done = bar0 + 8u * (2 * S + 4);
+  auto bar_empty = [&](int s) { return bar0 + 8u * (kBars + s); };
+  auto bar_tfull = [&](int b) { return bar0 + 8u * (2 * kBars + b); };
+  auto bar_tempty = [&](int b) { return bar0 + 8u * (2 * kBars + 2 + b); };
+  const uint32_t bar_mma_done = bar0 + 8u * (2 * kBars + 4);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffAbort);
   const Watch w{abort_flag, args.err, args.timeout_ns};
 
@@ -513,8 +520,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const bool is_a = warp == 0;
     const CUtensorMap* tm = is_a ? &tmA : &tmB;
     const bool mn = is_a ? args.a_mn != 0 : args.b_mn != 0;
-    const uint32_t op_bytes = is_a ? Cfg::kABytes : Cfg::kBBytes;
-    const uint32_t op_base = sb + (is_a ? Cfg::kOffA : Cfg::kOffB);
+    const uint32_t op_bytes = is_a ? a_stage : Cfg::kBBytes;
+    const uint32_t op_base = sb + (is_a ? Cfg::kOffA : off_b);
     const uint32_t op_tx = (is_a ? args.a_tx : op_bytes) * Cfg::kCtas;
     // The operand's rows arrive as kBoxes boxes per stage.  Gated forward, B:
     // the gate rows and up rows of the same columns of h (a pair's CTAs load
@@ -607,9 +614,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       const uint64_t b_kstep = args.b_mn ? 128u : 2u;
       const uint64_t a_desc0 = args.a_mn ? ptx::sw128_mnmajor_desc(sb + Cfg::kOffA)
                                          : ptx::sw128_kmajor_desc(sb + Cfg::kOffA);
-      const uint64_t b_desc0 = args.b_mn ? ptx::sw128_mnmajor_desc(sb + Cfg::kOffB)
-                                         : ptx::sw128_kmajor_desc(sb + Cfg::kOffB);
-      constexpr uint64_t kADescStage = Cfg::kABytes >> 4;
+      const uint64_t b_desc0 = args.b_mn ? ptx::sw128_mnmajor_desc(sb + off_b)
+                                         : ptx::sw128_kmajor_desc(sb + off_b);
+      const uint64_t a_desc_stage = a_stage >> 4;
       constexpr uint64_t kBDescStage = Cfg::kBBytes >> 4;
       int stage = 0;
       uint32_t phase = 0;
@@ -637,7 +644,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             break;
           }
           ptx::tc_fence_after();
-          const uint64_t a_desc = a_desc0 + kADescStage * static_cast<uint32_t>(stage);
+          const uint64_t a_desc = a_desc0 + a_desc_stage * static_cast<uint32_t>(stage);
           const uint64_t b_desc = b_desc0 + kBDescStage * static_cast<uint32_t>(stage);
           const uint32_t acc_first = kb != first ? 1u : 0u;
           if (ptx::elect_one()) {
