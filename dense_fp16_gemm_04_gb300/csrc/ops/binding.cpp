@@ -3,7 +3,8 @@
 // workspaces with torch's allocator and calls the C ABI.  Small products are
 // bound by the host: through ctypes and Python code the checks and the
 // marshalling of one w4_linear call took 10 us, of which the library itself
-// needs 2.4.  It is built without torch's headers: a tensor is used through
+// needs 2.4; through this binding it takes 7, of which 1.5 each allocate the
+// result and a workspace.  It is built without torch's headers: a tensor is used through
 // its Python attributes, and the library through addresses that ops.py hands
 // over once.
 #define PY_SSIZE_T_CLEAN
@@ -16,7 +17,7 @@
 namespace {
 
 // What ops.py hands over (setup).
-PyObject *g_empty, *g_f16, *g_bf16, *g_f32, *g_u8, *g_raw_stream, *g_error;
+PyObject *g_empty, *g_f16, *g_bf16, *g_u8, *g_raw_stream, *g_error;
 decltype(&gemm_gated_ffn_workspace) g_ffn_space;
 decltype(&gemm_gated_ffn) g_ffn;
 decltype(&gemm_gated_ffn_backward_workspace) g_bwd_space;
@@ -320,16 +321,16 @@ PyObject* py_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return out.release();
 }
 
-// (torch.empty, float16, bfloat16, float32, uint8, raw stream of a device,
+// (torch.empty, float16, bfloat16, uint8, raw stream of a device,
 // GemmError, then the addresses of the seven C functions)
 PyObject* py_setup(PyObject*, PyObject* args) {
   unsigned long long f[7];
-  PyObject* o[7];
-  if (!PyArg_ParseTuple(args, "OOOOOOOKKKKKKK", &o[0], &o[1], &o[2], &o[3], &o[4], &o[5], &o[6], &f[0], &f[1],
-                        &f[2], &f[3], &f[4], &f[5], &f[6]))
+  PyObject* o[6];
+  if (!PyArg_ParseTuple(args, "OOOOOOKKKKKKK", &o[0], &o[1], &o[2], &o[3], &o[4], &o[5], &f[0], &f[1], &f[2],
+                        &f[3], &f[4], &f[5], &f[6]))
     return nullptr;
-  PyObject** to[7] = {&g_empty, &g_f16, &g_bf16, &g_f32, &g_u8, &g_raw_stream, &g_error};
-  for (int i = 0; i < 7; ++i) Py_XSETREF(*to[i], Py_NewRef(o[i]));
+  PyObject** to[6] = {&g_empty, &g_f16, &g_bf16, &g_u8, &g_raw_stream, &g_error};
+  for (int i = 0; i < 6; ++i) Py_XSETREF(*to[i], Py_NewRef(o[i]));
   g_ffn_space = reinterpret_cast<decltype(g_ffn_space)>(f[0]);
   g_ffn = reinterpret_cast<decltype(g_ffn)>(f[1]);
   g_bwd_space = reinterpret_cast<decltype(g_bwd_space)>(f[2]);

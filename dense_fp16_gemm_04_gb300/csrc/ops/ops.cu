@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -17,7 +18,7 @@
 struct gemm_ops_s {
   int device = 0;
   int num_sms = 0;
-  int max_pairs = 0;  // CTA pairs of the pair kernels that fit on the device at once
+  int max_pairs = 0;      // CTA pairs of the pair kernels that fit on the device at once
   int max_twos = 0;       // clusters of two pairs sharing a tile
   int max_split[4] = {};  // clusters of 1, 2, 4, 8 CTAs sharing a tile
   void* encode = nullptr;
@@ -25,7 +26,7 @@ struct gemm_ops_s {
   uint32_t last_err[4] = {0, 0, 0, 0};
   uint64_t timeout_ns = 2000000000ull;
   int32_t skip_kb = -1;
-  uint64_t launches = 0;
+  std::atomic<uint64_t> launches{0};
 };
 
 namespace {
@@ -38,7 +39,11 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
-constexpr int64_t kMaxStreamTokens = 16;  // tokens of the streaming products of 16-bit weights
+// Tokens of the streaming products of 16-bit weights; more go to the tensor
+// cores' own products.  16 and 17 tokens: weights of 1024 x 4096 11.4 and 13.7
+// us, 2048 x 5632 22.1 and 25.3 us, 4096 x 8192 46.3 and 41.7 us, 8192 x 16384
+// 145 and 133 us.
+constexpr int64_t kMaxStreamTokens = 16;
 constexpr int kGroupM = 8;
 
 // Staging buffers of an epilogue warp: 64 KB in all beside five stages.
@@ -407,7 +412,10 @@ bool set_stream_attr() {
   return true;
 }
 
-// The forms of small groups for few tokens: see stream_kernel.cuh.
+// The forms of small groups for few tokens: as many as one 8-column tile holds.
+// 8192 x 8192 codes, 3 tokens in groups of 32: by columns (two tiles) 22.9 us, in
+// turn 22.3 us; 4 and 5 in groups of 64: by columns 17.9 (one tile) and 22.3 us,
+// in turn 18.1 and 18.4 us.
 constexpr int64_t kFewG32 = stream_tokens(kW4G32Few), kFewG64 = stream_tokens(kW4G64Few);
 
 template <bool kGlu>
@@ -538,7 +546,8 @@ gemm_status_t gemm_ops_create(gemm_ops_t* out, int device) {
       !set_attr<Lone<kEpiGlu>>() || !set_attr<Lone<kEpiGluBwd>>() || !set_attr<Lone<kEpiSplit>>() ||
       !set_attr<Lone<kEpiSplitSym>>() ||
       !set_attr<TwoPairs<kEpiStore>>() || !set_attr<TwoPairs<kEpiGlu>>() || !set_attr<TwoPairs<kEpiGluBwd>>() ||
-      !set_attr<TwoPairs<kEpiSplit>>() || !set_attr<TwoPairs<kEpiSplitSym>>() || !set_split_attr<2>() || !set_split_attr<4>() || !set_split_attr<8>() ||
+      !set_attr<TwoPairs<kEpiSplit>>() || !set_attr<TwoPairs<kEpiSplitSym>>() || !set_split_attr<2>() ||
+      !set_split_attr<4>() || !set_split_attr<8>() ||
       !set_stream_attr<kW16, false>() || !set_stream_attr<kW16, true>() ||
       !set_stream_attr<kW4G32, false>() || !set_stream_attr<kW4G32, true>() ||
       !set_stream_attr<kW4G64, false>() || !set_stream_attr<kW4G64, true>() ||
@@ -608,7 +617,7 @@ gemm_status_t gemm_ops_set_watchdog(gemm_ops_t h, uint64_t timeout_ns, int32_t s
   return GEMM_OK;
 }
 
-uint64_t gemm_ops_launch_count(gemm_ops_t h) { return h ? h->launches : 0; }
+uint64_t gemm_ops_launch_count(gemm_ops_t h) { return h ? h->launches.load() : 0; }
 
 size_t gemm_gated_ffn_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t F) {
   if (!h || T <= 0 || D <= 0 || F <= 0) return 0;
@@ -819,14 +828,16 @@ gemm_status_t gemm_w4_linear(gemm_ops_t h, const void* x, int64_t ldx, const voi
                              const void* scales, const void* zeros, void* y, int64_t ldy, void* workspace,
                              size_t workspace_bytes, int64_t T, int64_t N, int64_t K, int64_t group,
                              gemm_dtype_t dtype, void* stream) {
-  return w4_run(h, x, ldx, codes, scales, zeros, y, ldy, workspace, workspace_bytes, T, N, K, group, GEMM_ACT_SILU, dtype, false, stream);
+  return w4_run(h, x, ldx, codes, scales, zeros, y, ldy, workspace, workspace_bytes, T, N, K, group,
+                GEMM_ACT_SILU, dtype, false, stream);
 }
 
 gemm_status_t gemm_w4_gated(gemm_ops_t h, const void* x, int64_t ldx, const void* codes,
                             const void* scales, const void* zeros, void* y, int64_t ldy, void* workspace,
                             size_t workspace_bytes, int64_t T, int64_t N, int64_t K, int64_t group,
                             gemm_act_t act, gemm_dtype_t dtype, void* stream) {
-  return w4_run(h, x, ldx, codes, scales, zeros, y, ldy, workspace, workspace_bytes, T, N, K, group, act, dtype, true, stream);
+  return w4_run(h, x, ldx, codes, scales, zeros, y, ldy, workspace, workspace_bytes, T, N, K, group, act, dtype,
+                true, stream);
 }
 
 size_t gemm_orthogonalize_workspace(gemm_ops_t h, int64_t batch, int64_t M, int64_t N) {

@@ -1,6 +1,10 @@
 // ortho_kernels.cuh -- the memory-bound ends of the orthogonalised update:
 // the sum of squares of each matrix, its scaled split into a high and a low
-// fp16 part, and the sum of the two parts in the output's type.
+// fp16 part, and the sum of the two parts in the output's type.  Bound by their
+// bytes, or by a launch where they are few (4096 x 8192 from and to fp32 and
+// fp16: 3 launches of 15 to 40 us beside 4900 us of products; 512 x 512: 3 to 5
+// us each).  A single kernel for norm and split would have to wait for all
+// blocks in between; a launch does that for less.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

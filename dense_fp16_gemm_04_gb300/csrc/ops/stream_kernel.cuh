@@ -1,16 +1,22 @@
 // stream_kernel.cuh -- products of a few tokens with a weight matrix read
-// once:  y[t, n] = sum_k x[t, k] W[n, k]  for T <= 16 tokens, W in 16 bits or
-// in 4 bits with a scale (and a zero point) per group of a row:
+// once:  y[t, n] = sum_k x[t, k] W[n, k]  for up to 16 tokens at a time, W in 16
+// bits or in 4 bits with a scale (and a zero point) per group of a row:
 //
 //   W[n, k] = s[n, k / G] (q[n, k] - z[n, k / G]),   q, z in 0 .. 15.
 //
-// Bound by the weights' bytes.  The sums run on warp-level matrix products
-// (16 rows of W x 16 k x 8 tokens): tcgen05 would have to stage every weight
-// through shared memory for a tile of 64 rows or more, while here a warp's
-// weights are read by the lane that fetched them, 16 bytes a lane, in the order
-// a row stores them.  That order is free because a sum over k may be
-// taken in any order, the same for W and x: lane t of a row's four lanes takes
-// eight consecutive k of every 32 as its k-slots of two products.
+// The least it can take is the weights' bytes.  16-bit weights come close
+// (8192 x 16384 gated block, one token: 120 us, 99% of a copy's bandwidth); 4-bit
+// ones are bound by the instructions that unpack them (one token x 16384 gated
+// columns x 8192, groups of 32: 36 us for 151 MB, 61%; 300 instructions per warp
+// for 32 rows x 128 k, of which 96 unpack and 24 multiply, at 1.9 per clock).
+//
+// The sums run on warp-level matrix products (16 rows of W x 16 k x 8 tokens):
+// tcgen05 would have to stage every weight through shared memory for a tile of
+// 64 rows or more, while here a warp's weights are read by the lane that fetched
+// them, 16 bytes a lane, in the order a row stores them.  That order is free
+// because a sum over k may be taken in any order, the same for W and x: lane t of
+// a row's four lanes takes eight consecutive k of every 32 as its k-slots of two
+// products.
 //
 // 4-bit codes become 16-bit floats without a conversion: four bits set in the
 // mantissa of 64 (fp16) or 128 (bf16) read O + q with O that number.  With
@@ -24,22 +30,24 @@
 // result's own rounding.  The scale multiplies the finished fp32 sum.
 //
 // A lane's 16 bytes are 32 codes of one row, so the four lanes of a row hold
-// 128 k: one group, two, or four.  Smaller groups are kept apart by columns:
-// a product's eight columns are 8, 4 or 2 tokens x 1, 2 or 4 groups, and a
-// column's x is zero in the lanes whose k lie in another group.  A column then
-// sums one group alone, without moving any code between lanes.
+// 128 k: one group, two, or four.  Smaller groups are kept apart in one of two
+// ways.  In turn: the four lanes read a group's codes from shared memory together
+// (8 or 4 bytes a lane of what another lane fetched), so that a product sums one
+// group alone.  By columns, for as many tokens as fit: a product's eight columns
+// are 4 or 2 tokens x 2 or 4 groups, and a column's x is zero in the lanes whose k
+// lie in another group.  Columns cost fewer instructions while one tile of them
+// holds the tokens, and twice or four times the products beyond.
 //
 // CTAs are persistent: x (this CTA's k-slice of it) is staged in shared memory
 // once, and tiles of 32 rows of W follow one another (gated: 16 gate rows and
 // the 16 up rows of the same columns), two products for every read of x: with
-// 16 rows the reads of x alone filled shared memory's bandwidth (5 tokens,
-// 8192 x 8192 codes: 34 us at 81% of it).  A tile's k-blocks are dealt
-// to the warps in turn, so that the CTA reads contiguous pieces of each row;
-// every lane keeps its pieces of the next kRing blocks in flight (asynchronous
-// copies to a place of its own in shared memory: no barrier, no registers),
-// across tile ends.  The warps' sums meet in shared memory in warp order, so the result
-// does not depend on timing.  Where there are few tiles, or x does not fit,
-// K is also cut over CTAs and a second kernel adds the slices.
+// 16 rows the reads of x alone filled shared memory's bandwidth.  A tile's
+// k-blocks are dealt to the warps in turn, so that the CTA reads contiguous
+// pieces of each row; every lane keeps its pieces of the next `ring` blocks in
+// flight (asynchronous copies to shared memory: no barrier, no registers), across
+// tile ends.  The warps' sums meet in shared memory in warp order, so the result
+// does not depend on timing.  Where there are few tiles, or x does not fit, K is
+// also cut over CTAs and a second kernel adds the slices.
 #pragma once
 #include "act.cuh"
 #include "ptx_ops.cuh"

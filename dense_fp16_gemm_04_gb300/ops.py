@@ -1,11 +1,12 @@
 """Operators beside the GEMM: the gated feed-forward block, its backward pass,
 its products from 4-bit weights, and the orthogonalised update of its matrices.
 
-Thin bindings over the C ABI in ``include/gemm_ops.h`` (the calls of single
-products through the compiled ``_binding``, whose cost to the host is most of
-theirs); every step runs in the sm_103a kernels of ``libgb300gemm.so``.  Tensors are CUDA tensors of one
-device, float16 or bfloat16; workspaces come from torch's allocator on the
-current stream.  There is no fallback: wrong arguments and other devices raise.
+Thin bindings over the C ABI in ``include/gemm_ops.h``: the block and the 4-bit
+products through the compiled ``_binding`` (a call for one token costs the host
+more than the GPU), ``orthogonalize`` through ctypes.  Every step runs in the
+sm_103a kernels of ``libgb300gemm.so``.  Tensors are CUDA tensors of one device,
+float16 or bfloat16; workspaces come from torch's allocator on the current
+stream.  There is no fallback: wrong arguments and other devices raise.
 
     >>> import torch, dense_fp16_gemm_04_gb300 as g
     >>> x = torch.randn(4096, 1024, device="cuda", dtype=torch.float16)
@@ -96,8 +97,8 @@ def _load_binding():
             spec.loader.exec_module(mod)
             fns = ("gemm_gated_ffn_workspace", "gemm_gated_ffn", "gemm_gated_ffn_backward_workspace",
                    "gemm_gated_ffn_backward", "gemm_w4_workspace", "gemm_w4_linear", "gemm_w4_gated")
-            mod.setup(torch.empty, torch.float16, torch.bfloat16, torch.float32, torch.uint8, _current_stream,
-                      GemmError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in fns))
+            mod.setup(torch.empty, torch.float16, torch.bfloat16, torch.uint8, _current_stream, GemmError,
+                      *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in fns))
             _binding = mod
     return _binding
 

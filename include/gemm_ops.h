@@ -13,12 +13,15 @@
  * records GEMM_ERR_TIMEOUT, which gemm_ops_check_error reports.  Calls are
  * asynchronous on `stream` (a cudaStream_t of the handle's device; NULL =
  * legacy default stream), allocate nothing and do not synchronize.  A handle
- * holds no data between calls: it may serve any number of streams, from one
- * host thread at a time, as long as calls that overlap on the GPU have
- * workspaces of their own.
+ * holds no data between calls: the operators may be called with it on any
+ * number of streams and from any number of host threads, as long as calls that
+ * overlap on the GPU have workspaces of their own (gemm_ops_set_watchdog,
+ * _check_error and _destroy: while no other thread uses the handle).
  *
  * Every pointer must be device memory of the handle's device; outputs and
- * workspaces must not overlap inputs or one another.
+ * workspaces must not overlap inputs or one another.  Lengths are below 2^31
+ * (F and the N of 4-bit weights: 2^30) and row distances below 2^30.  Results do not depend on
+ * timing: no sum is taken in the order in which parts arrive.
  */
 #ifndef GB300_GEMM_OPS_H_
 #define GB300_GEMM_OPS_H_
@@ -77,7 +80,8 @@ GEMM_API uint64_t gemm_ops_launch_count(gemm_ops_t ops);
  * g, u and act(g) * u are fp32 until h is rounded to 16 bits as an operand of
  * the second product.  D and F are multiples of 8, pointers 16-byte aligned,
  * row distances multiples of 8 (GEMM_ERR_ALIGNMENT otherwise).  T == 0 or
- * D == 0: nothing to do; F == 0: y is zero.
+ * D == 0: nothing to do; F == 0: y is zero.  Infinities and NaN go where the
+ * formula puts them (silu and gelu of a gate of -inf are NaN).
  * workspace: gemm_gated_ffn_workspace(ops, T, D, F) bytes, 256-byte aligned. */
 GEMM_API size_t gemm_gated_ffn_workspace(gemm_ops_t ops, int64_t T, int64_t D, int64_t F);
 GEMM_API gemm_status_t gemm_gated_ffn(gemm_ops_t ops, const void* x, int64_t ldx, const void* w_in,
@@ -110,10 +114,13 @@ GEMM_API gemm_status_t gemm_gated_ffn_backward(
  *   scales : [N, K / G] 16-bit, contiguous
  *   zeros  : [N, K / G] bytes 0 .. 15, or NULL for 8 everywhere
  *   group  : G, a power of two from 32 on that divides K
- * Made for few tokens: the weights are read once for every 16 tokens.  x
- * and codes 16-byte aligned, ldx a multiple of 8 (GEMM_ERR_ALIGNMENT);
- * N, T and ldy are free.  The integers q - zero and their products with x are
- * exact; a group's sum is fp32 and so is its product with the scale.
+ * Made for few tokens: the weights are read once for every 16, and T is at most
+ * 8 * 65535.  x and codes 16-byte aligned, ldx a
+ * multiple of 8 (GEMM_ERR_ALIGNMENT); N and ldy are free; K is at most 2^28.
+ * A group's sum of x (O + q - (O + zero)), O = 64 (fp16) or 128 (bf16), and its
+ * product with the scale are fp32; the products x (O + q) are exact.  So x
+ * above 2^100 may overflow on the way, and a token with an infinite x becomes
+ * NaN.
  * workspace: gemm_w4_workspace(ops, T, N, K, gated) bytes (none for most
  * shapes), 256-byte aligned. */
 GEMM_API size_t gemm_w4_workspace(gemm_ops_t ops, int64_t T, int64_t N, int64_t K, int32_t gated);
@@ -143,7 +150,9 @@ GEMM_API gemm_status_t gemm_w4_gated(gemm_ops_t ops, const void* x, int64_t ldx,
  * them to one 16-bit number costs 1e-3 to 1e-2 of the result, since small
  * singular values grow by up to a^steps.  Their entries must stay below 8,
  * 32 and 64 (any coefficients that keep singular values below 2.8 and
- * |b| s^2 + |c| s^4 below 64); larger ones become infinite.
+ * |b| s^2 + |c| s^4 below 64); larger ones become infinite.  The sum of
+ * squares is fp32: |m| must be below 2^63.  A matrix of a batch gets the bits it
+ * gets by itself.
  * workspace: gemm_orthogonalize_workspace(ops, batch, M, N) bytes, 256-byte
  * aligned. */
 GEMM_API size_t gemm_orthogonalize_workspace(gemm_ops_t ops, int64_t batch, int64_t M, int64_t N);
