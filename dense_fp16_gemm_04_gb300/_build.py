@@ -1,12 +1,14 @@
 """Build the sm_103a CUDA library in-tree with nvcc (no torch, no cmake).
 
 Produces ``libgb300gemm.so`` next to this file from ``csrc/*.cu`` (the GEMM)
-and ``csrc/ops/*.cu`` (the operators beside it), and the operators' CPython
-binding ``_binding*.so`` from ``csrc/ops/binding.cpp``; the compiled code targets exactly sm_103a (GB300).
+and ``csrc/ops/*.cu`` (the operators beside it); the compiled code targets
+exactly sm_103a (GB300).  The operators' CPython binding ``_binding*.so``
+(``csrc/ops/binding.cpp``) is built against the installed torch.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -28,6 +30,10 @@ def _nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the GB300 GEMM library needs the CUDA toolkit to build")
+
+
+def _cuda() -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
 
 
 def sources():
@@ -57,8 +63,11 @@ def _binding_inputs():
 def _build_binding():
     """Start compiling the binding; returns (process, its output, command)."""
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
-           "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, BINDING_SRC, "-o", tmp]
+           "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(_cuda(), "include"), BINDING_SRC,
+           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", tmp]
     return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True), tmp, cmd
 
 
@@ -72,7 +81,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     # The CUDA runtime is linked shared: with torch in the process both use one
     # runtime (a second, static one slowed every call that follows a torch
     # allocation by about 3 us).
-    cudalib = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "lib64")
+    cudalib = os.path.join(_cuda(), "lib64")
     cmd = [nvcc, *ARCH_FLAGS, "-t", "0", "-O3", "-lineinfo", "-std=c++17",
            "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared",
            "-cudart", "shared", "-Xlinker", "-rpath," + cudalib, "-I", INCLUDE, "-I", CSRC, *sources(), "-o", tmp]

@@ -1,14 +1,17 @@
 // binding.cpp -- CPython binding of the operators in include/gemm_ops.h: reads
 // the tensors' type, device, shape and strides, allocates results and
-// workspaces with torch's allocator and calls the C ABI.  Small products are
-// bound by the host: through ctypes and Python code the checks and the
-// marshalling of one w4_linear call took 10 us, of which the library itself
-// needs 2.4; through this binding it takes 7, of which 1.5 each allocate the
-// result and a workspace.  It is built without torch's headers: a tensor is used through
-// its Python attributes, and the library through addresses that ops.py hands
-// over once.
+// workspaces with torch's allocator and calls the C ABI, whose functions ops.py
+// hands over once.  Calls for few tokens are bound by the host.  One of w4_linear
+// takes 4.5 us (10 us through ctypes and the tensors' Python attributes, 7.4 us
+// through those attributes from here), of gated_ffn 7.9 us (two launches; 12.9).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
 
@@ -17,7 +20,7 @@
 namespace {
 
 // What ops.py hands over (setup).
-PyObject *g_empty, *g_f16, *g_bf16, *g_u8, *g_raw_stream, *g_error;
+PyObject* g_error;
 decltype(&gemm_gated_ffn_workspace) g_ffn_space;
 decltype(&gemm_gated_ffn) g_ffn;
 decltype(&gemm_gated_ffn_backward_workspace) g_bwd_space;
@@ -26,7 +29,7 @@ decltype(&gemm_w4_workspace) g_w4_space;
 decltype(&gemm_w4_linear) g_w4;
 decltype(&gemm_w4_gated) g_w4g;
 
-PyObject *s_dtype, *s_shape, *s_get_device, *s_is_contiguous, *s_stride, *s_data_ptr, *s_cuda_stream, *kw_empty;
+PyObject* s_cuda_stream;
 
 // An owned reference.
 struct Ref {
@@ -42,23 +45,9 @@ struct Ref {
   }
 };
 
-PyObject* call0(PyObject* self, PyObject* name) {
-  PyObject* args[1] = {self};
-  return PyObject_VectorcallMethod(name, args, 1 | PY_VECTORCALL_ARGUMENTS_OFFSET, nullptr);
-}
-
 bool to_i64(PyObject* o, int64_t* v) {  // takes a borrowed reference
   *v = PyLong_AsLongLong(o);
   return *v != -1 || !PyErr_Occurred();
-}
-
-bool int_call(PyObject* self, PyObject* name, int64_t* v) {
-  Ref r(call0(self, name));
-  return r.p && to_i64(r.p, v);
-}
-
-bool pair(PyObject* tuple, int64_t* a, int64_t* b) {
-  return to_i64(PyTuple_GET_ITEM(tuple, 0), a) && to_i64(PyTuple_GET_ITEM(tuple, 1), b);
 }
 
 // One 2-D operand.
@@ -67,116 +56,140 @@ struct Mat {
   int64_t rows = 0, cols = 0, ld = 0;
 };
 
-// Reads t, which has to have this type and be on this device, and its row
-// distance; rows and cols, where not -1, are what it has to have.
-bool read(PyObject* t, const char* name, PyObject* dtype, int64_t index, int64_t rows, int64_t cols,
+const char* type_name(at::ScalarType t) {
+  switch (t) {
+    case at::kHalf: return "float16";
+    case at::kBFloat16: return "bfloat16";
+    case at::kByte: return "uint8";
+    default: return c10::toString(t);
+  }
+}
+
+const at::Tensor* tensor(PyObject* o, const char* name) {
+  if (THPVariable_Check(o)) return &THPVariable_Unpack(o);
+  PyErr_Format(PyExc_TypeError, "%s must be a tensor, got %R", name, reinterpret_cast<PyObject*>(Py_TYPE(o)));
+  return nullptr;
+}
+
+// Reads o, a tensor that has to have this type and be on this device, and its
+// row distance; rows and cols, where not -1, are what it has to have.
+bool read(PyObject* o, const char* name, at::ScalarType dtype, int64_t index, int64_t rows, int64_t cols,
           bool contiguous, Mat* m) {
-  Ref dt(PyObject_GetAttr(t, s_dtype));
-  if (!dt.p) return false;
-  if (dt.p != dtype) {
-    PyErr_Format(PyExc_TypeError, "%s must be %S, got %S", name, dtype, dt.p);
+  const at::Tensor* t = tensor(o, name);
+  if (!t) return false;
+  if (t->scalar_type() != dtype) {
+    PyErr_Format(PyExc_TypeError, "%s must be %s, got %s", name, type_name(dtype), type_name(t->scalar_type()));
     return false;
   }
-  int64_t dev;
-  if (!int_call(t, s_get_device, &dev)) return false;
-  if (dev != index) {
-    if (dev < 0)
-      PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", name);
-    else
-      PyErr_Format(PyExc_ValueError, "%s is on cuda:%lld, the handle on cuda:%lld", name, dev, index);
+  if (!t->is_cuda()) {
+    PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", name);
     return false;
   }
-  Ref shape(PyObject_GetAttr(t, s_shape));
-  if (!shape.p) return false;
-  if (!PyTuple_Check(shape.p) || PyTuple_GET_SIZE(shape.p) != 2) {
-    PyErr_Format(PyExc_ValueError, "%s must be 2-D, got %S", name, shape.p);
+  if (t->get_device() != index) {
+    PyErr_Format(PyExc_ValueError, "%s is on cuda:%d, the handle on cuda:%lld", name,
+                 static_cast<int>(t->get_device()), static_cast<long long>(index));
     return false;
   }
-  if (!pair(shape.p, &m->rows, &m->cols)) return false;
+  if (t->dim() != 2) {
+    PyErr_Format(PyExc_ValueError, "%s must be 2-D, got %lld dimensions", name, static_cast<long long>(t->dim()));
+    return false;
+  }
+  m->rows = t->size(0);
+  m->cols = t->size(1);
   if ((rows >= 0 && m->rows != rows) || (cols >= 0 && m->cols != cols)) {
-    if (rows >= 0 && cols >= 0)
-      PyErr_Format(PyExc_ValueError, "%s must be [%lld, %lld], got %S", name, rows, cols, shape.p);
-    else
-      PyErr_Format(PyExc_ValueError, "%s must have %lld %s, got %S", name, rows >= 0 ? rows : cols,
-                   rows >= 0 ? "rows" : "columns", shape.p);
+    PyErr_Format(PyExc_ValueError, "%s must be [%lld, %lld], got [%lld, %lld]", name,
+                 static_cast<long long>(rows >= 0 ? rows : m->rows), static_cast<long long>(cols >= 0 ? cols : m->cols),
+                 static_cast<long long>(m->rows), static_cast<long long>(m->cols));
     return false;
   }
-  Ref cont(call0(t, s_is_contiguous));
-  if (!cont.p) return false;
   m->ld = m->cols;
-  if (cont.p != Py_True) {
+  if (!t->is_contiguous()) {
     if (contiguous) {
       PyErr_Format(PyExc_ValueError, "%s must be contiguous", name);
       return false;
     }
-    Ref st(call0(t, s_stride));
-    int64_t ld, inner;
-    if (!st.p || !pair(st.p, &ld, &inner)) return false;
-    if ((m->cols > 1 && inner != 1) || (m->rows > 1 && ld < m->cols)) {
+    const int64_t ld = t->stride(0);
+    if ((m->cols > 1 && t->stride(1) != 1) || (m->rows > 1 && ld < m->cols)) {
       PyErr_Format(PyExc_ValueError, "%s's rows must be contiguous", name);
       return false;
     }
     // One row or none, or nothing in a row: the distance to the next is free.
     if (m->rows > 1 && m->cols > 0) m->ld = ld;
   }
-  int64_t p;
-  if (!int_call(t, s_data_ptr, &p)) return false;
-  m->p = reinterpret_cast<void*>(p);
+  m->p = t->data_ptr();
   return true;
 }
 
 // x's type: one of the two 16-bit ones.
-bool read_x(PyObject* x, int64_t index, PyObject** dtype, gemm_dtype_t* code, Mat* m) {
-  Ref dt(PyObject_GetAttr(x, s_dtype));
-  if (!dt.p) return false;
-  if (dt.p != g_f16 && dt.p != g_bf16) {
-    PyErr_Format(PyExc_TypeError, "x must be float16 or bfloat16, got %S", dt.p);
+bool read_x(PyObject* x, int64_t index, at::ScalarType* dtype, gemm_dtype_t* code, Mat* m) {
+  const at::Tensor* t = tensor(x, "x");
+  if (!t) return false;
+  *dtype = t->scalar_type();
+  if (*dtype != at::kHalf && *dtype != at::kBFloat16) {
+    PyErr_Format(PyExc_TypeError, "x must be float16 or bfloat16, got %s", type_name(*dtype));
     return false;
   }
-  *dtype = dt.p == g_f16 ? g_f16 : g_bf16;
-  *code = dt.p == g_f16 ? GEMM_F16 : GEMM_BF16;
+  *code = *dtype == at::kHalf ? GEMM_F16 : GEMM_BF16;
   return read(x, "x", *dtype, index, -1, -1, false, m);
 }
 
-// A new tensor: a matrix, or (cols < 0) `rows` bytes.
-PyObject* empty(int64_t rows, int64_t cols, PyObject* dtype, PyObject* device, void** p) {
-  Ref size(cols < 0 ? Py_BuildValue("(L)", static_cast<long long>(rows))
-                    : Py_BuildValue("(LL)", static_cast<long long>(rows), static_cast<long long>(cols)));
-  if (!size.p) return nullptr;
-  PyObject* args[3] = {size.p, dtype, device};
-  Ref t(PyObject_Vectorcall(g_empty, args, 1, kw_empty));
-  int64_t a;
-  if (!t.p || !int_call(t.p, s_data_ptr, &a)) return nullptr;
-  *p = reinterpret_cast<void*>(a);
-  return t.release();
+at::TensorOptions on(int64_t index, at::ScalarType dtype) {
+  return at::TensorOptions().dtype(dtype).device(at::kCUDA, static_cast<c10::DeviceIndex>(index));
 }
 
+// A new matrix.
+PyObject* empty(int64_t rows, int64_t cols, at::ScalarType dtype, int64_t index, void** p) {
+  at::Tensor t = at::empty({rows, cols}, on(index, dtype));
+  *p = t.data_ptr();
+  return THPVariable_Wrap(std::move(t));
+}
+
+// A workspace, freed in stream order when it goes out of scope; none for 0 bytes.
+struct Workspace {
+  at::Tensor t;
+  void* p = nullptr;
+  Workspace(size_t bytes, int64_t index) {
+    if (!bytes) return;
+    t = at::empty({static_cast<int64_t>(bytes)}, on(index, at::kByte));
+    p = t.data_ptr();
+  }
+};
+
 // `out`, checked, or a new matrix.
-PyObject* result(PyObject* out, int64_t rows, int64_t cols, PyObject* dtype, int64_t index, PyObject* device,
-                 Mat* m) {
+PyObject* result(PyObject* out, int64_t rows, int64_t cols, at::ScalarType dtype, int64_t index, Mat* m) {
   if (out == Py_None) {
     m->rows = rows, m->cols = cols, m->ld = cols;
-    return empty(rows, cols, dtype, device, &m->p);
+    return empty(rows, cols, dtype, index, &m->p);
   }
   if (!read(out, "out", dtype, index, rows, cols, false, m)) return nullptr;
   return Py_NewRef(out);
 }
 
-// The current stream of the device, an address, or a torch stream.
-bool stream_of(PyObject* o, PyObject* index, void** s) {
-  int64_t v;
-  if (o == Py_None) {
-    Ref r(PyObject_CallOneArg(g_raw_stream, index));
-    if (!r.p || !to_i64(r.p, &v)) return false;
-  } else if (PyLong_Check(o)) {
-    if (!to_i64(o, &v)) return false;
-  } else {
-    Ref r(PyObject_GetAttr(o, s_cuda_stream));
-    if (!r.p || !to_i64(r.p, &v)) return false;
+// The stream of a call: the device's current one, an address, or a torch
+// stream.  What the call allocates belongs to that stream: a workspace of the
+// current stream could be handed out again there while another still uses it.
+struct Stream {
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  void* s = nullptr;
+
+  bool open(PyObject* o, int64_t index) {
+    const auto dev = static_cast<c10::DeviceIndex>(index);
+    if (o == Py_None) {
+      s = c10::cuda::getCurrentCUDAStream(dev).stream();
+      return true;
+    }
+    int64_t v;
+    if (PyLong_Check(o)) {
+      if (!to_i64(o, &v)) return false;
+    } else {
+      Ref r(PyObject_GetAttr(o, s_cuda_stream));
+      if (!r.p || !to_i64(r.p, &v)) return false;
+    }
+    s = reinterpret_cast<void*>(v);
+    guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), dev));
+    return true;
   }
-  *s = reinterpret_cast<void*>(v);
-  return true;
-}
+};
 
 bool act_of(PyObject* o, gemm_act_t* a) {
   if (PyUnicode_Check(o)) {
@@ -195,11 +208,10 @@ bool failed(gemm_status_t st, const char* where) {
   return true;
 }
 
-// The first three arguments of every call: handle, device index, torch device.
+// The first two arguments of every call: handle, device index.
 struct Target {
   gemm_ops_t h;
   int64_t index;
-  PyObject* device;
 };
 bool target(PyObject* const* a, Py_ssize_t n, Py_ssize_t want, Target* t) {
   if (n != want) {
@@ -209,85 +221,90 @@ bool target(PyObject* const* a, Py_ssize_t n, Py_ssize_t want, Target* t) {
   int64_t h;
   if (!to_i64(a[0], &h) || !to_i64(a[1], &t->index)) return false;
   t->h = reinterpret_cast<gemm_ops_t>(h);
-  t->device = a[2];
   return true;
 }
 
-// (handle, index, device, x, w_in, w_down, act, save, out, stream)
+// (handle, index, x, w_in, w_down, act, save, out, stream)
 PyObject* py_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
   Target t;
   Mat x, wi, wd, y;
-  PyObject* dt;
+  at::ScalarType dt;
   gemm_dtype_t code;
   gemm_act_t act;
-  if (!target(a, n, 10, &t) || !act_of(a[6], &act) || !read_x(a[3], t.index, &dt, &code, &x) ||
-      !read(a[5], "w_down", dt, t.index, x.cols, -1, false, &wd) ||
-      !read(a[4], "w_in", dt, t.index, 2 * wd.cols, x.cols, false, &wi))
+  if (!target(a, n, 9, &t) || !act_of(a[5], &act) || !read_x(a[2], t.index, &dt, &code, &x) ||
+      !read(a[4], "w_down", dt, t.index, x.cols, -1, false, &wd) ||
+      !read(a[3], "w_in", dt, t.index, 2 * wd.cols, x.cols, false, &wi))
     return nullptr;
   const int64_t T = x.rows, D = x.cols, F = wd.cols;
-  const int save = PyObject_IsTrue(a[7]);
-  if (save < 0) return nullptr;
-  Ref out(result(a[8], T, D, dt, t.index, t.device, &y));
+  const int save = PyObject_IsTrue(a[6]);
+  Stream stream;
+  if (save < 0 || !stream.open(a[8], t.index)) return nullptr;
+  Ref out(result(a[7], T, D, dt, t.index, &y));
   if (!out.p) return nullptr;
-  void *gp = nullptr, *wp = nullptr, *s;
-  Ref gu(save ? empty(T, 2 * F, dt, t.device, &gp) : nullptr);
+  void* gp = nullptr;
+  Ref gu(save ? empty(T, 2 * F, dt, t.index, &gp) : nullptr);
   if (save && !gu.p) return nullptr;
   const size_t need = g_ffn_space(t.h, T, D, F);
-  Ref ws(need ? empty(static_cast<int64_t>(need), -1, g_u8, t.device, &wp) : nullptr);
-  if ((need && !ws.p) || !stream_of(a[9], a[1], &s)) return nullptr;
+  const Workspace ws(need, t.index);
   gemm_status_t st;
   Py_BEGIN_ALLOW_THREADS;
-  st = g_ffn(t.h, x.p, x.ld, wi.p, wi.ld, wd.p, wd.ld, y.p, y.ld, gp, wp, need, T, D, F, act, code, s);
+  st = g_ffn(t.h, x.p, x.ld, wi.p, wi.ld, wd.p, wd.ld, y.p, y.ld, gp, ws.p, need, T, D, F, act, code, stream.s);
   Py_END_ALLOW_THREADS;
   if (failed(st, "gemm_gated_ffn")) return nullptr;
   return save ? PyTuple_Pack(2, out.p, gu.p) : out.release();
+  END_HANDLE_TH_ERRORS
 }
 
-// (handle, index, device, dy, x, w_in, w_down, gu, act, stream)
+// (handle, index, dy, x, w_in, w_down, gu, act, stream)
 PyObject* py_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
   Target t;
   Mat dy, x, wi, wd, gu;
-  PyObject* dt;
+  at::ScalarType dt;
   gemm_dtype_t code;
   gemm_act_t act;
-  if (!target(a, n, 10, &t) || !act_of(a[8], &act) || !read_x(a[4], t.index, &dt, &code, &x) ||
-      !read(a[6], "w_down", dt, t.index, x.cols, -1, false, &wd) ||
-      !read(a[5], "w_in", dt, t.index, 2 * wd.cols, x.cols, false, &wi) ||
-      !read(a[3], "dy", dt, t.index, x.rows, x.cols, false, &dy) ||
-      !read(a[7], "gu", dt, t.index, x.rows, 2 * wd.cols, true, &gu))
+  if (!target(a, n, 9, &t) || !act_of(a[7], &act) || !read_x(a[3], t.index, &dt, &code, &x) ||
+      !read(a[5], "w_down", dt, t.index, x.cols, -1, false, &wd) ||
+      !read(a[4], "w_in", dt, t.index, 2 * wd.cols, x.cols, false, &wi) ||
+      !read(a[2], "dy", dt, t.index, x.rows, x.cols, false, &dy) ||
+      !read(a[6], "gu", dt, t.index, x.rows, 2 * wd.cols, true, &gu))
     return nullptr;
   const int64_t T = x.rows, D = x.cols, F = wd.cols;
-  void *dxp, *dip, *ddp, *wp = nullptr, *s;
-  Ref dx(empty(T, D, dt, t.device, &dxp));
+  Stream stream;
+  if (!stream.open(a[8], t.index)) return nullptr;
+  void *dxp, *dip, *ddp;
+  Ref dx(empty(T, D, dt, t.index, &dxp));
   if (!dx.p) return nullptr;
-  Ref di(empty(2 * F, D, dt, t.device, &dip));
+  Ref di(empty(2 * F, D, dt, t.index, &dip));
   if (!di.p) return nullptr;
-  Ref dd(empty(D, F, dt, t.device, &ddp));
+  Ref dd(empty(D, F, dt, t.index, &ddp));
   if (!dd.p) return nullptr;
   const size_t need = g_bwd_space(t.h, T, D, F);
-  Ref ws(need ? empty(static_cast<int64_t>(need), -1, g_u8, t.device, &wp) : nullptr);
-  if ((need && !ws.p) || !stream_of(a[9], a[1], &s)) return nullptr;
+  const Workspace ws(need, t.index);
   gemm_status_t st;
   Py_BEGIN_ALLOW_THREADS;
-  st = g_bwd(t.h, dy.p, dy.ld, x.p, x.ld, wi.p, wi.ld, wd.p, wd.ld, gu.p, dxp, D, dip, ddp, wp, need, T, D, F, act,
-             code, s);
+  st = g_bwd(t.h, dy.p, dy.ld, x.p, x.ld, wi.p, wi.ld, wd.p, wd.ld, gu.p, dxp, D, dip, ddp, ws.p, need, T, D, F, act,
+             code, stream.s);
   Py_END_ALLOW_THREADS;
   if (failed(st, "gemm_gated_ffn_backward")) return nullptr;
   return PyTuple_Pack(3, dx.p, di.p, dd.p);
+  END_HANDLE_TH_ERRORS
 }
 
-// (handle, index, device, x, codes, scales, zeros, act or None, out, stream);
+// (handle, index, x, codes, scales, zeros, act or None, out, stream);
 // act: gated.
 PyObject* py_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
   Target t;
   Mat x, codes, scales, zeros, y;
-  PyObject* dt;
+  at::ScalarType dt;
   gemm_dtype_t code;
   gemm_act_t act = GEMM_ACT_SILU;
-  const bool gated = n > 7 && a[7] != Py_None;
-  if (!target(a, n, 10, &t) || (gated && !act_of(a[7], &act)) || !read_x(a[3], t.index, &dt, &code, &x) ||
-      !read(a[4], "codes", g_u8, t.index, -1, -1, true, &codes) ||
-      !read(a[5], "scales", dt, t.index, codes.rows, -1, true, &scales))
+  const bool gated = n > 6 && a[6] != Py_None;
+  if (!target(a, n, 9, &t) || (gated && !act_of(a[6], &act)) || !read_x(a[2], t.index, &dt, &code, &x) ||
+      !read(a[3], "codes", at::kByte, t.index, -1, -1, true, &codes) ||
+      !read(a[4], "scales", dt, t.index, codes.rows, -1, true, &scales))
     return nullptr;
   const int64_t T = x.rows, K = x.cols, groups = scales.cols;
   if (codes.cols * 2 != K) {
@@ -300,37 +317,34 @@ PyObject* py_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
                  groups);
     return nullptr;
   }
-  if (a[6] != Py_None && !read(a[6], "zeros", g_u8, t.index, codes.rows, groups, true, &zeros)) return nullptr;
+  if (a[5] != Py_None && !read(a[5], "zeros", at::kByte, t.index, codes.rows, groups, true, &zeros)) return nullptr;
   if (gated && codes.rows % 2 != 0) {
     PyErr_SetString(PyExc_ValueError, "gated weights have an even number of rows: gate rows, then up rows");
     return nullptr;
   }
   const int64_t N = gated ? codes.rows / 2 : codes.rows, group = groups ? K / groups : 32;
-  Ref out(result(a[8], T, N, dt, t.index, t.device, &y));
+  Stream stream;
+  if (!stream.open(a[8], t.index)) return nullptr;
+  Ref out(result(a[7], T, N, dt, t.index, &y));
   if (!out.p) return nullptr;
-  void *wp = nullptr, *s;
   const size_t need = g_w4_space(t.h, T, N, K, gated);
-  Ref ws(need ? empty(static_cast<int64_t>(need), -1, g_u8, t.device, &wp) : nullptr);
-  if ((need && !ws.p) || !stream_of(a[9], a[1], &s)) return nullptr;
+  const Workspace ws(need, t.index);
   gemm_status_t st;
   Py_BEGIN_ALLOW_THREADS;
-  st = gated ? g_w4g(t.h, x.p, x.ld, codes.p, scales.p, zeros.p, y.p, y.ld, wp, need, T, N, K, group, act, code, s)
-             : g_w4(t.h, x.p, x.ld, codes.p, scales.p, zeros.p, y.p, y.ld, wp, need, T, N, K, group, code, s);
+  st = gated ? g_w4g(t.h, x.p, x.ld, codes.p, scales.p, zeros.p, y.p, y.ld, ws.p, need, T, N, K, group, act, code, stream.s)
+             : g_w4(t.h, x.p, x.ld, codes.p, scales.p, zeros.p, y.p, y.ld, ws.p, need, T, N, K, group, code, stream.s);
   Py_END_ALLOW_THREADS;
   if (failed(st, gated ? "gemm_w4_gated" : "gemm_w4_linear")) return nullptr;
   return out.release();
+  END_HANDLE_TH_ERRORS
 }
 
-// (torch.empty, float16, bfloat16, uint8, raw stream of a device,
-// GemmError, then the addresses of the seven C functions)
+// (GemmError, then the addresses of the seven C functions)
 PyObject* py_setup(PyObject*, PyObject* args) {
   unsigned long long f[7];
-  PyObject* o[6];
-  if (!PyArg_ParseTuple(args, "OOOOOOKKKKKKK", &o[0], &o[1], &o[2], &o[3], &o[4], &o[5], &f[0], &f[1], &f[2],
-                        &f[3], &f[4], &f[5], &f[6]))
-    return nullptr;
-  PyObject** to[6] = {&g_empty, &g_f16, &g_bf16, &g_u8, &g_raw_stream, &g_error};
-  for (int i = 0; i < 6; ++i) Py_XSETREF(*to[i], Py_NewRef(o[i]));
+  PyObject* error;
+  if (!PyArg_ParseTuple(args, "OKKKKKKK", &error, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6])) return nullptr;
+  Py_XSETREF(g_error, Py_NewRef(error));
   g_ffn_space = reinterpret_cast<decltype(g_ffn_space)>(f[0]);
   g_ffn = reinterpret_cast<decltype(g_ffn)>(f[1]);
   g_bwd_space = reinterpret_cast<decltype(g_bwd_space)>(f[2]);
@@ -353,15 +367,6 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 }  // namespace
 
 PyMODINIT_FUNC PyInit__binding(void) {
-  struct {
-    PyObject** to;
-    const char* text;
-  } const names[] = {{&s_dtype, "dtype"},   {&s_shape, "shape"},   {&s_get_device, "get_device"},
-                     {&s_is_contiguous, "is_contiguous"}, {&s_stride, "stride"}, {&s_data_ptr, "data_ptr"},
-                     {&s_cuda_stream, "cuda_stream"}};
-  for (const auto& n : names)
-    if (!(*n.to = PyUnicode_InternFromString(n.text))) return nullptr;
-  kw_empty = Py_BuildValue("(ss)", "dtype", "device");
-  if (!kw_empty) return nullptr;
+  if (!(s_cuda_stream = PyUnicode_InternFromString("cuda_stream"))) return nullptr;
   return PyModule_Create(&module);
 }

@@ -5,8 +5,8 @@ Thin bindings over the C ABI in ``include/gemm_ops.h``: the block and the 4-bit
 products through the compiled ``_binding`` (a call for one token costs the host
 more than the GPU), ``orthogonalize`` through ctypes.  Every step runs in the
 sm_103a kernels of ``libgb300gemm.so``.  Tensors are CUDA tensors of one device,
-float16 or bfloat16; workspaces come from torch's allocator on the current
-stream.  There is no fallback: wrong arguments and other devices raise.
+float16 or bfloat16; results and workspaces come from torch's allocator, on the
+stream of the call (the current one, or ``stream``).  There is no fallback: wrong arguments and other devices raise.
 
     >>> import torch, dense_fp16_gemm_04_gb300 as g
     >>> x = torch.randn(4096, 1024, device="cuda", dtype=torch.float16)
@@ -74,12 +74,6 @@ def _current_stream(index):
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
-def _stream(stream, index):
-    if stream is None:
-        return _current_stream(index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
 _binding = None
 
 
@@ -97,8 +91,7 @@ def _load_binding():
             spec.loader.exec_module(mod)
             fns = ("gemm_gated_ffn_workspace", "gemm_gated_ffn", "gemm_gated_ffn_backward_workspace",
                    "gemm_gated_ffn_backward", "gemm_w4_workspace", "gemm_w4_linear", "gemm_w4_gated")
-            mod.setup(torch.empty, torch.float16, torch.bfloat16, torch.uint8, _current_stream, GemmError,
-                      *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in fns))
+            mod.setup(GemmError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in fns))
             _binding = mod
     return _binding
 
@@ -146,20 +139,20 @@ class Ops:
 
     # -- the gated block ----------------------------------------------------
     def gated_ffn(self, x, w_in, w_down, act="silu", save=False, out=None, stream=None):
-        return self._b.gated_ffn(self._addr, self.index, self.device, x, w_in, w_down, act, save, out, stream)
+        return self._b.gated_ffn(self._addr, self.index, x, w_in, w_down, act, save, out, stream)
 
     def gated_ffn_backward(self, dy, x, w_in, w_down, gu, act="silu", stream=None):
-        return self._b.gated_ffn_backward(self._addr, self.index, self.device, dy, x, w_in, w_down, gu, act,
+        return self._b.gated_ffn_backward(self._addr, self.index, dy, x, w_in, w_down, gu, act,
                                           stream)
 
     # -- 4-bit weights ------------------------------------------------------
     def w4_linear(self, x, codes, scales, zeros=None, out=None, stream=None):
-        return self._b.w4(self._addr, self.index, self.device, x, codes, scales, zeros, None, out, stream)
+        return self._b.w4(self._addr, self.index, x, codes, scales, zeros, None, out, stream)
 
     def w4_gated(self, x, codes, scales, zeros=None, act="silu", out=None, stream=None):
         if act is None:
             raise ValueError("act must be 'silu', 'gelu_tanh' or 'relu', got None")
-        return self._b.w4(self._addr, self.index, self.device, x, codes, scales, zeros, act, out, stream)
+        return self._b.w4(self._addr, self.index, x, codes, scales, zeros, act, out, stream)
 
     # -- the orthogonalised update -------------------------------------------
     def orthogonalize(self, m, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, dtype=None, out=None, stream=None):
@@ -176,6 +169,11 @@ class Ops:
             dtype = out.dtype if out is not None else m.dtype
         if dtype not in _DTYPE:
             raise TypeError(f"dtype must be float16, bfloat16 or float32, got {dtype}")
+        if stream is not None:  # what is allocated belongs to the stream that uses it
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=self.device)
+            with torch.cuda.stream(stream):
+                return self.orthogonalize(m, steps, coeffs, eps, dtype, out)
         if out is None:
             out = torch.empty(m.shape, dtype=dtype, device=self.device)
         elif out.shape != m.shape or out.dtype != dtype or out.device != self.device:
@@ -193,7 +191,7 @@ class Ops:
         _check(self._lib.gemm_orthogonalize(
             self._h, m.data_ptr(), lds[0], lds[1], out.data_ptr(), lds[2], lds[3], ws.data_ptr(), need, B, M, N,
             int(steps), (ctypes.c_float * 3)(*coeffs), float(eps), _DTYPE[m.dtype], _DTYPE[dtype],
-            _stream(stream, self.index)), "gemm_orthogonalize")
+            _current_stream(self.index)), "gemm_orthogonalize")
         return out
 
 

@@ -669,3 +669,39 @@ def test_ffn_backward_of_large_gates(g, act):
     w_down = torch.eye(D, F, device="cuda", dtype=torch.bfloat16)
     dx, _, _ = g.gated_ffn_backward(one, one, w_in, w_down, gu, act=act)
     assert torch.equal(dx.float(), torch.tensor([[8.0], [0.0], [0.0]], device="cuda").expand(T, D))
+
+
+def test_another_stream_owns_what_it_uses(g):
+    """With ``stream`` given, workspaces and results come from that stream's
+    memory: the current stream does not get them back while they are in use."""
+    dt = torch.float16
+    x, w_in, w_down, dy = make_ffn(300, 512, 1024, dt, seed=5)
+    xm, codes, scales, z = make_w4(2, 64, 16384, 64, True, dt)
+    m = torch.randn(300, 400, device="cuda")
+    y, gu = g.gated_ffn(x, w_in, w_down, save=True)
+    want = (y, *g.gated_ffn_backward(dy, x, w_in, w_down, gu), g.w4_linear(xm, codes, scales, z), g.orthogonalize(m))
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        for call, ref in ((lambda: g.gated_ffn(x, w_in, w_down, stream=stream), want[:1]),
+                          (lambda: g.gated_ffn_backward(dy, x, w_in, w_down, gu, stream=stream), want[1:4]),
+                          (lambda: g.w4_linear(xm, codes, scales, z, stream=stream), want[4:5]),
+                          (lambda: g.orthogonalize(m, stream=stream), want[5:])):
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)  # about 10 ms, so that the call is still to run below
+            got = call()
+            trash = [torch.full((n,), float("nan"), device="cuda") for n in (1 << k for k in range(6, 22)) for _ in range(3)]
+            torch.cuda.synchronize()
+            got = got if isinstance(got, tuple) else (got,)
+            assert len(got) == len(ref) and all(torch.equal(a, b) for a, b in zip(got, ref))
+            del trash
+
+
+def test_wrong_objects_are_refused(g):
+    x, w_in, w_down, _ = make_ffn(2, 16, 16, torch.float16)
+    with pytest.raises(TypeError):
+        g.default_ops().gated_ffn([1, 2], w_in, w_down)
+    with pytest.raises(TypeError):
+        g.gated_ffn(x, None, w_down)
+    with pytest.raises(ValueError):
+        g.gated_ffn(x, w_in, w_down, out=torch.empty(2, 16, dtype=torch.float16))
