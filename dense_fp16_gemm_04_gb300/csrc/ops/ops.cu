@@ -633,7 +633,15 @@ gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const voi
                              int64_t D, int64_t F, gemm_act_t act, gemm_dtype_t dtype, void* stream) {
   gemm_status_t st = check_ffn(h, T, D, F, act, dtype);
   if (st != GEMM_OK) return st;
-  if (T == 0 || D == 0) return GEMM_OK;
+  if (T == 0) return GEMM_OK;
+  if (D == 0) {  // y has no elements; g and u are empty sums
+    if (!gu || F == 0) return GEMM_OK;
+    DeviceGuard g(h->device);
+    if (!g.ok) return GEMM_ERR_CUDA;
+    if (!on_device(gu, h->device)) return GEMM_ERR_INVALID_ARG;
+    return cudaMemsetAsync(gu, 0, T * 4 * F, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GEMM_OK
+                                                                                              : GEMM_ERR_CUDA;
+  }
   for (auto [ld, cols] : {std::pair<int64_t, int64_t>(ldx, D), {ldw_in, D}, {ldw_down, F}, {ldy, D}})
     if ((st = check_ld(ld, cols)) != GEMM_OK) return st;
   if (!aligned16(x) || !aligned16(w_in) || !aligned16(w_down) || !aligned16(y) || !aligned16(gu) ||

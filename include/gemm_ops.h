@@ -79,9 +79,9 @@ GEMM_API uint64_t gemm_ops_launch_count(gemm_ops_t ops);
  *            for the backward pass
  * g, u and act(g) * u are fp32 until h is rounded to 16 bits as an operand of
  * the second product.  D and F are multiples of 8, pointers 16-byte aligned,
- * row distances multiples of 8 (GEMM_ERR_ALIGNMENT otherwise).  T == 0 or
- * D == 0: nothing to do; F == 0: y is zero.  Infinities and NaN go where the
- * formula puts them (silu and gelu of a gate of -inf are NaN).
+ * row distances multiples of 8 (GEMM_ERR_ALIGNMENT otherwise).  T == 0:
+ * nothing to do; D == 0: gu is zero; F == 0: y is zero.  Infinities and NaN go
+ * where the formula puts them (silu and gelu of a gate of -inf are NaN).
  * workspace: gemm_gated_ffn_workspace(ops, T, D, F) bytes, 256-byte aligned. */
 GEMM_API size_t gemm_gated_ffn_workspace(gemm_ops_t ops, int64_t T, int64_t D, int64_t F);
 GEMM_API gemm_status_t gemm_gated_ffn(gemm_ops_t ops, const void* x, int64_t ldx, const void* w_in,
