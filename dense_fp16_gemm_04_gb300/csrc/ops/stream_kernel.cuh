@@ -27,7 +27,8 @@
 // product more, of a matrix of ones with the same x.  Products of 16-bit x and
 // O + q are exact; the offset makes the fp32 sum's roundings at most 16 to 30
 // times those of q x alone, 2^-20 of the group's size, far below the 16-bit
-// result's own rounding.  The scale multiplies the finished fp32 sum.
+// result's own rounding.  The scale multiplies the finished fp32 sum.  A sum that
+// does not come out finite is taken again product by product (direct_sum).
 //
 // A lane's 16 bytes are 32 codes of one row, so the four lanes of a row hold
 // 128 k: one group, two, or four.  Smaller groups are kept apart in one of two
@@ -120,6 +121,36 @@ __device__ __forceinline__ void offset_codes(uint32_t w, uint32_t (&p)[4]) {
 // The aligned 4-byte word that holds *p.
 __device__ __forceinline__ const void* word_of(const void* p) {
   return reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(3));
+}
+
+// Token tk's sum with row n of W (gated: of half m) over k0 <= k < k1 (multiples
+// of 32), product by product as the formula has it.
+template <bool kBf16>
+__device__ __forceinline__ float direct_sum(const StreamArgs& a, int32_t tk, int32_t n, int32_t m, int32_t k0,
+                                            int32_t k1) {
+  const int64_t groups = a.K >> a.group_shift, row = m * a.up_s + n * groups;
+  const uint16_t* const x = a.x + tk * a.ldx;
+  const uint8_t* const codes = static_cast<const uint8_t*>(a.w) + m * a.up_w + n * a.ldw;
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int32_t k = k0; k < k1; k += 8) {
+    const int64_t j = row + (k >> a.group_shift);
+    const float scale = widen16(kBf16, a.scales[j]);
+    const int32_t zero = a.zeros ? a.zeros[j] : 8;
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + (k >> 1));
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const int32_t q = static_cast<int32_t>(w >> (4 * i) & 15) - zero;
+      sum = fmaf(scale * static_cast<float>(q), widen16(kBf16, x[k + i]), sum);
+    }
+  }
+  return sum;
+}
+
+template <bool kBf16>
+__device__ __noinline__ float direct_sum_call(const StreamArgs& a, int32_t tk, int32_t n, int32_t m, int32_t k0,
+                                              int32_t k1) {
+  return direct_sum<kBf16>(a, tk, n, m, k0, k1);
 }
 
 template <bool kBf16, int kW, bool kGlu, int kNT>
@@ -482,6 +513,19 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps, 1) stream_kernel(const S
       const int tok = q % kNT * kTok + col / kGroups;
       const int32_t n = tile * kTileN + q / kNT * 16 + ((e >> 3) & 15), tk = t0 + tok;
       if (n >= a.N || tok >= tokens || col % kGroups != 0) continue;
+      if constexpr (kW4) {
+        // An infinite x, or one whose products with O + q overflow, leaves infinity
+        // less infinity where the formula has a signed infinity or a finite sum.
+        // Inline or as a call by what the loop over blocks keeps in registers: plain
+        // products of 9 to 16 tokens, groups of 64 (fp16, 16 x 8192 x 8192), 27.6 us
+        // inline and 23.4 as a call; of 128 22.0 and 22.7; one token (4096 x 4096,
+        // groups of 128) 4.3 and 4.8.
+        constexpr auto sum = kNT == 2 && !kGlu && kTurns > 1 ? direct_sum_call<kBf16> : direct_sum<kBf16>;
+        const int32_t k_end = min(b1 * kBK, a.K);
+#pragma unroll
+        for (int m = 0; m < kEach; ++m)
+          if (!isfinite(v[m])) v[m] = sum(a, tk, n, m, k_begin, k_end);
+      }
       if (gridDim.y > 1) {
 #pragma unroll
         for (int m = 0; m < kEach; ++m)

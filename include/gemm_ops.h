@@ -118,9 +118,10 @@ GEMM_API gemm_status_t gemm_gated_ffn_backward(
  * 8 * 65535.  x and codes 16-byte aligned, ldx a
  * multiple of 8 (GEMM_ERR_ALIGNMENT); N and ldy are free; K is at most 2^28.
  * A group's sum of x (O + q - (O + zero)), O = 64 (fp16) or 128 (bf16), and its
- * product with the scale are fp32; the products x (O + q) are exact.  So x
- * above 2^100 may overflow on the way, and a token with an infinite x becomes
- * NaN.
+ * product with the scale are fp32; the products x (O + q) are exact.  A sum that
+ * does not come out finite so (an infinite x, or one whose products with O + q
+ * overflow) is taken again, product by product (1 ms for 8192 x 8192): infinities
+ * and NaN go where the formula puts them.
  * workspace: gemm_w4_workspace(ops, T, N, K, gated) bytes (none for most
  * shapes), 256-byte aligned. */
 GEMM_API size_t gemm_w4_workspace(gemm_ops_t ops, int64_t T, int64_t N, int64_t K, int32_t gated);

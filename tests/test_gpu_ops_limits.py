@@ -4,6 +4,8 @@ Bounds as in test_gpu_ops.py."""
 import pytest
 import torch
 
+from test_gpu_ops import F64, check, make_w4, sum_eps, w4_ref
+
 pytestmark = pytest.mark.gpu
 
 
@@ -25,3 +27,76 @@ def test_ffn_of_empty_rows_keeps_zeros(g, T):
     assert y.shape == (T, 0) and gu.shape == (T, 2 * F) and not gu.any()
     assert g.gated_ffn(torch.empty(T, 0, dtype=dt, device="cuda"), torch.empty(0, 0, dtype=dt, device="cuda"),
                        torch.empty(0, 0, dtype=dt, device="cuda"), save=True)[1].shape == (T, 0)
+
+
+# ------------------------------------------------------------ 4-bit products --
+def same_specials(got, ref):
+    return (torch.equal(got.isnan(), ref.isnan()) and torch.equal(got.isposinf(), ref.isposinf()) and
+            torch.equal(got.isneginf(), ref.isneginf()))
+
+
+def w4_product(x, w):
+    """x W^T in 64 bits, product by product: infinities as the formula has them."""
+    return (x.to(F64).unsqueeze(1) * w).sum(-1)
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T", [1, 3, 5, 9, 17])
+def test_w4_infinite_x(g, T, group, dt):
+    """An infinite x makes each of its token's sums a signed infinity, or NaN where
+    its weight is zero or infinities of both signs meet; other tokens are as before."""
+    for K, zeros in ((512, True), (352 // group * group, False), (9 * group, True)):
+        x, codes, scales, z = make_w4(T, 50, K, group, zeros, dt, seed=T)
+        w = w4_ref(codes, scales, z)
+        before = g.w4_linear(x, codes, scales, z)
+        x[0, 77] = float("inf")
+        x[T // 2, 30] = float("-inf")
+        x[T - 1, K - 1] = float("inf")
+        got, ref = g.w4_linear(x, codes, scales, z), w4_product(x, w)
+        assert same_specials(got, ref)
+        rest = [t for t in range(T) if t not in (0, T // 2, T - 1)]
+        assert torch.equal(got[rest], before[rest])
+        x[0, 5] = float("nan")
+        assert g.w4_linear(x, codes, scales, z)[0].isnan().all()
+        x[0, 5] = 1.0
+        p = w4_product(x, w)
+        for act, ref in (("relu", p[:, :25].clamp_min(0) * p[:, 25:]), ("silu", p[:, :25] * torch.sigmoid(p[:, :25]) * p[:, 25:])):
+            assert same_specials(g.w4_gated(x, codes, scales, z, act=act), ref)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T", [1, 4, 11])
+def test_w4_very_large_x(g, T, group):
+    """x up to the type's largest: its products with the codes' offset overflow,
+    its products with the weights do not."""
+    K, dt = 640, torch.bfloat16
+    x, codes, scales, z = make_w4(T, 40, K, group, True, dt, seed=T)
+    x[0, 77], x[T - 1, 300] = 2.0 ** 126, -3e38
+    scales *= 2.0 ** -8
+    w = w4_ref(codes, scales, z)
+    check(g.w4_linear(x, codes, scales, z), w4_product(x, w), sum_eps(K) * (x.to(F64).abs() @ w.abs().t()), dt, "y")
+
+
+def test_w4_infinite_x_over_slices(g):
+    """K cut over CTAs: the slice that meets the infinity sums its own part."""
+    K, dt = 16384, torch.float16
+    x, codes, scales, z = make_w4(3, 33, K, 64, True, dt)
+    for at in (0, 8191, K - 1):
+        y = x.clone()
+        y[1, at] = float("-inf")
+        assert same_specials(g.w4_linear(y, codes, scales, z), w4_product(y, w4_ref(codes, scales, z)))
+
+
+def test_w4_infinite_scale(g):
+    """An infinite scale in the last group of rows that end inside a block."""
+    for group in (32, 64):
+        K = 3 * group
+        x, codes, scales, z = make_w4(2, 20, K, group, False, torch.float16)
+        x = x.abs()
+        codes[7, K // 2 - group // 2:] = 0xff  # weights of one sign: 7 times the scale
+        scales[7, 2] = float("inf")
+        got = g.w4_linear(x, codes, scales, z)
+        assert torch.isposinf(got[:, 7]).all()
+        keep = torch.arange(20, device="cuda") != 7
+        assert torch.isfinite(got[:, keep]).all()
