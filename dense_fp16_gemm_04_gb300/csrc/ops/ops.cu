@@ -106,7 +106,11 @@ gemm_status_t check_bufs(const gemm_ops_s* h, const Buf (&b)[kN]) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-bool dim_ok(int64_t v) { return v >= 0 && v <= INT32_MAX; }
+// The kernels' 32-bit counters of rows and columns run past the end of a matrix
+// by less than a tile (256 and 192 columns more), or by the stride of a loop: 256
+// columns, or the rows of one round of CTAs, 8 per SM.
+constexpr int64_t kMaxLength = INT32_MAX - 4095;
+bool dim_ok(int64_t v) { return v >= 0 && v <= kMaxLength; }
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int64_t cdiv(int64_t v, int64_t m) { return (v + m - 1) / m; }
 
@@ -849,7 +853,7 @@ gemm_status_t gemm_w4_gated(gemm_ops_t h, const void* x, int64_t ldx, const void
 }
 
 size_t gemm_orthogonalize_workspace(gemm_ops_t h, int64_t batch, int64_t M, int64_t N) {
-  if (!h || batch <= 0 || M <= 0 || N <= 0) return 0;
+  if (!h || batch <= 0 || M <= 0 || N <= 0 || batch > 65535 || !dim_ok(M) || !dim_ok(N)) return 0;
   return ortho_space(batch, M, N).total;
 }
 

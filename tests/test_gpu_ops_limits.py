@@ -100,3 +100,27 @@ def test_w4_infinite_scale(g):
         assert torch.isposinf(got[:, 7]).all()
         keep = torch.arange(20, device="cuda") != 7
         assert torch.isfinite(got[:, keep]).all()
+
+
+# ------------------------------------------------------ orthogonalised update --
+LONGEST = 2 ** 31 - 4096
+
+
+def test_orthogonalize_longest_rows(g):
+    """The kernels' 32-bit counters step past the end of a row: the longest they
+    can is taken and right to its end, a longer one refused before any launch."""
+    lib, h = g.default_ops()._lib, g.default_ops()._h
+    for M, N in ((1, LONGEST), (LONGEST, 1)):
+        assert lib.gemm_orthogonalize_workspace(h, 1, M, N) > 0
+    for batch, M, N in ((1, 1, LONGEST + 1), (1, LONGEST + 1, 1), (1, 1, 2 ** 31 - 1), (1, 2 ** 62, 2 ** 62), (65536, 1, 1)):
+        assert lib.gemm_orthogonalize_workspace(h, batch, M, N) == 0
+    m = torch.zeros(1, 2 ** 31 - 100, dtype=torch.float16, device="cuda")
+    with pytest.raises(g.GemmError) as e:
+        g.orthogonalize(m)
+    assert e.value.status == 1
+    at = [0, 255, 2 ** 30 + 7, LONGEST - 1]
+    m[0, at] = 3.0
+    o = g.orthogonalize(m[:, :LONGEST], steps=0, eps=0.0)
+    g.default_ops().check_error()
+    assert (o[0, at] == 0.5).all()
+    assert int((o != 0).sum()) == len(at)
