@@ -424,7 +424,8 @@ constexpr int64_t kFewG32 = stream_tokens(kW4G32Few), kFewG64 = stream_tokens(kW
 
 template <bool kGlu>
 size_t w4_workspace(gemm_ops_s* h, int64_t T, int64_t N, int64_t K) {
-  if (!h || T <= 0 || N <= 0 || K <= 0 || K / 2 > kMaxStreamRow) return 0;
+  // No group divides any other K: the product refuses it.
+  if (!h || T <= 0 || N <= 0 || K <= 0 || K % 32 != 0 || K / 2 > kMaxStreamRow) return 0;
   // Whatever the groups.
   return std::max({T <= kFewG32 ? stream_partial_bytes<kW4G32Few, kGlu>(h, T, N, K)
                                 : stream_partial_bytes<kW4G32, kGlu>(h, T, N, K),

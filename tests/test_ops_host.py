@@ -6,6 +6,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -101,3 +102,33 @@ def test_quantise_refusals():
             g.w4_quantize(w, group)
     codes, scales, _ = g.w4_quantize(w, 32)
     assert (codes == 0x88).all() and (scales == 0).all()
+
+
+# Sizes of workspaces depend on the handle's number of SMs alone (its second
+# word): a stand-in for a handle does where there is no device.
+SIZES = """
+import ctypes, sys
+import dense_fp16_gemm_04_gb300 as g
+h = (ctypes.c_int32 * 256)(0, 152)
+fn = getattr(g.load(), sys.argv[1])
+fn.restype = ctypes.c_size_t
+print(fn(h, *map(ctypes.c_int64, map(int, sys.argv[2:]))))
+"""
+
+
+def workspace(name, *sizes):
+    """The size that a function returns, in a process of its own: what it does
+    wrong may end the process."""
+    r = subprocess.run([sys.executable, "-c", SIZES, name, *map(str, sizes)], cwd=ROOT, capture_output=True, text=True,
+                       timeout=60)
+    assert r.returncode == 0, (name, sizes, r.returncode, r.stderr)
+    return int(r.stdout)
+
+
+@pytest.mark.parametrize("K", [1, 31, 33, 4095])
+def test_w4_workspace_of_rows_without_whole_groups(lib, K):
+    """No group divides K: the product refuses it, and its workspace is 0 bytes
+    (rows of K = 1 have no bytes to divide by)."""
+    for gated in (0, 1):
+        assert workspace("gemm_w4_workspace", 1, 8, K, gated) == 0
+        assert workspace("gemm_w4_workspace", 16, 8, 32 * 512, gated) > 0
