@@ -422,10 +422,13 @@ bool set_stream_attr() {
 // in turn 18.1 and 18.4 us.
 constexpr int64_t kFewG32 = stream_tokens(kW4G32Few), kFewG64 = stream_tokens(kW4G64Few);
 
+constexpr int64_t kMaxW4Tokens = 8 * 65535;  // tiles of 8 and more in a grid's third dimension
+
 template <bool kGlu>
 size_t w4_workspace(gemm_ops_s* h, int64_t T, int64_t N, int64_t K) {
   // No group divides any other K: the product refuses it.
-  if (!h || T <= 0 || N <= 0 || K <= 0 || K % 32 != 0 || K / 2 > kMaxStreamRow) return 0;
+  if (!h || T <= 0 || N <= 0 || K <= 0 || K % 32 != 0 || K / 2 > kMaxStreamRow || T > kMaxW4Tokens)
+    return 0;
   // Whatever the groups.
   return std::max({T <= kFewG32 ? stream_partial_bytes<kW4G32Few, kGlu>(h, T, N, K)
                                 : stream_partial_bytes<kW4G32, kGlu>(h, T, N, K),
@@ -481,10 +484,14 @@ int max_clusters() {
   return n;
 }
 
+bool ffn_dims_ok(int64_t T, int64_t D, int64_t F) {
+  return dim_ok(T) && dim_ok(D) && dim_ok(F) && F <= INT32_MAX / 2;
+}
+
 // Checks shared by the block's two passes.
 gemm_status_t check_ffn(const gemm_ops_s* h, int64_t T, int64_t D, int64_t F, gemm_act_t act,
                         gemm_dtype_t dtype) {
-  if (!h || !dim_ok(T) || !dim_ok(D) || !dim_ok(F) || F > INT32_MAX / 2) return GEMM_ERR_INVALID_ARG;
+  if (!h || !ffn_dims_ok(T, D, F)) return GEMM_ERR_INVALID_ARG;
   if (act < GEMM_ACT_SILU || act > GEMM_ACT_RELU) return GEMM_ERR_INVALID_ARG;
   if (dtype != GEMM_F16 && dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;
   if (D % 8 != 0 || F % 8 != 0) return GEMM_ERR_ALIGNMENT;
@@ -625,7 +632,7 @@ gemm_status_t gemm_ops_set_watchdog(gemm_ops_t h, uint64_t timeout_ns, int32_t s
 uint64_t gemm_ops_launch_count(gemm_ops_t h) { return h ? h->launches.load() : 0; }
 
 size_t gemm_gated_ffn_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t F) {
-  if (!h || T <= 0 || D <= 0 || F <= 0) return 0;
+  if (!h || T <= 0 || D <= 0 || F <= 0 || !ffn_dims_ok(T, D, F)) return 0;
   size_t s = hidden_bytes(T, F);
   if (T <= kMaxStreamTokens)
     s += std::max(stream_partial_bytes<kW16, true>(h, T, F, D), stream_partial_bytes<kW16, false>(h, T, D, F));
@@ -710,7 +717,7 @@ gemm_status_t gemm_gated_ffn(gemm_ops_t h, const void* x, int64_t ldx, const voi
 }
 
 size_t gemm_gated_ffn_backward_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t F) {
-  if (!h || T <= 0 || D <= 0 || F <= 0) return 0;
+  if (!h || T <= 0 || D <= 0 || F <= 0 || !ffn_dims_ok(T, D, F)) return 0;
   return 3 * hidden_bytes(T, F);
 }
 
@@ -787,7 +794,7 @@ static gemm_status_t w4_run(gemm_ops_t h, const void* x, int64_t ldx, const void
                             const void* scales, const void* zeros, void* y, int64_t ldy, void* workspace,
                             size_t workspace_bytes, int64_t T, int64_t N, int64_t K, int64_t group,
                             gemm_act_t act, gemm_dtype_t dtype, bool gated, void* stream) {
-  if (!h || !dim_ok(T) || !dim_ok(N) || !dim_ok(K) || N > INT32_MAX / 2 || T > 8 * 65535)
+  if (!h || !dim_ok(T) || !dim_ok(N) || !dim_ok(K) || N > INT32_MAX / 2 || T > kMaxW4Tokens)
     return GEMM_ERR_INVALID_ARG;
   if (act < GEMM_ACT_SILU || act > GEMM_ACT_RELU) return GEMM_ERR_INVALID_ARG;
   if (dtype != GEMM_F16 && dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;

@@ -132,3 +132,14 @@ def test_w4_workspace_of_rows_without_whole_groups(lib, K):
     for gated in (0, 1):
         assert workspace("gemm_w4_workspace", 1, 8, K, gated) == 0
         assert workspace("gemm_w4_workspace", 16, 8, 32 * 512, gated) > 0
+
+
+def test_workspaces_of_refused_lengths(lib):
+    """Lengths past the limits: 0 bytes at once, not a plan for them."""
+    top = 2 ** 31 - 4096
+    for name in ("gemm_gated_ffn_workspace", "gemm_gated_ffn_backward_workspace"):
+        assert workspace(name, 1, 8, 8) > 0 and workspace(name, 1, top, 8) > 0
+        for sizes in ((1, 2 ** 40, 8), (1, top + 1, 8), (2 ** 62, 8, 8), (16, 8, 2 ** 30), (16, 2 ** 62, 2 ** 62)):
+            assert workspace(name, *sizes) == 0, (name, sizes)
+    for sizes in ((8 * 65535 + 1, 1, 4096, 0), (2 ** 62, 1, 4096, 1), (16, 1, 2 ** 40, 0)):
+        assert workspace("gemm_w4_workspace", *sizes) == 0, sizes
