@@ -311,6 +311,7 @@ struct StreamPlan {
 };
 
 constexpr size_t kStreamSmem = 226 * 1024;
+constexpr int64_t kMaxSlices = 65535;  // a grid's second dimension
 
 // 8-column tiles per CTA.
 template <int kW>
@@ -326,14 +327,19 @@ StreamPlan stream_plan(const gemm_ops_s* h, int64_t T, int64_t N, int64_t K) {
   // Enough warps that each keeps a block or two of a tile; the rest of the
   // parallelism comes from tiles, or from cutting K where they are few.
   p.warps = blocks >= 16 ? 16 : blocks >= 8 ? 8 : 4;
-  p.ring = kStreamMaxRing;
-  p.slices = std::max<int64_t>(1, std::min(h->num_sms / tiles, blocks / (2 * p.warps)));
   auto smem = [&] {  // the warps' sums, their blocks in flight, and x
     return static_cast<size_t>(p.warps) * (2 * 2 * nt * 128 * sizeof(float) + p.ring * stream_slot_bytes(kW)) +
            static_cast<size_t>(cdiv(blocks, p.slices)) * bk * held * 2 + kStreamHead;
   };
-  while (p.ring > 2 && smem() > kStreamSmem) --p.ring;
-  while (p.slices < blocks && smem() > kStreamSmem) ++p.slices;
+  for (;; p.warps /= 2) {
+    p.ring = kStreamMaxRing;
+    p.slices = std::max<int64_t>(1, std::min(h->num_sms / tiles, blocks / (2 * p.warps)));
+    while (p.ring > 2 && smem() > kStreamSmem) --p.ring;
+    while (p.slices < blocks && smem() > kStreamSmem) ++p.slices;
+    // The longest rows of many tokens: fewer warps leave room for more of x in
+    // each slice (2^28 codes a row, 16 tokens: 104858 slices with 16, 55189 with 8).
+    if (p.slices <= kMaxSlices || p.warps == 4) break;
+  }
   while (p.ring < kStreamMaxRing) {  // what the slices freed
     ++p.ring;
     if (smem() > kStreamSmem) {

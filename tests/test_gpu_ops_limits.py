@@ -124,3 +124,23 @@ def test_orthogonalize_longest_rows(g):
     g.default_ops().check_error()
     assert (o[0, at] == 0.5).all()
     assert int((o != 0).sum()) == len(at)
+
+
+def test_w4_longest_rows(g):
+    """Rows of 2^28 codes for 16 tokens: K cut into more slices than 16 warps a CTA
+    would leave within a grid.  A few ones in x pick weights from every part."""
+    T, N, K, dt = 16, 2, 2 ** 28, torch.float16
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    codes = torch.randint(0, 256, (N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    scales = torch.full((N, K // 128), 0.25, dtype=dt, device="cuda")
+    x = torch.zeros(T, K, dtype=dt, device="cuda")
+    at = torch.cat((torch.tensor([0, 1, K // 2 - 1, K - 1], device="cuda"), torch.randint(0, K, (28,), generator=gen, device="cuda")))
+    on = torch.randint(0, 2, (T, at.numel()), generator=gen, device="cuda").to(dt)
+    x[:, at] = on
+    on = x[:, at].to(F64)  # what stands there where two positions are one
+    first = (at.unsqueeze(0) == at.unsqueeze(1)).int().argmax(1) == torch.arange(at.numel(), device="cuda")
+    q = (codes[:, at // 2] >> (4 * (at % 2)).to(torch.uint8) & 15).to(F64)
+    want = (on * first) @ ((q - 8) * 0.25).t()
+    got = g.w4_linear(x, codes, scales)
+    g.default_ops().check_error()
+    assert torch.equal(got.to(F64), want)

@@ -143,3 +143,12 @@ def test_workspaces_of_refused_lengths(lib):
             assert workspace(name, *sizes) == 0, (name, sizes)
     for sizes in ((8 * 65535 + 1, 1, 4096, 0), (2 ** 62, 1, 4096, 1), (16, 1, 2 ** 40, 0)):
         assert workspace("gemm_w4_workspace", *sizes) == 0, sizes
+
+
+@pytest.mark.parametrize("T", [1, 8, 16])
+def test_w4_longest_rows_fit_a_grid(lib, T):
+    """K is cut into as many slices as a grid's second dimension holds, at most:
+    their sums' workspace is 4 bytes per slice, token and column."""
+    for K in (2 ** 28, 2 ** 28 - 32, 2 ** 27, 3 * 2 ** 25):
+        for gated in (0, 1):
+            assert workspace("gemm_w4_workspace", T, 1, K, gated) <= 65535 * T * 4 * (1 + gated)
