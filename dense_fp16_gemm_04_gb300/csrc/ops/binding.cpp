@@ -9,6 +9,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -71,6 +72,21 @@ const at::Tensor* tensor(PyObject* o, const char* name) {
   return nullptr;
 }
 
+// The operators record no graph and carry no tangents on: a tensor that asks for
+// either is refused, rather than its gradient lost in silence.
+bool no_graph(const at::Tensor& t, const char* name) {
+  const auto& mode = c10::AutogradState::get_tls_state();
+  const char* asks = mode.get_grad_mode() && t.requires_grad()               ? "requires grad"
+                     : mode.get_fw_grad_mode() && t._fw_grad(0).defined() ? "has a forward-mode tangent"
+                                                                            : nullptr;
+  if (!asks) return true;
+  PyErr_Format(PyExc_RuntimeError,
+               "%s %s, and this operator records no graph: call it under torch.no_grad() or on detached tensors "
+               "(gated_ffn_backward computes the gradients of gated_ffn)",
+               name, asks);
+  return false;
+}
+
 // Reads o, a tensor that has to have this type and be on this device, and its
 // row distance; rows and cols, where not -1, are what it has to have.
 bool read(PyObject* o, const char* name, at::ScalarType dtype, int64_t index, int64_t rows, int64_t cols,
@@ -81,6 +97,7 @@ bool read(PyObject* o, const char* name, at::ScalarType dtype, int64_t index, in
     PyErr_Format(PyExc_TypeError, "%s must be %s, got %s", name, type_name(dtype), type_name(t->scalar_type()));
     return false;
   }
+  if (!no_graph(*t, name)) return false;
   if (!t->is_cuda()) {
     PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", name);
     return false;
@@ -339,6 +356,17 @@ PyObject* py_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// (tensor, name): refuses as no_graph does.
+PyObject* py_no_graph(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 2) return PyErr_Format(PyExc_TypeError, "%zd arguments, 2 expected", n);
+  const char* name = PyUnicode_AsUTF8(a[1]);
+  const at::Tensor* t = name ? tensor(a[0], name) : nullptr;
+  if (!t || !no_graph(*t, name)) return nullptr;
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
 // (GemmError, then the addresses of the seven C functions)
 PyObject* py_setup(PyObject*, PyObject* args) {
   unsigned long long f[7];
@@ -360,6 +388,7 @@ PyMethodDef methods[] = {
     {"gated_ffn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_ffn)), METH_FASTCALL, nullptr},
     {"gated_ffn_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_bwd)), METH_FASTCALL, nullptr},
     {"w4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_w4)), METH_FASTCALL, nullptr},
+    {"no_graph", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_no_graph)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -8,6 +8,11 @@ sm_103a kernels of ``libgb300gemm.so``.  Tensors are CUDA tensors of one device,
 float16 or bfloat16; results and workspaces come from torch's allocator, on the
 stream of the call (the current one, or ``stream``).  There is no fallback: wrong arguments and other devices raise.
 
+The operators record no graph.  A tensor that requires grad (while gradients are
+recorded) or has a forward-mode tangent is refused with a RuntimeError: call them
+under ``torch.no_grad()`` or on detached tensors, or from the methods of a
+``torch.autograd.Function``, whose backward is :func:`gated_ffn_backward`.
+
     >>> import torch, dense_fp16_gemm_04_gb300 as g
     >>> x = torch.randn(4096, 1024, device="cuda", dtype=torch.float16)
     >>> w_in = torch.randn(2 * 4096, 1024, device="cuda", dtype=torch.float16) / 32
@@ -158,6 +163,9 @@ class Ops:
     def orthogonalize(self, m, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, dtype=None, out=None, stream=None):
         if m.dtype not in _DTYPE:
             raise TypeError(f"m must be float16, bfloat16 or float32, got {m.dtype}")
+        for name, t in (("m", m), ("out", out)):
+            if t is not None:
+                self._b.no_graph(t, name)
         if m.device != self.device:
             raise ValueError(f"m must be on {self.device}, got {m.device}")
         if m.dim() not in (2, 3):
@@ -254,7 +262,8 @@ def w4_gated(x, codes, scales, zeros=None, act="silu", out=None, stream=None, op
 def w4_quantize(w, group=128, zero_point=False):
     """Codes, scales and zeros of w [N, K] for :func:`w4_linear`, by rounding to
     the nearest level: symmetric about code 8, or (``zero_point``) spread over
-    each group's range, zero included."""
+    each group's range, zero included.  No gradient goes back to w."""
+    w = w.detach()
     N, K = w.shape
     if group < 32 or group & (group - 1) or K % group:
         raise ValueError(f"group must be a power of two from 32 on that divides K = {K}, got {group}")

@@ -4,7 +4,7 @@ Bounds as in test_gpu_ops.py."""
 import pytest
 import torch
 
-from test_gpu_ops import F64, check, make_w4, sum_eps, w4_ref
+from test_gpu_ops import F64, check, make_ffn, make_w4, sum_eps, w4_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +144,39 @@ def test_w4_longest_rows(g):
     got = g.w4_linear(x, codes, scales)
     g.default_ops().check_error()
     assert torch.equal(got.to(F64), want)
+
+
+# --------------------------------------------------------------------- autograd --
+def test_tensors_that_ask_for_a_graph_are_refused(g):
+    """Whichever tensor it is, the output among them, while gradients are recorded;
+    without, the call is the one on plain tensors."""
+    dt = torch.float16
+    x, w_in, w_down, dy = make_ffn(4, 64, 128, dt)
+    gu = torch.randn(4, 256, device="cuda").to(dt)
+    xm, codes, scales, z = make_w4(4, 64, 256, 64, True, dt)
+    m = torch.randn(40, 30, device="cuda")
+    def empty(*s):
+        return torch.empty(*s, dtype=dt, device="cuda")
+    n = 0
+    for fn, args, out in ((g.gated_ffn, (x, w_in, w_down), empty(4, 64)), (g.gated_ffn_backward, (dy, x, w_in, w_down, gu), None),
+                          (g.w4_linear, (xm, codes, scales, z), empty(4, 64)), (g.w4_gated, (xm, codes, scales, z), empty(4, 32)),
+                          (g.orthogonalize, (m,), torch.empty_like(m))):
+        want = fn(*args)
+        for i, a in enumerate(args):
+            if not a.is_floating_point():
+                continue
+            other = list(args)
+            other[i] = torch.nn.Parameter(a.clone())
+            with pytest.raises(RuntimeError, match="requires grad"):
+                fn(*other)
+            for mode in (torch.no_grad, torch.inference_mode):
+                with mode():
+                    got = fn(*other)
+                assert all(torch.equal(p, q) for p, q in zip(*((t if isinstance(t, tuple) else (t,)) for t in (got, want))))
+            n += 1
+        if out is not None:
+            with pytest.raises(RuntimeError, match="requires grad"):
+                fn(*args, out=out.requires_grad_())
+            with torch.no_grad():
+                assert torch.equal(fn(*args, out=out), want)
+    assert n == 13

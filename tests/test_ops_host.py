@@ -152,3 +152,38 @@ def test_w4_longest_rows_fit_a_grid(lib, T):
     for K in (2 ** 28, 2 ** 28 - 32, 2 ** 27, 3 * 2 ** 25):
         for gated in (0, 1):
             assert workspace("gemm_w4_workspace", T, 1, K, gated) <= 65535 * T * 4 * (1 + gated)
+
+
+class Unbound:
+    """The operators' methods on no handle: what the binding refuses before it needs one."""
+    def __init__(self):
+        from dense_fp16_gemm_04_gb300 import ops
+        self._b, self._addr, self.index, self._ops = ops._load_binding(), 0, 0, ops.Ops
+
+    def __getattr__(self, name):
+        return getattr(self._ops, name).__get__(self)
+
+
+def test_tensors_that_ask_for_a_graph_are_refused(lib):
+    """Not answered without one; under no_grad they go on to the next check (the
+    device)."""
+    import torch.autograd.forward_ad as fw
+    h = lambda *s: torch.zeros(*s, dtype=torch.float16)
+    o, codes = Unbound(), torch.zeros(8, 32, dtype=torch.uint8)
+    calls = (lambda x: o.gated_ffn(x, h(256, 64), h(64, 128)),
+             lambda x: o.gated_ffn_backward(h(4, 64), x, h(256, 64), h(64, 128), h(4, 256)),
+             lambda x: o.w4_linear(x, codes, h(8, 2)), lambda x: o.w4_gated(x, codes, h(8, 2)))
+    for call in calls:
+        with pytest.raises(RuntimeError, match="requires grad"):
+            call(torch.nn.Parameter(h(4, 64)))
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            call(torch.nn.Parameter(h(4, 64)))
+        with fw.dual_level(), pytest.raises(RuntimeError, match="tangent"):
+            call(fw.make_dual(h(4, 64), h(4, 64)))
+    with pytest.raises(RuntimeError, match="requires grad"):
+        o.orthogonalize(torch.zeros(4, 4, requires_grad=True))
+
+
+def test_quantised_weights_leave_the_graph():
+    codes, scales, zeros = g.w4_quantize(torch.nn.Parameter(torch.ones(4, 64)), 32, zero_point=True)
+    assert not (codes.requires_grad or scales.requires_grad or zeros.requires_grad)
