@@ -134,10 +134,18 @@ bool make_map(const gemm_ops_s* h, CUtensorMap* m, const Stack& s, bool bf16, ui
   // promoting their requests to 256 bytes costs more than it saves.
   const CUtensorMapL2promotion l2 = s.pitch % 64 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                                       : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
-  return reinterpret_cast<EncodeTiledFn>(h->encode)(
-             m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-             const_cast<void*>(s.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-             l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&] {
+    return reinterpret_cast<EncodeTiledFn>(h->encode)(
+        m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+        const_cast<void*>(s.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+        l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  // A host thread that has not used CUDA (autograd's, a worker's) has a device but
+  // no context, which the driver's encoder needs: cudaSetDevice makes the primary
+  // one current.
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaSetDevice(h->device) == cudaSuccess) r = encode();
+  return r == CUDA_SUCCESS;
 }
 
 // ---------------------------------------------------------------- launches --

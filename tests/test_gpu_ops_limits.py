@@ -180,3 +180,51 @@ def test_tensors_that_ask_for_a_graph_are_refused(g):
             with torch.no_grad():
                 assert torch.equal(fn(*args, out=out), want)
     assert n == 13
+
+
+# ----------------------------------------------------------------- host threads --
+def test_calls_from_threads_that_have_not_used_cuda(g):
+    """Such a thread has no context until its first CUDA call; each operator makes
+    that call itself."""
+    import threading
+    dt = torch.float16
+    x, w_in, w_down, dy = make_ffn(40, 64, 128, dt)
+    xm, codes, scales, z = make_w4(4, 64, 256, 64, True, dt)
+    m = torch.randn(40, 30, device="cuda")
+    _, gu = g.gated_ffn(x, w_in, w_down, save=True)
+    for fn, args in ((g.gated_ffn, (x, w_in, w_down)), (g.gated_ffn, (x[:2], w_in, w_down)),
+                     (g.gated_ffn_backward, (dy, x, w_in, w_down, gu)), (g.w4_linear, (xm, codes, scales, z)),
+                     (g.w4_gated, (xm, codes, scales, z)), (g.orthogonalize, (m,))):
+        want, got = fn(*args), []
+        def body():
+            try:
+                got.append(fn(*args))
+            except Exception as e:
+                got.append(e)
+        t = threading.Thread(target=body)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert not isinstance(got[0], Exception), (fn.__name__, got[0])
+        assert all(torch.equal(p, q) for p, q in zip(*((v if isinstance(v, tuple) else (v,)) for v in (got[0], want))))
+
+
+def test_gated_block_as_an_autograd_function(g):
+    """The two passes as the methods of a Function: gradients reach the weights."""
+    class Block(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w_in, w_down):
+            y, gu = g.gated_ffn(x, w_in, w_down, save=True)
+            ctx.save_for_backward(x, w_in, w_down, gu)
+            return y
+
+        @staticmethod
+        def backward(ctx, dy):
+            return g.gated_ffn_backward(dy, *ctx.saved_tensors)
+
+    x, w_in, w_down, dy = make_ffn(40, 64, 128, torch.float16)
+    params = [torch.nn.Parameter(t.clone()) for t in (x, w_in, w_down)]
+    Block.apply(*params).backward(dy)
+    _, gu = g.gated_ffn(x, w_in, w_down, save=True)
+    for p, want in zip(params, g.gated_ffn_backward(dy, x, w_in, w_down, gu)):
+        assert torch.equal(p.grad, want)
