@@ -182,6 +182,14 @@ PyObject* result(PyObject* out, int64_t rows, int64_t cols, at::ScalarType dtype
   return Py_NewRef(out);
 }
 
+// A tensor given as `out` has been written: autograd then refuses to use a value
+// saved before.  (Tensors made in inference mode have no version.)
+void wrote(PyObject* out) {
+  if (out == Py_None) return;
+  const at::Tensor& t = THPVariable_Unpack(out);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // The stream of a call: the device's current one, an address, or a torch
 // stream.  What the call allocates belongs to that stream: a workspace of the
 // current stream could be handed out again there while another still uses it.
@@ -269,6 +277,7 @@ PyObject* py_ffn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   st = g_ffn(t.h, x.p, x.ld, wi.p, wi.ld, wd.p, wd.ld, y.p, y.ld, gp, ws.p, need, T, D, F, act, code, stream.s);
   Py_END_ALLOW_THREADS;
   if (failed(st, "gemm_gated_ffn")) return nullptr;
+  wrote(a[7]);
   return save ? PyTuple_Pack(2, out.p, gu.p) : out.release();
   END_HANDLE_TH_ERRORS
 }
@@ -352,6 +361,7 @@ PyObject* py_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
              : g_w4(t.h, x.p, x.ld, codes.p, scales.p, zeros.p, y.p, y.ld, ws.p, need, T, N, K, group, code, stream.s);
   Py_END_ALLOW_THREADS;
   if (failed(st, gated ? "gemm_w4_gated" : "gemm_w4_linear")) return nullptr;
+  wrote(a[7]);
   return out.release();
   END_HANDLE_TH_ERRORS
 }
@@ -363,6 +373,16 @@ PyObject* py_no_graph(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const char* name = PyUnicode_AsUTF8(a[1]);
   const at::Tensor* t = name ? tensor(a[0], name) : nullptr;
   if (!t || !no_graph(*t, name)) return nullptr;
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+// (tensor): it has been written.
+PyObject* py_wrote(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 1) return PyErr_Format(PyExc_TypeError, "%zd arguments, 1 expected", n);
+  if (!tensor(a[0], "out")) return nullptr;
+  wrote(a[0]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -389,6 +409,7 @@ PyMethodDef methods[] = {
     {"gated_ffn_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_bwd)), METH_FASTCALL, nullptr},
     {"w4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_w4)), METH_FASTCALL, nullptr},
     {"no_graph", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_no_graph)), METH_FASTCALL, nullptr},
+    {"wrote", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_wrote)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -182,6 +182,7 @@ class Ops:
                 stream = torch.cuda.ExternalStream(stream, device=self.device)
             with torch.cuda.stream(stream):
                 return self.orthogonalize(m, steps, coeffs, eps, dtype, out)
+        given = out
         if out is None:
             out = torch.empty(m.shape, dtype=dtype, device=self.device)
         elif out.shape != m.shape or out.dtype != dtype or out.device != self.device:
@@ -200,6 +201,8 @@ class Ops:
             self._h, m.data_ptr(), lds[0], lds[1], out.data_ptr(), lds[2], lds[3], ws.data_ptr(), need, B, M, N,
             int(steps), (ctypes.c_float * 3)(*coeffs), float(eps), _DTYPE[m.dtype], _DTYPE[dtype],
             _current_stream(self.index)), "gemm_orthogonalize")
+        if given is not None:
+            self._b.wrote(given)
         return out
 
 

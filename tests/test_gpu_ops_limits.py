@@ -228,3 +228,26 @@ def test_gated_block_as_an_autograd_function(g):
     _, gu = g.gated_ffn(x, w_in, w_down, save=True)
     for p, want in zip(params, g.gated_ffn_backward(dy, x, w_in, w_down, gu)):
         assert torch.equal(p.grad, want)
+
+
+def test_outputs_count_as_written(g):
+    """`out` raises the tensor's version: autograd sees that a value it saved has
+    been overwritten.  Tensors of inference mode, which have none, are written too."""
+    dt = torch.float16
+    x, w_in, w_down, _ = make_ffn(4, 64, 128, dt)
+    xm, codes, scales, z = make_w4(4, 64, 256, 64, True, dt)
+    m = torch.randn(4, 64, device="cuda")
+    for fn, args in ((g.gated_ffn, (x, w_in, w_down)), (g.w4_linear, (xm, codes, scales, z)),
+                     (lambda *a, out: g.w4_gated(*a, out=out[:, :32]), (xm, codes, scales, z)),
+                     (lambda *a, out: g.orthogonalize(*a, out=out, dtype=dt), (m,))):
+        out = torch.ones(4, 64, device="cuda", dtype=dt)
+        leaf = torch.ones(4, 64, device="cuda", dtype=dt, requires_grad=True)
+        y = leaf * out  # saves out
+        before = out._version
+        fn(*args, out=out)
+        assert out._version == before + 1
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+        with torch.inference_mode():
+            frozen = torch.ones(4, 64, device="cuda", dtype=dt)
+        assert torch.equal(fn(*args, out=frozen), fn(*args, out=out))
