@@ -1,9 +1,10 @@
-"""Build the sm_103a CUDA library in-tree with nvcc (no torch, no cmake).
+"""Build the sm_103a CUDA library in-tree with nvcc (no cmake; torch only for the binding).
 
 Produces ``libgb300gemm.so`` next to this file from ``csrc/*.cu`` (the GEMM)
 and ``csrc/ops/*.cu`` (the operators beside it); the compiled code targets
 exactly sm_103a (GB300).  The operators' CPython binding ``_binding*.so``
-(``csrc/ops/binding.cpp``) is built against the installed torch.
+(``csrc/ops/binding.cpp``) is built against the installed torch; without torch
+the library is built alone.
 """
 from __future__ import annotations
 
@@ -52,18 +53,23 @@ def _newer(target, inputs) -> bool:
     return all(os.path.getmtime(p) <= t for p in inputs)
 
 
+def _torch():
+    """The installed torch's folder, or None."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
 def up_to_date() -> bool:
-    return _newer(LIB_PATH, _inputs()) and _newer(BINDING_PATH, _binding_inputs())
+    return _newer(LIB_PATH, _inputs()) and (_torch() is None or _newer(BINDING_PATH, _binding_inputs()))
 
 
 def _binding_inputs():
     return [BINDING_SRC, *sorted(glob.glob(os.path.join(INCLUDE, "*.h"))), os.path.abspath(__file__)]
 
 
-def _build_binding():
+def _build_binding(torch):
     """Start compiling the binding; returns (process, its output, command)."""
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
            "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(_cuda(), "include"), BINDING_SRC,
@@ -75,7 +81,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the library if any source is newer than it; return its path."""
     if not force and up_to_date():
         return LIB_PATH
-    binding, binding_tmp, binding_cmd = _build_binding()
+    torch = _torch()
+    if torch is not None:
+        binding, binding_tmp, binding_cmd = _build_binding(torch)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     nvcc = _nvcc()
     # The CUDA runtime is linked shared: with torch in the process both use one
@@ -88,10 +96,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     res = subprocess.run(cmd, capture_output=True, text=True)
-    said, _ = binding.communicate()
-    if binding.returncode != 0:
-        raise RuntimeError("the binding failed to build:\n" + " ".join(binding_cmd) + "\n" + said)
-    os.replace(binding_tmp, BINDING_PATH)
+    if torch is not None:
+        said, _ = binding.communicate()
+        if binding.returncode != 0:
+            raise RuntimeError("the binding failed to build:\n" + " ".join(binding_cmd) + "\n" + said)
+        os.replace(binding_tmp, BINDING_PATH)
     if res.returncode != 0:
         raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
     if verbose:

@@ -1,0 +1,56 @@
+"""What build() compiles and when, with stand-ins for the compilers (each writes
+its output file and a line to a log) on a copy of the package."""
+import os
+import shutil
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PACKAGE = "dense_fp16_gemm_04_gb300"
+COMPILER = """#!/bin/sh
+echo {name} >> {log}
+while [ "$1" != -o ]; do shift; done
+echo {name} > "$2"
+"""
+
+
+@pytest.fixture
+def tree(tmp_path):
+    """A copy of the package's sources; run(code, ...) runs Python there and
+    returns the compilers it called."""
+    for d in (PACKAGE, "include"):
+        shutil.copytree(os.path.join(ROOT, d), tmp_path / d,
+                        ignore=shutil.ignore_patterns("*.so", "__pycache__", "*.tmp*"))
+    log = tmp_path / "log"
+    for name in ("nvcc", "cxx"):
+        path = tmp_path / name
+        path.write_text(COMPILER.format(name=name, log=log))
+        path.chmod(0o755)
+
+    def run(code, cxx="cxx", fails=False, **env):
+        log.write_text("")
+        r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True,
+                           env=dict(os.environ, NVCC=str(tmp_path / "nvcc"), CXX=shutil.which(cxx) or str(tmp_path / cxx), **env))
+        assert (r.returncode != 0) == fails, r.stderr
+        run.stderr = r.stderr
+        return sorted(log.read_text().split())
+
+    run.path = tmp_path
+    return run
+
+
+BUILD = f"import {PACKAGE} as g; g.build()"
+NO_TORCH = "import sys; sys.modules['torch'] = None; "
+
+
+def test_without_torch_the_library_is_built_alone(tree):
+    assert tree(NO_TORCH + BUILD) == ["nvcc"]
+    assert (tree.path / PACKAGE / "libgb300gemm.so").read_text() == "nvcc\n"
+    assert tree(NO_TORCH + BUILD) == []  # up to date
+
+
+def test_with_torch_the_binding_is_built_too(tree):
+    assert tree(BUILD) == ["cxx", "nvcc"]
+    assert tree(BUILD) == []
