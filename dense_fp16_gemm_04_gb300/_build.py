@@ -78,12 +78,28 @@ def _build_binding(torch):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if any source is newer than it; return its path."""
+    """Compile the library and the binding if any source is newer than them;
+    return the library's path."""
     if not force and up_to_date():
         return LIB_PATH
     torch = _torch()
-    if torch is not None:
+    binding = None
+    if torch is not None and (force or not _newer(BINDING_PATH, _binding_inputs())):
         binding, binding_tmp, binding_cmd = _build_binding(torch)
+    try:
+        if force or not _newer(LIB_PATH, _inputs()):
+            _build_library(verbose)
+    finally:
+        if binding is not None:
+            said, _ = binding.communicate()
+            if binding.returncode == 0:
+                os.replace(binding_tmp, BINDING_PATH)
+    if binding is not None and binding.returncode != 0:
+        raise RuntimeError("the binding failed to build:\n" + " ".join(binding_cmd) + "\n" + said)
+    return LIB_PATH
+
+
+def _build_library(verbose):
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     nvcc = _nvcc()
     # The CUDA runtime is linked shared: with torch in the process both use one
@@ -96,14 +112,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     res = subprocess.run(cmd, capture_output=True, text=True)
-    if torch is not None:
-        said, _ = binding.communicate()
-        if binding.returncode != 0:
-            raise RuntimeError("the binding failed to build:\n" + " ".join(binding_cmd) + "\n" + said)
-        os.replace(binding_tmp, BINDING_PATH)
     if res.returncode != 0:
         raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
     if verbose:
         print(res.stdout + res.stderr)
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH

@@ -54,3 +54,22 @@ def test_without_torch_the_library_is_built_alone(tree):
 def test_with_torch_the_binding_is_built_too(tree):
     assert tree(BUILD) == ["cxx", "nvcc"]
     assert tree(BUILD) == []
+
+
+def test_a_failed_binding_leaves_the_library(tree):
+    """A finished library is kept when the binding does not compile, and is not
+    compiled again for the next try."""
+    assert tree(BUILD, cxx="false", fails=True) == ["nvcc"]
+    assert "the binding failed to build" in tree.stderr
+    assert (tree.path / PACKAGE / "libgb300gemm.so").exists()
+    assert tree(BUILD) == ["cxx"]
+    assert tree(BUILD) == []
+
+
+def test_a_failed_library_leaves_the_binding(tree):
+    (tree.path / "nvcc").write_text("#!/bin/sh\necho nvcc >> %s\nexit 1\n" % (tree.path / "log"))
+    assert tree(BUILD, fails=True) == ["cxx", "nvcc"]
+    assert "nvcc failed" in tree.stderr
+    assert not (tree.path / PACKAGE / "libgb300gemm.so").exists()
+    (tree.path / "nvcc").write_text(COMPILER.format(name="nvcc", log=tree.path / "log"))
+    assert tree(BUILD) == ["nvcc"]
