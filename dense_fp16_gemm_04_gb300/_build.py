@@ -9,6 +9,7 @@ the library is built alone.
 from __future__ import annotations
 
 import glob
+import hashlib
 import importlib.util
 import os
 import shutil
@@ -22,7 +23,6 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libgb300gemm.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 BINDING_SRC = os.path.join(CSRC, "ops", "binding.cpp")
-BINDING_PATH = os.path.join(HERE, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -59,17 +59,34 @@ def _torch():
     return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
 
 
+def binding_path():
+    """Where the binding for the installed torch lies, or None without torch.  It
+    is compiled against torch's C++ classes, so its name holds a hash of which
+    torch that is: another one never loads it."""
+    torch = _torch()
+    if torch is None:
+        return None
+    which = hashlib.sha256(torch.encode())
+    version = os.path.join(torch, "version.py")
+    if os.path.exists(version):
+        with open(version, "rb") as f:
+            which.update(f.read())
+    return os.path.join(HERE, "_binding_" + which.hexdigest()[:8] + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
 def up_to_date() -> bool:
-    return _newer(LIB_PATH, _inputs()) and (_torch() is None or _newer(BINDING_PATH, _binding_inputs()))
+    path = binding_path()
+    return _newer(LIB_PATH, _inputs()) and (path is None or _newer(path, _binding_inputs()))
 
 
 def _binding_inputs():
     return [BINDING_SRC, *sorted(glob.glob(os.path.join(INCLUDE, "*.h"))), os.path.abspath(__file__)]
 
 
-def _build_binding(torch):
+def _build_binding(path):
     """Start compiling the binding; returns (process, its output, command)."""
-    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
+    torch = _torch()
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
            "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(_cuda(), "include"), BINDING_SRC,
@@ -82,10 +99,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return the library's path."""
     if not force and up_to_date():
         return LIB_PATH
-    torch = _torch()
+    path = binding_path()
     binding = None
-    if torch is not None and (force or not _newer(BINDING_PATH, _binding_inputs())):
-        binding, binding_tmp, binding_cmd = _build_binding(torch)
+    if path is not None and (force or not _newer(path, _binding_inputs())):
+        binding, binding_tmp, binding_cmd = _build_binding(path)
     try:
         if force or not _newer(LIB_PATH, _inputs()):
             _build_library(verbose)
@@ -93,7 +110,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if binding is not None:
             said, _ = binding.communicate()
             if binding.returncode == 0:
-                os.replace(binding_tmp, BINDING_PATH)
+                os.replace(binding_tmp, path)
     if binding is not None and binding.returncode != 0:
         raise RuntimeError("the binding failed to build:\n" + " ".join(binding_cmd) + "\n" + said)
     return LIB_PATH

@@ -88,10 +88,11 @@ def _load_binding():
     lib = _lib()
     with _sig_lock:
         if _binding is None:
-            if not os.path.exists(_build.BINDING_PATH):
-                raise ImportError(f"{_build.BINDING_PATH} is missing: build it with "
+            path = _build.binding_path()
+            if not os.path.exists(path):
+                raise ImportError(f"{path} is missing: build it for this torch with "
                                   "dense_fp16_gemm_04_gb300.build()")
-            spec = importlib.util.spec_from_file_location("_binding", _build.BINDING_PATH)
+            spec = importlib.util.spec_from_file_location("_binding", path)
             mod = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(mod)
             fns = ("gemm_gated_ffn_workspace", "gemm_gated_ffn", "gemm_gated_ffn_backward_workspace",

@@ -73,3 +73,20 @@ def test_a_failed_library_leaves_the_binding(tree):
     assert not (tree.path / PACKAGE / "libgb300gemm.so").exists()
     (tree.path / "nvcc").write_text(COMPILER.format(name="nvcc", log=tree.path / "log"))
     assert tree(BUILD) == ["nvcc"]
+
+
+def test_another_torch_gets_a_binding_of_its_own(tree):
+    """A binding is compiled against one torch's classes: after an upgrade in
+    place, or from another folder, it is built again and the old one not loaded."""
+    torch = tree.path / "site" / "torch"
+    torch.mkdir(parents=True)
+    (torch / "__init__.py").write_text("")
+    (torch / "version.py").write_text("__version__ = '1'\n")
+    old = os.path.getmtime(os.path.join(ROOT, "README.md"))
+    env = dict(PYTHONPATH=str(tree.path / "site"))
+    assert tree(BUILD, **env) == ["cxx", "nvcc"] and tree(BUILD, **env) == []
+    (torch / "version.py").write_text("__version__ = '2'\n")
+    os.utime(torch / "version.py", (old, old))  # an installer may keep the files' own dates
+    assert tree(BUILD, **env) == ["cxx"] and tree(BUILD, **env) == []
+    assert tree(BUILD) == ["cxx"]  # the installed one
+    assert len(list((tree.path / PACKAGE).glob("_binding_*.so"))) == 3
