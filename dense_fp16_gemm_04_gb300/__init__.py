@@ -18,6 +18,7 @@ sum_k A[i, k] * B[j, k].
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -27,10 +28,12 @@ __all__ = [
     "build", "load", "Plan", "GemmError", "gemm", "gemm_host", "default_plan",
     "ACC_F32", "ACC_F16", "K_CONTIGUOUS", "MN_CONTIGUOUS", "status_string", "variant_names", "variant_info",
     "LIB_PATH",
-    # Operators beside the GEMM (ops.py; loaded with torch on first use).
-    "Ops", "default_ops", "gated_ffn", "gated_ffn_backward", "w4_linear", "w4_gated", "w4_quantize",
-    "orthogonalize", "NEWTON_SCHULZ",
 ]
+# Operators beside the GEMM (ops.py; loaded with torch on first use).
+_OPS = ("Ops", "default_ops", "gated_ffn", "gated_ffn_backward", "w4_linear", "w4_gated",
+        "w4_quantize", "orthogonalize", "NEWTON_SCHULZ")
+if importlib.util.find_spec("torch") is not None:  # a star import looks every name up
+    __all__ += _OPS
 
 LIB_PATH = _build.LIB_PATH
 ACC_F32 = 0
@@ -386,10 +389,6 @@ def gemm_host(a, b, acc="f32", out=None, stream=None, plan: Plan | None = None):
                           pin_memory=bool(getattr(a, "is_pinned", lambda: False)()))
     (plan or default_plan()).run_host(a, b, out, acc=acc, stream=stream)
     return out
-
-
-_OPS = ("Ops", "default_ops", "gated_ffn", "gated_ffn_backward", "w4_linear", "w4_gated",
-        "w4_quantize", "orthogonalize", "NEWTON_SCHULZ")
 
 
 def __getattr__(name):

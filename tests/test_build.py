@@ -90,3 +90,12 @@ def test_another_torch_gets_a_binding_of_its_own(tree):
     assert tree(BUILD, **env) == ["cxx"] and tree(BUILD, **env) == []
     assert tree(BUILD) == ["cxx"]  # the installed one
     assert len(list((tree.path / PACKAGE).glob("_binding_*.so"))) == 3
+
+
+def test_star_import(tree):
+    """Without torch the GEMM's names; with it the operators' too, torch being
+    loaded when one of them is first looked up."""
+    star = f"from {PACKAGE} import *; assert gemm and Plan"
+    assert tree(NO_TORCH + star + "; assert 'gated_ffn' not in dir()") == []
+    assert tree(star + "; assert gated_ffn and w4_linear and orthogonalize") == []
+    assert tree(f"import sys, {PACKAGE} as g; assert 'torch' not in sys.modules; assert 'Ops' in g.__all__") == []
