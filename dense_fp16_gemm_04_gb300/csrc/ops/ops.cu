@@ -80,13 +80,38 @@ bool on_device(const void* ptr, int dev) {
   return at.type == cudaMemoryTypeDevice && at.device == dev;
 }
 
-// A buffer of a call: [rows] rows of `row` bytes, `pitch` bytes apart.
+// A buffer of a call: [rows] rows of `row` bytes, `pitch` bytes apart, in `batch`
+// matrices `stride` bytes apart.
 struct Buf {
   const void* p;
   int64_t rows, row, pitch;
   bool out;
-  size_t bytes() const { return rows > 0 && row > 0 ? static_cast<size_t>((rows - 1) * pitch + row) : 0; }
+  int64_t batch = 1, stride = 0;
+  int64_t matrix() const { return (rows - 1) * pitch + row; }
+  size_t bytes() const {
+    return rows > 0 && row > 0 && batch > 0 ? static_cast<size_t>((batch - 1) * stride + matrix()) : 0;
+  }
+  uintptr_t at() const { return reinterpret_cast<uintptr_t>(p); }
 };
+
+// Whether units of x and y (wx and wy bytes, nx and ny of them, px and py apart)
+// interleave without touching, as the halves of one matrix's columns do.  Units of
+// one pitch only: a lone one takes the other's.
+bool interleaved(uintptr_t x, int64_t wx, int64_t px, int64_t nx, uintptr_t y, int64_t wy, int64_t py, int64_t ny) {
+  const int64_t p = nx > 1 ? px : py;
+  if ((nx > 1 && ny > 1 && px != py) || p <= 0) return false;
+  const int64_t d = static_cast<int64_t>((x % p + p - y % p) % p);  // of x's units behind y's
+  return d >= wy && d + wx <= p;
+}
+
+bool overlap(const Buf& a, const Buf& b) {
+  if (a.at() >= b.at() + b.bytes() || b.at() >= a.at() + a.bytes()) return false;
+  // Whole matrices in turn, or rows, where every matrix starts on the same column.
+  if (interleaved(a.at(), a.matrix(), a.stride, a.batch, b.at(), b.matrix(), b.stride, b.batch)) return false;
+  const bool same = (a.batch <= 1 || (a.pitch > 0 && a.stride % a.pitch == 0)) &&
+                    (b.batch <= 1 || (b.pitch > 0 && b.stride % b.pitch == 0));
+  return !same || !interleaved(a.at(), a.row, a.pitch, a.rows * a.batch, b.at(), b.row, b.pitch, b.rows * b.batch);
+}
 
 // Device memory throughout, and no output overlapping another buffer.
 template <int kN>
@@ -95,12 +120,8 @@ gemm_status_t check_bufs(const gemm_ops_s* h, const Buf (&b)[kN]) {
     if (b[i].bytes() == 0) continue;
     if (!b[i].p || !on_device(b[i].p, h->device)) return GEMM_ERR_INVALID_ARG;
     if (!b[i].out) continue;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(b[i].p);
-    for (int j = 0; j < kN; ++j) {
-      if (j == i || b[j].bytes() == 0 || (b[j].out && j < i)) continue;
-      const uintptr_t y = reinterpret_cast<uintptr_t>(b[j].p);
-      if (x < y + b[j].bytes() && y < x + b[i].bytes()) return GEMM_ERR_INVALID_ARG;
-    }
+    for (int j = 0; j < kN; ++j)
+      if (j != i && b[j].bytes() != 0 && !(b[j].out && j < i) && overlap(b[i], b[j])) return GEMM_ERR_INVALID_ARG;
   }
   return GEMM_OK;
 }
@@ -900,9 +921,8 @@ gemm_status_t gemm_orthogonalize(gemm_ops_t h, const void* m, int64_t ldm, int64
   if (workspace_bytes < sp.total) return GEMM_ERR_INVALID_ARG;
   DeviceGuard g(h->device);
   if (!g.ok) return GEMM_ERR_CUDA;
-  const int64_t one_m = ((M - 1) * ldm + N) * ei, one_o = ((M - 1) * ldo + N) * eo;
-  const Buf bufs[] = {{m, batch, one_m, batch > 1 ? stride_m * ei : 0, false},
-                      {out, batch, one_o, batch > 1 ? stride_o * eo : 0, true},
+  const Buf bufs[] = {{m, M, N * ei, ldm * ei, false, batch, batch > 1 ? stride_m * ei : 0},
+                      {out, M, N * eo, ldo * eo, true, batch, batch > 1 ? stride_o * eo : 0},
                       {workspace, 1, static_cast<int64_t>(sp.total), 0, true}};
   gemm_status_t st = check_bufs(h, bufs);
   if (st != GEMM_OK) return st;

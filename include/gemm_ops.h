@@ -19,8 +19,9 @@
  * _check_error and _destroy: while no other thread uses the handle).
  *
  * Every pointer must be device memory of the handle's device; outputs and
- * workspaces must not overlap inputs or one another.  Lengths are at most
- * 2^31 - 4096 (F and the N of 4-bit weights: 2^30 - 1) and row distances below
+ * workspaces must not overlap inputs or one another (an output may have other
+ * columns of an input's matrix: rows of one pitch that share no element).
+ * Lengths are at most 2^31 - 4096 (F and the N of 4-bit weights: 2^30 - 1) and row distances below
  * 2^30 (gemm_orthogonalize's are free).  Results do not depend on timing: no sum
  * is taken in the order in which parts arrive.
  */

@@ -1,6 +1,8 @@
 """The operators at the limits of their arguments: empty sums, infinities and
 values near the types' largest, the longest rows, and what is refused there.
 Bounds as in test_gpu_ops.py."""
+import random
+
 import pytest
 import torch
 
@@ -251,3 +253,68 @@ def test_outputs_count_as_written(g):
         with torch.inference_mode():
             frozen = torch.ones(4, 64, device="cuda", dtype=dt)
         assert torch.equal(fn(*args, out=frozen), fn(*args, out=out))
+
+
+# -------------------------------------------------------------- views of one buffer --
+def test_outputs_beside_inputs_in_one_matrix(g):
+    """An output in other columns, or other matrices, of the buffer that holds an
+    input shares no element with it: taken, and nothing else is written."""
+    dt = torch.float16
+    for T in (1, 5, 40, 300):
+        x, w_in, w_down, _ = make_ffn(T, 64, 128, dt)
+        both = torch.cat((x, torch.full_like(x, 7.0), x), 1)
+        g.gated_ffn(both[:, :64], w_in, w_down, out=both[:, 64:128])
+        assert torch.equal(both[:, 64:128], g.gated_ffn(x, w_in, w_down))
+        assert torch.equal(both[:, :64], x) and torch.equal(both[:, 128:], x)
+        xm, codes, scales, z = make_w4(T, 40, 64, 32, True, dt)
+        both = torch.cat((torch.full((T, 41), 7.0, device="cuda", dtype=dt)[:, :40], xm), 1)
+        g.w4_linear(both[:, 40:], codes, scales, z, out=both[:, :40])
+        assert torch.equal(both[:, :40], g.w4_linear(xm, codes, scales, z)) and torch.equal(both[:, 40:], xm)
+    m = torch.randn(3, 20, 30, device="cuda")
+    want = g.orthogonalize(m)
+    beside = torch.cat((m, m), 2)
+    assert torch.equal(g.orthogonalize(beside[..., 30:], out=beside[..., :30]), want)
+    assert torch.equal(beside[..., 30:], m)
+    below = torch.cat((m, m), 1)
+    assert torch.equal(g.orthogonalize(below[:, :20], out=below[:, 20:]), want) and torch.equal(below[:, :20], m)
+    turns = m.repeat_interleave(2, 0)
+    assert torch.equal(g.orthogonalize(turns[0::2], out=turns[1::2]), want) and torch.equal(turns[0::2], m)
+    assert torch.equal(g.orthogonalize(m[:1].expand(3, 20, 30))[2], want[0])
+
+
+def test_outputs_are_refused_where_they_share_elements(g):
+    """Random views of one buffer: refused exactly where an element is in both."""
+    rng = random.Random(0)
+    refused = 0
+    for _ in range(400):
+        B, M, N = rng.randint(1, 4), rng.randint(1, 6), rng.randint(2, 12)
+        buf = torch.randn(B, M, N, device="cuda")
+        where = torch.arange(buf.numel()).view(B, M, N)
+        b, r, c = rng.randint(1, B), rng.randint(1, M), rng.randint(1, N - 1)
+        def view(step=rng.choice((1, 2))):
+            i = rng.randint(0, B - b) if step == 1 else rng.randint(0, 1)
+            r0, c0 = rng.randint(0, M - r), rng.randint(0, N - c)
+            cut = (slice(i, i + b) if step == 1 else slice(i, None, 2), slice(r0, r0 + r), slice(c0, c0 + c))
+            return buf[cut], set(where[cut].flatten().tolist())
+        (v, at), (w, on) = view(), view()
+        if v.shape != w.shape or not at:
+            continue
+        want = g.orthogonalize(v.contiguous())
+        if at & on:
+            refused += 1
+            before = buf.clone()
+            with pytest.raises(g.GemmError) as e:
+                g.orthogonalize(v, out=w)
+            assert e.value.status == 1 and torch.equal(buf, before)
+        else:
+            assert torch.equal(g.orthogonalize(v, out=w), want)
+    assert 50 < refused < 350
+    dt = torch.float16
+    x, w_in, w_down, _ = make_ffn(5, 64, 128, dt)
+    both = torch.cat((x, x), 1)
+    for first in (0, 8, 56):
+        with pytest.raises(g.GemmError):
+            g.gated_ffn(both[:, :64], w_in, w_down, out=both[:, first:first + 64])
+    flat = torch.zeros(2000, device="cuda", dtype=dt)  # rows of two pitches in one range: refused, whether or not they meet
+    with pytest.raises(g.GemmError):
+        g.gated_ffn(flat.as_strided((5, 64), (128, 1)), w_in, w_down, out=flat.as_strided((5, 64), (192, 1), 64))
