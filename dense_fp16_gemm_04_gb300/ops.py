@@ -162,11 +162,11 @@ class Ops:
 
     # -- the orthogonalised update -------------------------------------------
     def orthogonalize(self, m, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, dtype=None, out=None, stream=None):
+        for name, t in (("m", m), ("out", out)):
+            if t is not None or name == "m":
+                self._b.no_graph(t, name)
         if m.dtype not in _DTYPE:
             raise TypeError(f"m must be float16, bfloat16 or float32, got {m.dtype}")
-        for name, t in (("m", m), ("out", out)):
-            if t is not None:
-                self._b.no_graph(t, name)
         if m.device != self.device:
             raise ValueError(f"m must be on {self.device}, got {m.device}")
         if m.dim() not in (2, 3):
@@ -228,6 +228,8 @@ def default_ops(device=None) -> Ops:
 def _of(t, ops) -> Ops:
     if ops is not None:
         return ops
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"operands must be tensors, got {type(t)}")
     index = t.get_device()
     if index < 0:
         raise ValueError("tensors must be on a CUDA device")

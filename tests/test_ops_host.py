@@ -187,3 +187,16 @@ def test_tensors_that_ask_for_a_graph_are_refused(lib):
 def test_quantised_weights_leave_the_graph():
     codes, scales, zeros = g.w4_quantize(torch.nn.Parameter(torch.ones(4, 64)), 32, zero_point=True)
     assert not (codes.requires_grad or scales.requires_grad or zeros.requires_grad)
+
+
+@pytest.mark.parametrize("other", [None, [1.0, 2.0], 3])
+def test_operands_that_are_not_tensors_are_refused(lib, other):
+    h = lambda *s: torch.zeros(*s, dtype=torch.float16)
+    codes = torch.zeros(8, 32, dtype=torch.uint8)
+    o = Unbound()
+    for call in (lambda: g.gated_ffn(other, h(256, 64), h(64, 128)), lambda: g.w4_linear(other, codes, h(8, 2)),
+                 lambda: g.w4_gated(other, codes, h(8, 2)), lambda: g.orthogonalize(other),
+                 lambda: g.gated_ffn_backward(h(4, 64), other, h(256, 64), h(64, 128), h(4, 256)),
+                 lambda: o.gated_ffn(other, h(256, 64), h(64, 128)), lambda: o.orthogonalize(other)):
+        with pytest.raises(TypeError):
+            call()
