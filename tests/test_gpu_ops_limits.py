@@ -318,3 +318,41 @@ def test_outputs_are_refused_where_they_share_elements(g):
     flat = torch.zeros(2000, device="cuda", dtype=dt)  # rows of two pitches in one range: refused, whether or not they meet
     with pytest.raises(g.GemmError):
         g.gated_ffn(flat.as_strided((5, 64), (128, 1)), w_in, w_down, out=flat.as_strided((5, 64), (192, 1), 64))
+
+
+# --------------------------------------------------------------------- watchdog --
+# A form of the products each (the cost model's choice on 152 SMs), for the gated
+# product and the one after it: pairs; two pairs on a tile, then pairs; pairs, then
+# two pairs; clusters of four.
+@pytest.mark.parametrize("shape", [(1536, 4096, 1536), (1536, 4096, 768), (4096, 512, 2048), (17, 512, 512)],
+                         ids=["pairs", "two_pairs_first", "two_pairs_second", "clusters"])
+def test_watchdog_ends_a_stuck_wait_in_every_form(g, shape):
+    """A k-block that is never loaded: every role of the unit gives up after the
+    limit, in the CTAs that share its tile too; the next call is right."""
+    ops = g.Ops(0)
+    x, w_in, w_down, _ = make_ffn(*shape, torch.float16)
+    ops.set_watchdog(timeout_ns=50_000_000, skip_k_block=1)
+    ops.gated_ffn(x, w_in, w_down)
+    with pytest.raises(g.GemmError) as e:
+        ops.check_error()
+    assert e.value.status == 5 and ops.last_error_detail()[0] == 5
+    ops.set_watchdog()
+    assert torch.equal(ops.gated_ffn(x, w_in, w_down), g.gated_ffn(x, w_in, w_down))
+    ops.check_error()
+    ops.close()
+
+
+# The update's: k-ranges side by side in one CTA; lone CTAs, then pairs; two pairs.
+@pytest.mark.parametrize("shape", [(5, 900, 1000), (1, 3000, 3010), (1, 2048, 2048)], ids=["parts", "lone", "two_pairs"])
+def test_watchdog_ends_a_stuck_wait_of_an_update(g, shape):
+    ops = g.Ops(0)
+    m = torch.randn(*shape, device="cuda")
+    ops.set_watchdog(timeout_ns=50_000_000, skip_k_block=1)
+    ops.orthogonalize(m, steps=1)
+    with pytest.raises(g.GemmError) as e:
+        ops.check_error()
+    assert e.value.status == 5 and ops.last_error_detail()[0] == 5
+    ops.set_watchdog()
+    assert torch.equal(ops.orthogonalize(m, steps=1), g.orthogonalize(m, steps=1))
+    ops.check_error()
+    ops.close()
