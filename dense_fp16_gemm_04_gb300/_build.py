@@ -3,8 +3,8 @@
 Produces ``libgb300gemm.so`` next to this file from ``csrc/*.cu`` (the GEMM)
 and ``csrc/ops/*.cu`` (the operators beside it); the compiled code targets
 exactly sm_103a (GB300).  The operators' CPython binding ``_binding*.so``
-(``csrc/ops/binding.cpp``) is built against the installed torch; without torch
-the library is built alone.
+(``csrc/ops/binding.cpp``) is built against the installed torch; without torch,
+or with one that has no CUDA, the library is built alone.
 """
 from __future__ import annotations
 
@@ -12,6 +12,7 @@ import glob
 import hashlib
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -54,23 +55,27 @@ def _newer(target, inputs) -> bool:
 
 
 def _torch():
-    """The installed torch's folder, or None."""
+    """The installed torch's folder and the text of its version.py; None for no
+    torch, or one without CUDA (its version.py says cuda = None)."""
     spec = importlib.util.find_spec("torch")
-    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    folder, version = spec.submodule_search_locations[0], ""
+    path = os.path.join(folder, "version.py")
+    if os.path.exists(path):
+        with open(path, encoding="utf-8") as f:
+            version = f.read()
+    return None if re.search(r"^cuda\b[^=\n]*=\s*None", version, re.M) else (folder, version)
 
 
 def binding_path():
-    """Where the binding for the installed torch lies, or None without torch.  It
-    is compiled against torch's C++ classes, so its name holds a hash of which
-    torch that is: another one never loads it."""
+    """Where the binding for the installed torch lies, or None without a torch for
+    it.  It is compiled against torch's C++ classes, so its name holds a hash of
+    which torch that is: another one never loads it."""
     torch = _torch()
     if torch is None:
         return None
-    which = hashlib.sha256(torch.encode())
-    version = os.path.join(torch, "version.py")
-    if os.path.exists(version):
-        with open(version, "rb") as f:
-            which.update(f.read())
+    which = hashlib.sha256("\n".join(torch).encode())
     return os.path.join(HERE, "_binding_" + which.hexdigest()[:8] + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 
@@ -86,7 +91,7 @@ def _binding_inputs():
 def _build_binding(path):
     """Start compiling the binding; returns (process, its output, command)."""
     tmp = path + f".tmp{os.getpid()}"
-    torch = _torch()
+    torch, _ = _torch()
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
            "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(_cuda(), "include"), BINDING_SRC,

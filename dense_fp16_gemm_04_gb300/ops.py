@@ -89,6 +89,8 @@ def _load_binding():
     with _sig_lock:
         if _binding is None:
             path = _build.binding_path()
+            if path is None:
+                raise ImportError("the operators need a torch with CUDA")
             if not os.path.exists(path):
                 raise ImportError(f"{path} is missing: build it for this torch with "
                                   "dense_fp16_gemm_04_gb300.build()")

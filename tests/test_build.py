@@ -99,3 +99,15 @@ def test_star_import(tree):
     assert tree(NO_TORCH + star + "; assert 'gated_ffn' not in dir()") == []
     assert tree(star + "; assert gated_ffn and w4_linear and orthogonalize") == []
     assert tree(f"import sys, {PACKAGE} as g; assert 'torch' not in sys.modules; assert 'Ops' in g.__all__") == []
+
+
+def test_a_torch_without_cuda_leaves_the_binding_out(tree):
+    """The binding links torch's CUDA library; the GEMM does without."""
+    torch = tree.path / "site" / "torch"
+    torch.mkdir(parents=True)
+    (torch / "__init__.py").write_text("")
+    (torch / "version.py").write_text("from typing import Optional\n\n__version__ = '2+cpu'\ncuda: Optional[str] = None\n")
+    env = dict(PYTHONPATH=str(tree.path / "site"))
+    assert tree(BUILD, **env) == ["nvcc"] and tree(BUILD, **env) == []
+    (torch / "version.py").write_text("__version__ = '2+cu130'\ncuda: Optional[str] = '13.0'\nhip: Optional[str] = None\n")
+    assert tree(BUILD, **env) == ["cxx"]
