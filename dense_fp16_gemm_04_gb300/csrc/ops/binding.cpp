@@ -210,6 +210,7 @@ struct Stream {
       Ref r(PyObject_GetAttr(o, s_cuda_stream));
       if (!r.p || !to_i64(r.p, &v)) return false;
     }
+    if (v == 1) v = 0;  // the legacy default stream by its handle: torch knows it as 0
     s = reinterpret_cast<void*>(v);
     guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), dev));
     return true;

@@ -182,7 +182,8 @@ class Ops:
             raise TypeError(f"dtype must be float16, bfloat16 or float32, got {dtype}")
         if stream is not None:  # what is allocated belongs to the stream that uses it
             if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=self.device)
+                # The legacy default stream's handle is 1; torch knows it as 0.
+                stream = torch.cuda.ExternalStream(0 if stream == 1 else stream, device=self.device)
             with torch.cuda.stream(stream):
                 return self.orthogonalize(m, steps, coeffs, eps, dtype, out)
         given = out

@@ -356,3 +356,22 @@ def test_watchdog_ends_a_stuck_wait_of_an_update(g, shape):
     assert torch.equal(ops.orthogonalize(m, steps=1), g.orthogonalize(m, steps=1))
     ops.check_error()
     ops.close()
+
+
+# ---------------------------------------------------------------------- streams --
+@pytest.mark.parametrize("stream", [0, 1, 2], ids=["null", "legacy", "per_thread"])
+def test_streams_by_their_handles(g, stream):
+    """CUDA's own handles: the null stream, the legacy default stream and the
+    thread's default stream."""
+    dt = torch.float16
+    x, w_in, w_down, dy = make_ffn(40, 64, 128, dt)
+    xm, codes, scales, z = make_w4(4, 64, 256, 64, True, dt)
+    m = torch.randn(40, 30, device="cuda")
+    _, gu = g.gated_ffn(x, w_in, w_down, save=True)
+    for fn, args in ((g.gated_ffn, (x, w_in, w_down)), (g.gated_ffn_backward, (dy, x, w_in, w_down, gu)),
+                     (g.w4_linear, (xm, codes, scales, z)), (g.w4_gated, (xm, codes, scales, z)), (g.orthogonalize, (m,))):
+        want = fn(*args)
+        torch.cuda.synchronize()
+        got = fn(*args, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(*((v if isinstance(v, tuple) else (v,)) for v in (got, want))))
