@@ -24,9 +24,9 @@
 //                diagonal are computed, and each is also stored transposed.
 //
 // What bounds them.  Large products: the tensor cores, and the power they draw
-// (gated block of 8192 tokens, 8192 x 16384: 4050 us, 1630 TFLOP/s; its backward
-// pass at 4096 x 8192: 2040 us, 1615 TFLOP/s; update of 4096 x 8192, each product
-// three: 5000 us, 1440 TFLOP/s).  Few tokens: the weights' bytes (24 tokens,
+// (gated block of 8192 tokens, 8192 x 16384: 4100 us, 1610 TFLOP/s; its backward
+// pass at 4096 x 8192: 2180 us, 1510 TFLOP/s; update of 4096 x 8192, each product
+// three: 5100 us, 1410 TFLOP/s).  Few tokens: the weights' bytes (24 tokens,
 // 8192 x 16384: 134 us, 6.0 TB/s).  Small ones: a launch's start and end, 4 to 7
 // us (update of 512 x 512: 15 dependent products in 115 us).
 //

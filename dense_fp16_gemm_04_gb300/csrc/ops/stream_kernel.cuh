@@ -5,9 +5,9 @@
 //   W[n, k] = s[n, k / G] (q[n, k] - z[n, k / G]),   q, z in 0 .. 15.
 //
 // The least it can take is the weights' bytes.  16-bit weights come close
-// (8192 x 16384 gated block, one token: 120 us, 99% of a copy's bandwidth); 4-bit
+// (8192 x 16384 gated block, one token: 123 us, 96% of a copy's bandwidth); 4-bit
 // ones are bound by the instructions that unpack them (one token x 16384 gated
-// columns x 8192, groups of 32: 36 us for 151 MB, 61%; 300 instructions per warp
+// columns x 8192, groups of 32: 37 us for 151 MB, 60%; 303 instructions per warp
 // for 32 rows x 128 k, of which 96 unpack and 24 multiply, at 1.9 per clock).
 //
 // The sums run on warp-level matrix products (16 rows of W x 16 k x 8 tokens):

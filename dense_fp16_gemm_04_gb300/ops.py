@@ -6,7 +6,10 @@ products through the compiled ``_binding`` (a call for one token costs the host
 more than the GPU), ``orthogonalize`` through ctypes.  Every step runs in the
 sm_103a kernels of ``libgb300gemm.so``.  Tensors are CUDA tensors of one device,
 float16 or bfloat16; results and workspaces come from torch's allocator, on the
-stream of the call (the current one, or ``stream``).  There is no fallback: wrong arguments and other devices raise.
+stream of the call (the current one, or ``stream``).  As with any work on another
+stream, the caller orders it after what made the inputs and keeps them until it
+has run (``Tensor.record_stream``).  There is no fallback: wrong arguments and
+other devices raise.
 
 The operators record no graph.  A tensor that requires grad (while gradients are
 recorded) or has a forward-mode tangent is refused with a RuntimeError: call them

@@ -21,9 +21,9 @@
  * Every pointer must be device memory of the handle's device; outputs and
  * workspaces must not overlap inputs or one another (an output may have other
  * columns of an input's matrix: rows of one pitch that share no element).
- * Lengths are at most 2^31 - 4096 (F and the N of 4-bit weights: 2^30 - 1) and row distances below
- * 2^30 (gemm_orthogonalize's are free).  Results do not depend on timing: no sum
- * is taken in the order in which parts arrive.
+ * Lengths are at most 2^31 - 4096 (F and the N of 4-bit weights: 2^30 - 1) and
+ * row distances below 2^30 (free where a function says so).  Results do not
+ * depend on timing: no sum is taken in the order in which parts arrive.
  */
 #ifndef GB300_GEMM_OPS_H_
 #define GB300_GEMM_OPS_H_
@@ -117,8 +117,8 @@ GEMM_API gemm_status_t gemm_gated_ffn_backward(
  *   zeros  : [N, K / G] bytes 0 .. 15, or NULL for 8 everywhere
  *   group  : G, a power of two from 32 on that divides K
  * Made for few tokens: the weights are read once for every 16, and T is at most
- * 8 * 65535.  x and codes 16-byte aligned, ldx a
- * multiple of 8 (GEMM_ERR_ALIGNMENT); N and ldy are free; K is at most 2^28.
+ * 8 * 65535.  x and codes 16-byte aligned, ldx a multiple of 8
+ * (GEMM_ERR_ALIGNMENT); ldy and the alignment of N are free; K is at most 2^28.
  * A group's sum of x (O + q - (O + zero)), O = 64 (fp16) or 128 (bf16), and its
  * product with the scale are fp32; the products x (O + q) are exact.  A sum that
  * does not come out finite so (an infinite x, or one whose products with O + q
@@ -145,7 +145,7 @@ GEMM_API gemm_status_t gemm_w4_gated(gemm_ops_t ops, const void* x, int64_t ldx,
  *
  * on `batch` matrices of M x N.
  *   m, out   : rows ldm / ldo apart, matrices stride_m / stride_o apart
- *              (elements); no alignment or size rules
+ *              (elements), free and without alignment rules; batch <= 65535
  *   in_dtype, out_dtype : GEMM_F16, GEMM_BF16 or GEMM_F32
  *   coeffs   : a, b, c
  * X, P and b P + c P^2 are held to 22 bits, as the sum of two fp16 numbers
@@ -153,9 +153,10 @@ GEMM_API gemm_status_t gemm_w4_gated(gemm_ops_t ops, const void* x, int64_t ldx,
  * them to one 16-bit number costs 1e-3 to 1e-2 of the result, since small
  * singular values grow by up to a^steps.  Their entries must stay below 8,
  * 32 and 64 (any coefficients that keep singular values below 2.8 and
- * |b| s^2 + |c| s^4 below 64); larger ones become infinite.  The sum of
- * squares is fp32: |m| must be below 2^63.  A matrix of a batch gets the bits it
- * gets by itself.
+ * |b| s^2 + |c| s^4 below 64); larger ones end in infinities and NaN.  Entries of
+ * X below 2^-16 are held to 2^-38 instead.  The sum of squares is fp32: |m| must
+ * be below 2^63, and above 2^-63 where eps is 0.  A matrix of a batch gets the
+ * bits it gets by itself.
  * workspace: gemm_orthogonalize_workspace(ops, batch, M, N) bytes, 256-byte
  * aligned. */
 GEMM_API size_t gemm_orthogonalize_workspace(gemm_ops_t ops, int64_t batch, int64_t M, int64_t N);
