@@ -1,0 +1,350 @@
+// host.cuh -- what the host sides of the operators share: the handle, checks of
+// arguments, tensor maps, launches, and the choice of a fused product's form.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+
+#include "fused_kernel.cuh"
+#include "gemm_ops.h"
+
+struct gemm_ops_s {
+  int device = 0;
+  int num_sms = 0;
+  int max_pairs = 0;      // CTA pairs of the pair kernels that fit on the device at once
+  int max_twos = 0;       // clusters of two pairs sharing a tile
+  int max_split[4] = {};  // clusters of 1, 2, 4, 8 CTAs sharing a tile
+  void* encode = nullptr;
+  uint32_t* d_err = nullptr;  // 4-word watchdog record
+  uint32_t last_err[4] = {0, 0, 0, 0};
+  uint64_t timeout_ns = 2000000000ull;
+  int32_t skip_kb = -1;
+  std::atomic<uint64_t> launches{0};
+};
+
+namespace {
+
+using namespace gb300::ops;
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+constexpr int kGroupM = 8;
+
+// Staging buffers of an epilogue warp: 64 KB in all beside five stages.
+constexpr int epi_bufs(int epi) { return epi == kEpiSplit || epi == kEpiSplitSym ? 4 : 2; }
+
+// Tile configurations: a pair of CTAs on 256 x 256 sums, or one CTA on
+// 128 x 128 for problems of few tiles.
+template <int kEpi>
+using Pair = FusedCfg<2, 256, kEpi == kEpiStore ? 6 : 5, kEpi, kEpi == kEpiStore ? 1 : epi_bufs(kEpi)>;
+template <int kEpi>
+using TwoPairs = FusedCfg<2, 256, 5, kEpi, epi_bufs(kEpi), 2>;  // one tile, half of its k-blocks each
+template <int kEpi, int kSplit = 1, int kParts = 1>
+using Lone = FusedCfg<1, 128, 5, kEpi, epi_bufs(kEpi), kSplit, kParts>;
+
+struct DeviceGuard {
+  int prev = -1;
+  bool ok = false;
+  explicit DeviceGuard(int dev) {
+    if (cudaGetDevice(&prev) != cudaSuccess) return;
+    ok = (prev == dev) || (cudaSetDevice(dev) == cudaSuccess);
+  }
+  ~DeviceGuard() {
+    int cur = -1;
+    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+  }
+};
+
+bool on_device(const void* ptr, int dev) {
+  cudaPointerAttributes at;
+  if (cudaPointerGetAttributes(&at, ptr) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return at.type == cudaMemoryTypeDevice && at.device == dev;
+}
+
+// A buffer of a call: [rows] rows of `row` bytes, `pitch` bytes apart, in `batch`
+// matrices `stride` bytes apart.
+struct Buf {
+  const void* p;
+  int64_t rows, row, pitch;
+  bool out;
+  int64_t batch = 1, stride = 0;
+  int64_t matrix() const { return (rows - 1) * pitch + row; }
+  size_t bytes() const {
+    return rows > 0 && row > 0 && batch > 0 ? static_cast<size_t>((batch - 1) * stride + matrix()) : 0;
+  }
+  uintptr_t at() const { return reinterpret_cast<uintptr_t>(p); }
+};
+
+// Whether units of x and y (wx and wy bytes, nx and ny of them, px and py apart)
+// interleave without touching, as the halves of one matrix's columns do.  Units of
+// one pitch only: a lone one takes the other's.
+bool interleaved(uintptr_t x, int64_t wx, int64_t px, int64_t nx, uintptr_t y, int64_t wy, int64_t py, int64_t ny) {
+  const int64_t p = nx > 1 ? px : py;
+  if ((nx > 1 && ny > 1 && px != py) || p <= 0) return false;
+  const int64_t d = static_cast<int64_t>((x % p + p - y % p) % p);  // of x's units behind y's
+  return d >= wy && d + wx <= p;
+}
+
+bool overlap(const Buf& a, const Buf& b) {
+  if (a.at() >= b.at() + b.bytes() || b.at() >= a.at() + a.bytes()) return false;
+  // Whole matrices in turn, or rows, where every matrix starts on the same column.
+  if (interleaved(a.at(), a.matrix(), a.stride, a.batch, b.at(), b.matrix(), b.stride, b.batch)) return false;
+  const bool same = (a.batch <= 1 || (a.pitch > 0 && a.stride % a.pitch == 0)) &&
+                    (b.batch <= 1 || (b.pitch > 0 && b.stride % b.pitch == 0));
+  return !same || !interleaved(a.at(), a.row, a.pitch, a.rows * a.batch, b.at(), b.row, b.pitch, b.rows * b.batch);
+}
+
+// Device memory throughout, and no output overlapping another buffer.
+template <int kN>
+gemm_status_t check_bufs(const gemm_ops_s* h, const Buf (&b)[kN]) {
+  for (int i = 0; i < kN; ++i) {
+    if (b[i].bytes() == 0) continue;
+    if (!b[i].p || !on_device(b[i].p, h->device)) return GEMM_ERR_INVALID_ARG;
+    if (!b[i].out) continue;
+    for (int j = 0; j < kN; ++j)
+      if (j != i && b[j].bytes() != 0 && !(b[j].out && j < i) && overlap(b[i], b[j])) return GEMM_ERR_INVALID_ARG;
+  }
+  return GEMM_OK;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// The kernels' 32-bit counters of rows and columns run past the end of a matrix
+// by less than a tile (256 and 192 columns more), or by the stride of a loop: 256
+// columns, or the rows of one round of CTAs, 8 per SM.
+constexpr int64_t kMaxLength = INT32_MAX - 4095;
+bool dim_ok(int64_t v) { return v >= 0 && v <= kMaxLength; }
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int64_t cdiv(int64_t v, int64_t m) { return (v + m - 1) / m; }
+
+// ------------------------------------------------------------ tensor maps --
+// A stack of `z` row-major 16-bit matrices of rows x cols, rows `pitch` and
+// matrices `zstride` elements apart.
+struct Stack {
+  const void* p;
+  int64_t rows, cols, pitch, z, zstride;
+};
+
+bool make_map(const gemm_ops_s* h, CUtensorMap* m, const Stack& s, bool bf16, uint32_t box_cols,
+              uint32_t box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(s.cols), static_cast<cuuint64_t>(s.rows),
+                              static_cast<cuuint64_t>(s.z)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.pitch) * 2,
+                                 static_cast<cuuint64_t>(s.zstride) * 2};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  // Rows whose pitch is not a multiple of 128 bytes straddle L2 lines:
+  // promoting their requests to 256 bytes costs more than it saves.
+  const CUtensorMapL2promotion l2 = s.pitch % 64 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                                      : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+  auto encode = [&] {
+    return reinterpret_cast<EncodeTiledFn>(h->encode)(
+        m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+        const_cast<void*>(s.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+        l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  // A host thread that has not used CUDA (autograd's, a worker's) has a device but
+  // no context, which the driver's encoder needs: cudaSetDevice makes the primary
+  // one current.
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaSetDevice(h->device) == cudaSuccess) r = encode();
+  return r == CUDA_SUCCESS;
+}
+
+// ---------------------------------------------------------------- launches --
+template <class... Params, class... Args>
+gemm_status_t launch(gemm_ops_s* h, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                     int cluster, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  // Set-up may overlap the end of the previous kernel of the stream; every
+  // kernel waits for it before touching global memory.
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  ++h->launches;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return GEMM_OK;
+  cudaGetLastError();
+  return GEMM_ERR_CUDA;
+}
+
+// One product: acc[M, N] over segs x K, A and B stacks, their layouts.
+struct Product {
+  int64_t M, N, K;
+  Stack a, b;
+  bool a_mn, b_mn;  // stored [K, M] / [K, N]
+  bool bf16;
+  int64_t batch, segs;
+  int32_t a_zb, b_zb, c_zb;   // stack coordinates: FusedArgs
+  int32_t a_seg[3], b_seg[3];
+};
+
+FusedArgs base_args(const gemm_ops_s* h, const Product& p) {
+  FusedArgs a = {};
+  a.M = static_cast<int32_t>(p.M);
+  a.N = static_cast<int32_t>(p.N);
+  a.num_kb = static_cast<int32_t>(cdiv(p.K, 64));
+  a.segs = static_cast<int32_t>(p.segs);
+  a.a_zb = p.a_zb;
+  a.b_zb = p.b_zb;
+  a.c_zb = p.c_zb;
+  for (int i = 0; i < 3; ++i) {
+    a.a_seg[i] = p.a_seg[i];
+    a.b_seg[i] = p.b_seg[i];
+  }
+  a.group_m = kGroupM;
+  a.a_mn = p.a_mn;
+  a.b_mn = p.b_mn;
+  a.bf16 = p.bf16;
+  a.alpha = 1.0f;
+  a.err = h->d_err;
+  a.timeout_ns = h->timeout_ns;
+  a.skip_kb = h->skip_kb;
+  return a;
+}
+
+template <class Cfg>
+gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const Stack& c,
+                           const Stack& d, cudaStream_t stream) {
+  CUtensorMap ma, mb, mc, md;
+  const uint32_t b_rows = Cfg::kGlu && Cfg::kCtas == 1 ? Cfg::kBN / 2 : Cfg::kBRows;
+  // Fewer rows than a tile: a box of those alone, and more k-blocks in flight.
+  // What the MMA takes for the tile's other rows, the bytes that follow, meets
+  // no stored row of the product.  24 tokens, weights of 8192 x 16384 and of
+  // 2048 x 5632: whole boxes 143.4 and 30.6 us, boxes of 24 rows 142.7 and
+  // 25.7 us, with eight k-blocks in flight in place of five 133.8 and 25.4 us.
+  const uint32_t a_rows =
+      Cfg::kCtas == 1 && !p.a_mn ? static_cast<uint32_t>(std::min<int64_t>(Cfg::kBM, up(p.M, 8))) : Cfg::kBM;
+  a.a_tx = a_rows * Cfg::kBK * 2;
+  a.stages = std::min<int32_t>(Cfg::kMaxStages, Cfg::kStages * (Cfg::kABytes + Cfg::kBBytes) / (a.a_tx + Cfg::kBBytes));
+  bool ok = make_map(h, &ma, p.a, p.bf16, 64, p.a_mn ? 64 : a_rows) &&
+            make_map(h, &mb, p.b, p.bf16, 64, p.b_mn ? 64 : b_rows);
+  if (ok && c.p) ok = make_map(h, &mc, c, p.bf16, 64, 32);
+  if (ok && d.p)
+    ok = Cfg::kSym ? make_map(h, &md, d, p.bf16, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE)
+                   : make_map(h, &md, d, p.bf16, 64, 32);
+  if (!ok) return GEMM_ERR_CUDA;
+  if (!c.p) mc = ma;  // not used by this epilogue
+  if (!d.p) md = ma;
+  const int64_t tm = cdiv(p.M, Cfg::kTileM), tn = cdiv(p.N, Cfg::kOutN);
+  const int64_t per = Cfg::kSym ? tn * (tn + 1) / 2 : tm * tn;
+  const int64_t items = per * p.batch;
+  if (items > INT32_MAX / 2) return GEMM_ERR_INVALID_ARG;
+  a.tiles_m = static_cast<int32_t>(tm);
+  a.tiles_n = static_cast<int32_t>(tn);
+  a.per_batch = static_cast<int32_t>(per);
+  a.items = static_cast<int32_t>(items);
+  a.c = static_cast<uint16_t*>(const_cast<void*>(c.p));
+  a.ldc = c.pitch;
+  a.c_z = c.zstride;
+  a.ldd = d.pitch;
+  a.d_up = d.zstride;
+  a.d = static_cast<uint16_t*>(const_cast<void*>(d.p));
+  const int64_t fit = Cfg::kCtas == 2 ? h->max_pairs : h->num_sms;
+  const int64_t units = Cfg::kSplit > 1 ? items : std::min<int64_t>(items, fit);
+  return launch(h, fused_kernel<Cfg>, dim3(static_cast<unsigned>(units * Cfg::kCluster)), dim3(Cfg::kThreads),
+                Cfg::kSmemBytes, Cfg::kCluster, stream, ma, mb, mc, md, a);
+}
+
+// Which form: the one whose rounds of tiles take the least time by this model,
+// in units of 10 ns: a k-block takes a lone CTA 0.27 us (its 32 KB of operands
+// through the SM's L2 port), a pair 0.33 us (the tensor pipe), and a tile starts
+// and ends in 4 to 7 us.  Of clusters of two CTAs 76 fit at once, of four 36, of
+// eight 15.  Lone clusters split a tile only where all fit at once.
+//
+// The batched products (high and low parts) go by one matrix's tiles alone, so
+// that a matrix of a batch gets the same sums as by itself: the number of its
+// k-ranges is fixed, and the batch's tiles decide who sums them.
+template <int kEpi>
+gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const Stack& c,
+                    const Stack& d, cudaStream_t stream) {
+  constexpr bool kBatched = kEpi == kEpiSplit || kEpi == kEpiSplitSym;
+  auto tiles = [&](int64_t tm, int64_t tn) { return Pair<kEpi>::kSym ? tn * (tn + 1) / 2 : tm * tn; };
+  const int64_t n = kBatched ? 1 : p.batch, kb = cdiv(p.K, 64) * p.segs;
+  const int64_t small = tiles(cdiv(p.M, 128), cdiv(p.N, Lone<kEpi>::kOutN)) * n;
+  const int64_t big = tiles(cdiv(p.M, 256), cdiv(p.N, Pair<kEpi>::kOutN)) * n;
+  const int* most = h->max_split;
+  enum { kPairs, kPairs2, kLone, kLone2, kLone4, kLone8, kForms };
+  constexpr int64_t kNever = INT64_MAX;
+  const int64_t cost[kForms] = {
+      h->max_pairs > 0 ? cdiv(big, h->max_pairs) * (33 * kb + 500) : kNever,
+      h->max_twos > 0 && kb >= 4 ? cdiv(big, h->max_twos) * (33 * cdiv(kb, 2) + 700) : kNever,
+      cdiv(small, h->num_sms) * (27 * kb + 400),
+      small <= most[1] && kb >= 4 ? 27 * cdiv(kb, 2) + 550 : kNever,
+      small <= most[2] && kb >= (kBatched ? 4 : 8) ? 27 * cdiv(kb, 4) + 550 : kNever,
+      !kBatched && small <= std::min(8, most[3]) && kb >= 16 ? 27 * cdiv(kb, 8) + 550 : kNever};
+  switch (static_cast<int>(std::min_element(cost, cost + kForms) - cost)) {
+    case kPairs: return launch_fused<Pair<kEpi>>(h, p, a, c, d, stream);
+    case kPairs2: return launch_fused<TwoPairs<kEpi>>(h, p, a, c, d, stream);
+    case kLone2:
+      if constexpr (kBatched)
+        if (small * p.batch > most[1]) return launch_fused<Lone<kEpi, 1, 2>>(h, p, a, c, d, stream);
+      return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream);
+    case kLone4:
+      if constexpr (kBatched)
+        if (small * p.batch > most[2]) return launch_fused<Lone<kEpi, 1, 4>>(h, p, a, c, d, stream);
+      return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream);
+    case kLone8:
+      if constexpr (!kBatched) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream);
+      [[fallthrough]];
+    default: return launch_fused<Lone<kEpi>>(h, p, a, c, d, stream);
+  }
+}
+
+template <class Cfg>
+bool set_attr() {
+  return cudaFuncSetAttribute(fused_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Cfg::kSmemBytes) == cudaSuccess;
+}
+
+template <class Cfg>
+int max_clusters() {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(Cfg::kCluster, 1, 1);
+  cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = Cfg::kCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fused_kernel<Cfg>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+gemm_status_t check_ld(int64_t ld, int64_t cols) {
+  if (ld < cols || ld >= (1ll << 30)) return GEMM_ERR_INVALID_ARG;
+  return ld % 8 != 0 ? GEMM_ERR_ALIGNMENT : GEMM_OK;
+}
+
+}  // namespace
