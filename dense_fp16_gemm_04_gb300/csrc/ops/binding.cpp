@@ -15,6 +15,8 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <cstring>
+#include <utility>
 
 #include "gemm_ops.h"
 
@@ -29,6 +31,11 @@ decltype(&gemm_gated_ffn_backward) g_bwd;
 decltype(&gemm_w4_workspace) g_w4_space;
 decltype(&gemm_w4_linear) g_w4;
 decltype(&gemm_w4_gated) g_w4g;
+decltype(&gemm_layer_norm) g_ln;
+decltype(&gemm_rms_norm) g_rms;
+decltype(&gemm_norm_backward_workspace) g_norm_bwd_space;
+decltype(&gemm_layer_norm_backward) g_ln_bwd;
+decltype(&gemm_rms_norm_backward) g_rms_bwd;
 
 PyObject* s_cuda_stream;
 
@@ -82,31 +89,39 @@ bool no_graph(const at::Tensor& t, const char* name) {
   if (!asks) return true;
   PyErr_Format(PyExc_RuntimeError,
                "%s %s, and this operator records no graph: call it under torch.no_grad() or on detached tensors "
-               "(gated_ffn_backward computes the gradients of gated_ffn)",
+               "(gradients are operators of their own: gated_ffn_backward computes gated_ffn's)",
                name, asks);
   return false;
 }
 
-// Reads o, a tensor that has to have this type and be on this device, and its
-// row distance; rows and cols, where not -1, are what it has to have.
-bool read(PyObject* o, const char* name, at::ScalarType dtype, int64_t index, int64_t rows, int64_t cols,
-          bool contiguous, Mat* m) {
+// A tensor that has to have this type and be on this device; null, with an
+// error set, for any other object.
+const at::Tensor* operand(PyObject* o, const char* name, at::ScalarType dtype, int64_t index) {
   const at::Tensor* t = tensor(o, name);
-  if (!t) return false;
+  if (!t) return nullptr;
   if (t->scalar_type() != dtype) {
     PyErr_Format(PyExc_TypeError, "%s must be %s, got %s", name, type_name(dtype), type_name(t->scalar_type()));
-    return false;
+    return nullptr;
   }
-  if (!no_graph(*t, name)) return false;
+  if (!no_graph(*t, name)) return nullptr;
   if (!t->is_cuda()) {
     PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", name);
-    return false;
+    return nullptr;
   }
   if (t->get_device() != index) {
     PyErr_Format(PyExc_ValueError, "%s is on cuda:%d, the handle on cuda:%lld", name,
                  static_cast<int>(t->get_device()), static_cast<long long>(index));
-    return false;
+    return nullptr;
   }
+  return t;
+}
+
+// Reads o, such a tensor of two dimensions, and its row distance; rows and cols,
+// where not -1, are what it has to have.
+bool read(PyObject* o, const char* name, at::ScalarType dtype, int64_t index, int64_t rows, int64_t cols,
+          bool contiguous, Mat* m) {
+  const at::Tensor* t = operand(o, name, dtype, index);
+  if (!t) return false;
   if (t->dim() != 2) {
     PyErr_Format(PyExc_ValueError, "%s must be 2-D, got %lld dimensions", name, static_cast<long long>(t->dim()));
     return false;
@@ -137,17 +152,44 @@ bool read(PyObject* o, const char* name, at::ScalarType dtype, int64_t index, in
   return true;
 }
 
-// x's type: one of the two 16-bit ones.
-bool read_x(PyObject* x, int64_t index, at::ScalarType* dtype, gemm_dtype_t* code, Mat* m) {
+// x's type: one of the two 16-bit ones, or float32 where the operator takes it.
+bool read_x(PyObject* x, int64_t index, at::ScalarType* dtype, gemm_dtype_t* code, Mat* m, bool f32 = false) {
   const at::Tensor* t = tensor(x, "x");
   if (!t) return false;
   *dtype = t->scalar_type();
-  if (*dtype != at::kHalf && *dtype != at::kBFloat16) {
-    PyErr_Format(PyExc_TypeError, "x must be float16 or bfloat16, got %s", type_name(*dtype));
+  if (*dtype != at::kHalf && *dtype != at::kBFloat16 && !(f32 && *dtype == at::kFloat)) {
+    PyErr_Format(PyExc_TypeError, "x must be %s, got %s", f32 ? "float16, bfloat16 or float32" : "float16 or bfloat16",
+                 type_name(*dtype));
     return false;
   }
-  *code = *dtype == at::kHalf ? GEMM_F16 : GEMM_BF16;
+  *code = *dtype == at::kHalf ? GEMM_F16 : *dtype == at::kBFloat16 ? GEMM_BF16 : GEMM_F32;
   return read(x, "x", *dtype, index, -1, -1, false, m);
+}
+
+// A vector of n elements side by side.
+bool read_vector(PyObject* o, const char* name, at::ScalarType dtype, int64_t index, int64_t n, void** p) {
+  const at::Tensor* t = operand(o, name, dtype, index);
+  if (!t) return false;
+  if (t->dim() != 1 || t->size(0) != n) {
+    PyErr_Format(PyExc_ValueError, "%s must be 1-D of %lld elements", name, static_cast<long long>(n));
+    return false;
+  }
+  if (n > 1 && t->stride(0) != 1) {
+    PyErr_Format(PyExc_ValueError, "%s must be contiguous", name);
+    return false;
+  }
+  *p = t->data_ptr();
+  return true;
+}
+
+// A norm's weight, or None: of x's type or float32, which `dtype` becomes.
+bool read_weight(PyObject* o, int64_t index, int64_t n, at::ScalarType* dtype, gemm_dtype_t* code, void** p) {
+  *p = nullptr;
+  if (o == Py_None) return true;
+  const at::Tensor* t = tensor(o, "weight");
+  if (!t) return false;
+  if (t->scalar_type() == at::kFloat) *dtype = at::kFloat, *code = GEMM_F32;
+  return read_vector(o, "weight", *dtype, index, n, p);
 }
 
 at::TensorOptions on(int64_t index, at::ScalarType dtype) {
@@ -157,6 +199,12 @@ at::TensorOptions on(int64_t index, at::ScalarType dtype) {
 // A new matrix.
 PyObject* empty(int64_t rows, int64_t cols, at::ScalarType dtype, int64_t index, void** p) {
   at::Tensor t = at::empty({rows, cols}, on(index, dtype));
+  *p = t.data_ptr();
+  return THPVariable_Wrap(std::move(t));
+}
+
+PyObject* empty_vector(int64_t n, at::ScalarType dtype, int64_t index, void** p) {
+  at::Tensor t = at::empty({n}, on(index, dtype));
   *p = t.data_ptr();
   return THPVariable_Wrap(std::move(t));
 }
@@ -367,6 +415,98 @@ PyObject* py_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// (handle, index, x, weight, bias, eps, save, out, stream); kRms: without a bias.
+template <bool kRms>
+PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Target t;
+  Mat x, y;
+  at::ScalarType dt;
+  gemm_dtype_t code;
+  void *weight, *bias = nullptr;
+  if (!target(a, n, 9, &t) || !read_x(a[2], t.index, &dt, &code, &x, true)) return nullptr;
+  const int64_t T = x.rows, D = x.cols;
+  at::ScalarType wdt = dt;
+  gemm_dtype_t wcode = code;
+  if (!read_weight(a[3], t.index, D, &wdt, &wcode, &weight)) return nullptr;
+  if (!kRms && a[4] != Py_None) {
+    if (!weight) {
+      PyErr_SetString(PyExc_ValueError, "a bias needs a weight");
+      return nullptr;
+    }
+    if (!read_vector(a[4], "bias", wdt, t.index, D, &bias)) return nullptr;
+  }
+  const double eps = PyFloat_AsDouble(a[5]);
+  if (eps == -1.0 && PyErr_Occurred()) return nullptr;
+  const int save = PyObject_IsTrue(a[6]);
+  Stream stream;
+  if (save < 0 || !stream.open(a[8], t.index)) return nullptr;
+  Ref out(result(a[7], T, D, dt, t.index, &y));
+  if (!out.p) return nullptr;
+  void* sp = nullptr;
+  Ref stats(save ? empty(T, kRms ? 1 : 2, at::kFloat, t.index, &sp) : nullptr);
+  if (save && !stats.p) return nullptr;
+  gemm_status_t st;
+  Py_BEGIN_ALLOW_THREADS;
+  if constexpr (kRms)
+    st = g_rms(t.h, x.p, x.ld, weight, y.p, y.ld, static_cast<float*>(sp), T, D, static_cast<float>(eps), code, wcode,
+               stream.s);
+  else
+    st = g_ln(t.h, x.p, x.ld, weight, bias, y.p, y.ld, static_cast<float*>(sp), T, D, static_cast<float>(eps), code,
+              wcode, stream.s);
+  Py_END_ALLOW_THREADS;
+  if (failed(st, kRms ? "gemm_rms_norm" : "gemm_layer_norm")) return nullptr;
+  wrote(a[7]);
+  return save ? PyTuple_Pack(2, out.p, stats.p) : out.release();
+  END_HANDLE_TH_ERRORS
+}
+
+// (handle, index, dy, x, weight, stats, bias, stream); bias: whether its gradient
+// is wanted.
+template <bool kRms>
+PyObject* py_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Target t;
+  Mat dy, x, stats;
+  at::ScalarType dt;
+  gemm_dtype_t code;
+  void* weight;
+  if (!target(a, n, 8, &t) || !read_x(a[3], t.index, &dt, &code, &x, true)) return nullptr;
+  const int64_t T = x.rows, D = x.cols;
+  at::ScalarType wdt = dt;
+  gemm_dtype_t wcode = code;
+  if (!read_weight(a[4], t.index, D, &wdt, &wcode, &weight) || !read(a[2], "dy", dt, t.index, T, D, false, &dy) ||
+      !read(a[5], "stats", at::kFloat, t.index, T, kRms ? 1 : 2, true, &stats))
+    return nullptr;
+  const int bias = kRms ? 0 : PyObject_IsTrue(a[6]);
+  Stream stream;
+  if (bias < 0 || !stream.open(a[7], t.index)) return nullptr;
+  void *dxp, *dwp = nullptr, *dbp = nullptr;
+  Ref dx(empty(T, D, dt, t.index, &dxp));
+  if (!dx.p) return nullptr;
+  Ref dw(weight ? empty_vector(D, wdt, t.index, &dwp) : Py_NewRef(Py_None));
+  if (!dw.p) return nullptr;
+  Ref db(bias ? empty_vector(D, wdt, t.index, &dbp) : Py_NewRef(Py_None));
+  if (!db.p) return nullptr;
+  const size_t need = g_norm_bwd_space(t.h, T, D);
+  const Workspace ws(need, t.index);
+  gemm_status_t st;
+  Py_BEGIN_ALLOW_THREADS;
+  if constexpr (kRms)
+    st = g_rms_bwd(t.h, dy.p, dy.ld, x.p, x.ld, weight, static_cast<const float*>(stats.p), dxp, D, dwp, ws.p, need, T, D,
+                   code, wcode, stream.s);
+  else
+    st = g_ln_bwd(t.h, dy.p, dy.ld, x.p, x.ld, weight, static_cast<const float*>(stats.p), dxp, D, dwp, dbp, ws.p, need,
+                  T, D, code, wcode, stream.s);
+  Py_END_ALLOW_THREADS;
+  if (failed(st, kRms ? "gemm_rms_norm_backward" : "gemm_layer_norm_backward")) return nullptr;
+  if constexpr (kRms)
+    return PyTuple_Pack(2, dx.p, dw.p);
+  else
+    return PyTuple_Pack(3, dx.p, dw.p, db.p);
+  END_HANDLE_TH_ERRORS
+}
+
 // (tensor, name): refuses as no_graph does.
 PyObject* py_no_graph(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -388,29 +528,41 @@ PyObject* py_wrote(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (GemmError, then the addresses of the seven C functions)
-PyObject* py_setup(PyObject*, PyObject* args) {
-  unsigned long long f[7];
-  PyObject* error;
-  if (!PyArg_ParseTuple(args, "OKKKKKKK", &error, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6])) return nullptr;
-  Py_XSETREF(g_error, Py_NewRef(error));
-  g_ffn_space = reinterpret_cast<decltype(g_ffn_space)>(f[0]);
-  g_ffn = reinterpret_cast<decltype(g_ffn)>(f[1]);
-  g_bwd_space = reinterpret_cast<decltype(g_bwd_space)>(f[2]);
-  g_bwd = reinterpret_cast<decltype(g_bwd)>(f[3]);
-  g_w4_space = reinterpret_cast<decltype(g_w4_space)>(f[4]);
-  g_w4 = reinterpret_cast<decltype(g_w4)>(f[5]);
-  g_w4g = reinterpret_cast<decltype(g_w4g)>(f[6]);
+// (GemmError, then the addresses of the C functions, in this order)
+PyObject* py_setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  const std::pair<void*, size_t> fns[] = {
+      {&g_ffn_space, sizeof g_ffn_space}, {&g_ffn, sizeof g_ffn}, {&g_bwd_space, sizeof g_bwd_space},
+      {&g_bwd, sizeof g_bwd}, {&g_w4_space, sizeof g_w4_space}, {&g_w4, sizeof g_w4}, {&g_w4g, sizeof g_w4g},
+      {&g_ln, sizeof g_ln}, {&g_rms, sizeof g_rms}, {&g_norm_bwd_space, sizeof g_norm_bwd_space},
+      {&g_ln_bwd, sizeof g_ln_bwd}, {&g_rms_bwd, sizeof g_rms_bwd}};
+  constexpr Py_ssize_t want = 1 + sizeof fns / sizeof fns[0];
+  if (n != want) return PyErr_Format(PyExc_TypeError, "%zd arguments, %zd expected", n, want);
+  void* addr[want];
+  for (Py_ssize_t i = 1; i < want; ++i) {
+    addr[i] = PyLong_AsVoidPtr(a[i]);
+    if (!addr[i] && PyErr_Occurred()) return nullptr;
+  }
+  for (Py_ssize_t i = 1; i < want; ++i) std::memcpy(fns[i - 1].first, &addr[i], fns[i - 1].second);
+  Py_XSETREF(g_error, Py_NewRef(a[0]));
   Py_RETURN_NONE;
 }
 
+template <PyObject* (*kF)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyCFunction fast() {
+  return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kF));
+}
+
 PyMethodDef methods[] = {
-    {"setup", py_setup, METH_VARARGS, nullptr},
-    {"gated_ffn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_ffn)), METH_FASTCALL, nullptr},
-    {"gated_ffn_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_bwd)), METH_FASTCALL, nullptr},
-    {"w4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_w4)), METH_FASTCALL, nullptr},
-    {"no_graph", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_no_graph)), METH_FASTCALL, nullptr},
-    {"wrote", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_wrote)), METH_FASTCALL, nullptr},
+    {"setup", fast<py_setup>(), METH_FASTCALL, nullptr},
+    {"gated_ffn", fast<py_ffn>(), METH_FASTCALL, nullptr},
+    {"gated_ffn_backward", fast<py_bwd>(), METH_FASTCALL, nullptr},
+    {"w4", fast<py_w4>(), METH_FASTCALL, nullptr},
+    {"layer_norm", fast<py_norm<false>>(), METH_FASTCALL, nullptr},
+    {"rms_norm", fast<py_norm<true>>(), METH_FASTCALL, nullptr},
+    {"layer_norm_backward", fast<py_norm_bwd<false>>(), METH_FASTCALL, nullptr},
+    {"rms_norm_backward", fast<py_norm_bwd<true>>(), METH_FASTCALL, nullptr},
+    {"no_graph", fast<py_no_graph>(), METH_FASTCALL, nullptr},
+    {"wrote", fast<py_wrote>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,156 @@
+// norm.cu -- host side of the norms and their gradients.
+#include "host.cuh"
+#include "norm_kernels.cuh"
+
+namespace {
+
+using namespace gb300::ops;
+
+// f(x's type, the weight's): the weight is of x's type or fp32.
+template <class F>
+gemm_status_t with_types(gemm_dtype_t dtype, gemm_dtype_t wtype, F f) {
+  switch (dtype) {
+    case GEMM_F16: return wtype == GEMM_F32 ? f(__half(), float()) : f(__half(), __half());
+    case GEMM_BF16: return wtype == GEMM_F32 ? f(__nv_bfloat16(), float()) : f(__nv_bfloat16(), __nv_bfloat16());
+    default: return f(float(), float());
+  }
+}
+
+int64_t bytes_of(gemm_dtype_t t) { return t == GEMM_F32 ? 4 : 2; }
+
+gemm_status_t check_norm(const gemm_ops_s* h, int64_t T, int64_t D, gemm_dtype_t dtype, gemm_dtype_t wtype) {
+  if (!h || !dim_ok(T) || !dim_ok(D) || D == 0) return GEMM_ERR_INVALID_ARG;
+  if (dtype != GEMM_F16 && dtype != GEMM_BF16 && dtype != GEMM_F32) return GEMM_ERR_INVALID_ARG;
+  return wtype == dtype || wtype == GEMM_F32 ? GEMM_OK : GEMM_ERR_INVALID_ARG;
+}
+
+// Rows of D elements ld apart at an element's alignment.
+gemm_status_t check_rows(const void* p, int64_t ld, int64_t D, int64_t e) {
+  if (ld < D || ld >= (1ll << 30)) return GEMM_ERR_INVALID_ARG;
+  return reinterpret_cast<uintptr_t>(p) % e ? GEMM_ERR_ALIGNMENT : GEMM_OK;
+}
+
+unsigned row_threads(int64_t D) { return static_cast<unsigned>(std::min<int64_t>(512, up(D, 32))); }
+
+template <bool kRms>
+gemm_status_t norm(gemm_ops_s* h, const void* x, int64_t ldx, const void* weight, const void* bias, void* y, int64_t ldy,
+                   float* stats, int64_t T, int64_t D, float eps, gemm_dtype_t dtype, gemm_dtype_t wtype, void* stream) {
+  gemm_status_t st = check_norm(h, T, D, dtype, wtype);
+  if (st != GEMM_OK) return st;
+  if (!(eps >= 0.0f)) return GEMM_ERR_INVALID_ARG;
+  if (T == 0) return GEMM_OK;
+  const int64_t e = bytes_of(dtype), ew = bytes_of(wtype), ns = kRms ? 4 : 8;
+  if ((st = check_rows(x, ldx, D, e)) != GEMM_OK || (st = check_rows(y, ldy, D, e)) != GEMM_OK) return st;
+  for (auto [p, a] : {std::pair<const void*, int64_t>(weight, ew), {bias, ew}, {stats, 4}})
+    if (reinterpret_cast<uintptr_t>(p) % a) return GEMM_ERR_ALIGNMENT;
+  DeviceGuard g(h->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  const Buf bufs[] = {{x, T, D * e, ldx * e, false},
+                      {weight, weight ? 1 : 0, D * ew, D * ew, false},
+                      {bias, bias ? 1 : 0, D * ew, D * ew, false},
+                      {y, T, D * e, ldy * e, true},
+                      {stats, stats ? T : 0, ns, ns, true}};
+  if ((st = check_bufs(h, bufs)) != GEMM_OK) return st;
+  NormArgs a = {};
+  a.x = x, a.weight = weight, a.bias = bias, a.y = y, a.stats = stats;
+  a.ldx = ldx, a.ldy = ldy, a.T = T, a.D = D, a.eps = eps;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return with_types(dtype, wtype, [&](auto tx, auto tw) {
+    return launch(h, norm_any<decltype(tx), decltype(tw), kRms>, dim3(static_cast<unsigned>(T)), dim3(row_threads(D)), 0,
+                  1, s, a);
+  });
+}
+
+// Chunks of rows whose sums are taken apart: enough blocks of 32 columns for the
+// device, of at least 32 rows.
+int64_t row_chunks(const gemm_ops_s* h, int64_t T, int64_t D) {
+  return std::max<int64_t>(1, std::min(cdiv(T, 32), cdiv(8 * h->num_sms, cdiv(D, 32))));
+}
+
+template <bool kRms>
+gemm_status_t norm_backward(gemm_ops_s* h, const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* weight,
+                            const float* stats, void* dx, int64_t lddx, void* dweight, void* dbias, void* workspace,
+                            size_t workspace_bytes, int64_t T, int64_t D, gemm_dtype_t dtype, gemm_dtype_t wtype,
+                            void* stream) {
+  gemm_status_t st = check_norm(h, T, D, dtype, wtype);
+  if (st != GEMM_OK) return st;
+  const int64_t e = bytes_of(dtype), ew = bytes_of(wtype), ns = kRms ? 4 : 8;
+  for (auto [p, ld] : {std::pair<const void*, int64_t>(dy, lddy), {x, ldx}, {dx, lddx}})
+    if ((st = check_rows(p, ld, D, e)) != GEMM_OK) return st;
+  for (auto [p, a] : {std::pair<const void*, int64_t>(weight, ew), {dweight, ew}, {dbias, ew}, {stats, 4}, {workspace, 256}})
+    if (reinterpret_cast<uintptr_t>(p) % a) return GEMM_ERR_ALIGNMENT;
+  const size_t need = gemm_norm_backward_workspace(h, T, D);
+  if (workspace_bytes < need) return GEMM_ERR_INVALID_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  const Buf bufs[] = {{dy, T, D * e, lddy * e, false},
+                      {x, T, D * e, ldx * e, false},
+                      {weight, weight ? 1 : 0, D * ew, D * ew, false},
+                      {stats, T, ns, ns, false},
+                      {dx, T, D * e, lddx * e, true},
+                      {dweight, dweight ? 1 : 0, D * ew, D * ew, true},
+                      {dbias, dbias ? 1 : 0, D * ew, D * ew, true},
+                      {workspace, need ? 1 : 0, static_cast<int64_t>(need), static_cast<int64_t>(need), true}};
+  if ((st = check_bufs(h, bufs)) != GEMM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {  // no row, no gradient
+    for (void* p : {dweight, dbias})
+      if (p && cudaMemsetAsync(p, 0, D * ew, s) != cudaSuccess) return GEMM_ERR_CUDA;
+    return GEMM_OK;
+  }
+  NormArgs a = {};
+  a.x = x, a.dy = dy, a.weight = weight, a.y = dx, a.stats = const_cast<float*>(stats);
+  a.ldx = ldx, a.lddy = lddy, a.ldy = lddx, a.T = T, a.D = D;
+  a.partial = static_cast<float*>(workspace);
+  a.chunks = row_chunks(h, T, D);
+  a.dweight = dweight, a.dbias = dbias;
+  return with_types(dtype, wtype, [&](auto tx, auto tw) {
+    typedef decltype(tx) X;
+    typedef decltype(tw) W;
+    gemm_status_t st = launch(h, norm_dx_any<X, W, kRms>, dim3(static_cast<unsigned>(T)), dim3(row_threads(D)), 0, 1, s, a);
+    if (st != GEMM_OK || (!dweight && !dbias)) return st;
+    st = launch(h, norm_dw_any<X, kRms>, dim3(static_cast<unsigned>(cdiv(D, 32)), static_cast<unsigned>(a.chunks)),
+                dim3(256), 0, 1, s, a);
+    if (st != GEMM_OK) return st;
+    return launch(h, norm_dw_sum<W>, dim3(static_cast<unsigned>(cdiv(D, 256)), 2), dim3(256), 0, 1, s, a);
+  });
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_layer_norm(gemm_ops_t h, const void* x, int64_t ldx, const void* weight, const void* bias, void* y,
+                              int64_t ldy, float* stats, int64_t T, int64_t D, float eps, gemm_dtype_t dtype,
+                              gemm_dtype_t wtype, void* stream) {
+  return norm<false>(h, x, ldx, weight, bias, y, ldy, stats, T, D, eps, dtype, wtype, stream);
+}
+
+gemm_status_t gemm_rms_norm(gemm_ops_t h, const void* x, int64_t ldx, const void* weight, void* y, int64_t ldy,
+                            float* stats, int64_t T, int64_t D, float eps, gemm_dtype_t dtype, gemm_dtype_t wtype,
+                            void* stream) {
+  return norm<true>(h, x, ldx, weight, nullptr, y, ldy, stats, T, D, eps, dtype, wtype, stream);
+}
+
+size_t gemm_norm_backward_workspace(gemm_ops_t h, int64_t T, int64_t D) {
+  if (!h || T <= 0 || D <= 0 || !dim_ok(T) || !dim_ok(D)) return 0;
+  return row_chunks(h, T, D) * 2 * D * sizeof(float);
+}
+
+gemm_status_t gemm_layer_norm_backward(gemm_ops_t h, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                       const void* weight, const float* stats, void* dx, int64_t lddx, void* dweight,
+                                       void* dbias, void* workspace, size_t workspace_bytes, int64_t T, int64_t D,
+                                       gemm_dtype_t dtype, gemm_dtype_t wtype, void* stream) {
+  return norm_backward<false>(h, dy, lddy, x, ldx, weight, stats, dx, lddx, dweight, dbias, workspace, workspace_bytes, T,
+                              D, dtype, wtype, stream);
+}
+
+gemm_status_t gemm_rms_norm_backward(gemm_ops_t h, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                     const void* weight, const float* stats, void* dx, int64_t lddx, void* dweight,
+                                     void* workspace, size_t workspace_bytes, int64_t T, int64_t D, gemm_dtype_t dtype,
+                                     gemm_dtype_t wtype, void* stream) {
+  return norm_backward<true>(h, dy, lddy, x, ldx, weight, stats, dx, lddx, dweight, nullptr, workspace, workspace_bytes,
+                             T, D, dtype, wtype, stream);
+}
+
+}  // extern "C"

@@ -1,11 +1,12 @@
 """Operators beside the GEMM: the gated feed-forward block, its backward pass,
-its products from 4-bit weights, and the orthogonalised update of its matrices.
+its products from 4-bit weights, the orthogonalised update of its matrices, and
+layer and RMS norm with their gradients.
 
-Thin bindings over the C ABI in ``include/gemm_ops.h``: the block and the 4-bit
-products through the compiled ``_binding`` (a call for one token costs the host
-more than the GPU), ``orthogonalize`` through ctypes.  Every step runs in the
+Thin bindings over the C ABI in ``include/gemm_ops.h``: through the compiled
+``_binding`` (a call for one token costs the host more than the GPU), and
+``orthogonalize`` through ctypes.  Every step runs in the
 sm_103a kernels of ``libgb300gemm.so``.  Tensors are CUDA tensors of one device,
-float16 or bfloat16; results and workspaces come from torch's allocator, on the
+float16 or bfloat16 (the norms and ``orthogonalize`` also take float32); results and workspaces come from torch's allocator, on the
 stream of the call (the current one, or ``stream``).  As with any work on another
 stream, the caller orders it after what made the inputs and keeps them until it
 has run (``Tensor.record_stream``).  There is no fallback: wrong arguments and
@@ -14,7 +15,8 @@ other devices raise.
 The operators record no graph.  A tensor that requires grad (while gradients are
 recorded) or has a forward-mode tangent is refused with a RuntimeError: call them
 under ``torch.no_grad()`` or on detached tensors, or from the methods of a
-``torch.autograd.Function``, whose backward is :func:`gated_ffn_backward`.
+``torch.autograd.Function``, whose backward is :func:`gated_ffn_backward` (or
+the norm's).
 
     >>> import torch, dense_fp16_gemm_04_gb300 as g
     >>> x = torch.randn(4096, 1024, device="cuda", dtype=torch.float16)
@@ -36,7 +38,8 @@ import torch
 from . import GemmError, _build, _check, load as _load
 
 __all__ = ["Ops", "default_ops", "gated_ffn", "gated_ffn_backward", "w4_linear", "w4_gated",
-           "w4_quantize", "orthogonalize", "NEWTON_SCHULZ"]
+           "w4_quantize", "orthogonalize", "NEWTON_SCHULZ", "layer_norm", "layer_norm_backward",
+           "rms_norm", "rms_norm_backward"]
 
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
@@ -101,7 +104,9 @@ def _load_binding():
             mod = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(mod)
             fns = ("gemm_gated_ffn_workspace", "gemm_gated_ffn", "gemm_gated_ffn_backward_workspace",
-                   "gemm_gated_ffn_backward", "gemm_w4_workspace", "gemm_w4_linear", "gemm_w4_gated")
+                   "gemm_gated_ffn_backward", "gemm_w4_workspace", "gemm_w4_linear", "gemm_w4_gated",
+                   "gemm_layer_norm", "gemm_rms_norm", "gemm_norm_backward_workspace",
+                   "gemm_layer_norm_backward", "gemm_rms_norm_backward")
             mod.setup(GemmError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in fns))
             _binding = mod
     return _binding
@@ -164,6 +169,19 @@ class Ops:
         if act is None:
             raise ValueError("act must be 'silu', 'gelu_tanh' or 'relu', got None")
         return self._b.w4(self._addr, self.index, x, codes, scales, zeros, act, out, stream)
+
+    # -- norms --------------------------------------------------------------
+    def layer_norm(self, x, weight=None, bias=None, eps=1e-5, save=False, out=None, stream=None):
+        return self._b.layer_norm(self._addr, self.index, x, weight, bias, eps, save, out, stream)
+
+    def layer_norm_backward(self, dy, x, weight, stats, bias=True, stream=None):
+        return self._b.layer_norm_backward(self._addr, self.index, dy, x, weight, stats, bias, stream)
+
+    def rms_norm(self, x, weight=None, eps=1e-6, save=False, out=None, stream=None):
+        return self._b.rms_norm(self._addr, self.index, x, weight, None, eps, save, out, stream)
+
+    def rms_norm_backward(self, dy, x, weight, stats, stream=None):
+        return self._b.rms_norm_backward(self._addr, self.index, dy, x, weight, stats, False, stream)
 
     # -- the orthogonalised update -------------------------------------------
     def orthogonalize(self, m, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, dtype=None, out=None, stream=None):
@@ -302,3 +320,33 @@ def orthogonalize(m, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, dtype=None, out=No
     fp32 accuracy.  m is float16, bfloat16 or float32; the result has ``dtype``
     (m's by default)."""
     return _of(m, ops).orthogonalize(m, steps, coeffs, eps, dtype, out, stream)
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, save=False, out=None, stream=None, ops: Ops | None = None):
+    """y = (x - m) r weight + bias for each row of x [T, D], with the row's mean m
+    and r = 1 / sqrt(mean (x - m)^2 + eps).
+
+    x is float16, bfloat16 or float32, weight and bias [D] of its type or float32
+    (None for 1 and 0).  Returns y, of x's type, and with ``save`` also stats
+    [T, 2] float32, m and r, that :func:`layer_norm_backward` takes.  Rows may be
+    strided."""
+    return _of(x, ops).layer_norm(x, weight, bias, eps, save, out, stream)
+
+
+def layer_norm_backward(dy, x, weight, stats, bias=True, stream=None, ops: Ops | None = None):
+    """Gradients (dx, dweight, dbias) of :func:`layer_norm` from dy [T, D].  dweight
+    is None where weight is, dbias (of weight's type, x's without one) where ``bias``
+    is false."""
+    return _of(x, ops).layer_norm_backward(dy, x, weight, stats, bias, stream)
+
+
+def rms_norm(x, weight=None, eps=1e-6, save=False, out=None, stream=None, ops: Ops | None = None):
+    """y = x r weight for each row of x [T, D], with r = 1 / sqrt(mean x^2 + eps).
+    As :func:`layer_norm`; stats are [T, 1], r alone."""
+    return _of(x, ops).rms_norm(x, weight, eps, save, out, stream)
+
+
+def rms_norm_backward(dy, x, weight, stats, stream=None, ops: Ops | None = None):
+    """Gradients (dx, dweight) of :func:`rms_norm` from dy [T, D]; dweight is None
+    where weight is."""
+    return _of(x, ops).rms_norm_backward(dy, x, weight, stats, stream)

@@ -1,7 +1,8 @@
 /*
  * gemm_ops.h -- C ABI of the operators beside the GEMM of gemm.h: the gated
  * feed-forward block of a language model, its backward pass, its products
- * from 4-bit weights, and the orthogonalised update of its matrices.
+ * from 4-bit weights, the orthogonalised update of its matrices, and layer and
+ * RMS norm with their gradients.
  *
  * Types: GEMM_F16 or GEMM_BF16 for every 16-bit tensor of a call; sums run in
  * fp32.  Matrices are row-major; ld* is the distance between rows in elements
@@ -39,7 +40,7 @@ typedef struct gemm_ops_s* gemm_ops_t;
 typedef enum {
     GEMM_F16 = 0,
     GEMM_BF16 = 1,
-    GEMM_F32 = 2 /* gemm_orthogonalize's input and output only */
+    GEMM_F32 = 2 /* gemm_orthogonalize's input and output, and the norms */
 } gemm_dtype_t;
 
 /* The gate's activation.  GELU is its tanh form,
@@ -165,6 +166,49 @@ GEMM_API gemm_status_t gemm_orthogonalize(gemm_ops_t ops, const void* m, int64_t
                                           size_t workspace_bytes, int64_t batch, int64_t M, int64_t N,
                                           int32_t steps, const float coeffs[3], float eps,
                                           gemm_dtype_t in_dtype, gemm_dtype_t out_dtype, void* stream);
+
+/* Layer norm and RMS norm of T rows of D elements:
+ *
+ *     layer norm  m = mean x,  r = 1 / sqrt(mean (x - m)^2 + eps),  y = (x - m) r w + b
+ *     RMS norm    r = 1 / sqrt(mean x^2 + eps),                     y = x r w
+ *
+ *   x, y         : [T, D] of `dtype` (GEMM_F16, GEMM_BF16 or GEMM_F32)
+ *   weight, bias : [D] contiguous, of `wtype` (dtype or GEMM_F32); NULL for 1 and 0
+ *   stats        : fp32, contiguous, or NULL: receives m and r of each row ([T, 2];
+ *                  RMS norm: r, [T, 1]) for the backward pass
+ * Any alignment of whole elements and any row distance from D on (below 2^30);
+ * D is at least 1, T == 0 has nothing to do.  Statistics and sums are fp32: the sum
+ * of squares of a row's x - m (x) must stay below 2^128.  A row that holds an
+ * infinity or NaN comes out NaN where the formula has it, and no other row changes. */
+GEMM_API gemm_status_t gemm_layer_norm(gemm_ops_t ops, const void* x, int64_t ldx, const void* weight,
+                                       const void* bias, void* y, int64_t ldy, float* stats, int64_t T,
+                                       int64_t D, float eps, gemm_dtype_t dtype, gemm_dtype_t wtype,
+                                       void* stream);
+GEMM_API gemm_status_t gemm_rms_norm(gemm_ops_t ops, const void* x, int64_t ldx, const void* weight, void* y,
+                                     int64_t ldy, float* stats, int64_t T, int64_t D, float eps,
+                                     gemm_dtype_t dtype, gemm_dtype_t wtype, void* stream);
+
+/* Their gradients, given dy and the statistics kept: with h = (x - m) r (x r), q = dy w,
+ *
+ *     dx = r (q - mean q - h mean(q h))        (RMS norm: r (q - h mean(q h)))
+ *     dweight = sum over the rows of dy h,  dbias = sum over the rows of dy
+ *
+ *   dy, dx         : [T, D] of `dtype`
+ *   dweight, dbias : [D] contiguous, of `wtype`; NULL: not wanted
+ * Gradients are written, not accumulated; T == 0 gives zero dweight and dbias.
+ * The rows are summed in an order that T and D alone decide.  Rules as above.
+ * workspace: gemm_norm_backward_workspace(ops, T, D) bytes, 256-byte aligned. */
+GEMM_API size_t gemm_norm_backward_workspace(gemm_ops_t ops, int64_t T, int64_t D);
+GEMM_API gemm_status_t gemm_layer_norm_backward(gemm_ops_t ops, const void* dy, int64_t lddy, const void* x,
+                                                int64_t ldx, const void* weight, const float* stats, void* dx,
+                                                int64_t lddx, void* dweight, void* dbias, void* workspace,
+                                                size_t workspace_bytes, int64_t T, int64_t D, gemm_dtype_t dtype,
+                                                gemm_dtype_t wtype, void* stream);
+GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_ops_t ops, const void* dy, int64_t lddy, const void* x,
+                                              int64_t ldx, const void* weight, const float* stats, void* dx,
+                                              int64_t lddx, void* dweight, void* workspace, size_t workspace_bytes,
+                                              int64_t T, int64_t D, gemm_dtype_t dtype, gemm_dtype_t wtype,
+                                              void* stream);
 
 #ifdef __cplusplus
 }
