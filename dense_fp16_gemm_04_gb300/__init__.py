@@ -32,7 +32,7 @@ __all__ = [
 # Operators beside the GEMM (ops.py; loaded with torch on first use).
 _OPS = ("Ops", "default_ops", "gated_ffn", "gated_ffn_backward", "w4_linear", "w4_gated",
         "w4_quantize", "orthogonalize", "NEWTON_SCHULZ", "layer_norm", "layer_norm_backward",
-        "rms_norm", "rms_norm_backward")
+        "rms_norm", "rms_norm_backward", "linear_cross_entropy", "linear_cross_entropy_backward")
 if importlib.util.find_spec("torch") is not None:  # a star import looks every name up
     __all__ += _OPS
 

@@ -36,6 +36,10 @@ decltype(&gemm_rms_norm) g_rms;
 decltype(&gemm_norm_backward_workspace) g_norm_bwd_space;
 decltype(&gemm_layer_norm_backward) g_ln_bwd;
 decltype(&gemm_rms_norm_backward) g_rms_bwd;
+decltype(&gemm_linear_cross_entropy_workspace) g_xent_space;
+decltype(&gemm_linear_cross_entropy) g_xent;
+decltype(&gemm_linear_cross_entropy_backward_workspace) g_xent_bwd_space;
+decltype(&gemm_linear_cross_entropy_backward) g_xent_bwd;
 
 PyObject* s_cuda_stream;
 
@@ -69,6 +73,8 @@ const char* type_name(at::ScalarType t) {
     case at::kHalf: return "float16";
     case at::kBFloat16: return "bfloat16";
     case at::kByte: return "uint8";
+    case at::kFloat: return "float32";
+    case at::kLong: return "int64";
     default: return c10::toString(t);
   }
 }
@@ -166,15 +172,17 @@ bool read_x(PyObject* x, int64_t index, at::ScalarType* dtype, gemm_dtype_t* cod
   return read(x, "x", *dtype, index, -1, -1, false, m);
 }
 
-// A vector of n elements side by side.
-bool read_vector(PyObject* o, const char* name, at::ScalarType dtype, int64_t index, int64_t n, void** p) {
+// A vector of n elements side by side, or, where the operator takes any, `stride` apart.
+bool read_vector(PyObject* o, const char* name, at::ScalarType dtype, int64_t index, int64_t n, void** p,
+                 int64_t* stride = nullptr) {
   const at::Tensor* t = operand(o, name, dtype, index);
   if (!t) return false;
   if (t->dim() != 1 || t->size(0) != n) {
     PyErr_Format(PyExc_ValueError, "%s must be 1-D of %lld elements", name, static_cast<long long>(n));
     return false;
   }
-  if (n > 1 && t->stride(0) != 1) {
+  if (stride) *stride = n > 1 ? t->stride(0) : 1;
+  if (!stride && n > 1 && t->stride(0) != 1) {
     PyErr_Format(PyExc_ValueError, "%s must be contiguous", name);
     return false;
   }
@@ -507,6 +515,79 @@ PyObject* py_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// (handle, index, x, w, targets, ignore_index, save, out, stream)
+PyObject* py_xent(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Target t;
+  Mat x, w;
+  at::ScalarType dt;
+  gemm_dtype_t code;
+  void *targets, *loss, *lse = nullptr;
+  int64_t ignore;
+  if (!target(a, n, 9, &t) || !read_x(a[2], t.index, &dt, &code, &x) ||
+      !read(a[3], "w", dt, t.index, -1, x.cols, false, &w) ||
+      !read_vector(a[4], "targets", at::kLong, t.index, x.rows, &targets) || !to_i64(a[5], &ignore))
+    return nullptr;
+  const int64_t T = x.rows, D = x.cols, V = w.rows;
+  const int save = PyObject_IsTrue(a[6]);
+  Stream stream;
+  if (save < 0 || !stream.open(a[8], t.index)) return nullptr;
+  const bool given = a[7] != Py_None;
+  if (given && !read_vector(a[7], "out", at::kFloat, t.index, T, &loss)) return nullptr;
+  Ref out(given ? Py_NewRef(a[7]) : empty_vector(T, at::kFloat, t.index, &loss));
+  if (!out.p) return nullptr;
+  Ref kept(save ? empty_vector(T, at::kFloat, t.index, &lse) : nullptr);
+  if (save && !kept.p) return nullptr;
+  const size_t need = g_xent_space(t.h, T, D, V);
+  const Workspace ws(need, t.index);
+  gemm_status_t st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = g_xent(t.h, x.p, x.ld, w.p, w.ld, static_cast<const int64_t*>(targets), static_cast<float*>(loss),
+              static_cast<float*>(lse), ws.p, need, T, D, V, ignore, code, stream.s);
+  Py_END_ALLOW_THREADS;
+  if (failed(st, "gemm_linear_cross_entropy")) return nullptr;
+  wrote(a[7]);
+  return save ? PyTuple_Pack(2, out.p, kept.p) : out.release();
+  END_HANDLE_TH_ERRORS
+}
+
+// (handle, index, dloss, x, w, targets, lse, ignore_index, dlse or None, stream)
+PyObject* py_xent_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Target t;
+  Mat x, w;
+  at::ScalarType dt;
+  gemm_dtype_t code;
+  void *dloss, *dlse = nullptr, *targets, *lse;
+  int64_t ignore, dloss_stride, dlse_stride = 0;
+  if (!target(a, n, 10, &t) || !read_x(a[3], t.index, &dt, &code, &x) ||
+      !read(a[4], "w", dt, t.index, -1, x.cols, false, &w) ||
+      !read_vector(a[2], "dloss", at::kFloat, t.index, x.rows, &dloss, &dloss_stride) ||
+      !read_vector(a[5], "targets", at::kLong, t.index, x.rows, &targets) ||
+      !read_vector(a[6], "lse", at::kFloat, t.index, x.rows, &lse) || !to_i64(a[7], &ignore))
+    return nullptr;
+  if (a[8] != Py_None && !read_vector(a[8], "dlse", at::kFloat, t.index, x.rows, &dlse, &dlse_stride)) return nullptr;
+  const int64_t T = x.rows, D = x.cols, V = w.rows;
+  Stream stream;
+  if (!stream.open(a[9], t.index)) return nullptr;
+  void *dxp, *dwp;
+  Ref dx(empty(T, D, dt, t.index, &dxp));
+  if (!dx.p) return nullptr;
+  Ref dw(empty(V, D, dt, t.index, &dwp));
+  if (!dw.p) return nullptr;
+  const size_t need = g_xent_bwd_space(t.h, T, D, V);
+  const Workspace ws(need, t.index);
+  gemm_status_t st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = g_xent_bwd(t.h, static_cast<const float*>(dloss), dloss_stride, static_cast<const float*>(dlse), dlse_stride, x.p,
+                  x.ld, w.p, w.ld, static_cast<const int64_t*>(targets), static_cast<const float*>(lse), dxp, D, dwp, ws.p,
+                  need, T, D, V, ignore, code, stream.s);
+  Py_END_ALLOW_THREADS;
+  if (failed(st, "gemm_linear_cross_entropy_backward")) return nullptr;
+  return PyTuple_Pack(2, dx.p, dw.p);
+  END_HANDLE_TH_ERRORS
+}
+
 // (tensor, name): refuses as no_graph does.
 PyObject* py_no_graph(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -534,7 +615,9 @@ PyObject* py_setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
       {&g_ffn_space, sizeof g_ffn_space}, {&g_ffn, sizeof g_ffn}, {&g_bwd_space, sizeof g_bwd_space},
       {&g_bwd, sizeof g_bwd}, {&g_w4_space, sizeof g_w4_space}, {&g_w4, sizeof g_w4}, {&g_w4g, sizeof g_w4g},
       {&g_ln, sizeof g_ln}, {&g_rms, sizeof g_rms}, {&g_norm_bwd_space, sizeof g_norm_bwd_space},
-      {&g_ln_bwd, sizeof g_ln_bwd}, {&g_rms_bwd, sizeof g_rms_bwd}};
+      {&g_ln_bwd, sizeof g_ln_bwd}, {&g_rms_bwd, sizeof g_rms_bwd},
+      {&g_xent_space, sizeof g_xent_space}, {&g_xent, sizeof g_xent}, {&g_xent_bwd_space, sizeof g_xent_bwd_space},
+      {&g_xent_bwd, sizeof g_xent_bwd}};
   constexpr Py_ssize_t want = 1 + sizeof fns / sizeof fns[0];
   if (n != want) return PyErr_Format(PyExc_TypeError, "%zd arguments, %zd expected", n, want);
   void* addr[want];
@@ -561,6 +644,8 @@ PyMethodDef methods[] = {
     {"rms_norm", fast<py_norm<true>>(), METH_FASTCALL, nullptr},
     {"layer_norm_backward", fast<py_norm_bwd<false>>(), METH_FASTCALL, nullptr},
     {"rms_norm_backward", fast<py_norm_bwd<true>>(), METH_FASTCALL, nullptr},
+    {"linear_cross_entropy", fast<py_xent>(), METH_FASTCALL, nullptr},
+    {"linear_cross_entropy_backward", fast<py_xent_bwd>(), METH_FASTCALL, nullptr},
     {"no_graph", fast<py_no_graph>(), METH_FASTCALL, nullptr},
     {"wrote", fast<py_wrote>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

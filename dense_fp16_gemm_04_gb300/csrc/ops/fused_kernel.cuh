@@ -1,6 +1,6 @@
 // fused_kernel.cuh -- products with fused epilogues on the tensor cores
 // (tcgen05) of sm_103a: the matrix work of the gated feed-forward block, of
-// its backward pass and of the orthogonalised update.
+// its backward pass, of the orthogonalised update and of a vocabulary's loss.
 //
 //   acc[m, n] = sum over segments s, k of A[m, k; za(s)] B[n, k; zb(s)]
 //
@@ -22,6 +22,11 @@
 //                the source S.
 //   kEpiSplitSym the same for a symmetric C: only tiles on and above the
 //                diagonal are computed, and each is also stored transposed.
+//   kEpiLse      acc = logits z: no C, but for each row and each share of a
+//                tile's columns their maximum and sum of exponentials, and the
+//                row's target logit (xent_kernels.cuh).
+//   kEpiXent     acc = logits z: C = a exp(z - lse) - b [column = target].
+//   kEpiSum      C = acc or C += acc, fp32.
 //
 // What bounds them.  Large products: the tensor cores, and the power they draw
 // (gated block of 8192 tokens, 8192 x 16384: 4100 us, 1610 TFLOP/s; its backward
@@ -66,6 +71,17 @@ enum FusedEpi : int {
   kEpiGluBwd = 2,
   kEpiSplit = 3,
   kEpiSplitSym = 4,
+  kEpiLse = 5,
+  kEpiXent = 6,
+  kEpiSum = 7,
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// What kEpiXent needs of a row: lse log2(e), a, b and the target's column (-1: none).
+struct alignas(16) XentRow {
+  float lse2, a, b;
+  int32_t target;
 };
 
 struct FusedArgs {
@@ -97,10 +113,53 @@ struct FusedArgs {
   uint16_t *c, *d;
   int64_t ldd, d_up;
   int64_t ldc, c_z;           // c_z: from one matrix of C's stack to the next
+  const float* alpha_p;       // kEpiStore: times alpha, null for 1
+  // kEpiLse: targets [M], their logits [M] and the shares' (maximum, sum) [share][M].
+  const int64_t* targets;
+  float* target_z;
+  float2* shares;
+  const XentRow* xent_rows;   // kEpiXent: [M]
+  int32_t col_base;           // kEpiXent: column 0 in the vocabulary
+  int32_t add;                // kEpiSum: to what is there
   uint32_t* err;
   uint64_t timeout_ns;
   int32_t skip_kb;            // fault injection, -1 = off
 };
+
+// A share's running maximum m and sum s of exponentials, s = sum exp(z - m); where
+// m is infinite, s = sum exp(z).  Takes in kN more logits.
+template <int kN>
+__device__ __forceinline__ void lse_take(const float (&z)[kN], float& m, float& s) {
+  float top = z[0];
+#pragma unroll
+  for (int i = 1; i < kN; ++i) top = fmaxf(top, z[i]);
+  top = fmaxf(m, top);  // NaN drops out here, and comes back through s
+  const float ref = isinf(top) ? 0.0f : top;
+  const float k = -ref * kLog2e;
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kN; ++i) sum[i & 3] += ptx::ex2(fmaf(z[i], kLog2e, k));
+  s = fmaf(s, ptx::ex2((m - ref) * kLog2e), (sum[0] + sum[1]) + (sum[2] + sum[3]));
+  m = top;
+}
+
+// a exp(z - lse), less b at the target: what kEpiXent stores.  A row of no loss and
+// no gradient of its lse is zero, whatever its logits.
+template <int kN>
+__device__ __forceinline__ void xent_columns(const XentRow& r, int32_t col, float (&v)[kN]) {
+  const bool none = r.a == 0.0f && r.b == 0.0f;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const float e = r.a * ptx::ex2(fmaf(v[i], kLog2e, -r.lse2));
+    v[i] = none ? 0.0f : e;
+  }
+  const int32_t at = r.target - col;
+  if (at >= 0 && at < kN && !none) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (i == at) v[i] -= r.b;
+  }
+}
 
 template <int kCtas_, int kBN_, int kStages_, int kEpi_, int kEpiBufs_, int kSplit_ = 1, int kParts_ = 1>
 struct FusedCfg {
@@ -133,7 +192,8 @@ struct FusedCfg {
   static constexpr int kOffEpi = kOffB + kStages * kBBytes;
   static constexpr int kOffBar = kOffEpi + kEpiWarps * kEpiBufs * kBufBytes;
   // Few rows leave room for more k-blocks: their number is the launch's.
-  static constexpr bool kFlex = kCtas == 1 && (kEpi == kEpiStore || kEpi == kEpiGlu);
+  static constexpr bool kFlex =
+      kCtas == 1 && (kEpi == kEpiStore || kEpi == kEpiGlu || kEpi == kEpiLse || kEpi == kEpiXent);
   static constexpr int kMaxStages = kFlex ? 8 : kStages;
   static constexpr int kNumBars = 2 * kMaxStages + 5;
   static constexpr int kOffSlot = kOffBar + kNumBars * 8;
@@ -204,16 +264,35 @@ __device__ __forceinline__ void finish_columns(const FusedArgs& args, const Fuse
   // Columns come in groups of eight that are in or out together (four, gated
   // over eight CTAs): N is a multiple of 8, or the rows are padded to one.
   constexpr int kG = kN < 8 ? kN : 8;
-  if constexpr (Cfg::kEpi == kEpiStore) {
+  if constexpr (Cfg::kEpi == kEpiStore || Cfg::kEpi == kEpiXent) {
     uint16_t* c = args.c + wi.batch * args.c_zb * args.c_z + static_cast<int64_t>(row) * args.ldc + col0;
+    float w[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) w[i] = v[i];
+    if constexpr (Cfg::kEpi == kEpiXent) {
+      xent_columns<kN>(args.xent_rows[row], args.col_base + col0, w);
+    } else {
+      const float alpha = args.alpha_p ? args.alpha * *args.alpha_p : args.alpha;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) w[i] *= alpha;
+    }
 #pragma unroll
     for (int i = 0; i < kN; i += kG) {
       uint32_t p[kG / 2];
 #pragma unroll
-      for (int j = 0; j < kG / 2; ++j)
-        p[j] = pack16(bf16, args.alpha * v[i + 2 * j], args.alpha * v[i + 2 * j + 1]);
+      for (int j = 0; j < kG / 2; ++j) p[j] = pack16(bf16, w[i + 2 * j], w[i + 2 * j + 1]);
       if (col0 + i < args.N) store16<kG>(c + i, p);
     }
+  } else if constexpr (Cfg::kEpi == kEpiLse) {
+    float z[kN], m = -INFINITY, s = 0.0f;
+    const int64_t at = args.targets[row] - col0;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      z[i] = col0 + i < args.N ? v[i] : -INFINITY;
+      if (i == at && col0 + i < args.N) args.target_z[row] = v[i];
+    }
+    lse_take<kN>(z, m, s);
+    args.shares[static_cast<int64_t>(col0 / kN) * args.M + row] = make_float2(m, s);
   } else if constexpr (Cfg::kEpi == kEpiGlu) {
     uint16_t* c = args.c + static_cast<int64_t>(row) * args.ldc + col0;
     uint16_t* d = args.d + static_cast<int64_t>(row) * args.ldd + col0;
@@ -373,7 +452,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
   const FusedItem wi = fused_item<Cfg>(args, unit, rank);
   const int32_t row = wi.mb * Cfg::kBM + r;
   const int32_t col0 = wi.nb * Cfg::kOutN + rank * (Cfg::kOutN / kS) + half * kN;
-  const bool in = row < args.M && col0 < args.N;
+  const bool in = row < args.M && (col0 < args.N || Cfg::kEpi == kEpiLse);  // (every share is written)
   uint4 s0[Cfg::kReads ? kN / 8 : 1], s1[Cfg::kReads ? kN / 8 : 1];
   if (in) read_columns<Cfg, kN>(args, wi, row, col0, s0, s1);
   ptx::cluster_sync();
@@ -703,6 +782,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         sb + Cfg::kOffEpi + static_cast<uint32_t>((warp - 4) * Cfg::kEpiBufs * Cfg::kBufBytes);
     const uint32_t tempty_bar0 = kPair ? ptx::mapa(bar_tempty(0), leader) : bar_tempty(0);
     const bool bf16 = args.bf16 != 0;
+    const float alpha = Cfg::kEpi == kEpiStore && args.alpha_p ? args.alpha * *args.alpha_p : args.alpha;
     uint32_t next_buf = 0, used = 0;
     int32_t acc_iter = 0;
     // The next free staging buffer: once the store that last read it is done.
@@ -729,7 +809,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if (in) ptx::tma_store_3d(m, sbuf, col0, row0, z);
+        if (in) {
+          if (Cfg::kEpi == kEpiSum && args.add)
+            ptx::tma_add_3d(m, sbuf, col0, row0, z);
+          else
+            ptx::tma_store_3d(m, sbuf, col0, row0, z);
+        }
         ptx::bulk_commit_group();
       }
     };
@@ -801,7 +886,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         }
       };
       constexpr int kChunks = Cfg::kOutN / 64;
+      static_assert(Cfg::kEpi != kEpiLse || kChunks >= Cfg::kGroups, "every warp has a share");
       if (group >= kChunks) release_tmem();
+      // The share of this tile: kEpiLse.
+      float share_m = -INFINITY, share_s = 0.0f;
+      int64_t target = -1;
+      if constexpr (Cfg::kEpi == kEpiLse)
+        if (row_in) target = args.targets[row];
+      XentRow xr = {};
+      if constexpr (Cfg::kEpi == kEpiXent)
+        if (row_in) xr = args.xent_rows[row];
 #pragma unroll 1
       for (int c = group; c < kChunks; c += Cfg::kGroups) {
         const int32_t col0 = wi.nb * Cfg::kOutN + c * 64;
@@ -816,12 +910,62 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           if (last) release_tmem();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            packed[i] = pack16(bf16, args.alpha * __uint_as_float(v0[2 * i]),
-                               args.alpha * __uint_as_float(v0[2 * i + 1]));
-            packed[16 + i] = pack16(bf16, args.alpha * __uint_as_float(v1[2 * i]),
-                                    args.alpha * __uint_as_float(v1[2 * i + 1]));
+            packed[i] = pack16(bf16, alpha * __uint_as_float(v0[2 * i]), alpha * __uint_as_float(v0[2 * i + 1]));
+            packed[16 + i] = pack16(bf16, alpha * __uint_as_float(v1[2 * i]), alpha * __uint_as_float(v1[2 * i + 1]));
           }
           store_chunk(&tmC, packed, col0, row0, wi.batch * args.c_zb, in);
+        } else if constexpr (Cfg::kEpi == kEpiLse) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t v[32];
+            float z[32];
+            ptx::tmem_ld_32x32b_x32(t_row + c * 64 + half * 32, v);
+            ptx::tmem_wait_ld(v);
+            if (half == 1 && last) release_tmem();
+            const int32_t first = col0 + half * 32;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(v[i]);
+            // (target - first) is out of range for no target and for one past the vocabulary.
+            const int64_t at = target < args.N ? target - first : -1;
+            if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (at == i) args.target_z[row] = z[i];
+            }
+            if (first + 32 > args.N) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) z[i] = first + i < args.N ? z[i] : -INFINITY;
+            }
+            lse_take<32>(z, share_m, share_s);
+          }
+          if (last && row_in)
+            args.shares[(static_cast<int64_t>(wi.nb) * Cfg::kGroups + group) * args.M + row] =
+                make_float2(share_m, share_s);
+        } else if constexpr (Cfg::kEpi == kEpiXent) {
+          uint32_t packed[32];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t v[32];
+            float z[32];
+            ptx::tmem_ld_32x32b_x32(t_row + c * 64 + half * 32, v);
+            ptx::tmem_wait_ld(v);
+            if (half == 1 && last) release_tmem();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(v[i]);
+            xent_columns<32>(xr, args.col_base + col0 + half * 32, z);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) packed[half * 16 + i] = pack16(bf16, z[2 * i], z[2 * i + 1]);
+          }
+          store_chunk(&tmC, packed, col0, row0, 0, in);
+        } else if constexpr (Cfg::kEpi == kEpiSum) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t v[32];
+            ptx::tmem_ld_32x32b_x32(t_row + c * 64 + half * 32, v);
+            ptx::tmem_wait_ld(v);
+            if (half == 1 && last) release_tmem();
+            store_chunk(&tmC, v, col0 + half * 32, row0, 0, in && col0 + half * 32 < args.N);
+          }
         } else if constexpr (Cfg::kEpi == kEpiGlu) {
           uint32_t h[32], gp[32], up[32];
 #pragma unroll

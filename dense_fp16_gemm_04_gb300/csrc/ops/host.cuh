@@ -28,9 +28,8 @@ struct gemm_ops_s {
   std::atomic<uint64_t> launches{0};
 };
 
-namespace {
-
-using namespace gb300::ops;
+namespace gb300 {
+namespace ops {
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -65,7 +64,7 @@ struct DeviceGuard {
   }
 };
 
-bool on_device(const void* ptr, int dev) {
+inline bool on_device(const void* ptr, int dev) {
   cudaPointerAttributes at;
   if (cudaPointerGetAttributes(&at, ptr) != cudaSuccess) {
     cudaGetLastError();
@@ -91,14 +90,14 @@ struct Buf {
 // Whether units of x and y (wx and wy bytes, nx and ny of them, px and py apart)
 // interleave without touching, as the halves of one matrix's columns do.  Units of
 // one pitch only: a lone one takes the other's.
-bool interleaved(uintptr_t x, int64_t wx, int64_t px, int64_t nx, uintptr_t y, int64_t wy, int64_t py, int64_t ny) {
+inline bool interleaved(uintptr_t x, int64_t wx, int64_t px, int64_t nx, uintptr_t y, int64_t wy, int64_t py, int64_t ny) {
   const int64_t p = nx > 1 ? px : py;
   if ((nx > 1 && ny > 1 && px != py) || p <= 0) return false;
   const int64_t d = static_cast<int64_t>((x % p + p - y % p) % p);  // of x's units behind y's
   return d >= wy && d + wx <= p;
 }
 
-bool overlap(const Buf& a, const Buf& b) {
+inline bool overlap(const Buf& a, const Buf& b) {
   if (a.at() >= b.at() + b.bytes() || b.at() >= a.at() + a.bytes()) return false;
   // Whole matrices in turn, or rows, where every matrix starts on the same column.
   if (interleaved(a.at(), a.matrix(), a.stride, a.batch, b.at(), b.matrix(), b.stride, b.batch)) return false;
@@ -120,29 +119,30 @@ gemm_status_t check_bufs(const gemm_ops_s* h, const Buf (&b)[kN]) {
   return GEMM_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 // The kernels' 32-bit counters of rows and columns run past the end of a matrix
 // by less than a tile (256 and 192 columns more), or by the stride of a loop: 256
 // columns, or the rows of one round of CTAs, 8 per SM.
 constexpr int64_t kMaxLength = INT32_MAX - 4095;
-bool dim_ok(int64_t v) { return v >= 0 && v <= kMaxLength; }
-int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-int64_t cdiv(int64_t v, int64_t m) { return (v + m - 1) / m; }
+inline bool dim_ok(int64_t v) { return v >= 0 && v <= kMaxLength; }
+inline int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+inline int64_t cdiv(int64_t v, int64_t m) { return (v + m - 1) / m; }
 
 // ------------------------------------------------------------ tensor maps --
-// A stack of `z` row-major 16-bit matrices of rows x cols, rows `pitch` and
-// matrices `zstride` elements apart.
+// A stack of `z` row-major matrices of rows x cols, rows `pitch` and matrices
+// `zstride` elements apart.
 struct Stack {
   const void* p;
   int64_t rows, cols, pitch, z, zstride;
 };
 
-bool make_map(const gemm_ops_s* h, CUtensorMap* m, const Stack& s, bool bf16, uint32_t box_cols,
-              uint32_t box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+inline bool make_map(const gemm_ops_s* h, CUtensorMap* m, const Stack& s, gemm_dtype_t type, uint32_t box_cols,
+                     uint32_t box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+  const cuuint64_t size = type == GEMM_F32 ? 4 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(s.cols), static_cast<cuuint64_t>(s.rows),
                               static_cast<cuuint64_t>(s.z)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.pitch) * 2,
-                                 static_cast<cuuint64_t>(s.zstride) * 2};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.pitch) * size,
+                                 static_cast<cuuint64_t>(s.zstride) * size};
   const cuuint32_t box[3] = {box_cols, box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   // Rows whose pitch is not a multiple of 128 bytes straddle L2 lines:
@@ -151,8 +151,11 @@ bool make_map(const gemm_ops_s* h, CUtensorMap* m, const Stack& s, bool bf16, ui
                                                       : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
   auto encode = [&] {
     return reinterpret_cast<EncodeTiledFn>(h->encode)(
-        m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-        const_cast<void*>(s.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+        m,
+        type == GEMM_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+        : type == GEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+        3, const_cast<void*>(s.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
         l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
   // A host thread that has not used CUDA (autograd's, a worker's) has a device but
@@ -203,7 +206,7 @@ struct Product {
   int32_t a_seg[3], b_seg[3];
 };
 
-FusedArgs base_args(const gemm_ops_s* h, const Product& p) {
+inline FusedArgs base_args(const gemm_ops_s* h, const Product& p) {
   FusedArgs a = {};
   a.M = static_cast<int32_t>(p.M);
   a.N = static_cast<int32_t>(p.N);
@@ -229,7 +232,7 @@ FusedArgs base_args(const gemm_ops_s* h, const Product& p) {
 
 template <class Cfg>
 gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const Stack& c,
-                           const Stack& d, cudaStream_t stream) {
+                           const Stack& d, cudaStream_t stream, int64_t* shares = nullptr) {
   CUtensorMap ma, mb, mc, md;
   const uint32_t b_rows = Cfg::kGlu && Cfg::kCtas == 1 ? Cfg::kBN / 2 : Cfg::kBRows;
   // Fewer rows than a tile: a box of those alone, and more k-blocks in flight.
@@ -241,12 +244,14 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
       Cfg::kCtas == 1 && !p.a_mn ? static_cast<uint32_t>(std::min<int64_t>(Cfg::kBM, up(p.M, 8))) : Cfg::kBM;
   a.a_tx = a_rows * Cfg::kBK * 2;
   a.stages = std::min<int32_t>(Cfg::kMaxStages, Cfg::kStages * (Cfg::kABytes + Cfg::kBBytes) / (a.a_tx + Cfg::kBBytes));
-  bool ok = make_map(h, &ma, p.a, p.bf16, 64, p.a_mn ? 64 : a_rows) &&
-            make_map(h, &mb, p.b, p.bf16, 64, p.b_mn ? 64 : b_rows);
-  if (ok && c.p) ok = make_map(h, &mc, c, p.bf16, 64, 32);
+  const gemm_dtype_t type = p.bf16 ? GEMM_BF16 : GEMM_F16;
+  bool ok = make_map(h, &ma, p.a, type, 64, p.a_mn ? 64 : a_rows) &&
+            make_map(h, &mb, p.b, type, 64, p.b_mn ? 64 : b_rows);
+  if (ok && c.p)
+    ok = Cfg::kEpi == kEpiSum ? make_map(h, &mc, c, GEMM_F32, 32, 32) : make_map(h, &mc, c, type, 64, 32);
   if (ok && d.p)
-    ok = Cfg::kSym ? make_map(h, &md, d, p.bf16, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE)
-                   : make_map(h, &md, d, p.bf16, 64, 32);
+    ok = Cfg::kSym ? make_map(h, &md, d, type, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE)
+                   : make_map(h, &md, d, type, 64, 32);
   if (!ok) return GEMM_ERR_CUDA;
   if (!c.p) mc = ma;  // not used by this epilogue
   if (!d.p) md = ma;
@@ -264,6 +269,7 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
   a.ldd = d.pitch;
   a.d_up = d.zstride;
   a.d = static_cast<uint16_t*>(const_cast<void*>(d.p));
+  if (shares) *shares = tn * Cfg::kSplit * 2;  // kEpiLse: two groups of a tile's warps, or halves of a CTA's columns
   const int64_t fit = Cfg::kCtas == 2 ? h->max_pairs : h->num_sms;
   const int64_t units = Cfg::kSplit > 1 ? items : std::min<int64_t>(items, fit);
   return launch(h, fused_kernel<Cfg>, dim3(static_cast<unsigned>(units * Cfg::kCluster)), dim3(Cfg::kThreads),
@@ -281,8 +287,10 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
 // k-ranges is fixed, and the batch's tiles decide who sums them.
 template <int kEpi>
 gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const Stack& c,
-                    const Stack& d, cudaStream_t stream) {
+                    const Stack& d, cudaStream_t stream, int64_t* shares = nullptr) {
   constexpr bool kBatched = kEpi == kEpiSplit || kEpi == kEpiSplitSym;
+  // The loss's products: sums to add up are large, and the others' columns belong to lone CTAs.
+  constexpr bool kTwos = kEpi != kEpiSum && kEpi != kEpiLse && kEpi != kEpiXent, kSplits = kEpi != kEpiSum;
   auto tiles = [&](int64_t tm, int64_t tn) { return Pair<kEpi>::kSym ? tn * (tn + 1) / 2 : tm * tn; };
   const int64_t n = kBatched ? 1 : p.batch, kb = cdiv(p.K, 64) * p.segs;
   const int64_t small = tiles(cdiv(p.M, 128), cdiv(p.N, Lone<kEpi>::kOutN)) * n;
@@ -292,28 +300,45 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
   constexpr int64_t kNever = INT64_MAX;
   const int64_t cost[kForms] = {
       h->max_pairs > 0 ? cdiv(big, h->max_pairs) * (33 * kb + 500) : kNever,
-      h->max_twos > 0 && kb >= 4 ? cdiv(big, h->max_twos) * (33 * cdiv(kb, 2) + 700) : kNever,
+      kTwos && h->max_twos > 0 && kb >= 4 ? cdiv(big, h->max_twos) * (33 * cdiv(kb, 2) + 700) : kNever,
       cdiv(small, h->num_sms) * (27 * kb + 400),
-      small <= most[1] && kb >= 4 ? 27 * cdiv(kb, 2) + 550 : kNever,
-      small <= most[2] && kb >= (kBatched ? 4 : 8) ? 27 * cdiv(kb, 4) + 550 : kNever,
-      !kBatched && small <= std::min(8, most[3]) && kb >= 16 ? 27 * cdiv(kb, 8) + 550 : kNever};
+      kSplits && small <= most[1] && kb >= 4 ? 27 * cdiv(kb, 2) + 550 : kNever,
+      kSplits && small <= most[2] && kb >= (kBatched ? 4 : 8) ? 27 * cdiv(kb, 4) + 550 : kNever,
+      kSplits && !kBatched && small <= std::min(8, most[3]) && kb >= 16 ? 27 * cdiv(kb, 8) + 550 : kNever};
   switch (static_cast<int>(std::min_element(cost, cost + kForms) - cost)) {
-    case kPairs: return launch_fused<Pair<kEpi>>(h, p, a, c, d, stream);
-    case kPairs2: return launch_fused<TwoPairs<kEpi>>(h, p, a, c, d, stream);
+    case kPairs: return launch_fused<Pair<kEpi>>(h, p, a, c, d, stream, shares);
+    case kPairs2:
+      if constexpr (kTwos) return launch_fused<TwoPairs<kEpi>>(h, p, a, c, d, stream, shares);
+      break;
     case kLone2:
       if constexpr (kBatched)
-        if (small * p.batch > most[1]) return launch_fused<Lone<kEpi, 1, 2>>(h, p, a, c, d, stream);
-      return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream);
+        if (small * p.batch > most[1]) return launch_fused<Lone<kEpi, 1, 2>>(h, p, a, c, d, stream, shares);
+      if constexpr (kSplits) return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream, shares);
+      break;
     case kLone4:
       if constexpr (kBatched)
-        if (small * p.batch > most[2]) return launch_fused<Lone<kEpi, 1, 4>>(h, p, a, c, d, stream);
-      return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream);
+        if (small * p.batch > most[2]) return launch_fused<Lone<kEpi, 1, 4>>(h, p, a, c, d, stream, shares);
+      if constexpr (kSplits) return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream, shares);
+      break;
     case kLone8:
-      if constexpr (!kBatched) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream);
-      [[fallthrough]];
-    default: return launch_fused<Lone<kEpi>>(h, p, a, c, d, stream);
+      if constexpr (kSplits && !kBatched) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream, shares);
+      break;
+    default: break;
   }
+  return launch_fused<Lone<kEpi>>(h, p, a, c, d, stream, shares);
 }
+
+// out = alpha A B^T, rounded to 16 bits (alpha: on the device, null for 1).  `early`:
+// operands that may be loaded while the previous kernel ends.  A kernel of the
+// operators lets the next one start only after it has waited for the one before
+// it, so what is complete by then are the caller's tensors, and what the last
+// kernel but one wrote.
+enum { kEarlyA = 1, kEarlyB = 2 };
+gemm_status_t product(gemm_ops_s* h, const Product& p, const Stack& out, int early, cudaStream_t stream,
+                      const float* alpha = nullptr);
+
+// Attributes of the loss's kernels, and how many of their clusters fit.
+bool xent_setup(gemm_ops_s* h);
 
 template <class Cfg>
 bool set_attr() {
@@ -342,9 +367,10 @@ int max_clusters() {
   return n;
 }
 
-gemm_status_t check_ld(int64_t ld, int64_t cols) {
+inline gemm_status_t check_ld(int64_t ld, int64_t cols) {
   if (ld < cols || ld >= (1ll << 30)) return GEMM_ERR_INVALID_ARG;
   return ld % 8 != 0 ? GEMM_ERR_ALIGNMENT : GEMM_OK;
 }
 
-}  // namespace
+}  // namespace ops
+}  // namespace gb300

@@ -4,6 +4,20 @@
 #include "ortho_kernels.cuh"
 #include "stream_kernel.cuh"
 
+namespace gb300 {
+namespace ops {
+
+gemm_status_t product(gemm_ops_s* h, const Product& p, const Stack& out, int early, cudaStream_t stream,
+                      const float* alpha) {
+  FusedArgs a = base_args(h, p);
+  a.early = early;
+  a.alpha_p = alpha;
+  return fused<kEpiStore>(h, p, a, out, {}, stream);
+}
+
+}  // namespace ops
+}  // namespace gb300
+
 namespace {
 
 using namespace gb300::ops;
@@ -13,17 +27,6 @@ using namespace gb300::ops;
 // us, 2048 x 5632 22.1 and 25.3 us, 4096 x 8192 46.3 and 41.7 us, 8192 x 16384
 // 145 and 133 us.
 constexpr int64_t kMaxStreamTokens = 16;
-
-// out = A B^T, rounded to 16 bits.  `early`: operands that may be loaded while
-// the previous kernel ends.  A kernel of this file lets the next one start only
-// after it has waited for the one before it, so what is complete by then are
-// the caller's tensors, and what the last kernel but one wrote.
-enum { kEarlyA = 1, kEarlyB = 2 };
-gemm_status_t product(gemm_ops_s* h, const Product& p, const Stack& out, int early, cudaStream_t stream) {
-  FusedArgs a = base_args(h, p);
-  a.early = early;
-  return fused<kEpiStore>(h, p, a, out, {}, stream);
-}
 
 // How a product of few tokens is laid out: warps per CTA, CTAs per k-slice,
 // k-slices, and the CTA's shared memory.
@@ -277,6 +280,10 @@ gemm_status_t gemm_ops_create(gemm_ops_t* out, int device) {
   h->max_split[1] = max_clusters<Lone<kEpiStore, 2>>();
   h->max_split[2] = max_clusters<Lone<kEpiStore, 4>>();
   h->max_split[3] = max_clusters<Lone<kEpiStore, 8>>();
+  if (!xent_setup(h)) {
+    delete h;
+    return GEMM_ERR_CUDA;
+  }
   if (cudaMalloc(&h->d_err, sizeof(h->last_err)) != cudaSuccess) {
     delete h;
     return GEMM_ERR_OOM;

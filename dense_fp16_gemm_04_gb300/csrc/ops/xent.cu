@@ -1,0 +1,214 @@
+// xent.cu -- host side of the vocabulary's loss and its gradients.
+#include "host.cuh"
+#include "xent_kernels.cuh"
+
+namespace gb300 {
+namespace ops {
+
+bool xent_setup(gemm_ops_s* h) {
+  if (!set_attr<Pair<kEpiLse>>() || !set_attr<Pair<kEpiXent>>() || !set_attr<Pair<kEpiSum>>() ||
+      !set_attr<Lone<kEpiLse>>() || !set_attr<Lone<kEpiXent>>() || !set_attr<Lone<kEpiSum>>() ||
+      !set_attr<Lone<kEpiLse, 2>>() || !set_attr<Lone<kEpiXent, 2>>() || !set_attr<Lone<kEpiLse, 4>>() ||
+      !set_attr<Lone<kEpiXent, 4>>() || !set_attr<Lone<kEpiLse, 8>>() || !set_attr<Lone<kEpiXent, 8>>())
+    return false;
+  h->max_pairs = std::min({h->max_pairs, max_clusters<Pair<kEpiLse>>(), max_clusters<Pair<kEpiXent>>(),
+                           max_clusters<Pair<kEpiSum>>()});
+  return true;
+}
+
+}  // namespace ops
+}  // namespace gb300
+
+namespace {
+
+using namespace gb300::ops;
+
+// Tokens of one launch of the forward pass: bounds the shares' memory.
+constexpr int64_t kLseTokens = 16384;
+// Bytes of dz held at a time, where pieces of kMinPiece columns allow it.
+constexpr int64_t kPieceBytes = 512ll << 20, kMinPiece = 4096;
+constexpr int64_t kMaxVocab = 1 << 28;
+
+bool xent_dims_ok(int64_t T, int64_t D, int64_t V) {
+  return dim_ok(T) && dim_ok(D) && D > 0 && V > 0 && V <= kMaxVocab;
+}
+
+gemm_status_t check_xent(const gemm_ops_s* h, int64_t T, int64_t D, int64_t V, gemm_dtype_t dtype) {
+  if (!h || !xent_dims_ok(T, D, V)) return GEMM_ERR_INVALID_ARG;
+  if (dtype != GEMM_F16 && dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;
+  return D % 8 != 0 ? GEMM_ERR_ALIGNMENT : GEMM_OK;
+}
+
+// The most shares that any form leaves: two of a tile of 128 or 256 columns, or
+// sixteen of one of at most 76 tiles that a cluster shares.
+int64_t most_shares(int64_t V) { return std::max<int64_t>(2 * cdiv(V, 128), std::min<int64_t>(16 * cdiv(V, 128), 16 * 76)); }
+
+size_t target_bytes(int64_t T) { return up(std::min(T, kLseTokens) * 4, 256); }
+
+// Columns of a piece of the vocabulary: as few equal pieces as fit.
+int64_t piece_columns(int64_t T, int64_t V) {
+  const int64_t most = std::max(kMinPiece, kPieceBytes / (2 * T) / 256 * 256);
+  return V <= most ? V : up(cdiv(V, cdiv(V, most)), 256);
+}
+
+struct XentSpace {
+  int64_t piece, pitch;
+  size_t rows, scale, dz, sum, total;
+};
+XentSpace xent_space(int64_t T, int64_t D, int64_t V) {
+  XentSpace s;
+  s.piece = piece_columns(T, V);
+  s.pitch = up(s.piece, 64);
+  s.rows = 0;
+  s.scale = up(T * static_cast<int64_t>(sizeof(XentRow)), 256);
+  s.dz = s.scale + 256;
+  s.sum = s.dz + up(T * s.pitch * 2, 256);
+  s.total = s.sum + (s.piece < V ? up(T * D * 4, 256) : 0);  // several pieces: fp32 sums of dx
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gemm_linear_cross_entropy_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t V) {
+  if (!h || T <= 0 || !xent_dims_ok(T, D, V)) return 0;
+  return target_bytes(T) + up(most_shares(V) * std::min(T, kLseTokens) * 8, 256);
+}
+
+gemm_status_t gemm_linear_cross_entropy(gemm_ops_t h, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                        const int64_t* targets, float* loss, float* lse, void* workspace,
+                                        size_t workspace_bytes, int64_t T, int64_t D, int64_t V,
+                                        int64_t ignore_index, gemm_dtype_t dtype, void* stream) {
+  gemm_status_t st = check_xent(h, T, D, V, dtype);
+  if (st != GEMM_OK) return st;
+  if (T == 0) return GEMM_OK;
+  for (auto ld : {ldx, ldw})
+    if ((st = check_ld(ld, D)) != GEMM_OK) return st;
+  if (!aligned16(x) || !aligned16(w) || (reinterpret_cast<uintptr_t>(targets) & 7) ||
+      (reinterpret_cast<uintptr_t>(loss) & 3) || (reinterpret_cast<uintptr_t>(lse) & 3) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return GEMM_ERR_ALIGNMENT;
+  const size_t need = gemm_linear_cross_entropy_workspace(h, T, D, V);
+  if (workspace_bytes < need) return GEMM_ERR_INVALID_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  const Buf bufs[] = {{x, T, D * 2, ldx * 2, false},
+                      {w, V, D * 2, ldw * 2, false},
+                      {targets, T, 8, 8, false},
+                      {loss, T, 4, 4, true},
+                      {lse, lse ? T : 0, 4, 4, true},
+                      {workspace, 1, static_cast<int64_t>(need), static_cast<int64_t>(need), true}};
+  if ((st = check_bufs(h, bufs)) != GEMM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* target_z = static_cast<float*>(workspace);
+  float2* shares = reinterpret_cast<float2*>(static_cast<char*>(workspace) + target_bytes(T));
+  for (int64_t t0 = 0; t0 < T; t0 += kLseTokens) {
+    const int64_t n = std::min(kLseTokens, T - t0);
+    const Product p = {n, V, D, {static_cast<const uint16_t*>(x) + t0 * ldx, n, D, ldx, 1, n * ldx},
+                       {w, V, D, ldw, 1, V * ldw}, false, false, dtype == GEMM_BF16, 1, 1};
+    FusedArgs a = base_args(h, p);
+    if (t0 > 0) a.early = kEarlyA | kEarlyB;  // the kernels before wrote neither x nor W
+    a.targets = targets + t0;
+    a.target_z = target_z;
+    a.shares = shares;
+    int64_t num = 0;
+    if ((st = fused<kEpiLse>(h, p, a, {}, {}, s, &num)) != GEMM_OK) return st;
+    XentArgs j = {};
+    j.targets = targets + t0;
+    j.T = n, j.V = V, j.ignore = ignore_index;
+    j.shares = shares, j.num_shares = num, j.target_z = target_z;
+    j.loss = loss + t0, j.lse = lse ? lse + t0 : nullptr;
+    int32_t per = 1;
+    while (per < 32 && per < n) per *= 2;
+    st = launch(h, xent_join, dim3(static_cast<unsigned>(cdiv(n, per))), dim3(kJoinThreads), 0, 1, s, j, per);
+    if (st != GEMM_OK) return st;
+  }
+  return GEMM_OK;
+}
+
+size_t gemm_linear_cross_entropy_backward_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t V) {
+  if (!h || T <= 0 || !xent_dims_ok(T, D, V)) return 0;
+  return xent_space(T, D, V).total;
+}
+
+gemm_status_t gemm_linear_cross_entropy_backward(gemm_ops_t h, const float* dloss, int64_t dloss_stride,
+                                                 const float* dlse, int64_t dlse_stride, const void* x, int64_t ldx,
+                                                 const void* w, int64_t ldw, const int64_t* targets, const float* lse,
+                                                 void* dx, int64_t lddx, void* dw, void* workspace,
+                                                 size_t workspace_bytes, int64_t T, int64_t D, int64_t V,
+                                                 int64_t ignore_index, gemm_dtype_t dtype, void* stream) {
+  gemm_status_t st = check_xent(h, T, D, V, dtype);
+  if (st != GEMM_OK) return st;
+  if (dloss_stride < 0 || dlse_stride < 0 || dloss_stride >= (1ll << 30) || dlse_stride >= (1ll << 30))
+    return GEMM_ERR_INVALID_ARG;
+  for (auto ld : {ldx, ldw, lddx})
+    if ((st = check_ld(ld, D)) != GEMM_OK) return st;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(dx) || !aligned16(dw) || (reinterpret_cast<uintptr_t>(targets) & 7) ||
+      (reinterpret_cast<uintptr_t>(dloss) & 3) || (reinterpret_cast<uintptr_t>(dlse) & 3) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3) || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return GEMM_ERR_ALIGNMENT;
+  const size_t need = gemm_linear_cross_entropy_backward_workspace(h, T, D, V);
+  if (workspace_bytes < need) return GEMM_ERR_INVALID_ARG;
+  DeviceGuard g(h->device);
+  if (!g.ok) return GEMM_ERR_CUDA;
+  const Buf bufs[] = {{dloss, T, 4, dloss_stride * 4, false},
+                      {dlse, dlse ? T : 0, 4, dlse_stride * 4, false},
+                      {x, T, D * 2, ldx * 2, false},
+                      {w, V, D * 2, ldw * 2, false},
+                      {targets, T, 8, 8, false},
+                      {lse, T, 4, 4, false},
+                      {dx, T, D * 2, lddx * 2, true},
+                      {dw, V, D * 2, D * 2, true},
+                      {workspace, need ? 1 : 0, static_cast<int64_t>(need), static_cast<int64_t>(need), true}};
+  if ((st = check_bufs(h, bufs)) != GEMM_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0)  // no token, no gradient
+    return cudaMemsetAsync(dw, 0, V * D * 2, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  const bool bf16 = dtype == GEMM_BF16;
+  const XentSpace sp = xent_space(T, D, V);
+  char* ws = static_cast<char*>(workspace);
+  XentArgs r = {};
+  r.targets = targets;
+  r.T = T, r.V = V, r.ignore = ignore_index, r.D = D;
+  r.lse = const_cast<float*>(lse);
+  r.dloss = dloss, r.dlse = dlse, r.dloss_stride = dloss_stride, r.dlse_stride = dlse_stride;
+  r.rows = reinterpret_cast<XentRow*>(ws + sp.rows);
+  r.scale = reinterpret_cast<float*>(ws + sp.scale);
+  r.hold = bf16 ? 1.0f : 16384.0f;
+  if ((st = launch(h, xent_rows, dim3(1), dim3(1024), 0, 1, s, r)) != GEMM_OK) return st;
+  void* dz = ws + sp.dz;
+  float* sum = reinterpret_cast<float*>(ws + sp.sum);
+  const bool whole = sp.piece >= V;
+  const Stack xs = {x, T, D, ldx, 1, T * ldx};
+  for (int64_t v0 = 0; v0 < V; v0 += sp.piece) {
+    const int64_t n = std::min(sp.piece, V - v0);
+    const Stack ws_ = {static_cast<const uint16_t*>(w) + v0 * ldw, n, D, ldw, 1, n * ldw};
+    const Stack dzs = {dz, T, n, sp.pitch, 1, T * sp.pitch};
+    {  // dz, from the logits x W^T
+      const Product p = {T, n, D, xs, ws_, false, false, bf16, 1, 1};
+      FusedArgs a = base_args(h, p);
+      a.early = kEarlyA | kEarlyB;  // the kernels before wrote neither x nor W
+      a.xent_rows = r.rows;
+      a.col_base = static_cast<int32_t>(v0);
+      if ((st = fused<kEpiXent>(h, p, a, dzs, {}, s)) != GEMM_OK) return st;
+    }
+    // dW = dz^T x, whole for this piece
+    const Product pw = {n, D, T, dzs, xs, true, true, bf16, 1, 1};
+    const Stack out = {static_cast<uint16_t*>(dw) + v0 * D, n, D, D, 1, n * D};
+    if ((st = product(h, pw, out, kEarlyB, s, r.scale)) != GEMM_OK) return st;
+    // dx = dz W, or its sum over the pieces
+    const Product px = {T, D, n, dzs, ws_, false, true, bf16, 1, 1};
+    if (whole) return product(h, px, {dx, T, D, lddx, 1, T * lddx}, kEarlyA | kEarlyB, s, r.scale);
+    FusedArgs a = base_args(h, px);
+    a.early = kEarlyA | kEarlyB;
+    a.add = v0 > 0;
+    if ((st = fused<kEpiSum>(h, px, a, {sum, T, D, D, 1, T * D}, {}, s)) != GEMM_OK) return st;
+  }
+  r.sum = sum;
+  r.dx = dx, r.lddx = lddx, r.bf16 = bf16;
+  const int64_t blocks = std::min<int64_t>(cdiv(T * (D / 8), 256), 8 * h->num_sms);
+  return launch(h, xent_dx, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, s, r);
+}
+
+}  // extern "C"

@@ -1,0 +1,145 @@
+// xent_kernels.cuh -- the ends of the vocabulary's loss, around the products of
+// fused_kernel.cuh.  For a token with logits z = x W^T
+//
+//   lse = log sum exp z,  loss = lse - z[target]   (0 where the token is ignored)
+//   dz = (dloss + dlse) exp(z - lse) - dloss [column = target]
+//   dx = dz W,  dW = dz^T x
+//
+// Forward: the product's epilogue leaves for each token and each share of a tile's
+// columns a maximum m and s = sum exp(z - m), and the target's logit; xent_join
+// joins the shares,  (m1, s1) + (m2, s2) = (M, s1 exp(m1 - M) + s2 exp(m2 - M)),
+// M = max(m1, m2).  Where m is infinite, s stands for sum exp(z) itself.
+//
+// Backward: the logits come again, and dz, a piece of the vocabulary at a time, is
+// rounded to 16 bits as an operand of the two products.  In fp16 dz of a mean over
+// thousands of tokens would be lost below 6e-8, so dz is held times 2^14 / 2^e, 2^e
+// the power of two above the largest |dloss| and |dloss + dlse|: at most 2^15, and
+// exact to 2^-40 of the largest.  The products undo it in fp32.
+#pragma once
+#include "fused_kernel.cuh"
+
+namespace gb300 {
+namespace ops {
+
+struct XentArgs {
+  const int64_t* targets;
+  int64_t T, V, ignore;
+  // Forward: the shares [shares][T] and the targets' logits.
+  const float2* shares;
+  int64_t num_shares;
+  const float* target_z;
+  float *loss, *lse;  // forward: lse may be null; backward: lse is read
+  // Backward.
+  const float *dloss, *dlse;  // dlse may be null
+  int64_t dloss_stride, dlse_stride;
+  XentRow* rows;
+  float* scale;  // what the products are to be multiplied by
+  float hold;    // dz is held times hold / 2^e
+  // The sums of dx, [T][D], and dx itself.
+  const float* sum;
+  void* dx;
+  int64_t lddx, D;
+  int32_t bf16;
+};
+
+__device__ __forceinline__ float2 lse_join(float2 a, float2 b) {
+  const float top = fmaxf(a.x, b.x), ref = isinf(top) ? 0.0f : top;
+  return make_float2(top, fmaf(a.y, ptx::ex2((a.x - ref) * kLog2e), b.y * ptx::ex2((b.x - ref) * kLog2e)));
+}
+
+constexpr int kJoinThreads = 512;
+
+// A block joins the shares of `per` tokens (a power of two up to 32), thread p per
+// + t every (512 / per)-th share of token t from p on; then in pairs.
+__global__ void __launch_bounds__(kJoinThreads) xent_join(const XentArgs a, int32_t per) {
+  __shared__ float2 sm[kJoinThreads];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int groups = kJoinThreads / per, at = threadIdx.x % per, group = threadIdx.x / per;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * per + at;
+  float2 v = make_float2(-INFINITY, 0.0f);
+  if (t < a.T)
+    for (int64_t i = group; i < a.num_shares; i += groups) v = lse_join(v, a.shares[i * a.T + t]);
+  sm[threadIdx.x] = v;
+  for (int n = groups / 2; n > 0; n /= 2) {
+    __syncthreads();
+    if (group < n) sm[threadIdx.x] = lse_join(sm[threadIdx.x], sm[threadIdx.x + n * per]);
+  }
+  if (group == 0 && t < a.T) {
+    v = sm[at];
+    const float lse = (isinf(v.x) ? 0.0f : v.x) + logf(v.y);
+    const int64_t target = a.targets[t];
+    // A target outside the vocabulary has no logit: NaN.
+    float loss = 0.0f;
+    if (target != a.ignore) loss = target >= 0 && target < a.V ? lse - a.target_z[t] : NAN;
+    a.loss[t] = loss;
+    if (a.lse) a.lse[t] = lse;
+  }
+}
+
+// One block: the power of two above the largest finite |dloss| and |dloss + dlse|
+// of the tokens, then every token's row.
+__global__ void __launch_bounds__(1024) xent_rows(const XentArgs a) {
+  __shared__ float sm[32];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  // a, b and the target of token t.
+  auto row = [&](int64_t t) {
+    const int64_t target = a.targets[t];
+    XentRow r;
+    r.b = target != a.ignore ? a.dloss[t * a.dloss_stride] : 0.0f;
+    r.a = a.dlse ? r.b + a.dlse[t * a.dlse_stride] : r.b;
+    r.target = -1;
+    if (target != a.ignore) {
+      if (target >= 0 && target < a.V)
+        r.target = static_cast<int32_t>(target);
+      else
+        r.a = NAN;  // as the loss
+    }
+    r.lse2 = a.lse[t] * kLog2e;
+    return r;
+  };
+  float top = 0.0f;
+  for (int64_t t = threadIdx.x; t < a.T; t += blockDim.x) {
+    const XentRow r = row(t);
+    if (isfinite(r.a)) top = fmaxf(top, fabsf(r.a));
+    if (isfinite(r.b)) top = fmaxf(top, fabsf(r.b));
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = top;
+  __syncthreads();
+  top = sm[threadIdx.x & 31];
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  int e = 0;
+  if (top > 0.0f) frexpf(top, &e);
+  e = max(-100, min(100, e));  // both factors stay normal
+  const float up = ldexpf(a.hold, -e);
+  for (int64_t t = threadIdx.x; t < a.T; t += blockDim.x) {
+    XentRow r = row(t);
+    r.a *= up;
+    r.b *= up;
+    a.rows[t] = r;
+  }
+  if (threadIdx.x == 0) *a.scale = ldexpf(1.0f / a.hold, e);
+}
+
+// dx = scale sum, rounded: eight columns a thread (D is a multiple of 8).
+__global__ void __launch_bounds__(256) xent_dx(const XentArgs a) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const float scale = *a.scale;
+  const int64_t per = a.D / 8, n = a.T * per, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
+    const int64_t t = i / per, c = (i - t * per) * 8;
+    const float4 u = ptx::ld_global_cg_v4(a.sum + t * a.D + c), v = ptx::ld_global_cg_v4(a.sum + t * a.D + c + 4);
+    const bool bf16 = a.bf16 != 0;
+    ptx::st_global_v4(static_cast<uint16_t*>(a.dx) + t * a.lddx + c, pack16(bf16, u.x * scale, u.y * scale),
+                      pack16(bf16, u.z * scale, u.w * scale), pack16(bf16, v.x * scale, v.y * scale),
+                      pack16(bf16, v.z * scale, v.w * scale));
+  }
+}
+
+}  // namespace ops
+}  // namespace gb300

@@ -1,6 +1,6 @@
 """Operators beside the GEMM: the gated feed-forward block, its backward pass,
-its products from 4-bit weights, the orthogonalised update of its matrices, and
-layer and RMS norm with their gradients.
+its products from 4-bit weights, the orthogonalised update of its matrices, layer
+and RMS norm and the loss over a vocabulary, with their gradients.
 
 Thin bindings over the C ABI in ``include/gemm_ops.h``: through the compiled
 ``_binding`` (a call for one token costs the host more than the GPU), and
@@ -16,7 +16,7 @@ The operators record no graph.  A tensor that requires grad (while gradients are
 recorded) or has a forward-mode tangent is refused with a RuntimeError: call them
 under ``torch.no_grad()`` or on detached tensors, or from the methods of a
 ``torch.autograd.Function``, whose backward is :func:`gated_ffn_backward` (or
-the norm's).
+its sisters).
 
     >>> import torch, dense_fp16_gemm_04_gb300 as g
     >>> x = torch.randn(4096, 1024, device="cuda", dtype=torch.float16)
@@ -39,7 +39,7 @@ from . import GemmError, _build, _check, load as _load
 
 __all__ = ["Ops", "default_ops", "gated_ffn", "gated_ffn_backward", "w4_linear", "w4_gated",
            "w4_quantize", "orthogonalize", "NEWTON_SCHULZ", "layer_norm", "layer_norm_backward",
-           "rms_norm", "rms_norm_backward"]
+           "rms_norm", "rms_norm_backward", "linear_cross_entropy", "linear_cross_entropy_backward"]
 
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
@@ -106,7 +106,9 @@ def _load_binding():
             fns = ("gemm_gated_ffn_workspace", "gemm_gated_ffn", "gemm_gated_ffn_backward_workspace",
                    "gemm_gated_ffn_backward", "gemm_w4_workspace", "gemm_w4_linear", "gemm_w4_gated",
                    "gemm_layer_norm", "gemm_rms_norm", "gemm_norm_backward_workspace",
-                   "gemm_layer_norm_backward", "gemm_rms_norm_backward")
+                   "gemm_layer_norm_backward", "gemm_rms_norm_backward",
+                   "gemm_linear_cross_entropy_workspace", "gemm_linear_cross_entropy",
+                   "gemm_linear_cross_entropy_backward_workspace", "gemm_linear_cross_entropy_backward")
             mod.setup(GemmError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in fns))
             _binding = mod
     return _binding
@@ -182,6 +184,14 @@ class Ops:
 
     def rms_norm_backward(self, dy, x, weight, stats, stream=None):
         return self._b.rms_norm_backward(self._addr, self.index, dy, x, weight, stats, False, stream)
+
+    # -- the loss over a vocabulary -------------------------------------------
+    def linear_cross_entropy(self, x, w, targets, ignore_index=-100, save=False, out=None, stream=None):
+        return self._b.linear_cross_entropy(self._addr, self.index, x, w, targets, ignore_index, save, out, stream)
+
+    def linear_cross_entropy_backward(self, dloss, x, w, targets, lse, ignore_index=-100, dlse=None, stream=None):
+        return self._b.linear_cross_entropy_backward(self._addr, self.index, dloss, x, w, targets, lse, ignore_index,
+                                                     dlse, stream)
 
     # -- the orthogonalised update -------------------------------------------
     def orthogonalize(self, m, steps=5, coeffs=NEWTON_SCHULZ, eps=1e-7, dtype=None, out=None, stream=None):
@@ -350,3 +360,23 @@ def rms_norm_backward(dy, x, weight, stats, stream=None, ops: Ops | None = None)
     """Gradients (dx, dweight) of :func:`rms_norm` from dy [T, D]; dweight is None
     where weight is."""
     return _of(x, ops).rms_norm_backward(dy, x, weight, stats, stream)
+
+
+def linear_cross_entropy(x, w, targets, ignore_index=-100, save=False, out=None, stream=None,
+                         ops: Ops | None = None):
+    """The loss of each token over a vocabulary, from logits z = x w^T that are never
+    stored:  loss = lse - z[target],  lse = log sum exp z.
+
+    x [T, D], w [V, D], float16 or bfloat16, D a multiple of 8; targets [T] int64.
+    Returns loss [T] float32, 0 where the target is ``ignore_index`` and NaN where it
+    is outside the vocabulary, and with ``save`` also lse [T] float32 (of every token),
+    that :func:`linear_cross_entropy_backward` takes.  Minus the loss is the target's
+    log-probability."""
+    return _of(x, ops).linear_cross_entropy(x, w, targets, ignore_index, save, out, stream)
+
+
+def linear_cross_entropy_backward(dloss, x, w, targets, lse, ignore_index=-100, dlse=None, stream=None,
+                                  ops: Ops | None = None):
+    """Gradients (dx, dw) of :func:`linear_cross_entropy` from dloss [T] float32 (an
+    expanded scalar will do) and, where the lse was used too, dlse [T]."""
+    return _of(x, ops).linear_cross_entropy_backward(dloss, x, w, targets, lse, ignore_index, dlse, stream)

@@ -1,8 +1,8 @@
 /*
  * gemm_ops.h -- C ABI of the operators beside the GEMM of gemm.h: the gated
  * feed-forward block of a language model, its backward pass, its products
- * from 4-bit weights, the orthogonalised update of its matrices, and layer and
- * RMS norm with their gradients.
+ * from 4-bit weights, the orthogonalised update of its matrices, layer and RMS
+ * norm and the loss over a vocabulary, with their gradients.
  *
  * Types: GEMM_F16 or GEMM_BF16 for every 16-bit tensor of a call; sums run in
  * fp32.  Matrices are row-major; ld* is the distance between rows in elements
@@ -209,6 +209,48 @@ GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_ops_t ops, const void* dy, in
                                               int64_t lddx, void* dweight, void* workspace, size_t workspace_bytes,
                                               int64_t T, int64_t D, gemm_dtype_t dtype, gemm_dtype_t wtype,
                                               void* stream);
+
+/* The loss of T tokens over a vocabulary of V, without keeping their logits z = x W^T:
+ *
+ *     lse = log sum over v of exp(z[v]),  loss = lse - z[target]
+ *
+ *   x       : [T, D];  w : [V, D], one row per entry of the vocabulary
+ *   targets : [T] int64, contiguous: an entry, or ignore_index (any value) for a token
+ *             without a loss (0); any other target outside 0 .. V - 1 gives NaN
+ *   loss    : [T] fp32;  lse : [T] fp32, or NULL (the lse of every token, ignored ones too)
+ * D is a positive multiple of 8, x and w 16-byte aligned, their row distances multiples
+ * of 8 (GEMM_ERR_ALIGNMENT otherwise); V is 1 to 2^28; T == 0: nothing to do.  Logits
+ * and sums are fp32.  Infinities and NaN go where the formula puts them: an infinite
+ * logit gives an infinite lse.
+ * workspace: gemm_linear_cross_entropy_workspace(ops, T, D, V) bytes, 256-byte aligned. */
+GEMM_API size_t gemm_linear_cross_entropy_workspace(gemm_ops_t ops, int64_t T, int64_t D, int64_t V);
+GEMM_API gemm_status_t gemm_linear_cross_entropy(gemm_ops_t ops, const void* x, int64_t ldx, const void* w,
+                                                 int64_t ldw, const int64_t* targets, float* loss, float* lse,
+                                                 void* workspace, size_t workspace_bytes, int64_t T, int64_t D,
+                                                 int64_t V, int64_t ignore_index, gemm_dtype_t dtype, void* stream);
+
+/* Its gradients, given those of loss and lse and the lse that the forward pass kept:
+ *
+ *     dz = (dloss + dlse) exp(z - lse) - dloss [v = target]     (dloss of an ignored token: 0)
+ *     dx = dz W,  dw = dz^T x
+ *
+ *   dloss, dlse : [T] fp32, elements a stride apart (0: one for all); dlse may be NULL
+ *   lse         : [T] fp32, contiguous
+ *   dx : [T, D];  dw : [V, D], contiguous
+ * The logits are computed again, a piece of the vocabulary at a time.  dz is rounded to
+ * 16 bits as an operand, in fp16 scaled by a power of two so that entries down to 2^-40
+ * of the largest |dloss| (|dloss + dlse|) of the call count.  A token whose dloss and
+ * dlse are 0 (or which is ignored, without dlse) has dz = 0 and dx = 0.
+ * Gradients are written, not accumulated; T == 0 gives zero dw.  Rules as above.
+ * workspace: gemm_linear_cross_entropy_backward_workspace(ops, T, D, V) bytes, 256-byte
+ * aligned (up to about 512 MB of dz, from 2^16 tokens on 4096 columns of it, and fp32
+ * sums of dx). */
+GEMM_API size_t gemm_linear_cross_entropy_backward_workspace(gemm_ops_t ops, int64_t T, int64_t D, int64_t V);
+GEMM_API gemm_status_t gemm_linear_cross_entropy_backward(
+    gemm_ops_t ops, const float* dloss, int64_t dloss_stride, const float* dlse, int64_t dlse_stride, const void* x,
+    int64_t ldx, const void* w, int64_t ldw, const int64_t* targets, const float* lse, void* dx, int64_t lddx, void* dw,
+    void* workspace, size_t workspace_bytes, int64_t T, int64_t D, int64_t V, int64_t ignore_index, gemm_dtype_t dtype,
+    void* stream);
 
 #ifdef __cplusplus
 }
