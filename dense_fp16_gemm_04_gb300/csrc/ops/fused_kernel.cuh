@@ -173,6 +173,12 @@ struct FusedCfg {
   static constexpr int kEpiBufs = kEpiBufs_;  // 32 x 64 staging buffers per epilogue warp
   static constexpr bool kGlu = kEpi == kEpiGlu;
   static constexpr bool kSym = kEpi == kEpiSplitSym;
+  // The logits of the loss: sums of at most kPartKb k-blocks, added up in registers
+  // (of a split cluster: in kParts accumulators, added up as they are sent).  The
+  // tensor cores truncate a sum at each of its K / 16 steps, always towards zero:
+  // the loss of one token over 4096 products was off by 9e-6 of itself, of which
+  // 16 steps at a time leave 5e-7 (4096 tokens x 4096 x 131072: 2545 -> 2577 us).
+  static constexpr bool kPartial = kEpi == kEpiLse;
   static constexpr bool kReads = kEpi == kEpiGluBwd || kEpi == kEpiSplit || kSym;  // the epilogue reads too
   static constexpr int kOutN = kGlu ? kBN / 2 : kBN;  // output columns per tile
   static constexpr int kBM = 128, kBK = 64;
@@ -208,13 +214,23 @@ struct FusedCfg {
   static_assert(kOutN % 64 == 0, "the epilogue works on 64-column chunks");
   static_assert(!kSym || kTileM == kBN, "symmetric tiles are square");
   static_assert(kTmemCols <= 512, "TMEM columns");
-  static_assert(kParts == 1 || (kSplit == 1 && (kEpi == kEpiSplit || kEpi == kEpiSplitSym)), "parts");
+  static_assert(kParts == 1 || (kSplit == 1 && (kEpi == kEpiSplit || kEpi == kEpiSplitSym)) ||
+                    (kSplit > 1 && kPartial),
+                "parts");
   // The partials a split CTA receives (a lone one its own among them): 128 rows
   // x 128 columns in all, in the staging buffers' place.
   static_assert(kSplit == 1 || kEpiWarps * kEpiBufs * kBufBytes >= kBM * 128 * 4, "partials");
   static_assert(kSplit == 1 || (kCtas == 1 && kBN == 128) || (kCtas == 2 && kBN == 256 && kSplit == 2),
                 "split clusters: lone CTAs on 128 x 128 tiles, two pairs on 256 x 256 ones");
 };
+
+constexpr int kPartKb = 4;
+
+// Cfg::kPartial: k-blocks of a partial sum, of a k-range of n.
+template <class Cfg>
+__device__ __forceinline__ int32_t part_length(int32_t n) {
+  return Cfg::kSplit > 1 ? max(kPartKb, (n + Cfg::kParts - 1) / Cfg::kParts) : kPartKb;
+}
 
 // One tile, and a CTA's k-range of it.
 struct FusedItem {
@@ -415,6 +431,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   ptx::griddep_wait();  // reads S, g and u; writes the outputs
   ptx::griddep_launch_dependents();
+  const FusedItem wi = fused_item<Cfg>(args, unit, rank);
   bool ok = wait_bar_warp<false>(tfull, 0u, w, kSiteTmemFull, unit);
   if (ok) {
     // Send: warp quarter q owns 32 rows, warps 0-3 columns 0-63, warps 4-7 the
@@ -429,6 +446,16 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
       uint32_t v[16];
       ptx::tmem_ld_32x32b_x16(t_row + g * 16, v);
       ptx::tmem_wait_ld(v);
+      if constexpr (Cfg::kParts > 1) {
+        const int32_t n = wi.kb1 - wi.kb0, length = part_length<Cfg>(n);
+        for (int32_t q = 1; q * length < n; ++q) {
+          uint32_t u[16];
+          ptx::tmem_ld_32x32b_x16(t_row + q * Cfg::kBN + g * 16, u);
+          ptx::tmem_wait_ld(u);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = g * 16 + j * 4;  // of this side's 64
@@ -449,7 +476,6 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
   // reads comes in while the partials do.
   constexpr int kN = Cfg::kGlu ? kHalfCols / 2 : kCols / 2;
   const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
-  const FusedItem wi = fused_item<Cfg>(args, unit, rank);
   const int32_t row = wi.mb * Cfg::kBM + r;
   const int32_t col0 = wi.nb * Cfg::kOutN + rank * (Cfg::kOutN / kS) + half * kN;
   const bool in = row < args.M && (col0 < args.N || Cfg::kEpi == kEpiLse);  // (every share is written)
@@ -713,54 +739,59 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       bool ok = true;
       for (int32_t it = unit; ok && it < args.items; it += units) {
         const FusedItem wi = fused_item<Cfg>(args, it, rank);
-        const int buf = acc_iter % Cfg::kAccBufs;
-        const uint32_t use_par = static_cast<uint32_t>((acc_iter / Cfg::kAccBufs) & 1);
-        if (!wait_bar_warp<kPair>(bar_tempty(buf), use_par ^ 1u, w, kSiteTmemEmpty, it)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * Cfg::kBN);
-        int32_t first = wi.kb0, part = 0;  // first k-block of the current accumulator
-        for (int32_t kb = wi.kb0; kb < wi.kb1; ++kb) {
-          if (Cfg::kParts > 1 && kb == (part + 1) * wi.kb1 / Cfg::kParts) {
-            ++part;
-            first = kb;
-            d_tmem += Cfg::kBN;
-          }
-          if (!wait_bar_warp<kPair>(bar_full(stage), phase, w, kSiteFull, it)) {
+        int32_t kb = wi.kb0;
+        do {  // once, or for each partial sum
+          const int32_t end = Cfg::kPartial && Cfg::kSplit == 1 ? min(wi.kb1, kb + kPartKb) : wi.kb1;
+          const int buf = acc_iter % Cfg::kAccBufs;
+          const uint32_t use_par = static_cast<uint32_t>((acc_iter / Cfg::kAccBufs) & 1);
+          if (!wait_bar_warp<kPair>(bar_tempty(buf), use_par ^ 1u, w, kSiteTmemEmpty, it)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint64_t a_desc = a_desc0 + a_desc_stage * static_cast<uint32_t>(stage);
-          const uint64_t b_desc = b_desc0 + kBDescStage * static_cast<uint32_t>(stage);
-          const uint32_t acc_first = kb != first ? 1u : 0u;
-          if (ptx::elect_one()) {
+          uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * Cfg::kBN);
+          int32_t first = kb, part = 0;  // first k-block of the current accumulator
+          for (; kb < end; ++kb) {
+            if (Cfg::kParts > 1 &&
+                kb == (Cfg::kPartial ? first + part_length<Cfg>(wi.kb1 - wi.kb0) : (part + 1) * wi.kb1 / Cfg::kParts)) {
+              ++part;
+              first = kb;
+              d_tmem += Cfg::kBN;
+            }
+            if (!wait_bar_warp<kPair>(bar_full(stage), phase, w, kSiteFull, it)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            const uint64_t a_desc = a_desc0 + a_desc_stage * static_cast<uint32_t>(stage);
+            const uint64_t b_desc = b_desc0 + kBDescStage * static_cast<uint32_t>(stage);
+            const uint32_t acc_first = kb != first ? 1u : 0u;
+            if (ptx::elect_one()) {
 #pragma unroll
-            for (int k = 0; k < Cfg::kBK / 16; ++k)
-              ptx::mma_f16<Cfg::kCtas>(d_tmem, a_desc + a_kstep * k, b_desc + b_kstep * k, idesc,
-                                       k != 0 ? 1u : acc_first);
+              for (int k = 0; k < Cfg::kBK / 16; ++k)
+                ptx::mma_f16<Cfg::kCtas>(d_tmem, a_desc + a_kstep * k, b_desc + b_kstep * k, idesc,
+                                         k != 0 ? 1u : acc_first);
+              if constexpr (kPair)
+                ptx::mma_commit_pair(bar_empty(stage), pair_mask);
+              else
+                ptx::mma_commit(bar_empty(stage));
+            }
+            __syncwarp();
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          if (ptx::elect_one()) {
             if constexpr (kPair)
-              ptx::mma_commit_pair(bar_empty(stage), pair_mask);
+              ptx::mma_commit_pair(bar_tfull(buf), pair_mask);
             else
-              ptx::mma_commit(bar_empty(stage));
+              ptx::mma_commit(bar_tfull(buf));
           }
           __syncwarp();
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        if (!ok) break;
-        if (ptx::elect_one()) {
-          if constexpr (kPair)
-            ptx::mma_commit_pair(bar_tfull(buf), pair_mask);
-          else
-            ptx::mma_commit(bar_tfull(buf));
-        }
-        __syncwarp();
-        ++acc_iter;
+          ++acc_iter;
+        } while (kb < wi.kb1);
       }
       // Every MMA has finished before tensor memory is freed.
       if (ptx::elect_one()) {
@@ -836,6 +867,64 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         ptx::bulk_commit_group();
       }
     };
+    if constexpr (Cfg::kPartial) {
+      // Each warp for itself: 32 rows, and this group's half of the tile's columns.
+      constexpr int kCols = Cfg::kOutN / Cfg::kGroups;
+      bool ok = true;
+      for (int32_t it = unit; ok && it < args.items; it += units) {
+        const FusedItem wi = fused_item<Cfg>(args, it, rank);
+        const int32_t row = wi.mb * Cfg::kTileM + static_cast<int32_t>(cta) * Cfg::kBM + q * 32 + lane;
+        const int32_t col0 = wi.nb * Cfg::kOutN + group * kCols;
+        const bool row_in = row < args.M;
+        const int64_t target = row_in ? args.targets[row] - col0 : -1;
+        float z[kCols];
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) z[i] = 0.0f;
+        for (int32_t kb = wi.kb0; kb < wi.kb1; kb += kPartKb) {
+          const int buf = acc_iter % Cfg::kAccBufs;
+          const uint32_t use_par = static_cast<uint32_t>((acc_iter / Cfg::kAccBufs) & 1);
+          ++acc_iter;
+          ok = wait_bar_warp<kPair>(bar_tfull(buf), use_par, w, kSiteTmemFull, it);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                 static_cast<uint32_t>(buf * Cfg::kBN + group * kCols);
+#pragma unroll
+          for (int c = 0; c < kCols; c += 16) {
+            uint32_t v[16];
+            ptx::tmem_ld_32x32b_x16(t_row + c, v);
+            ptx::tmem_wait_ld(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[c + i] += __uint_as_float(v[i]);
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (kPair)
+              ptx::mbar_arrive_cluster(tempty_bar0 + 8u * buf);
+            else
+              ptx::mbar_arrive(tempty_bar0 + 8u * buf);
+          }
+        }
+        if (!ok) break;
+        // No lane's target is among these columns but for a few tiles of a row.
+        const bool here = target >= 0 && target < kCols && target < args.N - col0;
+        if (__any_sync(0xffffffffu, here)) {
+#pragma unroll
+          for (int i = 0; i < kCols; ++i)
+            if (here && target == i) args.target_z[row] = z[i];
+        }
+        if (col0 + kCols > args.N) {
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) z[i] = col0 + i < args.N ? z[i] : -INFINITY;
+        }
+        float share_m = -INFINITY, share_s = 0.0f;
+        lse_take<kCols>(z, share_m, share_s);
+        if (row_in)
+          args.shares[(static_cast<int64_t>(wi.nb) * Cfg::kGroups + group) * args.M + row] =
+              make_float2(share_m, share_s);
+      }
+    } else
     for (int32_t it = unit;; it += units) {
       // Every warp takes the same decision, so none is left at a barrier.
       if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, it < args.items)) break;
@@ -886,13 +975,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         }
       };
       constexpr int kChunks = Cfg::kOutN / 64;
-      static_assert(Cfg::kEpi != kEpiLse || kChunks >= Cfg::kGroups, "every warp has a share");
       if (group >= kChunks) release_tmem();
-      // The share of this tile: kEpiLse.
-      float share_m = -INFINITY, share_s = 0.0f;
-      int64_t target = -1;
-      if constexpr (Cfg::kEpi == kEpiLse)
-        if (row_in) target = args.targets[row];
       XentRow xr = {};
       if constexpr (Cfg::kEpi == kEpiXent)
         if (row_in) xr = args.xent_rows[row];
@@ -914,33 +997,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             packed[16 + i] = pack16(bf16, alpha * __uint_as_float(v1[2 * i]), alpha * __uint_as_float(v1[2 * i + 1]));
           }
           store_chunk(&tmC, packed, col0, row0, wi.batch * args.c_zb, in);
-        } else if constexpr (Cfg::kEpi == kEpiLse) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t v[32];
-            float z[32];
-            ptx::tmem_ld_32x32b_x32(t_row + c * 64 + half * 32, v);
-            ptx::tmem_wait_ld(v);
-            if (half == 1 && last) release_tmem();
-            const int32_t first = col0 + half * 32;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(v[i]);
-            // (target - first) is out of range for no target and for one past the vocabulary.
-            const int64_t at = target < args.N ? target - first : -1;
-            if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (at == i) args.target_z[row] = z[i];
-            }
-            if (first + 32 > args.N) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) z[i] = first + i < args.N ? z[i] : -INFINITY;
-            }
-            lse_take<32>(z, share_m, share_s);
-          }
-          if (last && row_in)
-            args.shares[(static_cast<int64_t>(wi.nb) * Cfg::kGroups + group) * args.M + row] =
-                make_float2(share_m, share_s);
         } else if constexpr (Cfg::kEpi == kEpiXent) {
           uint32_t packed[32];
 #pragma unroll

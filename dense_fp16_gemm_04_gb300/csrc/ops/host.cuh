@@ -49,7 +49,7 @@ using Pair = FusedCfg<2, 256, kEpi == kEpiStore ? 6 : 5, kEpi, kEpi == kEpiStore
 template <int kEpi>
 using TwoPairs = FusedCfg<2, 256, 5, kEpi, epi_bufs(kEpi), 2>;  // one tile, half of its k-blocks each
 template <int kEpi, int kSplit = 1, int kParts = 1>
-using Lone = FusedCfg<1, 128, 5, kEpi, epi_bufs(kEpi), kSplit, kParts>;
+using Lone = FusedCfg<1, 128, 5, kEpi, epi_bufs(kEpi), kSplit, kEpi == kEpiLse && (kSplit > 1) ? 4 : kParts>;
 
 struct DeviceGuard {
   int prev = -1;
