@@ -30,6 +30,41 @@ gemm_status_t check_rows(const void* p, int64_t ld, int64_t D, int64_t e) {
   return reinterpret_cast<uintptr_t>(p) % e ? GEMM_ERR_ALIGNMENT : GEMM_OK;
 }
 
+// Whether rows of D elements of e bytes may be read 16 bytes at a time.
+bool vectors(int64_t D, int64_t e, std::initializer_list<std::pair<const void*, int64_t>> rows) {
+  bool ok = D * e % 16 == 0;
+  for (auto [p, ld] : rows) ok = ok && aligned16(p) && ld * e % 16 == 0;
+  return ok;
+}
+
+// Blocks of a kernel that fit on the device at once.
+template <class K>
+int64_t resident(const gemm_ops_s* h, K kernel, int threads, size_t smem) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess) {
+    cudaGetLastError();
+    n = 1;
+  }
+  return static_cast<int64_t>(std::max(1, n)) * h->num_sms;
+}
+
+template <int kV>
+using Int = std::integral_constant<int, kV>;
+
+// f(team, vectors a thread, teams) for rows of n vectors: the smallest team that
+// holds one, false for none.
+template <int kMostPer, class F>
+bool with_team(int64_t n, F f) {
+  if (n <= 32) return f(Int<32>(), Int<1>(), Int<8>());
+  if (n <= 64) return f(Int<32>(), Int<2>(), Int<8>());
+  if (n <= 32 * kMostPer) return f(Int<32>(), Int<kMostPer>(), Int<8>());
+  if (n <= 128 * kMostPer) return f(Int<128>(), Int<kMostPer>(), Int<2>());
+  if (n <= 256 * kMostPer) return f(Int<256>(), Int<kMostPer>(), Int<1>());
+  if (n <= 512 * kMostPer) return f(Int<512>(), Int<kMostPer>(), Int<1>());
+  if (n <= 1024 * kMostPer) return f(Int<1024>(), Int<kMostPer>(), Int<1>());
+  return false;
+}
+
 unsigned row_threads(int64_t D) { return static_cast<unsigned>(std::min<int64_t>(512, up(D, 32))); }
 
 template <bool kRms>
@@ -55,16 +90,40 @@ gemm_status_t norm(gemm_ops_s* h, const void* x, int64_t ldx, const void* weight
   a.x = x, a.weight = weight, a.bias = bias, a.y = y, a.stats = stats;
   a.ldx = ldx, a.ldy = ldy, a.T = T, a.D = D, a.eps = eps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool vec = vectors(D, e, {{x, ldx}, {y, ldy}}) && aligned16(weight) && aligned16(bias);
   return with_types(dtype, wtype, [&](auto tx, auto tw) {
-    return launch(h, norm_any<decltype(tx), decltype(tw), kRms>, dim3(static_cast<unsigned>(T)), dim3(row_threads(D)), 0,
-                  1, s, a);
+    typedef decltype(tx) X;
+    typedef decltype(tw) W;
+    gemm_status_t st = GEMM_OK;
+    auto rows = [&](auto vec, auto team, auto per, auto teams) {
+      auto kernel = norm_rows<X, W, kRms, vec, team, per, teams>;
+      static const int64_t fit = resident(h, kernel, team * teams, 0);
+      const int64_t blocks = std::min(cdiv(T, teams), fit);
+      st = launch(h, kernel, dim3(static_cast<unsigned>(blocks)), dim3(team * teams), 0, 1, s, a);
+      return true;
+    };
+    constexpr int kVec = 16 / sizeof(X);
+    if (vec && with_team<4>(D / kVec, [&](auto... v) { return rows(Int<kVec>(), v...); })) return st;
+    if (!vec && with_team<8>(D, [&](auto... v) { return rows(Int<1>(), v...); })) return st;
+    return launch(h, norm_any<X, W, kRms>, dim3(static_cast<unsigned>(T)), dim3(row_threads(D)), 0, 1, s, a);
   });
 }
 
-// Chunks of rows whose sums are taken apart: enough blocks of 32 columns for the
-// device, of at least 32 rows.
+// Chunks of rows whose sums are taken apart by norm_dw_any: enough blocks of 32
+// columns for the device, of at least 32 rows.
 int64_t row_chunks(const gemm_ops_s* h, int64_t T, int64_t D) {
   return std::max<int64_t>(1, std::min(cdiv(T, 32), cdiv(8 * h->num_sms, cdiv(D, 32))));
+}
+
+// Blocks of norm_rows_back, of `teams` teams: four to an SM (kBackThreads threads
+// in all), each with a few rows for its one row of sums.
+constexpr int kBackThreads = 512;
+int64_t back_blocks(const gemm_ops_s* h, int64_t T, int team, int teams) {
+  return std::max<int64_t>(1, std::min<int64_t>(cdiv(T, 2 * teams), h->num_sms * std::max(1, kBackThreads / (team * teams))));
+}
+// The most of either.
+int64_t most_chunks(const gemm_ops_s* h, int64_t T, int64_t D) {
+  return std::max(row_chunks(h, T, D), std::min<int64_t>(cdiv(T, 2), 2 * h->num_sms));
 }
 
 template <bool kRms>
@@ -104,15 +163,30 @@ gemm_status_t norm_backward(gemm_ops_s* h, const void* dy, int64_t lddy, const v
   a.partial = static_cast<float*>(workspace);
   a.chunks = row_chunks(h, T, D);
   a.dweight = dweight, a.dbias = dbias;
+  const bool vec = vectors(D, e, {{x, ldx}, {dy, lddy}, {dx, lddx}}) && aligned16(weight);
   return with_types(dtype, wtype, [&](auto tx, auto tw) {
     typedef decltype(tx) X;
     typedef decltype(tw) W;
-    gemm_status_t st = launch(h, norm_dx_any<X, W, kRms>, dim3(static_cast<unsigned>(T)), dim3(row_threads(D)), 0, 1, s, a);
-    if (st != GEMM_OK || (!dweight && !dbias)) return st;
-    st = launch(h, norm_dw_any<X, kRms>, dim3(static_cast<unsigned>(cdiv(D, 32)), static_cast<unsigned>(a.chunks)),
-                dim3(256), 0, 1, s, a);
-    if (st != GEMM_OK) return st;
-    return launch(h, norm_dw_sum<W>, dim3(static_cast<unsigned>(cdiv(D, 256)), 2), dim3(256), 0, 1, s, a);
+    const bool sums = dweight || dbias;
+    gemm_status_t st = GEMM_OK;
+    if (!sums) a.partial = nullptr;
+    auto rows = [&](auto vec, auto team, auto per, auto teams) {
+      a.chunks = back_blocks(h, T, team, teams);
+      const size_t smem = teams > 1 ? 2 * D * sizeof(float) : 0;
+      st = launch(h, norm_rows_back<X, W, kRms, vec, team, per, teams>, dim3(static_cast<unsigned>(a.chunks)),
+                  dim3(team * teams), smem, 1, s, a);
+      return true;
+    };
+    constexpr int kVec = 16 / sizeof(X), kPer = 16 / kVec;
+    if (!(vec && with_team<kPer>(D / kVec, [&](auto... v) { return rows(Int<kVec>(), v...); })) &&
+        !(!vec && with_team<8>(D, [&](auto... v) { return rows(Int<1>(), v...); }))) {
+      st = launch(h, norm_dx_any<X, W, kRms>, dim3(static_cast<unsigned>(T)), dim3(row_threads(D)), 0, 1, s, a);
+      if (st == GEMM_OK && sums)
+        st = launch(h, norm_dw_any<X, kRms>, dim3(static_cast<unsigned>(cdiv(D, 32)), static_cast<unsigned>(a.chunks)),
+                    dim3(256), 0, 1, s, a);
+    }
+    if (st != GEMM_OK || !sums) return st;
+    return launch(h, norm_dw_sum<W>, dim3(static_cast<unsigned>(cdiv(D, 32)), 2), dim3(512), 0, 1, s, a);
   });
 }
 
@@ -134,7 +208,7 @@ gemm_status_t gemm_rms_norm(gemm_ops_t h, const void* x, int64_t ldx, const void
 
 size_t gemm_norm_backward_workspace(gemm_ops_t h, int64_t T, int64_t D) {
   if (!h || T <= 0 || D <= 0 || !dim_ok(T) || !dim_ok(D)) return 0;
-  return row_chunks(h, T, D) * 2 * D * sizeof(float);
+  return most_chunks(h, T, D) * 2 * D * sizeof(float);
 }
 
 gemm_status_t gemm_layer_norm_backward(gemm_ops_t h, const void* dy, int64_t lddy, const void* x, int64_t ldx,

@@ -15,7 +15,9 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
+#include "act.cuh"
 #include "ptx_ops.cuh"
 
 namespace gb300 {
@@ -57,6 +59,276 @@ __device__ __forceinline__ float2 block_sums(float a, float b, float* sm) {
   for (int i = 0; i < warps; ++i) s.x += sm[i], s.y += sm[32 + i];
   __syncthreads();
   return s;
+}
+
+// kN elements of X as they lie in memory: 16 aligned bytes, or one element.
+template <class X, int kN>
+struct Vec {
+  static_assert(kN * sizeof(X) == 16, "16 bytes");
+  uint4 r;
+  // Each row is read once: it need not stay in L1, where the weight does.
+  __device__ void load(const X* p) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+  }
+  __device__ void get(float (&f)[kN]) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(X) == 4) {
+        f[i] = __uint_as_float(w[i]);
+      } else {
+        const float2 v = unpack16(std::is_same<X, __nv_bfloat16>::value, w[i]);
+        f[2 * i] = v.x, f[2 * i + 1] = v.y;
+      }
+    }
+  }
+  static __device__ void store(X* p, const float (&f)[kN]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(X) == 4)
+        w[i] = __float_as_uint(f[i]);
+      else
+        w[i] = pack16(std::is_same<X, __nv_bfloat16>::value, f[2 * i], f[2 * i + 1]);
+    }
+    ptx::st_global_v4(p, w[0], w[1], w[2], w[3]);
+  }
+};
+template <class X>
+struct Vec<X, 1> {
+  X r;
+  __device__ void load(const X* p) { r = *p; }
+  __device__ void get(float (&f)[1]) const { f[0] = widen(r); }
+  static __device__ void store(X* p, const float (&f)[1]) { narrow(f[0], p); }
+};
+
+// kN elements of a weight or bias, which stay in L1.
+template <class W, int kN>
+__device__ __forceinline__ void load_weight(const W* p, float (&f)[kN]) {
+  if constexpr (kN == 1) {
+    f[0] = widen(*p);
+  } else if constexpr (sizeof(W) == 4) {
+#pragma unroll
+    for (int i = 0; i < kN; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + i);
+      f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+    }
+  } else {
+    Vec<W, kN> v;
+    v.r = *reinterpret_cast<const uint4*>(p);
+    v.get(f);
+  }
+}
+
+// Sums of a and b over a team of kTeam threads (a warp, or whole warps), the same in
+// each and in a fixed order.  sm: 2 x 32 float2 of the team, whose halves alternate
+// (turn), so that one barrier between two uses of a half is enough.
+template <int kTeam>
+__device__ __forceinline__ float2 team_sums(float a, float b, float2* sm, int turn, int team) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, d);
+    b += __shfl_xor_sync(0xffffffffu, b, d);
+  }
+  if constexpr (kTeam == 32) return make_float2(a, b);
+  constexpr int kWarps = kTeam / 32;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x % kTeam) >> 5;
+  float2* half = sm + 32 * turn;
+  if (lane == 0) half[warp] = make_float2(a, b);
+  ptx::named_barrier_sync(1 + team, kTeam);
+  const float2 v = lane < kWarps ? half[lane] : make_float2(0.0f, 0.0f);
+  a = v.x, b = v.y;
+#pragma unroll
+  for (int d = kWarps / 2; d >= 1; d >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, d);
+    b += __shfl_xor_sync(0xffffffffu, b, d);
+  }
+  return make_float2(__shfl_sync(0xffffffffu, a, 0), __shfl_sync(0xffffffffu, b, 0));
+}
+
+// A team of kTeam threads holds a row in registers, kPer vectors of kVec elements a
+// thread, and loads its next row before it works on this one.
+template <class X, class W, bool kRms, int kVec, int kTeam, int kPer, int kTeams>
+__global__ void __launch_bounds__(kTeam* kTeams) norm_rows(const NormArgs a) {
+  __shared__ float2 sm[kTeam > 32 ? kTeams * 64 : 1];
+  const int team = threadIdx.x / kTeam, at = threadIdx.x % kTeam;
+  const int32_t D = static_cast<int32_t>(a.D);
+  const X* x = static_cast<const X*>(a.x);
+  const W *w = static_cast<const W*>(a.weight), *b = static_cast<const W*>(a.bias);
+  const float n = static_cast<float>(D);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + team;
+  Vec<X, kVec> v[kPer], next[kPer];
+  auto column = [&](int i) { return (i * kTeam + at) * kVec; };
+  auto load = [&](Vec<X, kVec>(&d)[kPer], int64_t row) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (column(i) < D) d[i].load(x + row * a.ldx + column(i));
+  };
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  if (t < a.T) load(next, t);
+  for (int turn = 0; t < a.T; t += step) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = next[i];
+    if (t + step < a.T) load(next, t + step);
+    float f[kVec];
+    float m1 = 0.0f, s1 = 0.0f, s2 = 0.0f;
+    if constexpr (!kRms) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (column(i) < D) {
+          v[i].get(f);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) s1 += f[j];
+        }
+      m1 = team_sums<kTeam>(s1, 0.0f, sm + team * 64, turn, team).x / n;
+      turn ^= 1;
+      s1 = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (column(i) < D) {
+        v[i].get(f);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const float d = f[j] - m1;
+          s1 += d;
+          s2 = fmaf(d, d, s2);
+        }
+      }
+    const float2 s = team_sums<kTeam>(s1, s2, sm + team * 64, turn, team);
+    turn ^= 1;
+    const float c = kRms ? 0.0f : s.x / n;
+    const float var = s.y / n - c * c;
+    const float r = __frsqrt_rn((var < 0.0f ? 0.0f : var) + a.eps);  // (fmaxf would lose a NaN)
+    X* y = static_cast<X*>(a.y) + t * a.ldy;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int col = column(i);
+      if (col >= D) continue;
+      float g[kVec];
+      v[i].get(f);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) f[j] = ((f[j] - m1) - c) * r;
+      if (w) {
+        load_weight<W, kVec>(w + col, g);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) f[j] *= g[j];
+      }
+      if (!kRms && b) {
+        load_weight<W, kVec>(b + col, g);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) f[j] += g[j];
+      }
+      Vec<X, kVec>::store(y + col, f);
+    }
+    if (a.stats && at == 0) {
+      if (kRms) {
+        a.stats[t] = r;
+      } else {
+        a.stats[2 * t] = m1 + c;
+        a.stats[2 * t + 1] = r;
+      }
+    }
+  }
+}
+
+// The gradients: teams as above.  A thread's columns are the same in every row, so
+// that it keeps their sums of dy h and dy in registers; at the end a block adds up its
+// teams' in order, and leaves one row of `partial`.
+template <class X, class W, bool kRms, int kVec, int kTeam, int kPer, int kTeams>
+__global__ void __launch_bounds__(kTeam* kTeams) norm_rows_back(const NormArgs a) {
+  extern __shared__ float sums[];  // [2][D], where kTeams > 1
+  __shared__ float2 sm[kTeam > 32 ? kTeams * 64 : 1];
+  const int team = threadIdx.x / kTeam, at = threadIdx.x % kTeam;
+  const int32_t D = static_cast<int32_t>(a.D);
+  const X *x = static_cast<const X*>(a.x), *dy = static_cast<const X*>(a.dy);
+  const W* w = static_cast<const W*>(a.weight);
+  const float n = static_cast<float>(D);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + team;
+  Vec<X, kVec> xv[kPer], gv[kPer], xn[kPer], gn[kPer];
+  float m = 0.0f, r = 0.0f, mn = 0.0f, rn = 0.0f;
+  float sw[kPer][kVec] = {}, sb[kRms ? 1 : kPer][kVec] = {};
+  auto column = [&](int i) { return (i * kTeam + at) * kVec; };
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (column(i) < D) {
+        xn[i].load(x + row * a.ldx + column(i));
+        gn[i].load(dy + row * a.lddy + column(i));
+      }
+    if (!kRms) mn = a.stats[2 * row];
+    rn = a.stats[kRms ? row : 2 * row + 1];
+  };
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  if (t < a.T) load(t);
+  for (int turn = 0; t < a.T; t += step, turn ^= 1) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) xv[i] = xn[i], gv[i] = gn[i];
+    m = mn, r = rn;
+    if (t + step < a.T) load(t + step);
+    float f[kVec], g[kVec], q[kVec], s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (column(i) < D) {
+        xv[i].get(f);
+        gv[i].get(g);
+        if (w) load_weight<W, kVec>(w + column(i), q);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const float h = (f[j] - m) * r;
+          const float qj = w ? g[j] * q[j] : g[j];
+          s1 += qj;
+          s2 = fmaf(qj, h, s2);
+          sw[i][j] = fmaf(g[j], h, sw[i][j]);
+          if (!kRms) sb[i][j] += g[j];
+        }
+      }
+    const float2 s = team_sums<kTeam>(s1, s2, sm + team * 64, turn, team);
+    const float c1 = kRms ? 0.0f : s.x / n, c2 = s.y / n;
+    X* dx = static_cast<X*>(a.y) + t * a.ldy;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (column(i) < D) {
+        xv[i].get(f);
+        gv[i].get(g);
+        if (w) load_weight<W, kVec>(w + column(i), q);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const float h = (f[j] - m) * r;
+          const float qj = w ? g[j] * q[j] : g[j];
+          f[j] = r * ((qj - c1) - h * c2);
+        }
+        Vec<X, kVec>::store(dx + column(i), f);
+      }
+  }
+  if (!a.partial) return;
+  float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * D;
+#pragma unroll 1
+  for (int k = 0; k < kTeams; ++k) {
+    if (team == k) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int col = column(i);
+        if (col >= D) continue;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          float vw = sw[i][j], vb = kRms ? 0.0f : sb[kRms ? 0 : i][j];
+          if (k > 0) vw += sums[col + j], vb += sums[D + col + j];
+          float* to = k + 1 < kTeams ? sums : out;
+          to[col + j] = vw;
+          if (!kRms) to[D + col + j] = vb;
+        }
+      }
+    }
+    if (kTeams > 1) __syncthreads();
+  }
 }
 
 // One block per row, element by element: rows of any length, start and distance.
@@ -156,17 +428,29 @@ __global__ void __launch_bounds__(256) norm_dw_any(const NormArgs a) {
   }
 }
 
-// The sums of all chunks, in order: thread (column, weight or bias).
+// The sums of all chunks: 32 columns by 16 groups of chunks, each in order, then the
+// groups in order.  grid (columns / 32, weight or bias).
 template <class W>
-__global__ void __launch_bounds__(256) norm_dw_sum(const NormArgs a) {
+__global__ void __launch_bounds__(512) norm_dw_sum(const NormArgs a) {
+  __shared__ float sm[16][32];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   W* out = static_cast<W*>(blockIdx.y == 0 ? a.dweight : a.dbias);
-  if (col >= a.D || !out) return;
+  if (!out) return;
   float s = 0.0f;
-  for (int64_t c = 0; c < a.chunks; ++c) s += a.partial[(2 * c + blockIdx.y) * a.D + col];
-  narrow(s, out + col);
+  if (col < a.D) {
+#pragma unroll 8
+    for (int64_t c = group; c < a.chunks; c += 16) s += a.partial[(2 * c + blockIdx.y) * a.D + col];
+  }
+  sm[group][lane] = s;
+  __syncthreads();
+  if (group == 0 && col < a.D) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s += sm[i][lane];
+    narrow(s, out + col);
+  }
 }
 
 }  // namespace ops
