@@ -118,6 +118,7 @@ int64_t row_chunks(const gemm_ops_s* h, int64_t T, int64_t D) {
 // Blocks of norm_rows_back, of `teams` teams: four to an SM (kBackThreads threads
 // in all), each with a few rows for its one row of sums.
 constexpr int kBackThreads = 512;
+constexpr int kBackSmem = 200 * 1024;
 int64_t back_blocks(const gemm_ops_s* h, int64_t T, int team, int teams) {
   return std::max<int64_t>(1, std::min<int64_t>(cdiv(T, 2 * teams), h->num_sms * std::max(1, kBackThreads / (team * teams))));
 }
@@ -172,12 +173,15 @@ gemm_status_t norm_backward(gemm_ops_s* h, const void* dy, int64_t lddy, const v
     if (!sums) a.partial = nullptr;
     auto rows = [&](auto vec, auto team, auto per, auto teams) {
       a.chunks = back_blocks(h, T, team, teams);
-      const size_t smem = teams > 1 ? 2 * D * sizeof(float) : 0;
-      st = launch(h, norm_rows_back<X, W, kRms, vec, team, per, teams>, dim3(static_cast<unsigned>(a.chunks)),
-                  dim3(team * teams), smem, 1, s, a);
+      const size_t smem = std::max(back_ring<vec, per>(team * teams), teams > 1 ? 2 * D * sizeof(float) : 0);
+      auto kernel = norm_rows_back<X, W, kRms, vec, team, per, teams>;
+      static const bool set =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBackSmem) == cudaSuccess;
+      st = set ? launch(h, kernel, dim3(static_cast<unsigned>(a.chunks)), dim3(team * teams), smem, 1, s, a)
+               : GEMM_ERR_CUDA;
       return true;
     };
-    constexpr int kVec = 16 / sizeof(X), kPer = 16 / kVec;
+    constexpr int kVec = 16 / sizeof(X), kPer = 2;
     if (!(vec && with_team<kPer>(D / kVec, [&](auto... v) { return rows(Int<kVec>(), v...); })) &&
         !(!vec && with_team<8>(D, [&](auto... v) { return rows(Int<1>(), v...); }))) {
       st = launch(h, norm_dx_any<X, W, kRms>, dim3(static_cast<unsigned>(T)), dim3(row_threads(D)), 0, 1, s, a);

@@ -105,6 +105,79 @@ struct Vec<X, 1> {
   static __device__ void store(X* p, const float (&f)[1]) { narrow(f[0], p); }
 };
 
+// a + b, a b and a b + c of two pairs at once: the norms of 16-bit rows are bound by
+// the instructions they issue, of which these save half.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+// The same of kN elements, b and c arrays or one number for all.
+__device__ __forceinline__ float2 pair(const float* p, int j) { return make_float2(p[j], p[j + 1]); }
+__device__ __forceinline__ float2 pair(float v, int) { return make_float2(v, v); }
+__device__ __forceinline__ float single(const float* p) { return p[0]; }
+__device__ __forceinline__ float single(float v) { return v; }
+template <int kN, class B>
+__device__ __forceinline__ void vadd(float (&a)[kN], const B& b) {
+  if constexpr (kN == 1) a[0] += single(b);
+#pragma unroll
+  for (int j = 0; j + 1 < kN; j += 2) {
+    const float2 d = add2(pair(a, j), pair(b, j));
+    a[j] = d.x, a[j + 1] = d.y;
+  }
+}
+template <int kN, class B>
+__device__ __forceinline__ void vmul(float (&a)[kN], const B& b) {
+  if constexpr (kN == 1) a[0] *= single(b);
+#pragma unroll
+  for (int j = 0; j + 1 < kN; j += 2) {
+    const float2 d = mul2(pair(a, j), pair(b, j));
+    a[j] = d.x, a[j + 1] = d.y;
+  }
+}
+// d = a b + c
+template <int kN, class B, class C>
+__device__ __forceinline__ void vfma(float (&d)[kN], const float (&a)[kN], const B& b, const C& c) {
+  if constexpr (kN == 1) d[0] = fmaf(a[0], single(b), single(c));
+#pragma unroll
+  for (int j = 0; j + 1 < kN; j += 2) {
+    const float2 v = fma2(pair(a, j), pair(b, j), pair(c, j));
+    d[j] = v.x, d[j + 1] = v.y;
+  }
+}
+// s += the sum of a, s += the sum of a b
+template <int kN>
+__device__ __forceinline__ void vsum(float2& s, const float (&a)[kN]) {
+  if constexpr (kN == 1) s.x += a[0];
+#pragma unroll
+  for (int j = 0; j + 1 < kN; j += 2) s = add2(s, pair(a, j));
+}
+template <int kN>
+__device__ __forceinline__ void vdot(float2& s, const float (&a)[kN], const float (&b)[kN]) {
+  if constexpr (kN == 1) s.x = fmaf(a[0], b[0], s.x);
+#pragma unroll
+  for (int j = 0; j + 1 < kN; j += 2) s = fma2(pair(a, j), pair(b, j), s);
+}
+
 // kN elements of a weight or bias, which stay in L1.
 template <class W, int kN>
 __device__ __forceinline__ void load_weight(const W* p, float (&f)[kN]) {
@@ -161,46 +234,42 @@ __global__ void __launch_bounds__(kTeam* kTeams) norm_rows(const NormArgs a) {
   const float n = static_cast<float>(D);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + team;
-  Vec<X, kVec> v[kPer], next[kPer];
+  Vec<X, kVec> next[kPer];
   auto column = [&](int i) { return (i * kTeam + at) * kVec; };
-  auto load = [&](Vec<X, kVec>(&d)[kPer], int64_t row) {
+  auto load = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (column(i) < D) d[i].load(x + row * a.ldx + column(i));
+      if (column(i) < D) next[i].load(x + row * a.ldx + column(i));
   };
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  if (t < a.T) load(next, t);
+  if (t < a.T) load(t);
   for (int turn = 0; t < a.T; t += step) {
+    float f[kPer][kVec];
+    float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = next[i];
-    if (t + step < a.T) load(next, t + step);
-    float f[kVec];
-    float m1 = 0.0f, s1 = 0.0f, s2 = 0.0f;
+    for (int i = 0; i < kPer; ++i)
+      if (column(i) < D) {
+        next[i].get(f[i]);
+        if (!kRms) vsum(s1, f[i]);
+      }
+    if (t + step < a.T) load(t + step);
+    float m1 = 0.0f;
     if constexpr (!kRms) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (column(i) < D) {
-          v[i].get(f);
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) s1 += f[j];
-        }
-      m1 = team_sums<kTeam>(s1, 0.0f, sm + team * 64, turn, team).x / n;
+      m1 = team_sums<kTeam>(s1.x + s1.y, 0.0f, sm + team * 64, turn, team).x / n;
       turn ^= 1;
-      s1 = 0.0f;
+      s1 = make_float2(0.0f, 0.0f);
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (column(i) < D) {
-        v[i].get(f);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const float d = f[j] - m1;
-          s1 += d;
-          s2 = fmaf(d, d, s2);
+        if (!kRms) {
+          vadd(f[i], -m1);
+          vsum(s1, f[i]);
         }
+        vdot(s2, f[i], f[i]);
       }
-    const float2 s = team_sums<kTeam>(s1, s2, sm + team * 64, turn, team);
+    const float2 s = team_sums<kTeam>(s1.x + s1.y, s2.x + s2.y, sm + team * 64, turn, team);
     turn ^= 1;
     const float c = kRms ? 0.0f : s.x / n;
     const float var = s.y / n - c * c;
@@ -211,20 +280,24 @@ __global__ void __launch_bounds__(kTeam* kTeams) norm_rows(const NormArgs a) {
       const int col = column(i);
       if (col >= D) continue;
       float g[kVec];
-      v[i].get(f);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) f[j] = ((f[j] - m1) - c) * r;
+      if (kRms)
+        vmul(f[i], r);
+      else
+        vfma(f[i], f[i], r, -c * r);
       if (w) {
         load_weight<W, kVec>(w + col, g);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) f[j] *= g[j];
-      }
-      if (!kRms && b) {
+        if (!kRms && b) {
+          float h[kVec];
+          load_weight<W, kVec>(b + col, h);
+          vfma(f[i], f[i], g, h);
+        } else {
+          vmul(f[i], g);
+        }
+      } else if (!kRms && b) {
         load_weight<W, kVec>(b + col, g);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) f[j] += g[j];
+        vadd(f[i], g);
       }
-      Vec<X, kVec>::store(y + col, f);
+      Vec<X, kVec>::store(y + col, f[i]);
     }
     if (a.stats && at == 0) {
       if (kRms) {
@@ -237,13 +310,32 @@ __global__ void __launch_bounds__(kTeam* kTeams) norm_rows(const NormArgs a) {
   }
 }
 
+// Rows of norm_rows_back on their way: vectors come through shared memory, of which
+// every thread copies and reads its own columns alone (a row ahead in registers keeps
+// 32 KB of an SM's loads in flight, three rows ahead 96 KB); single elements through
+// registers.
+__host__ __device__ constexpr int back_ahead(int threads) { return threads > 512 ? 2 : 3; }
+template <class X, int kVec, int kPer>
+struct BackRow {
+  Vec<X, kVec> x[kPer], g[kPer];
+};
+template <int kVec, int kPer>
+constexpr size_t back_ring(int threads) {
+  return kVec > 1 ? static_cast<size_t>(back_ahead(threads) + 1) * 2 * kPer * threads * 16 : 0;
+}
+
 // The gradients: teams as above.  A thread's columns are the same in every row, so
-// that it keeps their sums of dy h and dy in registers; at the end a block adds up its
-// teams' in order, and leaves one row of `partial`.
+// that it keeps their sums of dy h and dy in registers, and their weights; at the end a
+// block adds up its teams' sums in order, and leaves one row of `partial`.
 template <class X, class W, bool kRms, int kVec, int kTeam, int kPer, int kTeams>
-__global__ void __launch_bounds__(kTeam* kTeams) norm_rows_back(const NormArgs a) {
-  extern __shared__ float sums[];  // [2][D], where kTeams > 1
+__global__ void __launch_bounds__(kTeam* kTeams, 512 / (kTeam * kTeams) > 0 ? 512 / (kTeam * kTeams) : 1)
+    norm_rows_back(const NormArgs a) {
+  extern __shared__ __align__(16) uint8_t ring[];  // the rows on their way; then sums [2][D], where kTeams > 1
   __shared__ float2 sm[kTeam > 32 ? kTeams * 64 : 1];
+  constexpr bool kRing = kVec > 1;
+  constexpr int kThreads = kTeam * kTeams, kBackAhead = back_ahead(kThreads), kSlots = kBackAhead + 1;
+  // A block of 1024 threads has registers for the sums, and reads the row twice.
+  constexpr bool kHold = !kRing || kThreads <= 512;
   const int team = threadIdx.x / kTeam, at = threadIdx.x % kTeam;
   const int32_t D = static_cast<int32_t>(a.D);
   const X *x = static_cast<const X*>(a.x), *dy = static_cast<const X*>(a.dy);
@@ -251,63 +343,113 @@ __global__ void __launch_bounds__(kTeam* kTeams) norm_rows_back(const NormArgs a
   const float n = static_cast<float>(D);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + team;
-  Vec<X, kVec> xv[kPer], gv[kPer], xn[kPer], gn[kPer];
-  float m = 0.0f, r = 0.0f, mn = 0.0f, rn = 0.0f;
-  float sw[kPer][kVec] = {}, sb[kRms ? 1 : kPer][kVec] = {};
+  BackRow<X, kVec, kPer> next;
+  float mn = 0.0f, rn = 0.0f;
+  float sw[kPer][kVec] = {}, sb[kRms ? 1 : kPer][kVec] = {}, wv[kHold ? kPer : 1][kVec];
   auto column = [&](int i) { return (i * kTeam + at) * kVec; };
-  auto load = [&](int64_t row) {
+  // Slot s, vector i of x (which = 0) or dy (1) of this thread.
+  const uint32_t mine = ptx::smem_addr(ring) + threadIdx.x * 16;
+  auto slot = [&](int s, int which, int i) {
+    return mine + static_cast<uint32_t>(((s * 2 + which) * kPer + i) * kThreads) * 16u;
+  };
+  auto fetch = [&](int64_t row, int s) {
+    if (row < a.T) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (column(i) < D) {
-        xn[i].load(x + row * a.ldx + column(i));
-        gn[i].load(dy + row * a.lddy + column(i));
-      }
-    if (!kRms) mn = a.stats[2 * row];
-    rn = a.stats[kRms ? row : 2 * row + 1];
+      for (int i = 0; i < kPer; ++i)
+        if (column(i) < D) {
+          if constexpr (kRing) {
+            ptx::cp_async_16(slot(s, 0, i), x + row * a.ldx + column(i));
+            ptx::cp_async_16(slot(s, 1, i), dy + row * a.lddy + column(i));
+          } else {
+            next.x[i].load(x + row * a.ldx + column(i));
+            next.g[i].load(dy + row * a.lddy + column(i));
+          }
+        }
+    }
+    if constexpr (kRing) ptx::cp_async_commit();
+  };
+  auto stats = [&](int64_t row) {
+    if (row < a.T) {
+      if (!kRms) mn = a.stats[2 * row];
+      rn = a.stats[kRms ? row : 2 * row + 1];
+    }
   };
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  if (t < a.T) load(t);
-  for (int turn = 0; t < a.T; t += step, turn ^= 1) {
+  for (int s = 0; s < (kRing ? kBackAhead : 1); ++s) fetch(t + s * step, s);
+  stats(t);
+  auto weights = [&](int i, float(&v)[kVec]) {
+    if (w && column(i) < D) {
+      load_weight<W, kVec>(w + column(i), v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) xv[i] = xn[i], gv[i] = gn[i];
-    m = mn, r = rn;
-    if (t + step < a.T) load(t + step);
-    float f[kVec], g[kVec], q[kVec], s1 = 0.0f, s2 = 0.0f;
+      for (int j = 0; j < kVec; ++j) v[j] = 1.0f;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < (kHold ? kPer : 0); ++i) weights(i, wv[i]);
+  // h and q of vector i, and dy.
+  auto work_out = [&](int i, float m, float r, float(&h)[kVec], float(&q)[kVec], float(&g)[kVec]) {
+    next.x[i].get(h);
+    next.g[i].get(g);
+    if (!kRms) vadd(h, -m);
+    vmul(h, r);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) q[j] = g[j];
+    if constexpr (!kHold) weights(i, wv[0]);
+    vmul(q, wv[kHold ? i : 0]);
+  };
+  int at_slot = 0;
+  for (int turn = 0; t < a.T; t += step, turn ^= 1) {
+    const float m = mn, r = rn;
+    float h[kHold ? kPer : 1][kVec], q[kHold ? kPer : 1][kVec], g[kVec];
+    const int here = at_slot;
+    float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+    if constexpr (kRing) {
+      ptx::cp_async_wait<kBackAhead - 1>();
+      const int free_slot = at_slot == 0 ? kSlots - 1 : at_slot - 1;  // read in the turn before
+      fetch(t + kBackAhead * step, free_slot);
+      at_slot = at_slot + 1 == kSlots ? 0 : at_slot + 1;
+    }
+    stats(t + step);
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (column(i) < D) {
-        xv[i].get(f);
-        gv[i].get(g);
-        if (w) load_weight<W, kVec>(w + column(i), q);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const float h = (f[j] - m) * r;
-          const float qj = w ? g[j] * q[j] : g[j];
-          s1 += qj;
-          s2 = fmaf(qj, h, s2);
-          sw[i][j] = fmaf(g[j], h, sw[i][j]);
-          if (!kRms) sb[i][j] += g[j];
+        if constexpr (kRing) {
+          next.x[i].r = ptx::ld_shared_v4_u32(slot(here, 0, i));
+          next.g[i].r = ptx::ld_shared_v4_u32(slot(here, 1, i));
         }
+        const int k = kHold ? i : 0;
+        work_out(i, m, r, h[k], q[k], g);
+        vfma(sw[i], g, h[k], sw[i]);
+        if (!kRms) vadd(sb[kRms ? 0 : i], g);
+        if (!kRms) vsum(s1, q[k]);
+        vdot(s2, q[k], h[k]);
       }
-    const float2 s = team_sums<kTeam>(s1, s2, sm + team * 64, turn, team);
+    if constexpr (!kRing) fetch(t + step, 0);
+    const float2 s = team_sums<kTeam>(s1.x + s1.y, s2.x + s2.y, sm + team * 64, turn, team);
     const float c1 = kRms ? 0.0f : s.x / n, c2 = s.y / n;
     X* dx = static_cast<X*>(a.y) + t * a.ldy;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (column(i) < D) {
-        xv[i].get(f);
-        gv[i].get(g);
-        if (w) load_weight<W, kVec>(w + column(i), q);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const float h = (f[j] - m) * r;
-          const float qj = w ? g[j] * q[j] : g[j];
-          f[j] = r * ((qj - c1) - h * c2);
+        const int k = kHold ? i : 0;
+        if constexpr (!kHold) {
+          next.x[i].r = ptx::ld_shared_v4_u32(slot(here, 0, i));
+          next.g[i].r = ptx::ld_shared_v4_u32(slot(here, 1, i));
+          work_out(i, m, r, h[k], q[k], g);
         }
-        Vec<X, kVec>::store(dx + column(i), f);
+        if (!kRms) vadd(q[k], -c1);
+        vfma(q[k], h[k], -c2, q[k]);
+        vmul(q[k], r);
+        Vec<X, kVec>::store(dx + column(i), q[k]);
       }
   }
+  if constexpr (kRing) {
+    ptx::cp_async_wait<0>();
+    if (kTeams > 1) __syncthreads();  // the sums take the ring's place
+  }
+  float* sums = reinterpret_cast<float*>(ring);
   if (!a.partial) return;
   float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * D;
 #pragma unroll 1
