@@ -58,6 +58,7 @@ bool with_team(int64_t n, F f) {
   if (n <= 32) return f(Int<32>(), Int<1>(), Int<8>());
   if (n <= 64) return f(Int<32>(), Int<2>(), Int<8>());
   if (n <= 32 * kMostPer) return f(Int<32>(), Int<kMostPer>(), Int<8>());
+  if (n <= 256) return f(Int<128>(), Int<2>(), Int<2>());
   if (n <= 128 * kMostPer) return f(Int<128>(), Int<kMostPer>(), Int<2>());
   if (n <= 256 * kMostPer) return f(Int<256>(), Int<kMostPer>(), Int<1>());
   if (n <= 512 * kMostPer) return f(Int<512>(), Int<kMostPer>(), Int<1>());
@@ -173,12 +174,17 @@ gemm_status_t norm_backward(gemm_ops_s* h, const void* dy, int64_t lddy, const v
     if (!sums) a.partial = nullptr;
     auto rows = [&](auto vec, auto team, auto per, auto teams) {
       a.chunks = back_blocks(h, T, team, teams);
-      const size_t smem = std::max(back_ring<vec, per>(team * teams), teams > 1 ? 2 * D * sizeof(float) : 0);
-      auto kernel = norm_rows_back<X, W, kRms, vec, team, per, teams>;
-      static const bool set =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBackSmem) == cudaSuccess;
-      st = set ? launch(h, kernel, dim3(static_cast<unsigned>(a.chunks)), dim3(team * teams), smem, 1, s, a)
-               : GEMM_ERR_CUDA;
+      const size_t sums_bytes = teams > 1 ? 2 * D * sizeof(float) : 0;
+      const dim3 grid(static_cast<unsigned>(a.chunks)), block(team * teams);
+      if constexpr (vec == 1) {
+        st = launch(h, norm_rows_back_single<X, W, kRms, team, per, teams>, grid, block, sums_bytes, 1, s, a);
+      } else {
+        auto kernel = norm_rows_back<X, W, kRms, vec, team, per, teams>;
+        static const bool set =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBackSmem) == cudaSuccess;
+        st = set ? launch(h, kernel, grid, block, std::max(back_ring<per>(team * teams), sums_bytes), 1, s, a)
+                 : GEMM_ERR_CUDA;
+      }
       return true;
     };
     constexpr int kVec = 16 / sizeof(X), kPer = 2;

@@ -61,7 +61,61 @@ __device__ __forceinline__ float2 block_sums(float a, float b, float* sm) {
   return s;
 }
 
-// kN elements of X as they lie in memory: 16 aligned bytes, or one element.
+// Two fp32 numbers in a pair of registers, with add, multiply and fused multiply-add
+// of both at once: the norms of 16-bit rows are bound by the instructions they issue,
+// of which these save half.  The same names for one number.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ f32x2 vadd(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 vmul(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 vfma(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float vadd(float a, float b) { return a + b; }
+__device__ __forceinline__ float vmul(float a, float b) { return a * b; }
+__device__ __forceinline__ float vfma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float total(f32x2 v) {
+  const float2 f = unpack2(v);
+  return f.x + f.y;
+}
+__device__ __forceinline__ float total(float v) { return v; }
+
+// kN elements of X: as they lie in memory, 16 aligned bytes or one element (Vec), and
+// as fp32 numbers, in kW pairs or as one (Reg).
+template <int kN>
+struct Reg {
+  typedef f32x2 E;
+  static constexpr int kW = kN / 2;
+  E v[kW];
+  static __device__ E all(float f) { return pack2(f, f); }
+};
+template <>
+struct Reg<1> {
+  typedef float E;
+  static constexpr int kW = 1;
+  E v[1];
+  static __device__ E all(float f) { return f; }
+};
+
 template <class X, int kN>
 struct Vec {
   static_assert(kN * sizeof(X) == 16, "16 bytes");
@@ -73,26 +127,38 @@ struct Vec {
                  : "l"(p)
                  : "memory");
   }
-  __device__ void get(float (&f)[kN]) const {
+  __device__ void get(Reg<kN>& f) const {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    if constexpr (sizeof(X) == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(X) == 4) {
-        f[i] = __uint_as_float(w[i]);
-      } else {
-        const float2 v = unpack16(std::is_same<X, __nv_bfloat16>::value, w[i]);
-        f[2 * i] = v.x, f[2 * i + 1] = v.y;
+      for (int i = 0; i < 2; ++i) f.v[i] = pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<X, __nv_bfloat16>::value) {
+          // bf16 is the upper half of an fp32 (two instructions; the conversion takes three).
+          f.v[i] = pack2(__uint_as_float(__byte_perm(w[i], 0, 0x1044)), __uint_as_float(w[i] & 0xffff0000u));
+        } else {
+          const float2 v = unpack16(false, w[i]);
+          f.v[i] = pack2(v.x, v.y);
+        }
       }
     }
   }
-  static __device__ void store(X* p, const float (&f)[kN]) {
+  static __device__ void store(X* p, const Reg<kN>& f) {
     uint32_t w[4];
+    if constexpr (sizeof(X) == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(X) == 4)
-        w[i] = __float_as_uint(f[i]);
-      else
-        w[i] = pack16(std::is_same<X, __nv_bfloat16>::value, f[2 * i], f[2 * i + 1]);
+      for (int i = 0; i < 2; ++i) {
+        const float2 v = unpack2(f.v[i]);
+        w[2 * i] = __float_as_uint(v.x), w[2 * i + 1] = __float_as_uint(v.y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack2(f.v[i]);
+        w[i] = pack16(std::is_same<X, __nv_bfloat16>::value, v.x, v.y);
+      }
     }
     ptx::st_global_v4(p, w[0], w[1], w[2], w[3]);
   }
@@ -101,93 +167,20 @@ template <class X>
 struct Vec<X, 1> {
   X r;
   __device__ void load(const X* p) { r = *p; }
-  __device__ void get(float (&f)[1]) const { f[0] = widen(r); }
-  static __device__ void store(X* p, const float (&f)[1]) { narrow(f[0], p); }
+  __device__ void get(Reg<1>& f) const { f.v[0] = widen(r); }
+  static __device__ void store(X* p, const Reg<1>& f) { narrow(f.v[0], p); }
 };
-
-// a + b, a b and a b + c of two pairs at once: the norms of 16-bit rows are bound by
-// the instructions they issue, of which these save half.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-// The same of kN elements, b and c arrays or one number for all.
-__device__ __forceinline__ float2 pair(const float* p, int j) { return make_float2(p[j], p[j + 1]); }
-__device__ __forceinline__ float2 pair(float v, int) { return make_float2(v, v); }
-__device__ __forceinline__ float single(const float* p) { return p[0]; }
-__device__ __forceinline__ float single(float v) { return v; }
-template <int kN, class B>
-__device__ __forceinline__ void vadd(float (&a)[kN], const B& b) {
-  if constexpr (kN == 1) a[0] += single(b);
-#pragma unroll
-  for (int j = 0; j + 1 < kN; j += 2) {
-    const float2 d = add2(pair(a, j), pair(b, j));
-    a[j] = d.x, a[j + 1] = d.y;
-  }
-}
-template <int kN, class B>
-__device__ __forceinline__ void vmul(float (&a)[kN], const B& b) {
-  if constexpr (kN == 1) a[0] *= single(b);
-#pragma unroll
-  for (int j = 0; j + 1 < kN; j += 2) {
-    const float2 d = mul2(pair(a, j), pair(b, j));
-    a[j] = d.x, a[j + 1] = d.y;
-  }
-}
-// d = a b + c
-template <int kN, class B, class C>
-__device__ __forceinline__ void vfma(float (&d)[kN], const float (&a)[kN], const B& b, const C& c) {
-  if constexpr (kN == 1) d[0] = fmaf(a[0], single(b), single(c));
-#pragma unroll
-  for (int j = 0; j + 1 < kN; j += 2) {
-    const float2 v = fma2(pair(a, j), pair(b, j), pair(c, j));
-    d[j] = v.x, d[j + 1] = v.y;
-  }
-}
-// s += the sum of a, s += the sum of a b
-template <int kN>
-__device__ __forceinline__ void vsum(float2& s, const float (&a)[kN]) {
-  if constexpr (kN == 1) s.x += a[0];
-#pragma unroll
-  for (int j = 0; j + 1 < kN; j += 2) s = add2(s, pair(a, j));
-}
-template <int kN>
-__device__ __forceinline__ void vdot(float2& s, const float (&a)[kN], const float (&b)[kN]) {
-  if constexpr (kN == 1) s.x = fmaf(a[0], b[0], s.x);
-#pragma unroll
-  for (int j = 0; j + 1 < kN; j += 2) s = fma2(pair(a, j), pair(b, j), s);
-}
 
 // kN elements of a weight or bias, which stay in L1.
 template <class W, int kN>
-__device__ __forceinline__ void load_weight(const W* p, float (&f)[kN]) {
+__device__ __forceinline__ void load_weight(const W* p, Reg<kN>& f) {
   if constexpr (kN == 1) {
-    f[0] = widen(*p);
+    f.v[0] = widen(*p);
   } else if constexpr (sizeof(W) == 4) {
 #pragma unroll
     for (int i = 0; i < kN; i += 4) {
       const float4 v = *reinterpret_cast<const float4*>(p + i);
-      f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+      f.v[i / 2] = pack2(v.x, v.y), f.v[i / 2 + 1] = pack2(v.z, v.w);
     }
   } else {
     Vec<W, kN> v;
@@ -196,37 +189,55 @@ __device__ __forceinline__ void load_weight(const W* p, float (&f)[kN]) {
   }
 }
 
-// Sums of a and b over a team of kTeam threads (a warp, or whole warps), the same in
-// each and in a fixed order.  sm: 2 x 32 float2 of the team, whose halves alternate
-// (turn), so that one barrier between two uses of a half is enough.
+// Sums of two numbers over a team of kTeam threads (a warp, or whole warps), the same
+// in each and in a fixed order: add() by every thread, ready() before get().  sm: 128
+// floats of the team, whose halves are for turns 0 and 1: with one ready() between a
+// half's get() and its next add(), one barrier a turn is enough.
 template <int kTeam>
-__device__ __forceinline__ float2 team_sums(float a, float b, float2* sm, int turn, int team) {
+struct TeamSums {
+  static constexpr int kWarps = kTeam / 32;
+  float *sm, held;  // a warp's own: a in its lower half, b in the upper
+  int team;
+  __device__ TeamSums(float* sm, int team) : sm(sm), held(0.0f), team(team) {}
+  __device__ void add(float2 v, int turn) {
+    const int lane = threadIdx.x & 31;
+    const bool low = lane < 16;
+    float s = low ? v.x : v.y;
+    s += __shfl_xor_sync(0xffffffffu, low ? v.y : v.x, 16);
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, d);
-    b += __shfl_xor_sync(0xffffffffu, b, d);
+    for (int d = 8; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if constexpr (kWarps == 1)
+      held = s;
+    else if ((lane & 15) == 0)
+      sm[64 * turn + 2 * lane + (threadIdx.x % kTeam) / 32] = s;
   }
-  if constexpr (kTeam == 32) return make_float2(a, b);
-  constexpr int kWarps = kTeam / 32;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x % kTeam) >> 5;
-  float2* half = sm + 32 * turn;
-  if (lane == 0) half[warp] = make_float2(a, b);
-  ptx::named_barrier_sync(1 + team, kTeam);
-  const float2 v = lane < kWarps ? half[lane] : make_float2(0.0f, 0.0f);
-  a = v.x, b = v.y;
+  __device__ void ready() {
+    if constexpr (kWarps > 1) ptx::named_barrier_sync(1 + team, kTeam);
+  }
+  __device__ float2 get(int turn) {
+    float s = held;
+    if constexpr (kWarps > 1) {
+      constexpr int kHalf = kWarps > 16 ? 16 : kWarps;  // a lane takes one warp's, or two
+      const float* from = sm + 64 * turn + 2 * (threadIdx.x & 16);
+      s = from[threadIdx.x & (kHalf - 1)];
+      if (kWarps > 16) s += from[16 + (threadIdx.x & 15)];
 #pragma unroll
-  for (int d = kWarps / 2; d >= 1; d >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, d);
-    b += __shfl_xor_sync(0xffffffffu, b, d);
+      for (int d = kHalf / 2; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    }
+    return make_float2(__shfl_sync(0xffffffffu, s, 0), __shfl_sync(0xffffffffu, s, 16));
   }
-  return make_float2(__shfl_sync(0xffffffffu, a, 0), __shfl_sync(0xffffffffu, b, 0));
-}
+  __device__ float2 all(float2 v, int turn) {
+    add(v, turn);
+    ready();
+    return get(turn);
+  }
+};
 
 // A team of kTeam threads holds a row in registers, kPer vectors of kVec elements a
 // thread, and loads its next row before it works on this one.
 template <class X, class W, bool kRms, int kVec, int kTeam, int kPer, int kTeams>
 __global__ void __launch_bounds__(kTeam* kTeams) norm_rows(const NormArgs a) {
-  __shared__ float2 sm[kTeam > 32 ? kTeams * 64 : 1];
+  __shared__ float sm[kTeam > 32 ? kTeams * 128 : 1];
   const int team = threadIdx.x / kTeam, at = threadIdx.x % kTeam;
   const int32_t D = static_cast<int32_t>(a.D);
   const X* x = static_cast<const X*>(a.x);
@@ -234,6 +245,8 @@ __global__ void __launch_bounds__(kTeam* kTeams) norm_rows(const NormArgs a) {
   const float n = static_cast<float>(D);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + team;
+  typedef Reg<kVec> Row;
+  TeamSums<kTeam> sums(sm + team * 128, team);
   Vec<X, kVec> next[kPer];
   auto column = [&](int i) { return (i * kTeam + at) * kVec; };
   auto load = [&](int64_t row) {
@@ -245,57 +258,71 @@ __global__ void __launch_bounds__(kTeam* kTeams) norm_rows(const NormArgs a) {
   ptx::griddep_launch_dependents();
   if (t < a.T) load(t);
   for (int turn = 0; t < a.T; t += step) {
-    float f[kPer][kVec];
-    float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+    Row f[kPer];
+    typename Row::E s1 = Row::all(0.0f), s2 = s1;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (column(i) < D) {
         next[i].get(f[i]);
-        if (!kRms) vsum(s1, f[i]);
+#pragma unroll
+        for (int j = 0; j < (kRms ? 0 : Row::kW); ++j) s1 = vadd(s1, f[i].v[j]);
       }
     if (t + step < a.T) load(t + step);
     float m1 = 0.0f;
     if constexpr (!kRms) {
-      m1 = team_sums<kTeam>(s1.x + s1.y, 0.0f, sm + team * 64, turn, team).x / n;
+      m1 = sums.all(make_float2(total(s1), 0.0f), turn).x / n;
       turn ^= 1;
-      s1 = make_float2(0.0f, 0.0f);
+      s1 = s2;
     }
+    const typename Row::E back = Row::all(-m1);
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (column(i) < D) {
-        if (!kRms) {
-          vadd(f[i], -m1);
-          vsum(s1, f[i]);
+#pragma unroll
+        for (int j = 0; j < Row::kW; ++j) {
+          if (!kRms) {
+            f[i].v[j] = vadd(f[i].v[j], back);
+            s1 = vadd(s1, f[i].v[j]);
+          }
+          s2 = vfma(f[i].v[j], f[i].v[j], s2);
         }
-        vdot(s2, f[i], f[i]);
       }
-    const float2 s = team_sums<kTeam>(s1.x + s1.y, s2.x + s2.y, sm + team * 64, turn, team);
+    const float2 s = sums.all(make_float2(kRms ? 0.0f : total(s1), total(s2)), turn);
     turn ^= 1;
     const float c = kRms ? 0.0f : s.x / n;
     const float var = s.y / n - c * c;
     const float r = __frsqrt_rn((var < 0.0f ? 0.0f : var) + a.eps);  // (fmaxf would lose a NaN)
+    const typename Row::E rs = Row::all(r), cr = Row::all(-c * r);
     X* y = static_cast<X*>(a.y) + t * a.ldy;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int col = column(i);
       if (col >= D) continue;
-      float g[kVec];
-      if (kRms)
-        vmul(f[i], r);
-      else
-        vfma(f[i], f[i], r, -c * r);
-      if (w) {
-        load_weight<W, kVec>(w + col, g);
-        if (!kRms && b) {
-          float h[kVec];
-          load_weight<W, kVec>(b + col, h);
-          vfma(f[i], f[i], g, h);
+      if constexpr (kRms) {
+        if (w) {
+          Row g;
+          load_weight<W, kVec>(w + col, g);
+#pragma unroll
+          for (int j = 0; j < Row::kW; ++j) f[i].v[j] = vmul(vmul(f[i].v[j], rs), g.v[j]);
         } else {
-          vmul(f[i], g);
+#pragma unroll
+          for (int j = 0; j < Row::kW; ++j) f[i].v[j] = vmul(f[i].v[j], rs);
         }
-      } else if (!kRms && b) {
-        load_weight<W, kVec>(b + col, g);
-        vadd(f[i], g);
+      } else {
+#pragma unroll
+        for (int j = 0; j < Row::kW; ++j) f[i].v[j] = vfma(f[i].v[j], rs, cr);
+        if (w && b) {
+          Row g, h;
+          load_weight<W, kVec>(w + col, g);
+          load_weight<W, kVec>(b + col, h);
+#pragma unroll
+          for (int j = 0; j < Row::kW; ++j) f[i].v[j] = vfma(f[i].v[j], g.v[j], h.v[j]);
+        } else if (w || b) {
+          Row g;
+          load_weight<W, kVec>((w ? w : b) + col, g);
+#pragma unroll
+          for (int j = 0; j < Row::kW; ++j) f[i].v[j] = w ? vmul(f[i].v[j], g.v[j]) : vadd(f[i].v[j], g.v[j]);
+        }
       }
       Vec<X, kVec>::store(y + col, f[i]);
     }
@@ -310,42 +337,81 @@ __global__ void __launch_bounds__(kTeam* kTeams) norm_rows(const NormArgs a) {
   }
 }
 
-// Rows of norm_rows_back on their way: vectors come through shared memory, of which
-// every thread copies and reads its own columns alone (a row ahead in registers keeps
-// 32 KB of an SM's loads in flight, three rows ahead 96 KB); single elements through
-// registers.
-__host__ __device__ constexpr int back_ahead(int threads) { return threads > 512 ? 2 : 3; }
-template <class X, int kVec, int kPer>
-struct BackRow {
-  Vec<X, kVec> x[kPer], g[kPer];
-};
-template <int kVec, int kPer>
-constexpr size_t back_ring(int threads) {
-  return kVec > 1 ? static_cast<size_t>(back_ahead(threads) + 1) * 2 * kPer * threads * 16 : 0;
+// A block's sums of dy h and dy, its teams' added up in order, to row blockIdx.x of
+// `partial`.  sums: [2][D] of shared memory, where kTeams > 1.
+template <bool kRms, int kVec, int kTeam, int kPer, int kTeams>
+__device__ __forceinline__ void leave_sums(const NormArgs& a, int team, int at, const Reg<kVec> (&sw)[kPer],
+                                           const Reg<kVec>* sb, float* sums) {
+  if (!a.partial) return;
+  const int32_t D = static_cast<int32_t>(a.D);
+  float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * D;
+#pragma unroll 1
+  for (int k = 0; k < kTeams; ++k) {
+    if (team == k) {
+      float* to = k + 1 < kTeams ? sums : out;
+      auto leave = [&](const Reg<kVec>& v, int64_t i) {
+        if constexpr (kVec == 1) {
+          to[i] = k > 0 ? v.v[0] + sums[i] : v.v[0];
+        } else {
+#pragma unroll
+          for (int j = 0; j < kVec; j += 4) {  // (D is a multiple of 4)
+            const float2 p = unpack2(v.v[j / 2]), q = unpack2(v.v[j / 2 + 1]);
+            float4 f = make_float4(p.x, p.y, q.x, q.y);
+            if (k > 0) {
+              const float4 o = *reinterpret_cast<const float4*>(sums + i + j);
+              f = make_float4(f.x + o.x, f.y + o.y, f.z + o.z, f.w + o.w);
+            }
+            *reinterpret_cast<float4*>(to + i + j) = f;
+          }
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int col = (i * kTeam + at) * kVec;
+        if (col >= D) continue;
+        leave(sw[i], col);
+        if constexpr (!kRms) leave(sb[i], D + col);
+      }
+    }
+    if (kTeams > 1) __syncthreads();
+  }
 }
 
 // The gradients: teams as above.  A thread's columns are the same in every row, so
-// that it keeps their sums of dy h and dy in registers, and their weights; at the end a
-// block adds up its teams' sums in order, and leaves one row of `partial`.
+// that it keeps their sums of dy h and dy in registers, and their weights.
+//
+// Rows come through a ring in shared memory, of which every thread copies and reads
+// its own columns alone: 96 KB of an SM's loads in flight, where a row ahead in
+// registers is 32 KB.  A row's sums meet at a barrier while the team is at the first
+// half of the next row, and its dx follows, from the ring again: waiting for the sums
+// of each row in turn left the SM idle for half of the time (8192 x 8192: 81 us).
+__host__ __device__ constexpr int back_slots(int threads) { return threads > 512 ? 3 : 5; }
+template <int kPer>
+constexpr size_t back_ring(int threads) {
+  return static_cast<size_t>(back_slots(threads)) * 2 * kPer * threads * 16;
+}
+
 template <class X, class W, bool kRms, int kVec, int kTeam, int kPer, int kTeams>
 __global__ void __launch_bounds__(kTeam* kTeams, 512 / (kTeam * kTeams) > 0 ? 512 / (kTeam * kTeams) : 1)
     norm_rows_back(const NormArgs a) {
-  extern __shared__ __align__(16) uint8_t ring[];  // the rows on their way; then sums [2][D], where kTeams > 1
-  __shared__ float2 sm[kTeam > 32 ? kTeams * 64 : 1];
-  constexpr bool kRing = kVec > 1;
-  constexpr int kThreads = kTeam * kTeams, kBackAhead = back_ahead(kThreads), kSlots = kBackAhead + 1;
-  // A block of 1024 threads has registers for the sums, and reads the row twice.
-  constexpr bool kHold = !kRing || kThreads <= 512;
+  extern __shared__ __align__(16) uint8_t ring[];  // then the sums, where kTeams > 1
+  __shared__ float sm[kTeam > 32 ? kTeams * 128 : 1];
+  constexpr int kThreads = kTeam * kTeams, kSlots = back_slots(kThreads);
+  constexpr bool kHold = kThreads <= 512;  // a block of 1024 threads has no registers for the weights
+  typedef Reg<kVec> Row;
+  typedef typename Row::E E;
   const int team = threadIdx.x / kTeam, at = threadIdx.x % kTeam;
   const int32_t D = static_cast<int32_t>(a.D);
   const X *x = static_cast<const X*>(a.x), *dy = static_cast<const X*>(a.dy);
   const W* w = static_cast<const W*>(a.weight);
   const float n = static_cast<float>(D);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + team;
-  BackRow<X, kVec, kPer> next;
-  float mn = 0.0f, rn = 0.0f;
-  float sw[kPer][kVec] = {}, sb[kRms ? 1 : kPer][kVec] = {}, wv[kHold ? kPer : 1][kVec];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTeams + team;
+  Row sw[kPer], sb[kRms ? 1 : kPer], wv[kHold ? kPer : 1];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+#pragma unroll
+    for (int j = 0; j < Row::kW; ++j) sw[i].v[j] = sb[kRms ? 0 : i].v[j] = Row::all(0.0f);
   auto column = [&](int i) { return (i * kTeam + at) * kVec; };
   // Slot s, vector i of x (which = 0) or dy (1) of this thread.
   const uint32_t mine = ptx::smem_addr(ring) + threadIdx.x * 16;
@@ -357,120 +423,170 @@ __global__ void __launch_bounds__(kTeam* kTeams, 512 / (kTeam * kTeams) > 0 ? 51
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         if (column(i) < D) {
-          if constexpr (kRing) {
-            ptx::cp_async_16(slot(s, 0, i), x + row * a.ldx + column(i));
-            ptx::cp_async_16(slot(s, 1, i), dy + row * a.lddy + column(i));
-          } else {
-            next.x[i].load(x + row * a.ldx + column(i));
-            next.g[i].load(dy + row * a.lddy + column(i));
-          }
+          ptx::cp_async_16(slot(s, 0, i), x + row * a.ldx + column(i));
+          ptx::cp_async_16(slot(s, 1, i), dy + row * a.lddy + column(i));
         }
     }
-    if constexpr (kRing) ptx::cp_async_commit();
+    ptx::cp_async_commit();
   };
   auto stats = [&](int64_t row) {
-    if (row < a.T) {
-      if (!kRms) mn = a.stats[2 * row];
-      rn = a.stats[kRms ? row : 2 * row + 1];
-    }
+    if (row >= a.T) return make_float2(0.0f, 0.0f);
+    return kRms ? make_float2(0.0f, a.stats[row]) : make_float2(a.stats[2 * row], a.stats[2 * row + 1]);
   };
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
-  for (int s = 0; s < (kRing ? kBackAhead : 1); ++s) fetch(t + s * step, s);
-  stats(t);
-  auto weights = [&](int i, float(&v)[kVec]) {
+  auto weights = [&](int i, Row& v) {
     if (w && column(i) < D) {
       load_weight<W, kVec>(w + column(i), v);
     } else {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) v[j] = 1.0f;
+      for (int j = 0; j < Row::kW; ++j) v.v[j] = Row::all(1.0f);
     }
   };
-#pragma unroll
-  for (int i = 0; i < (kHold ? kPer : 0); ++i) weights(i, wv[i]);
-  // h and q of vector i, and dy.
-  auto work_out = [&](int i, float m, float r, float(&h)[kVec], float(&q)[kVec], float(&g)[kVec]) {
-    next.x[i].get(h);
-    next.g[i].get(g);
-    if (!kRms) vadd(h, -m);
-    vmul(h, r);
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) q[j] = g[j];
-    if constexpr (!kHold) weights(i, wv[0]);
-    vmul(q, wv[kHold ? i : 0]);
+  // x and dy of vector i, from slot s; the weights.
+  auto take = [&](int s, int i, Row& f, Row& g, Row& q) {
+    Vec<X, kVec> v;
+    v.r = ptx::ld_shared_v4_u32(slot(s, 0, i));
+    v.get(f);
+    v.r = ptx::ld_shared_v4_u32(slot(s, 1, i));
+    v.get(g);
+    if constexpr (kHold)
+      q = wv[i];
+    else
+      weights(i, q);
   };
-  int at_slot = 0;
-  for (int turn = 0; t < a.T; t += step, turn ^= 1) {
-    const float m = mn, r = rn;
-    float h[kHold ? kPer : 1][kVec], q[kHold ? kPer : 1][kVec], g[kVec];
-    const int here = at_slot;
-    float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
-    if constexpr (kRing) {
-      ptx::cp_async_wait<kBackAhead - 1>();
-      const int free_slot = at_slot == 0 ? kSlots - 1 : at_slot - 1;  // read in the turn before
-      fetch(t + kBackAhead * step, free_slot);
-      at_slot = at_slot + 1 == kSlots ? 0 : at_slot + 1;
-    }
-    stats(t + step);
+  // The first half of a row: its sums of q and q h, and its share of the weights'.
+  auto first = [&](int s, float2 st) {
+    const E back = Row::all(-st.x), rs = Row::all(st.y);
+    E s1 = Row::all(0.0f), s2 = s1;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (column(i) < D) {
-        if constexpr (kRing) {
-          next.x[i].r = ptx::ld_shared_v4_u32(slot(here, 0, i));
-          next.g[i].r = ptx::ld_shared_v4_u32(slot(here, 1, i));
+        Row h, g, q;
+        take(s, i, h, g, q);
+#pragma unroll
+        for (int j = 0; j < Row::kW; ++j) {
+          if (!kRms) h.v[j] = vadd(h.v[j], back);
+          h.v[j] = vmul(h.v[j], rs);
+          q.v[j] = vmul(g.v[j], q.v[j]);
+          sw[i].v[j] = vfma(g.v[j], h.v[j], sw[i].v[j]);
+          if (!kRms) {
+            sb[kRms ? 0 : i].v[j] = vadd(sb[kRms ? 0 : i].v[j], g.v[j]);
+            s1 = vadd(s1, q.v[j]);
+          }
+          s2 = vfma(q.v[j], h.v[j], s2);
         }
-        const int k = kHold ? i : 0;
-        work_out(i, m, r, h[k], q[k], g);
-        vfma(sw[i], g, h[k], sw[i]);
-        if (!kRms) vadd(sb[kRms ? 0 : i], g);
-        if (!kRms) vsum(s1, q[k]);
-        vdot(s2, q[k], h[k]);
       }
-    if constexpr (!kRing) fetch(t + step, 0);
-    const float2 s = team_sums<kTeam>(s1.x + s1.y, s2.x + s2.y, sm + team * 64, turn, team);
-    const float c1 = kRms ? 0.0f : s.x / n, c2 = s.y / n;
+    return make_float2(kRms ? 0.0f : total(s1), total(s2));
+  };
+  // The second:  dx = r q - h r c2 - r c1.
+  auto second = [&](int s, int64_t t, float2 st, float2 sum) {
+    const float r = st.y, c1 = kRms ? 0.0f : sum.x / n, c2 = sum.y / n;
+    const E back = Row::all(-st.x), rs = Row::all(r), k2 = Row::all(-r * c2), k1 = Row::all(-r * c1);
     X* dx = static_cast<X*>(a.y) + t * a.ldy;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (column(i) < D) {
-        const int k = kHold ? i : 0;
-        if constexpr (!kHold) {
-          next.x[i].r = ptx::ld_shared_v4_u32(slot(here, 0, i));
-          next.g[i].r = ptx::ld_shared_v4_u32(slot(here, 1, i));
-          work_out(i, m, r, h[k], q[k], g);
-        }
-        if (!kRms) vadd(q[k], -c1);
-        vfma(q[k], h[k], -c2, q[k]);
-        vmul(q[k], r);
-        Vec<X, kVec>::store(dx + column(i), q[k]);
-      }
-  }
-  if constexpr (kRing) {
-    ptx::cp_async_wait<0>();
-    if (kTeams > 1) __syncthreads();  // the sums take the ring's place
-  }
-  float* sums = reinterpret_cast<float*>(ring);
-  if (!a.partial) return;
-  float* out = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * D;
-#pragma unroll 1
-  for (int k = 0; k < kTeams; ++k) {
-    if (team == k) {
+        Row f, g, q;
+        take(s, i, f, g, q);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int col = column(i);
-        if (col >= D) continue;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          float vw = sw[i][j], vb = kRms ? 0.0f : sb[kRms ? 0 : i][j];
-          if (k > 0) vw += sums[col + j], vb += sums[D + col + j];
-          float* to = k + 1 < kTeams ? sums : out;
-          to[col + j] = vw;
-          if (!kRms) to[D + col + j] = vb;
+        for (int j = 0; j < Row::kW; ++j) {
+          const E h = vmul(kRms ? f.v[j] : vadd(f.v[j], back), rs);
+          f.v[j] = vfma(vmul(g.v[j], q.v[j]), rs, kRms ? vmul(h, k2) : vfma(h, k2, k1));
         }
+        Vec<X, kVec>::store(dx + column(i), f);
       }
+  };
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  // Row k of this team is in slot k % kSlots; rows k + 1 .. k + kSlots - 2 are on their
+  // way while the team is at row k's first half (and at row k - 1's second).
+#pragma unroll
+  for (int s = 0; s < kSlots - 1; ++s) fetch(t0 + s * step, s);
+#pragma unroll
+  for (int i = 0; i < (kHold ? kPer : 0); ++i) weights(i, wv[i]);
+  float2 st = stats(t0), last_st = make_float2(0.0f, 0.0f);
+  int s = 0, turn = 0;
+  TeamSums<kTeam> sums(sm + team * 128, team);
+  for (int64_t t = t0; t - step < a.T; t += step, turn ^= 1) {
+    const int before = s == 0 ? kSlots - 1 : s - 1;
+    const bool again = t > t0;
+    const float2 next_st = stats(t + step);  // on its way while this row is worked on
+    if (again) sums.ready();
+    float2 last = make_float2(0.0f, 0.0f);
+    if (kTeam == 32 && again) last = sums.get(0);  // before the next row's take its place
+    if (t < a.T) {
+      ptx::cp_async_wait<kSlots - 2>();
+      sums.add(first(s, st), turn);
     }
-    if (kTeams > 1) __syncthreads();
+    if (kTeam > 32 && again) last = sums.get(turn ^ 1);
+    if (again) second(before, t - step, last_st, last);
+    fetch(t + (kSlots - 1) * step, before);
+    last_st = st;
+    st = next_st;
+    s = s + 1 == kSlots ? 0 : s + 1;
   }
+  ptx::cp_async_wait<0>();
+  if (kTeams > 1) __syncthreads();  // the sums take the ring's place
+  leave_sums<kRms, kVec, kTeam, kPer, kTeams>(a, team, at, sw, sb, reinterpret_cast<float*>(ring));
+}
+
+// The same for rows that start on any element, a row ahead in registers.
+template <class X, class W, bool kRms, int kTeam, int kPer, int kTeams>
+__global__ void __launch_bounds__(kTeam* kTeams) norm_rows_back_single(const NormArgs a) {
+  extern __shared__ float block_sums_of[];  // [2][D], where kTeams > 1
+  __shared__ float sm[kTeam > 32 ? kTeams * 128 : 1];
+  const int team = threadIdx.x / kTeam, at = threadIdx.x % kTeam;
+  const int32_t D = static_cast<int32_t>(a.D);
+  const X *x = static_cast<const X*>(a.x), *dy = static_cast<const X*>(a.dy);
+  const W* w = static_cast<const W*>(a.weight);
+  const float n = static_cast<float>(D);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
+  TeamSums<kTeam> sums(sm + team * 128, team);
+  X xn[kPer], gn[kPer];
+  float mn = 0.0f, rn = 0.0f, wv[kPer];
+  Reg<1> sw[kPer], sb[kRms ? 1 : kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) sw[i].v[0] = sb[kRms ? 0 : i].v[0] = 0.0f;
+  auto column = [&](int i) { return i * kTeam + at; };
+  auto fetch = [&](int64_t t) {
+    if (t >= a.T) return;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (column(i) < D) {
+        xn[i] = x[t * a.ldx + column(i)];
+        gn[i] = dy[t * a.lddy + column(i)];
+      }
+    if (!kRms) mn = a.stats[2 * t];
+    rn = a.stats[kRms ? t : 2 * t + 1];
+  };
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + team;
+  fetch(t);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) wv[i] = w && column(i) < D ? widen(w[column(i)]) : 1.0f;
+  for (int turn = 0; t < a.T; t += step, turn ^= 1) {
+    const float m = mn, r = rn;
+    float h[kPer], q[kPer], s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (column(i) < D) {
+        const float g = widen(gn[i]);
+        h[i] = (widen(xn[i]) - m) * r;
+        q[i] = g * wv[i];
+        sw[i].v[0] = fmaf(g, h[i], sw[i].v[0]);
+        if (!kRms) sb[kRms ? 0 : i].v[0] += g;
+        s1 += q[i];
+        s2 = fmaf(q[i], h[i], s2);
+      }
+    fetch(t + step);
+    const float2 s = sums.all(make_float2(s1, s2), turn);
+    const float c1 = kRms ? 0.0f : s.x / n, c2 = s.y / n;
+    X* dx = static_cast<X*>(a.y) + t * a.ldy;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (column(i) < D) narrow(r * ((q[i] - c1) - h[i] * c2), dx + column(i));
+  }
+  leave_sums<kRms, 1, kTeam, kPer, kTeams>(a, team, at, sw, sb, block_sums_of);
 }
 
 // One block per row, element by element: rows of any length, start and distance.
