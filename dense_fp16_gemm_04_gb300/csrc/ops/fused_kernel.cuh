@@ -27,6 +27,10 @@
 //                row's target logit (xent_kernels.cuh).
 //   kEpiXent     acc = logits z: C = a exp(z - lse) - b [column = target].
 //   kEpiSum      C = acc or C += acc, fp32.
+//   kEpiStoreLive  C = alpha acc with alpha on the device, its rows where row_map
+//                says.
+// The last three may have fewer rows or k-blocks than the launch was laid out for:
+// their number is on the device (live), with the tokens that have a gradient.
 //
 // What bounds them.  Large products: the tensor cores, and the power they draw
 // (gated block of 8192 tokens, 8192 x 16384: 4100 us, 1610 TFLOP/s; its backward
@@ -74,6 +78,7 @@ enum FusedEpi : int {
   kEpiLse = 5,
   kEpiXent = 6,
   kEpiSum = 7,
+  kEpiStoreLive = 8,
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -99,8 +104,8 @@ struct FusedArgs {
   uint32_t a_tx;              // bytes of A a CTA loads per k-block
   int32_t stages;             // kFlex: k-blocks in flight, A's a_tx bytes apart
   int32_t a_mn, b_mn;         // operand layouts: 0 K-contiguous, 1 MN-contiguous
-  // Bit 0, 1: A, B were complete before the previous kernel of the stream let
-  // this one start, and may be loaded before it ends.
+  // Bit 0, 1, 2: A, B, `live` were complete before the previous kernel of the stream
+  // let this one start, and may be loaded before it ends.
   int32_t early;
   int32_t bf16;               // operands and 16-bit outputs are bf16
   int32_t act, save;          // gated epilogues: activation; keep g and u
@@ -113,7 +118,11 @@ struct FusedArgs {
   uint16_t *c, *d;
   int64_t ldd, d_up;
   int64_t ldc, c_z;           // c_z: from one matrix of C's stack to the next
-  const float* alpha_p;       // kEpiStore: times alpha, null for 1
+  const float* alpha_p;       // kEpiStoreLive: alpha
+  // kLive: rows, or with live_k k (64 of them a block), that the product has (null: all);
+  // at least live_min tiles of rows.  row_map: where a row of C goes (null: in place).
+  const int32_t *live, *row_map;
+  int32_t live_k, live_min;
   // kEpiLse: targets [M], their logits [M] and the shares' (maximum, sum) [share][M].
   const int64_t* targets;
   float* target_z;
@@ -179,6 +188,7 @@ struct FusedCfg {
   // the loss of one token over 4096 products was off by 9e-6 of itself, of which
   // 16 steps at a time leave 5e-7 (4096 tokens x 4096 x 131072: 2545 -> 2577 us).
   static constexpr bool kPartial = kEpi == kEpiLse;
+  static constexpr bool kLive = kEpi == kEpiXent || kEpi == kEpiSum || kEpi == kEpiStoreLive;
   static constexpr bool kReads = kEpi == kEpiGluBwd || kEpi == kEpiSplit || kSym;  // the epilogue reads too
   static constexpr int kOutN = kGlu ? kBN / 2 : kBN;  // output columns per tile
   static constexpr int kBM = 128, kBK = 64;
@@ -199,7 +209,8 @@ struct FusedCfg {
   static constexpr int kOffBar = kOffEpi + kEpiWarps * kEpiBufs * kBufBytes;
   // Few rows leave room for more k-blocks: their number is the launch's.
   static constexpr bool kFlex =
-      kCtas == 1 && (kEpi == kEpiStore || kEpi == kEpiGlu || kEpi == kEpiLse || kEpi == kEpiXent);
+      kCtas == 1 && (kEpi == kEpiStore || kEpi == kEpiGlu || kEpi == kEpiLse || kEpi == kEpiXent ||
+                     kEpi == kEpiStoreLive);
   static constexpr int kMaxStages = kFlex ? 8 : kStages;
   static constexpr int kNumBars = 2 * kMaxStages + 5;
   static constexpr int kOffSlot = kOffBar + kNumBars * 8;
@@ -237,14 +248,38 @@ struct FusedItem {
   int32_t mb, nb, batch, kb0, kb1;
 };
 
+// What of a launch's size may be on the device.
+struct FusedDims {
+  int32_t rows, tiles_m, per_batch, items, num_kb;
+};
+
 template <class Cfg>
-__device__ __forceinline__ FusedItem fused_item(const FusedArgs& a, int32_t t, int32_t rank) {
+__device__ __forceinline__ FusedDims fused_dims(const FusedArgs& a) {
+  FusedDims d = {a.M, a.tiles_m, a.per_batch, a.items, a.num_kb};
+  if constexpr (Cfg::kLive) {
+    if (a.live) {
+      if (!(a.early & 4)) ptx::griddep_wait();
+      const int32_t n = *reinterpret_cast<const volatile int32_t*>(a.live);
+      if (a.live_k) {
+        d.num_kb = max(1, (n + 63) / 64);
+      } else {
+        d.rows = n;
+        d.tiles_m = max(a.live_min, (n + Cfg::kTileM - 1) / Cfg::kTileM);
+        d.items = d.per_batch = d.tiles_m * a.tiles_n;
+      }
+    }
+  }
+  return d;
+}
+
+template <class Cfg>
+__device__ __forceinline__ FusedItem fused_item(const FusedArgs& a, const FusedDims& d, int32_t t, int32_t rank) {
   FusedItem w;
-  const int32_t total = a.num_kb * a.segs;
+  const int32_t total = d.num_kb * a.segs;
   w.kb0 = Cfg::kSplit > 1 ? rank * total / Cfg::kSplit : 0;
   w.kb1 = Cfg::kSplit > 1 ? (rank + 1) * total / Cfg::kSplit : total;
-  w.batch = t / a.per_batch;
-  const int32_t r = t - w.batch * a.per_batch;
+  w.batch = t / d.per_batch;
+  const int32_t r = t - w.batch * d.per_batch;
   if constexpr (Cfg::kSym) {
     // Triangle r: column nb holds rows 0 .. nb.
     int32_t j = static_cast<int32_t>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
@@ -253,7 +288,7 @@ __device__ __forceinline__ FusedItem fused_item(const FusedArgs& a, int32_t t, i
     w.nb = j;
     w.mb = r - j * (j + 1) / 2;
   } else {
-    raster(r, a.tiles_m, a.tiles_n, a.group_m, w.mb, w.nb);
+    raster(r, d.tiles_m, a.tiles_n, a.group_m, w.mb, w.nb);
   }
   return w;
 }
@@ -280,23 +315,24 @@ __device__ __forceinline__ void finish_columns(const FusedArgs& args, const Fuse
   // Columns come in groups of eight that are in or out together (four, gated
   // over eight CTAs): N is a multiple of 8, or the rows are padded to one.
   constexpr int kG = kN < 8 ? kN : 8;
-  if constexpr (Cfg::kEpi == kEpiStore || Cfg::kEpi == kEpiXent) {
+  if constexpr (Cfg::kEpi == kEpiStore) {
     uint16_t* c = args.c + wi.batch * args.c_zb * args.c_z + static_cast<int64_t>(row) * args.ldc + col0;
-    float w[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i) w[i] = v[i];
-    if constexpr (Cfg::kEpi == kEpiXent) {
-      xent_columns<kN>(args.xent_rows[row], args.col_base + col0, w);
-    } else {
-      const float alpha = args.alpha_p ? args.alpha * *args.alpha_p : args.alpha;
-#pragma unroll
-      for (int i = 0; i < kN; ++i) w[i] *= alpha;
-    }
 #pragma unroll
     for (int i = 0; i < kN; i += kG) {
       uint32_t p[kG / 2];
 #pragma unroll
-      for (int j = 0; j < kG / 2; ++j) p[j] = pack16(bf16, w[i + 2 * j], w[i + 2 * j + 1]);
+      for (int j = 0; j < kG / 2; ++j)
+        p[j] = pack16(bf16, args.alpha * v[i + 2 * j], args.alpha * v[i + 2 * j + 1]);
+      if (col0 + i < args.N) store16<kG>(c + i, p);
+    }
+  } else if constexpr (Cfg::kEpi == kEpiStoreLive) {
+    const float alpha = *args.alpha_p;
+    uint16_t* c = args.c + static_cast<int64_t>(args.row_map ? args.row_map[row] : row) * args.ldc + col0;
+#pragma unroll
+    for (int i = 0; i < kN; i += kG) {
+      uint32_t p[kG / 2];
+#pragma unroll
+      for (int j = 0; j < kG / 2; ++j) p[j] = pack16(bf16, alpha * v[i + 2 * j], alpha * v[i + 2 * j + 1]);
       if (col0 + i < args.N) store16<kG>(c + i, p);
     }
   } else if constexpr (Cfg::kEpi == kEpiLse) {
@@ -422,7 +458,7 @@ __device__ __forceinline__ void read_columns(const FusedArgs& args, const FusedI
 // The end of a split cluster's tile, run by all 256 threads of each CTA: lone
 // CTAs.
 template <class Cfg>
-__device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t unit, int32_t rank,
+__device__ __forceinline__ void split_epilogue(const FusedArgs& args, const FusedDims& dims, int32_t unit, int32_t rank,
                                                uint32_t tmem_base, uint32_t recv, uint32_t tfull,
                                                const Watch& w) {
   constexpr int kS = Cfg::kSplit;
@@ -431,7 +467,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   ptx::griddep_wait();  // reads S, g and u; writes the outputs
   ptx::griddep_launch_dependents();
-  const FusedItem wi = fused_item<Cfg>(args, unit, rank);
+  const FusedItem wi = fused_item<Cfg>(args, dims, unit, rank);
   bool ok = wait_bar_warp<false>(tfull, 0u, w, kSiteTmemFull, unit);
   if (ok) {
     // Send: warp quarter q owns 32 rows, warps 0-3 columns 0-63, warps 4-7 the
@@ -478,7 +514,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
   const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
   const int32_t row = wi.mb * Cfg::kBM + r;
   const int32_t col0 = wi.nb * Cfg::kOutN + rank * (Cfg::kOutN / kS) + half * kN;
-  const bool in = row < args.M && (col0 < args.N || Cfg::kEpi == kEpiLse);  // (every share is written)
+  const bool in = row < dims.rows && (col0 < args.N || Cfg::kEpi == kEpiLse);  // (every share is written)
   uint4 s0[Cfg::kReads ? kN / 8 : 1], s1[Cfg::kReads ? kN / 8 : 1];
   if (in) read_columns<Cfg, kN>(args, wi, row, col0, s0, s1);
   ptx::cluster_sync();
@@ -506,7 +542,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, int32_t un
 // up projection's), and each CTA sends its 128 rows of the other half to the
 // CTA of the same rows in the other pair.  A sum of two: its order is free.
 template <class Cfg>
-__device__ __forceinline__ void pair_split_epilogue(const FusedArgs& args, int32_t unit, int32_t k, uint32_t cta,
+__device__ __forceinline__ void pair_split_epilogue(const FusedArgs& args, const FusedDims& dims, int32_t unit, int32_t k, uint32_t cta,
                                                     uint32_t tmem_base, uint32_t recv, uint32_t tfull,
                                                     const Watch& w) {
   constexpr int kOut = Cfg::kOutN / 2;           // output columns a pair finishes
@@ -534,10 +570,10 @@ __device__ __forceinline__ void pair_split_epilogue(const FusedArgs& args, int32
                                   v[4 * j + 2], v[4 * j + 3]);
     }
   }
-  const FusedItem wi = fused_item<Cfg>(args, unit, k);
+  const FusedItem wi = fused_item<Cfg>(args, dims, unit, k);
   const int32_t row = wi.mb * Cfg::kTileM + static_cast<int32_t>(cta) * Cfg::kBM + r;
   const int32_t col0 = wi.nb * Cfg::kOutN + k * kOut + side * kN;
-  const bool in = row < args.M && col0 < args.N;
+  const bool in = row < dims.rows && col0 < args.N;
   uint4 s0[Cfg::kReads ? kN / 8 : 1], s1[Cfg::kReads ? kN / 8 : 1];
   if (in) read_columns<Cfg, kN>(args, wi, row, col0, s0, s1);
   ptx::cluster_sync();
@@ -629,6 +665,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffSlot);
+  const FusedDims dims = fused_dims<Cfg>(args);
 
   if (warp == 0 || warp == Cfg::kWarpB) {
     // ------------------------------------------------------- TMA producers --
@@ -650,8 +687,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     uint32_t phase = 0;
     int64_t fills = 0;
     bool ok = true, first_item = true;
-    for (int32_t it = unit; ok && it < args.items; it += units) {
-      const FusedItem wi = fused_item<Cfg>(args, it, rank);
+    for (int32_t it = unit; ok && it < dims.items; it += units) {
+      const FusedItem wi = fused_item<Cfg>(args, dims, it, rank);
       int32_t row;
       const int32_t z0 = wi.batch * (is_a ? args.a_zb : args.b_zb);
       if (is_a)
@@ -660,7 +697,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         row = wi.nb * Cfg::kOutN;
       else
         row = wi.nb * Cfg::kBN + static_cast<int32_t>(cta) * Cfg::kBRows;
-      int32_t seg = wi.kb0 / args.num_kb, k = wi.kb0 - seg * args.num_kb;
+      int32_t seg = wi.kb0 / dims.num_kb, k = wi.kb0 - seg * dims.num_kb;
       for (int32_t kb = wi.kb0; kb < wi.kb1; ++kb) {
         if (!wait_bar_warp<kPair>(bar_empty(stage), phase ^ 1u, w, kSiteEmpty, it)) {
           ok = false;
@@ -697,7 +734,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           }
         }
         __syncwarp();
-        if (++k == args.num_kb) {
+        if (++k == dims.num_kb) {
           k = 0;
           ++seg;
         }
@@ -737,8 +774,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       uint32_t phase = 0;
       int32_t acc_iter = 0;
       bool ok = true;
-      for (int32_t it = unit; ok && it < args.items; it += units) {
-        const FusedItem wi = fused_item<Cfg>(args, it, rank);
+      for (int32_t it = unit; ok && it < dims.items; it += units) {
+        const FusedItem wi = fused_item<Cfg>(args, dims, it, rank);
         int32_t kb = wi.kb0;
         do {  // once, or for each partial sum
           const int32_t end = Cfg::kPartial && Cfg::kSplit == 1 ? min(wi.kb1, kb + kPartKb) : wi.kb1;
@@ -813,7 +850,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         sb + Cfg::kOffEpi + static_cast<uint32_t>((warp - 4) * Cfg::kEpiBufs * Cfg::kBufBytes);
     const uint32_t tempty_bar0 = kPair ? ptx::mapa(bar_tempty(0), leader) : bar_tempty(0);
     const bool bf16 = args.bf16 != 0;
-    const float alpha = Cfg::kEpi == kEpiStore && args.alpha_p ? args.alpha * *args.alpha_p : args.alpha;
+    const float alpha = Cfg::kEpi == kEpiStoreLive ? *args.alpha_p : args.alpha;
     uint32_t next_buf = 0, used = 0;
     int32_t acc_iter = 0;
     // The next free staging buffer: once the store that last read it is done.
@@ -871,8 +908,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       // Each warp for itself: 32 rows, and this group's half of the tile's columns.
       constexpr int kCols = Cfg::kOutN / Cfg::kGroups;
       bool ok = true;
-      for (int32_t it = unit; ok && it < args.items; it += units) {
-        const FusedItem wi = fused_item<Cfg>(args, it, rank);
+      for (int32_t it = unit; ok && it < dims.items; it += units) {
+        const FusedItem wi = fused_item<Cfg>(args, dims, it, rank);
         const int32_t row = wi.mb * Cfg::kTileM + static_cast<int32_t>(cta) * Cfg::kBM + q * 32 + lane;
         const int32_t col0 = wi.nb * Cfg::kOutN + group * kCols;
         const bool row_in = row < args.M;
@@ -927,14 +964,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     } else
     for (int32_t it = unit;; it += units) {
       // Every warp takes the same decision, so none is left at a barrier.
-      if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, it < args.items)) break;
-      const FusedItem wi = fused_item<Cfg>(args, it, rank);
+      if (!ptx::named_barrier_and(1, 32 * Cfg::kEpiWarps, it < dims.items)) break;
+      const FusedItem wi = fused_item<Cfg>(args, dims, it, rank);
       const int buf = acc_iter % Cfg::kAccBufs;
       const uint32_t use_par = static_cast<uint32_t>((acc_iter / Cfg::kAccBufs) & 1);
       ++acc_iter;
       const int32_t row0 = wi.mb * Cfg::kTileM + static_cast<int32_t>(cta) * Cfg::kBM + q * 32;
       const int32_t row = row0 + lane;
-      const bool row_in = row < args.M;
+      const bool row_in = row < dims.rows;
       // S of a chunk (high and low part; 64 columns each) comes in while the sums
       // do, or while the chunk before is stored (updates of 12 x 512 x 512: 268 us;
       // 292 us with S read when it is needed).
@@ -984,7 +1021,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const int32_t col0 = wi.nb * Cfg::kOutN + c * 64;
         const bool in = row0 < args.M && col0 < args.N;
         const bool last = c + Cfg::kGroups >= kChunks;
-        if constexpr (Cfg::kEpi == kEpiStore) {
+        if constexpr (Cfg::kEpi == kEpiStore || Cfg::kEpi == kEpiStoreLive) {
           uint32_t v0[32], v1[32], packed[32];
           ptx::tmem_ld_32x32b_x32(t_row + c * 64, v0);
           ptx::tmem_ld_32x32b_x32(t_row + c * 64 + 32, v1);
@@ -996,7 +1033,18 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             packed[i] = pack16(bf16, alpha * __uint_as_float(v0[2 * i]), alpha * __uint_as_float(v0[2 * i + 1]));
             packed[16 + i] = pack16(bf16, alpha * __uint_as_float(v1[2 * i]), alpha * __uint_as_float(v1[2 * i + 1]));
           }
-          store_chunk(&tmC, packed, col0, row0, wi.batch * args.c_zb, in);
+          if (Cfg::kEpi == kEpiStoreLive && args.row_map) {
+            // Each row to its own place: 128 bytes a lane.
+            if (row_in) {
+              uint16_t* to = args.c + static_cast<int64_t>(args.row_map[row]) * args.ldc + col0;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (col0 + 8 * j < args.N)  // (a multiple of 8)
+                  ptx::st_global_v4(to + 8 * j, packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+            }
+          } else {
+            store_chunk(&tmC, packed, col0, row0, wi.batch * args.c_zb, in);
+          }
         } else if constexpr (Cfg::kEpi == kEpiXent) {
           uint32_t packed[32];
 #pragma unroll
@@ -1135,10 +1183,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
   if constexpr (Cfg::kSplit > 1) {
     __syncwarp();
-    if constexpr (kPair)
-      pair_split_epilogue<Cfg>(args, unit, rank, cta, tmem_base, sb + Cfg::kOffEpi, bar_tfull(0), w);
-    else
-      split_epilogue<Cfg>(args, unit, rank, tmem_base, sb + Cfg::kOffEpi, bar_tfull(0), w);
+    if (!Cfg::kLive || unit < dims.items) {  // (alike in all of the cluster)
+      if constexpr (kPair)
+        pair_split_epilogue<Cfg>(args, dims, unit, rank, cta, tmem_base, sb + Cfg::kOffEpi, bar_tfull(0), w);
+      else
+        split_epilogue<Cfg>(args, dims, unit, rank, tmem_base, sb + Cfg::kOffEpi, bar_tfull(0), w);
+    }
   }
 
   ptx::tc_fence_before();

@@ -289,8 +289,10 @@ template <int kEpi>
 gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const Stack& c,
                     const Stack& d, cudaStream_t stream, int64_t* shares = nullptr) {
   constexpr bool kBatched = kEpi == kEpiSplit || kEpi == kEpiSplitSym;
-  // The loss's products: sums to add up are large, and the others' columns belong to lone CTAs.
-  constexpr bool kTwos = kEpi != kEpiSum && kEpi != kEpiLse && kEpi != kEpiXent, kSplits = kEpi != kEpiSum;
+  // The loss's logits and sums over pieces have many tiles; a k-range of fewer
+  // k-blocks than it was laid out for could be empty.
+  constexpr bool kSplits = kEpi != kEpiSum && kEpi != kEpiXent, kTwos = kSplits && kEpi != kEpiLse;
+  const bool split = kSplits && !(Pair<kEpi>::kLive && a.live_k);
   auto tiles = [&](int64_t tm, int64_t tn) { return Pair<kEpi>::kSym ? tn * (tn + 1) / 2 : tm * tn; };
   const int64_t n = kBatched ? 1 : p.batch, kb = cdiv(p.K, 64) * p.segs;
   const int64_t small = tiles(cdiv(p.M, 128), cdiv(p.N, Lone<kEpi>::kOutN)) * n;
@@ -300,11 +302,11 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
   constexpr int64_t kNever = INT64_MAX;
   const int64_t cost[kForms] = {
       h->max_pairs > 0 ? cdiv(big, h->max_pairs) * (33 * kb + 500) : kNever,
-      kTwos && h->max_twos > 0 && kb >= 4 ? cdiv(big, h->max_twos) * (33 * cdiv(kb, 2) + 700) : kNever,
+      kTwos && split && h->max_twos > 0 && kb >= 4 ? cdiv(big, h->max_twos) * (33 * cdiv(kb, 2) + 700) : kNever,
       cdiv(small, h->num_sms) * (27 * kb + 400),
-      kSplits && small <= most[1] && kb >= 4 ? 27 * cdiv(kb, 2) + 550 : kNever,
-      kSplits && small <= most[2] && kb >= (kBatched ? 4 : 8) ? 27 * cdiv(kb, 4) + 550 : kNever,
-      kSplits && !kBatched && small <= std::min(8, most[3]) && kb >= 16 ? 27 * cdiv(kb, 8) + 550 : kNever};
+      split && small <= most[1] && kb >= 4 ? 27 * cdiv(kb, 2) + 550 : kNever,
+      split && small <= most[2] && kb >= (kBatched ? 4 : 8) ? 27 * cdiv(kb, 4) + 550 : kNever,
+      split && !kBatched && small <= std::min(8, most[3]) && kb >= 16 ? 27 * cdiv(kb, 8) + 550 : kNever};
   switch (static_cast<int>(std::min_element(cost, cost + kForms) - cost)) {
     case kPairs: return launch_fused<Pair<kEpi>>(h, p, a, c, d, stream, shares);
     case kPairs2:
@@ -328,14 +330,11 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
   return launch_fused<Lone<kEpi>>(h, p, a, c, d, stream, shares);
 }
 
-// out = alpha A B^T, rounded to 16 bits (alpha: on the device, null for 1).  `early`:
-// operands that may be loaded while the previous kernel ends.  A kernel of the
-// operators lets the next one start only after it has waited for the one before
-// it, so what is complete by then are the caller's tensors, and what the last
-// kernel but one wrote.
-enum { kEarlyA = 1, kEarlyB = 2 };
-gemm_status_t product(gemm_ops_s* h, const Product& p, const Stack& out, int early, cudaStream_t stream,
-                      const float* alpha = nullptr);
+// `early`: operands (and FusedArgs::live) that may be loaded while the previous
+// kernel ends.  A kernel of the operators lets the next one start only after it has
+// waited for the one before it, so what is complete by then are the caller's tensors,
+// and what the last kernel but one wrote.
+enum { kEarlyA = 1, kEarlyB = 2, kEarlyLive = 4 };
 
 // Attributes of the loss's kernels, and how many of their clusters fit.
 bool xent_setup(gemm_ops_s* h);

@@ -4,20 +4,6 @@
 #include "ortho_kernels.cuh"
 #include "stream_kernel.cuh"
 
-namespace gb300 {
-namespace ops {
-
-gemm_status_t product(gemm_ops_s* h, const Product& p, const Stack& out, int early, cudaStream_t stream,
-                      const float* alpha) {
-  FusedArgs a = base_args(h, p);
-  a.early = early;
-  a.alpha_p = alpha;
-  return fused<kEpiStore>(h, p, a, out, {}, stream);
-}
-
-}  // namespace ops
-}  // namespace gb300
-
 namespace {
 
 using namespace gb300::ops;
@@ -27,6 +13,13 @@ using namespace gb300::ops;
 // us, 2048 x 5632 22.1 and 25.3 us, 4096 x 8192 46.3 and 41.7 us, 8192 x 16384
 // 145 and 133 us.
 constexpr int64_t kMaxStreamTokens = 16;
+
+// out = A B^T, rounded to 16 bits.
+gemm_status_t product(gemm_ops_s* h, const Product& p, const Stack& out, int early, cudaStream_t stream) {
+  FusedArgs a = base_args(h, p);
+  a.early = early;
+  return fused<kEpiStore>(h, p, a, out, {}, stream);
+}
 
 // How a product of few tokens is laid out: warps per CTA, CTAs per k-slice,
 // k-slices, and the CTA's shared memory.

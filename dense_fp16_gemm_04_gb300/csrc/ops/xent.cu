@@ -6,13 +6,15 @@ namespace gb300 {
 namespace ops {
 
 bool xent_setup(gemm_ops_s* h) {
-  if (!set_attr<Pair<kEpiLse>>() || !set_attr<Pair<kEpiXent>>() || !set_attr<Pair<kEpiSum>>() ||
-      !set_attr<Lone<kEpiLse>>() || !set_attr<Lone<kEpiXent>>() || !set_attr<Lone<kEpiSum>>() ||
-      !set_attr<Lone<kEpiLse, 2>>() || !set_attr<Lone<kEpiXent, 2>>() || !set_attr<Lone<kEpiLse, 4>>() ||
-      !set_attr<Lone<kEpiXent, 4>>() || !set_attr<Lone<kEpiLse, 8>>() || !set_attr<Lone<kEpiXent, 8>>())
+  if (!set_attr<Pair<kEpiLse>>() || !set_attr<Lone<kEpiLse>>() || !set_attr<Lone<kEpiLse, 2>>() ||
+      !set_attr<Lone<kEpiLse, 4>>() || !set_attr<Lone<kEpiLse, 8>>() || !set_attr<Pair<kEpiXent>>() ||
+      !set_attr<Lone<kEpiXent>>() || !set_attr<Pair<kEpiSum>>() || !set_attr<Lone<kEpiSum>>() ||
+      !set_attr<Pair<kEpiStoreLive>>() || !set_attr<TwoPairs<kEpiStoreLive>>() || !set_attr<Lone<kEpiStoreLive>>() ||
+      !set_attr<Lone<kEpiStoreLive, 2>>() || !set_attr<Lone<kEpiStoreLive, 4>>() || !set_attr<Lone<kEpiStoreLive, 8>>())
     return false;
   h->max_pairs = std::min({h->max_pairs, max_clusters<Pair<kEpiLse>>(), max_clusters<Pair<kEpiXent>>(),
-                           max_clusters<Pair<kEpiSum>>()});
+                           max_clusters<Pair<kEpiSum>>(), max_clusters<Pair<kEpiStoreLive>>()});
+  h->max_twos = std::min(h->max_twos, max_clusters<TwoPairs<kEpiStoreLive>>());
   return true;
 }
 
@@ -53,15 +55,17 @@ int64_t piece_columns(int64_t T, int64_t V) {
 
 struct XentSpace {
   int64_t piece, pitch;
-  size_t rows, scale, dz, sum, total;
+  size_t rows, scalars, order, packed, dz, sum, total;
 };
 XentSpace xent_space(int64_t T, int64_t D, int64_t V) {
   XentSpace s;
   s.piece = piece_columns(T, V);
   s.pitch = up(s.piece, 64);
   s.rows = 0;
-  s.scale = up(T * static_cast<int64_t>(sizeof(XentRow)), 256);
-  s.dz = s.scale + 256;
+  s.scalars = up(T * static_cast<int64_t>(sizeof(XentRow)), 256);
+  s.order = s.scalars + 256;
+  s.packed = s.order + up(T * 4, 256);
+  s.dz = s.packed + up(T * D * 2, 256);
   s.sum = s.dz + up(T * s.pitch * 2, 256);
   s.total = s.sum + (s.piece < V ? up(T * D * 4, 256) : 0);  // several pieces: fp32 sums of dx
   return s;
@@ -170,45 +174,62 @@ gemm_status_t gemm_linear_cross_entropy_backward(gemm_ops_t h, const float* dlos
   char* ws = static_cast<char*>(workspace);
   XentArgs r = {};
   r.targets = targets;
-  r.T = T, r.V = V, r.ignore = ignore_index, r.D = D;
+  r.T = T, r.V = V, r.D = D, r.ignore = ignore_index;
   r.lse = const_cast<float*>(lse);
   r.dloss = dloss, r.dlse = dlse, r.dloss_stride = dloss_stride, r.dlse_stride = dlse_stride;
+  r.x = x, r.ldx = ldx, r.dx = dx, r.lddx = lddx, r.bf16 = bf16;
   r.rows = reinterpret_cast<XentRow*>(ws + sp.rows);
-  r.scale = reinterpret_cast<float*>(ws + sp.scale);
+  r.scale = reinterpret_cast<float*>(ws + sp.scalars);
+  r.live = reinterpret_cast<int32_t*>(ws + sp.scalars) + 1;
+  r.order = reinterpret_cast<int32_t*>(ws + sp.order);
+  r.packed = ws + sp.packed;
   r.hold = bf16 ? 1.0f : 16384.0f;
-  if ((st = launch(h, xent_rows, dim3(1), dim3(1024), 0, 1, s, r)) != GEMM_OK) return st;
+  r.sum = reinterpret_cast<const float*>(ws + sp.sum);
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(cdiv(T, 4), 2 * h->num_sms));
+  if ((st = launch(h, xent_pack, dim3(blocks), dim3(kPackThreads), 0, 1, s, r)) != GEMM_OK) return st;
   void* dz = ws + sp.dz;
-  float* sum = reinterpret_cast<float*>(ws + sp.sum);
   const bool whole = sp.piece >= V;
-  const Stack xs = {x, T, D, ldx, 1, T * ldx};
+  // Laid out for all T tokens; r.live of them take part.
+  const Stack xs = {r.packed, T, D, D, 1, T * D};
   for (int64_t v0 = 0; v0 < V; v0 += sp.piece) {
     const int64_t n = std::min(sp.piece, V - v0);
-    const Stack ws_ = {static_cast<const uint16_t*>(w) + v0 * ldw, n, D, ldw, 1, n * ldw};
+    const Stack wv = {static_cast<const uint16_t*>(w) + v0 * ldw, n, D, ldw, 1, n * ldw};
     const Stack dzs = {dz, T, n, sp.pitch, 1, T * sp.pitch};
-    {  // dz, from the logits x W^T
-      const Product p = {T, n, D, xs, ws_, false, false, bf16, 1, 1};
+    {  // dz, from the logits x W^T: at least one tile, of zeros, for dW
+      const Product p = {T, n, D, xs, wv, false, false, bf16, 1, 1};
       FusedArgs a = base_args(h, p);
-      a.early = kEarlyA | kEarlyB;  // the kernels before wrote neither x nor W
+      a.early = v0 > 0 ? kEarlyA | kEarlyB | kEarlyLive : kEarlyB;
+      a.live = r.live;
+      a.live_min = 1;
       a.xent_rows = r.rows;
       a.col_base = static_cast<int32_t>(v0);
       if ((st = fused<kEpiXent>(h, p, a, dzs, {}, s)) != GEMM_OK) return st;
     }
-    // dW = dz^T x, whole for this piece
-    const Product pw = {n, D, T, dzs, xs, true, true, bf16, 1, 1};
-    const Stack out = {static_cast<uint16_t*>(dw) + v0 * D, n, D, D, 1, n * D};
-    if ((st = product(h, pw, out, kEarlyB, s, r.scale)) != GEMM_OK) return st;
+    {  // dW = dz^T x, whole for this piece
+      const Product p = {n, D, T, dzs, xs, true, true, bf16, 1, 1};
+      FusedArgs a = base_args(h, p);
+      a.early = kEarlyB | kEarlyLive;
+      a.live = r.live;
+      a.live_k = 1;
+      a.alpha_p = r.scale;
+      const Stack out = {static_cast<uint16_t*>(dw) + v0 * D, n, D, D, 1, n * D};
+      if ((st = fused<kEpiStoreLive>(h, p, a, out, {}, s)) != GEMM_OK) return st;
+    }
     // dx = dz W, or its sum over the pieces
-    const Product px = {T, D, n, dzs, ws_, false, true, bf16, 1, 1};
-    if (whole) return product(h, px, {dx, T, D, lddx, 1, T * lddx}, kEarlyA | kEarlyB, s, r.scale);
-    FusedArgs a = base_args(h, px);
-    a.early = kEarlyA | kEarlyB;
+    const Product p = {T, D, n, dzs, wv, false, true, bf16, 1, 1};
+    FusedArgs a = base_args(h, p);
+    a.early = kEarlyA | kEarlyB | kEarlyLive;
+    a.live = r.live;
+    if (whole) {
+      a.alpha_p = r.scale;
+      a.row_map = r.order;
+      return fused<kEpiStoreLive>(h, p, a, {dx, T, D, lddx, 1, T * lddx}, {}, s);
+    }
     a.add = v0 > 0;
-    if ((st = fused<kEpiSum>(h, px, a, {sum, T, D, D, 1, T * D}, {}, s)) != GEMM_OK) return st;
+    if ((st = fused<kEpiSum>(h, p, a, {r.sum, T, D, D, 1, T * D}, {}, s)) != GEMM_OK) return st;
   }
-  r.sum = sum;
-  r.dx = dx, r.lddx = lddx, r.bf16 = bf16;
-  const int64_t blocks = std::min<int64_t>(cdiv(T * (D / 8), 256), 8 * h->num_sms);
-  return launch(h, xent_dx, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, 1, s, r);
+  const int64_t ctas = std::min<int64_t>(cdiv(T * (D / 8), 256), 8 * h->num_sms);
+  return launch(h, xent_dx, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, 1, s, r);
 }
 
 }  // extern "C"

@@ -240,11 +240,12 @@ GEMM_API gemm_status_t gemm_linear_cross_entropy(gemm_ops_t ops, const void* x, 
  * The logits are computed again, a piece of the vocabulary at a time.  dz is rounded to
  * 16 bits as an operand, in fp16 scaled by a power of two so that entries down to 2^-40
  * of the largest |dloss| (|dloss + dlse|) of the call count.  A token whose dloss and
- * dlse are 0 (or which is ignored, without dlse) has dz = 0 and dx = 0.
+ * dlse are 0 (or which is ignored, without dlse) takes no part, whatever its x holds, and
+ * costs nothing: its dx is 0.
  * Gradients are written, not accumulated; T == 0 gives zero dw.  Rules as above.
  * workspace: gemm_linear_cross_entropy_backward_workspace(ops, T, D, V) bytes, 256-byte
- * aligned (up to about 512 MB of dz, from 2^16 tokens on 4096 columns of it, and fp32
- * sums of dx). */
+ * aligned (a copy of x, up to about 512 MB of dz, from 2^16 tokens on 4096 columns of
+ * it, and fp32 sums of dx). */
 GEMM_API size_t gemm_linear_cross_entropy_backward_workspace(gemm_ops_t ops, int64_t T, int64_t D, int64_t V);
 GEMM_API gemm_status_t gemm_linear_cross_entropy_backward(
     gemm_ops_t ops, const float* dloss, int64_t dloss_stride, const float* dlse, int64_t dlse_stride, const void* x,

@@ -204,6 +204,37 @@ def test_xent_empty_and_ignored(g, T):
     assert not dx.any() and not dw.any()
 
 
+@pytest.mark.parametrize("shape", [(5, 64, 700), (300, 136, 5000), (4000, 72, 40000), (9000, 64, 33000)])
+@pytest.mark.parametrize("kept", [0.0, 0.01, 0.3, 0.9])
+def test_xent_tokens_without_a_gradient_take_no_part(g, shape, kept):
+    """Ignored tokens' x may hold anything, and the others' gradients are those of a
+    batch of them alone."""
+    T = shape[0]
+    x, w, targets, dloss = make(*shape, torch.bfloat16, seed=4)
+    targets.clamp_min_(0)
+    gone = torch.rand(T, generator=torch.Generator().manual_seed(T)).cuda() >= kept
+    targets[gone] = -100
+    lse = torch.zeros(T, device="cuda")
+    if (~gone).any():
+        lse[~gone] = g.linear_cross_entropy(x[~gone], w, targets[~gone], save=True)[1]
+    bad = x.clone()
+    bad[gone] = float("nan")
+    lse[gone], dloss[gone] = float("nan"), float("inf")
+    dx, dw = g.linear_cross_entropy_backward(dloss, bad, w, targets, lse)
+    g.default_ops().check_error()
+    assert not dx[gone].any() and torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    if (~gone).any():
+        rx, rw = backward_ref(dloss[~gone], None, x[~gone], w, targets[~gone], lse[~gone], torch.bfloat16)
+        check(dx[~gone], *rx, "dx")
+        check(dw, *rw, "dw")
+    else:
+        assert not dw.any()
+    # A dloss of 0 is as good as an ignored token; a dlse takes part.
+    dloss[gone] = 0.0
+    dx2, dw2 = g.linear_cross_entropy_backward(dloss, bad, w, targets.clamp_min(0), lse)
+    assert torch.equal(dx2, dx) and torch.equal(dw2, dw)
+
+
 def test_xent_other_ignore_index_and_bad_targets(g):
     x, w, targets, dloss = make(40, 64, 500, torch.bfloat16, ignore=7)
     run(g, x, w, targets, dloss, ignore=7)
