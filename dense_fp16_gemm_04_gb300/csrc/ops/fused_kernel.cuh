@@ -139,10 +139,15 @@ struct FusedArgs {
 // m is infinite, s = sum exp(z).  Takes in kN more logits.
 template <int kN>
 __device__ __forceinline__ void lse_take(const float (&z)[kN], float& m, float& s) {
-  float top = z[0];
+  constexpr int kW = kN < 8 ? kN : 8;
+  float tops[kW];
 #pragma unroll
-  for (int i = 1; i < kN; ++i) top = fmaxf(top, z[i]);
-  top = fmaxf(m, top);  // NaN drops out here, and comes back through s
+  for (int i = 0; i < kW; ++i) tops[i] = z[i];
+#pragma unroll
+  for (int i = kW; i < kN; ++i) tops[i % kW] = fmaxf(tops[i % kW], z[i]);
+  float top = m;  // NaN drops out here, and comes back through s
+#pragma unroll
+  for (int i = 0; i < kW; ++i) top = fmaxf(top, tops[i]);
   const float ref = isinf(top) ? 0.0f : top;
   const float k = -ref * kLog2e;
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -199,7 +204,10 @@ struct FusedCfg {
   // Eight epilogue warps where few k-blocks make the epilogue the bound (weight
   // gradients of 1000 tokens: -5%); four where K is three times as long and the
   // power cap sets the speed (update of 4096 x 8192: eight cost 2%).
-  static constexpr int kEpiWarps = kEpi == kEpiSplit || kEpi == kEpiSplitSym ? 4 : 8;
+  // Sixteen for a pair's logits, of which each thread holds 64 in registers: with eight
+  // and 128 of them the epilogue was longer than the MMAs of D = 1032 (44 us for 1000 x
+  // 1032 x 20011, XXX).
+  static constexpr int kEpiWarps = kEpi == kEpiSplit || kEpi == kEpiSplitSym ? 4 : kEpi == kEpiLse && kCtas == 2 ? 16 : 8;
   static constexpr int kGroups = kEpiWarps / 4;  // warps per quarter of the rows
   static constexpr int kWarpB = kSplit > 1 ? 6 : 2;  // loads B
   static constexpr int kBufBytes = 32 * 128;
@@ -211,7 +219,7 @@ struct FusedCfg {
   static constexpr bool kFlex =
       kCtas == 1 && (kEpi == kEpiStore || kEpi == kEpiGlu || kEpi == kEpiLse || kEpi == kEpiXent ||
                      kEpi == kEpiStoreLive);
-  static constexpr int kMaxStages = kFlex ? 8 : kStages;
+  static constexpr int kMaxStages = !kFlex ? kStages : kEpi == kEpiLse ? 12 : 8;
   static constexpr int kNumBars = 2 * kMaxStages + 5;
   static constexpr int kOffSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffAbort = kOffSlot + 4;
@@ -913,6 +921,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const int32_t row = wi.mb * Cfg::kTileM + static_cast<int32_t>(cta) * Cfg::kBM + q * 32 + lane;
         const int32_t col0 = wi.nb * Cfg::kOutN + group * kCols;
         const bool row_in = row < args.M;
+        const bool idle = row - lane >= args.M || col0 >= args.N;  // of all 32 rows
         const int64_t target = row_in ? args.targets[row] - col0 : -1;
         float z[kCols];
 #pragma unroll
@@ -926,13 +935,15 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           ptx::tc_fence_after();
           const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                  static_cast<uint32_t>(buf * Cfg::kBN + group * kCols);
+          if (!idle) {
 #pragma unroll
-          for (int c = 0; c < kCols; c += 16) {
-            uint32_t v[16];
-            ptx::tmem_ld_32x32b_x16(t_row + c, v);
-            ptx::tmem_wait_ld(v);
+            for (int c = 0; c < kCols; c += 16) {
+              uint32_t v[16];
+              ptx::tmem_ld_32x32b_x16(t_row + c, v);
+              ptx::tmem_wait_ld(v);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) z[c + i] += __uint_as_float(v[i]);
+              for (int i = 0; i < 16; ++i) z[c + i] += __uint_as_float(v[i]);
+            }
           }
           ptx::tc_fence_before();
           __syncwarp();
@@ -956,7 +967,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           for (int i = 0; i < kCols; ++i) z[i] = col0 + i < args.N ? z[i] : -INFINITY;
         }
         float share_m = -INFINITY, share_s = 0.0f;
-        lse_take<kCols>(z, share_m, share_s);
+        if (!idle) lse_take<kCols>(z, share_m, share_s);
         if (row_in)
           args.shares[(static_cast<int64_t>(wi.nb) * Cfg::kGroups + group) * args.M + row] =
               make_float2(share_m, share_s);

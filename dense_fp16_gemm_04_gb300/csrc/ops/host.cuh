@@ -45,11 +45,14 @@ constexpr int epi_bufs(int epi) { return epi == kEpiSplit || epi == kEpiSplitSym
 // Tile configurations: a pair of CTAs on 256 x 256 sums, or one CTA on
 // 128 x 128 for problems of few tiles.
 template <int kEpi>
-using Pair = FusedCfg<2, 256, kEpi == kEpiStore ? 6 : 5, kEpi, kEpi == kEpiStore ? 1 : epi_bufs(kEpi)>;
+using Pair = FusedCfg<2, 256, kEpi == kEpiLse ? 7 : kEpi == kEpiStore ? 6 : 5, kEpi,
+                      kEpi == kEpiLse ? 0 : kEpi == kEpiStore ? 1 : epi_bufs(kEpi)>;
 template <int kEpi>
 using TwoPairs = FusedCfg<2, 256, 5, kEpi, epi_bufs(kEpi), 2>;  // one tile, half of its k-blocks each
 template <int kEpi, int kSplit = 1, int kParts = 1>
-using Lone = FusedCfg<1, 128, 5, kEpi, epi_bufs(kEpi), kSplit, kEpi == kEpiLse && (kSplit > 1) ? 4 : kParts>;
+using Lone = FusedCfg<1, 128, kEpi == kEpiLse && kSplit == 1 ? 7 : 5, kEpi,
+                      kEpi == kEpiLse && kSplit == 1 ? 0 : epi_bufs(kEpi), kSplit,
+                      kEpi == kEpiLse && (kSplit > 1) ? 4 : kParts>;
 
 struct DeviceGuard {
   int prev = -1;
@@ -269,7 +272,7 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
   a.ldd = d.pitch;
   a.d_up = d.zstride;
   a.d = static_cast<uint16_t*>(const_cast<void*>(d.p));
-  if (shares) *shares = tn * Cfg::kSplit * 2;  // kEpiLse: two groups of a tile's warps, or halves of a CTA's columns
+  if (shares) *shares = tn * (Cfg::kSplit > 1 ? 2 * Cfg::kSplit : Cfg::kGroups);  // kEpiLse
   const int64_t fit = Cfg::kCtas == 2 ? h->max_pairs : h->num_sms;
   const int64_t units = Cfg::kSplit > 1 ? items : std::min<int64_t>(items, fit);
   return launch(h, fused_kernel<Cfg>, dim3(static_cast<unsigned>(units * Cfg::kCluster)), dim3(Cfg::kThreads),

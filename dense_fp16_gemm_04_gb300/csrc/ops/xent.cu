@@ -41,9 +41,9 @@ gemm_status_t check_xent(const gemm_ops_s* h, int64_t T, int64_t D, int64_t V, g
   return D % 8 != 0 ? GEMM_ERR_ALIGNMENT : GEMM_OK;
 }
 
-// The most shares that any form leaves: two of a tile of 128 or 256 columns, or
+// The most shares that any form leaves: one of 64 columns, four of a pair's tile, or
 // sixteen of one of at most 76 tiles that a cluster shares.
-int64_t most_shares(int64_t V) { return std::max<int64_t>(2 * cdiv(V, 128), std::min<int64_t>(16 * cdiv(V, 128), 16 * 76)); }
+int64_t most_shares(int64_t V) { return std::max<int64_t>(4 * cdiv(V, 256), std::min<int64_t>(16 * cdiv(V, 128), 16 * 76)); }
 
 size_t target_bytes(int64_t T) { return up(std::min(T, kLseTokens) * 4, 256); }
 
@@ -123,8 +123,8 @@ gemm_status_t gemm_linear_cross_entropy(gemm_ops_t h, const void* x, int64_t ldx
     j.T = n, j.V = V, j.ignore = ignore_index;
     j.shares = shares, j.num_shares = num, j.target_z = target_z;
     j.loss = loss + t0, j.lse = lse ? lse + t0 : nullptr;
-    int32_t per = 1;
-    while (per < 32 && per < n) per *= 2;
+    int32_t per = 1;  // a block's tokens: 32 bytes of their shares at least, where there are as many
+    while (per < 32 && per < n && (per < 4 || n / per > 2 * h->num_sms)) per *= 2;
     st = launch(h, xent_join, dim3(static_cast<unsigned>(cdiv(n, per))), dim3(kJoinThreads), 0, 1, s, j, per);
     if (st != GEMM_OK) return st;
   }

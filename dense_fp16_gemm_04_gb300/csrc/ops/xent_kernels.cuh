@@ -66,7 +66,15 @@ __global__ void __launch_bounds__(kJoinThreads) xent_join(const XentArgs a, int3
   const int64_t t = static_cast<int64_t>(blockIdx.x) * per + at;
   float2 v = make_float2(-INFINITY, 0.0f);
   if (t < a.T)
-    for (int64_t i = group; i < a.num_shares; i += groups) v = lse_join(v, a.shares[i * a.T + t]);
+    for (int64_t i = group; i < a.num_shares; i += 4 * groups) {
+      float2 w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t j = i + k * groups;
+        w[k] = j < a.num_shares ? a.shares[j * a.T + t] : make_float2(-INFINITY, 0.0f);
+      }
+      v = lse_join(v, lse_join(lse_join(w[0], w[1]), lse_join(w[2], w[3])));
+    }
   sm[threadIdx.x] = v;
   for (int n = groups / 2; n > 0; n /= 2) {
     __syncthreads();
@@ -96,12 +104,13 @@ __global__ void __launch_bounds__(kPackThreads) xent_pack(const XentArgs a) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // a, b and the target of token t.
+  // a, b and the target of token t, from loads that wait for none of one another.
   auto row = [&](int64_t t) {
     const int64_t target = a.targets[t];
+    const float dloss = a.dloss[t * a.dloss_stride], dlse = a.dlse ? a.dlse[t * a.dlse_stride] : 0.0f;
     XentRow r;
-    r.b = target != a.ignore ? a.dloss[t * a.dloss_stride] : 0.0f;
-    r.a = a.dlse ? r.b + a.dlse[t * a.dlse_stride] : r.b;
+    r.b = target != a.ignore ? dloss : 0.0f;
+    r.a = a.dlse ? r.b + dlse : r.b;
     r.target = -1;
     if (target != a.ignore) {
       if (target >= 0 && target < a.V)
@@ -109,13 +118,16 @@ __global__ void __launch_bounds__(kPackThreads) xent_pack(const XentArgs a) {
       else
         r.a = NAN;  // as the loss
     }
-    r.lse2 = 0.0f;
+    r.lse2 = a.lse[t] * kLog2e;
     return r;
   };
   auto has = [](const XentRow& r) { return !(r.a == 0.0f && r.b == 0.0f); };  // (NaN has)
   const int64_t c0 = a.T * blockIdx.x / gridDim.x, c1 = a.T * (blockIdx.x + 1) / gridDim.x;
+  XentRow mine = {};  // this block's tokens are on their way while it looks at all
+  if (c0 + threadIdx.x < c1) mine = row(c0 + threadIdx.x);
   float top = 0.0f;
   int32_t count = 0, before = 0;
+#pragma unroll 2
   for (int64_t t = threadIdx.x; t < a.T; t += kPackThreads) {
     const XentRow r = row(t);
     if (isfinite(r.a)) top = fmaxf(top, fabsf(r.a));
@@ -139,8 +151,8 @@ __global__ void __launch_bounds__(kPackThreads) xent_pack(const XentArgs a) {
   uint16_t *packed = static_cast<uint16_t*>(a.packed), *dx = static_cast<uint16_t*>(a.dx);
   for (int64_t t0 = c0; t0 < c1; t0 += kPackThreads) {
     const int64_t t = t0 + threadIdx.x;
-    XentRow r = {};
-    if (t < c1) r = row(t);
+    XentRow r = mine;
+    if (t0 > c0 && t < c1) r = row(t);
     const bool own = t < c1 && has(r);
     const uint32_t votes = __ballot_sync(0xffffffffu, own);
     __syncthreads();  // counts and place are read
@@ -155,7 +167,6 @@ __global__ void __launch_bounds__(kPackThreads) xent_pack(const XentArgs a) {
     if (own) {
       r.a *= up;
       r.b *= up;
-      r.lse2 = a.lse[t] * kLog2e;
       a.rows[at] = r;
       a.order[at] = static_cast<int32_t>(t);
     }
