@@ -123,6 +123,7 @@ struct FusedArgs {
   // at least live_min tiles of rows.  row_map: where a row of C goes (null: in place).
   const int32_t *live, *row_map;
   int32_t live_k, live_min;
+  int32_t k_slices;           // kEpiSum: the batch is of so many shares of the k-blocks (0: no such batch)
   // kEpiLse: targets [M], their logits [M] and the shares' (maximum, sum) [share][M].
   const int64_t* targets;
   float* target_z;
@@ -217,7 +218,7 @@ struct FusedCfg {
   static constexpr int kOffBar = kOffEpi + kEpiWarps * kEpiBufs * kBufBytes;
   // Few rows leave room for more k-blocks: their number is the launch's.
   static constexpr bool kFlex =
-      kCtas == 1 && (kEpi == kEpiStore || kEpi == kEpiGlu || kEpi == kEpiLse || kEpi == kEpiXent ||
+      kCtas == 1 && (kEpi == kEpiStore || kEpi == kEpiGlu || kEpi == kEpiLse || kEpi == kEpiXent || kEpi == kEpiSum ||
                      kEpi == kEpiStoreLive);
   static constexpr int kMaxStages = !kFlex ? kStages : kEpi == kEpiLse ? 12 : 8;
   static constexpr int kNumBars = 2 * kMaxStages + 5;
@@ -273,7 +274,8 @@ __device__ __forceinline__ FusedDims fused_dims(const FusedArgs& a) {
       } else {
         d.rows = n;
         d.tiles_m = max(a.live_min, (n + Cfg::kTileM - 1) / Cfg::kTileM);
-        d.items = d.per_batch = d.tiles_m * a.tiles_n;
+        d.per_batch = d.tiles_m * a.tiles_n;
+        d.items = d.per_batch * max(1, a.k_slices);
       }
     }
   }
@@ -288,6 +290,10 @@ __device__ __forceinline__ FusedItem fused_item(const FusedArgs& a, const FusedD
   w.kb1 = Cfg::kSplit > 1 ? (rank + 1) * total / Cfg::kSplit : total;
   w.batch = t / d.per_batch;
   const int32_t r = t - w.batch * d.per_batch;
+  if (Cfg::kEpi == kEpiSum && a.k_slices > 0) {
+    w.kb0 = static_cast<int32_t>(static_cast<int64_t>(w.batch) * total / a.k_slices);
+    w.kb1 = static_cast<int32_t>(static_cast<int64_t>(w.batch + 1) * total / a.k_slices);
+  }
   if constexpr (Cfg::kSym) {
     // Triangle r: column nb holds rows 0 .. nb.
     int32_t j = static_cast<int32_t>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
@@ -341,6 +347,21 @@ __device__ __forceinline__ void finish_columns(const FusedArgs& args, const Fuse
       uint32_t p[kG / 2];
 #pragma unroll
       for (int j = 0; j < kG / 2; ++j) p[j] = pack16(bf16, alpha * v[i + 2 * j], alpha * v[i + 2 * j + 1]);
+      if (col0 + i < args.N) store16<kG>(c + i, p);
+    }
+  } else if constexpr (Cfg::kEpi == kEpiXent) {
+    uint16_t* c = args.c + static_cast<int64_t>(row) * args.ldc + col0;
+    float w[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) w[i] = v[i];
+    XentRow r = {};  // behind the last row: zeros, up to a whole k-block of the next product
+    if (row < *args.live) r = args.xent_rows[row];
+    xent_columns<kN>(r, args.col_base + col0, w);
+#pragma unroll
+    for (int i = 0; i < kN; i += kG) {
+      uint32_t p[kG / 2];
+#pragma unroll
+      for (int j = 0; j < kG / 2; ++j) p[j] = pack16(bf16, w[i + 2 * j], w[i + 2 * j + 1]);
       if (col0 + i < args.N) store16<kG>(c + i, p);
     }
   } else if constexpr (Cfg::kEpi == kEpiLse) {
@@ -399,6 +420,7 @@ __device__ __forceinline__ void finish_columns(const FusedArgs& args, const Fuse
       store16<kG>(d + args.d_up + i, du);
     }
   } else {
+    static_assert(Cfg::kEpi == kEpiSplit || Cfg::kEpi == kEpiSplitSym, "no other epilogue splits a tile");
     uint16_t* base = args.c + wi.batch * args.c_zb * args.c_z;
     uint16_t* c = base + static_cast<int64_t>(row) * args.ldc + col0;
 #pragma unroll
@@ -522,7 +544,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, const Fuse
   const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
   const int32_t row = wi.mb * Cfg::kBM + r;
   const int32_t col0 = wi.nb * Cfg::kOutN + rank * (Cfg::kOutN / kS) + half * kN;
-  const bool in = row < dims.rows && (col0 < args.N || Cfg::kEpi == kEpiLse);  // (every share is written)
+  const bool in = row < (Cfg::kEpi == kEpiXent ? args.M : dims.rows) && (col0 < args.N || Cfg::kEpi == kEpiLse);  // (every share is written)
   uint4 s0[Cfg::kReads ? kN / 8 : 1], s1[Cfg::kReads ? kN / 8 : 1];
   if (in) read_columns<Cfg, kN>(args, wi, row, col0, s0, s1);
   ptx::cluster_sync();
@@ -1079,7 +1101,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             ptx::tmem_ld_32x32b_x32(t_row + c * 64 + half * 32, v);
             ptx::tmem_wait_ld(v);
             if (half == 1 && last) release_tmem();
-            store_chunk(&tmC, v, col0 + half * 32, row0, 0, in && col0 + half * 32 < args.N);
+            store_chunk(&tmC, v, col0 + half * 32, row0, wi.batch * args.c_zb, in && col0 + half * 32 < args.N);
           }
         } else if constexpr (Cfg::kEpi == kEpiGlu) {
           uint32_t h[32], gp[32], up[32];

@@ -292,9 +292,9 @@ template <int kEpi>
 gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const Stack& c,
                     const Stack& d, cudaStream_t stream, int64_t* shares = nullptr) {
   constexpr bool kBatched = kEpi == kEpiSplit || kEpi == kEpiSplitSym;
-  // The loss's logits and sums over pieces have many tiles; a k-range of fewer
+  // The loss's sums have tiles enough, or shares of the k-blocks; a k-range of fewer
   // k-blocks than it was laid out for could be empty.
-  constexpr bool kSplits = kEpi != kEpiSum && kEpi != kEpiXent, kTwos = kSplits && kEpi != kEpiLse;
+  constexpr bool kSplits = kEpi != kEpiSum, kTwos = kSplits && kEpi != kEpiLse && kEpi != kEpiXent;
   const bool split = kSplits && !(Pair<kEpi>::kLive && a.live_k);
   auto tiles = [&](int64_t tm, int64_t tn) { return Pair<kEpi>::kSym ? tn * (tn + 1) / 2 : tm * tn; };
   const int64_t n = kBatched ? 1 : p.batch, kb = cdiv(p.K, 64) * p.segs;

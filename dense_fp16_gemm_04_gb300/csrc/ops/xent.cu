@@ -8,7 +8,8 @@ namespace ops {
 bool xent_setup(gemm_ops_s* h) {
   if (!set_attr<Pair<kEpiLse>>() || !set_attr<Lone<kEpiLse>>() || !set_attr<Lone<kEpiLse, 2>>() ||
       !set_attr<Lone<kEpiLse, 4>>() || !set_attr<Lone<kEpiLse, 8>>() || !set_attr<Pair<kEpiXent>>() ||
-      !set_attr<Lone<kEpiXent>>() || !set_attr<Pair<kEpiSum>>() || !set_attr<Lone<kEpiSum>>() ||
+      !set_attr<Lone<kEpiXent>>() || !set_attr<Lone<kEpiXent, 2>>() || !set_attr<Lone<kEpiXent, 4>>() ||
+      !set_attr<Lone<kEpiXent, 8>>() || !set_attr<Pair<kEpiSum>>() || !set_attr<Lone<kEpiSum>>() ||
       !set_attr<Pair<kEpiStoreLive>>() || !set_attr<TwoPairs<kEpiStoreLive>>() || !set_attr<Lone<kEpiStoreLive>>() ||
       !set_attr<Lone<kEpiStoreLive, 2>>() || !set_attr<Lone<kEpiStoreLive, 4>>() || !set_attr<Lone<kEpiStoreLive, 8>>())
     return false;
@@ -53,11 +54,22 @@ int64_t piece_columns(int64_t T, int64_t V) {
   return V <= most ? V : up(cdiv(V, cdiv(V, most)), 256);
 }
 
+// Shares of the k-blocks (64 entries of the vocabulary) that CTAs sum on their own for
+// dx of few tiles, 0 where a cluster's four or two are as good (27 x k-blocks + 550 of
+// the model in host.cuh, 400 more for adding the shares up): 4 x 1288 x 66557, XXX.
+int64_t dx_slices(const gemm_ops_s* h, int64_t T, int64_t D, int64_t V) {
+  const int64_t tiles = cdiv(T, 128) * cdiv(D, 128), kb = cdiv(V, 64);
+  const int64_t slices = std::min(h->num_sms / tiles, kb / 8);
+  if (slices < 2) return 0;
+  const int64_t cluster = 27 * cdiv(kb, tiles <= 36 ? 4 : 2) + 550;
+  return 27 * cdiv(kb, slices) + 800 < cluster ? slices : 0;
+}
+
 struct XentSpace {
-  int64_t piece, pitch;
+  int64_t piece, pitch, slices;
   size_t rows, scalars, order, packed, dz, sum, total;
 };
-XentSpace xent_space(int64_t T, int64_t D, int64_t V) {
+XentSpace xent_space(const gemm_ops_s* h, int64_t T, int64_t D, int64_t V) {
   XentSpace s;
   s.piece = piece_columns(T, V);
   s.pitch = up(s.piece, 64);
@@ -67,7 +79,9 @@ XentSpace xent_space(int64_t T, int64_t D, int64_t V) {
   s.packed = s.order + up(T * 4, 256);
   s.dz = s.packed + up(T * D * 2, 256);
   s.sum = s.dz + up(T * s.pitch * 2, 256);
-  s.total = s.sum + (s.piece < V ? up(T * D * 4, 256) : 0);  // several pieces: fp32 sums of dx
+  // Several pieces, or shares of one: fp32 sums of dx.
+  s.slices = s.piece < V ? 1 : dx_slices(h, T, D, V);
+  s.total = s.sum + up(s.slices * T * D * 4, 256);
   return s;
 }
 
@@ -133,7 +147,7 @@ gemm_status_t gemm_linear_cross_entropy(gemm_ops_t h, const void* x, int64_t ldx
 
 size_t gemm_linear_cross_entropy_backward_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t V) {
   if (!h || T <= 0 || !xent_dims_ok(T, D, V)) return 0;
-  return xent_space(T, D, V).total;
+  return xent_space(h, T, D, V).total;
 }
 
 gemm_status_t gemm_linear_cross_entropy_backward(gemm_ops_t h, const float* dloss, int64_t dloss_stride,
@@ -170,7 +184,7 @@ gemm_status_t gemm_linear_cross_entropy_backward(gemm_ops_t h, const float* dlos
   if (T == 0)  // no token, no gradient
     return cudaMemsetAsync(dw, 0, V * D * 2, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
   const bool bf16 = dtype == GEMM_BF16;
-  const XentSpace sp = xent_space(T, D, V);
+  const XentSpace sp = xent_space(h, T, D, V);
   char* ws = static_cast<char*>(workspace);
   XentArgs r = {};
   r.targets = targets;
@@ -185,6 +199,7 @@ gemm_status_t gemm_linear_cross_entropy_backward(gemm_ops_t h, const float* dlos
   r.packed = ws + sp.packed;
   r.hold = bf16 ? 1.0f : 16384.0f;
   r.sum = reinterpret_cast<const float*>(ws + sp.sum);
+  r.slices = sp.slices;
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(cdiv(T, 4), 2 * h->num_sms));
   if ((st = launch(h, xent_pack, dim3(blocks), dim3(kPackThreads), 0, 1, s, r)) != GEMM_OK) return st;
   void* dz = ws + sp.dz;
@@ -205,29 +220,36 @@ gemm_status_t gemm_linear_cross_entropy_backward(gemm_ops_t h, const float* dlos
       a.col_base = static_cast<int32_t>(v0);
       if ((st = fused<kEpiXent>(h, p, a, dzs, {}, s)) != GEMM_OK) return st;
     }
-    {  // dW = dz^T x, whole for this piece
-      const Product p = {n, D, T, dzs, xs, true, true, bf16, 1, 1};
+    {  // dx = dz W, right after dz, while W is in L2; or its sums over the pieces, or shares
+      const Product p = {T, D, n, dzs, wv, false, true, bf16, std::max<int64_t>(1, whole ? sp.slices : 1), 1};
       FusedArgs a = base_args(h, p);
       a.early = kEarlyB | kEarlyLive;
       a.live = r.live;
-      a.live_k = 1;
-      a.alpha_p = r.scale;
-      const Stack out = {static_cast<uint16_t*>(dw) + v0 * D, n, D, D, 1, n * D};
-      if ((st = fused<kEpiStoreLive>(h, p, a, out, {}, s)) != GEMM_OK) return st;
+      if (sp.slices == 0) {
+        a.alpha_p = r.scale;
+        a.row_map = r.order;
+        st = fused<kEpiStoreLive>(h, p, a, {dx, T, D, lddx, 1, T * lddx}, {}, s);
+      } else if (whole) {
+        a.k_slices = static_cast<int32_t>(sp.slices);
+        a.c_zb = 1;
+        st = launch_fused<Lone<kEpiSum>>(h, p, a, {r.sum, T, D, D, sp.slices, T * D}, {}, s);
+      } else {
+        a.add = v0 > 0;
+        st = fused<kEpiSum>(h, p, a, {r.sum, T, D, D, 1, T * D}, {}, s);
+      }
+      if (st != GEMM_OK) return st;
     }
-    // dx = dz W, or its sum over the pieces
-    const Product p = {T, D, n, dzs, wv, false, true, bf16, 1, 1};
+    // dW = dz^T x, whole for this piece
+    const Product p = {n, D, T, dzs, xs, true, true, bf16, 1, 1};
     FusedArgs a = base_args(h, p);
     a.early = kEarlyA | kEarlyB | kEarlyLive;
     a.live = r.live;
-    if (whole) {
-      a.alpha_p = r.scale;
-      a.row_map = r.order;
-      return fused<kEpiStoreLive>(h, p, a, {dx, T, D, lddx, 1, T * lddx}, {}, s);
-    }
-    a.add = v0 > 0;
-    if ((st = fused<kEpiSum>(h, p, a, {r.sum, T, D, D, 1, T * D}, {}, s)) != GEMM_OK) return st;
+    a.live_k = 1;
+    a.alpha_p = r.scale;
+    const Stack out = {static_cast<uint16_t*>(dw) + v0 * D, n, D, D, 1, n * D};
+    if ((st = fused<kEpiStoreLive>(h, p, a, out, {}, s)) != GEMM_OK) return st;
   }
+  if (sp.slices == 0) return GEMM_OK;
   const int64_t ctas = std::min<int64_t>(cdiv(T * (D / 8), 256), 8 * h->num_sms);
   return launch(h, xent_dx, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, 1, s, r);
 }

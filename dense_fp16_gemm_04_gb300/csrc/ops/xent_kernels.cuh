@@ -42,8 +42,9 @@ struct XentArgs {
   void* packed;    // their x, [T][D]; zeros up to a whole k-block of 64
   float* scale;    // what the products are to be multiplied by
   float hold;      // dz is held times hold / 2^e
-  // The sums of dx, [T][D], and dx itself.
+  // The sums of dx, [slices][T][D] to be added up in order, and dx itself.
   const float* sum;
+  int64_t slices;
   void* dx;
   int64_t ldx, lddx, D;
   int32_t bf16;
@@ -171,16 +172,22 @@ __global__ void __launch_bounds__(kPackThreads) xent_pack(const XentArgs a) {
       a.order[at] = static_cast<int32_t>(t);
     }
     __syncthreads();
-    for (int i = warp; i < kPackThreads && t0 + i < c1; i += kWarps) {
-      const int32_t to = place[i];
-      const uint16_t* from = x + (t0 + i) * a.ldx;
-      uint16_t* dst = to >= 0 ? packed + to * a.D : dx + (t0 + i) * a.lddx;
-#pragma unroll 4
-      for (int64_t c = lane * 8; c < a.D; c += 256) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (to >= 0) v = ptx::ld_global_v4_u32(from + c);
-        ptx::st_global_v4(dst + c, v.x, v.y, v.z, v.w);
+    // The warps take pieces of up to 4 x 256 columns of the rows in turn.
+    const int64_t pieces = (a.D + 1023) / 1024, all = pieces * min(c1 - t0, static_cast<int64_t>(kPackThreads));
+    for (int64_t i = warp; i < all; i += kWarps) {
+      const int64_t k = i / pieces, c = (i - k * pieces) * 1024 + lane * 8;
+      const int32_t to = place[k];
+      const uint16_t* from = x + (t0 + k) * a.ldx;
+      uint16_t* dst = to >= 0 ? packed + to * a.D : dx + (t0 + k) * a.lddx;
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (to >= 0 && c + j * 256 < a.D) v[j] = ptx::ld_global_v4_u32(from + c + j * 256);
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j * 256 < a.D) ptx::st_global_v4(dst + c + j * 256, v[j].x, v[j].y, v[j].z, v[j].w);
     }
   }
   if (blockIdx.x + 1 == gridDim.x) {
@@ -204,7 +211,14 @@ __global__ void __launch_bounds__(256) xent_dx(const XentArgs a) {
   const int64_t per = a.D / 8, n = *a.live * per, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
     const int64_t t = i / per, c = (i - t * per) * 8;
-    const float4 u = ptx::ld_global_cg_v4(a.sum + t * a.D + c), v = ptx::ld_global_cg_v4(a.sum + t * a.D + c + 4);
+    float4 u = make_float4(0, 0, 0, 0), v = u;
+#pragma unroll 4
+    for (int64_t k = 0; k < a.slices; ++k) {
+      const float* p = a.sum + (k * a.T + t) * a.D + c;
+      const float4 p0 = ptx::ld_global_cg_v4(p), p1 = ptx::ld_global_cg_v4(p + 4);
+      u.x += p0.x, u.y += p0.y, u.z += p0.z, u.w += p0.w;
+      v.x += p1.x, v.y += p1.y, v.z += p1.z, v.w += p1.w;
+    }
     ptx::st_global_v4(static_cast<uint16_t*>(a.dx) + a.order[t] * a.lddx + c, pack16(bf16, u.x * scale, u.y * scale),
                       pack16(bf16, u.z * scale, u.w * scale), pack16(bf16, v.x * scale, v.y * scale),
                       pack16(bf16, v.z * scale, v.w * scale));
