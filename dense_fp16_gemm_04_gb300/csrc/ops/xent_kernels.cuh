@@ -57,13 +57,14 @@ __device__ __forceinline__ float2 lse_join(float2 a, float2 b) {
 
 constexpr int kJoinThreads = 512;
 
-// A block joins the shares of `per` tokens (a power of two up to 32), thread p per
-// + t every (512 / per)-th share of token t from p on; then in pairs.
+// A block joins the shares of `per` tokens (a power of two up to 32): thread at + per
+// group every (512 / per)-th share of token `at` from `group` on; then a warp's lanes
+// of a token in pairs, and the warps in order.
 __global__ void __launch_bounds__(kJoinThreads) xent_join(const XentArgs a, int32_t per) {
   __shared__ float2 sm[kJoinThreads];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int groups = kJoinThreads / per, at = threadIdx.x % per, group = threadIdx.x / per;
+  const int groups = kJoinThreads / per, at = threadIdx.x % per, group = threadIdx.x / per, warp = threadIdx.x / 32;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * per + at;
   float2 v = make_float2(-INFINITY, 0.0f);
   if (t < a.T)
@@ -76,13 +77,13 @@ __global__ void __launch_bounds__(kJoinThreads) xent_join(const XentArgs a, int3
       }
       v = lse_join(v, lse_join(lse_join(w[0], w[1]), lse_join(w[2], w[3])));
     }
-  sm[threadIdx.x] = v;
-  for (int n = groups / 2; n > 0; n /= 2) {
-    __syncthreads();
-    if (group < n) sm[threadIdx.x] = lse_join(sm[threadIdx.x], sm[threadIdx.x + n * per]);
-  }
+  for (int d = 16; d >= per; d >>= 1)
+    v = lse_join(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d)));
+  if ((threadIdx.x & 31) < per) sm[warp * per + at] = v;
+  __syncthreads();
   if (group == 0 && t < a.T) {
     v = sm[at];
+    for (int i = 1; i < kJoinThreads / 32; ++i) v = lse_join(v, sm[i * per + at]);
     const float lse = (isinf(v.x) ? 0.0f : v.x) + logf(v.y);
     const int64_t target = a.targets[t];
     // A target outside the vocabulary has no logit: NaN.
