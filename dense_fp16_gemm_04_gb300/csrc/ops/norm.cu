@@ -16,6 +16,8 @@ gemm_status_t with_types(gemm_dtype_t dtype, gemm_dtype_t wtype, F f) {
   }
 }
 
+constexpr int kBackSmem = 200 * 1024;  // the largest ring of norm_rows_back: 192 KB
+
 int64_t bytes_of(gemm_dtype_t t) { return t == GEMM_F32 ? 4 : 2; }
 
 gemm_status_t check_norm(const gemm_ops_s* h, int64_t T, int64_t D, gemm_dtype_t dtype, gemm_dtype_t wtype) {
@@ -37,15 +39,30 @@ bool vectors(int64_t D, int64_t e, std::initializer_list<std::pair<const void*, 
   return ok;
 }
 
-// Blocks of a kernel that fit on the device at once.
+// Blocks of a kernel that fit on an SM at once (the SMs of every device this library
+// runs on are alike); asked once, since the question takes longer than a launch.
 template <class K>
-int64_t resident(const gemm_ops_s* h, K kernel, int threads, size_t smem) {
+int per_sm(K kernel, int threads) {
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess) {
     cudaGetLastError();
     n = 1;
   }
-  return static_cast<int64_t>(std::max(1, n)) * h->num_sms;
+  return std::max(1, n);
+}
+
+// Allows a kernel kBackSmem bytes of shared memory, once on each device (`done`: a bit
+// for each of the first 64).
+template <class K>
+bool allow_smem(const gemm_ops_s* h, K kernel, std::atomic<uint64_t>& done) {
+  const uint64_t bit = h->device < 64 ? 1ull << h->device : 0;
+  if (done.load() & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBackSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  done |= bit;
+  return true;
 }
 
 template <int kV>
@@ -98,8 +115,8 @@ gemm_status_t norm(gemm_ops_s* h, const void* x, int64_t ldx, const void* weight
     gemm_status_t st = GEMM_OK;
     auto rows = [&](auto vec, auto team, auto per, auto teams) {
       auto kernel = norm_rows<X, W, kRms, vec, team, per, teams>;
-      static const int64_t fit = resident(h, kernel, team * teams, 0);
-      const int64_t blocks = std::min(cdiv(T, teams), fit);
+      static const int fit = per_sm(kernel, team * teams);
+      const int64_t blocks = std::min<int64_t>(cdiv(T, teams), fit * h->num_sms);
       st = launch(h, kernel, dim3(static_cast<unsigned>(blocks)), dim3(team * teams), 0, 1, s, a);
       return true;
     };
@@ -119,7 +136,6 @@ int64_t row_chunks(const gemm_ops_s* h, int64_t T, int64_t D) {
 // Blocks of norm_rows_back, of `teams` teams: four to an SM (kBackThreads threads
 // in all), each with a few rows for its one row of sums.
 constexpr int kBackThreads = 512;
-constexpr int kBackSmem = 200 * 1024;
 int64_t back_blocks(const gemm_ops_s* h, int64_t T, int team, int teams) {
   return std::max<int64_t>(1, std::min<int64_t>(cdiv(T, 2 * teams), h->num_sms * std::max(1, kBackThreads / (team * teams))));
 }
@@ -180,9 +196,9 @@ gemm_status_t norm_backward(gemm_ops_s* h, const void* dy, int64_t lddy, const v
         st = launch(h, norm_rows_back_single<X, W, kRms, team, per, teams>, grid, block, sums_bytes, 1, s, a);
       } else {
         auto kernel = norm_rows_back<X, W, kRms, vec, team, per, teams>;
-        static const bool set =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBackSmem) == cudaSuccess;
-        st = set ? launch(h, kernel, grid, block, std::max(back_ring<per>(team * teams), sums_bytes), 1, s, a)
+        static std::atomic<uint64_t> allowed{0};
+        st = allow_smem(h, kernel, allowed)
+                 ? launch(h, kernel, grid, block, std::max(back_ring<per>(team * teams), sums_bytes), 1, s, a)
                  : GEMM_ERR_CUDA;
       }
       return true;
