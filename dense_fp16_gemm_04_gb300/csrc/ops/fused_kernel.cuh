@@ -192,8 +192,10 @@ struct FusedCfg {
   // (of a split cluster: in kParts accumulators, added up as they are sent).  The
   // tensor cores truncate a sum at each of its K / 16 steps, always towards zero:
   // the loss of one token over 4096 products was off by 9e-6 of itself, of which
-  // 16 steps at a time leave 5e-7 (4096 tokens x 4096 x 131072: 2545 -> 2577 us).
-  static constexpr bool kPartial = kEpi == kEpiLse;
+  // 16 steps at a time leave 5e-7 (4096 tokens x 4096 x 131072: 2545 -> 2577 us).  The
+  // backward pass's logits the same: exp(z - lse) - 1 of a token that the model is sure of
+  // is the difference of two numbers whose errors then agree.
+  static constexpr bool kPartial = kEpi == kEpiLse || kEpi == kEpiXent;
   static constexpr bool kLive = kEpi == kEpiXent || kEpi == kEpiSum || kEpi == kEpiStoreLive;
   static constexpr bool kReads = kEpi == kEpiGluBwd || kEpi == kEpiSplit || kSym;  // the epilogue reads too
   static constexpr int kOutN = kGlu ? kBN / 2 : kBN;  // output columns per tile
@@ -205,10 +207,9 @@ struct FusedCfg {
   // Eight epilogue warps where few k-blocks make the epilogue the bound (weight
   // gradients of 1000 tokens: -5%); four where K is three times as long and the
   // power cap sets the speed (update of 4096 x 8192: eight cost 2%).
-  // Sixteen for a pair's logits, of which each thread holds 64 in registers: with eight
-  // and 128 of them the epilogue was longer than the MMAs of D = 1032 (44 us for 1000 x
-  // 1032 x 20011, XXX).
-  static constexpr int kEpiWarps = kEpi == kEpiSplit || kEpi == kEpiSplitSym ? 4 : kEpi == kEpiLse && kCtas == 2 ? 16 : 8;
+  // Sixteen for a pair's logits, of which each thread holds 64 in registers (eight, 128 of
+  // them: 4096 x 4096 x 131072 2577 us, 2531 with sixteen).
+  static constexpr int kEpiWarps = kEpi == kEpiSplit || kEpi == kEpiSplitSym ? 4 : kPartial && kCtas == 2 ? 16 : 8;
   static constexpr int kGroups = kEpiWarps / 4;  // warps per quarter of the rows
   static constexpr int kWarpB = kSplit > 1 ? 6 : 2;  // loads B
   static constexpr int kBufBytes = 32 * 128;
@@ -940,11 +941,18 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       bool ok = true;
       for (int32_t it = unit; ok && it < dims.items; it += units) {
         const FusedItem wi = fused_item<Cfg>(args, dims, it, rank);
-        const int32_t row = wi.mb * Cfg::kTileM + static_cast<int32_t>(cta) * Cfg::kBM + q * 32 + lane;
+        const int32_t row0 = wi.mb * Cfg::kTileM + static_cast<int32_t>(cta) * Cfg::kBM + q * 32, row = row0 + lane;
         const int32_t col0 = wi.nb * Cfg::kOutN + group * kCols;
-        const bool row_in = row < args.M;
-        const bool idle = row - lane >= args.M || col0 >= args.N;  // of all 32 rows
-        const int64_t target = row_in ? args.targets[row] - col0 : -1;
+        const bool row_in = row < dims.rows;
+        const bool idle = row0 >= dims.rows || col0 >= args.N;  // none of the warp's logits counts
+        int64_t target = -1;
+        XentRow xr = {};
+        if (row_in) {
+          if constexpr (Cfg::kEpi == kEpiLse)
+            target = args.targets[row] - col0;
+          else
+            xr = args.xent_rows[row];
+        }
         float z[kCols];
 #pragma unroll
         for (int i = 0; i < kCols; ++i) z[i] = 0.0f;
@@ -977,22 +985,41 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           }
         }
         if (!ok) break;
-        // No lane's target is among these columns but for a few tiles of a row.
-        const bool here = target >= 0 && target < kCols && target < args.N - col0;
-        if (__any_sync(0xffffffffu, here)) {
+        if constexpr (Cfg::kEpi == kEpiLse) {
+          // No lane's target is among these columns but for a few tiles of a row.
+          const bool here = target >= 0 && target < kCols && target < args.N - col0;
+          if (__any_sync(0xffffffffu, here)) {
 #pragma unroll
-          for (int i = 0; i < kCols; ++i)
-            if (here && target == i) args.target_z[row] = z[i];
-        }
-        if (col0 + kCols > args.N) {
+            for (int i = 0; i < kCols; ++i)
+              if (here && target == i) args.target_z[row] = z[i];
+          }
+          if (col0 + kCols > args.N) {
 #pragma unroll
-          for (int i = 0; i < kCols; ++i) z[i] = col0 + i < args.N ? z[i] : -INFINITY;
+            for (int i = 0; i < kCols; ++i) z[i] = col0 + i < args.N ? z[i] : -INFINITY;
+          }
+          float share_m = -INFINITY, share_s = 0.0f;
+          if (!idle) lse_take<kCols>(z, share_m, share_s);
+          if (row_in)
+            args.shares[(static_cast<int64_t>(wi.nb) * Cfg::kGroups + group) * args.M + row] =
+                make_float2(share_m, share_s);
+        } else if (row0 < args.M && col0 < args.N) {
+          // Rows behind the last: zeros, up to a whole k-block of the next product.
+          static_assert(Cfg::kEpi != kEpiXent || kCols == 64, "one staging buffer");
+          const uint32_t sbuf = take_buf();
+          xent_columns<kCols>(xr, args.col_base + col0, z);
+#pragma unroll
+          for (int j = 0; j < kCols / 8; ++j) {
+            const uint32_t at = sbuf + static_cast<uint32_t>(lane) * 128u + ((static_cast<uint32_t>(j) ^ (lane & 7u)) << 4);
+            ptx::st_shared_v4(at, pack16(bf16, z[8 * j], z[8 * j + 1]), pack16(bf16, z[8 * j + 2], z[8 * j + 3]),
+                              pack16(bf16, z[8 * j + 4], z[8 * j + 5]), pack16(bf16, z[8 * j + 6], z[8 * j + 7]));
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::tma_store_3d(&tmC, sbuf, col0, row0, 0);
+            ptx::bulk_commit_group();
+          }
         }
-        float share_m = -INFINITY, share_s = 0.0f;
-        if (!idle) lse_take<kCols>(z, share_m, share_s);
-        if (row_in)
-          args.shares[(static_cast<int64_t>(wi.nb) * Cfg::kGroups + group) * args.M + row] =
-              make_float2(share_m, share_s);
       }
     } else
     for (int32_t it = unit;; it += units) {
@@ -1046,9 +1073,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       };
       constexpr int kChunks = Cfg::kOutN / 64;
       if (group >= kChunks) release_tmem();
-      XentRow xr = {};
-      if constexpr (Cfg::kEpi == kEpiXent)
-        if (row_in) xr = args.xent_rows[row];
 #pragma unroll 1
       for (int c = group; c < kChunks; c += Cfg::kGroups) {
         const int32_t col0 = wi.nb * Cfg::kOutN + c * 64;
@@ -1078,22 +1102,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           } else {
             store_chunk(&tmC, packed, col0, row0, wi.batch * args.c_zb, in);
           }
-        } else if constexpr (Cfg::kEpi == kEpiXent) {
-          uint32_t packed[32];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t v[32];
-            float z[32];
-            ptx::tmem_ld_32x32b_x32(t_row + c * 64 + half * 32, v);
-            ptx::tmem_wait_ld(v);
-            if (half == 1 && last) release_tmem();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(v[i]);
-            xent_columns<32>(xr, args.col_base + col0 + half * 32, z);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) packed[half * 16 + i] = pack16(bf16, z[2 * i], z[2 * i + 1]);
-          }
-          store_chunk(&tmC, packed, col0, row0, 0, in);
         } else if constexpr (Cfg::kEpi == kEpiSum) {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {

@@ -46,13 +46,13 @@ constexpr int epi_bufs(int epi) { return epi == kEpiSplit || epi == kEpiSplitSym
 // 128 x 128 for problems of few tiles.
 template <int kEpi>
 using Pair = FusedCfg<2, 256, kEpi == kEpiLse ? 7 : kEpi == kEpiStore ? 6 : 5, kEpi,
-                      kEpi == kEpiLse ? 0 : kEpi == kEpiStore ? 1 : epi_bufs(kEpi)>;
+                      kEpi == kEpiLse ? 0 : kEpi == kEpiStore || kEpi == kEpiXent ? 1 : epi_bufs(kEpi)>;
 template <int kEpi>
 using TwoPairs = FusedCfg<2, 256, 5, kEpi, epi_bufs(kEpi), 2>;  // one tile, half of its k-blocks each
 template <int kEpi, int kSplit = 1, int kParts = 1>
 using Lone = FusedCfg<1, 128, kEpi == kEpiLse && kSplit == 1 ? 7 : 5, kEpi,
                       kEpi == kEpiLse && kSplit == 1 ? 0 : epi_bufs(kEpi), kSplit,
-                      kEpi == kEpiLse && (kSplit > 1) ? 4 : kParts>;
+                      ((kEpi == kEpiLse || kEpi == kEpiXent) && kSplit > 1) ? 4 : kParts>;
 
 struct DeviceGuard {
   int prev = -1;

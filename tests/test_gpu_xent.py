@@ -298,6 +298,34 @@ def test_xent_sharp_and_far_logits(g, dt):
     run(g, x2, shifted, targets, dloss)
 
 
+@pytest.mark.parametrize("shape", [(300, 4096, 3000), (5, 4096, 3000), (40, 4096, 300)])
+def test_xent_gradients_of_sure_tokens(g, shape):
+    """Tokens that the model is sure of, exp(-loss) within 1e-5 of 1: the target's dz is
+    the difference of two numbers near 1.  Their errors must agree: a logit of 20 summed
+    by the tensor cores alone is off by 1e-4.  Logits here are off by 16 truncations of
+    2^-23 of at most the sum of magnitudes of 256 products, and the lse by as much: 2e-6
+    of dloss for each, 2e-5 and half an exponent's rounding in all."""
+    T, D, V = shape
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.randn(V, D, generator=gen, device="cuda") * D ** -0.5
+    targets = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    x = (20 * w[targets]).half()
+    w = w.half()
+    loss, lse = g.linear_cross_entropy(x, w, targets, save=True)
+    z = x.to(F64) @ w.to(F64).t()
+    p = torch.softmax(z, 1)
+    pt = p.gather(1, targets[:, None])[:, 0]
+    assert (1 - pt).max() < 1e-4 and (loss.to(F64) + pt.log()).abs().max() < 2e-5
+    dloss = torch.full((T,), 1024.0, device="cuda")  # (dx would be below fp16's normal range)
+    dx, _ = g.linear_cross_entropy_backward(dloss, x, w, targets, lse)
+    dz = p.clone()
+    dz[torch.arange(T, device="cuda"), targets] -= 1
+    ref = 1024 * (dz @ w.to(F64))
+    # dz off by 2e-5 at the target, the rest of it by 2^-11 of itself.
+    err = 2e-5 * w[targets].to(F64).abs() + 2.0 ** -9 * (p @ w.to(F64).abs() - pt[:, None] * w[targets].to(F64).abs()).abs()
+    check(dx, ref, 1024 * err + 2.0 ** -20 * ref.abs(), "dx")
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e-9, 1.0, 1e20])
 def test_xent_gradients_of_any_scale(g, scale):
     """fp16's dz is scaled by the largest dloss, tokens of far smaller ones beside it."""
