@@ -26,14 +26,14 @@ namespace {
 
 using namespace gb300::ops;
 
-// Tokens of one launch of the forward pass: bounds the shares' memory.
-constexpr int64_t kLseTokens = 16384;
+// Tokens of one launch of the forward pass at most, and bytes of their shares.
+constexpr int64_t kLseTokens = 16384, kShareBytes = 512ll << 20;
 // Bytes of dz held at a time, where pieces of kMinPiece columns allow it.
 constexpr int64_t kPieceBytes = 512ll << 20, kMinPiece = 4096;
-constexpr int64_t kMaxVocab = 1 << 28;
+constexpr int64_t kMaxVocab = 1 << 28, kMaxWidth = 1 << 24;
 
 bool xent_dims_ok(int64_t T, int64_t D, int64_t V) {
-  return dim_ok(T) && dim_ok(D) && D > 0 && V > 0 && V <= kMaxVocab;
+  return dim_ok(T) && D > 0 && D <= kMaxWidth && V > 0 && V <= kMaxVocab;
 }
 
 gemm_status_t check_xent(const gemm_ops_s* h, int64_t T, int64_t D, int64_t V, gemm_dtype_t dtype) {
@@ -46,7 +46,11 @@ gemm_status_t check_xent(const gemm_ops_s* h, int64_t T, int64_t D, int64_t V, g
 // sixteen of one of at most 76 tiles that a cluster shares.
 int64_t most_shares(int64_t V) { return std::max<int64_t>(4 * cdiv(V, 256), std::min<int64_t>(16 * cdiv(V, 128), 16 * 76)); }
 
-size_t target_bytes(int64_t T) { return up(std::min(T, kLseTokens) * 4, 256); }
+// Tokens of a launch: a multiple of a pair's 256 rows.
+int64_t lse_tokens(int64_t T, int64_t V) {
+  return std::min(T, std::clamp<int64_t>(kShareBytes / (8 * most_shares(V)) / 256 * 256, 256, kLseTokens));
+}
+size_t target_bytes(int64_t n) { return up(n * 4, 256); }
 
 // Columns of a piece of the vocabulary: as few equal pieces as fit.
 int64_t piece_columns(int64_t T, int64_t V) {
@@ -56,7 +60,8 @@ int64_t piece_columns(int64_t T, int64_t V) {
 
 // Shares of the k-blocks (64 entries of the vocabulary) that CTAs sum on their own for
 // dx of few tiles, 0 where a cluster's four or two are as good (27 x k-blocks + 550 of
-// the model in host.cuh, 400 more for adding the shares up): 4 x 1288 x 66557, XXX.
+// the model in host.cuh, 400 more for adding the shares up): 4 x 1288 x 66557
+// 148 us with a cluster's, 121 with 13 shares.
 int64_t dx_slices(const gemm_ops_s* h, int64_t T, int64_t D, int64_t V) {
   const int64_t tiles = cdiv(T, 128) * cdiv(D, 128), kb = cdiv(V, 64);
   const int64_t slices = std::min(h->num_sms / tiles, kb / 8);
@@ -91,7 +96,8 @@ extern "C" {
 
 size_t gemm_linear_cross_entropy_workspace(gemm_ops_t h, int64_t T, int64_t D, int64_t V) {
   if (!h || T <= 0 || !xent_dims_ok(T, D, V)) return 0;
-  return target_bytes(T) + up(most_shares(V) * std::min(T, kLseTokens) * 8, 256);
+  const int64_t n = lse_tokens(T, V);
+  return target_bytes(n) + up(most_shares(V) * n * 8, 256);
 }
 
 gemm_status_t gemm_linear_cross_entropy(gemm_ops_t h, const void* x, int64_t ldx, const void* w, int64_t ldw,
@@ -120,9 +126,10 @@ gemm_status_t gemm_linear_cross_entropy(gemm_ops_t h, const void* x, int64_t ldx
   if ((st = check_bufs(h, bufs)) != GEMM_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* target_z = static_cast<float*>(workspace);
-  float2* shares = reinterpret_cast<float2*>(static_cast<char*>(workspace) + target_bytes(T));
-  for (int64_t t0 = 0; t0 < T; t0 += kLseTokens) {
-    const int64_t n = std::min(kLseTokens, T - t0);
+  const int64_t step = lse_tokens(T, V);
+  float2* shares = reinterpret_cast<float2*>(static_cast<char*>(workspace) + target_bytes(step));
+  for (int64_t t0 = 0; t0 < T; t0 += step) {
+    const int64_t n = std::min(step, T - t0);
     const Product p = {n, V, D, {static_cast<const uint16_t*>(x) + t0 * ldx, n, D, ldx, 1, n * ldx},
                        {w, V, D, ldw, 1, V * ldw}, false, false, dtype == GEMM_BF16, 1, 1};
     FusedArgs a = base_args(h, p);

@@ -337,7 +337,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, save=False, out=None, stream
     and r = 1 / sqrt(mean (x - m)^2 + eps).
 
     x is float16, bfloat16 or float32, weight and bias [D] of its type or float32
-    (None for 1 and 0).  Returns y, of x's type, and with ``save`` also stats
+    (None for 1 and 0; a bias needs a weight).  Returns y, of x's type, and with ``save`` also stats
     [T, 2] float32, m and r, that :func:`layer_norm_backward` takes.  Rows may be
     strided."""
     return _of(x, ops).layer_norm(x, weight, bias, eps, save, out, stream)

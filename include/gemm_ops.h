@@ -216,10 +216,11 @@ GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_ops_t ops, const void* dy, in
  *
  *   x       : [T, D];  w : [V, D], one row per entry of the vocabulary
  *   targets : [T] int64, contiguous: an entry, or ignore_index (any value) for a token
- *             without a loss (0); any other target outside 0 .. V - 1 gives NaN
+ *             without a loss (0); any other target outside 0 .. V - 1 gives NaN, and NaN
+ *             gradients
  *   loss    : [T] fp32;  lse : [T] fp32, or NULL (the lse of every token, ignored ones too)
  * D is a positive multiple of 8, x and w 16-byte aligned, their row distances multiples
- * of 8 (GEMM_ERR_ALIGNMENT otherwise); V is 1 to 2^28; T == 0: nothing to do.  Logits
+ * of 8 (GEMM_ERR_ALIGNMENT otherwise); D is at most 2^24, V 1 to 2^28; T == 0: nothing to do.  Logits
  * and sums are fp32.  Infinities and NaN go where the formula puts them: an infinite
  * logit gives an infinite lse.
  * workspace: gemm_linear_cross_entropy_workspace(ops, T, D, V) bytes, 256-byte aligned. */
