@@ -71,18 +71,19 @@ int64_t dx_slices(const gemm_ops_s* h, int64_t T, int64_t D, int64_t V) {
 }
 
 struct XentSpace {
-  int64_t piece, pitch, slices;
+  int64_t piece, pitch, pitch_x, slices;  // pitch_x: of the copy of x, in whole 128-byte lines
   size_t rows, scalars, order, packed, dz, sum, total;
 };
 XentSpace xent_space(const gemm_ops_s* h, int64_t T, int64_t D, int64_t V) {
   XentSpace s;
   s.piece = piece_columns(T, V);
   s.pitch = up(s.piece, 64);
+  s.pitch_x = up(D, 64);
   s.rows = 0;
   s.scalars = up(T * static_cast<int64_t>(sizeof(XentRow)), 256);
   s.order = s.scalars + 256;
   s.packed = s.order + up(T * 4, 256);
-  s.dz = s.packed + up(T * D * 2, 256);
+  s.dz = s.packed + up(T * s.pitch_x * 2, 256);
   s.sum = s.dz + up(T * s.pitch * 2, 256);
   // Several pieces, or shares of one: fp32 sums of dx.
   s.slices = s.piece < V ? 1 : dx_slices(h, T, D, V);
@@ -204,6 +205,7 @@ gemm_status_t gemm_linear_cross_entropy_backward(gemm_ops_t h, const float* dlos
   r.live = reinterpret_cast<int32_t*>(ws + sp.scalars) + 1;
   r.order = reinterpret_cast<int32_t*>(ws + sp.order);
   r.packed = ws + sp.packed;
+  r.pitch = sp.pitch_x;
   r.hold = bf16 ? 1.0f : 16384.0f;
   r.sum = reinterpret_cast<const float*>(ws + sp.sum);
   r.slices = sp.slices;
@@ -212,7 +214,7 @@ gemm_status_t gemm_linear_cross_entropy_backward(gemm_ops_t h, const float* dlos
   void* dz = ws + sp.dz;
   const bool whole = sp.piece >= V;
   // Laid out for all T tokens; r.live of them take part.
-  const Stack xs = {r.packed, T, D, D, 1, T * D};
+  const Stack xs = {r.packed, T, D, sp.pitch_x, 1, T * sp.pitch_x};
   for (int64_t v0 = 0; v0 < V; v0 += sp.piece) {
     const int64_t n = std::min(sp.piece, V - v0);
     const Stack wv = {static_cast<const uint16_t*>(w) + v0 * ldw, n, D, ldw, 1, n * ldw};

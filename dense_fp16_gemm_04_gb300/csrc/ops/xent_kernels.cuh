@@ -39,14 +39,14 @@ struct XentArgs {
   const void* x;
   XentRow* rows;   // of the tokens that have a gradient, in order
   int32_t *live, *order;  // how many, and which
-  void* packed;    // their x, [T][D]; zeros up to a whole k-block of 64
+  void* packed;    // their x, [T][D], rows `pitch` apart; zeros up to a whole k-block of 64
   float* scale;    // what the products are to be multiplied by
   float hold;      // dz is held times hold / 2^e
   // The sums of dx, [slices][T][D] to be added up in order, and dx itself.
   const float* sum;
   int64_t slices;
   void* dx;
-  int64_t ldx, lddx, D;
+  int64_t ldx, lddx, pitch, D;
   int32_t bf16;
 };
 
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kPackThreads) xent_pack(const XentArgs a) {
       const int64_t k = i / pieces, c = (i - k * pieces) * 1024 + lane * 8;
       const int32_t to = place[k];
       const uint16_t* from = x + (t0 + k) * a.ldx;
-      uint16_t* dst = to >= 0 ? packed + to * a.D : dx + (t0 + k) * a.lddx;
+      uint16_t* dst = to >= 0 ? packed + to * a.pitch : dx + (t0 + k) * a.lddx;
       uint4 v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -192,8 +192,8 @@ __global__ void __launch_bounds__(kPackThreads) xent_pack(const XentArgs a) {
     }
   }
   if (blockIdx.x + 1 == gridDim.x) {
-    const int64_t end = min(a.T, static_cast<int64_t>(max(64, (count + 63) / 64 * 64))) * a.D;
-    for (int64_t i = count * a.D + threadIdx.x * 8; i < end; i += kPackThreads * 8)
+    const int64_t end = min(a.T, static_cast<int64_t>(max(64, (count + 63) / 64 * 64))) * a.pitch;
+    for (int64_t i = count * a.pitch + threadIdx.x * 8; i < end; i += kPackThreads * 8)
       ptx::st_global_v4(packed + i, 0, 0, 0, 0);
     if (threadIdx.x == 0) {
       *a.scale = ldexpf(1.0f / a.hold, e);

@@ -340,26 +340,30 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, save=False, out=None, stream
     (None for 1 and 0; a bias needs a weight).  Returns y, of x's type, and with ``save`` also stats
     [T, 2] float32, m and r, that :func:`layer_norm_backward` takes.  Rows may be
     strided."""
-    return _of(x, ops).layer_norm(x, weight, bias, eps, save, out, stream)
+    o = _of(x, ops)  # not through the method: 0.4 of 4.7 us for one row
+    return o._b.layer_norm(o._addr, o.index, x, weight, bias, eps, save, out, stream)
 
 
 def layer_norm_backward(dy, x, weight, stats, bias=True, stream=None, ops: Ops | None = None):
     """Gradients (dx, dweight, dbias) of :func:`layer_norm` from dy [T, D].  dweight
     is None where weight is, dbias (of weight's type, x's without one) where ``bias``
     is false."""
-    return _of(x, ops).layer_norm_backward(dy, x, weight, stats, bias, stream)
+    o = _of(x, ops)
+    return o._b.layer_norm_backward(o._addr, o.index, dy, x, weight, stats, bias, stream)
 
 
 def rms_norm(x, weight=None, eps=1e-6, save=False, out=None, stream=None, ops: Ops | None = None):
     """y = x r weight for each row of x [T, D], with r = 1 / sqrt(mean x^2 + eps).
     As :func:`layer_norm`; stats are [T, 1], r alone."""
-    return _of(x, ops).rms_norm(x, weight, eps, save, out, stream)
+    o = _of(x, ops)
+    return o._b.rms_norm(o._addr, o.index, x, weight, None, eps, save, out, stream)
 
 
 def rms_norm_backward(dy, x, weight, stats, stream=None, ops: Ops | None = None):
     """Gradients (dx, dweight) of :func:`rms_norm` from dy [T, D]; dweight is None
     where weight is."""
-    return _of(x, ops).rms_norm_backward(dy, x, weight, stats, stream)
+    o = _of(x, ops)
+    return o._b.rms_norm_backward(o._addr, o.index, dy, x, weight, stats, False, stream)
 
 
 def linear_cross_entropy(x, w, targets, ignore_index=-100, save=False, out=None, stream=None,

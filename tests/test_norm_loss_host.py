@@ -63,7 +63,7 @@ def test_loss_workspaces(lib):
     for T, D, V in ((1, 8, 1), (300, 64, 5000), (4096, 4096, 131072), (10 ** 6, 64, 10 ** 5), (top, 2 ** 24, 2 ** 28)):
         piece = min(V, 4096)
         assert bwd(T, D, V) >= 2 * T * (D + piece)
-        assert bwd(T, D, V) <= 2 * T * (D + min(V + 256, max(4096, 2 ** 28 // T) + 256)) + 4 * T * D + 20 * T + 2 ** 25
+        assert bwd(T, D, V) <= 2 * T * (D + 64 + min(V + 256, max(4096, 2 ** 28 // T) + 256)) + 4 * T * D + 20 * T + 2 ** 25
     for sizes in ((0, 8, 8), (8, 0, 8), (8, 8, 0), (top + 1, 8, 8), (8, 2 ** 24 + 1, 8), (8, 8, 2 ** 28 + 1), (2 ** 62,) * 3):
         assert fwd(*sizes) == 0 and bwd(*sizes) == 0
 
