@@ -94,6 +94,25 @@ __global__ void __launch_bounds__(kJoinThreads) xent_join(const XentArgs a, int3
   }
 }
 
+// x, its rows `pitch` apart: a warp takes pieces of up to 4 x 256 columns.
+__global__ void __launch_bounds__(256) xent_copy(const XentArgs a) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int64_t pieces = (a.D + 1023) / 1024, all = pieces * a.T;
+  for (int64_t i = blockIdx.x * 8 + threadIdx.x / 32; i < all; i += gridDim.x * 8) {
+    const int64_t t = i / pieces, c = (i - t * pieces) * 1024 + (threadIdx.x & 31) * 8;
+    const uint16_t* from = static_cast<const uint16_t*>(a.x) + t * a.ldx + c;
+    uint16_t* to = static_cast<uint16_t*>(a.packed) + t * a.pitch + c;
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j * 256 < a.D) v[j] = ptx::ld_global_v4_u32(from + j * 256);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j * 256 < a.D) ptx::st_global_v4(to + j * 256, v[j].x, v[j].y, v[j].z, v[j].w);
+  }
+}
+
 constexpr int kPackThreads = 512;
 
 // grid: blocks, each for a share of the tokens; every one looks at all of them for the

@@ -116,7 +116,7 @@ def run(g, x, w, targets, dloss, dlse=None, ignore=-100):
 # long rows, which clusters of 2, 4 and 8 CTAs share; pairs of CTAs.
 SHAPES = [(1, 8, 1), (1, 64, 1000), (2, 16, 2), (3, 136, 129), (5, 4096, 300), (17, 512, 2000), (64, 2048, 1500),
           (100, 1024, 6000), (33, 264, 4099), (128, 1032, 8191), (130, 72, 20001), (257, 520, 5003), (700, 1000, 9973),
-          (2000, 256, 33000), (1500, 2056, 12345)]
+          (2000, 256, 33000), (1500, 2056, 12345), (300, 200, 7001)]
 
 
 @pytest.mark.parametrize("dt", DTYPES, ids=["f16", "bf16"])
@@ -127,7 +127,7 @@ def test_xent(g, i, shape, dt):
     run(g, x, w, targets, dloss, dlse)
 
 
-@pytest.mark.parametrize("shape", [(16500, 64, 16500), (70000, 64, 9001), (40000, 136, 20000)])
+@pytest.mark.parametrize("shape", [(16500, 64, 16500), (70000, 64, 9001), (40000, 136, 20000), (17000, 72, 5000)])
 def test_xent_in_pieces(g, shape):
     """More tokens than one launch of the forward pass takes, and more of dz than is
     held at a time: pieces of the vocabulary, the last one shorter."""

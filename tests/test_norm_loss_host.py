@@ -64,6 +64,7 @@ def test_loss_workspaces(lib):
         piece = min(V, 4096)
         assert bwd(T, D, V) >= 2 * T * (D + piece)
         assert bwd(T, D, V) <= 2 * T * (D + 64 + min(V + 256, max(4096, 2 ** 28 // T) + 256)) + 4 * T * D + 20 * T + 2 ** 25
+    assert fwd(300, 136, 9000) - fwd(300, 128, 9000) == 300 * 192 * 2  # a copy of x in whole lines
     for sizes in ((0, 8, 8), (8, 0, 8), (8, 8, 0), (top + 1, 8, 8), (8, 2 ** 24 + 1, 8), (8, 8, 2 ** 28 + 1), (2 ** 62,) * 3):
         assert fwd(*sizes) == 0 and bwd(*sizes) == 0
 
