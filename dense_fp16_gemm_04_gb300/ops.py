@@ -340,7 +340,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, save=False, out=None, stream
     (None for 1 and 0; a bias needs a weight).  Returns y, of x's type, and with ``save`` also stats
     [T, 2] float32, m and r, that :func:`layer_norm_backward` takes.  Rows may be
     strided."""
-    o = _of(x, ops)  # not through the method: 0.4 of 4.7 us for one row
+    o = _of(x, ops)  # not through the method: one row takes the host 4.2 us, and 4.7 through it
     return o._b.layer_norm(o._addr, o.index, x, weight, bias, eps, save, out, stream)
 
 
