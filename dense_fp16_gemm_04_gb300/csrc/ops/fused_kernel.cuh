@@ -245,7 +245,7 @@ struct FusedCfg {
                 "split clusters: lone CTAs on 128 x 128 tiles, two pairs on 256 x 256 ones");
 };
 
-constexpr int kPartKb = 4;
+constexpr int kPartKb = 4;  // 256 products: 16 steps of the tensor cores
 
 // Cfg::kPartial: k-blocks of a partial sum, of a k-range of n.
 template <class Cfg>
@@ -936,7 +936,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       }
     };
     if constexpr (Cfg::kPartial) {
-      // Each warp for itself: 32 rows, and this group's half of the tile's columns.
+      // Each warp for itself: 32 rows, and this group's 64 columns of the tile.
       constexpr int kCols = Cfg::kOutN / Cfg::kGroups;
       bool ok = true;
       for (int32_t it = unit; ok && it < dims.items; it += units) {

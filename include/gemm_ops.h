@@ -196,7 +196,8 @@ GEMM_API gemm_status_t gemm_rms_norm(gemm_ops_t ops, const void* x, int64_t ldx,
  *   dy, dx         : [T, D] of `dtype`
  *   dweight, dbias : [D] contiguous, of `wtype`; NULL: not wanted
  * Gradients are written, not accumulated; T == 0 gives zero dweight and dbias.
- * The rows are summed in an order that T and D alone decide.  Rules as above.
+ * The rows are summed in an order that sizes, types and alignments alone decide.
+ * Rules as above.
  * workspace: gemm_norm_backward_workspace(ops, T, D) bytes, 256-byte aligned. */
 GEMM_API size_t gemm_norm_backward_workspace(gemm_ops_t ops, int64_t T, int64_t D);
 GEMM_API gemm_status_t gemm_layer_norm_backward(gemm_ops_t ops, const void* dy, int64_t lddy, const void* x,
