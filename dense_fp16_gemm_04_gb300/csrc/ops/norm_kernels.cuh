@@ -99,8 +99,8 @@ __device__ __forceinline__ float total(f32x2 v) {
 }
 __device__ __forceinline__ float total(float v) { return v; }
 
-// kN elements of X: as they lie in memory, 16 aligned bytes or one element (Vec), and
-// as fp32 numbers, in kW pairs or as one (Reg).
+// kN elements of X: as they lie in memory, 16 or 4 aligned bytes or one element (Vec),
+// and as fp32 numbers, in kW pairs or as one (Reg).
 template <int kN>
 struct Reg {
   typedef f32x2 E;
@@ -119,7 +119,9 @@ struct Reg<1> {
 template <class X, int kN>
 struct Vec {
   static_assert(kN * sizeof(X) == 16, "16 bytes");
+  static constexpr int kBytes = 16;
   uint4 r;
+  __device__ void load_shared(uint32_t addr) { r = ptx::ld_shared_v4_u32(addr); }
   // Each row is read once: it need not stay in L1, where the weight does.
   __device__ void load(const X* p) {
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -164,9 +166,27 @@ struct Vec {
   }
 };
 template <class X>
+struct Vec<X, 2> {
+  static_assert(sizeof(X) == 2, "4 bytes");
+  static constexpr int kBytes = 4;
+  uint32_t r;
+  __device__ void load(const X* p) { r = *reinterpret_cast<const uint32_t*>(p); }
+  __device__ void load_shared(uint32_t addr) { r = ptx::ld_shared_u32(addr); }
+  __device__ void get(Reg<2>& f) const {
+    const float2 v = unpack16(std::is_same<X, __nv_bfloat16>::value, r);
+    f.v[0] = pack2(v.x, v.y);
+  }
+  static __device__ void store(X* p, const Reg<2>& f) {
+    const float2 v = unpack2(f.v[0]);
+    *reinterpret_cast<uint32_t*>(p) = pack16(std::is_same<X, __nv_bfloat16>::value, v.x, v.y);
+  }
+};
+template <class X>
 struct Vec<X, 1> {
+  static constexpr int kBytes = sizeof(X);
   X r;
   __device__ void load(const X* p) { r = *p; }
+  __device__ void load_shared(uint32_t addr) { r = __uint_as_float(ptx::ld_shared_u32(addr)); }  // (of fp32 alone)
   __device__ void get(Reg<1>& f) const { f.v[0] = widen(r); }
   static __device__ void store(X* p, const Reg<1>& f) { narrow(f.v[0], p); }
 };
@@ -176,6 +196,8 @@ template <class W, int kN>
 __device__ __forceinline__ void load_weight(const W* p, Reg<kN>& f) {
   if constexpr (kN == 1) {
     f.v[0] = widen(*p);
+  } else if constexpr (kN == 2) {  // (which may start on any element)
+    f.v[0] = pack2(widen(p[0]), widen(p[1]));
   } else if constexpr (sizeof(W) == 4) {
 #pragma unroll
     for (int i = 0; i < kN; i += 4) {
@@ -352,6 +374,10 @@ __device__ __forceinline__ void leave_sums(const NormArgs& a, int team, int at, 
       auto leave = [&](const Reg<kVec>& v, int64_t i) {
         if constexpr (kVec == 1) {
           to[i] = k > 0 ? v.v[0] + sums[i] : v.v[0];
+        } else if constexpr (kVec == 2) {
+          float2 f = unpack2(v.v[0]);
+          if (k > 0) f.x += sums[i], f.y += sums[i + 1];
+          *reinterpret_cast<float2*>(to + i) = f;  // (D is even)
         } else {
 #pragma unroll
           for (int j = 0; j < kVec; j += 4) {  // (D is a multiple of 4)
@@ -386,9 +412,9 @@ __device__ __forceinline__ void leave_sums(const NormArgs& a, int team, int at, 
 // half of the next row, and its dx follows, from the ring again: waiting for the sums
 // of each row in turn left the SM idle for half of the time (8192 x 8192: 81 us).
 __host__ __device__ constexpr int back_slots(int threads) { return threads > 512 ? 3 : 5; }
-template <int kPer>
+template <class X, int kVec, int kPer>
 constexpr size_t back_ring(int threads) {
-  return static_cast<size_t>(back_slots(threads)) * 2 * kPer * threads * 16;
+  return static_cast<size_t>(back_slots(threads)) * 2 * kPer * threads * kVec * sizeof(X);
 }
 
 template <class X, class W, bool kRms, int kVec, int kTeam, int kPer, int kTeams>
@@ -414,17 +440,24 @@ __global__ void __launch_bounds__(kTeam* kTeams, 512 / (kTeam * kTeams) > 0 ? 51
     for (int j = 0; j < Row::kW; ++j) sw[i].v[j] = sb[kRms ? 0 : i].v[j] = Row::all(0.0f);
   auto column = [&](int i) { return (i * kTeam + at) * kVec; };
   // Slot s, vector i of x (which = 0) or dy (1) of this thread.
-  const uint32_t mine = ptx::smem_addr(ring) + threadIdx.x * 16;
+  constexpr uint32_t kBytes = Vec<X, kVec>::kBytes;
+  const uint32_t mine = ptx::smem_addr(ring) + threadIdx.x * kBytes;
   auto slot = [&](int s, int which, int i) {
-    return mine + static_cast<uint32_t>(((s * 2 + which) * kPer + i) * kThreads) * 16u;
+    return mine + static_cast<uint32_t>(((s * 2 + which) * kPer + i) * kThreads) * kBytes;
+  };
+  auto copy = [&](uint32_t to, const X* from) {
+    if constexpr (kBytes == 16)
+      ptx::cp_async_16(to, from);
+    else
+      ptx::cp_async_4(to, from);
   };
   auto fetch = [&](int64_t row, int s) {
     if (row < a.T) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         if (column(i) < D) {
-          ptx::cp_async_16(slot(s, 0, i), x + row * a.ldx + column(i));
-          ptx::cp_async_16(slot(s, 1, i), dy + row * a.lddy + column(i));
+          copy(slot(s, 0, i), x + row * a.ldx + column(i));
+          copy(slot(s, 1, i), dy + row * a.lddy + column(i));
         }
     }
     ptx::cp_async_commit();
@@ -444,9 +477,9 @@ __global__ void __launch_bounds__(kTeam* kTeams, 512 / (kTeam * kTeams) > 0 ? 51
   // x and dy of vector i, from slot s; the weights.
   auto take = [&](int s, int i, Row& f, Row& g, Row& q) {
     Vec<X, kVec> v;
-    v.r = ptx::ld_shared_v4_u32(slot(s, 0, i));
+    v.load_shared(slot(s, 0, i));
     v.get(f);
-    v.r = ptx::ld_shared_v4_u32(slot(s, 1, i));
+    v.load_shared(slot(s, 1, i));
     v.get(g);
     if constexpr (kHold)
       q = wv[i];
@@ -529,11 +562,15 @@ __global__ void __launch_bounds__(kTeam* kTeams, 512 / (kTeam * kTeams) > 0 ? 51
   leave_sums<kRms, kVec, kTeam, kPer, kTeams>(a, team, at, sw, sb, reinterpret_cast<float*>(ring));
 }
 
-// The same for rows that start on any element, a row ahead in registers.
-template <class X, class W, bool kRms, int kTeam, int kPer, int kTeams>
+// The same for rows that are no whole vectors, by elements or pairs of 16-bit ones: a
+// row ahead in registers (through the ring, 4 bytes a copy, 2713 x 6563 fp32 took 78 us
+// in place of 62).
+template <class X, class W, bool kRms, int kVec, int kTeam, int kPer, int kTeams>
 __global__ void __launch_bounds__(kTeam* kTeams) norm_rows_back_single(const NormArgs a) {
-  extern __shared__ float block_sums_of[];  // [2][D], where kTeams > 1
+  extern __shared__ __align__(16) float block_sums_of[];  // [2][D], where kTeams > 1
   __shared__ float sm[kTeam > 32 ? kTeams * 128 : 1];
+  typedef Reg<kVec> Row;
+  typedef typename Row::E E;
   const int team = threadIdx.x / kTeam, at = threadIdx.x % kTeam;
   const int32_t D = static_cast<int32_t>(a.D);
   const X *x = static_cast<const X*>(a.x), *dy = static_cast<const X*>(a.dy);
@@ -541,19 +578,19 @@ __global__ void __launch_bounds__(kTeam* kTeams) norm_rows_back_single(const Nor
   const float n = static_cast<float>(D);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
   TeamSums<kTeam> sums(sm + team * 128, team);
-  X xn[kPer], gn[kPer];
-  float mn = 0.0f, rn = 0.0f, wv[kPer];
-  Reg<1> sw[kPer], sb[kRms ? 1 : kPer];
+  Vec<X, kVec> xn[kPer], gn[kPer];
+  float mn = 0.0f, rn = 0.0f;
+  Row sw[kPer], sb[kRms ? 1 : kPer], wv[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) sw[i].v[0] = sb[kRms ? 0 : i].v[0] = 0.0f;
-  auto column = [&](int i) { return i * kTeam + at; };
+  for (int i = 0; i < kPer; ++i) sw[i].v[0] = sb[kRms ? 0 : i].v[0] = Row::all(0.0f);
+  auto column = [&](int i) { return (i * kTeam + at) * kVec; };
   auto fetch = [&](int64_t t) {
     if (t >= a.T) return;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (column(i) < D) {
-        xn[i] = x[t * a.ldx + column(i)];
-        gn[i] = dy[t * a.lddy + column(i)];
+        xn[i].load(x + t * a.ldx + column(i));
+        gn[i].load(dy + t * a.lddy + column(i));
       }
     if (!kRms) mn = a.stats[2 * t];
     rn = a.stats[kRms ? t : 2 * t + 1];
@@ -563,30 +600,41 @@ __global__ void __launch_bounds__(kTeam* kTeams) norm_rows_back_single(const Nor
   int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + team;
   fetch(t);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) wv[i] = w && column(i) < D ? widen(w[column(i)]) : 1.0f;
+  for (int i = 0; i < kPer; ++i) {
+    wv[i].v[0] = Row::all(1.0f);
+    if (w && column(i) < D) load_weight<W, kVec>(w + column(i), wv[i]);
+  }
   for (int turn = 0; t < a.T; t += step, turn ^= 1) {
-    const float m = mn, r = rn;
-    float h[kPer], q[kPer], s1 = 0.0f, s2 = 0.0f;
+    const E back = Row::all(-mn), rs = Row::all(rn);
+    const float r = rn;
+    Row h[kPer], q[kPer], g;
+    E s1 = Row::all(0.0f), s2 = s1;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (column(i) < D) {
-        const float g = widen(gn[i]);
-        h[i] = (widen(xn[i]) - m) * r;
-        q[i] = g * wv[i];
-        sw[i].v[0] = fmaf(g, h[i], sw[i].v[0]);
-        if (!kRms) sb[kRms ? 0 : i].v[0] += g;
-        s1 += q[i];
-        s2 = fmaf(q[i], h[i], s2);
+        xn[i].get(h[i]);
+        gn[i].get(g);
+        h[i].v[0] = vmul(kRms ? h[i].v[0] : vadd(h[i].v[0], back), rs);
+        q[i].v[0] = vmul(g.v[0], wv[i].v[0]);
+        sw[i].v[0] = vfma(g.v[0], h[i].v[0], sw[i].v[0]);
+        if (!kRms) {
+          sb[kRms ? 0 : i].v[0] = vadd(sb[kRms ? 0 : i].v[0], g.v[0]);
+          s1 = vadd(s1, q[i].v[0]);
+        }
+        s2 = vfma(q[i].v[0], h[i].v[0], s2);
       }
     fetch(t + step);
-    const float2 s = sums.all(make_float2(s1, s2), turn);
-    const float c1 = kRms ? 0.0f : s.x / n, c2 = s.y / n;
+    const float2 s = sums.all(make_float2(kRms ? 0.0f : total(s1), total(s2)), turn);
+    const E k1 = Row::all(kRms ? 0.0f : -r * (s.x / n)), k2 = Row::all(-r * (s.y / n));
     X* dx = static_cast<X*>(a.y) + t * a.ldy;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (column(i) < D) narrow(r * ((q[i] - c1) - h[i] * c2), dx + column(i));
+      if (column(i) < D) {
+        q[i].v[0] = vfma(q[i].v[0], rs, kRms ? vmul(h[i].v[0], k2) : vfma(h[i].v[0], k2, k1));
+        Vec<X, kVec>::store(dx + column(i), q[i]);
+      }
   }
-  leave_sums<kRms, 1, kTeam, kPer, kTeams>(a, team, at, sw, sb, block_sums_of);
+  leave_sums<kRms, kVec, kTeam, kPer, kTeams>(a, team, at, sw, sb, block_sums_of);
 }
 
 // One block per row, element by element: rows of any length, start and distance.

@@ -117,7 +117,7 @@ def back(g, dy, x, weight, stats, rms):
 SHAPES = [(1, 1), (3, 2), (2, 7), (5, 8), (4, 31), (1, 33), (9, 64), (17, 100), (33, 255), (2, 256), (6, 264),
           (130, 520), (64, 1000), (3, 1003), (7, 1024), (40, 1032), (5, 2048), (300, 2056), (2, 4096), (19, 4100),
           (1, 8192), (6, 8200), (700, 96), (1025, 1280), (2, 16384), (3, 16392), (2, 20001), (1, 65536), (2, 70008),
-          (1, 300001)]
+          (1, 300001), (50, 130), (9, 1002), (40, 4098), (3, 8190), (7, 12346), (2, 16386), (300, 66)]
 
 
 @pytest.mark.parametrize("rms", [False, True], ids=["ln", "rms"])
@@ -177,7 +177,7 @@ def test_norm_against_differences(g, D, rms):
 
 
 @pytest.mark.parametrize("rms", [False, True], ids=["ln", "rms"])
-@pytest.mark.parametrize("D", [40, 1000, 1024, 4104, 33000])
+@pytest.mark.parametrize("D", [40, 1000, 1024, 1026, 4104, 33000])
 @pytest.mark.parametrize("types", TYPES, ids=IDS)
 def test_norm_strided_rows_from_any_element(g, types, D, rms):
     T = 6
@@ -186,7 +186,7 @@ def test_norm_strided_rows_from_any_element(g, types, D, rms):
     want = back(g, dy, x, weight, stats, rms)
     ref, err, _ = forward_ref(x, weight, None if rms else bias, 1e-5, rms)
     refs = backward_ref(dy, x, weight, stats, rms)
-    for start, extra in ((8, 16), (1, 2), (3, 8), (8, 13)):
+    for start, extra in ((8, 16), (1, 2), (3, 8), (8, 13), (2, 4)):
         def pad(t):
             big = torch.full((T, D + start + extra), float("nan"), dtype=t.dtype, device="cuda")
             v = big[:, start:start + D]
