@@ -290,6 +290,30 @@ def test_norm_past_two_gigaelements(g):
         assert torch.equal(a, b)
 
 
+def test_norm_of_more_than_two_gigaelements(g):
+    T, D = 300_000, 8192
+    x = torch.empty(T, D, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    for part in x.split(30_000):
+        part.copy_(torch.randn(part.shape, generator=gen, device="cuda"))
+    weight = 1 + 0.1 * torch.randn(D, generator=gen, device="cuda")
+    y, stats = g.rms_norm(x, weight, save=True)
+    pick = torch.cat((torch.arange(100, device="cuda"), torch.arange(262_100, 262_200, device="cuda"),
+                      torch.arange(T - 100, T, device="cuda")))
+    ref, err, sref = forward_ref(x[pick], weight, None, 1e-6, True)
+    check(y[pick], ref, err, "y")
+    check_stats(stats[pick], sref, True)
+    dx, dw = g.rms_norm_backward(y, x, weight, stats)
+    check(dx[pick], *backward_ref(y[pick], x[pick], weight, stats[pick], True)[0], "dx")
+    ref, err = torch.zeros(D, dtype=F64, device="cuda"), torch.zeros(D, dtype=F64, device="cuda")
+    for a in range(0, T, 15_000):
+        b = slice(a, a + 15_000)
+        h = x[b].to(F64) * stats[b].to(F64)
+        ref += (y[b].to(F64) * h).sum(0)
+        err += (T + 64) * E * (y[b].to(F64) * h).abs().sum(0)
+    check(dw, ref, err, "dweight")
+
+
 # ------------------------------------------------------------ streams, graphs --
 def test_norm_streams_and_graphs(g):
     x, weight, bias, dy = make(300, 1032, torch.bfloat16, torch.float32)

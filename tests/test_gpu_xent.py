@@ -367,6 +367,74 @@ def test_xent_single_entries_are_exact(g):
     check(lse, w[0].to(F64) + torch.log(torch.tensor(300.0, dtype=F64, device="cuda")), 32 * E * 8, "lse")
 
 
+def test_xent_many_tokens(g):
+    """dz of 2.5e9 elements: tokens' offsets past 32 bits, ignored ones among them."""
+    T, D, V = 600_000, 64, 4096
+    x, w, targets, dloss = make(T, D, V, torch.bfloat16, seed=9)
+    dloss = dloss * T
+    loss, lse = g.linear_cross_entropy(x, w, targets, save=True)
+    dx, dw = g.linear_cross_entropy_backward(dloss, x, w, targets, lse)
+    g.default_ops().check_error()
+    pick = torch.cat((torch.arange(300, device="cuda"), torch.arange(T - 300, T, device="cuda"),
+                      torch.randint(0, T, (2000,), device="cuda")))
+    rl, rz = forward_ref(x[pick], w, targets[pick])
+    check(loss[pick], *rl, "loss")
+    check(lse[pick], *rz, "lse")
+    rx, _ = backward_ref(dloss[pick], None, x[pick], w, targets[pick], lse[pick], x.dtype)
+    check(dx[pick], *rx, "dx")
+    assert not dx[targets < 0].any()
+    ref, err = torch.zeros(V, D, dtype=F64, device="cuda"), torch.zeros(V, D, dtype=F64, device="cuda")
+    for a in range(0, T, 30_000):
+        b = slice(a, a + 30_000)
+        _, (r, e) = backward_ref(dloss[b], None, x[b], w, targets[b], lse[b], x.dtype)
+        ref += r
+        err += e
+    # (each part's bound has sum_eps of its own tokens; the sums of all of them pass on as many times more)
+    check(dw, ref, err + sum_eps(T) / sum_eps(30_000) * err, "dw")
+
+
+def test_xent_large_vocabulary(g):
+    """W of 2.5e9 elements: entries' offsets past 32 bits, in either pass."""
+    T, D, V = 3, 4096, 600_001
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.empty(V, D, dtype=torch.float16, device="cuda")
+    for part in w.split(100_000):
+        part.copy_(torch.randn(part.shape, generator=gen, device="cuda") * 2 * D ** -0.5)
+    x = torch.randn(T, D, generator=gen, device="cuda").half()
+    targets = torch.tensor([V - 1, 524_288, 5], device="cuda")
+    loss, lse = g.linear_cross_entropy(x, w, targets, save=True)
+    dloss = torch.full((T,), 64.0, device="cuda")
+    dx, dw = g.linear_cross_entropy_backward(dloss, x, w, targets, lse)
+    g.default_ops().check_error()
+    zs = [logits(x, part) for part in w.split(100_000)]
+    z, ez = (torch.cat(t, 1) for t in zip(*zs))
+    ref = torch.logsumexp(z, 1)
+    e = (torch.exp(z - ref[:, None]) * ez).sum(1) + 4 * E * (z.abs().amax(1) + 2 * (16 + V / 2 ** 15)) + 2 * E * ref.abs()
+    check(lse, ref, e, "lse")
+    zt = z.gather(1, targets[:, None])[:, 0]
+    check(loss, ref - zt, e + ez.gather(1, targets[:, None])[:, 0] + 2 * E * (ref.abs() + zt.abs()), "loss")
+    sel = torch.cat((targets, torch.randint(0, V, (500,), generator=gen, device="cuda"), torch.arange(V - 200, V, device="cuda")))
+    hit = (sel[:, None] == targets).to(F64)
+    dz = 64 * (torch.exp(z[:, sel] - lse.to(F64)[:, None]) - hit.t())
+    edz = 64 * torch.exp(z[:, sel] - lse.to(F64)[:, None]) * (ez[:, sel] + 4 * E * (z[:, sel].abs() + lse[:, None].abs() + 2))
+    edz = edz + u(w.dtype) * (dz.abs() + edz) + 2.0 ** -38 * 64 + 8 * E * 64
+    xd = x.to(F64)
+    check(dw[sel], dz.t() @ xd, edz.t() @ xd.abs() + sum_eps(T) * (dz.abs() + edz).t() @ xd.abs(), "dw")
+    want, err = torch.zeros(T, D, dtype=F64, device="cuda"), torch.zeros(T, D, dtype=F64, device="cuda")
+    for i, part in enumerate(w.split(100_000)):
+        c = slice(i * 100_000, i * 100_000 + len(part))
+        p = 64 * torch.exp(z[:, c] - lse.to(F64)[:, None])
+        ep = p * (ez[:, c] + 4 * E * (z[:, c].abs() + lse[:, None].abs() + 2))
+        ep = ep + u(w.dtype) * (p + ep) + 2.0 ** -38 * 64
+        for t in range(T):
+            if i * 100_000 <= targets[t] < i * 100_000 + len(part):
+                p[t, targets[t] - i * 100_000] -= 64
+                ep[t, targets[t] - i * 100_000] += (u(w.dtype) + 8 * E) * 64
+        want += p @ part.to(F64)
+        err += (ep + sum_eps(V) * (p.abs() + ep)) @ part.to(F64).abs()
+    check(dx, want, err, "dx")
+
+
 # ------------------------------------------------------------ streams, graphs --
 def test_xent_streams_and_graphs(g):
     x, w, targets, dloss = make(300, 264, 5000, torch.bfloat16)
