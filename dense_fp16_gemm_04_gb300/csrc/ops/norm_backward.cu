@@ -110,7 +110,7 @@ gemm_status_t norm_backward(gemm_ops_s* h, const void* dy, int64_t lddy, const v
                     dim3(256), 0, 1, s, a);
     }
     if (st != GEMM_OK || !sums) return st;
-    return launch(h, norm_dw_sum<W>, dim3(static_cast<unsigned>(cdiv(D, 32)), 2), dim3(512), 0, 1, s, a);
+    return launch(h, norm_dw_sum<W>, dim3(static_cast<unsigned>(cdiv(D, 32)), dbias ? 2 : 1), dim3(512), 0, 1, s, a);
   });
 }
 
