@@ -4,19 +4,20 @@ and RMS norm and the loss over a vocabulary, with their gradients.
 
 Thin bindings over the C ABI in ``include/gemm_ops.h``: through the compiled
 ``_binding`` (a call for one token costs the host more than the GPU), and
-``orthogonalize`` through ctypes.  Every step runs in the
-sm_103a kernels of ``libgb300gemm.so``.  Tensors are CUDA tensors of one device,
-float16 or bfloat16 (the norms and ``orthogonalize`` also take float32); results and workspaces come from torch's allocator, on the
-stream of the call (the current one, or ``stream``).  As with any work on another
-stream, the caller orders it after what made the inputs and keeps them until it
-has run (``Tensor.record_stream``).  There is no fallback: wrong arguments and
-other devices raise.
+``orthogonalize`` through ctypes.  Every step runs in the sm_103a kernels of
+``libgb300gemm.so``.  Tensors are CUDA tensors of one device, float16 or bfloat16
+(the norms and ``orthogonalize`` also take float32); results and workspaces come
+from torch's allocator, on the stream of the call (the current one, or
+``stream``).  As with any work on another stream, the caller orders it after what
+made the inputs and keeps them until it has run (``Tensor.record_stream``).  There
+is no fallback: wrong arguments and other devices raise.
 
 The operators record no graph.  A tensor that requires grad (while gradients are
 recorded) or has a forward-mode tangent is refused with a RuntimeError: call them
 under ``torch.no_grad()`` or on detached tensors, or from the methods of a
-``torch.autograd.Function``, whose backward is :func:`gated_ffn_backward` (or
-its sisters).
+``torch.autograd.Function``, whose backward is :func:`gated_ffn_backward`,
+:func:`layer_norm_backward`, :func:`rms_norm_backward` or
+:func:`linear_cross_entropy_backward`.
 
     >>> import torch, dense_fp16_gemm_04_gb300 as g
     >>> x = torch.randn(4096, 1024, device="cuda", dtype=torch.float16)
@@ -25,6 +26,9 @@ its sisters).
     >>> y, gu = g.gated_ffn(x, w_in, w_down, save=True)
     >>> dx, dw_in, dw_down = g.gated_ffn_backward(y, x, w_in, w_down, gu)
     >>> step = g.orthogonalize(dw_down)
+    >>> head = torch.randn(32000, 1024, device="cuda", dtype=torch.float16) / 32
+    >>> targets = torch.randint(0, 32000, (4096,), device="cuda")
+    >>> loss, lse = g.linear_cross_entropy(g.rms_norm(y), head, targets, save=True)
 """
 from __future__ import annotations
 
@@ -337,9 +341,9 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, save=False, out=None, stream
     and r = 1 / sqrt(mean (x - m)^2 + eps).
 
     x is float16, bfloat16 or float32, weight and bias [D] of its type or float32
-    (None for 1 and 0; a bias needs a weight).  Returns y, of x's type, and with ``save`` also stats
-    [T, 2] float32, m and r, that :func:`layer_norm_backward` takes.  Rows may be
-    strided."""
+    (None for 1 and 0; a bias needs a weight).  Returns y, of x's type, and with
+    ``save`` also stats [T, 2] float32, m and r, that :func:`layer_norm_backward`
+    takes.  Rows may be strided."""
     o = _of(x, ops)  # not through the method: one row takes the host 4.2 us, and 4.7 through it
     return o._b.layer_norm(o._addr, o.index, x, weight, bias, eps, save, out, stream)
 
@@ -382,5 +386,6 @@ def linear_cross_entropy(x, w, targets, ignore_index=-100, save=False, out=None,
 def linear_cross_entropy_backward(dloss, x, w, targets, lse, ignore_index=-100, dlse=None, stream=None,
                                   ops: Ops | None = None):
     """Gradients (dx, dw) of :func:`linear_cross_entropy` from dloss [T] float32 (an
-    expanded scalar will do) and, where the lse was used too, dlse [T]."""
+    expanded scalar will do) and, where the lse was used too, dlse [T].  Ignored tokens
+    cost nothing, and their x may hold anything."""
     return _of(x, ops).linear_cross_entropy_backward(dloss, x, w, targets, lse, ignore_index, dlse, stream)

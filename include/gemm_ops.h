@@ -221,9 +221,9 @@ GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_ops_t ops, const void* dy, in
  *             gradients
  *   loss    : [T] fp32;  lse : [T] fp32, or NULL (the lse of every token, ignored ones too)
  * D is a positive multiple of 8, x and w 16-byte aligned, their row distances multiples
- * of 8 (GEMM_ERR_ALIGNMENT otherwise); D is at most 2^24, V 1 to 2^28; T == 0: nothing to do.  Logits
- * and sums are fp32.  Infinities and NaN go where the formula puts them: an infinite
- * logit gives an infinite lse.
+ * of 8 (GEMM_ERR_ALIGNMENT otherwise); D is at most 2^24, V 1 to 2^28; T == 0: nothing
+ * to do.  Logits and sums are fp32.  Infinities and NaN go where the formula puts them:
+ * an infinite logit gives an infinite lse.
  * workspace: gemm_linear_cross_entropy_workspace(ops, T, D, V) bytes, 256-byte aligned. */
 GEMM_API size_t gemm_linear_cross_entropy_workspace(gemm_ops_t ops, int64_t T, int64_t D, int64_t V);
 GEMM_API gemm_status_t gemm_linear_cross_entropy(gemm_ops_t ops, const void* x, int64_t ldx, const void* w,
