@@ -207,9 +207,9 @@ struct FusedCfg {
   // Eight epilogue warps where few k-blocks make the epilogue the bound (weight
   // gradients of 1000 tokens: -5%); four where K is three times as long and the
   // power cap sets the speed (update of 4096 x 8192: eight cost 2%).
-  // Sixteen for a pair's logits, of which each thread holds 64 in registers (eight, 128 of
-  // them: 4096 x 4096 x 131072 2577 us, 2531 with sixteen).
-  static constexpr int kEpiWarps = kEpi == kEpiSplit || kEpi == kEpiSplitSym ? 4 : kPartial && kCtas == 2 ? 16 : 8;
+  // Sixteen for 256 columns of logits, of which each thread holds 64 in registers (eight,
+  // 128 of them: 4096 x 4096 x 131072 2577 us, 2531 with sixteen).
+  static constexpr int kEpiWarps = kEpi == kEpiSplit || kEpi == kEpiSplitSym ? 4 : kPartial && kBN == 256 ? 16 : 8;
   static constexpr int kGroups = kEpiWarps / 4;  // warps per quarter of the rows
   static constexpr int kWarpB = kSplit > 1 ? 6 : 2;  // loads B
   static constexpr int kBufBytes = 32 * 128;

@@ -54,6 +54,12 @@ using Lone = FusedCfg<1, 128, kEpi == kEpiLse && kSplit == 1 ? 7 : 5, kEpi,
                       kEpi == kEpiLse && kSplit == 1 ? 0 : epi_bufs(kEpi), kSplit,
                       ((kEpi == kEpiLse || kEpi == kEpiXent) && kSplit > 1) ? 4 : kParts>;
 
+// One CTA on 128 x 256 logits of the loss, for the rounds that tiles of a pair or of 128
+// columns fill badly: 1 token, 4096 x 32000 49.5 -> 45.1 us, 101 x 512 x 32000 13.4 ->
+// 9.7, 333 x 1024 x 100003 79.6 -> 65.4.
+template <int kEpi>
+using Wide = FusedCfg<1, 256, kEpi == kEpiLse ? 4 : 3, kEpi, kEpi == kEpiLse ? 0 : 1>;
+
 struct DeviceGuard {
   int prev = -1;
   bool ok = false;
@@ -281,8 +287,8 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
 
 // Which form: the one whose rounds of tiles take the least time by this model,
 // in units of 10 ns: a k-block takes a lone CTA 0.27 us (its 32 KB of operands
-// through the SM's L2 port), a pair 0.33 us (the tensor pipe), and a tile starts
-// and ends in 4 to 7 us.  Of clusters of two CTAs 76 fit at once, of four 36, of
+// through the SM's L2 port; 0.4 us and 48 KB for 256 columns), a pair 0.33 us (the
+// tensor pipe), and a tile starts and ends in 4 to 7 us.  Of clusters of two CTAs 76 fit at once, of four 36, of
 // eight 15.  Lone clusters split a tile only where all fit at once.
 //
 // The batched products (high and low parts) go by one matrix's tiles alone, so
@@ -300,8 +306,10 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
   const int64_t n = kBatched ? 1 : p.batch, kb = cdiv(p.K, 64) * p.segs;
   const int64_t small = tiles(cdiv(p.M, 128), cdiv(p.N, Lone<kEpi>::kOutN)) * n;
   const int64_t big = tiles(cdiv(p.M, 256), cdiv(p.N, Pair<kEpi>::kOutN)) * n;
+  constexpr bool kWides = kEpi == kEpiLse || kEpi == kEpiXent;
+  const int64_t wide = cdiv(p.M, 128) * cdiv(p.N, 256);
   const int* most = h->max_split;
-  enum { kPairs, kPairs2, kLone, kLone2, kLone4, kLone8, kForms };
+  enum { kPairs, kPairs2, kLone, kLone2, kLone4, kLone8, kWide, kForms };
   constexpr int64_t kNever = INT64_MAX;
   const int64_t cost[kForms] = {
       h->max_pairs > 0 ? cdiv(big, h->max_pairs) * (33 * kb + 500) : kNever,
@@ -309,7 +317,8 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
       cdiv(small, h->num_sms) * (27 * kb + 400),
       split && small <= most[1] && kb >= 4 ? 27 * cdiv(kb, 2) + 550 : kNever,
       split && small <= most[2] && kb >= (kBatched ? 4 : 8) ? 27 * cdiv(kb, 4) + 550 : kNever,
-      split && !kBatched && small <= std::min(8, most[3]) && kb >= 16 ? 27 * cdiv(kb, 8) + 550 : kNever};
+      split && !kBatched && small <= std::min(8, most[3]) && kb >= 16 ? 27 * cdiv(kb, 8) + 550 : kNever,
+      kWides ? cdiv(wide, h->num_sms) * (40 * kb + 450) : kNever};
   switch (static_cast<int>(std::min_element(cost, cost + kForms) - cost)) {
     case kPairs: return launch_fused<Pair<kEpi>>(h, p, a, c, d, stream, shares);
     case kPairs2:
@@ -327,6 +336,9 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
       break;
     case kLone8:
       if constexpr (kSplits && !kBatched) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream, shares);
+      break;
+    case kWide:
+      if constexpr (kWides) return launch_fused<Wide<kEpi>>(h, p, a, c, d, stream, shares);
       break;
     default: break;
   }
