@@ -56,9 +56,9 @@ using Lone = FusedCfg<1, 128, kEpi == kEpiLse && kSplit == 1 ? 7 : 5, kEpi,
 
 // One CTA on 128 x 256 logits of the loss, for the rounds that tiles of a pair or of 128
 // columns fill badly: 1 token, 4096 x 32000 49.5 -> 45.1 us, 101 x 512 x 32000 13.4 ->
-// 9.7, 333 x 1024 x 100003 79.6 -> 65.4.
-template <int kEpi>
-using Wide = FusedCfg<1, 256, kEpi == kEpiLse ? 4 : 3, kEpi, kEpi == kEpiLse ? 0 : 1>;
+// 9.7, 333 x 1024 x 100003 79.6 -> 65.4.  (The backward pass's, with dz to stage and
+// three k-blocks in flight, gained nothing.)
+using WideLse = FusedCfg<1, 256, 4, kEpiLse, 0>;
 
 struct DeviceGuard {
   int prev = -1;
@@ -288,8 +288,9 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
 // Which form: the one whose rounds of tiles take the least time by this model,
 // in units of 10 ns: a k-block takes a lone CTA 0.27 us (its 32 KB of operands
 // through the SM's L2 port; 0.4 us and 48 KB for 256 columns), a pair 0.33 us (the
-// tensor pipe), and a tile starts and ends in 4 to 7 us.  Of clusters of two CTAs 76 fit at once, of four 36, of
-// eight 15.  Lone clusters split a tile only where all fit at once.
+// tensor pipe), and a tile starts and ends in 4 to 7 us.  Of clusters of two CTAs 76
+// fit at once, of four 36, of eight 15.  Lone clusters split a tile only where all fit
+// at once.
 //
 // The batched products (high and low parts) go by one matrix's tiles alone, so
 // that a matrix of a batch gets the same sums as by itself: the number of its
@@ -306,7 +307,7 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
   const int64_t n = kBatched ? 1 : p.batch, kb = cdiv(p.K, 64) * p.segs;
   const int64_t small = tiles(cdiv(p.M, 128), cdiv(p.N, Lone<kEpi>::kOutN)) * n;
   const int64_t big = tiles(cdiv(p.M, 256), cdiv(p.N, Pair<kEpi>::kOutN)) * n;
-  constexpr bool kWides = kEpi == kEpiLse || kEpi == kEpiXent;
+  constexpr bool kWides = kEpi == kEpiLse;
   const int64_t wide = cdiv(p.M, 128) * cdiv(p.N, 256);
   const int* most = h->max_split;
   enum { kPairs, kPairs2, kLone, kLone2, kLone4, kLone8, kWide, kForms };
@@ -338,7 +339,7 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
       if constexpr (kSplits && !kBatched) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream, shares);
       break;
     case kWide:
-      if constexpr (kWides) return launch_fused<Wide<kEpi>>(h, p, a, c, d, stream, shares);
+      if constexpr (kWides) return launch_fused<WideLse>(h, p, a, c, d, stream, shares);
       break;
     default: break;
   }

@@ -6,7 +6,7 @@ namespace gb300 {
 namespace ops {
 
 bool xent_setup(gemm_ops_s* h) {
-  if (!set_attr<Wide<kEpiLse>>() || !set_attr<Wide<kEpiXent>>() || !set_attr<Pair<kEpiLse>>() || !set_attr<Lone<kEpiLse>>() || !set_attr<Lone<kEpiLse, 2>>() ||
+  if (!set_attr<WideLse>() || !set_attr<Pair<kEpiLse>>() || !set_attr<Lone<kEpiLse>>() || !set_attr<Lone<kEpiLse, 2>>() ||
       !set_attr<Lone<kEpiLse, 4>>() || !set_attr<Lone<kEpiLse, 8>>() || !set_attr<Pair<kEpiXent>>() ||
       !set_attr<Lone<kEpiXent>>() || !set_attr<Lone<kEpiXent, 2>>() || !set_attr<Lone<kEpiXent, 4>>() ||
       !set_attr<Lone<kEpiXent, 8>>() || !set_attr<Pair<kEpiSum>>() || !set_attr<Lone<kEpiSum>>() ||
