@@ -58,6 +58,12 @@ size_t target_bytes(int64_t n) { return up(n * 4, 256); }
 // 276 and 237, 3708 x 1880 x 58569 570 and 517.  Few rows are one tile anyway.
 bool copies_x(int64_t T, int64_t D, int64_t V) { return D % 64 != 0 && T >= 256 && T * V >= 1 << 21; }
 
+// Tile rows of logits that are worked on before the next columns of W: as many as 32 MB of
+// x hold, which stay in L2 while W streams past them (eight, and by this rule: 16384 x
+// 1024 x 32768 630 and 609 us, its gradients 2060 and 2010, of 8192 x 2048 x 65536 4150
+// and 4030).
+int32_t logits_group(int64_t D) { return static_cast<int32_t>(std::clamp<int64_t>((32 << 20) / (512 * D), kGroupM, 32)); }
+
 // Columns of a piece of the vocabulary: as few equal pieces as fit.
 int64_t piece_columns(int64_t T, int64_t V) {
   const int64_t most = std::max(kMinPiece, kPieceBytes / (2 * T) / 256 * 256);
@@ -154,6 +160,7 @@ gemm_status_t gemm_linear_cross_entropy(gemm_ops_t h, const void* x, int64_t ldx
       a.early = kEarlyB;
     else if (t0 > 0)
       a.early = kEarlyA | kEarlyB;  // the kernels before wrote neither x nor W
+    a.group_m = logits_group(D);
     a.targets = targets + t0;
     a.target_z = target_z;
     a.shares = shares;
@@ -243,6 +250,7 @@ gemm_status_t gemm_linear_cross_entropy_backward(gemm_ops_t h, const float* dlos
       a.early = v0 > 0 ? kEarlyA | kEarlyB | kEarlyLive : kEarlyB;
       a.live = r.live;
       a.live_min = 1;
+      a.group_m = logits_group(D);
       a.xent_rows = r.rows;
       a.col_base = static_cast<int32_t>(v0);
       if ((st = fused<kEpiXent>(h, p, a, dzs, {}, s)) != GEMM_OK) return st;
