@@ -51,9 +51,12 @@ template <int kMostPer, class F>
 bool with_team(int64_t n, F f) {
   if (n <= 32) return f(Int<32>(), Int<1>(), Int<8>());
   if (n <= 64) return f(Int<32>(), Int<2>(), Int<8>());
-  if (n <= 32 * kMostPer) return f(Int<32>(), Int<kMostPer>(), Int<8>());
-  if (n <= 256) return f(Int<128>(), Int<2>(), Int<2>());
-  if (n <= 128 * kMostPer) return f(Int<128>(), Int<kMostPer>(), Int<2>());
+  if constexpr (kMostPer > 2)
+    if (n <= 32 * kMostPer) return f(Int<32>(), Int<kMostPer>(), Int<8>());
+  if constexpr (kMostPer < 8)
+    if (n <= 256) return f(Int<128>(), Int<2>(), Int<2>());
+  if constexpr (kMostPer > 2)
+    if (n <= 128 * kMostPer) return f(Int<128>(), Int<kMostPer>(), Int<2>());
   if (n <= 256 * kMostPer) return f(Int<256>(), Int<kMostPer>(), Int<1>());
   if (n <= 512 * kMostPer) return f(Int<512>(), Int<kMostPer>(), Int<1>());
   if (n <= 1024 * kMostPer) return f(Int<1024>(), Int<kMostPer>(), Int<1>());
