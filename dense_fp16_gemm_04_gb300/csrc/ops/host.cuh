@@ -295,51 +295,74 @@ gemm_status_t launch_fused(gemm_ops_s* h, const Product& p, FusedArgs a, const S
 // The batched products (high and low parts) go by one matrix's tiles alone, so
 // that a matrix of a batch gets the same sums as by itself: the number of its
 // k-ranges is fixed, and the batch's tiles decide who sums them.
+enum Form { kPairs, kPairs2, kLone, kLone2, kLone4, kLone8, kWide, kForms };
+struct FormCosts {
+  static constexpr int64_t kNever = INT64_MAX;
+  int64_t small;  // tiles of lone CTAs
+  int64_t cost[kForms];
+  Form best() const { return static_cast<Form>(std::min_element(cost, cost + kForms) - cost); }
+  int64_t least() const { return cost[best()]; }
+};
+
+// Whether matrices of a batch are to get the same sums as by themselves.
+template <int kEpi>
+constexpr bool kBatched = kEpi == kEpiSplit || kEpi == kEpiSplitSym;
+// Which forms there are.  The loss's sums have tiles enough, or shares of the k-blocks.
+template <int kEpi>
+constexpr bool kSplits = kEpi != kEpiSum;
+template <int kEpi>
+constexpr bool kTwos = kSplits<kEpi> && kEpi != kEpiLse && kEpi != kEpiXent;
+
+// Of M x N sums over kb k-blocks, n times.  may_split false: a k-range of fewer k-blocks
+// than the launch was laid out for could be empty.
+template <int kEpi>
+FormCosts form_costs(const gemm_ops_s* h, int64_t M, int64_t N, int64_t kb, int64_t n, bool may_split) {
+  constexpr int64_t kNever = FormCosts::kNever;
+  const bool split = kSplits<kEpi> && may_split;
+  auto tiles = [&](int64_t tm, int64_t tn) { return Pair<kEpi>::kSym ? tn * (tn + 1) / 2 : tm * tn; };
+  const int64_t small = tiles(cdiv(M, 128), cdiv(N, Lone<kEpi>::kOutN)) * n;
+  const int64_t big = tiles(cdiv(M, 256), cdiv(N, Pair<kEpi>::kOutN)) * n;
+  const int64_t wide = cdiv(M, 128) * cdiv(N, 256);
+  const int* most = h->max_split;
+  FormCosts f = {small, {}};
+  std::fill(f.cost, f.cost + kForms, kNever);
+  if (h->max_pairs > 0) f.cost[kPairs] = cdiv(big, h->max_pairs) * (33 * kb + 500);
+  if (kTwos<kEpi> && split && h->max_twos > 0 && kb >= 4)
+    f.cost[kPairs2] = cdiv(big, h->max_twos) * (33 * cdiv(kb, 2) + 700);
+  f.cost[kLone] = cdiv(small, h->num_sms) * (27 * kb + 400);
+  if (split && small <= most[1] && kb >= 4) f.cost[kLone2] = 27 * cdiv(kb, 2) + 550;
+  if (split && small <= most[2] && kb >= (kBatched<kEpi> ? 4 : 8)) f.cost[kLone4] = 27 * cdiv(kb, 4) + 550;
+  if (split && !kBatched<kEpi> && small <= std::min(8, most[3]) && kb >= 16)
+    f.cost[kLone8] = 27 * cdiv(kb, 8) + 550;
+  if (kEpi == kEpiLse) f.cost[kWide] = cdiv(wide, h->num_sms) * (40 * kb + 450);
+  return f;
+}
+
 template <int kEpi>
 gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const Stack& c,
                     const Stack& d, cudaStream_t stream, int64_t* shares = nullptr) {
-  constexpr bool kBatched = kEpi == kEpiSplit || kEpi == kEpiSplitSym;
-  // The loss's sums have tiles enough, or shares of the k-blocks; a k-range of fewer
-  // k-blocks than it was laid out for could be empty.
-  constexpr bool kSplits = kEpi != kEpiSum, kTwos = kSplits && kEpi != kEpiLse && kEpi != kEpiXent;
-  const bool split = kSplits && !(Pair<kEpi>::kLive && a.live_k);
-  auto tiles = [&](int64_t tm, int64_t tn) { return Pair<kEpi>::kSym ? tn * (tn + 1) / 2 : tm * tn; };
-  const int64_t n = kBatched ? 1 : p.batch, kb = cdiv(p.K, 64) * p.segs;
-  const int64_t small = tiles(cdiv(p.M, 128), cdiv(p.N, Lone<kEpi>::kOutN)) * n;
-  const int64_t big = tiles(cdiv(p.M, 256), cdiv(p.N, Pair<kEpi>::kOutN)) * n;
-  constexpr bool kWides = kEpi == kEpiLse;
-  const int64_t wide = cdiv(p.M, 128) * cdiv(p.N, 256);
-  const int* most = h->max_split;
-  enum { kPairs, kPairs2, kLone, kLone2, kLone4, kLone8, kWide, kForms };
-  constexpr int64_t kNever = INT64_MAX;
-  const int64_t cost[kForms] = {
-      h->max_pairs > 0 ? cdiv(big, h->max_pairs) * (33 * kb + 500) : kNever,
-      kTwos && split && h->max_twos > 0 && kb >= 4 ? cdiv(big, h->max_twos) * (33 * cdiv(kb, 2) + 700) : kNever,
-      cdiv(small, h->num_sms) * (27 * kb + 400),
-      split && small <= most[1] && kb >= 4 ? 27 * cdiv(kb, 2) + 550 : kNever,
-      split && small <= most[2] && kb >= (kBatched ? 4 : 8) ? 27 * cdiv(kb, 4) + 550 : kNever,
-      split && !kBatched && small <= std::min(8, most[3]) && kb >= 16 ? 27 * cdiv(kb, 8) + 550 : kNever,
-      kWides ? cdiv(wide, h->num_sms) * (40 * kb + 450) : kNever};
-  switch (static_cast<int>(std::min_element(cost, cost + kForms) - cost)) {
+  const int64_t n = kBatched<kEpi> ? 1 : p.batch, kb = cdiv(cdiv(p.K, 64) * p.segs, std::max(1, a.k_slices));
+  const FormCosts f = form_costs<kEpi>(h, p.M, p.N, kb, n, !(Pair<kEpi>::kLive && a.live_k));
+  switch (f.best()) {
     case kPairs: return launch_fused<Pair<kEpi>>(h, p, a, c, d, stream, shares);
     case kPairs2:
-      if constexpr (kTwos) return launch_fused<TwoPairs<kEpi>>(h, p, a, c, d, stream, shares);
+      if constexpr (kTwos<kEpi>) return launch_fused<TwoPairs<kEpi>>(h, p, a, c, d, stream, shares);
       break;
     case kLone2:
-      if constexpr (kBatched)
-        if (small * p.batch > most[1]) return launch_fused<Lone<kEpi, 1, 2>>(h, p, a, c, d, stream, shares);
-      if constexpr (kSplits) return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream, shares);
+      if constexpr (kBatched<kEpi>)
+        if (f.small * p.batch > h->max_split[1]) return launch_fused<Lone<kEpi, 1, 2>>(h, p, a, c, d, stream, shares);
+      if constexpr (kSplits<kEpi>) return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream, shares);
       break;
     case kLone4:
-      if constexpr (kBatched)
-        if (small * p.batch > most[2]) return launch_fused<Lone<kEpi, 1, 4>>(h, p, a, c, d, stream, shares);
-      if constexpr (kSplits) return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream, shares);
+      if constexpr (kBatched<kEpi>)
+        if (f.small * p.batch > h->max_split[2]) return launch_fused<Lone<kEpi, 1, 4>>(h, p, a, c, d, stream, shares);
+      if constexpr (kSplits<kEpi>) return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream, shares);
       break;
     case kLone8:
-      if constexpr (kSplits && !kBatched) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream, shares);
+      if constexpr (kSplits<kEpi> && !kBatched<kEpi>) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream, shares);
       break;
     case kWide:
-      if constexpr (kWides) return launch_fused<WideLse>(h, p, a, c, d, stream, shares);
+      if constexpr (kEpi == kEpiLse) return launch_fused<WideLse>(h, p, a, c, d, stream, shares);
       break;
     default: break;
   }

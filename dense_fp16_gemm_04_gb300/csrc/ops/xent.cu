@@ -70,16 +70,21 @@ int64_t piece_columns(int64_t T, int64_t V) {
   return V <= most ? V : up(cdiv(V, cdiv(V, most)), 256);
 }
 
-// Shares of the k-blocks (64 entries of the vocabulary) that CTAs sum on their own for
-// dx of few tiles, 0 where a cluster's four or two are as good (27 x k-blocks + 550 of
-// the model in host.cuh, 400 more for adding the shares up): 4 x 1288 x 66557
-// 148 us with a cluster's, 121 with 13 shares.
+// Shares of the k-blocks (64 entries of the vocabulary) that are summed on their own for
+// dx of few tiles, 0 where the forms that finish dx at once take no longer by the model in
+// host.cuh: as many as lone CTAs or pairs run at once.  Writing the shares and adding them
+// up takes 4 us.  4 x 1288 x 66557 148 us with clusters of four, 121 with 13 shares.
+constexpr int64_t kAddShares = 400;
 int64_t dx_slices(const gemm_ops_s* h, int64_t T, int64_t D, int64_t V) {
-  const int64_t tiles = cdiv(T, 128) * cdiv(D, 128), kb = cdiv(V, 64);
-  const int64_t slices = std::min(h->num_sms / tiles, kb / 8);
-  if (slices < 2) return 0;
-  const int64_t cluster = 27 * cdiv(kb, tiles <= 36 ? 4 : 2) + 550;
-  return 27 * cdiv(kb, slices) + 800 < cluster ? slices : 0;
+  const int64_t kb = cdiv(V, 64);
+  int64_t slices = 0, least = form_costs<kEpiStoreLive>(h, T, D, kb, 1, true).least();
+  for (int64_t fit : {h->num_sms / (cdiv(T, 128) * cdiv(D, 128)), h->max_pairs / (cdiv(T, 256) * cdiv(D, 256))}) {
+    const int64_t s = std::min(fit, kb / 8);
+    if (s < 2) continue;
+    const int64_t cost = form_costs<kEpiSum>(h, T, D, cdiv(kb, s), s, false).least() + kAddShares;
+    if (cost < least) least = cost, slices = s;
+  }
+  return slices;
 }
 
 struct XentSpace {
@@ -267,7 +272,7 @@ gemm_status_t gemm_linear_cross_entropy_backward(gemm_ops_t h, const float* dlos
       } else if (whole) {
         a.k_slices = static_cast<int32_t>(sp.slices);
         a.c_zb = 1;
-        st = launch_fused<Lone<kEpiSum>>(h, p, a, {r.sum, T, D, D, sp.slices, T * D}, {}, s);
+        st = fused<kEpiSum>(h, p, a, {r.sum, T, D, D, sp.slices, T * D}, {}, s);
       } else {
         a.add = v0 > 0;
         st = fused<kEpiSum>(h, p, a, {r.sum, T, D, D, 1, T * D}, {}, s);
