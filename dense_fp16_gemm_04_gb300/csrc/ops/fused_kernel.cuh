@@ -176,9 +176,11 @@ __device__ __forceinline__ void xent_columns(const XentRow& r, int32_t col, floa
   }
 }
 
+constexpr int kSumKb = 128;  // 8192 products: 512 steps of the tensor cores
+
 template <int kCtas_, int kBN_, int kStages_, int kEpi_, int kEpiBufs_, int kSplit_ = 1, int kParts_ = 1>
 struct FusedCfg {
-  static constexpr int kParts = kParts_;  // accumulators of a tile, one per k-range
+  static constexpr int kParts = kParts_;  // accumulators of a tile, one per k-range (0: joined in registers)
   static constexpr int kSplit = kSplit_;  // CTAs sharing a tile, each a k-range
   static constexpr int kCluster = kCtas_ * kSplit_;
   static constexpr int kCtas = kCtas_;
@@ -188,14 +190,23 @@ struct FusedCfg {
   static constexpr int kEpiBufs = kEpiBufs_;  // 32 x 64 staging buffers per epilogue warp
   static constexpr bool kGlu = kEpi == kEpiGlu;
   static constexpr bool kSym = kEpi == kEpiSplitSym;
-  // The logits of the loss: sums of at most kPartKb k-blocks, added up in registers
-  // (of a split cluster: in kParts accumulators, added up as they are sent).  The
-  // tensor cores truncate a sum at each of its K / 16 steps, always towards zero:
-  // the loss of one token over 4096 products was off by 9e-6 of itself, of which
-  // 16 steps at a time leave 5e-7 (4096 tokens x 4096 x 131072: 2545 -> 2577 us).  The
-  // backward pass's logits the same: exp(z - lse) - 1 of a token that the model is sure of
-  // is the difference of two numbers whose errors then agree.
+  // The loss's products: sums of kPartKb k-blocks at a time, added up in registers (of a
+  // split cluster: in kParts accumulators, added up as they are sent).  The tensor cores
+  // truncate a sum at each of its K / 16 steps, always towards zero: the loss of one token
+  // over 4096 products was off by 9e-6 of itself, of which 16 steps at a time leave 5e-7
+  // (4096 tokens x 4096 x 131072: 2545 -> 2577 us).  The backward pass's logits the same:
+  // exp(z - lse) - 1 of a token that the model is sure of is the difference of two numbers
+  // that are both off by little.
+  //
+  // dx and dW: up to kSumKb k-blocks in one accumulator, longer sums in forms of their own
+  // (kParts 0, or a cluster's).  131072 products at a stretch lost 1.5e-4 of dx and 262144
+  // 2.6e-4, where fp16 rounds by 2.1e-4; of 8192 at a time 8e-6 are lost.  Every 2048 took
+  // longer (16384 tokens x 1024 x 32768 2250 -> 2345 us; at a stretch 2257).  Short
+  // sums keep a form without the registers: the 168 of the long one leave no room on an SM
+  // for the blocks of the next kernel (128 x 1032 x 8191: 32 us, 41 with the long form).
   static constexpr bool kPartial = kEpi == kEpiLse || kEpi == kEpiXent;
+  static constexpr bool kSums = kEpi == kEpiSum || kEpi == kEpiStoreLive;
+  static constexpr int kPartKb = kPartial ? 4 : kSums && kParts != 1 ? kSumKb : 0;
   static constexpr bool kLive = kEpi == kEpiXent || kEpi == kEpiSum || kEpi == kEpiStoreLive;
   static constexpr bool kReads = kEpi == kEpiGluBwd || kEpi == kEpiSplit || kSym;  // the epilogue reads too
   static constexpr int kOutN = kGlu ? kBN / 2 : kBN;  // output columns per tile
@@ -227,7 +238,7 @@ struct FusedCfg {
   static constexpr int kOffAbort = kOffSlot + 4;
   static constexpr int kSmemBytes = kOffAbort + 4 + 1024;  // + slack to align the base
   static constexpr int kAccBufs = kParts > 1 ? 1 : 2;  // tiles in tensor memory
-  static constexpr int kTmemCols = kAccBufs * kParts * kBN;
+  static constexpr int kTmemCols = kAccBufs * (kParts > 0 ? kParts : 1) * kBN;
   // Split clusters end in an epilogue of all eight warps; else warps 4 and on.
   static constexpr int kThreads = kSplit > 1 ? 256 : 128 + 32 * kEpiWarps;
   static constexpr uint32_t kIdesc = ptx::idesc_f16(kTileM, kBN, true);
@@ -236,7 +247,7 @@ struct FusedCfg {
   static_assert(!kSym || kTileM == kBN, "symmetric tiles are square");
   static_assert(kTmemCols <= 512, "TMEM columns");
   static_assert(kParts == 1 || (kSplit == 1 && (kEpi == kEpiSplit || kEpi == kEpiSplitSym)) ||
-                    (kSplit > 1 && kPartial),
+                    (kSplit > 1 && kPartKb > 0) || (kSplit == 1 && kSums && kParts == 0),
                 "parts");
   // The partials a split CTA receives (a lone one its own among them): 128 rows
   // x 128 columns in all, in the staging buffers' place.
@@ -245,12 +256,11 @@ struct FusedCfg {
                 "split clusters: lone CTAs on 128 x 128 tiles, two pairs on 256 x 256 ones");
 };
 
-constexpr int kPartKb = 4;  // 256 products: 16 steps of the tensor cores
-
-// Cfg::kPartial: k-blocks of a partial sum, of a k-range of n.
+// Cfg::kPartKb: k-blocks of a partial sum, of a k-range of n.  A split cluster's CTA has
+// kParts of them, longer ones where its range is.
 template <class Cfg>
 __device__ __forceinline__ int32_t part_length(int32_t n) {
-  return Cfg::kSplit > 1 ? max(kPartKb, (n + Cfg::kParts - 1) / Cfg::kParts) : kPartKb;
+  return Cfg::kSplit > 1 ? max(Cfg::kPartKb, (n + Cfg::kParts - 1) / Cfg::kParts) : Cfg::kPartKb;
 }
 
 // One tile, and a CTA's k-range of it.
@@ -486,6 +496,23 @@ __device__ __forceinline__ void read_columns(const FusedArgs& args, const FusedI
   }
 }
 
+// 16 columns of a split CTA's sums: its partial ones added up in order.
+template <class Cfg>
+__device__ __forceinline__ void load_parts(const FusedItem& wi, uint32_t t, uint32_t (&v)[16]) {
+  ptx::tmem_ld_32x32b_x16(t, v);
+  ptx::tmem_wait_ld(v);
+  if constexpr (Cfg::kParts > 1) {
+    const int32_t n = wi.kb1 - wi.kb0, length = part_length<Cfg>(n);
+    for (int32_t q = 1; q * length < n; ++q) {
+      uint32_t u[16];
+      ptx::tmem_ld_32x32b_x16(t + q * Cfg::kBN, u);
+      ptx::tmem_wait_ld(u);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
+    }
+  }
+}
+
 // The end of a split cluster's tile, run by all 256 threads of each CTA: lone
 // CTAs.
 template <class Cfg>
@@ -511,18 +538,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, const Fuse
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       uint32_t v[16];
-      ptx::tmem_ld_32x32b_x16(t_row + g * 16, v);
-      ptx::tmem_wait_ld(v);
-      if constexpr (Cfg::kParts > 1) {
-        const int32_t n = wi.kb1 - wi.kb0, length = part_length<Cfg>(n);
-        for (int32_t q = 1; q * length < n; ++q) {
-          uint32_t u[16];
-          ptx::tmem_ld_32x32b_x16(t_row + q * Cfg::kBN + g * 16, u);
-          ptx::tmem_wait_ld(u);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
-        }
-      }
+      load_parts<Cfg>(wi, t_row + g * 16, v);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = g * 16 + j * 4;  // of this side's 64
@@ -583,6 +599,7 @@ __device__ __forceinline__ void pair_split_epilogue(const FusedArgs& args, const
   const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
+  const FusedItem wi = fused_item<Cfg>(args, dims, unit, k);
   const bool ok = wait_bar_warp<true>(tfull, 0u, w, kSiteTmemFull, unit);
   const int r = q * 32 + lane;
   if (ok) {
@@ -593,15 +610,13 @@ __device__ __forceinline__ void pair_split_epilogue(const FusedArgs& args, const
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       uint32_t v[16];
-      ptx::tmem_ld_32x32b_x16(t_row + (k ^ 1) * kOut + side * kSide + g * 16, v);
-      ptx::tmem_wait_ld(v);
+      load_parts<Cfg>(wi, t_row + (k ^ 1) * kOut + side * kSide + g * 16, v);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         ptx::st_shared_cluster_v4(to + static_cast<uint32_t>((g * 4 + j) * 128) * 16u, v[4 * j], v[4 * j + 1],
                                   v[4 * j + 2], v[4 * j + 3]);
     }
   }
-  const FusedItem wi = fused_item<Cfg>(args, dims, unit, k);
   const int32_t row = wi.mb * Cfg::kTileM + static_cast<int32_t>(cta) * Cfg::kBM + r;
   const int32_t col0 = wi.nb * Cfg::kOutN + k * kOut + side * kN;
   const bool in = row < dims.rows && col0 < args.N;
@@ -611,8 +626,7 @@ __device__ __forceinline__ void pair_split_epilogue(const FusedArgs& args, const
   if (!ok) return;
   auto sum = [&](int col, int group4, float (&v)[16]) {  // every lane: tensor memory
     uint32_t t[16];
-    ptx::tmem_ld_32x32b_x16(t_row + col, t);
-    ptx::tmem_wait_ld(t);
+    load_parts<Cfg>(wi, t_row + col, t);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 p = ptx::ld_shared_v4_f32(recv + static_cast<uint32_t>((group4 + i) * 128 + r) * 16u);
@@ -809,7 +823,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const FusedItem wi = fused_item<Cfg>(args, dims, it, rank);
         int32_t kb = wi.kb0;
         do {  // once, or for each partial sum
-          const int32_t end = Cfg::kPartial && Cfg::kSplit == 1 ? min(wi.kb1, kb + kPartKb) : wi.kb1;
+          const int32_t end = Cfg::kPartKb > 0 && Cfg::kSplit == 1 ? min(wi.kb1, kb + Cfg::kPartKb) : wi.kb1;
           const int buf = acc_iter % Cfg::kAccBufs;
           const uint32_t use_par = static_cast<uint32_t>((acc_iter / Cfg::kAccBufs) & 1);
           if (!wait_bar_warp<kPair>(bar_tempty(buf), use_par ^ 1u, w, kSiteTmemEmpty, it)) {
@@ -820,8 +834,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * Cfg::kBN);
           int32_t first = kb, part = 0;  // first k-block of the current accumulator
           for (; kb < end; ++kb) {
-            if (Cfg::kParts > 1 &&
-                kb == (Cfg::kPartial ? first + part_length<Cfg>(wi.kb1 - wi.kb0) : (part + 1) * wi.kb1 / Cfg::kParts)) {
+            if (Cfg::kParts > 1 && kb == (Cfg::kPartKb > 0 ? first + part_length<Cfg>(wi.kb1 - wi.kb0)
+                                                           : (part + 1) * wi.kb1 / Cfg::kParts)) {
               ++part;
               first = kb;
               d_tmem += Cfg::kBN;
@@ -893,18 +907,17 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       ++used;
       return b;
     };
-    // A 32 x 64 chunk (row `lane`, columns packed in pairs) through a swizzled
-    // buffer to rows row0.., columns col0.. of matrix z.  Every buffer taken
+    // A 32 x 64 chunk (row `lane`, columns in pairs: word(0) .. word(31)) through a
+    // swizzled buffer to rows row0.., columns col0.. of matrix z.  Every buffer taken
     // commits one group, empty where nothing of the chunk is in range, so that
     // the count in take_buf holds.
-    auto store_chunk = [&](const CUtensorMap* m, const uint32_t (&packed)[32], int32_t col0,
-                           int32_t row0, int32_t z, bool in) {
+    auto store_words = [&](const CUtensorMap* m, auto word, int32_t col0, int32_t row0, int32_t z, bool in) {
       const uint32_t sbuf = take_buf();
       const uint32_t row_addr = sbuf + static_cast<uint32_t>(lane) * 128u;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        ptx::st_shared_v4(row_addr + ((static_cast<uint32_t>(j) ^ (lane & 7u)) << 4), packed[4 * j],
-                          packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+        ptx::st_shared_v4(row_addr + ((static_cast<uint32_t>(j) ^ (lane & 7u)) << 4), word(4 * j), word(4 * j + 1),
+                          word(4 * j + 2), word(4 * j + 3));
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -917,6 +930,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         ptx::bulk_commit_group();
       }
     };
+    auto store_chunk = [&](const CUtensorMap* m, const uint32_t (&packed)[32], int32_t col0, int32_t row0, int32_t z,
+                           bool in) { store_words(m, [&](int i) { return packed[i]; }, col0, row0, z, in); };
     // The same chunk transposed: 64 rows of 32 columns, unswizzled (a warp's
     // 2-byte stores of one column are 64 contiguous bytes).
     auto store_chunk_t = [&](const uint32_t (&packed)[32], int32_t col0, int32_t row0, int32_t z,
@@ -935,28 +950,47 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         ptx::bulk_commit_group();
       }
     };
-    if constexpr (Cfg::kPartial) {
-      // Each warp for itself: 32 rows, and this group's 64 columns of the tile.
+    // dx, dW: a 32 x 64 chunk of sums.
+    auto store_sums = [&](auto sum, int32_t col0, int32_t row0, int32_t row, bool row_in, int32_t batch) {
+      if constexpr (Cfg::kEpi == kEpiSum) {
+#pragma unroll
+        for (int half = 0; half < 64; half += 32)
+          store_words(&tmC, [&](int i) { return __float_as_uint(sum(half + i)); }, col0 + half, row0, batch * args.c_zb,
+                      col0 + half < args.N);
+      } else if constexpr (Cfg::kEpi == kEpiStoreLive) {
+        auto word = [&](int i) { return pack16(bf16, alpha * sum(2 * i), alpha * sum(2 * i + 1)); };
+        if (!args.row_map) {
+          store_words(&tmC, word, col0, row0, 0, true);
+        } else if (row_in) {  // each row to its own place: 128 bytes a lane
+          uint16_t* to = args.c + static_cast<int64_t>(args.row_map[row]) * args.ldc + col0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (col0 + 8 * j < args.N)  // (a multiple of 8)
+              ptx::st_global_v4(to + 8 * j, word(4 * j), word(4 * j + 1), word(4 * j + 2), word(4 * j + 3));
+        }
+      }
+    };
+    if constexpr (Cfg::kPartKb > 0) {
+      // Each warp for itself: 32 rows, and this group's columns of the tile.
       constexpr int kCols = Cfg::kOutN / Cfg::kGroups;
+      constexpr int kLoad = kCols > 64 ? 8 : 16;  // (128 sums and 16 loads do not fit in registers)
       bool ok = true;
       for (int32_t it = unit; ok && it < dims.items; it += units) {
         const FusedItem wi = fused_item<Cfg>(args, dims, it, rank);
         const int32_t row0 = wi.mb * Cfg::kTileM + static_cast<int32_t>(cta) * Cfg::kBM + q * 32, row = row0 + lane;
         const int32_t col0 = wi.nb * Cfg::kOutN + group * kCols;
         const bool row_in = row < dims.rows;
-        const bool idle = row0 >= dims.rows || col0 >= args.N;  // none of the warp's logits counts
+        const bool idle = row0 >= dims.rows || col0 >= args.N;  // none of the warp's sums counts
         int64_t target = -1;
         XentRow xr = {};
         if (row_in) {
-          if constexpr (Cfg::kEpi == kEpiLse)
-            target = args.targets[row] - col0;
-          else
-            xr = args.xent_rows[row];
+          if constexpr (Cfg::kEpi == kEpiLse) target = args.targets[row] - col0;
+          if constexpr (Cfg::kEpi == kEpiXent) xr = args.xent_rows[row];
         }
         float z[kCols];
 #pragma unroll
         for (int i = 0; i < kCols; ++i) z[i] = 0.0f;
-        for (int32_t kb = wi.kb0; kb < wi.kb1; kb += kPartKb) {
+        for (int32_t kb = wi.kb0; kb < wi.kb1; kb += Cfg::kPartKb) {
           const int buf = acc_iter % Cfg::kAccBufs;
           const uint32_t use_par = static_cast<uint32_t>((acc_iter / Cfg::kAccBufs) & 1);
           ++acc_iter;
@@ -967,12 +1001,15 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                                  static_cast<uint32_t>(buf * Cfg::kBN + group * kCols);
           if (!idle) {
 #pragma unroll
-            for (int c = 0; c < kCols; c += 16) {
-              uint32_t v[16];
-              ptx::tmem_ld_32x32b_x16(t_row + c, v);
+            for (int c = 0; c < kCols; c += kLoad) {
+              uint32_t v[kLoad];
+              if constexpr (kLoad == 8)
+                ptx::tmem_ld_32x32b_x8(t_row + c, v);
+              else
+                ptx::tmem_ld_32x32b_x16(t_row + c, v);
               ptx::tmem_wait_ld(v);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) z[c + i] += __uint_as_float(v[i]);
+              for (int i = 0; i < kLoad; ++i) z[c + i] += __uint_as_float(v[i]);
             }
           }
           ptx::tc_fence_before();
@@ -1002,6 +1039,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           if (row_in)
             args.shares[(static_cast<int64_t>(wi.nb) * Cfg::kGroups + group) * args.M + row] =
                 make_float2(share_m, share_s);
+        } else if constexpr (Cfg::kSums) {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 64)
+            if (!idle && col0 + c < args.N)
+              store_sums([&](int i) { return z[c + i]; }, col0 + c, row0, row, row_in, wi.batch);
         } else if (row0 < args.M && col0 < args.N) {
           // Rows behind the last: zeros, up to a whole k-block of the next product.
           static_assert(Cfg::kEpi != kEpiXent || kCols == 64, "one staging buffer");
@@ -1078,7 +1120,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const int32_t col0 = wi.nb * Cfg::kOutN + c * 64;
         const bool in = row0 < args.M && col0 < args.N;
         const bool last = c + Cfg::kGroups >= kChunks;
-        if constexpr (Cfg::kEpi == kEpiStore || Cfg::kEpi == kEpiStoreLive) {
+        if constexpr (Cfg::kEpi == kEpiStore) {
           uint32_t v0[32], v1[32], packed[32];
           ptx::tmem_ld_32x32b_x32(t_row + c * 64, v0);
           ptx::tmem_ld_32x32b_x32(t_row + c * 64 + 32, v1);
@@ -1087,30 +1129,22 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           if (last) release_tmem();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            packed[i] = pack16(bf16, alpha * __uint_as_float(v0[2 * i]), alpha * __uint_as_float(v0[2 * i + 1]));
-            packed[16 + i] = pack16(bf16, alpha * __uint_as_float(v1[2 * i]), alpha * __uint_as_float(v1[2 * i + 1]));
+            packed[i] = pack16(bf16, args.alpha * __uint_as_float(v0[2 * i]),
+                               args.alpha * __uint_as_float(v0[2 * i + 1]));
+            packed[16 + i] = pack16(bf16, args.alpha * __uint_as_float(v1[2 * i]),
+                                    args.alpha * __uint_as_float(v1[2 * i + 1]));
           }
-          if (Cfg::kEpi == kEpiStoreLive && args.row_map) {
-            // Each row to its own place: 128 bytes a lane.
-            if (row_in) {
-              uint16_t* to = args.c + static_cast<int64_t>(args.row_map[row]) * args.ldc + col0;
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (col0 + 8 * j < args.N)  // (a multiple of 8)
-                  ptx::st_global_v4(to + 8 * j, packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
-            }
-          } else {
-            store_chunk(&tmC, packed, col0, row0, wi.batch * args.c_zb, in);
-          }
-        } else if constexpr (Cfg::kEpi == kEpiSum) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t v[32];
-            ptx::tmem_ld_32x32b_x32(t_row + c * 64 + half * 32, v);
-            ptx::tmem_wait_ld(v);
-            if (half == 1 && last) release_tmem();
-            store_chunk(&tmC, v, col0 + half * 32, row0, wi.batch * args.c_zb, in && col0 + half * 32 < args.N);
-          }
+          store_chunk(&tmC, packed, col0, row0, wi.batch * args.c_zb, in);
+        } else if constexpr (Cfg::kSums) {
+          uint32_t v0[32], v1[32];
+          ptx::tmem_ld_32x32b_x32(t_row + c * 64, v0);
+          ptx::tmem_ld_32x32b_x32(t_row + c * 64 + 32, v1);
+          ptx::tmem_wait_ld(v0);
+          ptx::tmem_regs_ready(v1);
+          if (last) release_tmem();
+          if (row0 < dims.rows && col0 < args.N)
+            store_sums([&](int i) { return __uint_as_float(i < 32 ? v0[i & 31] : v1[i & 31]); }, col0, row0, row, row_in,
+                       wi.batch);
         } else if constexpr (Cfg::kEpi == kEpiGlu) {
           uint32_t h[32], gp[32], up[32];
 #pragma unroll

@@ -48,11 +48,15 @@ template <int kEpi>
 using Pair = FusedCfg<2, 256, kEpi == kEpiLse ? 7 : kEpi == kEpiStore ? 6 : 5, kEpi,
                       kEpi == kEpiLse ? 0 : kEpi == kEpiStore || kEpi == kEpiXent ? 1 : epi_bufs(kEpi)>;
 template <int kEpi>
-using TwoPairs = FusedCfg<2, 256, 5, kEpi, epi_bufs(kEpi), 2>;  // one tile, half of its k-blocks each
+using TwoPairs = FusedCfg<2, 256, 5, kEpi, epi_bufs(kEpi), 2, kEpi == kEpiStoreLive ? 2 : 1>;  // one tile, half of its k-blocks each
 template <int kEpi, int kSplit = 1, int kParts = 1>
 using Lone = FusedCfg<1, 128, kEpi == kEpiLse && kSplit == 1 ? 7 : 5, kEpi,
                       kEpi == kEpiLse && kSplit == 1 ? 0 : epi_bufs(kEpi), kSplit,
-                      ((kEpi == kEpiLse || kEpi == kEpiXent) && kSplit > 1) ? 4 : kParts>;
+                      ((kEpi == kEpiLse || kEpi == kEpiXent || kEpi == kEpiStoreLive) && kSplit > 1) ? 4 : kParts>;
+
+// dx and dW of long sums.
+template <class Cfg>
+using Long = FusedCfg<Cfg::kCtas, Cfg::kBN, Cfg::kStages, Cfg::kEpi, Cfg::kEpiBufs, 1, 0>;
 
 // One CTA on 128 x 256 logits of the loss, for the rounds that tiles of a pair or of 128
 // columns fill badly: 1 token, 4096 x 32000 49.5 -> 45.1 us, 101 x 512 x 32000 13.4 ->
@@ -324,15 +328,18 @@ FormCosts form_costs(const gemm_ops_s* h, int64_t M, int64_t N, int64_t kb, int6
   const int64_t big = tiles(cdiv(M, 256), cdiv(N, Pair<kEpi>::kOutN)) * n;
   const int64_t wide = cdiv(M, 128) * cdiv(N, 256);
   const int* most = h->max_split;
+  // k-blocks that a cluster's CTA has room to sum: dx's four or (of pairs) two accumulators.
+  const int64_t room = kEpi == kEpiStoreLive ? 4 * kSumKb : kNever / 8;
+  const int64_t room_two = kEpi == kEpiStoreLive ? 2 * kSumKb : kNever / 8;
   FormCosts f = {small, {}};
   std::fill(f.cost, f.cost + kForms, kNever);
   if (h->max_pairs > 0) f.cost[kPairs] = cdiv(big, h->max_pairs) * (33 * kb + 500);
-  if (kTwos<kEpi> && split && h->max_twos > 0 && kb >= 4)
+  if (kTwos<kEpi> && split && h->max_twos > 0 && kb >= 4 && kb <= 2 * room_two)
     f.cost[kPairs2] = cdiv(big, h->max_twos) * (33 * cdiv(kb, 2) + 700);
   f.cost[kLone] = cdiv(small, h->num_sms) * (27 * kb + 400);
-  if (split && small <= most[1] && kb >= 4) f.cost[kLone2] = 27 * cdiv(kb, 2) + 550;
-  if (split && small <= most[2] && kb >= (kBatched<kEpi> ? 4 : 8)) f.cost[kLone4] = 27 * cdiv(kb, 4) + 550;
-  if (split && !kBatched<kEpi> && small <= std::min(8, most[3]) && kb >= 16)
+  if (split && small <= most[1] && kb >= 4 && kb <= 2 * room) f.cost[kLone2] = 27 * cdiv(kb, 2) + 550;
+  if (split && small <= most[2] && kb >= (kBatched<kEpi> ? 4 : 8) && kb <= 4 * room) f.cost[kLone4] = 27 * cdiv(kb, 4) + 550;
+  if (split && !kBatched<kEpi> && small <= std::min(8, most[3]) && kb >= 16 && kb <= 8 * room)
     f.cost[kLone8] = 27 * cdiv(kb, 8) + 550;
   if (kEpi == kEpiLse) f.cost[kWide] = cdiv(wide, h->num_sms) * (40 * kb + 450);
   return f;
@@ -343,7 +350,13 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
                     const Stack& d, cudaStream_t stream, int64_t* shares = nullptr) {
   const int64_t n = kBatched<kEpi> ? 1 : p.batch, kb = cdiv(cdiv(p.K, 64) * p.segs, std::max(1, a.k_slices));
   const FormCosts f = form_costs<kEpi>(h, p.M, p.N, kb, n, !(Pair<kEpi>::kLive && a.live_k));
-  switch (f.best()) {
+  const Form form = f.best();
+  if constexpr (Lone<kEpi>::kSums)
+    if (kb > kSumKb) {
+      if (form == kPairs) return launch_fused<Long<Pair<kEpi>>>(h, p, a, c, d, stream, shares);
+      if (form == kLone) return launch_fused<Long<Lone<kEpi>>>(h, p, a, c, d, stream, shares);
+    }
+  switch (form) {
     case kPairs: return launch_fused<Pair<kEpi>>(h, p, a, c, d, stream, shares);
     case kPairs2:
       if constexpr (kTwos<kEpi>) return launch_fused<TwoPairs<kEpi>>(h, p, a, c, d, stream, shares);

@@ -10,11 +10,13 @@ bool xent_setup(gemm_ops_s* h) {
       !set_attr<Lone<kEpiLse, 4>>() || !set_attr<Lone<kEpiLse, 8>>() || !set_attr<Pair<kEpiXent>>() ||
       !set_attr<Lone<kEpiXent>>() || !set_attr<Lone<kEpiXent, 2>>() || !set_attr<Lone<kEpiXent, 4>>() ||
       !set_attr<Lone<kEpiXent, 8>>() || !set_attr<Pair<kEpiSum>>() || !set_attr<Lone<kEpiSum>>() ||
-      !set_attr<Pair<kEpiStoreLive>>() || !set_attr<TwoPairs<kEpiStoreLive>>() || !set_attr<Lone<kEpiStoreLive>>() ||
+      !set_attr<Long<Pair<kEpiSum>>>() || !set_attr<Long<Lone<kEpiSum>>>() || !set_attr<Long<Pair<kEpiStoreLive>>>() ||
+      !set_attr<Long<Lone<kEpiStoreLive>>>() || !set_attr<Pair<kEpiStoreLive>>() || !set_attr<TwoPairs<kEpiStoreLive>>() || !set_attr<Lone<kEpiStoreLive>>() ||
       !set_attr<Lone<kEpiStoreLive, 2>>() || !set_attr<Lone<kEpiStoreLive, 4>>() || !set_attr<Lone<kEpiStoreLive, 8>>())
     return false;
   h->max_pairs = std::min({h->max_pairs, max_clusters<Pair<kEpiLse>>(), max_clusters<Pair<kEpiXent>>(),
-                           max_clusters<Pair<kEpiSum>>(), max_clusters<Pair<kEpiStoreLive>>()});
+                           max_clusters<Pair<kEpiSum>>(), max_clusters<Pair<kEpiStoreLive>>(),
+                           max_clusters<Long<Pair<kEpiSum>>>(), max_clusters<Long<Pair<kEpiStoreLive>>>()});
   h->max_twos = std::min(h->max_twos, max_clusters<TwoPairs<kEpiStoreLive>>());
   return true;
 }
