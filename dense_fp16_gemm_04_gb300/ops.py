@@ -344,7 +344,10 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, save=False, out=None, stream
     (None for 1 and 0; a bias needs a weight).  Returns y, of x's type, and with
     ``save`` also stats [T, 2] float32, m and r, that :func:`layer_norm_backward`
     takes.  Rows may be strided."""
-    o = _of(x, ops)  # not through the method: one row takes the host 4.2 us, and 4.7 through it
+    o = _of(x, ops)
+    if ops is not None:
+        return o.layer_norm(x, weight, bias, eps, save, out, stream)
+    # Not through the method: one row takes the host 4.2 us, and 4.7 through it.
     return o._b.layer_norm(o._addr, o.index, x, weight, bias, eps, save, out, stream)
 
 
@@ -353,6 +356,8 @@ def layer_norm_backward(dy, x, weight, stats, bias=True, stream=None, ops: Ops |
     is None where weight is, dbias (of weight's type, x's without one) where ``bias``
     is false."""
     o = _of(x, ops)
+    if ops is not None:
+        return o.layer_norm_backward(dy, x, weight, stats, bias, stream)
     return o._b.layer_norm_backward(o._addr, o.index, dy, x, weight, stats, bias, stream)
 
 
@@ -360,6 +365,8 @@ def rms_norm(x, weight=None, eps=1e-6, save=False, out=None, stream=None, ops: O
     """y = x r weight for each row of x [T, D], with r = 1 / sqrt(mean x^2 + eps).
     As :func:`layer_norm`; stats are [T, 1], r alone."""
     o = _of(x, ops)
+    if ops is not None:
+        return o.rms_norm(x, weight, eps, save, out, stream)
     return o._b.rms_norm(o._addr, o.index, x, weight, None, eps, save, out, stream)
 
 
@@ -367,6 +374,8 @@ def rms_norm_backward(dy, x, weight, stats, stream=None, ops: Ops | None = None)
     """Gradients (dx, dweight) of :func:`rms_norm` from dy [T, D]; dweight is None
     where weight is."""
     o = _of(x, ops)
+    if ops is not None:
+        return o.rms_norm_backward(dy, x, weight, stats, stream)
     return o._b.rms_norm_backward(o._addr, o.index, dy, x, weight, stats, False, stream)
 
 
