@@ -184,10 +184,8 @@ struct Vec<X, 2> {
 };
 template <class X>
 struct Vec<X, 1> {
-  static constexpr int kBytes = sizeof(X);
   X r;
   __device__ void load(const X* p) { r = *p; }
-  __device__ void load_shared(uint32_t addr) { r = __uint_as_float(ptx::ld_shared_u32(addr)); }  // (of fp32 alone)
   __device__ void get(Reg<1>& f) const { f.v[0] = widen(r); }
   static __device__ void store(X* p, const Reg<1>& f) { narrow(f.v[0], p); }
 };
@@ -421,6 +419,7 @@ constexpr size_t back_ring(int threads) {
 template <class X, class W, bool kRms, int kVec, int kTeam, int kPer, int kTeams>
 __global__ void __launch_bounds__(kTeam* kTeams, 512 / (kTeam * kTeams) > 0 ? 512 / (kTeam * kTeams) : 1)
     norm_rows_back(const NormArgs a) {
+  static_assert(kVec >= 2, "copies of 4 or 16 bytes");
   extern __shared__ __align__(16) uint8_t ring[];  // then the sums, where kTeams > 1
   __shared__ float sm[kTeam > 32 ? kTeams * 128 : 1];
   constexpr int kThreads = kTeam * kTeams, kSlots = back_slots(kThreads, kPer);
