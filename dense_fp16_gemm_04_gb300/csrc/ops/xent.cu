@@ -254,7 +254,8 @@ gemm_status_t gemm_linear_cross_entropy_backward(gemm_ops_t h, const float* dlos
     {  // dz, from the logits x W^T: at least one tile, of zeros, for dW
       const Product p = {T, n, D, xs, wv, false, false, bf16, 1, 1};
       FusedArgs a = base_args(h, p);
-      a.early = v0 > 0 ? kEarlyA | kEarlyB | kEarlyLive : kEarlyB;
+      // (The first needs `live`, which the kernel before it writes, to know its tiles at all.)
+      if (v0 > 0) a.early = kEarlyA | kEarlyB | kEarlyLive;
       a.live = r.live;
       a.live_min = 1;
       a.group_m = logits_group(D);
