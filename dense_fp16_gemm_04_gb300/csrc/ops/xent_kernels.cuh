@@ -13,8 +13,9 @@
 // Backward: the logits come again, and dz, a piece of the vocabulary at a time, is
 // rounded to 16 bits as an operand of the two products.  In fp16 dz of a mean over
 // thousands of tokens would be lost below 6e-8, so dz is held times 2^14 / 2^e, 2^e
-// the power of two above the largest |dloss| and |dloss + dlse|: at most 2^15, and
-// exact to 2^-40 of the largest.  The products undo it in fp32.
+// the power of two above the largest |dloss| and |dloss + dlse|: below 2^15, and
+// off by at most 2^-25, half of fp16's last step, where the largest is 2^13 at least:
+// by 2^-38 of it.  The products undo it in fp32.
 //
 // Tokens without a gradient (ignored ones, a prompt's) take no part: xent_pack copies
 // the others' x side by side, and the three products run on those alone.  Where an

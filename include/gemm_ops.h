@@ -240,8 +240,8 @@ GEMM_API gemm_status_t gemm_linear_cross_entropy(gemm_ops_t ops, const void* x, 
  *   lse         : [T] fp32, contiguous
  *   dx : [T, D];  dw : [V, D], contiguous
  * The logits are computed again, a piece of the vocabulary at a time.  dz is rounded to
- * 16 bits as an operand, in fp16 scaled by a power of two so that entries down to 2^-40
- * of the largest |dloss| (|dloss + dlse|) of the call count.  A token whose dloss and
+ * 16 bits as an operand, in fp16 scaled by a power of two: entries are off by at most
+ * 2^-38 of the largest |dloss| (|dloss + dlse|) of the call, and those above that count.  A token whose dloss and
  * dlse are 0 (or which is ignored, without dlse) takes no part, whatever its x holds, and
  * costs nothing: its dx is 0.
  * Gradients are written, not accumulated; T == 0 gives zero dw.  Rules as above.
