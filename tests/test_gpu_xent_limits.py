@@ -1,7 +1,9 @@
-"""The loss's gradients at the ends of their ranges: the smallest entries that
-fp16's dz holds."""
+"""The loss's gradients at the ends of their ranges: dz of more than 2^31 elements, and the
+smallest entries that fp16's dz holds."""
 import pytest
 import torch
+
+from test_gpu_xent import backward_ref, check, make, sum_eps
 
 pytestmark = pytest.mark.gpu
 
@@ -13,6 +15,33 @@ def g():
     import dense_fp16_gemm_04_gb300 as m
     m.build()
     return m
+
+
+def test_dz_of_more_than_2_to_31_elements(g):
+    """Tokens with a gradient are packed side by side, so that only those reach far: their dz
+    alone has 2.29e9 elements, of which rows 524288 and on start past 2^31 and 2^32 bytes."""
+    T, D, V = 700_000, 64, 4096
+    x, w, targets, dloss = make(T, D, V, torch.bfloat16, seed=11)
+    dloss = dloss * T
+    live = torch.nonzero(targets >= 0)[:, 0]
+    assert len(live) * V > 2 ** 31
+    _, lse = g.linear_cross_entropy(x, w, targets, save=True)
+    dx, dw = g.linear_cross_entropy_backward(dloss, x, w, targets, lse)
+    g.default_ops().check_error()
+    # Packed rows around 2^31 elements, around 2^32 bytes (the same row), and the last ones.
+    pick = torch.cat((live[:200], live[524_188:524_388], live[-300:], live[torch.randint(524_288, len(live), (1000,), device="cuda")]))
+    rx, _ = backward_ref(dloss[pick], None, x[pick], w, targets[pick], lse[pick], x.dtype)
+    check(dx[pick], *rx, "dx")
+    assert not dx[targets < 0].any()
+    ref, err = torch.zeros(V, D, dtype=F64, device="cuda"), torch.zeros(V, D, dtype=F64, device="cuda")
+    part = 30_000
+    for a in range(0, T, part):
+        b = slice(a, a + part)
+        _, (r, e) = backward_ref(dloss[b], None, x[b], w, targets[b], lse[b], x.dtype)
+        ref += r
+        err += e
+    # (each part's bound has sum_eps of its own tokens; the sums of all of them pass on as many times more)
+    check(dw, ref, err + sum_eps(T) / sum_eps(part) * err, "dw")
 
 
 @pytest.mark.parametrize("top", [1.0, 1.99])
