@@ -177,6 +177,7 @@ __device__ __forceinline__ void xent_columns(const XentRow& r, int32_t col, floa
 }
 
 constexpr int kSumKb = 128;  // 8192 products: 512 steps of the tensor cores
+constexpr int kSplitKb = 8;  // 512 products
 
 template <int kCtas_, int kBN_, int kStages_, int kEpi_, int kEpiBufs_, int kSplit_ = 1, int kParts_ = 1>
 struct FusedCfg {
@@ -190,23 +191,27 @@ struct FusedCfg {
   static constexpr int kEpiBufs = kEpiBufs_;  // 32 x 64 staging buffers per epilogue warp
   static constexpr bool kGlu = kEpi == kEpiGlu;
   static constexpr bool kSym = kEpi == kEpiSplitSym;
-  // The loss's products: sums of kPartKb k-blocks at a time, added up in registers (of a
-  // split cluster: in kParts accumulators, added up as they are sent).  The tensor cores
-  // truncate a sum at each of its K / 16 steps, always towards zero: the loss of one token
-  // over 4096 products was off by 9e-6 of itself, of which 16 steps at a time leave 5e-7
-  // (4096 tokens x 4096 x 131072: 2545 -> 2577 us).  The backward pass's logits the same:
-  // exp(z - lse) - 1 of a token that the model is sure of is the difference of two numbers
-  // that are both off by little.
+  // The loss's products: sums of kPartKb k-blocks at a time, added up in registers.  The
+  // tensor cores truncate a sum at each of its K / 16 steps, always towards zero: the loss
+  // of one token over 4096 products was off by 9e-6 of itself, of which 16 steps at a time
+  // leave 5e-7 (4096 tokens x 4096 x 131072: 2545 -> 2577 us).  The backward pass's logits
+  // the same: exp(z - lse) - 1 of a token that the model is sure of is the difference of two
+  // numbers that are both off by little.  Of a split cluster, kParts accumulators that are
+  // added up as they are sent, up to kSplitKb k-blocks in each; longer ranges (kParts 0)
+  // go to registers, kSplitKb at a time (collect_parts).
   //
   // dx and dW: up to kSumKb k-blocks in one accumulator, longer sums in forms of their own
-  // (kParts 0, or a cluster's).  131072 products at a stretch lost 1.5e-4 of dx and 262144
+  // (kParts 0; of a split cluster kParts accumulators).  131072 products at a stretch lost 1.5e-4 of dx and 262144
   // 2.6e-4, where fp16 rounds by 2.1e-4; of 8192 at a time 8e-6 are lost.  Every 2048 took
   // longer (16384 tokens x 1024 x 32768 2250 -> 2345 us; at a stretch 2257).  Short
   // sums keep a form without the registers: the 168 of the long one leave no room on an SM
   // for the blocks of the next kernel (128 x 1032 x 8191: 32 us, 41 with the long form).
   static constexpr bool kPartial = kEpi == kEpiLse || kEpi == kEpiXent;
   static constexpr bool kSums = kEpi == kEpiSum || kEpi == kEpiStoreLive;
-  static constexpr int kPartKb = kPartial ? 4 : kSums && kParts != 1 ? kSumKb : 0;
+  static constexpr int kPartKb =
+      kPartial ? (kSplit > 1 && kParts == 0 ? kSplitKb : 4) : kSums && kParts != 1 ? kSumKb : 0;
+  static constexpr bool kHands = kPartKb > 0 && kParts <= 1;  // partial sums go to registers one by one
+  static constexpr bool kCollect = kHands && kSplit > 1;
   static constexpr bool kLive = kEpi == kEpiXent || kEpi == kEpiSum || kEpi == kEpiStoreLive;
   static constexpr bool kReads = kEpi == kEpiGluBwd || kEpi == kEpiSplit || kSym;  // the epilogue reads too
   static constexpr int kOutN = kGlu ? kBN / 2 : kBN;  // output columns per tile
@@ -247,7 +252,7 @@ struct FusedCfg {
   static_assert(!kSym || kTileM == kBN, "symmetric tiles are square");
   static_assert(kTmemCols <= 512, "TMEM columns");
   static_assert(kParts == 1 || (kSplit == 1 && (kEpi == kEpiSplit || kEpi == kEpiSplitSym)) ||
-                    (kSplit > 1 && kPartKb > 0) || (kSplit == 1 && kSums && kParts == 0),
+                    (kSplit > 1 && kPartKb > 0) || (kSums && kParts == 0),
                 "parts");
   // The partials a split CTA receives (a lone one its own among them): 128 rows
   // x 128 columns in all, in the staging buffers' place.
@@ -256,11 +261,10 @@ struct FusedCfg {
                 "split clusters: lone CTAs on 128 x 128 tiles, two pairs on 256 x 256 ones");
 };
 
-// Cfg::kPartKb: k-blocks of a partial sum, of a k-range of n.  A split cluster's CTA has
-// kParts of them, longer ones where its range is.
+// k-blocks of one of the kParts accumulators of a split CTA, of a k-range of n.
 template <class Cfg>
 __device__ __forceinline__ int32_t part_length(int32_t n) {
-  return Cfg::kSplit > 1 ? max(Cfg::kPartKb, (n + Cfg::kParts - 1) / Cfg::kParts) : Cfg::kPartKb;
+  return max(Cfg::kPartKb, (n + Cfg::kParts - 1) / Cfg::kParts);
 }
 
 // One tile, and a CTA's k-range of it.
@@ -513,6 +517,45 @@ __device__ __forceinline__ void load_parts(const FusedItem& wi, uint32_t t, uint
   }
 }
 
+// A split CTA's partial sums of logits: four warps (2 to 5) add them up while the next are
+// made, each 32 rows of 128 columns, and send them as split_epilogue would.  The loss of
+// one token, 16384 x 9000, is off by 3e-6 so; with four accumulators for the whole range it
+// was by 1.3e-5 (52.0 -> 52.7 us; 3 tokens, 8192 x 5000: 21.4 -> 22.2).
+template <class Cfg>
+__device__ __forceinline__ void collect_parts(const FusedItem& wi, int32_t rank, uint32_t tmem_base, uint32_t recv,
+                                              uint32_t tfull0, uint32_t tempty0, const Watch& w) {
+  constexpr int kCols = 128 / Cfg::kSplit;
+  const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  float z[128];
+#pragma unroll
+  for (int i = 0; i < 128; ++i) z[i] = 0.0f;
+  int32_t acc_iter = 0;
+  for (int32_t kb = wi.kb0; kb < wi.kb1; kb += Cfg::kPartKb, ++acc_iter) {
+    const int buf = acc_iter % Cfg::kAccBufs;
+    const uint32_t use_par = static_cast<uint32_t>((acc_iter / Cfg::kAccBufs) & 1);
+    if (!wait_bar_warp<false>(tfull0 + 8u * buf, use_par, w, kSiteTmemFull, wi.mb)) return;
+    ptx::tc_fence_after();
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * Cfg::kBN);
+#pragma unroll
+    for (int c = 0; c < 128; c += 16) {
+      uint32_t v[16];
+      ptx::tmem_ld_32x32b_x16(t_row + c, v);
+      ptx::tmem_wait_ld(v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z[c + i] += __uint_as_float(v[i]);
+    }
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(tempty0 + 8u * buf);
+  }
+  const uint32_t mine = recv + static_cast<uint32_t>(rank * (kCols / 4) * 128 + q * 32 + lane) * 16u;
+#pragma unroll
+  for (int c = 0; c < 128; c += 4)
+    ptx::st_shared_cluster_v4(ptx::mapa(mine + static_cast<uint32_t>(c % kCols / 4 * 128) * 16u, static_cast<uint32_t>(c / kCols)),
+                              __float_as_uint(z[c]), __float_as_uint(z[c + 1]), __float_as_uint(z[c + 2]),
+                              __float_as_uint(z[c + 3]));
+}
+
 // The end of a split cluster's tile, run by all 256 threads of each CTA: lone
 // CTAs.
 template <class Cfg>
@@ -526,8 +569,8 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, const Fuse
   ptx::griddep_wait();  // reads S, g and u; writes the outputs
   ptx::griddep_launch_dependents();
   const FusedItem wi = fused_item<Cfg>(args, dims, unit, rank);
-  bool ok = wait_bar_warp<false>(tfull, 0u, w, kSiteTmemFull, unit);
-  if (ok) {
+  const bool ok = Cfg::kCollect || wait_bar_warp<false>(tfull, 0u, w, kSiteTmemFull, unit);
+  if (ok && !Cfg::kCollect) {
     // Send: warp quarter q owns 32 rows, warps 0-3 columns 0-63, warps 4-7 the
     // rest (gated: gate, up).  Receiver's slot: [source][4 columns][row][16 B],
     // so a warp writes 512 contiguous bytes at a time.
@@ -565,7 +608,7 @@ __device__ __forceinline__ void split_epilogue(const FusedArgs& args, const Fuse
   uint4 s0[Cfg::kReads ? kN / 8 : 1], s1[Cfg::kReads ? kN / 8 : 1];
   if (in) read_columns<Cfg, kN>(args, wi, row, col0, s0, s1);
   ptx::cluster_sync();
-  if (!ok || !in) return;
+  if (!ok || !in || (Cfg::kCollect && *w.abort)) return;
   auto sum = [&](int first4, float (&v)[kN]) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) v[i] = 0.0f;
@@ -693,7 +736,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(bar_tfull(b), 1);
-      ptx::mbar_init(bar_tempty(b), Cfg::kEpiWarps * Cfg::kCtas);
+      ptx::mbar_init(bar_tempty(b), Cfg::kCollect ? 4 : Cfg::kEpiWarps * Cfg::kCtas);
     }
     ptx::mbar_init(bar_mma_done, 1);
     *abort_flag = 0u;
@@ -823,7 +866,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const FusedItem wi = fused_item<Cfg>(args, dims, it, rank);
         int32_t kb = wi.kb0;
         do {  // once, or for each partial sum
-          const int32_t end = Cfg::kPartKb > 0 && Cfg::kSplit == 1 ? min(wi.kb1, kb + Cfg::kPartKb) : wi.kb1;
+          const int32_t end = Cfg::kHands ? min(wi.kb1, kb + Cfg::kPartKb) : wi.kb1;
           const int buf = acc_iter % Cfg::kAccBufs;
           const uint32_t use_par = static_cast<uint32_t>((acc_iter / Cfg::kAccBufs) & 1);
           if (!wait_bar_warp<kPair>(bar_tempty(buf), use_par ^ 1u, w, kSiteTmemEmpty, it)) {
@@ -885,6 +928,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       __syncwarp();
       wait_bar_warp<kPair>(bar_mma_done, 0u, w, kSiteMmaDone, -1, /*honor_abort=*/false);
     }
+  } else if (Cfg::kCollect && warp >= 2 && warp < 6) {
+    if constexpr (Cfg::kCollect)
+      if (unit < dims.items)
+        collect_parts<Cfg>(fused_item<Cfg>(args, dims, unit, rank), rank, tmem_base, sb + Cfg::kOffEpi, bar_tfull(0),
+                           bar_tempty(0), w);
   } else if (Cfg::kSplit == 1 && warp >= 4) {
     // ------------------------------------------------------------ epilogue --
     ptx::griddep_wait();  // reads S, g and u; writes the outputs
@@ -970,7 +1018,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         }
       }
     };
-    if constexpr (Cfg::kPartKb > 0) {
+    if constexpr (Cfg::kHands) {
       // Each warp for itself: 32 rows, and this group's columns of the tile.
       constexpr int kCols = Cfg::kOutN / Cfg::kGroups;
       constexpr int kLoad = kCols > 64 ? 8 : 16;  // (128 sums and 16 loads do not fit in registers)

@@ -54,9 +54,9 @@ using Lone = FusedCfg<1, 128, kEpi == kEpiLse && kSplit == 1 ? 7 : 5, kEpi,
                       kEpi == kEpiLse && kSplit == 1 ? 0 : epi_bufs(kEpi), kSplit,
                       ((kEpi == kEpiLse || kEpi == kEpiXent || kEpi == kEpiStoreLive) && kSplit > 1) ? 4 : kParts>;
 
-// dx and dW of long sums.
+// dx and dW of long sums, clusters' logits of wide rows.
 template <class Cfg>
-using Long = FusedCfg<Cfg::kCtas, Cfg::kBN, Cfg::kStages, Cfg::kEpi, Cfg::kEpiBufs, 1, 0>;
+using Long = FusedCfg<Cfg::kCtas, Cfg::kBN, Cfg::kStages, Cfg::kEpi, Cfg::kEpiBufs, Cfg::kSplit, 0>;
 
 // One CTA on 128 x 256 logits of the loss, for the rounds that tiles of a pair or of 128
 // columns fill badly: 1 token, 4096 x 32000 49.5 -> 45.1 us, 101 x 512 x 32000 13.4 ->
@@ -364,14 +364,20 @@ gemm_status_t fused(gemm_ops_s* h, const Product& p, const FusedArgs& a, const S
     case kLone2:
       if constexpr (kBatched<kEpi>)
         if (f.small * p.batch > h->max_split[1]) return launch_fused<Lone<kEpi, 1, 2>>(h, p, a, c, d, stream, shares);
+      if constexpr (Lone<kEpi>::kPartial)
+        if (kb > 2 * 4 * kSplitKb) return launch_fused<Long<Lone<kEpi, 2>>>(h, p, a, c, d, stream, shares);
       if constexpr (kSplits<kEpi>) return launch_fused<Lone<kEpi, 2>>(h, p, a, c, d, stream, shares);
       break;
     case kLone4:
       if constexpr (kBatched<kEpi>)
         if (f.small * p.batch > h->max_split[2]) return launch_fused<Lone<kEpi, 1, 4>>(h, p, a, c, d, stream, shares);
+      if constexpr (Lone<kEpi>::kPartial)
+        if (kb > 4 * 4 * kSplitKb) return launch_fused<Long<Lone<kEpi, 4>>>(h, p, a, c, d, stream, shares);
       if constexpr (kSplits<kEpi>) return launch_fused<Lone<kEpi, 4>>(h, p, a, c, d, stream, shares);
       break;
     case kLone8:
+      if constexpr (Lone<kEpi>::kPartial)
+        if (kb > 8 * 4 * kSplitKb) return launch_fused<Long<Lone<kEpi, 8>>>(h, p, a, c, d, stream, shares);
       if constexpr (kSplits<kEpi> && !kBatched<kEpi>) return launch_fused<Lone<kEpi, 8>>(h, p, a, c, d, stream, shares);
       break;
     case kWide:

@@ -14,6 +14,9 @@ bool xent_setup(gemm_ops_s* h) {
       !set_attr<Long<Lone<kEpiStoreLive>>>() || !set_attr<Pair<kEpiStoreLive>>() || !set_attr<TwoPairs<kEpiStoreLive>>() || !set_attr<Lone<kEpiStoreLive>>() ||
       !set_attr<Lone<kEpiStoreLive, 2>>() || !set_attr<Lone<kEpiStoreLive, 4>>() || !set_attr<Lone<kEpiStoreLive, 8>>())
     return false;
+  if (!set_attr<Long<Lone<kEpiLse, 2>>>() || !set_attr<Long<Lone<kEpiLse, 4>>>() || !set_attr<Long<Lone<kEpiLse, 8>>>() ||
+      !set_attr<Long<Lone<kEpiXent, 2>>>() || !set_attr<Long<Lone<kEpiXent, 4>>>() || !set_attr<Long<Lone<kEpiXent, 8>>>())
+    return false;
   h->max_pairs = std::min({h->max_pairs, max_clusters<Pair<kEpiLse>>(), max_clusters<Pair<kEpiXent>>(),
                            max_clusters<Pair<kEpiSum>>(), max_clusters<Pair<kEpiStoreLive>>(),
                            max_clusters<Long<Pair<kEpiSum>>>(), max_clusters<Long<Pair<kEpiStoreLive>>>()});

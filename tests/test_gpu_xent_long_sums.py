@@ -1,15 +1,17 @@
-"""dx and dW of the vocabulary's loss over sums of many products.
+"""The products of the vocabulary's loss over sums of many terms: dx, dW, logits of wide rows.
 
 The tensor cores truncate a sum, always towards zero, at each step of 16 products, by at
 most 2^-23 of what it has come to.  Sums of at most 8192 products stand in one accumulator
-(512 steps); such parts are added in fp32.  Logits here are all 0, so that every
-probability is a power of two and dz is exact in 16 bits, and the sums come to large values
-on the way to small results: what truncation loses is seen whole, where the rounding of an
-ordinary result would cover it."""
+(512 steps), of logits at most 512; such parts are added in fp32.  For dx and dW logits are
+all 0, so that every probability is a power of two and dz is exact in 16 bits, and the sums
+come to large values on the way to small results: what truncation loses is seen whole, where
+the rounding of an ordinary result would cover it."""
 import math
 
 import pytest
 import torch
+
+from test_gpu_xent import make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -85,7 +87,33 @@ def test_dw_of_many_tokens(g, T, D, V):
         assert worst <= err, f"row {row}: off by {worst:.3g}, allowed {err:.3g}"
 
 
-@pytest.mark.parametrize("T,D,V", [(600, 4096, 16384), (9000, 64, 256)])
+@pytest.mark.parametrize("D,V,ctas", [(2 ** 20, 1000, 8), (2 ** 18, 4000, 4), (2 ** 18, 9000, 2)])
+def test_logits_of_very_wide_rows(g, D, V, ctas):
+    """One token, all products near 1, so that logits grow to D: clusters of CTAs share the
+    rows, each a k-range."""
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    x, w = near_one(gen, 1, D), near_one(gen, V, D)
+    _, lse = g.linear_cross_entropy(x, w, torch.zeros(1, dtype=torch.int64, device="cuda"), save=True)
+    g.default_ops().check_error()
+    z = torch.cat([p.to(F64) @ x[0].to(F64) for p in w.split(2 ** 26 // D)])
+    ref = torch.logsumexp(z, 0)
+    # Parts of 512 products grow to 528: half of that on average.  A CTA's parts are added up
+    # to its share of D, the CTAs' sums to D.  The lse itself is rounded a few times.
+    top, share, part = 1.04 * D, 1.04 * D / ctas, 512
+    err = (D / part * (part / STEP) * 2.0 ** -23 * 528 / 2 + D / part * 2.0 ** -24 * share / 2
+           + ctas * 2.0 ** -24 * top + 4 * 2.0 ** -24 * top)
+    off = (lse[0].to(F64) - ref).abs().item()
+    assert off <= 1.02 * err, f"off by {off:.3g}, allowed {1.02 * err:.3g}"
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("T,D,V", [(3, 8200, 5000), (1, 16392, 4000), (20, 65536, 700), (130, 8328, 4099)])
+def test_wide_rows(g, T, D, V, dt):
+    x, w, targets, dloss = make(T, D, V, dt, seed=D)
+    run(g, x, w, targets, dloss, 0.3 * dloss)
+
+
+@pytest.mark.parametrize("T,D,V", [(600, 4096, 16384), (9000, 128, 256), (5, 16392, 4000)])
 def test_stuck_waits_of_long_sums_end(g, T, D, V):
     """A k-block that is never loaded, in products of long sums: the kernels give up and
     report, and the next call is right."""
@@ -97,11 +125,14 @@ def test_stuck_waits_of_long_sums_end(g, T, D, V):
     dloss = torch.ones(T, device="cuda")
     _, lse = g.linear_cross_entropy(x, w, targets, save=True)
     ops.set_watchdog(timeout_ns=50_000_000, skip_k_block=1)
-    ops.linear_cross_entropy_backward(dloss, x, w, targets, lse)
-    with pytest.raises(g.GemmError) as e:
-        ops.check_error()
-    assert e.value.status == 5
+    for call in (lambda: ops.linear_cross_entropy_backward(dloss, x, w, targets, lse),
+                 lambda: ops.linear_cross_entropy(x, w, targets)):
+        call()
+        with pytest.raises(g.GemmError) as e:
+            ops.check_error()
+        assert e.value.status == 5
     ops.set_watchdog()
+    assert torch.equal(ops.linear_cross_entropy(x, w, targets, save=True)[1], lse)
     got = ops.linear_cross_entropy_backward(dloss, x, w, targets, lse)
     ops.check_error()
     want = g.linear_cross_entropy_backward(dloss, x, w, targets, lse)
