@@ -178,7 +178,8 @@ GEMM_API gemm_status_t gemm_orthogonalize(gemm_ops_t ops, const void* m, int64_t
  *                  RMS norm: r, [T, 1]) for the backward pass
  * Any alignment of whole elements and any row distance from D on (below 2^30);
  * D is at least 1, T == 0 has nothing to do.  Statistics and sums are fp32: the sum
- * of squares of a row's x - m (x) must stay below 2^128.  A row that holds an
+ * of a row's x (layer norm) and that of the squares of x - m (x) must stay below 2^128
+ * in magnitude, and squares below 2^-149 are lost, which shows where eps is 0.  A row that holds an
  * infinity or NaN comes out NaN where the formula has it, and no other row changes. */
 GEMM_API gemm_status_t gemm_layer_norm(gemm_ops_t ops, const void* x, int64_t ldx, const void* weight,
                                        const void* bias, void* y, int64_t ldy, float* stats, int64_t T,
@@ -222,8 +223,9 @@ GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_ops_t ops, const void* dy, in
  *   loss    : [T] fp32;  lse : [T] fp32, or NULL (the lse of every token, ignored ones too)
  * D is a positive multiple of 8, x and w 16-byte aligned, their row distances multiples
  * of 8 (GEMM_ERR_ALIGNMENT otherwise); D is at most 2^24, V 1 to 2^28; T == 0: nothing
- * to do.  Logits and sums are fp32.  Infinities and NaN go where the formula puts them:
- * an infinite logit gives an infinite lse.
+ * to do.  Logits and sums are fp32; finite logits must stay below 2^127 in magnitude.
+ * Infinities and NaN go where the formula puts them: an infinite logit gives an infinite
+ * lse.
  * workspace: gemm_linear_cross_entropy_workspace(ops, T, D, V) bytes, 256-byte aligned. */
 GEMM_API size_t gemm_linear_cross_entropy_workspace(gemm_ops_t ops, int64_t T, int64_t D, int64_t V);
 GEMM_API gemm_status_t gemm_linear_cross_entropy(gemm_ops_t ops, const void* x, int64_t ldx, const void* w,
